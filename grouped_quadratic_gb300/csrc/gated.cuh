@@ -1,0 +1,145 @@
+// gated.cuh -- what the gated linear recurrence's kernels share.
+//
+// Per (batch, KV head), with a log decay g_t per token and a 64 x 64 state:
+//     S_t = exp(g_t) S_{t-1} + k_t v_t^T,      y_t = scale S_t^T q_t.
+// With G the sums of g inside a chunk of 64 tokens, S_in the state before it:
+//     y_i   = scale [ sum_{j<=i} e^{G_i-G_j} (q_i.k_j) v_j + e^{G_i} S_in^T q_i ]
+//     S_out = e^{G_63} S_in + sum_j e^{G_63-G_j} k_j v_j^T.
+// A sequence is cut into segments of whole chunks: the segments' own states
+// are formed side by side, a scan turns them into the state before each
+// segment, and a last pass walks every segment from there.
+#pragma once
+#include "oal_internal.cuh"
+
+namespace oal {
+
+constexpr int kGC = 64;                 // tokens of a chunk
+constexpr int kGS = kD * kDv;           // elements of a state
+// exp(g) is 0 in fp32 from here down, so such a gate starts from nothing like
+// -inf does; it is counted instead of summed, which keeps the sums small.
+constexpr float kGateCut = -104.f;
+
+struct GatedArgs {
+  const void *Q, *K, *V, *dY;
+  const float *g;
+  int B, Hq, Hkv, T;
+  float scale;
+  const int32_t *lengths;               // null: every sequence has T tokens
+  const float *state_in;                // state before token 0, null: zeros
+  float *state_out;                     // prefill: state after the last token
+  void *Y;
+  const float *dstate;                  // backward: gradient of the last state, null: zeros
+  float *dstate0;                       // backward: gradient of state_in, may be null
+  void *dQ, *dK, *dV;
+  float *dg;
+  int seg_chunks, nseg;                 // chunks of a segment, segments of T tokens
+  float *seg_state, *seg_decay;         // [B Hkv][nseg][64 64], [B Hkv][nseg]
+  float *seg_grad;                      // backward: the same for the state's gradient
+  int *status;
+};
+
+// Segment sizes in chunks (gated_simt.cu), and how many of them T tokens have.
+int gated_prefill_segment(int B, int Hkv, int T, int is_bf16);
+int gated_backward_segment(int is_bf16);
+inline int gated_segments(int T, int seg_chunks) {
+  const int chunks = (int)(((long long)T + kGC - 1) / kGC);
+  return (chunks + seg_chunks - 1) / seg_chunks;
+}
+
+// Length of sequence b, clamped to 0..T; one outside is recorded.
+__device__ __forceinline__ int gated_len(const GatedArgs &p, int b) {
+  if (!p.lengths) return p.T;
+  const int n = p.lengths[b];
+  if (n < 0 || n > p.T) {
+    if (threadIdx.x == 0) atomicCAS(p.status, kStatusOk, (int)OAL_ERR_INVALID_ARG);
+    return n < 0 ? 0 : p.T;
+  }
+  return n;
+}
+__device__ __forceinline__ int gated_last_seg(int n, int seg_tokens) {
+  return n > 0 ? (n - 1) / seg_tokens : 0;
+}
+
+// Sums of g inside a chunk: the sum as an unevaluated pair hi + lo, so the
+// difference of two neighbours keeps its digits behind a large drop, and the
+// gates cut so far, which are left out of the sum.
+struct GateSums {
+  float hi[kGC], lo[kGC];
+  int cuts[kGC];
+};
+
+__device__ __forceinline__ void two_sum(float a, float b, float &s, float &e) {
+  s = a + b;
+  const float t = s - a;
+  e = (a - (s - t)) + (b - t);
+}
+
+// One warp: lane l takes tokens 2l, 2l+1 of the chunk at t0; rows from n on
+// count as gates of 1 (g = 0).
+__device__ __forceinline__ void gate_sums(const float *__restrict__ g, int t0, int n, GateSums &out) {
+  const int lane = threadIdx.x & 31, t = t0 + 2 * lane;
+  const float x0 = t < n ? __ldg(g + t) : 0.f, x1 = t + 1 < n ? __ldg(g + t + 1) : 0.f;
+  const int c0 = x0 <= kGateCut, c1 = x1 <= kGateCut;
+  const float a = c0 ? 0.f : x0, b = c1 ? 0.f : x1;
+  float hi, lo;
+  two_sum(a, b, hi, lo);
+  int cuts = c0 + c1;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const float oh = __shfl_up_sync(0xffffffffu, hi, d), ol = __shfl_up_sync(0xffffffffu, lo, d);
+    const int oc = __shfl_up_sync(0xffffffffu, cuts, d);
+    if (lane >= d) {
+      float s, e;
+      two_sum(oh, hi, s, e);
+      e += ol + lo;
+      hi = s + e;
+      lo = e - (hi - s);
+      cuts += oc;
+    }
+  }
+  float ph = __shfl_up_sync(0xffffffffu, hi, 1), pl = __shfl_up_sync(0xffffffffu, lo, 1);
+  int pc = __shfl_up_sync(0xffffffffu, cuts, 1);
+  if (lane == 0) ph = pl = 0.f, pc = 0;
+  float s, e;
+  two_sum(ph, a, s, e);
+  e += pl;
+  const float h0 = s + e;
+  out.hi[2 * lane] = h0;
+  out.lo[2 * lane] = e - (h0 - s);
+  out.cuts[2 * lane] = pc + c0;
+  out.hi[2 * lane + 1] = hi;
+  out.lo[2 * lane + 1] = lo;
+  out.cuts[2 * lane + 1] = cuts;
+}
+
+// Decay between tokens j <= i of the chunk, exp(G_i - G_j).
+__device__ __forceinline__ float gate_pair(const GateSums &s, int i, int j) {
+  return s.cuts[i] == s.cuts[j] ? expf((s.hi[i] - s.hi[j]) + (s.lo[i] - s.lo[j])) : 0.f;
+}
+// Decay from the chunk's start to token i, exp(G_i).
+__device__ __forceinline__ float gate_head(const GateSums &s, int i) {
+  return s.cuts[i] == 0 ? expf(s.hi[i] + s.lo[i]) : 0.f;
+}
+// Decay from behind token j to the chunk's end, exp(G_63 - G_j).
+__device__ __forceinline__ float gate_tail(const GateSums &s, int j) {
+  return gate_pair(s, kGC - 1, j);
+}
+
+// Eight elements of a row as fp32.
+__device__ __forceinline__ void gated_load8(const __nv_bfloat16 *p, float (&o)[8]) {
+  const uint4 w = __ldg(reinterpret_cast<const uint4 *>(p));
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    o[2 * e] = __uint_as_float(u[e] << 16);
+    o[2 * e + 1] = __uint_as_float(u[e] & 0xFFFF0000u);
+  }
+}
+__device__ __forceinline__ void gated_load8(const float *p, float (&o)[8]) {
+  const float4 a = __ldg(reinterpret_cast<const float4 *>(p));
+  const float4 b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
+  o[0] = a.x, o[1] = a.y, o[2] = a.z, o[3] = a.w;
+  o[4] = b.x, o[5] = b.y, o[6] = b.z, o[7] = b.w;
+}
+
+}  // namespace oal

@@ -7,7 +7,7 @@
 
 #include <algorithm>
 
-#include "oal_internal.cuh"
+#include "gated.cuh"
 
 namespace oal {
 oal_status launch_expand_coeffs(const float *L, const int32_t *group, int Hq, int G,
@@ -45,6 +45,15 @@ oal_status launch_contrib(const void *Q, const void *K, int is_bf16, int P, int 
 oal_status group_dims_host(const float *chi_p, int P, int d, const int32_t *boot_idx,
                            int nboot, double alpha, double tau, double gamma, int g_min,
                            double eps, int32_t *group, int *G);
+
+oal_status launch_gated_prefill_simt(const GatedArgs &p, int is_bf16, cudaStream_t stream);
+oal_status launch_gated_backward_simt(const GatedArgs &p, int is_bf16, cudaStream_t stream);
+oal_status launch_gated_decode(const void *q, const void *k, const void *v, int is_bf16,
+                               const float *g, int B, int Hq, int Hkv, float scale,
+                               const int32_t *slots, int n_slots, float *state, void *y,
+                               cudaStream_t stream);
+oal_status launch_state_remap(void *pool, size_t slot_bytes, int n, const int32_t *map,
+                              cudaStream_t stream);
 
 // Device control block (one per device the library runs on): the status
 // word kernels record errors in; then, for tests of the failure path, the
@@ -425,6 +434,181 @@ oal_status oal_group_dims(const float *chi_p, int P, int d, const int32_t *boot_
                               group, G);
 }
 
+// ---- gated linear recurrence
+
+static oal_status check_gated(int B, int Hq, int Hkv, int T, int d, int dv, oal_dtype dtype,
+                              float scale) {
+  OAL_TRY(check_common(B, Hq, Hkv, d, dv, dtype, OAL_STATE_FULL));
+  if (T < 0) return oal_fail(OAL_ERR_INVALID_ARG, "T=%d", T);
+  if (!isfinite(scale)) return oal_fail(OAL_ERR_INVALID_ARG, "scale=%g", scale);
+  if (T > 1 << 30 ||
+      (long long)B * Hkv * ((T + oal::kGC - 1) / oal::kGC + 1) > 0x3fffffffLL ||
+      (long long)B * Hq > 0x7fffffffLL / 64)
+    return oal_fail(OAL_ERR_UNSUPPORTED, "problem too large");
+  return OAL_OK;
+}
+
+static oal_status check_workspace(const void *workspace, size_t bytes, size_t need) {
+  OAL_TRY(check_ptr(workspace, "workspace"));
+  if (((uintptr_t)workspace & 255u) != 0)
+    return oal_fail(OAL_ERR_INVALID_ARG, "workspace is not 256-byte aligned");
+  if (bytes < need)
+    return oal_fail(OAL_ERR_INVALID_ARG, "workspace too small: %zu < %zu bytes", bytes, need);
+  return OAL_OK;
+}
+
+// The workspace: per (batch, KV head) and segment one state, (backward) one
+// state gradient, and one decay.
+static size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
+static size_t gated_states_bytes(int B, int Hkv, int nseg) {
+  return (size_t)B * Hkv * nseg * oal::kGS * sizeof(float);
+}
+
+size_t oal_gated_prefill_workspace_bytes(int B, int Hq, int Hkv, int T, int d, int dv,
+                                         oal_dtype dtype) {
+  if (check_gated(B, Hq, Hkv, T, d, dv, dtype, 1.f) != OAL_OK) return 0;
+  if (B == 0 || T == 0) return 256;
+  const int chunks = oal::gated_prefill_segment(B, Hkv, T, dtype == OAL_BF16);
+  const int nseg = oal::gated_segments(T, chunks);
+  if (nseg == 1) return 256;
+  return gated_states_bytes(B, Hkv, nseg) + round256((size_t)B * Hkv * nseg * sizeof(float));
+}
+
+oal_status oal_gated_prefill(const void *Q, const void *K, const void *V, oal_dtype dtype,
+                             const float *g, int B, int Hq, int Hkv, int T, int d, int dv,
+                             float scale, const int32_t *lengths, float *state,
+                             int continue_from_state, void *Y, void *workspace,
+                             size_t workspace_bytes, cudaStream_t stream) {
+  t_msg[0] = 0;
+  OAL_TRY(check_gated(B, Hq, Hkv, T, d, dv, dtype, scale));
+  t_call_launches = 0;
+  if (B == 0) return OAL_OK;
+  OAL_TRY(check_ptr(state, "state"));
+  if (T == 0) {
+    if (!continue_from_state &&
+        cudaMemsetAsync(state, 0, gated_states_bytes(B, Hkv, 1), stream) != cudaSuccess)
+      return oal_check_launch("state reset");
+    return OAL_OK;
+  }
+  OAL_TRY(check_ptr(Q, "Q"));
+  OAL_TRY(check_ptr(K, "K"));
+  OAL_TRY(check_ptr(V, "V"));
+  OAL_TRY(check_ptr(g, "g"));
+  OAL_TRY(check_ptr(Y, "Y"));
+  if (lengths) OAL_TRY(check_ptr(lengths, "lengths"));
+  OAL_TRY(check_workspace(workspace, workspace_bytes,
+                          oal_gated_prefill_workspace_bytes(B, Hq, Hkv, T, d, dv, dtype)));
+  oal::GatedArgs p = {};
+  p.Q = Q, p.K = K, p.V = V, p.g = g, p.Y = Y;
+  p.B = B, p.Hq = Hq, p.Hkv = Hkv, p.T = T, p.scale = scale, p.lengths = lengths;
+  p.state_in = continue_from_state ? state : nullptr;
+  p.state_out = state;
+  p.seg_chunks = oal::gated_prefill_segment(B, Hkv, T, dtype == OAL_BF16);
+  p.nseg = oal::gated_segments(T, p.seg_chunks);
+  p.seg_state = static_cast<float *>(workspace);
+  p.seg_decay = reinterpret_cast<float *>(static_cast<char *>(workspace) +
+                                          gated_states_bytes(B, Hkv, p.nseg));
+  p.status = oal_device_status_word();
+  if (!p.status) return oal_fail(OAL_ERR_CUDA, "no device status word");
+  oal_begin_call(stream);
+  return oal::launch_gated_prefill_simt(p, dtype == OAL_BF16, stream);
+}
+
+size_t oal_gated_backward_workspace_bytes(int B, int Hq, int Hkv, int T, int d, int dv,
+                                          oal_dtype dtype) {
+  if (check_gated(B, Hq, Hkv, T, d, dv, dtype, 1.f) != OAL_OK) return 0;
+  if (B == 0 || T == 0) return 256;
+  const int nseg = oal::gated_segments(T, oal::gated_backward_segment(dtype == OAL_BF16));
+  return 2 * gated_states_bytes(B, Hkv, nseg) + round256((size_t)B * Hkv * nseg * sizeof(float));
+}
+
+oal_status oal_gated_backward(const void *Q, const void *K, const void *V, oal_dtype dtype,
+                              const float *g, const void *dY, int B, int Hq, int Hkv, int T,
+                              int d, int dv, float scale, const int32_t *lengths,
+                              const float *state0, const float *dstate, void *dQ, void *dK,
+                              void *dV, float *dg, float *dstate0, void *workspace,
+                              size_t workspace_bytes, cudaStream_t stream) {
+  t_msg[0] = 0;
+  OAL_TRY(check_gated(B, Hq, Hkv, T, d, dv, dtype, scale));
+  t_call_launches = 0;
+  if (B == 0) return OAL_OK;
+  if (state0) OAL_TRY(check_ptr(state0, "state0"));
+  if (dstate) OAL_TRY(check_ptr(dstate, "dstate"));
+  if (dstate0) OAL_TRY(check_ptr(dstate0, "dstate0"));
+  if (T == 0) {   // the state passes through
+    if (!dstate0) return OAL_OK;
+    const size_t bytes = gated_states_bytes(B, Hkv, 1);
+    const cudaError_t e = dstate ? cudaMemcpyAsync(dstate0, dstate, bytes, cudaMemcpyDeviceToDevice, stream)
+                                 : cudaMemsetAsync(dstate0, 0, bytes, stream);
+    return e == cudaSuccess ? OAL_OK : oal_check_launch("dstate0");
+  }
+  OAL_TRY(check_ptr(Q, "Q"));
+  OAL_TRY(check_ptr(K, "K"));
+  OAL_TRY(check_ptr(V, "V"));
+  OAL_TRY(check_ptr(g, "g"));
+  OAL_TRY(check_ptr(dY, "dY"));
+  OAL_TRY(check_ptr(dQ, "dQ"));
+  OAL_TRY(check_ptr(dK, "dK"));
+  OAL_TRY(check_ptr(dV, "dV"));
+  OAL_TRY(check_ptr(dg, "dg"));
+  if (lengths) OAL_TRY(check_ptr(lengths, "lengths"));
+  OAL_TRY(check_workspace(workspace, workspace_bytes,
+                          oal_gated_backward_workspace_bytes(B, Hq, Hkv, T, d, dv, dtype)));
+  oal::GatedArgs p = {};
+  p.Q = Q, p.K = K, p.V = V, p.g = g, p.dY = dY;
+  p.B = B, p.Hq = Hq, p.Hkv = Hkv, p.T = T, p.scale = scale, p.lengths = lengths;
+  p.state_in = state0, p.dstate = dstate, p.dstate0 = dstate0;
+  p.dQ = dQ, p.dK = dK, p.dV = dV, p.dg = dg;
+  p.seg_chunks = oal::gated_backward_segment(dtype == OAL_BF16);
+  p.nseg = oal::gated_segments(T, p.seg_chunks);
+  const size_t states = gated_states_bytes(B, Hkv, p.nseg);
+  p.seg_state = static_cast<float *>(workspace);
+  p.seg_grad = reinterpret_cast<float *>(static_cast<char *>(workspace) + states);
+  p.seg_decay = reinterpret_cast<float *>(static_cast<char *>(workspace) + 2 * states);
+  p.status = oal_device_status_word();
+  if (!p.status) return oal_fail(OAL_ERR_CUDA, "no device status word");
+  oal_begin_call(stream);
+  return oal::launch_gated_backward_simt(p, dtype == OAL_BF16, stream);
+}
+
+oal_status oal_gated_decode_step(const void *q, const void *k, const void *v, oal_dtype dtype,
+                                 const float *g, int B, int Hq, int Hkv, int d, int dv,
+                                 float scale, const int32_t *slots, int n_slots, float *state,
+                                 void *y, cudaStream_t stream) {
+  t_msg[0] = 0;
+  OAL_TRY(check_gated(B, Hq, Hkv, 1, d, dv, dtype, scale));
+  if (n_slots < 0 || (!slots && n_slots < B))
+    return oal_fail(OAL_ERR_INVALID_ARG, "n_slots=%d for %d sequences", n_slots, B);
+  t_call_launches = 0;
+  if (B == 0) return OAL_OK;
+  OAL_TRY(check_ptr(q, "q"));
+  OAL_TRY(check_ptr(k, "k"));
+  OAL_TRY(check_ptr(v, "v"));
+  OAL_TRY(check_ptr(g, "g"));
+  OAL_TRY(check_ptr(y, "y"));
+  if (slots) OAL_TRY(check_ptr(slots, "slots"));
+  if (n_slots > 0) OAL_TRY(check_ptr(state, "state"));
+  oal_begin_call(stream);
+  return oal::launch_gated_decode(q, k, v, dtype == OAL_BF16, g, B, Hq, Hkv, scale, slots,
+                                  n_slots, state, y, stream);
+}
+
+oal_status oal_state_remap(void *pool, size_t slot_bytes, int n_slots, const int32_t *map,
+                           cudaStream_t stream) {
+  t_msg[0] = 0;
+  if (n_slots < 0) return oal_fail(OAL_ERR_INVALID_ARG, "n_slots=%d", n_slots);
+  if (n_slots > OAL_REMAP_MAX_SLOTS)
+    return oal_fail(OAL_ERR_UNSUPPORTED, "n_slots=%d above %d", n_slots, OAL_REMAP_MAX_SLOTS);
+  t_call_launches = 0;
+  if (n_slots == 0 || slot_bytes == 0) return OAL_OK;
+  if (slot_bytes > ((size_t)1 << 46) / (size_t)n_slots)
+    return oal_fail(OAL_ERR_UNSUPPORTED, "pool too large");
+  OAL_TRY(check_ptr(pool, "pool"));
+  OAL_TRY(check_ptr(map, "map"));
+  oal_begin_call(stream);
+  return oal::launch_state_remap(pool, slot_bytes, n_slots, map, stream);
+}
+
 oal_status oal_debug_wait_test(uint64_t wait_limit_cycles, int starve) {
   t_msg[0] = 0;
   if (starve < 0 || starve > 3) return oal_fail(OAL_ERR_INVALID_ARG, "starve=%d", starve);
@@ -462,8 +646,9 @@ oal_status oal_sync_status(cudaStream_t stream) {
   if (v != 0) {
     const int zero = 0;
     cudaMemcpy(w, &zero, sizeof zero, cudaMemcpyHostToDevice);
-    const char *what = v == OAL_ERR_INVALID_ARG ? "a group id outside 1..G or a prompt "
-                                                  "length outside 0..T"
+    const char *what = v == OAL_ERR_INVALID_ARG ? "a group id outside 1..G, a "
+                                                  "sequence length outside 0..T or a "
+                                                  "slot out of range or taken twice"
                        : v == OAL_ERR_TIMEOUT   ? "a device-side wait timed out"
                                                 : "device error";
     return oal_fail((oal_status)v, "device status %d: %s", v, what);

@@ -1,0 +1,98 @@
+// state_remap.cu -- copying, forking, compacting and freeing the slots of a
+// pool of states in place: new[i] = old[map[i]], zeros where map[i] is -1.
+//
+// Every source has to be read before any target is written, whatever cycles
+// the map holds.  The slots are cut into slices of a few words; a
+// block takes a slice of ALL slots that change, holds their old words in
+// registers, waits for its threads and writes them to their new places.
+// Slices do not meet, so no block waits for another, and no workspace is
+// needed.  Each changed slot's source is read once and its target written
+// once: HBM-bound.
+#include <algorithm>
+
+#include "gated.cuh"
+
+namespace oal {
+namespace {
+
+constexpr int kMoveThreads = 1024;
+constexpr int kMoveWords = 8;                           // words a thread holds
+constexpr int kMoveMost = kMoveThreads * kMoveWords;    // words a block holds
+
+// Word: the widest type that slot_bytes is a multiple of (a packed prefix
+// state has 557,700 bytes a head, so slots need not start on 16).
+template <typename Word>
+__global__ void __launch_bounds__(kMoveThreads)
+state_remap_kernel(Word *pool, long long slot_words, int n, const int32_t *__restrict__ map, int *status) {
+  pdl_trigger();
+  pdl_wait();
+  extern __shared__ int2 s_move[];      // (target, source) of the slots that change
+  __shared__ int s_count;
+  if (threadIdx.x == 0) s_count = 0;
+  __syncthreads();
+  for (int i = threadIdx.x; i < n; i += kMoveThreads) {
+    const int from = map[i];
+    if (from < -1 || from >= n) {
+      atomicCAS(status, kStatusOk, (int)OAL_ERR_INVALID_ARG);
+    } else if (from != i) {
+      s_move[atomicAdd(&s_count, 1)] = make_int2(i, from);   // any order: targets differ
+    }
+  }
+  __syncthreads();
+  const int count = s_count;
+  if (count == 0) return;
+  // words of a slice: as many as the block holds, at most what spreads the
+  // slot over the grid
+  const long long spread = (slot_words + gridDim.x - 1) / gridDim.x;
+  const int width = (int)min((long long)(kMoveMost / count), spread);
+  const int total = width * count;
+  for (long long w0 = (long long)blockIdx.x * width; w0 < slot_words; w0 += (long long)gridDim.x * width) {
+    Word held[kMoveWords];
+#pragma unroll
+    for (int k = 0; k < kMoveWords; ++k) {
+      const int x = threadIdx.x + k * kMoveThreads, m = x / width, w = x - m * width;
+      held[k] = Word();
+      if (x < total && w0 + w < slot_words && s_move[m].y >= 0)
+        held[k] = pool[(long long)s_move[m].y * slot_words + w0 + w];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kMoveWords; ++k) {
+      const int x = threadIdx.x + k * kMoveThreads, m = x / width, w = x - m * width;
+      if (x < total && w0 + w < slot_words) pool[(long long)s_move[m].x * slot_words + w0 + w] = held[k];
+    }
+  }
+}
+
+template <typename Word>
+oal_status remap(void *pool, size_t slot_bytes, int n, const int32_t *map, int *status, cudaStream_t stream) {
+  static bool done[kMaxDevices];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices)
+    return oal_fail(OAL_ERR_CUDA, "no current device");
+  if (!done[dev]) {
+    if (cudaFuncSetAttribute(state_remap_kernel<Word>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)(kMoveMost * sizeof(int2))) != cudaSuccess)
+      return oal_check_launch("shared memory of the remap kernel");
+    done[dev] = true;
+  }
+  const long long words = (long long)(slot_bytes / sizeof(Word));
+  const int blocks = (int)std::min<long long>(words, 2 * 152);
+  launch_pdl(state_remap_kernel<Word>, dim3(blocks), dim3(kMoveThreads), (size_t)n * sizeof(int2), stream,
+             static_cast<Word *>(pool), words, n, map, status);
+  return oal_after_launch("state_remap_kernel", stream);
+}
+
+}  // namespace
+
+oal_status launch_state_remap(void *pool, size_t slot_bytes, int n, const int32_t *map, cudaStream_t stream) {
+  int *status = oal_device_status_word();
+  if (!status) return oal_fail(OAL_ERR_CUDA, "no device status word");
+  if (slot_bytes % 16 == 0) return remap<uint4>(pool, slot_bytes, n, map, status, stream);
+  if (slot_bytes % 8 == 0) return remap<uint2>(pool, slot_bytes, n, map, status, stream);
+  if (slot_bytes % 4 == 0) return remap<uint32_t>(pool, slot_bytes, n, map, status, stream);
+  if (slot_bytes % 2 == 0) return remap<uint16_t>(pool, slot_bytes, n, map, status, stream);
+  return remap<uint8_t>(pool, slot_bytes, n, map, status, stream);
+}
+
+}  // namespace oal

@@ -9,7 +9,9 @@ Tensor layouts (row-major, contiguous, CUDA):
   Q [B,Hq,T,64], K/V [B,Hkv,T,64] (float32 or bfloat16)
   L [Hq,G+1,G+1] float32 (lower triangle), group [Hq,64] int32 in 1..G
   state [B,Hkv,F,65] float32 (F = 4161 FULL, 2145 PACKED)
+  gated recurrence: g [B,Hkv,T] float32 (log decays), state [B,Hkv,64,64] float32
 """
+import contextlib
 import ctypes
 import os
 
@@ -74,6 +76,21 @@ def load_library(path: str = LIB_PATH):
     lib.oal_contribution_workspace_bytes.restype = sz
     lib.oal_contribution_scores.argtypes = [vp, vp, ci, ci, ci, ci, ci, ci, vp, vp, vp, sz, vp]
     lib.oal_contribution_scores.restype = ci
+    lib.oal_gated_prefill_workspace_bytes.argtypes = [ci] * 7
+    lib.oal_gated_prefill_workspace_bytes.restype = sz
+    lib.oal_gated_prefill.argtypes = [vp, vp, vp, ci, vp, ci, ci, ci, ci, ci, ci, cf, vp, vp, ci,
+                                      vp, vp, sz, vp]
+    lib.oal_gated_prefill.restype = ci
+    lib.oal_gated_backward_workspace_bytes.argtypes = [ci] * 7
+    lib.oal_gated_backward_workspace_bytes.restype = sz
+    lib.oal_gated_backward.argtypes = [vp, vp, vp, ci, vp, vp, ci, ci, ci, ci, ci, ci, cf, vp, vp,
+                                       vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.oal_gated_backward.restype = ci
+    lib.oal_gated_decode_step.argtypes = [vp, vp, vp, ci, vp, ci, ci, ci, ci, ci, cf, vp, ci, vp,
+                                          vp, vp]
+    lib.oal_gated_decode_step.restype = ci
+    lib.oal_state_remap.argtypes = [vp, sz, ci, vp, vp]
+    lib.oal_state_remap.restype = ci
     cd = ctypes.c_double
     lib.oal_group_dims.argtypes = [vp, ci, ci, vp, ci, cd, cd, cd, ci, cd, vp, vp]
     lib.oal_group_dims.restype = ci
@@ -320,6 +337,211 @@ def oal_group_dims(chi_p, boot_idx, alpha, tau, gamma, g_min, eps=1e-12):
                               float(alpha), float(tau), float(gamma), int(g_min), float(eps),
                               group.ctypes.data, ctypes.byref(G)))
     return group, G.value
+
+
+def _need(ok, what):
+    if not ok:
+        raise OALError(OAL_ERR_INVALID_ARG, what)
+
+
+def _need_tensor(t, name, dtype, shape, dev):
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+        raise OALError(OAL_ERR_INVALID_ARG, "%s must be %s %s (got %s %s)"
+                       % (name, dtype, tuple(shape), t.dtype, tuple(t.shape)))
+    if t.device != dev or not t.is_cuda or not t.is_contiguous():
+        raise OALError(OAL_ERR_INVALID_ARG, "%s must be a contiguous CUDA tensor on %s" % (name, dev))
+
+
+def _on_device(dev, stream):
+    """(context that makes dev current, stream of dev to launch on).  Without a
+    stream argument: the current stream of the tensors' device."""
+    if dev.type != "cuda":
+        raise OALError(OAL_ERR_INVALID_ARG, "tensors must be contiguous CUDA tensors")
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    elif stream.device != dev:
+        raise OALError(OAL_ERR_INVALID_ARG, "the stream is on %s, the tensors on %s"
+                       % (stream.device, dev))
+    if torch.cuda.current_device() == dev.index:
+        return contextlib.nullcontext(), stream
+    return torch.cuda.device(dev), stream
+
+
+def _made_here(stream, dev, *ts):
+    """Tensors this call allocated, from the current stream's pool, while
+    `stream` may be another: their memory must not be handed out again before
+    `stream` is done with it."""
+    if stream != torch.cuda.current_stream(dev):
+        for t in ts:
+            t.record_stream(stream)
+
+
+def _gated_shapes(Q, K, V, g):
+    _need(Q.dim() == 4 and K.dim() == 4 and V.dim() == 4, "Q, K and V must have 4 dimensions")
+    B, Hq, T, d = Q.shape
+    Hkv, dv = K.shape[1], V.shape[3]
+    dev = Q.device
+    _need_tensor(Q, "Q", Q.dtype, (B, Hq, T, d), dev)
+    _need_tensor(K, "K", Q.dtype, (B, Hkv, T, d), dev)
+    _need_tensor(V, "V", Q.dtype, (B, Hkv, T, dv), dev)
+    _need_tensor(g, "g", torch.float32, (B, Hkv, T), dev)
+    return B, Hq, Hkv, T, d, dv, dev
+
+
+def _need_lengths(lengths, B, dev):
+    if lengths is not None:
+        _need_tensor(lengths, "lengths", torch.int32, (B,), dev)
+
+
+def _workspace(given, need, dev):
+    if given is None:
+        return torch.empty(max(int(need), 256), dtype=torch.uint8, device=dev)
+    _need(given.device == dev and given.is_contiguous(), "workspace must be contiguous on %s" % dev)
+    return given
+
+
+def oal_gated_prefill_workspace_bytes(B, Hq, Hkv, T, d=64, dv=64, dtype=OAL_BF16):
+    return int(load_library().oal_gated_prefill_workspace_bytes(B, Hq, Hkv, T, d, dv, dtype))
+
+
+def oal_gated_prefill(Q, K, V, g, scale=0.125, lengths=None, state=None,
+                      continue_from_state=False, Y=None, workspace=None, stream=None):
+    """Gated linear recurrence over T tokens: Q [B,Hq,T,64], K/V [B,Hkv,T,64],
+    g [B,Hkv,T] float32 log decays, lengths [B] int32 (CUDA) or None.  `state`
+    [B,Hkv,64,64] float32 is updated in place (from zeros unless
+    continue_from_state).  Returns (Y, state).  Rows of Y behind a sequence's
+    length stay as given; a Y made here has zeros there."""
+    lib = load_library()
+    B, Hq, Hkv, T, d, dv, dev = _gated_shapes(Q, K, V, g)
+    dt = _dtype_code(Q)
+    _need_lengths(lengths, B, dev)
+    _need(state is not None or not continue_from_state, "continue_from_state needs a state")
+    ctx, stream = _on_device(dev, stream)
+    with ctx:
+        made = []
+        if state is None:
+            state = torch.empty(B, Hkv, d, dv, dtype=torch.float32, device=dev)
+            made.append(state)
+        if Y is None:
+            make = torch.empty if lengths is None else torch.zeros
+            Y = make(B, Hq, T, dv, dtype=Q.dtype, device=dev)
+            made.append(Y)
+        if workspace is None:
+            need = lib.oal_gated_prefill_workspace_bytes(B, Hq, Hkv, T, d, dv, dt)
+            workspace = _workspace(None, need, dev)
+            made.append(workspace)
+        else:
+            _workspace(workspace, 0, dev)
+        _need_tensor(state, "state", torch.float32, (B, Hkv, d, dv), dev)
+        _need_tensor(Y, "Y", Q.dtype, (B, Hq, T, dv), dev)
+        _made_here(stream, dev, *made)
+        _check(lib.oal_gated_prefill(Q.data_ptr(), K.data_ptr(), V.data_ptr(), dt, g.data_ptr(),
+                                     B, Hq, Hkv, T, d, dv, float(scale),
+                                     None if lengths is None else lengths.data_ptr(),
+                                     state.data_ptr(), int(bool(continue_from_state)),
+                                     Y.data_ptr(), workspace.data_ptr(),
+                                     workspace.numel() * workspace.element_size(),
+                                     stream.cuda_stream))
+    return Y, state
+
+
+def oal_gated_backward_workspace_bytes(B, Hq, Hkv, T, d=64, dv=64, dtype=OAL_BF16):
+    return int(load_library().oal_gated_backward_workspace_bytes(B, Hq, Hkv, T, d, dv, dtype))
+
+
+def oal_gated_backward(Q, K, V, g, dY, scale=0.125, lengths=None, state0=None, dstate=None,
+                       dQ=None, dK=None, dV=None, dg=None, dstate0=None, workspace=None,
+                       stream=None):
+    """Gradients of <dY, Y> + <dstate, S_T> for oal_gated_prefill from state0
+    (None: zeros).  Returns (dQ, dK, dV, dg, dstate0): the first three in the
+    dtype of Q, dg and dstate0 float32.  Rows behind a sequence's length stay
+    as given; gradients made here have zeros there."""
+    lib = load_library()
+    B, Hq, Hkv, T, d, dv, dev = _gated_shapes(Q, K, V, g)
+    dt = _dtype_code(Q)
+    _need_lengths(lengths, B, dev)
+    _need_tensor(dY, "dY", Q.dtype, (B, Hq, T, dv), dev)
+    for name, t in (("state0", state0), ("dstate", dstate)):
+        if t is not None:
+            _need_tensor(t, name, torch.float32, (B, Hkv, d, dv), dev)
+    ctx, stream = _on_device(dev, stream)
+    with ctx:
+        made, out = [], []
+        make = torch.empty if lengths is None else torch.zeros
+        for name, t, like in (("dQ", dQ, Q), ("dK", dK, K), ("dV", dV, V), ("dg", dg, g)):
+            if t is None:
+                t = make(like.shape, dtype=like.dtype, device=dev)
+                made.append(t)
+            _need_tensor(t, name, like.dtype, like.shape, dev)
+            out.append(t)
+        if dstate0 is None:
+            dstate0 = torch.empty(B, Hkv, d, dv, dtype=torch.float32, device=dev)
+            made.append(dstate0)
+        _need_tensor(dstate0, "dstate0", torch.float32, (B, Hkv, d, dv), dev)
+        out.append(dstate0)
+        if workspace is None:
+            need = lib.oal_gated_backward_workspace_bytes(B, Hq, Hkv, T, d, dv, dt)
+            workspace = _workspace(None, need, dev)
+            made.append(workspace)
+        else:
+            _workspace(workspace, 0, dev)
+        _made_here(stream, dev, *made)
+        _check(lib.oal_gated_backward(Q.data_ptr(), K.data_ptr(), V.data_ptr(), dt, g.data_ptr(),
+                                      dY.data_ptr(), B, Hq, Hkv, T, d, dv, float(scale),
+                                      None if lengths is None else lengths.data_ptr(),
+                                      None if state0 is None else state0.data_ptr(),
+                                      None if dstate is None else dstate.data_ptr(),
+                                      *(t.data_ptr() for t in out), workspace.data_ptr(),
+                                      workspace.numel() * workspace.element_size(),
+                                      stream.cuda_stream))
+    return tuple(out)
+
+
+def oal_gated_decode_step(q, k, v, g, state, scale=0.125, slots=None, y=None, stream=None):
+    """One token of the gated recurrence: q [B,Hq,64], k/v [B,Hkv,64], g [B,Hkv]
+    float32.  `state` is a pool [n,Hkv,64,64] float32, updated in place;
+    sequence b has slot slots[b] (int32 CUDA; -1: no sequence, y is 0), or slot
+    b without slots.  Returns y."""
+    lib = load_library()
+    _need(q.dim() == 3 and k.dim() == 3 and v.dim() == 3 and state.dim() == 4,
+          "q, k and v must have 3 dimensions, state 4")
+    B, Hq, d = q.shape
+    Hkv, dv = k.shape[1], v.shape[2]
+    dt, dev, n = _dtype_code(q), q.device, state.shape[0]
+    _need_tensor(q, "q", q.dtype, (B, Hq, d), dev)
+    _need_tensor(k, "k", q.dtype, (B, Hkv, d), dev)
+    _need_tensor(v, "v", q.dtype, (B, Hkv, dv), dev)
+    _need_tensor(g, "g", torch.float32, (B, Hkv), dev)
+    _need_tensor(state, "state", torch.float32, (n, Hkv, d, dv), dev)
+    if slots is not None:
+        _need_tensor(slots, "slots", torch.int32, (B,), dev)
+    ctx, stream = _on_device(dev, stream)
+    with ctx:
+        if y is None:
+            y = torch.empty(B, Hq, dv, dtype=q.dtype, device=dev)
+            _made_here(stream, dev, y)
+        _need_tensor(y, "y", q.dtype, (B, Hq, dv), dev)
+        _check(lib.oal_gated_decode_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), dt,
+                                         g.data_ptr(), B, Hq, Hkv, d, dv, float(scale),
+                                         None if slots is None else slots.data_ptr(), n,
+                                         state.data_ptr(), y.data_ptr(), stream.cuda_stream))
+    return y
+
+
+def oal_state_remap(pool, map, stream=None):
+    """Moves the slots of `pool` (first dimension: slots) in place:
+    new[i] = old[map[i]], zeros where map[i] is -1; map [n] int32 (CUDA).
+    Copies, forks, compacts and frees states of any kind.  Returns pool."""
+    lib = load_library()
+    _need(pool.dim() >= 1, "pool must have a dimension of slots")
+    n, dev = pool.shape[0], pool.device
+    _need_tensor(pool, "pool", pool.dtype, pool.shape, dev)
+    _need_tensor(map, "map", torch.int32, (n,), dev)
+    ctx, stream = _on_device(dev, stream)
+    with ctx:
+        _check(lib.oal_state_remap(pool.data_ptr(), pool[0].numel() * pool.element_size() if n else 0,
+                                   n, map.data_ptr(), stream.cuda_stream))
+    return pool
 
 
 def oal_sync_status(stream=None):

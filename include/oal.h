@@ -230,6 +230,100 @@ oal_status oal_decode_step(const void *q, const void *k, const void *v,
                            size_t workspace_bytes, cudaStream_t stream);
 
 /*
+ * The gated linear recurrence, for the layers that forget.  Per (batch, KV
+ * head), with a log decay g_t per token and a state S of d x dv:
+ *     S_t = exp(g_t) S_{t-1} + k_t v_t^T,     y_t = scale S_t^T q_t.
+ * Query heads share the state of their KV head as above.  g is the natural
+ * logarithm of the gate, fp32, at most 0 in use; a value of -104 or less (-inf
+ * among them), where exp gives 0 in fp32, starts from nothing, as at the
+ * first token of a packed document.  NaN and +inf gates and inputs that are
+ * not finite make the results of their sequence unspecified.
+ * Supported: d == dv == 64.  State layout: [B][Hkv][d][dv] fp32.
+ *
+ * oal_gated_prefill -- T tokens.
+ *  Q [B][Hq][T][d], K [B][Hkv][T][d], V [B][Hkv][T][dv] in `dtype`,
+ *  g [B][Hkv][T] fp32, Y [B][Hq][T][dv] in `dtype`.
+ *  lengths  [B] int32 (device): tokens of each sequence, 0..T; NULL = T each.
+ *           Rows behind a sequence's length are neither read nor written; the
+ *           state is that after its last token.  A length outside 0..T is
+ *           clamped and recorded in the device status word
+ *           (OAL_ERR_INVALID_ARG at oal_sync_status).
+ *  state    in/out; continue_from_state != 0 starts from it, 0 from zeros.
+ *  workspace  >= oal_gated_prefill_workspace_bytes(...) bytes, 256-byte
+ *           aligned, contents need not be initialised.  Calls that may
+ *           overlap on the GPU (streams, captured graphs) need one each.
+ * Arithmetic: fp32 sums and states.  T == 0 leaves Y untouched and zeroes
+ * the state unless continue_from_state != 0.
+ */
+size_t oal_gated_prefill_workspace_bytes(int B, int Hq, int Hkv, int T, int d, int dv,
+                                         oal_dtype dtype);
+oal_status oal_gated_prefill(const void *Q, const void *K, const void *V, oal_dtype dtype,
+                             const float *g, int B, int Hq, int Hkv, int T, int d, int dv,
+                             float scale, const int32_t *lengths, float *state,
+                             int continue_from_state, void *Y, void *workspace,
+                             size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * oal_gated_backward -- gradients of <dY, Y> + <dstate, S_T> for
+ * oal_gated_prefill from state0.  With dS_t = scale q_t dy_t^T (summed over
+ * the query heads of the KV head) + exp(g_{t+1}) dS_{t+1}, dS_T plus dstate:
+ *     dq_t = scale S_t dy_t,  dk_t = dS_t v_t,  dv_t = dS_t^T k_t,
+ *     dg_t = exp(g_t) <S_{t-1}, dS_t>  (0 where g_t is -104 or less),
+ *     dstate0 = exp(g_0) dS_0.
+ *  state0, dstate  [B][Hkv][d][dv] fp32 or NULL (zeros).
+ *  dQ, dK, dV  as Q, K, V in `dtype`, rounded once from fp32 (dK and dV after
+ *           the sum over query heads); dg [B][Hkv][T] fp32; dstate0 as
+ *           state0, or NULL if not wanted.  No output may overlap an input or
+ *           another output.  Rows behind a sequence's length
+ *           are neither read nor written.
+ * Deterministic: no atomics on the outputs.  T == 0: dstate0 = dstate.
+ */
+size_t oal_gated_backward_workspace_bytes(int B, int Hq, int Hkv, int T, int d, int dv,
+                                          oal_dtype dtype);
+oal_status oal_gated_backward(const void *Q, const void *K, const void *V, oal_dtype dtype,
+                              const float *g, const void *dY, int B, int Hq, int Hkv, int T,
+                              int d, int dv, float scale, const int32_t *lengths,
+                              const float *state0, const float *dstate, void *dQ, void *dK,
+                              void *dV, float *dg, float *dstate0, void *workspace,
+                              size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * oal_gated_decode_step -- one token for B sequences whose states are slots
+ * of a pool state [n_slots][Hkv][d][dv] (in/out).
+ *  q [B][Hq][d], k [B][Hkv][d], v [B][Hkv][dv] in `dtype`, g [B][Hkv] fp32,
+ *  y [B][Hq][dv] in `dtype`.
+ *  slots  [B] int32 (device), the slot of each sequence; NULL = slot b for
+ *         sequence b.  -1: no sequence here, y is 0 and no state changes (the
+ *         spare rows of a captured graph).  A slot outside -1..n_slots-1, or
+ *         one that an earlier sequence of the batch holds, counts as -1 and
+ *         is recorded in the device status word (OAL_ERR_INVALID_ARG).
+ * Arithmetic: fp32 on the CUDA cores.  No workspace.
+ */
+oal_status oal_gated_decode_step(const void *q, const void *k, const void *v, oal_dtype dtype,
+                                 const float *g, int B, int Hq, int Hkv, int d, int dv,
+                                 float scale, const int32_t *slots, int n_slots, float *state,
+                                 void *y, cudaStream_t stream);
+
+/*
+ * oal_state_remap -- moves the slots of a pool of states in place:
+ *     new[i] = old[map[i]]  for map[i] in 0..n_slots-1,  zeros for -1.
+ * One table copies, forks (a source named several times), compacts and frees
+ * (-1), as if all of old were read before new is written.  The pool may hold
+ * anything whose slots are contiguous and equally long: the states of
+ * oal_decode_step and oal_gated_decode_step alike.
+ *  pool  n_slots * slot_bytes bytes (device); any slot_bytes, fastest at a multiple
+ *        of 16.
+ *  map   [n_slots] int32 (device), not inside the pool.  An entry outside
+ *        -1..n_slots-1 leaves its slot as it is and is recorded in the device
+ *        status word (OAL_ERR_INVALID_ARG).
+ * A slot that maps to itself is neither read nor written.  No workspace.
+ * Supported: n_slots <= OAL_REMAP_MAX_SLOTS.
+ */
+#define OAL_REMAP_MAX_SLOTS 8192
+oal_status oal_state_remap(void *pool, size_t slot_bytes, int n_slots, const int32_t *map,
+                           cudaStream_t stream);
+
+/*
  * Calibration, the step before the path ([OAL] Sec. 3.1 and App. B "Dimension
  * grouping"): the groups of each query head follow from contribution scores.
  *

@@ -1,0 +1,527 @@
+"""Gated recurrence (prefill, decode step, backward) and state remap on a GPU,
+against the definitions in 64 bits, one token after another.
+
+Tolerances, rel-L2 over a tensor:
+  * fp32 inputs: every output is a sum of at most a few thousand products in
+    fp32; independent roundings grow like sqrt(n) 2^-24, 4e-6 at n = 4096;
+    1e-5 leaves room for the few sums in a row that an output passes.
+  * bf16 inputs, bf16 outputs: three roundings to bf16 (a score, a state, the
+    result), each off by at most 2^-8 of its value: 3 * 2^-8 = 1.2e-2.
+  * bf16 inputs, fp32 outputs (states and their gradients): one factor of each
+    product is held as two bf16 terms, off by at most 2^-16; with the fp32 sums
+    2^-16 + 4e-6 < 2e-5.  dg is a sum of four such parts: 2 * 2^-16 < 3.1e-5,
+    4e-5 with the sums.
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+SCALE = 0.125
+OUT = {torch.float32: 1e-5, torch.bfloat16: 3 * 2.0 ** -8}
+STATE = {torch.float32: 1e-5, torch.bfloat16: 2e-5}
+DG = {torch.float32: 1e-5, torch.bfloat16: 4e-5}
+DTYPES = [torch.float32, torch.bfloat16]
+
+
+@pytest.fixture(scope="module")
+def oal():
+    from grouped_quadratic_gb300 import build, oal as binding
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    build.build()
+    binding.load_library()
+    return binding
+
+
+class Case:
+    def __init__(self, dtype, B, Hq, Hkv, T, seed=0, cut=0.0, span=30.0, lengths=None):
+        gen = torch.Generator().manual_seed(1000 + seed)
+        n = lambda *s: torch.randn(*s, generator=gen)
+        self.dtype, self.B, self.Hq, self.Hkv, self.T = dtype, B, Hq, Hkv, T
+        self.Q, self.dY = (n(B, Hq, T, 64).to(dtype).cuda() for _ in range(2))
+        self.K, self.V = (n(B, Hkv, T, 64).to(dtype).cuda() for _ in range(2))
+        self.g = torch.nn.functional.logsigmoid(n(B, Hkv, T) + math.log(span))
+        if cut:
+            self.g[torch.rand(B, Hkv, T, generator=gen) < cut] = -math.inf
+        self.g = self.g.cuda()
+        self.state0, self.dstate = (n(B, Hkv, 64, 64).cuda() for _ in range(2))
+        self.lengths = None if lengths is None else torch.tensor(lengths, dtype=torch.int32).cuda()
+
+    def rows(self, like):
+        """Which rows of a [B, H, T, ...] tensor are inside their sequence."""
+        n = self.lengths.tolist() if self.lengths is not None else [self.T] * self.B
+        m = torch.tensor([[t < x for t in range(self.T)] for x in n], dtype=torch.bool).cuda()
+        return m.view(self.B, 1, self.T, *[1] * (like.dim() - 3)).expand_as(like)
+
+
+def oracle(c, state0=None, dstate=None, backward=False, scale=SCALE):
+    """fp64: Y and the last state, or dQ, dK, dV, dg, dstate0."""
+    B, Hkv, T, rho = c.B, c.Hkv, c.T, c.Hq // c.Hkv
+    n = c.lengths.tolist() if c.lengths is not None else [T] * B
+    Q, K, V, g, dY = (x.double().cpu() for x in (c.Q, c.K, c.V, c.g, c.dY))
+    Q, dY = Q.view(B, Hkv, rho, T, 64), dY.view(B, Hkv, rho, T, 64)
+    first = torch.zeros(B, Hkv, 64, 64, dtype=torch.float64) if state0 is None else state0.double().cpu()
+    last = torch.zeros_like(first) if dstate is None else dstate.double().cpu()
+    Y, dQ = torch.zeros_like(Q), torch.zeros_like(Q)
+    dK, dV, dg = torch.zeros_like(K), torch.zeros_like(V), torch.zeros_like(g)
+    S_end, dS0 = first.clone(), last.clone()
+    for b in range(B):
+        S, path = first[b], [first[b]]
+        for t in range(min(max(n[b], 0), T)):
+            S = g[b, :, t].exp()[:, None, None] * S + K[b, :, t, :, None] * V[b, :, t, None, :]
+            path.append(S)
+            Y[b, :, :, t] = scale * torch.einsum("hrd,hde->hre", Q[b, :, :, t], S)
+            dQ[b, :, :, t] = scale * torch.einsum("hre,hde->hrd", dY[b, :, :, t], S)
+        S_end[b] = S
+        if not backward:
+            continue
+        R = last[b]
+        for t in reversed(range(len(path) - 1)):
+            R = R + scale * torch.einsum("hrd,hre->hde", Q[b, :, :, t], dY[b, :, :, t])
+            dK[b, :, t] = torch.einsum("hde,he->hd", R, V[b, :, t])
+            dV[b, :, t] = torch.einsum("hde,hd->he", R, K[b, :, t])
+            R = g[b, :, t].exp()[:, None, None] * R
+            dg[b, :, t] = (R * path[t]).sum((-1, -2))
+        dS0[b] = R
+    if not backward:
+        return Y.view(B, c.Hq, T, 64), S_end
+    return dQ.view(B, c.Hq, T, 64), dK, dV, dg, dS0
+
+
+def rel(got, want):
+    got, want = got.double().cpu(), want.double().cpu()
+    assert torch.isfinite(got).all()
+    return float((got - want).norm() / max(float(want.norm()), 1e-30))
+
+
+def run_forward(oal, c, cont=False, **kw):
+    state = c.state0.clone() if cont else torch.full_like(c.state0, math.nan)
+    Y = torch.full_like(c.Q, 7.0)
+    oal.oal_gated_prefill(c.Q, c.K, c.V, c.g, SCALE, lengths=c.lengths, state=state,
+                          continue_from_state=cont, Y=Y, **kw)
+    oal.oal_sync_status()
+    return Y, state
+
+
+def check_forward(oal, c, cont):
+    Y, state = run_forward(oal, c, cont)
+    want, S = oracle(c, c.state0 if cont else None)
+    inside = c.rows(Y)
+    assert (Y[~inside] == 7.0).all()                       # rows behind a sequence stay
+    assert rel(torch.where(inside, Y, 0), want) <= OUT[c.dtype]
+    assert rel(state, S) <= STATE[c.dtype]
+
+
+def check_backward(oal, c, cont):
+    out = [torch.full_like(x, 7.0) for x in (c.Q, c.K, c.V, c.g)]
+    got = oal.oal_gated_backward(c.Q, c.K, c.V, c.g, c.dY, SCALE, lengths=c.lengths,
+                                 state0=c.state0 if cont else None, dstate=c.dstate if cont else None,
+                                 dQ=out[0], dK=out[1], dV=out[2], dg=out[3])
+    oal.oal_sync_status()
+    want = oracle(c, c.state0 if cont else None, c.dstate if cont else None, backward=True)
+    tol = [OUT[c.dtype]] * 3 + [DG[c.dtype], STATE[c.dtype]]
+    for name, a, w, t in zip(("dQ", "dK", "dV", "dg", "dstate0"), got, want, tol):
+        if name != "dstate0":
+            assert (a[~c.rows(a)] == 7.0).all(), name
+            a = torch.where(c.rows(a), a, 0)
+        if w.norm() == 0:                                  # one token from no state
+            assert (a == 0).all(), name
+        else:
+            assert rel(a, w) <= t, (name, rel(a, w))
+
+
+SHAPES = [  # B, Hq, Hkv, T, cut, lengths, cont
+    (1, 1, 1, 1, 0.0, None, False), (1, 1, 1, 1, 0.0, None, True), (2, 3, 3, 2, 0.3, None, True),
+    (1, 2, 1, 63, 0.0, None, False), (1, 2, 2, 64, 0.0, None, True), (2, 2, 1, 65, 0.05, None, True),
+    (1, 7, 1, 128, 0.0, None, False), (1, 14, 2, 129, 0.02, None, True), (2, 10, 2, 191, 0.0, [191, 17], False),
+    (4, 4, 2, 333, 0.01, [0, 1, 333, 64], True), (1, 4, 4, 640, 0.0, None, False),
+    (3, 9, 1, 257, 1.0, [257, 256, 3], True), (1, 8, 1, 2050, 0.001, None, True)]
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["f32", "bf16"])
+@pytest.mark.parametrize("B,Hq,Hkv,T,cut,lengths,cont", SHAPES)
+def test_prefill(oal, dtype, B, Hq, Hkv, T, cut, lengths, cont):
+    check_forward(oal, Case(dtype, B, Hq, Hkv, T, seed=T + B, cut=cut, lengths=lengths), cont)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["f32", "bf16"])
+@pytest.mark.parametrize("B,Hq,Hkv,T,cut,lengths,cont", SHAPES)
+def test_backward(oal, dtype, B, Hq, Hkv, T, cut, lengths, cont):
+    check_backward(oal, Case(dtype, B, Hq, Hkv, T, seed=T + B + 1, cut=cut, lengths=lengths), cont)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["f32", "bf16"])
+@pytest.mark.parametrize("gate", [0.0, -1e-4, -3.0, -60.0, -103.0, -104.0, -2e38, -math.inf])
+def test_one_gate_everywhere(oal, dtype, gate):
+    c = Case(dtype, 1, 4, 2, 200, seed=3)
+    c.g = torch.full_like(c.g, gate)
+    check_forward(oal, c, True)
+    check_backward(oal, c, True)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["f32", "bf16"])
+def test_gates_of_very_different_size(oal, dtype):
+    """A large drop must not cost the digits of the small ones behind it."""
+    c = Case(dtype, 1, 4, 2, 300, seed=4, span=500.0)
+    c.g[:, :, 5::23] = -90.0
+    c.g[:, :, 11::31] = -40.0
+    check_forward(oal, c, True)
+    check_backward(oal, c, True)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["f32", "bf16"])
+def test_growing_gates(oal, dtype):
+    c = Case(dtype, 1, 4, 2, 150, seed=5)
+    c.g = c.g.abs() * 0.2
+    check_forward(oal, c, True)
+    check_backward(oal, c, True)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["f32", "bf16"])
+def test_many_segments(oal, dtype):
+    c = Case(dtype, 1, 2, 1, 6000, seed=6, span=2000.0)
+    check_forward(oal, c, True)
+    check_backward(oal, c, True)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["f32", "bf16"])
+def test_padding_is_not_read(oal, dtype):
+    lengths = [70, 0, 200]
+    c = Case(dtype, 3, 4, 2, 200, seed=7, lengths=lengths)
+    Y0, S0 = run_forward(oal, c, True)
+    G0 = oal.oal_gated_backward(c.Q, c.K, c.V, c.g, c.dY, SCALE, lengths=c.lengths, state0=c.state0)
+    for b, n in enumerate(lengths):
+        for x in (c.Q, c.K, c.V, c.g, c.dY):
+            x[b, :, n:] = math.nan
+    Y1, S1 = run_forward(oal, c, True)
+    G1 = oal.oal_gated_backward(c.Q, c.K, c.V, c.g, c.dY, SCALE, lengths=c.lengths, state0=c.state0)
+    oal.oal_sync_status()
+    assert torch.equal(Y0, Y1) and torch.equal(S0, S1)
+    assert all(torch.equal(a, b) for a, b in zip(G0, G1))
+
+
+def test_made_here_rows_are_zero(oal):
+    c = Case(torch.bfloat16, 2, 2, 1, 100, seed=8, lengths=[40, 100])
+    Y, _ = oal.oal_gated_prefill(c.Q, c.K, c.V, c.g, lengths=c.lengths)
+    G = oal.oal_gated_backward(c.Q, c.K, c.V, c.g, c.dY, lengths=c.lengths)
+    oal.oal_sync_status()
+    for x in (Y,) + G[:4]:
+        assert (x[0, :, 40:] == 0).all()
+
+
+@pytest.mark.parametrize("bad", [-1, 51])
+def test_length_out_of_range_is_recorded(oal, bad):
+    c = Case(torch.float32, 2, 2, 1, 50, seed=9)
+    lengths = torch.tensor([50, bad], dtype=torch.int32).cuda()
+    Y, S = oal.oal_gated_prefill(c.Q, c.K, c.V, c.g, SCALE, lengths=lengths)
+    with pytest.raises(oal.OALError) as e:
+        oal.oal_sync_status()
+    assert e.value.status == oal.OAL_ERR_INVALID_ARG
+    oal.oal_gated_backward(c.Q, c.K, c.V, c.g, c.dY, SCALE, lengths=lengths)
+    with pytest.raises(oal.OALError):
+        oal.oal_sync_status()
+    oal.oal_sync_status()
+    c.lengths = torch.tensor([50, max(0, min(50, bad))], dtype=torch.int32).cuda()   # clamped
+    want, S64 = oracle(c)
+    assert rel(Y, want) <= OUT[c.dtype] and rel(S, S64) <= STATE[c.dtype]
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["f32", "bf16"])
+def test_empty_sequences(oal, dtype):
+    c = Case(dtype, 2, 2, 1, 0, seed=10)
+    _, S = run_forward(oal, c, False)
+    assert (S == 0).all()
+    _, S = run_forward(oal, c, True)
+    assert torch.equal(S, c.state0)
+    out = oal.oal_gated_backward(c.Q, c.K, c.V, c.g, c.dY, dstate=c.dstate)
+    assert torch.equal(out[4], c.dstate)
+    assert (oal.oal_gated_backward(c.Q, c.K, c.V, c.g, c.dY)[4] == 0).all()
+    none = Case(dtype, 0, 2, 1, 5, seed=11)
+    oal.oal_gated_prefill(none.Q, none.K, none.V, none.g)
+    oal.oal_gated_backward(none.Q, none.K, none.V, none.g, none.dY)
+    oal.oal_sync_status()
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["f32", "bf16"])
+def test_later_tokens_change_nothing_before(oal, dtype):
+    c = Case(dtype, 1, 4, 2, 500, seed=12)
+    Y0, _ = run_forward(oal, c)
+    for x in (c.Q, c.K, c.V):
+        x[:, :, 331:] = 3.0
+    c.g[:, :, 331:] = -1.0
+    Y1, _ = run_forward(oal, c)
+    assert torch.equal(Y0[:, :, :331], Y1[:, :, :331])
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["f32", "bf16"])
+def test_two_calls_of_the_same_agree_bit_for_bit(oal, dtype):
+    c = Case(dtype, 2, 14, 2, 1500, seed=13)
+    a, b = run_forward(oal, c, True), run_forward(oal, c, True)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    x, y = (oal.oal_gated_backward(c.Q, c.K, c.V, c.g, c.dY, state0=c.state0, dstate=c.dstate) for _ in range(2))
+    assert all(torch.equal(p, q) for p, q in zip(x, y))
+
+
+def test_gradients_against_differences(oal):
+    """fp32: <gradient, direction> against central differences of the oracle's
+    <dY, Y> + <dstate, S_T> (64 bits, step 1e-4: error 1e-8; 1e-5 is the fp32
+    gradients' own)."""
+    c = Case(torch.float32, 2, 4, 2, 90, seed=14, cut=0.02, lengths=[90, 77])
+    got = oal.oal_gated_backward(c.Q, c.K, c.V, c.g, c.dY, SCALE, lengths=c.lengths, state0=c.state0,
+                                 dstate=c.dstate)
+    oal.oal_sync_status()
+    gen = torch.Generator().manual_seed(5)
+    base = dict(Q=c.Q, K=c.K, V=c.V, g=c.g, state0=c.state0)
+    inside = c.rows(c.Q).cpu()
+
+    def value(**kw):
+        class X:
+            pass
+        x = X()
+        x.__dict__.update(c.__dict__)
+        for k, v in kw.items():
+            setattr(x, k, v)
+        Y, S = oracle(x, x.state0)
+        return float((Y * c.dY.double().cpu() * inside).sum() + (S * c.dstate.double().cpu()).sum())
+
+    for name, grad in zip(("Q", "K", "V", "g", "state0"), got):
+        x = base[name].double()
+        way = torch.randn(x.shape, generator=gen, dtype=torch.float64).cuda()
+        h = 1e-4
+        diff = (value(**{name: x + h * way}) - value(**{name: x - h * way})) / (2 * h)
+        if name == "g":
+            way = torch.where(torch.isinf(x), 0.0, way)
+        mine = float((grad.double() * way).sum())
+        assert abs(mine - diff) <= 1e-5 * float(grad.double().norm() * way.norm()), (name, mine, diff)
+
+
+# ---------------------------------------------------------------- decode
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["f32", "bf16"])
+@pytest.mark.parametrize("B,Hq,Hkv,n", [(1, 1, 1, 1), (1, 14, 2, 4), (3, 34, 2, 7), (40, 32, 8, 64), (160, 2, 1, 160)])
+def test_decode(oal, dtype, B, Hq, Hkv, n):
+    c = Case(dtype, B, Hq, Hkv, 1, seed=B)
+    gen = torch.Generator().manual_seed(B)
+    pool = torch.randn(n, Hkv, 64, 64, generator=gen).cuda()
+    slots = torch.randperm(n, generator=gen)[:B]
+    c.g[0, 0, 0] = -math.inf                         # this one starts from nothing
+    before = pool.clone()
+    want, S = oracle(c, pool[slots.cuda()])
+    y = oal.oal_gated_decode_step(c.Q[:, :, 0].contiguous(), c.K[:, :, 0].contiguous(), c.V[:, :, 0].contiguous(),
+                                  c.g[:, :, 0].contiguous(), pool, SCALE, slots=slots.to(torch.int32).cuda())
+    oal.oal_sync_status()
+    # the state is not rounded here: bf16 only at the end
+    assert rel(y, want[:, :, 0]) <= (1e-5 if dtype == torch.float32 else 2.0 ** -8)
+    assert rel(pool[slots.cuda()], S) <= 1e-5
+    rest = torch.ones(n, dtype=torch.bool)
+    rest[slots] = False
+    assert torch.equal(pool[rest.cuda()], before[rest.cuda()])
+
+
+def test_decode_spare_rows_and_bad_slots(oal):
+    c = Case(torch.bfloat16, 6, 4, 2, 1, seed=20)
+    args = [x[:, :, 0].contiguous() for x in (c.Q, c.K, c.V, c.g)]
+    pool = torch.randn(5, 2, 64, 64, generator=torch.Generator().manual_seed(1)).cuda()
+    ref = pool.clone()
+    y0 = oal.oal_gated_decode_step(*[a[:2].contiguous() for a in args], ref, slots=torch.tensor([3, 1], dtype=torch.int32).cuda())
+    oal.oal_sync_status()
+    got = pool.clone()
+    y = oal.oal_gated_decode_step(*args, got, slots=torch.tensor([3, 1, -1, -1, -1, -1], dtype=torch.int32).cuda())
+    oal.oal_sync_status()                                       # -1 is no error
+    assert torch.equal(y[:2], y0) and (y[2:] == 0).all() and torch.equal(got, ref)
+    for bad in ([3, 1, 5, -1, -1, -1], [3, 1, -2, -1, -1, -1], [3, 1, 3, -1, 1, -1]):
+        got = pool.clone()
+        y = oal.oal_gated_decode_step(*args, got, slots=torch.tensor(bad, dtype=torch.int32).cuda())
+        with pytest.raises(oal.OALError) as e:
+            oal.oal_sync_status()
+        assert e.value.status == oal.OAL_ERR_INVALID_ARG
+        assert torch.equal(y[:2], y0) and (y[2:] == 0).all() and torch.equal(got, ref)
+
+
+# ---------------------------------------------------------------- remap
+
+def remapped(pool, table):
+    new = pool.clone()
+    for i, j in enumerate(table):
+        new[i] = pool[j] if j >= 0 else 0
+    return new
+
+
+@pytest.mark.parametrize("n,shape,dtype", [
+    (1, (4,), torch.float32), (2, (3,), torch.uint8), (7, (2, 5), torch.bfloat16), (5, (16640,), torch.float32),
+    (33, (64, 64), torch.float32), (8, (2, 2145, 65), torch.float32), (700, (67,), torch.float32), (8192, (2, 2), torch.float32),
+    (8192, (5,), torch.int16), (3, (1 << 21,), torch.float32), (1100, (129, 2), torch.float32)])
+@pytest.mark.parametrize("kind", ["random", "cycle", "swap", "free", "fork", "stay"])
+def test_remap(oal, n, shape, dtype, kind):
+    gen = torch.Generator().manual_seed(n)
+    pool = torch.randint(0, 200, (n,) + shape, generator=gen).to(dtype).cuda()
+    table = list(range(n))
+    if kind == "random":
+        table = torch.randint(-1, n, (n,), generator=gen).tolist()
+    elif kind == "cycle":
+        table = [(i + 1) % n for i in range(n)]
+    elif kind == "swap":
+        table[0], table[-1] = n - 1, 0
+    elif kind == "free":
+        table = [-1] * n
+    elif kind == "fork":
+        table = [n // 2] * n
+    want = remapped(pool, table)
+    out = oal.oal_state_remap(pool, torch.tensor(table, dtype=torch.int32).cuda())
+    oal.oal_sync_status()
+    assert out is pool and torch.equal(pool, want)
+
+
+def test_remap_bad_entries_stay_and_are_recorded(oal):
+    pool = torch.randn(6, 40, generator=torch.Generator().manual_seed(2)).cuda()
+    want = remapped(pool, [5, 1, 2, 0, -1, 5])
+    oal.oal_state_remap(pool, torch.tensor([5, 6, -2, 0, -1, 5], dtype=torch.int32).cuda())
+    with pytest.raises(oal.OALError) as e:
+        oal.oal_sync_status()
+    assert e.value.status == oal.OAL_ERR_INVALID_ARG
+    assert torch.equal(pool, want)
+
+
+# ---------------------------------------------------------------- together
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["f32", "bf16"])
+def test_serving_run(oal, dtype):
+    """Prompts of unequal length, a fork, decode steps on slots, an end with
+    compaction, more steps: against the oracle over each sequence's own tokens."""
+    B, Hq, Hkv, T, steps = 3, 4, 2, 130, 4
+    lengths = [130, 50, 97]
+    c = Case(dtype, B, Hq, Hkv, T, seed=30, lengths=lengths)
+    pool = torch.zeros(6, Hkv, 64, 64).cuda()
+    oal.oal_gated_prefill(c.Q, c.K, c.V, c.g, SCALE, lengths=c.lengths, state=pool[:B])
+    # slot 3 forks sequence 0, slot 4 forks sequence 2
+    oal.oal_state_remap(pool, torch.tensor([0, 1, 2, 0, 2, -1], dtype=torch.int32).cuda())
+    parents = [0, 1, 2, 0, 2]
+    new = Case(dtype, 5, Hq, Hkv, 2 * steps, seed=31)
+    live, ys = [0, 1, 2, 3, 4], {}
+    for t in range(2 * steps):
+        if t == steps:       # sequences 1 and 2 end; 3 and 4 move into their slots
+            oal.oal_state_remap(pool, torch.tensor([0, 3, 4, -1, -1, -1], dtype=torch.int32).cuda())
+            live = [0, 3, 4]
+        rows = torch.tensor(live).cuda()
+        y = oal.oal_gated_decode_step(*[x[rows, :, t].contiguous() for x in (new.Q, new.K, new.V, new.g)], pool, SCALE,
+                                      slots=torch.arange(len(live), dtype=torch.int32).cuda())
+        for i, s in enumerate(live):
+            ys[s, t] = y[i]
+    oal.oal_sync_status()
+    assert (pool[3:] == 0).all()
+    for s in range(5):
+        p, end = parents[s], 2 * steps if s in (0, 3, 4) else steps
+        n = lengths[p]
+        one = Case(dtype, 1, Hq, Hkv, n + end, seed=0)
+        for name in ("Q", "K", "V", "g"):
+            setattr(one, name, torch.cat([getattr(c, name)[p:p + 1, :, :n], getattr(new, name)[s:s + 1, :, :end]], 2))
+        want, S = oracle(one)
+        got = torch.stack([ys[s, t] for t in range(end)], 1)[None]
+        assert rel(got, want[:, :, n:]) <= OUT[dtype]
+        if s in (0, 3, 4):
+            assert rel(pool[[0, 3, 4].index(s)][None], S) <= STATE[dtype]
+
+
+def test_prefix_states_of_the_quadratic_kernel_move_too(oal):
+    """oal_decode_step on states that were forked and moved by a remap."""
+    from grouped_quadratic_gb300 import inputs
+    w = inputs.make_workload("remap", B=2, Hq=4, Hkv=2, T=70, G=3, dtype="f32", seed=77)
+    Q, K, V = w.torch_inputs("cuda")
+    L, group = torch.from_numpy(w.L).cuda(), torch.from_numpy(w.group).cuda()
+    lay = oal.OAL_STATE_PACKED
+    a, b, C = oal.oal_expand_coeffs(L, group, w.eps, lay)
+    pool = torch.zeros(4, 2, oal.oal_state_rows(64, lay), 65, device="cuda")
+    first = [x[:, :, :69].contiguous() for x in (Q, K, V)]
+    oal.oal_prefill(*first, L, group, w.eps, a, b, C, lay, state=pool[:2])
+    oal.oal_state_remap(pool, torch.tensor([1, 0, 1, -1], dtype=torch.int32).cuda())
+    last = [x[:, :, 69] for x in (Q, K, V)]
+    order = [1, 0, 1]
+    y = oal.oal_decode_step(*[x[order].contiguous() for x in last], a, b, C, pool[:3], lay)
+    Y, _ = oal.oal_prefill(Q, K, V, L, group, w.eps, a, b, C, lay)
+    oal.oal_sync_status()
+    assert torch.equal(y[0], y[2])
+    assert rel(y, Y[order][:, :, 69]) <= 1e-5
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["f32", "bf16"])
+def test_prefill_in_parts(oal, dtype):
+    c = Case(dtype, 2, 4, 2, 300, seed=32)
+    state = torch.empty(2, 2, 64, 64, device="cuda")
+    ys, at = [], 0
+    for n in (1, 64, 100, 135):
+        part = [x[:, :, at:at + n].contiguous() for x in (c.Q, c.K, c.V, c.g)]
+        y, _ = oal.oal_gated_prefill(*part, SCALE, state=state, continue_from_state=at > 0)
+        ys.append(y)
+        at += n
+    oal.oal_sync_status()
+    want, S = oracle(c)
+    assert rel(torch.cat(ys, 2), want) <= OUT[dtype] and rel(state, S) <= STATE[dtype]
+
+
+def test_captured_and_replayed(oal):
+    """A prefill, a backward, a decode step and a remap in one graph, replayed
+    on new inputs in the same buffers."""
+    c, d = Case(torch.bfloat16, 2, 4, 2, 700, seed=40), Case(torch.bfloat16, 2, 4, 2, 700, seed=41)
+    q, k, v, g = (x[:, :, 0].contiguous() for x in (d.Q, d.K, d.V, d.g))
+    slots, table = torch.tensor([1, 0], dtype=torch.int32).cuda(), torch.tensor([1, 0], dtype=torch.int32).cuda()
+
+    def step(state):
+        Y, _ = oal.oal_gated_prefill(c.Q, c.K, c.V, c.g, SCALE, state=state)
+        grads = oal.oal_gated_backward(c.Q, c.K, c.V, c.g, c.dY, SCALE)
+        oal.oal_state_remap(state, table)
+        return (Y,) + grads + (oal.oal_gated_decode_step(q, k, v, g, state, SCALE, slots=slots),)
+
+    state = torch.empty(2, 2, 64, 64, device="cuda")
+    step(state)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step(state)
+    for src in (d, Case(torch.bfloat16, 2, 4, 2, 700, seed=42)):
+        for name in ("Q", "K", "V", "g", "dY"):
+            getattr(c, name).copy_(getattr(src, name))
+        graph.replay()
+        torch.cuda.synchronize()
+        again = torch.empty_like(state)
+        want = step(again)
+        oal.oal_sync_status()
+        assert all(torch.equal(x, y) for x, y in zip(out, want)) and torch.equal(state, again)
+
+
+def test_on_another_stream(oal):
+    c = Case(torch.bfloat16, 2, 14, 2, 3000, seed=43)
+    want = run_forward(oal, c, True)
+    grads = oal.oal_gated_backward(c.Q, c.K, c.V, c.g, c.dY, state0=c.state0)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    got = []
+    for _ in range(3):
+        got.append(run_forward(oal, c, True, stream=side))
+        more = oal.oal_gated_backward(c.Q, c.K, c.V, c.g, c.dY, state0=c.state0, stream=side)
+        torch.full((1 << 22,), math.nan, device="cuda")     # would land in scratch that was freed too early
+        side.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(grads, more))
+    oal.oal_sync_status()
+    assert all(torch.equal(x, y) for g in got for x, y in zip(g, want))
+
+
+def test_offsets_beyond_32_bits(oal):
+    """More than 2^32 bytes and 2^31 elements of Q and Y: the last rows against
+    a call on the last part alone that goes on from the state before it."""
+    T, Hq, tail = 1 << 20, 36, 1000
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    Q = torch.randn(1, Hq, T, 64, generator=gen, device="cuda", dtype=torch.bfloat16)
+    assert Q.numel() > 1 << 31
+    K, V = (torch.randn(1, 1, T, 64, generator=gen, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    g = torch.full((1, 1, T), -0.01, device="cuda")
+    Y, S = oal.oal_gated_prefill(Q, K, V, g)
+    cut = lambda a, b: [x[:, :, a:b].contiguous() for x in (Q, K, V, g)]
+    _, S0 = oal.oal_gated_prefill(*cut(T - tail - 4000, T - tail))       # exp(-40) of what is before
+    y, s = oal.oal_gated_prefill(*cut(T - tail, T), state=S0, continue_from_state=True)
+    oal.oal_sync_status()
+    assert rel(Y[:, :, T - tail:], y) <= OUT[torch.bfloat16]
+    assert rel(S, s) <= STATE[torch.bfloat16]
