@@ -11,7 +11,6 @@ Tensor layouts (row-major, contiguous, CUDA):
   state [B,Hkv,F,65] float32 (F = 4161 FULL, 2145 PACKED)
   gated recurrence: g [B,Hkv,T] float32 (log decays), state [B,Hkv,64,64] float32
 """
-import contextlib
 import ctypes
 import os
 
@@ -345,35 +344,39 @@ def _need(ok, what):
 
 
 def _need_tensor(t, name, dtype, shape, dev):
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+    if t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous():
+        return
+    if t.dtype != dtype or t.shape != shape:
         raise OALError(OAL_ERR_INVALID_ARG, "%s must be %s %s (got %s %s)"
                        % (name, dtype, tuple(shape), t.dtype, tuple(t.shape)))
-    if t.device != dev or not t.is_cuda or not t.is_contiguous():
-        raise OALError(OAL_ERR_INVALID_ARG, "%s must be a contiguous CUDA tensor on %s" % (name, dev))
+    raise OALError(OAL_ERR_INVALID_ARG, "%s must be contiguous on %s" % (name, dev))
 
 
-def _on_device(dev, stream):
-    """(context that makes dev current, stream of dev to launch on).  Without a
-    stream argument: the current stream of the tensors' device."""
+def _elsewhere(dev):
+    """Whether dev is a CUDA device other than the current one (the call then
+    repeats itself with dev current)."""
     if dev.type != "cuda":
         raise OALError(OAL_ERR_INVALID_ARG, "tensors must be contiguous CUDA tensors")
+    return dev.index != torch.cuda.current_device()
+
+
+def _stream_on(dev, stream, made):
+    """The handle to launch on: that of `stream`, or of the current stream of
+    dev.  `made`: tensors this call allocated, from the current stream's pool;
+    their memory must not be handed out again before `stream` is done with it."""
     if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    elif stream.device != dev:
+        return torch._C._cuda_getCurrentRawStream(dev.index)
+    if stream.device != dev:
         raise OALError(OAL_ERR_INVALID_ARG, "the stream is on %s, the tensors on %s"
                        % (stream.device, dev))
-    if torch.cuda.current_device() == dev.index:
-        return contextlib.nullcontext(), stream
-    return torch.cuda.device(dev), stream
-
-
-def _made_here(stream, dev, *ts):
-    """Tensors this call allocated, from the current stream's pool, while
-    `stream` may be another: their memory must not be handed out again before
-    `stream` is done with it."""
     if stream != torch.cuda.current_stream(dev):
-        for t in ts:
+        for t in made:
             t.record_stream(stream)
+    return stream.cuda_stream
+
+
+def _ptr_or_null(t):
+    return None if t is None else t.data_ptr()
 
 
 def _gated_shapes(Q, K, V, g):
@@ -393,10 +396,11 @@ def _need_lengths(lengths, B, dev):
         _need_tensor(lengths, "lengths", torch.int32, (B,), dev)
 
 
-def _workspace(given, need, dev):
+def _workspace(given, size, made, sizes, dev):
     if given is None:
-        return torch.empty(max(int(need), 256), dtype=torch.uint8, device=dev)
-    _need(given.device == dev and given.is_contiguous(), "workspace must be contiguous on %s" % dev)
+        given = torch.empty(max(size(*sizes), 256), dtype=torch.uint8, device=dev)
+        made.append(given)
+    _need_tensor(given, "workspace", given.dtype, given.shape, dev)
     return given
 
 
@@ -416,32 +420,27 @@ def oal_gated_prefill(Q, K, V, g, scale=0.125, lengths=None, state=None,
     dt = _dtype_code(Q)
     _need_lengths(lengths, B, dev)
     _need(state is not None or not continue_from_state, "continue_from_state needs a state")
-    ctx, stream = _on_device(dev, stream)
-    with ctx:
-        made = []
-        if state is None:
-            state = torch.empty(B, Hkv, d, dv, dtype=torch.float32, device=dev)
-            made.append(state)
-        if Y is None:
-            make = torch.empty if lengths is None else torch.zeros
-            Y = make(B, Hq, T, dv, dtype=Q.dtype, device=dev)
-            made.append(Y)
-        if workspace is None:
-            need = lib.oal_gated_prefill_workspace_bytes(B, Hq, Hkv, T, d, dv, dt)
-            workspace = _workspace(None, need, dev)
-            made.append(workspace)
-        else:
-            _workspace(workspace, 0, dev)
-        _need_tensor(state, "state", torch.float32, (B, Hkv, d, dv), dev)
-        _need_tensor(Y, "Y", Q.dtype, (B, Hq, T, dv), dev)
-        _made_here(stream, dev, *made)
-        _check(lib.oal_gated_prefill(Q.data_ptr(), K.data_ptr(), V.data_ptr(), dt, g.data_ptr(),
-                                     B, Hq, Hkv, T, d, dv, float(scale),
-                                     None if lengths is None else lengths.data_ptr(),
-                                     state.data_ptr(), int(bool(continue_from_state)),
-                                     Y.data_ptr(), workspace.data_ptr(),
-                                     workspace.numel() * workspace.element_size(),
-                                     stream.cuda_stream))
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return oal_gated_prefill(Q, K, V, g, scale, lengths, state, continue_from_state, Y,
+                                     workspace, stream)
+    made = []
+    if state is None:
+        state = torch.empty(B, Hkv, d, dv, dtype=torch.float32, device=dev)
+        made.append(state)
+    if Y is None:
+        make = torch.empty if lengths is None else torch.zeros
+        Y = make(B, Hq, T, dv, dtype=Q.dtype, device=dev)
+        made.append(Y)
+    workspace = _workspace(workspace, lib.oal_gated_prefill_workspace_bytes, made,
+                           (B, Hq, Hkv, T, d, dv, dt), dev)
+    _need_tensor(state, "state", torch.float32, (B, Hkv, d, dv), dev)
+    _need_tensor(Y, "Y", Q.dtype, (B, Hq, T, dv), dev)
+    _check(lib.oal_gated_prefill(Q.data_ptr(), K.data_ptr(), V.data_ptr(), dt, g.data_ptr(), B, Hq,
+                                 Hkv, T, d, dv, scale, _ptr_or_null(lengths), state.data_ptr(),
+                                 bool(continue_from_state), Y.data_ptr(), workspace.data_ptr(),
+                                 workspace.numel() * workspace.element_size(),
+                                 _stream_on(dev, stream, made)))
     return Y, state
 
 
@@ -464,36 +463,32 @@ def oal_gated_backward(Q, K, V, g, dY, scale=0.125, lengths=None, state0=None, d
     for name, t in (("state0", state0), ("dstate", dstate)):
         if t is not None:
             _need_tensor(t, name, torch.float32, (B, Hkv, d, dv), dev)
-    ctx, stream = _on_device(dev, stream)
-    with ctx:
-        made, out = [], []
-        make = torch.empty if lengths is None else torch.zeros
-        for name, t, like in (("dQ", dQ, Q), ("dK", dK, K), ("dV", dV, V), ("dg", dg, g)):
-            if t is None:
-                t = make(like.shape, dtype=like.dtype, device=dev)
-                made.append(t)
-            _need_tensor(t, name, like.dtype, like.shape, dev)
-            out.append(t)
-        if dstate0 is None:
-            dstate0 = torch.empty(B, Hkv, d, dv, dtype=torch.float32, device=dev)
-            made.append(dstate0)
-        _need_tensor(dstate0, "dstate0", torch.float32, (B, Hkv, d, dv), dev)
-        out.append(dstate0)
-        if workspace is None:
-            need = lib.oal_gated_backward_workspace_bytes(B, Hq, Hkv, T, d, dv, dt)
-            workspace = _workspace(None, need, dev)
-            made.append(workspace)
-        else:
-            _workspace(workspace, 0, dev)
-        _made_here(stream, dev, *made)
-        _check(lib.oal_gated_backward(Q.data_ptr(), K.data_ptr(), V.data_ptr(), dt, g.data_ptr(),
-                                      dY.data_ptr(), B, Hq, Hkv, T, d, dv, float(scale),
-                                      None if lengths is None else lengths.data_ptr(),
-                                      None if state0 is None else state0.data_ptr(),
-                                      None if dstate is None else dstate.data_ptr(),
-                                      *(t.data_ptr() for t in out), workspace.data_ptr(),
-                                      workspace.numel() * workspace.element_size(),
-                                      stream.cuda_stream))
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return oal_gated_backward(Q, K, V, g, dY, scale, lengths, state0, dstate, dQ, dK, dV,
+                                      dg, dstate0, workspace, stream)
+    made, out = [], []
+    make = torch.empty if lengths is None else torch.zeros
+    for name, t, like in (("dQ", dQ, Q), ("dK", dK, K), ("dV", dV, V), ("dg", dg, g)):
+        if t is None:
+            t = make(like.shape, dtype=like.dtype, device=dev)
+            made.append(t)
+        _need_tensor(t, name, like.dtype, like.shape, dev)
+        out.append(t)
+    if dstate0 is None:
+        dstate0 = torch.empty(B, Hkv, d, dv, dtype=torch.float32, device=dev)
+        made.append(dstate0)
+    _need_tensor(dstate0, "dstate0", torch.float32, (B, Hkv, d, dv), dev)
+    out.append(dstate0)
+    workspace = _workspace(workspace, lib.oal_gated_backward_workspace_bytes, made,
+                           (B, Hq, Hkv, T, d, dv, dt), dev)
+    _check(lib.oal_gated_backward(Q.data_ptr(), K.data_ptr(), V.data_ptr(), dt, g.data_ptr(),
+                                  dY.data_ptr(), B, Hq, Hkv, T, d, dv, scale,
+                                  _ptr_or_null(lengths), _ptr_or_null(state0),
+                                  _ptr_or_null(dstate), *(t.data_ptr() for t in out),
+                                  workspace.data_ptr(),
+                                  workspace.numel() * workspace.element_size(),
+                                  _stream_on(dev, stream, made)))
     return tuple(out)
 
 
@@ -515,16 +510,19 @@ def oal_gated_decode_step(q, k, v, g, state, scale=0.125, slots=None, y=None, st
     _need_tensor(state, "state", torch.float32, (n, Hkv, d, dv), dev)
     if slots is not None:
         _need_tensor(slots, "slots", torch.int32, (B,), dev)
-    ctx, stream = _on_device(dev, stream)
-    with ctx:
-        if y is None:
-            y = torch.empty(B, Hq, dv, dtype=q.dtype, device=dev)
-            _made_here(stream, dev, y)
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return oal_gated_decode_step(q, k, v, g, state, scale, slots, y, stream)
+    made = ()
+    if y is None:
+        y = torch.empty_like(q) if d == dv else q.new_empty(B, Hq, dv)
+        made = (y,)
+    else:
         _need_tensor(y, "y", q.dtype, (B, Hq, dv), dev)
-        _check(lib.oal_gated_decode_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), dt,
-                                         g.data_ptr(), B, Hq, Hkv, d, dv, float(scale),
-                                         None if slots is None else slots.data_ptr(), n,
-                                         state.data_ptr(), y.data_ptr(), stream.cuda_stream))
+    _check(lib.oal_gated_decode_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), dt, g.data_ptr(), B,
+                                     Hq, Hkv, d, dv, scale, _ptr_or_null(slots), n,
+                                     state.data_ptr(), y.data_ptr(),
+                                     _stream_on(dev, stream, made)))
     return y
 
 
@@ -537,10 +535,11 @@ def oal_state_remap(pool, map, stream=None):
     n, dev = pool.shape[0], pool.device
     _need_tensor(pool, "pool", pool.dtype, pool.shape, dev)
     _need_tensor(map, "map", torch.int32, (n,), dev)
-    ctx, stream = _on_device(dev, stream)
-    with ctx:
-        _check(lib.oal_state_remap(pool.data_ptr(), pool[0].numel() * pool.element_size() if n else 0,
-                                   n, map.data_ptr(), stream.cuda_stream))
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return oal_state_remap(pool, map, stream)
+    _check(lib.oal_state_remap(pool.data_ptr(), pool.numel() // n * pool.element_size() if n else 0,
+                               n, map.data_ptr(), _stream_on(dev, stream, ())))
     return pool
 
 
