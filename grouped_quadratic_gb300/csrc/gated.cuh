@@ -46,6 +46,9 @@ inline int gated_segments(int T, int seg_chunks) {
   return (chunks + seg_chunks - 1) / seg_chunks;
 }
 
+// Kernels above 48 KB of shared memory ask for it once per device.
+oal_status gated_need_smem(const void *kernel, size_t bytes, bool (&done)[kMaxDevices]);
+
 // Length of sequence b, clamped to 0..T; one outside is recorded.
 __device__ __forceinline__ int gated_len(const GatedArgs &p, int b) {
   if (!p.lengths) return p.T;
@@ -63,7 +66,7 @@ __device__ __forceinline__ int gated_last_seg(int n, int seg_tokens) {
 // Sums of g inside a chunk: the sum as an unevaluated pair hi + lo, so the
 // difference of two neighbours keeps its digits behind a large drop, and the
 // gates cut so far, which are left out of the sum.
-struct GateSums {
+struct __align__(16) GateSums {
   float hi[kGC], lo[kGC];
   int cuts[kGC];
 };
@@ -74,13 +77,23 @@ __device__ __forceinline__ void two_sum(float a, float b, float &s, float &e) {
   e = (a - (s - t)) + (b - t);
 }
 
-// One warp: lane l takes tokens 2l, 2l+1 of the chunk at t0; rows from n on
-// count as gates of 1 (g = 0).
-__device__ __forceinline__ void gate_sums(const float *__restrict__ g, int t0, int n, GateSums &out) {
-  const int lane = threadIdx.x & 31, t = t0 + 2 * lane;
-  const float x0 = t < n ? __ldg(g + t) : 0.f, x1 = t + 1 < n ? __ldg(g + t + 1) : 0.f;
-  const int c0 = x0 <= kGateCut, c1 = x1 <= kGateCut;
-  const float a = c0 ? 0.f : x0, b = c1 ? 0.f : x1;
+// The same held by a warp: lane l has tokens 2l and 2l + 1.
+struct GateLane {
+  float hi[2], lo[2];
+  int cuts[2];
+};
+
+// Gates of lane l's tokens of the chunk at t0; rows from n on count as gates
+// of 1 (g = 0).
+__device__ __forceinline__ float2 gate_load(const float *__restrict__ g, int t0, int n) {
+  const int t = t0 + 2 * (threadIdx.x & 31);
+  return make_float2(t < n ? __ldg(g + t) : 0.f, t + 1 < n ? __ldg(g + t + 1) : 0.f);
+}
+
+__device__ __forceinline__ GateLane gate_sums(float2 x) {
+  const int lane = threadIdx.x & 31;
+  const int c0 = x.x <= kGateCut, c1 = x.y <= kGateCut;
+  const float a = c0 ? 0.f : x.x, b = c1 ? 0.f : x.y;
   float hi, lo;
   two_sum(a, b, hi, lo);
   int cuts = c0 + c1;
@@ -103,13 +116,20 @@ __device__ __forceinline__ void gate_sums(const float *__restrict__ g, int t0, i
   float s, e;
   two_sum(ph, a, s, e);
   e += pl;
-  const float h0 = s + e;
-  out.hi[2 * lane] = h0;
-  out.lo[2 * lane] = e - (h0 - s);
-  out.cuts[2 * lane] = pc + c0;
-  out.hi[2 * lane + 1] = hi;
-  out.lo[2 * lane + 1] = lo;
-  out.cuts[2 * lane + 1] = cuts;
+  GateLane out;
+  out.hi[0] = s + e;
+  out.lo[0] = e - (out.hi[0] - s);
+  out.cuts[0] = pc + c0;
+  out.hi[1] = hi;
+  out.lo[1] = lo;
+  out.cuts[1] = cuts;
+  return out;
+}
+__device__ __forceinline__ void gate_store(const GateLane &x, GateSums &out) {
+  const int l = threadIdx.x & 31;
+  *reinterpret_cast<float2 *>(&out.hi[2 * l]) = make_float2(x.hi[0], x.hi[1]);
+  *reinterpret_cast<float2 *>(&out.lo[2 * l]) = make_float2(x.lo[0], x.lo[1]);
+  *reinterpret_cast<int2 *>(&out.cuts[2 * l]) = make_int2(x.cuts[0], x.cuts[1]);
 }
 
 // Decay between tokens j <= i of the chunk, exp(G_i - G_j).

@@ -1,0 +1,122 @@
+// gated_mma.cuh -- register-level tensor-core products of the gated
+// recurrence on 64 x 64 bf16 tiles in shared memory (rows of 128 bytes, the
+// 16-byte chunk c of row r at chunk c ^ (r & 7), as a 128-byte-swizzled TMA
+// copy leaves it).
+//
+// The states live in registers, split over four warps (warp w owns rows
+// 16 w .. 16 w + 15), because every chunk scales them by a decay and adds a
+// product: in tensor memory that would be a read and a write of the state per
+// chunk besides the product.
+#pragma once
+#include "gated.cuh"
+#include "tc_ptx.cuh"
+
+namespace oal {
+
+constexpr int kTileBytes = kGC * 128;     // one 64 x 64 bf16 tile
+
+__device__ __forceinline__ uint32_t tile_at(int row, int chunk) {
+  return (uint32_t)(row * 128 + ((chunk ^ (row & 7)) << 4));
+}
+
+__device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// A 64 x 64 fp32 matrix over four warps: acc[nb][0..3] = rows r, r, r + 8,
+// r + 8 (r = 16 warp + lane / 4), columns 8 nb + 2 (lane % 4) and the next.
+struct StateAcc {
+  float v[8][4];
+};
+
+// s += sum_j w_j a_j b_j^T over the 64 rows j of two tiles, w in shared
+// memory.  w_j a_j is held as two bf16 terms, off by at most 2^-16 of it, so
+// the sum keeps about 16 bits more than a rounded factor would; b is exact.
+__device__ __forceinline__ void state_add(StateAcc &s, const void *a_tile, const void *b_tile, const float *w) {
+  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3;
+  const uint32_t at = tc::smem_u32(a_tile), bt = tc::smem_u32(b_tile);
+  const int mat = lane >> 3, r = lane & 7, q = lane & 3;
+#pragma unroll
+  for (int ks = 0; ks < 4; ++ks) {
+    uint32_t a[4], hi[4], lo[4];
+    ldsm4t(at + tile_at(16 * ks + 8 * (mat >> 1) + r, 2 * warp + (mat & 1)), a);
+    const float2 w0 = *reinterpret_cast<const float2 *>(w + 16 * ks + 2 * q);
+    const float2 w1 = *reinterpret_cast<const float2 *>(w + 16 * ks + 8 + 2 * q);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 f = e < 2 ? w0 : w1;
+      const float x = __uint_as_float(a[e] << 16) * f.x, y = __uint_as_float(a[e] & 0xFFFF0000u) * f.y;
+      hi[e] = tc::pack_bf16x2(x, y);
+      lo[e] = tc::pack_bf16x2(x - __uint_as_float(hi[e] << 16), y - __uint_as_float(hi[e] & 0xFFFF0000u));
+    }
+#pragma unroll
+    for (int np = 0; np < 4; ++np) {
+      uint32_t b[4];
+      ldsm4t(bt + tile_at(16 * ks + 8 * (mat & 1) + r, 2 * np + (mat >> 1)), b);
+      mma16816(s.v[2 * np], hi, b[0], b[1]);
+      mma16816(s.v[2 * np + 1], hi, b[2], b[3]);
+      mma16816(s.v[2 * np], lo, b[0], b[1]);
+      mma16816(s.v[2 * np + 1], lo, b[2], b[3]);
+    }
+  }
+}
+__device__ __forceinline__ void state_scale(StateAcc &s, float f) {
+#pragma unroll
+  for (int nb = 0; nb < 8; ++nb)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s.v[nb][e] *= f;
+}
+__device__ __forceinline__ void state_load(StateAcc &s, const float *src) {
+  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3;
+  const int r = 16 * warp + (lane >> 2), c = 2 * (lane & 3);
+#pragma unroll
+  for (int nb = 0; nb < 8; ++nb)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float2 x = src ? *reinterpret_cast<const float2 *>(src + (r + 8 * h) * 64 + 8 * nb + c) : make_float2(0.f, 0.f);
+      s.v[nb][2 * h] = x.x, s.v[nb][2 * h + 1] = x.y;
+    }
+}
+__device__ __forceinline__ void state_store(const StateAcc &s, float *dst) {
+  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3;
+  const int r = 16 * warp + (lane >> 2), c = 2 * (lane & 3);
+#pragma unroll
+  for (int nb = 0; nb < 8; ++nb)
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      *reinterpret_cast<float2 *>(dst + (r + 8 * h) * 64 + 8 * nb + c) = make_float2(s.v[nb][2 * h], s.v[nb][2 * h + 1]);
+}
+// The matrix rounded to bf16 as a tile (row d of the state = row d of the tile).
+__device__ __forceinline__ void state_round(const StateAcc &s, void *tile) {
+  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3;
+  const int r = 16 * warp + (lane >> 2), c = 4 * (lane & 3);
+  uint8_t *t = static_cast<uint8_t *>(tile);
+#pragma unroll
+  for (int nb = 0; nb < 8; ++nb)
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      *reinterpret_cast<uint32_t *>(t + tile_at(r + 8 * h, nb) + c) = tc::pack_bf16x2(s.v[nb][2 * h], s.v[nb][2 * h + 1]);
+}
+
+// Decays from behind each token to the end of the chunk (out, 64 floats of
+// this warp's own) and over the whole chunk (returned).
+__device__ __forceinline__ float gate_tails(const GateLane &x, float *out) {
+  const float eh = __shfl_sync(0xffffffffu, x.hi[1], 31), el = __shfl_sync(0xffffffffu, x.lo[1], 31);
+  const int ec = __shfl_sync(0xffffffffu, x.cuts[1], 31);
+  float t[2];
+#pragma unroll
+  for (int e = 0; e < 2; ++e) t[e] = x.cuts[e] == ec ? __expf((eh - x.hi[e]) + (el - x.lo[e])) : 0.f;
+  *reinterpret_cast<float2 *>(out + 2 * (threadIdx.x & 31)) = make_float2(t[0], t[1]);
+  return ec == 0 ? __expf(eh + el) : 0.f;
+}
+
+}  // namespace oal

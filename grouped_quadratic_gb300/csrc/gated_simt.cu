@@ -129,7 +129,7 @@ struct Decays {
   float head[kGC], tail[kGC];
 };
 __device__ __forceinline__ void chunk_decays(const float *g, int t0, int n, Decays &d) {
-  if (threadIdx.x < 32) gate_sums(g, t0, n, d.sums);
+  if (threadIdx.x < 32) gate_store(gate_sums(gate_load(g, t0, n)), d.sums);
   __syncthreads();
   if (threadIdx.x < kGC) {
     d.head[threadIdx.x] = gate_head(d.sums, threadIdx.x);
@@ -472,9 +472,15 @@ __global__ void __launch_bounds__(kThreads) gated_grad_kernel(GatedArgs p) {
   }
 }
 
-// Kernels above 48 KB of shared memory have to ask for it once per device.
-template <typename K>
-oal_status need_smem(K kernel, size_t bytes, bool (&done)[kMaxDevices]) {
+#define GATED_TRY(x)             \
+  do {                           \
+    const oal_status _s = (x);   \
+    if (_s != OAL_OK) return _s; \
+  } while (0)
+
+}  // namespace
+
+oal_status gated_need_smem(const void *kernel, size_t bytes, bool (&done)[kMaxDevices]) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices)
     return oal_fail(OAL_ERR_CUDA, "no current device");
@@ -485,20 +491,12 @@ oal_status need_smem(K kernel, size_t bytes, bool (&done)[kMaxDevices]) {
   return OAL_OK;
 }
 
-#define GATED_TRY(x)             \
-  do {                           \
-    const oal_status _s = (x);   \
-    if (_s != OAL_OK) return _s; \
-  } while (0)
-
-}  // namespace
-
-// Enough segments for about three blocks per SM; one segment, and so one
-// launch, where the (batch, KV head) units alone are that many.
+// As many segments as give three blocks per SM one wave; one segment, and so
+// one launch, where the (batch, KV head) units alone are that many.
 int gated_prefill_segment(int B, int Hkv, int T, int is_bf16) {
   (void)is_bf16;
   const long long units = (long long)B * Hkv, chunks = ((long long)T + kGC - 1) / kGC;
-  const long long want = (3 * 152 + units - 1) / units;
+  const long long want = std::max<long long>(1, 3 * 152 / units);
   return (int)std::max<long long>(1, (chunks + want - 1) / want);
 }
 int gated_backward_segment(int is_bf16) {
@@ -515,8 +513,8 @@ template <typename T>
 static oal_status prefill_simt(const GatedArgs &p, cudaStream_t stream) {
   static bool done_seg[kMaxDevices], done_out[kMaxDevices];
   const size_t seg_smem = 2 * kTile * sizeof(float), out_smem = 5 * kTile * sizeof(float);
-  GATED_TRY(need_smem(gated_segment_kernel<T>, seg_smem, done_seg));
-  GATED_TRY(need_smem(gated_out_kernel<T>, out_smem, done_out));
+  GATED_TRY(gated_need_smem(reinterpret_cast<const void *>(gated_segment_kernel<T>), seg_smem, done_seg));
+  GATED_TRY(gated_need_smem(reinterpret_cast<const void *>(gated_out_kernel<T>), out_smem, done_out));
   if (p.nseg > 1) {
     launch_pdl(gated_segment_kernel<T>, dim3(p.nseg * p.B * p.Hkv), dim3(kThreads), seg_smem, stream, p);
     GATED_TRY(oal_after_launch("gated_segment_kernel", stream));
@@ -530,8 +528,8 @@ template <typename T>
 static oal_status backward_simt(const GatedArgs &p, cudaStream_t stream) {
   static bool done_seg[kMaxDevices], done_grad[kMaxDevices];
   const size_t seg_smem = 2 * kTile * sizeof(float), grad_smem = 8 * kTile * sizeof(float);
-  GATED_TRY(need_smem(gated_segment_kernel<T>, seg_smem, done_seg));
-  GATED_TRY(need_smem(gated_grad_kernel<T>, grad_smem, done_grad));
+  GATED_TRY(gated_need_smem(reinterpret_cast<const void *>(gated_segment_kernel<T>), seg_smem, done_seg));
+  GATED_TRY(gated_need_smem(reinterpret_cast<const void *>(gated_grad_kernel<T>), grad_smem, done_grad));
   launch_pdl(gated_segment_kernel<T>, dim3(p.nseg * p.B * p.Hkv, 2), dim3(kThreads), seg_smem, stream, p);
   GATED_TRY(oal_after_launch("gated_segment_kernel", stream));
   GATED_TRY(launch_gated_scan(p, 1, stream));

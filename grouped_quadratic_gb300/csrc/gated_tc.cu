@@ -1,0 +1,448 @@
+// gated_tc.cu -- the gated linear recurrence for bf16 on the tensor cores.
+//
+// Prefill.  gated_tc_segment_kernel forms the segments' own states,
+// gated_scan_kernel (gated_simt.cu) the state before each segment, and
+// gated_tc_out_kernel walks every segment: per chunk of 64 tokens and pair of
+// query heads of the KV head (128 rows: 64 tokens of each)
+//     X = Q K^T,  D = Q S_in           tcgen05, operands as TMA left them
+//     P = X o pair (bf16),  D *= head  four warps, tensor memory -> registers -> tensor memory
+//     D += P V                         tcgen05, P from tensor memory
+// and the state itself in registers (gated_mma.cuh).  Decays exp(G_i - G_j)
+// inside a 32-token half are formed directly, those from the first half to the
+// second as exp(G_i - G_31) exp(G_31 - G_j): for gates at most 1 no factor
+// exceeds 1, whatever the drop.
+#include <algorithm>
+#include <mutex>
+
+#include <cudaTypedefs.h>
+
+#include "gated_mma.cuh"
+
+namespace oal {
+namespace {
+using namespace tc;
+
+constexpr int kStages = 4;                  // chunks in flight of the segment kernel
+constexpr int kSegThreads = 128;
+constexpr int kOutThreads = 160;            // four computing warps and one that issues
+constexpr uint32_t kOutCols = 128;          // tensor memory: X (then P) 64, D 64
+constexpr uint32_t kColX = 0, kColD = 64;
+
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, const void *src, int x, int y, int z) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(smem_u32(src)), "r"(x), "r"(y), "r"(z)
+               : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+// mbar_wait by a whole warp, whose lanes agree on the outcome (the tensor-
+// memory instructions that follow want all of them).
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort, int *status) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, status));
+}
+__device__ __forceinline__ void *align1024(void *p) {
+  return reinterpret_cast<void *>((reinterpret_cast<uintptr_t>(p) + 1023) & ~(uintptr_t)1023);
+}
+
+// Rows from `rows` on of a tile become zeros (threads 0 .. 127).
+__device__ __forceinline__ void clear_rows(void *tile, int rows) {
+  for (int x = threadIdx.x; x < 64 * 8; x += 128)
+    if ((x >> 3) >= rows) reinterpret_cast<uint4 *>(tile)[x] = make_uint4(0u, 0u, 0u, 0u);
+}
+
+// ---------------------------------------------------------------- segments
+
+struct SegSmem {
+  uint8_t a[kStages][kTileBytes], b[kStages][kTileBytes];
+  float tail[4][kGC];
+  uint64_t full[kStages];
+  int abort_flag;
+};
+
+// Own state of each segment but a sequence's last.  HBM-bound: K and V once.
+__global__ void __launch_bounds__(kSegThreads)
+gated_tc_segment_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                        GatedArgs p) {
+  pdl_trigger();
+  extern __shared__ uint8_t smem_raw[];
+  SegSmem &s = *static_cast<SegSmem *>(align1024(smem_raw));
+  const int bh = blockIdx.x / p.nseg, seg = blockIdx.x % p.nseg, b = bh / p.Hkv;
+  const int tid = threadIdx.x, warp = tid >> 5;
+  if (tid == 0) {
+    s.abort_flag = 0;
+    for (int i = 0; i < kStages; ++i) mbar_init(&s.full[i], 1);
+    fence_mbar_init();
+  }
+  pdl_wait();
+  const int n = gated_len(p, b);
+  if (seg >= gated_last_seg(n, p.seg_chunks * kGC)) return;
+  __syncthreads();
+  const int c0 = seg * p.seg_chunks, nc = p.seg_chunks;   // whole chunks: not the last segment
+  volatile int *abort_flag = &s.abort_flag;
+  auto load = [&](int c) {
+    const int st = c % kStages;
+    mbar_arrive_expect_tx(&s.full[st], 2 * kTileBytes);
+    tma_load_3d(s.a[st], &tmK, &s.full[st], 0, (c0 + c) * kGC, bh);
+    tma_load_3d(s.b[st], &tmV, &s.full[st], 0, (c0 + c) * kGC, bh);
+  };
+  if (tid == 0)
+    for (int c = 0; c < min(kStages, nc); ++c) load(c);
+  const float *g = p.g + (size_t)bh * p.T;
+  float2 gate = gate_load(g, c0 * kGC, n);
+  StateAcc acc;
+  state_load(acc, nullptr);
+  float decay = 1.f;
+  bool ok = true;
+  for (int c = 0; c < nc; ++c) {
+    const GateLane sums = gate_sums(gate);
+    if (c + 1 < nc) gate = gate_load(g, (c0 + c + 1) * kGC, n);
+    const float whole = gate_tails(sums, s.tail[warp]);
+    decay *= whole;
+    state_scale(acc, whole);
+    __syncwarp();
+    ok = ok && mbar_wait(&s.full[c % kStages], (c / kStages) & 1, abort_flag, p.status);
+    if (ok) state_add(acc, s.a[c % kStages], s.b[c % kStages], s.tail[warp]);
+    __syncthreads();
+    if (tid == 0 && ok && c + kStages < nc) load(c + kStages);
+  }
+  if (tid == 0 && !ok)   // copies still in flight land before the block ends
+    for (int i = 0; i < min(kStages, nc); ++i)
+      for (int ph = 0; ph < 2; ++ph) mbar_wait_teardown(&s.full[i], ph, p.status);
+  state_store(acc, p.seg_state + ((size_t)bh * p.nseg + seg) * kGS);
+  if (tid == 0) p.seg_decay[(size_t)bh * p.nseg + seg] = decay;
+}
+
+// ---------------------------------------------------------------- outputs
+
+struct OutSmem {
+  uint8_t k[2][kTileBytes], v[2][kTileBytes];
+  uint8_t q[2][2 * kTileBytes];          // two heads' queries, then their outputs
+  uint8_t state[kTileBytes];             // the state before the chunk, bf16
+  GateSums sums;
+  float tail[4][kGC], mid[kGC / 2];      // to the chunk's end (a copy a warp), to token 31
+  uint64_t kv_full[2], q_full[2], xd_full, p_full, y_full, go, meet, drain;
+  uint32_t tmem;
+  int abort_flag;
+};
+
+__global__ void __launch_bounds__(kOutThreads, 3)
+gated_tc_out_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                    const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmY,
+                    GatedArgs p) {
+  pdl_trigger();
+  extern __shared__ uint8_t smem_raw[];
+  OutSmem &s = *static_cast<OutSmem *>(align1024(smem_raw));
+  const int bh = blockIdx.x / p.nseg, seg = blockIdx.x % p.nseg, b = bh / p.Hkv, kv = bh % p.Hkv;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rho = p.Hq / p.Hkv, npair = (rho + 1) / 2;
+  if (tid == 0) {
+    s.abort_flag = 0;
+    for (int i = 0; i < 2; ++i) mbar_init(&s.kv_full[i], 1), mbar_init(&s.q_full[i], 1);
+    mbar_init(&s.xd_full, 1);
+    mbar_init(&s.p_full, 4);
+    mbar_init(&s.y_full, 1);
+    mbar_init(&s.go, 4);
+    mbar_init(&s.meet, 4);
+    mbar_init(&s.drain, 1);
+    fence_mbar_init();
+  }
+  pdl_wait();
+  const int n = gated_len(p, b), last = gated_last_seg(n, p.seg_chunks * kGC);
+  if (seg > last) return;
+  if (warp == 4) {
+    tmem_alloc(&s.tmem, kOutCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tb = s.tmem;
+  const int c0 = seg * p.seg_chunks, nc = max(0, min((n + kGC - 1) / kGC - c0, p.seg_chunks));
+  const int steps = nc * npair;              // step it: chunk it / npair, heads 2 (it % npair), + 1
+  volatile int *abort_flag = &s.abort_flag;
+  const int h0 = b * p.Hq + kv * rho;
+  // rows behind a sequence that ends before T must stay: its last tile is
+  // stored row by row instead of by TMA (which drops rows from T on)
+  auto by_rows = [&](int t0) { return t0 + kGC > n && n < p.T; };
+
+  if (warp == 4) {
+    const uint32_t id_k = idesc_bf16_f32(128, 64, 0), id_mn = idesc_bf16_f32(128, 64, 1);
+    auto load_q = [&](int it) {
+      const int pr = it % npair, heads = min(2, rho - 2 * pr), st = it & 1;
+      mbar_arrive_expect_tx(&s.q_full[st], heads * kTileBytes);
+      for (int h = 0; h < heads; ++h)
+        tma_load_3d(s.q[st] + h * kTileBytes, &tmQ, &s.q_full[st], 0, (c0 + it / npair) * kGC, h0 + 2 * pr + h);
+    };
+    auto load_kv = [&](int c) {
+      mbar_arrive_expect_tx(&s.kv_full[c & 1], 2 * kTileBytes);
+      tma_load_3d(s.k[c & 1], &tmK, &s.kv_full[c & 1], 0, (c0 + c) * kGC, bh);
+      tma_load_3d(s.v[c & 1], &tmV, &s.kv_full[c & 1], 0, (c0 + c) * kGC, bh);
+    };
+    auto store_y = [&](int it) {
+      const int pr = it % npair, heads = min(2, rho - 2 * pr), t0 = (c0 + it / npair) * kGC;
+      if (!by_rows(t0))
+        for (int h = 0; h < heads; ++h) tma_store_3d(&tmY, s.q[it & 1] + h * kTileBytes, 0, t0, h0 + 2 * pr + h);
+      bulk_commit();
+    };
+    int kv_loads = 0, q_loads = 0;
+    if (lane == 0) {
+      for (; kv_loads < min(2, nc); ++kv_loads) load_kv(kv_loads);
+      for (; q_loads < min(2, steps); ++q_loads) load_q(q_loads);
+    }
+    const uint64_t sd = sdesc_sw128(smem_u32(s.state), 16, 1024);
+    bool ok = true;
+    for (int it = 0; it < steps && ok; ++it) {
+      const int c = it / npair, pr = it % npair;
+      // the step before is done: its D is read, its outputs and (a new chunk)
+      // the state are in shared memory
+      ok = warp_wait(&s.go, it & 1, abort_flag, p.status) &&
+           warp_wait(&s.q_full[it & 1], (it >> 1) & 1, abort_flag, p.status) &&
+           warp_wait(&s.kv_full[c & 1], (c >> 1) & 1, abort_flag, p.status);
+      if (!ok) break;
+      tc_fence_after();
+      const uint64_t qd = sdesc_sw128(smem_u32(s.q[it & 1]), 16, 1024);
+      const uint64_t kd = sdesc_sw128(smem_u32(s.k[c & 1]), 16, 1024);
+      const uint64_t vd = sdesc_sw128(smem_u32(s.v[c & 1]), 16, 1024);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) umma_ss_warp(tb + kColX, qd + 2 * k, kd + 2 * k, id_k, k > 0);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) umma_ss_warp(tb + kColD, qd + 2 * k, sd + 128 * k, id_mn, k > 0);
+      umma_commit_warp(&s.xd_full);
+      if (lane == 0) {
+        if (it > 0) store_y(it - 1);
+        if (pr == 0 && c > 0 && c + 1 < nc) load_kv(c + 1), ++kv_loads;
+        if (it > 0 && it + 1 < steps) {
+          bulk_wait_read();
+          load_q(it + 1), ++q_loads;
+        }
+      }
+      __syncwarp();
+      ok = warp_wait(&s.p_full, it & 1, abort_flag, p.status);
+      if (!ok) break;
+      tc_fence_after();
+#pragma unroll
+      for (int k = 0; k < 4; ++k) umma_ts_warp(tb + kColD, tb + kColX + 8 * k, vd + 128 * k, id_mn, 1u);
+      umma_commit_warp(&s.y_full);
+    }
+    if (ok && steps > 0 && warp_wait(&s.go, steps & 1, abort_flag, p.status) && lane == 0) store_y(steps - 1);
+    umma_commit_warp(&s.drain);
+    if (lane == 0) {   // nothing in flight at the block's end
+      mbar_wait_teardown(&s.drain, 0, p.status);
+      for (int i = max(0, kv_loads - 2); i < kv_loads; ++i) mbar_wait_teardown(&s.kv_full[i & 1], (i >> 1) & 1, p.status);
+      for (int i = max(0, q_loads - 2); i < q_loads; ++i) mbar_wait_teardown(&s.q_full[i & 1], (i >> 1) & 1, p.status);
+      bulk_wait_all();
+    }
+    __syncwarp();
+  } else {
+    const int i = tid & 63, half = warp & 1;            // token of this thread's row, its 32-token half
+    const uint32_t tm = tb + ((uint32_t)(32 * warp) << 16);
+    const float *g = p.g + (size_t)bh * p.T;
+    StateAcc acc;
+    state_load(acc, p.nseg > 1 ? p.seg_state + ((size_t)bh * p.nseg + seg) * kGS
+                               : p.state_in ? p.state_in + (size_t)bh * kGS : nullptr);
+    state_round(acc, s.state);
+    fence_proxy_async();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&s.go);
+    float2 gate = gate_load(g, c0 * kGC, n);
+    float near[32];                                      // decays within the row's half
+    float head = 0.f, far = 0.f, whole = 0.f;
+    bool ok = true;
+    // the four computing warps meet (a wait that ends, unlike a barrier of threads)
+    int met = 0;
+    auto meet = [&]() {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s.meet);
+      return warp_wait(&s.meet, met++ & 1, abort_flag, p.status);
+    };
+    for (int it = 0; it < steps && ok; ++it) {
+      const int c = it / npair, pr = it % npair, t0 = (c0 + c) * kGC;
+      if (pr == 0) {
+        const GateLane sums = gate_sums(gate);
+        if (c + 1 < nc) gate = gate_load(g, t0 + kGC, n);
+        whole = gate_tails(sums, s.tail[warp]);
+        ok = c == 0 || meet();                           // the chunk before is done with sums and mid
+        if (warp == 0) {
+          gate_store(sums, s.sums);
+          const float mh = __shfl_sync(0xffffffffu, sums.hi[1], 15), ml = __shfl_sync(0xffffffffu, sums.lo[1], 15);
+          const int mc = __shfl_sync(0xffffffffu, sums.cuts[1], 15);
+          if (lane < 16)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              s.mid[2 * lane + e] = sums.cuts[e] == mc ? __expf((mh - sums.hi[e]) + (ml - sums.lo[e])) : 0.f;
+        }
+        ok = ok && meet();
+        const float gh = s.sums.hi[i], gl = s.sums.lo[i];
+        const int gc = s.sums.cuts[i];
+        head = gc == 0 ? __expf(gh + gl) : 0.f;
+        far = half && gc == s.sums.cuts[31] ? __expf((gh - s.sums.hi[31]) + (gl - s.sums.lo[31])) : 0.f;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          const int jj = 32 * half + j;
+          near[j] = j <= lane && gc == s.sums.cuts[jj] ? __expf((gh - s.sums.hi[jj]) + (gl - s.sums.lo[jj])) : 0.f;
+        }
+        ok = ok && warp_wait(&s.kv_full[c & 1], (c >> 1) & 1, abort_flag, p.status);
+      }
+      ok = ok && warp_wait(&s.xd_full, it & 1, abort_flag, p.status);
+      if (!ok) break;
+      tc_fence_after();
+      if (pr == 0 && t0 + kGC > n) {                     // rows behind the sequence count as zeros
+        clear_rows(s.k[c & 1], n - t0);
+        clear_rows(s.v[c & 1], n - t0);
+        fence_proxy_async();
+        ok = meet();
+        if (!ok) break;
+      }
+      uint32_t pk[16];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {                      // keys of the row's own half
+        uint32_t x[16];
+        tmem_ld16(tm + kColX + 32 * half + 16 * h, x);
+        tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 16; e += 2) {
+          const int j = 16 * h + e;
+          pk[8 * h + (e >> 1)] = pack_bf16x2(j <= lane ? __uint_as_float(x[e]) * near[j] : 0.f,
+                                             j + 1 <= lane ? __uint_as_float(x[e + 1]) * near[j + 1] : 0.f);
+        }
+      }
+      uint32_t po[16];                                   // keys of the other half
+      if (half) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t x[16];
+          tmem_ld16(tm + kColX + 16 * h, x);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 16; e += 4) {
+            const float4 m = *reinterpret_cast<const float4 *>(&s.mid[16 * h + e]);
+            po[8 * h + (e >> 1)] = pack_bf16x2(__uint_as_float(x[e]) * (far * m.x), __uint_as_float(x[e + 1]) * (far * m.y));
+            po[8 * h + (e >> 1) + 1] = pack_bf16x2(__uint_as_float(x[e + 2]) * (far * m.z), __uint_as_float(x[e + 3]) * (far * m.w));
+          }
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) po[e] = 0u;
+      }
+      tmem_st16(tm + kColX + 16 * half, pk);
+      tmem_st16(tm + kColX + 16 * (1 - half), po);
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        uint32_t x[16];
+        tmem_ld16(tm + kColD + 16 * h, x);
+        tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 16; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * head);
+        tmem_st16(tm + kColD + 16 * h, x);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s.p_full);
+      if (pr == npair - 1) {                             // Q S_in of the chunk's last pair is done
+        state_scale(acc, whole);
+        state_add(acc, s.k[c & 1], s.v[c & 1], s.tail[warp]);
+        state_round(acc, s.state);
+      }
+      ok = warp_wait(&s.y_full, it & 1, abort_flag, p.status);
+      if (!ok) break;
+      tc_fence_after();
+      const int hd = 2 * pr + (warp >> 1);
+      const bool rows = by_rows(t0);
+      uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.Y) + ((size_t)(h0 + hd) * p.T + t0 + i) * 64);
+      uint8_t *tile = s.q[it & 1] + (warp >> 1) * kTileBytes;
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        uint32_t x[16];
+        tmem_ld16(tm + kColD + 16 * h, x);
+        tmem_wait_ld();
+        uint32_t y[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          y[e] = pack_bf16x2(__uint_as_float(x[2 * e]) * p.scale, __uint_as_float(x[2 * e + 1]) * p.scale);
+        const uint4 lo = make_uint4(y[0], y[1], y[2], y[3]), hi = make_uint4(y[4], y[5], y[6], y[7]);
+        if (!rows) {
+          *reinterpret_cast<uint4 *>(tile + tile_at(i, 2 * h)) = lo;
+          *reinterpret_cast<uint4 *>(tile + tile_at(i, 2 * h + 1)) = hi;
+        } else if (hd < rho && t0 + i < n) {
+          dst[2 * h] = lo;
+          dst[2 * h + 1] = hi;
+        }
+      }
+      fence_proxy_async();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s.go);
+    }
+    if (seg == last && ok) state_store(acc, p.state_out + (size_t)bh * kGS);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 4) {
+    tc_fence_after();
+    tmem_dealloc(tb, kOutCols);
+  }
+}
+
+// ---------------------------------------------------------------- host side
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void *f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return (PFN_cuTensorMapEncodeTiled_v12000)f;
+  }();
+  return fn;
+}
+
+// [heads][T][64] bf16 in boxes of 64 rows, 128-byte swizzle; rows from T on
+// read as zeros and are not written.
+oal_status make_map(CUtensorMap *m, const void *ptr, int T, long long heads) {
+  auto fn = encode_fn();
+  if (!fn) return oal_fail(OAL_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
+  const cuuint64_t dims[3] = {64, (cuuint64_t)T, (cuuint64_t)heads};
+  const cuuint64_t strides[2] = {128, (cuuint64_t)T * 128};
+  const cuuint32_t box[3] = {64, kGC, 1}, es[3] = {1, 1, 1};
+  if (fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(ptr), dims, strides, box, es,
+         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return oal_fail(OAL_ERR_CUDA, "cuTensorMapEncodeTiled failed");
+  return OAL_OK;
+}
+
+#define GATED_TRY(x)             \
+  do {                           \
+    const oal_status _s = (x);   \
+    if (_s != OAL_OK) return _s; \
+  } while (0)
+
+}  // namespace
+
+oal_status launch_gated_scan(const GatedArgs &p, int both, cudaStream_t stream);
+
+oal_status launch_gated_prefill_tc(const GatedArgs &p, cudaStream_t stream) {
+  static bool done_seg[kMaxDevices], done_out[kMaxDevices];
+  const size_t seg_smem = sizeof(SegSmem) + 1024, out_smem = sizeof(OutSmem) + 1024;
+  GATED_TRY(gated_need_smem(reinterpret_cast<const void *>(gated_tc_segment_kernel), seg_smem, done_seg));
+  GATED_TRY(gated_need_smem(reinterpret_cast<const void *>(gated_tc_out_kernel), out_smem, done_out));
+  CUtensorMap tmQ, tmK, tmV, tmY;
+  GATED_TRY(make_map(&tmQ, p.Q, p.T, (long long)p.B * p.Hq));
+  GATED_TRY(make_map(&tmK, p.K, p.T, (long long)p.B * p.Hkv));
+  GATED_TRY(make_map(&tmV, p.V, p.T, (long long)p.B * p.Hkv));
+  GATED_TRY(make_map(&tmY, p.Y, p.T, (long long)p.B * p.Hq));
+  const dim3 grid(p.nseg * p.B * p.Hkv);
+  if (p.nseg > 1) {
+    launch_pdl(gated_tc_segment_kernel, grid, dim3(kSegThreads), seg_smem, stream, tmK, tmV, p);
+    GATED_TRY(oal_after_launch("gated_tc_segment_kernel", stream));
+    GATED_TRY(launch_gated_scan(p, 0, stream));
+  }
+  launch_pdl(gated_tc_out_kernel, grid, dim3(kOutThreads), out_smem, stream, tmQ, tmK, tmV, tmY, p);
+  return oal_after_launch("gated_tc_out_kernel", stream);
+}
+
+}  // namespace oal

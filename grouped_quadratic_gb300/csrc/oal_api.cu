@@ -47,6 +47,7 @@ oal_status group_dims_host(const float *chi_p, int P, int d, const int32_t *boot
                            double eps, int32_t *group, int *G);
 
 oal_status launch_gated_prefill_simt(const GatedArgs &p, int is_bf16, cudaStream_t stream);
+oal_status launch_gated_prefill_tc(const GatedArgs &p, cudaStream_t stream);
 oal_status launch_gated_backward_simt(const GatedArgs &p, int is_bf16, cudaStream_t stream);
 oal_status launch_gated_decode(const void *q, const void *k, const void *v, int is_bf16,
                                const float *g, int B, int Hq, int Hkv, float scale,
@@ -511,7 +512,8 @@ oal_status oal_gated_prefill(const void *Q, const void *K, const void *V, oal_dt
   p.status = oal_device_status_word();
   if (!p.status) return oal_fail(OAL_ERR_CUDA, "no device status word");
   oal_begin_call(stream);
-  return oal::launch_gated_prefill_simt(p, dtype == OAL_BF16, stream);
+  if (dtype == OAL_BF16) return oal::launch_gated_prefill_tc(p, stream);
+  return oal::launch_gated_prefill_simt(p, 0, stream);
 }
 
 size_t oal_gated_backward_workspace_bytes(int B, int Hq, int Hkv, int T, int d, int dv,
