@@ -9,6 +9,8 @@
 // are formed side by side, a scan turns them into the state before each
 // segment, and a last pass walks every segment from there.
 #pragma once
+#include <math.h>
+
 #include "oal_internal.cuh"
 
 namespace oal {
@@ -132,13 +134,18 @@ __device__ __forceinline__ void gate_store(const GateLane &x, GateSums &out) {
   *reinterpret_cast<int2 *>(&out.cuts[2 * l]) = make_int2(x.cuts[0], x.cuts[1]);
 }
 
+// exp(x) where `on`, else 0, without a branch: a row of these under branches
+// runs one after another (32 of them: 8,000 cycles instead of 300).
+__device__ __forceinline__ float gate_exp(bool on, float x) { return expf(on ? x : -INFINITY); }
+__device__ __forceinline__ float gate_exp_fast(bool on, float x) { return __expf(on ? x : -INFINITY); }
+
 // Decay between tokens j <= i of the chunk, exp(G_i - G_j).
 __device__ __forceinline__ float gate_pair(const GateSums &s, int i, int j) {
-  return s.cuts[i] == s.cuts[j] ? expf((s.hi[i] - s.hi[j]) + (s.lo[i] - s.lo[j])) : 0.f;
+  return gate_exp(s.cuts[i] == s.cuts[j], (s.hi[i] - s.hi[j]) + (s.lo[i] - s.lo[j]));
 }
 // Decay from the chunk's start to token i, exp(G_i).
 __device__ __forceinline__ float gate_head(const GateSums &s, int i) {
-  return s.cuts[i] == 0 ? expf(s.hi[i] + s.lo[i]) : 0.f;
+  return gate_exp(s.cuts[i] == 0, s.hi[i] + s.lo[i]);
 }
 // Decay from behind token j to the chunk's end, exp(G_63 - G_j).
 __device__ __forceinline__ float gate_tail(const GateSums &s, int j) {

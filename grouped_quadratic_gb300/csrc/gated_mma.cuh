@@ -114,9 +114,9 @@ __device__ __forceinline__ float gate_tails(const GateLane &x, float *out) {
   const int ec = __shfl_sync(0xffffffffu, x.cuts[1], 31);
   float t[2];
 #pragma unroll
-  for (int e = 0; e < 2; ++e) t[e] = x.cuts[e] == ec ? __expf((eh - x.hi[e]) + (el - x.lo[e])) : 0.f;
+  for (int e = 0; e < 2; ++e) t[e] = gate_exp_fast(x.cuts[e] == ec, (eh - x.hi[e]) + (el - x.lo[e]));
   *reinterpret_cast<float2 *>(out + 2 * (threadIdx.x & 31)) = make_float2(t[0], t[1]);
-  return ec == 0 ? __expf(eh + el) : 0.f;
+  return gate_exp_fast(ec == 0, eh + el);
 }
 
 }  // namespace oal

@@ -282,7 +282,7 @@ __global__ void __launch_bounds__(kThreads) gated_out_kernel(GatedArgs p) {
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        pair[i][j] = tx + 16 * j <= 4 * ty + i ? gate_pair(dec.sums, 4 * ty + i, tx + 16 * j) : 0.f;
+        pair[i][j] = gate_pair(dec.sums, 4 * ty + i, min(tx + 16 * j, 4 * ty + i));
     for (int r = 0; r < rho; ++r) {
       const size_t row = ((size_t)b * p.Hq + kv * rho + r) * p.T * 64;
       __syncthreads();
@@ -364,7 +364,7 @@ __global__ void __launch_bounds__(kThreads) gated_grad_kernel(GatedArgs p) {
   for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      pair[i][j] = tx + 16 * j <= 4 * ty + i ? gate_pair(dec.sums, 4 * ty + i, tx + 16 * j) : 0.f;
+      pair[i][j] = gate_pair(dec.sums, 4 * ty + i, min(tx + 16 * j, 4 * ty + i));
       w[i][j] = 0.f;
     }
   Acc dK, dV;

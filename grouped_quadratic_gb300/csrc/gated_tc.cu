@@ -271,17 +271,17 @@ gated_tc_out_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
           if (lane < 16)
 #pragma unroll
             for (int e = 0; e < 2; ++e)
-              s.mid[2 * lane + e] = sums.cuts[e] == mc ? __expf((mh - sums.hi[e]) + (ml - sums.lo[e])) : 0.f;
+              s.mid[2 * lane + e] = gate_exp_fast(sums.cuts[e] == mc, (mh - sums.hi[e]) + (ml - sums.lo[e]));
         }
         ok = ok && meet();
         const float gh = s.sums.hi[i], gl = s.sums.lo[i];
         const int gc = s.sums.cuts[i];
-        head = gc == 0 ? __expf(gh + gl) : 0.f;
-        far = half && gc == s.sums.cuts[31] ? __expf((gh - s.sums.hi[31]) + (gl - s.sums.lo[31])) : 0.f;
+        head = gate_exp_fast(gc == 0, gh + gl);
+        far = gate_exp_fast(half && gc == s.sums.cuts[31], (gh - s.sums.hi[31]) + (gl - s.sums.lo[31]));
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
           const int jj = 32 * half + j;
-          near[j] = j <= lane && gc == s.sums.cuts[jj] ? __expf((gh - s.sums.hi[jj]) + (gl - s.sums.lo[jj])) : 0.f;
+          near[j] = gate_exp_fast(j <= lane && gc == s.sums.cuts[jj], (gh - s.sums.hi[jj]) + (gl - s.sums.lo[jj]));
         }
         ok = ok && warp_wait(&s.kv_full[c & 1], (c >> 1) & 1, abort_flag, p.status);
       }
