@@ -39,14 +39,15 @@ struct StateAcc {
 };
 
 // s += sum_j w_j a_j b_j^T over the 64 rows j of two tiles, w in shared
-// memory.  w_j a_j is held as two bf16 terms, off by at most 2^-16 of it, so
+// memory (kFrom, kTo: of the rows, 16 at a time).  w_j a_j is held as two bf16 terms, off by at most 2^-16 of it, so
 // the sum keeps about 16 bits more than a rounded factor would; b is exact.
+template <int kFrom = 0, int kTo = 4>
 __device__ __forceinline__ void state_add(StateAcc &s, const void *a_tile, const void *b_tile, const float *w) {
   const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3;
   const uint32_t at = tc::smem_u32(a_tile), bt = tc::smem_u32(b_tile);
   const int mat = lane >> 3, r = lane & 7, q = lane & 3;
 #pragma unroll
-  for (int ks = 0; ks < 4; ++ks) {
+  for (int ks = kFrom; ks < kTo; ++ks) {
     uint32_t a[4], hi[4], lo[4];
     ldsm4t(at + tile_at(16 * ks + 8 * (mat >> 1) + r, 2 * warp + (mat & 1)), a);
     const float2 w0 = *reinterpret_cast<const float2 *>(w + 16 * ks + 2 * q);

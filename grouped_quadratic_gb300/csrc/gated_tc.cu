@@ -5,12 +5,15 @@
 // gated_tc_out_kernel walks every segment: per chunk of 64 tokens and pair of
 // query heads of the KV head (128 rows: 64 tokens of each)
 //     X = Q K^T,  D = Q S_in           tcgen05, operands as TMA left them
-//     P = X o pair (bf16),  D *= head  four warps, tensor memory -> registers -> tensor memory
+//     P = X o decays (bf16)            four warps, tensor memory -> registers -> tensor memory
 //     D += P V                         tcgen05, P from tensor memory
-// and the state itself in registers (gated_mma.cuh).  Decays exp(G_i - G_j)
-// inside a 32-token half are formed directly, those from the first half to the
-// second as exp(G_i - G_31) exp(G_31 - G_j): for gates at most 1 no factor
-// exceeds 1, whatever the drop.
+// and the state itself in registers (gated_mma.cuh).
+//
+// Where the chunk's sums G stay within +-60 and no gate is cut, a row's factor
+// is taken out of the sum: y_i = scale e^{G_i} [ S_in^T q_i + sum_j (q_i.k_j)
+// e^{-G_j} v_j ], one product a score and one a result; no factor exceeds
+// e^60, and a row's terms keep their ratios.  Other chunks form every decay
+// exp(G_i - G_j) by itself and scale D before P V is added.
 #include <algorithm>
 #include <mutex>
 
@@ -34,9 +37,20 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, const void 
                "r"(smem_u32(src)), "r"(x), "r"(y), "r"(z)
                : "memory");
 }
+__device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap *map, int x, int y, int z) {
+  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(x), "r"(y), "r"(z)
+               : "memory");
+}
 __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 __device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 __device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t *r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
 // mbar_wait by a whole warp, whose lanes agree on the outcome (the tensor-
 // memory instructions that follow want all of them).
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort, int *status) {
@@ -120,12 +134,48 @@ struct OutSmem {
   uint8_t k[2][kTileBytes], v[2][kTileBytes];
   uint8_t q[2][2 * kTileBytes];          // two heads' queries, then their outputs
   uint8_t state[kTileBytes];             // the state before the chunk, bf16
-  GateSums sums;
-  float tail[4][kGC], mid[kGC / 2];      // to the chunk's end (a copy a warp), to token 31
-  uint64_t kv_full[2], q_full[2], xd_full, p_full, y_full, go, meet, drain;
+  struct alignas(16) Gates {             // of a chunk, by the issuing warp
+    float tail[kGC], rest[kGC], head[kGC];   // e^{G_63-G_j}, e^{-G_j}, e^{G_i}
+    int fast;
+  } gates[2];
+  uint64_t kv_full[2], q_full[2], gate_full, x_full, d_full, p_full, y_full, go, meet, drain;
   uint32_t tmem;
   int abort_flag;
 };
+static_assert(3 * (sizeof(OutSmem) + 2 * 1024) <= 228 * 1024, "three blocks per SM");
+
+// Scores and D of a chunk whose gates are cut or drop far: every decay by
+// itself, P in the place of X, D scaled by e^{G_i} (one row a thread; compact,
+// not fast: a few chunks of a packed sequence pass here).
+__device__ __noinline__ void slow_scores(const float *g, int t0, int n, int i, float head, uint32_t tm) {
+  const GateLane s = gate_sums(gate_load(g, t0, n));
+  const bool odd = i & 1;
+  const float h0 = __shfl_sync(0xffffffffu, s.hi[0], i >> 1), h1 = __shfl_sync(0xffffffffu, s.hi[1], i >> 1);
+  const float l0 = __shfl_sync(0xffffffffu, s.lo[0], i >> 1), l1 = __shfl_sync(0xffffffffu, s.lo[1], i >> 1);
+  const int c0 = __shfl_sync(0xffffffffu, s.cuts[0], i >> 1), c1 = __shfl_sync(0xffffffffu, s.cuts[1], i >> 1);
+  const float hi = odd ? h1 : h0, lo = odd ? l1 : l0;
+  const int cut = odd ? c1 : c0;
+  for (int h = 0; h < 4; ++h) {         // P's 8 columns lie in front of the X still to be read
+    uint32_t x[16], d[16];
+    tmem_ld16(tm + kColX + 16 * h, x);
+    tmem_ld16(tm + kColD + 16 * h, d);
+    tmem_wait_ld();
+    float f[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const int from = 8 * h + (e >> 1), j = 16 * h + e;
+      const float hj = __shfl_sync(0xffffffffu, s.hi[e & 1], from), lj = __shfl_sync(0xffffffffu, s.lo[e & 1], from);
+      const int cj = __shfl_sync(0xffffffffu, s.cuts[e & 1], from);
+      const float w = gate_exp_fast(j <= i && cj == cut, (hi - hj) + (lo - lj));
+      f[e] = j <= i ? __uint_as_float(x[e]) * w : 0.f;
+      d[e] = __float_as_uint(__uint_as_float(d[e]) * head);
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = pack_bf16x2(f[2 * e], f[2 * e + 1]);
+    tmem_st8(tm + kColX + 8 * h, x);
+    tmem_st16(tm + kColD + 16 * h, d);
+  }
+}
 
 __global__ void __launch_bounds__(kOutThreads, 3)
 gated_tc_out_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -140,7 +190,9 @@ gated_tc_out_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
   if (tid == 0) {
     s.abort_flag = 0;
     for (int i = 0; i < 2; ++i) mbar_init(&s.kv_full[i], 1), mbar_init(&s.q_full[i], 1);
-    mbar_init(&s.xd_full, 1);
+    mbar_init(&s.gate_full, 1);
+    mbar_init(&s.x_full, 1);
+    mbar_init(&s.d_full, 1);
     mbar_init(&s.p_full, 4);
     mbar_init(&s.y_full, 1);
     mbar_init(&s.go, 4);
@@ -175,6 +227,10 @@ gated_tc_out_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
       for (int h = 0; h < heads; ++h)
         tma_load_3d(s.q[st] + h * kTileBytes, &tmQ, &s.q_full[st], 0, (c0 + it / npair) * kGC, h0 + 2 * pr + h);
     };
+    auto prefetch_q = [&](int it) {
+      const int pr = it % npair, heads = min(2, rho - 2 * pr);
+      for (int h = 0; h < heads; ++h) tma_prefetch_3d(&tmQ, 0, (c0 + it / npair) * kGC, h0 + 2 * pr + h);
+    };
     auto load_kv = [&](int c) {
       mbar_arrive_expect_tx(&s.kv_full[c & 1], 2 * kTileBytes);
       tma_load_3d(s.k[c & 1], &tmK, &s.kv_full[c & 1], 0, (c0 + c) * kGC, bh);
@@ -192,24 +248,50 @@ gated_tc_out_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
       for (; q_loads < min(2, steps); ++q_loads) load_q(q_loads);
     }
     const uint64_t sd = sdesc_sw128(smem_u32(s.state), 16, 1024);
-    bool ok = true;
+    // X of step it, while the step before writes its outputs
+    auto issue_x = [&](int it) {
+      const int c = it / npair;
+      if (!warp_wait(&s.q_full[it & 1], (it >> 1) & 1, abort_flag, p.status) ||
+          !warp_wait(&s.kv_full[c & 1], (c >> 1) & 1, abort_flag, p.status))
+        return false;
+      const uint64_t qd = sdesc_sw128(smem_u32(s.q[it & 1]), 16, 1024);
+      const uint64_t kd = sdesc_sw128(smem_u32(s.k[c & 1]), 16, 1024);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) umma_ss_warp(tb + kColX, qd + 2 * k, kd + 2 * k, id_k, k > 0);
+      umma_commit_warp(&s.x_full);
+      return true;
+    };
+    const float *g = p.g + (size_t)bh * p.T;
+    float2 gate = gate_load(g, c0 * kGC, n);
+    auto make_gates = [&](int c) {
+      const GateLane sums = gate_sums(gate);
+      if (c + 1 < nc) gate = gate_load(g, (c0 + c + 1) * kGC, n);
+      OutSmem::Gates &to = s.gates[c & 1];
+      gate_tails(sums, to.tail);
+      reinterpret_cast<float2 *>(to.rest)[lane] = make_float2(__expf(-sums.hi[0]), __expf(-sums.hi[1]));
+      reinterpret_cast<float2 *>(to.head)[lane] = make_float2(gate_exp_fast(sums.cuts[0] == 0, sums.hi[0] + sums.lo[0]),
+                                                              gate_exp_fast(sums.cuts[1] == 0, sums.hi[1] + sums.lo[1]));
+      const float most = fmaxf(fabsf(sums.hi[0]), fabsf(sums.hi[1]));
+      const int fast = __all_sync(0xffffffffu, most <= 60.f && sums.cuts[1] == 0);
+      if (lane == 0) to.fast = fast;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s.gate_full);
+    };
+    __syncwarp();
+    if (nc > 0) make_gates(0);
+    bool ok = steps == 0 || issue_x(0);
     for (int it = 0; it < steps && ok; ++it) {
       const int c = it / npair, pr = it % npair;
       // the step before is done: its D is read, its outputs and (a new chunk)
       // the state are in shared memory
-      ok = warp_wait(&s.go, it & 1, abort_flag, p.status) &&
-           warp_wait(&s.q_full[it & 1], (it >> 1) & 1, abort_flag, p.status) &&
-           warp_wait(&s.kv_full[c & 1], (c >> 1) & 1, abort_flag, p.status);
+      ok = warp_wait(&s.go, it & 1, abort_flag, p.status);
       if (!ok) break;
       tc_fence_after();
       const uint64_t qd = sdesc_sw128(smem_u32(s.q[it & 1]), 16, 1024);
-      const uint64_t kd = sdesc_sw128(smem_u32(s.k[c & 1]), 16, 1024);
       const uint64_t vd = sdesc_sw128(smem_u32(s.v[c & 1]), 16, 1024);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) umma_ss_warp(tb + kColX, qd + 2 * k, kd + 2 * k, id_k, k > 0);
-#pragma unroll
       for (int k = 0; k < 4; ++k) umma_ss_warp(tb + kColD, qd + 2 * k, sd + 128 * k, id_mn, k > 0);
-      umma_commit_warp(&s.xd_full);
+      umma_commit_warp(&s.d_full);
       if (lane == 0) {
         if (it > 0) store_y(it - 1);
         if (pr == 0 && c > 0 && c + 1 < nc) load_kv(c + 1), ++kv_loads;
@@ -217,6 +299,7 @@ gated_tc_out_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
           bulk_wait_read();
           load_q(it + 1), ++q_loads;
         }
+        if (it + 2 < steps) prefetch_q(it + 2);
       }
       __syncwarp();
       ok = warp_wait(&s.p_full, it & 1, abort_flag, p.status);
@@ -225,6 +308,9 @@ gated_tc_out_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
 #pragma unroll
       for (int k = 0; k < 4; ++k) umma_ts_warp(tb + kColD, tb + kColX + 8 * k, vd + 128 * k, id_mn, 1u);
       umma_commit_warp(&s.y_full);
+      // P, which lies in X, has been read
+      if (it + 1 < steps) ok = warp_wait(&s.y_full, it & 1, abort_flag, p.status) && issue_x(it + 1);
+      if (pr == 0 && c + 1 < nc) make_gates(c + 1);
     }
     if (ok && steps > 0 && warp_wait(&s.go, steps & 1, abort_flag, p.status) && lane == 0) store_y(steps - 1);
     umma_commit_warp(&s.drain);
@@ -238,7 +324,6 @@ gated_tc_out_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
   } else {
     const int i = tid & 63, half = warp & 1;            // token of this thread's row, its 32-token half
     const uint32_t tm = tb + ((uint32_t)(32 * warp) << 16);
-    const float *g = p.g + (size_t)bh * p.T;
     StateAcc acc;
     state_load(acc, p.nseg > 1 ? p.seg_state + ((size_t)bh * p.nseg + seg) * kGS
                                : p.state_in ? p.state_in + (size_t)bh * kGS : nullptr);
@@ -246,10 +331,9 @@ gated_tc_out_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
     fence_proxy_async();
     __syncwarp();
     if (lane == 0) mbar_arrive(&s.go);
-    float2 gate = gate_load(g, c0 * kGC, n);
-    float near[32];                                      // decays within the row's half
-    float head = 0.f, far = 0.f, whole = 0.f;
+    float row = 0.f;                                      // factor of the row's result
     bool ok = true;
+    int fast = 1;
     // the four computing warps meet (a wait that ends, unlike a barrier of threads)
     int met = 0;
     auto meet = [&]() {
@@ -259,33 +343,15 @@ gated_tc_out_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
     };
     for (int it = 0; it < steps && ok; ++it) {
       const int c = it / npair, pr = it % npair, t0 = (c0 + c) * kGC;
+      const OutSmem::Gates &gates = s.gates[c & 1];
       if (pr == 0) {
-        const GateLane sums = gate_sums(gate);
-        if (c + 1 < nc) gate = gate_load(g, t0 + kGC, n);
-        whole = gate_tails(sums, s.tail[warp]);
-        ok = c == 0 || meet();                           // the chunk before is done with sums and mid
-        if (warp == 0) {
-          gate_store(sums, s.sums);
-          const float mh = __shfl_sync(0xffffffffu, sums.hi[1], 15), ml = __shfl_sync(0xffffffffu, sums.lo[1], 15);
-          const int mc = __shfl_sync(0xffffffffu, sums.cuts[1], 15);
-          if (lane < 16)
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-              s.mid[2 * lane + e] = gate_exp_fast(sums.cuts[e] == mc, (mh - sums.hi[e]) + (ml - sums.lo[e]));
-        }
-        ok = ok && meet();
-        const float gh = s.sums.hi[i], gl = s.sums.lo[i];
-        const int gc = s.sums.cuts[i];
-        head = gate_exp_fast(gc == 0, gh + gl);
-        far = gate_exp_fast(half && gc == s.sums.cuts[31], (gh - s.sums.hi[31]) + (gl - s.sums.lo[31]));
-#pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          const int jj = 32 * half + j;
-          near[j] = gate_exp_fast(j <= lane && gc == s.sums.cuts[jj], (gh - s.sums.hi[jj]) + (gl - s.sums.lo[jj]));
-        }
-        ok = ok && warp_wait(&s.kv_full[c & 1], (c >> 1) & 1, abort_flag, p.status);
+        ok = warp_wait(&s.gate_full, c & 1, abort_flag, p.status);
+        if (!ok) break;
+        fast = gates.fast;
+        row = fast ? p.scale * gates.head[i] : p.scale;
+        ok = warp_wait(&s.kv_full[c & 1], (c >> 1) & 1, abort_flag, p.status);
       }
-      ok = ok && warp_wait(&s.xd_full, it & 1, abort_flag, p.status);
+      ok = ok && warp_wait(&s.x_full, it & 1, abort_flag, p.status);
       if (!ok) break;
       tc_fence_after();
       if (pr == 0 && t0 + kGC > n) {                     // rows behind the sequence count as zeros
@@ -295,55 +361,64 @@ gated_tc_out_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
         ok = meet();
         if (!ok) break;
       }
-      uint32_t pk[16];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {                      // keys of the row's own half
-        uint32_t x[16];
-        tmem_ld16(tm + kColX + 32 * half + 16 * h, x);
-        tmem_wait_ld();
-#pragma unroll
-        for (int e = 0; e < 16; e += 2) {
-          const int j = 16 * h + e;
-          pk[8 * h + (e >> 1)] = pack_bf16x2(j <= lane ? __uint_as_float(x[e]) * near[j] : 0.f,
-                                             j + 1 <= lane ? __uint_as_float(x[e + 1]) * near[j + 1] : 0.f);
-        }
-      }
-      uint32_t po[16];                                   // keys of the other half
-      if (half) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t x[16];
-          tmem_ld16(tm + kColX + 16 * h, x);
+      if (fast) {
+        // P's columns lie in front of the X still to be read: first the first
+        // half's keys for rows of the second, then the keys of the row's own half
+        uint32_t x[2][16], pk[16];
+        if (half) {
+          tmem_ld16(tm + kColX, x[0]);
+          tmem_ld16(tm + kColX + 16, x[1]);
           tmem_wait_ld();
 #pragma unroll
-          for (int e = 0; e < 16; e += 4) {
-            const float4 m = *reinterpret_cast<const float4 *>(&s.mid[16 * h + e]);
-            po[8 * h + (e >> 1)] = pack_bf16x2(__uint_as_float(x[e]) * (far * m.x), __uint_as_float(x[e + 1]) * (far * m.y));
-            po[8 * h + (e >> 1) + 1] = pack_bf16x2(__uint_as_float(x[e + 2]) * (far * m.z), __uint_as_float(x[e + 3]) * (far * m.w));
-          }
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int e = 0; e < 16; e += 4) {
+              const float4 r = *reinterpret_cast<const float4 *>(gates.rest + 16 * h + e);
+              pk[8 * h + (e >> 1)] = pack_bf16x2(__uint_as_float(x[h][e]) * r.x, __uint_as_float(x[h][e + 1]) * r.y);
+              pk[8 * h + (e >> 1) + 1] =
+                  pack_bf16x2(__uint_as_float(x[h][e + 2]) * r.z, __uint_as_float(x[h][e + 3]) * r.w);
+            }
+          tmem_st16(tm + kColX, pk);
         }
-      } else {
-#pragma unroll
-        for (int e = 0; e < 16; ++e) po[e] = 0u;
-      }
-      tmem_st16(tm + kColX + 16 * half, pk);
-      tmem_st16(tm + kColX + 16 * (1 - half), po);
-#pragma unroll
-      for (int h = 0; h < 4; ++h) {
-        uint32_t x[16];
-        tmem_ld16(tm + kColD + 16 * h, x);
+        tmem_ld16(tm + kColX + 32 * half, x[0]);
+        tmem_ld16(tm + kColX + 32 * half + 16, x[1]);
         tmem_wait_ld();
 #pragma unroll
-        for (int e = 0; e < 16; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * head);
-        tmem_st16(tm + kColD + 16 * h, x);
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int e = 0; e < 16; e += 4) {
+            const float4 r = *reinterpret_cast<const float4 *>(gates.rest + 32 * half + 16 * h + e);
+            const int j = 16 * h + e;
+            pk[8 * h + (e >> 1)] = pack_bf16x2(j <= lane ? __uint_as_float(x[h][e]) * r.x : 0.f,
+                                               j + 1 <= lane ? __uint_as_float(x[h][e + 1]) * r.y : 0.f);
+            pk[8 * h + (e >> 1) + 1] = pack_bf16x2(j + 2 <= lane ? __uint_as_float(x[h][e + 2]) * r.z : 0.f,
+                                                   j + 3 <= lane ? __uint_as_float(x[h][e + 3]) * r.w : 0.f);
+          }
+        tmem_st16(tm + kColX + 16 * half, pk);
+        if (!half) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) pk[e] = 0u;
+          tmem_st16(tm + kColX + 16, pk);
+        }
+      } else {
+        ok = warp_wait(&s.d_full, it & 1, abort_flag, p.status);
+        if (!ok) break;
+        tc_fence_after();
+        slow_scores(p.g + (size_t)bh * p.T, t0, n, i, gates.head[i], tm);
       }
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&s.p_full);
-      if (pr == npair - 1) {                             // Q S_in of the chunk's last pair is done
-        state_scale(acc, whole);
-        state_add(acc, s.k[c & 1], s.v[c & 1], s.tail[warp]);
+      // the state, while P V runs: half of the chunk with its first pair, the rest with its last
+      if (pr == 0) {
+        state_scale(acc, gates.head[kGC - 1]);
+        state_add<0, 2>(acc, s.k[c & 1], s.v[c & 1], gates.tail);
+      }
+      if (pr == npair - 1) {
+        state_add<2, 4>(acc, s.k[c & 1], s.v[c & 1], gates.tail);
+        ok = warp_wait(&s.d_full, it & 1, abort_flag, p.status);   // the chunk's last Q S_in is done
+        if (!ok) break;
         state_round(acc, s.state);
       }
       ok = warp_wait(&s.y_full, it & 1, abort_flag, p.status);
@@ -353,15 +428,16 @@ gated_tc_out_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
       const bool rows = by_rows(t0);
       uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.Y) + ((size_t)(h0 + hd) * p.T + t0 + i) * 64);
       uint8_t *tile = s.q[it & 1] + (warp >> 1) * kTileBytes;
+      uint32_t x[4][16];
+#pragma unroll
+      for (int h = 0; h < 4; ++h) tmem_ld16(tm + kColD + 16 * h, x[h]);
+      tmem_wait_ld();
 #pragma unroll
       for (int h = 0; h < 4; ++h) {
-        uint32_t x[16];
-        tmem_ld16(tm + kColD + 16 * h, x);
-        tmem_wait_ld();
         uint32_t y[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-          y[e] = pack_bf16x2(__uint_as_float(x[2 * e]) * p.scale, __uint_as_float(x[2 * e + 1]) * p.scale);
+          y[e] = pack_bf16x2(__uint_as_float(x[h][2 * e]) * row, __uint_as_float(x[h][2 * e + 1]) * row);
         const uint4 lo = make_uint4(y[0], y[1], y[2], y[3]), hi = make_uint4(y[4], y[5], y[6], y[7]);
         if (!rows) {
           *reinterpret_cast<uint4 *>(tile + tile_at(i, 2 * h)) = lo;

@@ -139,7 +139,9 @@ SHAPES = [  # B, Hq, Hkv, T, cut, lengths, cont
     (1, 2, 1, 63, 0.0, None, False), (1, 2, 2, 64, 0.0, None, True), (2, 2, 1, 65, 0.05, None, True),
     (1, 7, 1, 128, 0.0, None, False), (1, 14, 2, 129, 0.02, None, True), (2, 10, 2, 191, 0.0, [191, 17], False),
     (4, 4, 2, 333, 0.01, [0, 1, 333, 64], True), (1, 4, 4, 640, 0.0, None, False),
-    (3, 9, 1, 257, 1.0, [257, 256, 3], True), (1, 8, 1, 2050, 0.001, None, True)]
+    (3, 9, 1, 257, 1.0, [257, 256, 3], True), (1, 8, 1, 2050, 0.001, None, True),
+    # segments of several chunks: one segment a sequence, and two
+    (160, 3, 3, 170, 0.003, [170, 169, 128, 129, 5, 0, 64, 65] * 20, True), (60, 10, 2, 400, 0.003, None, False)]
 
 
 @pytest.mark.parametrize("dtype", DTYPES, ids=["f32", "bf16"])
