@@ -9,11 +9,14 @@
 //     D += P V                         tcgen05, P from tensor memory
 // and the state itself in registers (gated_mma.cuh).
 //
-// Where the chunk's sums G stay within +-60 and no gate is cut, a row's factor
-// is taken out of the sum: y_i = scale e^{G_i} [ S_in^T q_i + sum_j (q_i.k_j)
-// e^{-G_j} v_j ], one product a score and one a result; no factor exceeds
-// e^60, and a row's terms keep their ratios.  Other chunks form every decay
-// exp(G_i - G_j) by itself and scale D before P V is added.
+// Where the sums G of each half chunk span at most 60, a row's factor is taken
+// out of its sum: with R = 0 for the first 32 rows, and G_31 for the others
+// unless the whole chunk spans at most 60,
+//     y_i = scale e^{G_i-R} [ e^R S_in^T q_i + sum_j (q_i.k_j) e^{R-G_j} v_j ],
+// one product a score and one a result; no factor exceeds e^60, and the terms
+// of a row keep their ratios.  A cut gate leaves the sums alone and masks the
+// scores and S_in instead.  Other chunks form every decay exp(G_i - G_j) by
+// itself.
 #include <algorithm>
 #include <mutex>
 
@@ -59,6 +62,11 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volati
 __device__ __forceinline__ void *align1024(void *p) {
   return reinterpret_cast<void *>((reinterpret_cast<uintptr_t>(p) + 1023) & ~(uintptr_t)1023);
 }
+
+// What a chunk's gates ask for: nothing (R = 0, no cuts), R per half and
+// masks, or every decay by itself.
+constexpr int kPlain = 0, kHalves = 1, kEach = 2;
+constexpr float kSpan = 60.f;
 
 // Rows from `rows` on of a tile become zeros (threads 0 .. 127).
 __device__ __forceinline__ void clear_rows(void *tile, int rows) {
@@ -135,8 +143,10 @@ struct OutSmem {
   uint8_t q[2][2 * kTileBytes];          // two heads' queries, then their outputs
   uint8_t state[kTileBytes];             // the state before the chunk, bf16
   struct alignas(16) Gates {             // of a chunk, by the issuing warp
-    float tail[kGC], rest[kGC], head[kGC];   // e^{G_63-G_j}, e^{-G_j}, e^{G_i}
-    int fast;
+    float tail[kGC], rest[kGC], row[kGC];   // e^{G_63-G_j}, e^{R-G_j}, e^{G_i-R}
+    float whole, first;                     // e^{G_63} (0 if cut), e^{G_31}
+    uint32_t cut_even, cut_odd;             // bit l: the gate of token 2l (2l + 1) is cut
+    int mode;
   } gates[2];
   uint64_t kv_full[2], q_full[2], gate_full, x_full, d_full, p_full, y_full, go, meet, drain;
   uint32_t tmem;
@@ -144,10 +154,9 @@ struct OutSmem {
 };
 static_assert(3 * (sizeof(OutSmem) + 2 * 1024) <= 228 * 1024, "three blocks per SM");
 
-// Scores and D of a chunk whose gates are cut or drop far: every decay by
-// itself, P in the place of X, D scaled by e^{G_i} (one row a thread; compact,
-// not fast: a few chunks of a packed sequence pass here).
-__device__ __noinline__ void slow_scores(const float *g, int t0, int n, int i, float head, uint32_t tm) {
+// Scores and D of a chunk whose gates drop too far for the other ways: every
+// decay by itself, P in the place of X, D scaled by e^{G_i} (one row a thread).
+__device__ __noinline__ void slow_scores(const float *g, int t0, int n, int i, uint32_t tm) {
   const GateLane s = gate_sums(gate_load(g, t0, n));
   const bool odd = i & 1;
   const float h0 = __shfl_sync(0xffffffffu, s.hi[0], i >> 1), h1 = __shfl_sync(0xffffffffu, s.hi[1], i >> 1);
@@ -155,6 +164,7 @@ __device__ __noinline__ void slow_scores(const float *g, int t0, int n, int i, f
   const int c0 = __shfl_sync(0xffffffffu, s.cuts[0], i >> 1), c1 = __shfl_sync(0xffffffffu, s.cuts[1], i >> 1);
   const float hi = odd ? h1 : h0, lo = odd ? l1 : l0;
   const int cut = odd ? c1 : c0;
+  const float head = gate_exp_fast(cut == 0, hi + lo);
   for (int h = 0; h < 4; ++h) {         // P's 8 columns lie in front of the X still to be read
     uint32_t x[16], d[16];
     tmem_ld16(tm + kColX + 16 * h, x);
@@ -236,12 +246,6 @@ gated_tc_out_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
       tma_load_3d(s.k[c & 1], &tmK, &s.kv_full[c & 1], 0, (c0 + c) * kGC, bh);
       tma_load_3d(s.v[c & 1], &tmV, &s.kv_full[c & 1], 0, (c0 + c) * kGC, bh);
     };
-    auto store_y = [&](int it) {
-      const int pr = it % npair, heads = min(2, rho - 2 * pr), t0 = (c0 + it / npair) * kGC;
-      if (!by_rows(t0))
-        for (int h = 0; h < heads; ++h) tma_store_3d(&tmY, s.q[it & 1] + h * kTileBytes, 0, t0, h0 + 2 * pr + h);
-      bulk_commit();
-    };
     int kv_loads = 0, q_loads = 0;
     if (lane == 0) {
       for (; kv_loads < min(2, nc); ++kv_loads) load_kv(kv_loads);
@@ -265,15 +269,27 @@ gated_tc_out_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
     float2 gate = gate_load(g, c0 * kGC, n);
     auto make_gates = [&](int c) {
       const GateLane sums = gate_sums(gate);
-      if (c + 1 < nc) gate = gate_load(g, (c0 + c + 1) * kGC, n);
       OutSmem::Gates &to = s.gates[c & 1];
-      gate_tails(sums, to.tail);
-      reinterpret_cast<float2 *>(to.rest)[lane] = make_float2(__expf(-sums.hi[0]), __expf(-sums.hi[1]));
-      reinterpret_cast<float2 *>(to.head)[lane] = make_float2(gate_exp_fast(sums.cuts[0] == 0, sums.hi[0] + sums.lo[0]),
-                                                              gate_exp_fast(sums.cuts[1] == 0, sums.hi[1] + sums.lo[1]));
-      const float most = fmaxf(fabsf(sums.hi[0]), fabsf(sums.hi[1]));
-      const int fast = __all_sync(0xffffffffu, most <= 60.f && sums.cuts[1] == 0);
-      if (lane == 0) to.fast = fast;
+      const uint32_t even = __ballot_sync(0xffffffffu, gate.x <= kGateCut);
+      const uint32_t odd = __ballot_sync(0xffffffffu, gate.y <= kGateCut);
+      if (c + 1 < nc) gate = gate_load(g, (c0 + c + 1) * kGC, n);
+      const float whole = gate_tails(sums, to.tail);
+      const float mh = __shfl_sync(0xffffffffu, sums.hi[1], 15), ml = __shfl_sync(0xffffffffu, sums.lo[1], 15);
+      const float span = fmaxf(fabsf(sums.hi[0]), fabsf(sums.hi[1]));
+      const bool plain = __all_sync(0xffffffffu, span <= kSpan) && (even | odd) == 0u;
+      const float rh = plain || lane < 16 ? 0.f : mh, rl = plain || lane < 16 ? 0.f : ml;
+      const float near = fmaxf(fabsf(sums.hi[0] - rh), fabsf(sums.hi[1] - rh));
+      const bool halves = __all_sync(0xffffffffu, near <= kSpan);
+      const float x0 = (sums.hi[0] - rh) + (sums.lo[0] - rl), x1 = (sums.hi[1] - rh) + (sums.lo[1] - rl);
+      reinterpret_cast<float2 *>(to.rest)[lane] = make_float2(__expf(-x0), __expf(-x1));
+      reinterpret_cast<float2 *>(to.row)[lane] = make_float2(__expf(x0), __expf(x1));
+      if (lane == 0) {
+        to.whole = whole;
+        to.first = __expf(mh + ml);
+        to.cut_even = even;
+        to.cut_odd = odd;
+        to.mode = plain ? kPlain : halves ? kHalves : kEach;
+      }
       __syncwarp();
       if (lane == 0) mbar_arrive(&s.gate_full);
     };
@@ -293,12 +309,7 @@ gated_tc_out_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
       for (int k = 0; k < 4; ++k) umma_ss_warp(tb + kColD, qd + 2 * k, sd + 128 * k, id_mn, k > 0);
       umma_commit_warp(&s.d_full);
       if (lane == 0) {
-        if (it > 0) store_y(it - 1);
         if (pr == 0 && c > 0 && c + 1 < nc) load_kv(c + 1), ++kv_loads;
-        if (it > 0 && it + 1 < steps) {
-          bulk_wait_read();
-          load_q(it + 1), ++q_loads;
-        }
         if (it + 2 < steps) prefetch_q(it + 2);
       }
       __syncwarp();
@@ -308,17 +319,18 @@ gated_tc_out_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
 #pragma unroll
       for (int k = 0; k < 4; ++k) umma_ts_warp(tb + kColD, tb + kColX + 8 * k, vd + 128 * k, id_mn, 1u);
       umma_commit_warp(&s.y_full);
+      // the outputs of the step before have left their buffer (p_full says so)
+      if (lane == 0 && it > 0 && it + 1 < steps) load_q(it + 1), ++q_loads;
+      __syncwarp();
       // P, which lies in X, has been read
       if (it + 1 < steps) ok = warp_wait(&s.y_full, it & 1, abort_flag, p.status) && issue_x(it + 1);
       if (pr == 0 && c + 1 < nc) make_gates(c + 1);
     }
-    if (ok && steps > 0 && warp_wait(&s.go, steps & 1, abort_flag, p.status) && lane == 0) store_y(steps - 1);
     umma_commit_warp(&s.drain);
     if (lane == 0) {   // nothing in flight at the block's end
       mbar_wait_teardown(&s.drain, 0, p.status);
       for (int i = max(0, kv_loads - 2); i < kv_loads; ++i) mbar_wait_teardown(&s.kv_full[i & 1], (i >> 1) & 1, p.status);
       for (int i = max(0, q_loads - 2); i < q_loads; ++i) mbar_wait_teardown(&s.q_full[i & 1], (i >> 1) & 1, p.status);
-      bulk_wait_all();
     }
     __syncwarp();
   } else {
@@ -332,8 +344,9 @@ gated_tc_out_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
     __syncwarp();
     if (lane == 0) mbar_arrive(&s.go);
     float row = 0.f;                                      // factor of the row's result
+    float into = 1.f;                                    // (kHalves) factor of S_in^T q_i
+    int begin = 0, mode = kPlain;                        // first key of the row
     bool ok = true;
-    int fast = 1;
     // the four computing warps meet (a wait that ends, unlike a barrier of threads)
     int met = 0;
     auto meet = [&]() {
@@ -347,8 +360,16 @@ gated_tc_out_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
       if (pr == 0) {
         ok = warp_wait(&s.gate_full, c & 1, abort_flag, p.status);
         if (!ok) break;
-        fast = gates.fast;
-        row = fast ? p.scale * gates.head[i] : p.scale;
+        mode = gates.mode;
+        row = mode == kEach ? p.scale : p.scale * gates.row[i];
+        begin = 0;
+        into = half && mode == kHalves ? gates.first : 1.f;
+        const uint32_t upto = (2u << (i >> 1)) - 1u;     // bits l with 2 l <= i
+        const uint32_t even = gates.cut_even & upto, odd = gates.cut_odd & (i & 1 ? upto : upto >> 1);
+        if (even | odd) {                                // keys from the row's last cut gate on, nothing from S_in
+          begin = max(2 * (31 - __clz(even)), 2 * (31 - __clz(odd)) + 1);
+          into = 0.f;
+        }
         ok = warp_wait(&s.kv_full[c & 1], (c >> 1) & 1, abort_flag, p.status);
       }
       ok = ok && warp_wait(&s.x_full, it & 1, abort_flag, p.status);
@@ -361,7 +382,7 @@ gated_tc_out_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
         ok = meet();
         if (!ok) break;
       }
-      if (fast) {
+      if (mode != kEach) {
         // P's columns lie in front of the X still to be read: first the first
         // half's keys for rows of the second, then the keys of the row's own half
         uint32_t x[2][16], pk[16];
@@ -369,6 +390,11 @@ gated_tc_out_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
           tmem_ld16(tm + kColX, x[0]);
           tmem_ld16(tm + kColX + 16, x[1]);
           tmem_wait_ld();
+          if (mode == kHalves) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              x[e >> 4][e & 15] = e >= begin ? __float_as_uint(__uint_as_float(x[e >> 4][e & 15]) * gates.first) : 0u;
+          }
 #pragma unroll
           for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -380,6 +406,7 @@ gated_tc_out_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
             }
           tmem_st16(tm + kColX, pk);
         }
+        const uint32_t mask = (0xFFFFFFFFu >> (31 - lane)) & (0xFFFFFFFFu << max(0, begin - 32 * half));   // begin <= i
         tmem_ld16(tm + kColX + 32 * half, x[0]);
         tmem_ld16(tm + kColX + 32 * half + 16, x[1]);
         tmem_wait_ld();
@@ -389,10 +416,10 @@ gated_tc_out_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
           for (int e = 0; e < 16; e += 4) {
             const float4 r = *reinterpret_cast<const float4 *>(gates.rest + 32 * half + 16 * h + e);
             const int j = 16 * h + e;
-            pk[8 * h + (e >> 1)] = pack_bf16x2(j <= lane ? __uint_as_float(x[h][e]) * r.x : 0.f,
-                                               j + 1 <= lane ? __uint_as_float(x[h][e + 1]) * r.y : 0.f);
-            pk[8 * h + (e >> 1) + 1] = pack_bf16x2(j + 2 <= lane ? __uint_as_float(x[h][e + 2]) * r.z : 0.f,
-                                                   j + 3 <= lane ? __uint_as_float(x[h][e + 3]) * r.w : 0.f);
+            pk[8 * h + (e >> 1)] = pack_bf16x2(mask & (1u << (j)) ? __uint_as_float(x[h][e]) * r.x : 0.f,
+                                               mask & (1u << (j + 1)) ? __uint_as_float(x[h][e + 1]) * r.y : 0.f);
+            pk[8 * h + (e >> 1) + 1] = pack_bf16x2(mask & (1u << (j + 2)) ? __uint_as_float(x[h][e + 2]) * r.z : 0.f,
+                                                   mask & (1u << (j + 3)) ? __uint_as_float(x[h][e + 3]) * r.w : 0.f);
           }
         tmem_st16(tm + kColX + 16 * half, pk);
         if (!half) {
@@ -404,15 +431,32 @@ gated_tc_out_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
         ok = warp_wait(&s.d_full, it & 1, abort_flag, p.status);
         if (!ok) break;
         tc_fence_after();
-        slow_scores(p.g + (size_t)bh * p.T, t0, n, i, gates.head[i], tm);
+        slow_scores(p.g + (size_t)bh * p.T, t0, n, i, tm);
+      }
+      if (mode == kHalves) {
+        ok = warp_wait(&s.d_full, it & 1, abort_flag, p.status);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll 1
+        for (int h = 0; h < 4; ++h) {
+          uint32_t x[16];
+          tmem_ld16(tm + kColD + 16 * h, x);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 16; ++e) x[e] = into == 0.f ? 0u : __float_as_uint(__uint_as_float(x[e]) * into);
+          tmem_st16(tm + kColD + 16 * h, x);
+        }
       }
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&s.p_full);
+      if (lane == 0) {
+        bulk_wait_read();                                // the outputs of the step before are out of shared memory
+        mbar_arrive(&s.p_full);
+      }
       // the state, while P V runs: half of the chunk with its first pair, the rest with its last
       if (pr == 0) {
-        state_scale(acc, gates.head[kGC - 1]);
+        state_scale(acc, gates.whole);
         state_add<0, 2>(acc, s.k[c & 1], s.v[c & 1], gates.tail);
       }
       if (pr == npair - 1) {
@@ -450,8 +494,13 @@ gated_tc_out_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
       fence_proxy_async();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&s.go);
+      if (lane == 0) {
+        if (!rows && hd < rho && t0 + 32 * half < n) tma_store_3d(&tmY, tile + 32 * half * 128, 0, t0 + 32 * half, h0 + hd);
+        bulk_commit();
+        mbar_arrive(&s.go);
+      }
     }
+    if (lane == 0) bulk_wait_all();
     if (seg == last && ok) state_store(acc, p.state_out + (size_t)bh * kGS);
   }
   tc_fence_before();
@@ -476,14 +525,14 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-// [heads][T][64] bf16 in boxes of 64 rows, 128-byte swizzle; rows from T on
+// [heads][T][64] bf16 in boxes of 64 columns, 128-byte swizzle; rows from T on
 // read as zeros and are not written.
-oal_status make_map(CUtensorMap *m, const void *ptr, int T, long long heads) {
+oal_status make_map(CUtensorMap *m, const void *ptr, int T, long long heads, int rows = kGC) {
   auto fn = encode_fn();
   if (!fn) return oal_fail(OAL_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
   const cuuint64_t dims[3] = {64, (cuuint64_t)T, (cuuint64_t)heads};
   const cuuint64_t strides[2] = {128, (cuuint64_t)T * 128};
-  const cuuint32_t box[3] = {64, kGC, 1}, es[3] = {1, 1, 1};
+  const cuuint32_t box[3] = {64, (cuuint32_t)rows, 1}, es[3] = {1, 1, 1};
   if (fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(ptr), dims, strides, box, es,
          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
@@ -510,7 +559,7 @@ oal_status launch_gated_prefill_tc(const GatedArgs &p, cudaStream_t stream) {
   GATED_TRY(make_map(&tmQ, p.Q, p.T, (long long)p.B * p.Hq));
   GATED_TRY(make_map(&tmK, p.K, p.T, (long long)p.B * p.Hkv));
   GATED_TRY(make_map(&tmV, p.V, p.T, (long long)p.B * p.Hkv));
-  GATED_TRY(make_map(&tmY, p.Y, p.T, (long long)p.B * p.Hq));
+  GATED_TRY(make_map(&tmY, p.Y, p.T, (long long)p.B * p.Hq, 32));
   const dim3 grid(p.nseg * p.B * p.Hkv);
   if (p.nseg > 1) {
     launch_pdl(gated_tc_segment_kernel, grid, dim3(kSegThreads), seg_smem, stream, tmK, tmV, p);
