@@ -3,8 +3,8 @@
 // 16-byte chunk c of row r at chunk c ^ (r & 7), as a 128-byte-swizzled TMA
 // copy leaves it).
 //
-// The states live in registers, split over four warps (warp w owns rows
-// 16 w .. 16 w + 15), because every chunk scales them by a decay and adds a
+// The states live in registers, split over four or eight warps (warp w owns
+// rows 16 (w % 4) .. + 15 of all columns or of half of them), because every chunk scales them by a decay and adds a
 // product: in tensor memory that would be a read and a write of the state per
 // chunk besides the product.
 #pragma once
@@ -32,24 +32,34 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// A 64 x 64 fp32 matrix over four warps: acc[nb][0..3] = rows r, r, r + 8,
-// r + 8 (r = 16 warp + lane / 4), columns 8 nb + 2 (lane % 4) and the next.
+// Columns 8 nb0 .. 8 (nb0 + kNb) - 1 of a 64 x 64 fp32 matrix over four warps:
+// v[nb][0..3] = rows r, r, r + 8, r + 8 (r = 16 warp + lane / 4), columns
+// 8 (nb0 + nb) + 2 (lane % 4) and the next.
+template <int kNb>
 struct StateAcc {
-  float v[8][4];
+  float v[kNb][4];
 };
 
 // s += sum_j w_j a_j b_j^T over the 64 rows j of two tiles, w in shared
-// memory (kFrom, kTo: of the rows, 16 at a time).  w_j a_j is held as two bf16 terms, off by at most 2^-16 of it, so
-// the sum keeps about 16 bits more than a rounded factor would; b is exact.
-template <int kFrom = 0, int kTo = 4>
-__device__ __forceinline__ void state_add(StateAcc &s, const void *a_tile, const void *b_tile, const float *w) {
+// memory (kFrom, kTo: of the rows, 16 at a time).  w_j a_j is held as two bf16
+// terms, off by at most 2^-16 of it, so the sum keeps about 16 bits more than
+// a rounded factor would; b is exact.
+// The two terms of one accumulator are kNb products apart, and the next
+// 16 rows' operand is under way while these multiply.
+template <int kFrom, int kTo, int kNb>
+__device__ __forceinline__ void state_add(StateAcc<kNb> &s, int nb0, const void *a_tile, const void *b_tile,
+                                          const float *w) {
   const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3;
   const uint32_t at = tc::smem_u32(a_tile), bt = tc::smem_u32(b_tile);
   const int mat = lane >> 3, r = lane & 7, q = lane & 3;
+  uint32_t a[4], b[kNb / 2][4];
+  ldsm4t(at + tile_at(16 * kFrom + 8 * (mat >> 1) + r, 2 * warp + (mat & 1)), a);
 #pragma unroll
   for (int ks = kFrom; ks < kTo; ++ks) {
-    uint32_t a[4], hi[4], lo[4];
-    ldsm4t(at + tile_at(16 * ks + 8 * (mat >> 1) + r, 2 * warp + (mat & 1)), a);
+#pragma unroll
+    for (int np = 0; np < kNb / 2; ++np)
+      ldsm4t(bt + tile_at(16 * ks + 8 * (mat & 1) + r, nb0 + 2 * np + (mat >> 1)), b[np]);
+    uint32_t hi[4], lo[4];
     const float2 w0 = *reinterpret_cast<const float2 *>(w + 16 * ks + 2 * q);
     const float2 w1 = *reinterpret_cast<const float2 *>(w + 16 * ks + 8 + 2 * q);
 #pragma unroll
@@ -59,53 +69,54 @@ __device__ __forceinline__ void state_add(StateAcc &s, const void *a_tile, const
       hi[e] = tc::pack_bf16x2(x, y);
       lo[e] = tc::pack_bf16x2(x - __uint_as_float(hi[e] << 16), y - __uint_as_float(hi[e] & 0xFFFF0000u));
     }
+    if (ks + 1 < kTo) ldsm4t(at + tile_at(16 * (ks + 1) + 8 * (mat >> 1) + r, 2 * warp + (mat & 1)), a);
 #pragma unroll
-    for (int np = 0; np < 4; ++np) {
-      uint32_t b[4];
-      ldsm4t(bt + tile_at(16 * ks + 8 * (mat & 1) + r, 2 * np + (mat >> 1)), b);
-      mma16816(s.v[2 * np], hi, b[0], b[1]);
-      mma16816(s.v[2 * np + 1], hi, b[2], b[3]);
-      mma16816(s.v[2 * np], lo, b[0], b[1]);
-      mma16816(s.v[2 * np + 1], lo, b[2], b[3]);
-    }
+    for (int nb = 0; nb < kNb; ++nb) mma16816(s.v[nb], hi, b[nb >> 1][2 * (nb & 1)], b[nb >> 1][2 * (nb & 1) + 1]);
+#pragma unroll
+    for (int nb = 0; nb < kNb; ++nb) mma16816(s.v[nb], lo, b[nb >> 1][2 * (nb & 1)], b[nb >> 1][2 * (nb & 1) + 1]);
   }
 }
-__device__ __forceinline__ void state_scale(StateAcc &s, float f) {
+template <int kNb>
+__device__ __forceinline__ void state_scale(StateAcc<kNb> &s, float f) {
 #pragma unroll
-  for (int nb = 0; nb < 8; ++nb)
+  for (int nb = 0; nb < kNb; ++nb)
 #pragma unroll
     for (int e = 0; e < 4; ++e) s.v[nb][e] *= f;
 }
-__device__ __forceinline__ void state_load(StateAcc &s, const float *src) {
+template <int kNb>
+__device__ __forceinline__ void state_load(StateAcc<kNb> &s, int nb0, const float *src) {
   const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3;
-  const int r = 16 * warp + (lane >> 2), c = 2 * (lane & 3);
+  const int r = 16 * warp + (lane >> 2), c = 8 * nb0 + 2 * (lane & 3);
 #pragma unroll
-  for (int nb = 0; nb < 8; ++nb)
+  for (int nb = 0; nb < kNb; ++nb)
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const float2 x = src ? *reinterpret_cast<const float2 *>(src + (r + 8 * h) * 64 + 8 * nb + c) : make_float2(0.f, 0.f);
       s.v[nb][2 * h] = x.x, s.v[nb][2 * h + 1] = x.y;
     }
 }
-__device__ __forceinline__ void state_store(const StateAcc &s, float *dst) {
+template <int kNb>
+__device__ __forceinline__ void state_store(const StateAcc<kNb> &s, int nb0, float *dst) {
   const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3;
-  const int r = 16 * warp + (lane >> 2), c = 2 * (lane & 3);
+  const int r = 16 * warp + (lane >> 2), c = 8 * nb0 + 2 * (lane & 3);
 #pragma unroll
-  for (int nb = 0; nb < 8; ++nb)
+  for (int nb = 0; nb < kNb; ++nb)
 #pragma unroll
     for (int h = 0; h < 2; ++h)
       *reinterpret_cast<float2 *>(dst + (r + 8 * h) * 64 + 8 * nb + c) = make_float2(s.v[nb][2 * h], s.v[nb][2 * h + 1]);
 }
-// The matrix rounded to bf16 as a tile (row d of the state = row d of the tile).
-__device__ __forceinline__ void state_round(const StateAcc &s, void *tile) {
+// The columns rounded to bf16 into a tile (row d of the state = row d of the tile).
+template <int kNb>
+__device__ __forceinline__ void state_round(const StateAcc<kNb> &s, int nb0, void *tile) {
   const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3;
   const int r = 16 * warp + (lane >> 2), c = 4 * (lane & 3);
   uint8_t *t = static_cast<uint8_t *>(tile);
 #pragma unroll
-  for (int nb = 0; nb < 8; ++nb)
+  for (int nb = 0; nb < kNb; ++nb)
 #pragma unroll
     for (int h = 0; h < 2; ++h)
-      *reinterpret_cast<uint32_t *>(t + tile_at(r + 8 * h, nb) + c) = tc::pack_bf16x2(s.v[nb][2 * h], s.v[nb][2 * h + 1]);
+      *reinterpret_cast<uint32_t *>(t + tile_at(r + 8 * h, nb0 + nb) + c) =
+          tc::pack_bf16x2(s.v[nb][2 * h], s.v[nb][2 * h + 1]);
 }
 
 // Decays from behind each token to the end of the chunk (out, 64 floats of

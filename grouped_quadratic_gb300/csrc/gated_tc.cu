@@ -59,9 +59,10 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t *r) {
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort, int *status) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, status));
 }
-__device__ __forceinline__ void *align1024(void *p) {
-  return reinterpret_cast<void *>((reinterpret_cast<uintptr_t>(p) + 1023) & ~(uintptr_t)1023);
-}
+// The first 1024-byte boundary of the dynamic shared memory.  (By an offset: a
+// pointer rounded as an integer is one the compiler no longer knows to be
+// shared, and every access through it a generic one.)
+__device__ __forceinline__ uint8_t *align1024(uint8_t *p) { return p + ((1024u - (smem_u32(p) & 1023u)) & 1023u); }
 
 // What a chunk's gates ask for: nothing (R = 0, no cuts), R per half and
 // masks, or every decay by itself.
@@ -89,7 +90,7 @@ gated_tc_segment_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_co
                         GatedArgs p) {
   pdl_trigger();
   extern __shared__ uint8_t smem_raw[];
-  SegSmem &s = *static_cast<SegSmem *>(align1024(smem_raw));
+  SegSmem &s = *reinterpret_cast<SegSmem *>(align1024(smem_raw));
   const int bh = blockIdx.x / p.nseg, seg = blockIdx.x % p.nseg, b = bh / p.Hkv;
   const int tid = threadIdx.x, warp = tid >> 5;
   if (tid == 0) {
@@ -113,8 +114,8 @@ gated_tc_segment_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_co
     for (int c = 0; c < min(kStages, nc); ++c) load(c);
   const float *g = p.g + (size_t)bh * p.T;
   float2 gate = gate_load(g, c0 * kGC, n);
-  StateAcc acc;
-  state_load(acc, nullptr);
+  StateAcc<8> acc;
+  state_load(acc, 0, nullptr);
   float decay = 1.f;
   bool ok = true;
   for (int c = 0; c < nc; ++c) {
@@ -125,14 +126,14 @@ gated_tc_segment_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_co
     state_scale(acc, whole);
     __syncwarp();
     ok = ok && mbar_wait(&s.full[c % kStages], (c / kStages) & 1, abort_flag, p.status);
-    if (ok) state_add(acc, s.a[c % kStages], s.b[c % kStages], s.tail[warp]);
+    if (ok) state_add<0, 4>(acc, 0, s.a[c % kStages], s.b[c % kStages], s.tail[warp]);
     __syncthreads();
     if (tid == 0 && ok && c + kStages < nc) load(c + kStages);
   }
   if (tid == 0 && !ok)   // copies still in flight land before the block ends
     for (int i = 0; i < min(kStages, nc); ++i)
       for (int ph = 0; ph < 2; ++ph) mbar_wait_teardown(&s.full[i], ph, p.status);
-  state_store(acc, p.seg_state + ((size_t)bh * p.nseg + seg) * kGS);
+  state_store(acc, 0, p.seg_state + ((size_t)bh * p.nseg + seg) * kGS);
   if (tid == 0) p.seg_decay[(size_t)bh * p.nseg + seg] = decay;
 }
 
@@ -193,7 +194,7 @@ gated_tc_out_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
                     GatedArgs p) {
   pdl_trigger();
   extern __shared__ uint8_t smem_raw[];
-  OutSmem &s = *static_cast<OutSmem *>(align1024(smem_raw));
+  OutSmem &s = *reinterpret_cast<OutSmem *>(align1024(smem_raw));
   const int bh = blockIdx.x / p.nseg, seg = blockIdx.x % p.nseg, b = bh / p.Hkv, kv = bh % p.Hkv;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rho = p.Hq / p.Hkv, npair = (rho + 1) / 2;
@@ -336,10 +337,10 @@ gated_tc_out_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
   } else {
     const int i = tid & 63, half = warp & 1;            // token of this thread's row, its 32-token half
     const uint32_t tm = tb + ((uint32_t)(32 * warp) << 16);
-    StateAcc acc;
-    state_load(acc, p.nseg > 1 ? p.seg_state + ((size_t)bh * p.nseg + seg) * kGS
+    StateAcc<8> acc;
+    state_load(acc, 0, p.nseg > 1 ? p.seg_state + ((size_t)bh * p.nseg + seg) * kGS
                                : p.state_in ? p.state_in + (size_t)bh * kGS : nullptr);
-    state_round(acc, s.state);
+    state_round(acc, 0, s.state);
     fence_proxy_async();
     __syncwarp();
     if (lane == 0) mbar_arrive(&s.go);
@@ -457,13 +458,13 @@ gated_tc_out_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
       // the state, while P V runs: half of the chunk with its first pair, the rest with its last
       if (pr == 0) {
         state_scale(acc, gates.whole);
-        state_add<0, 2>(acc, s.k[c & 1], s.v[c & 1], gates.tail);
+        state_add<0, 2>(acc, 0, s.k[c & 1], s.v[c & 1], gates.tail);
       }
       if (pr == npair - 1) {
-        state_add<2, 4>(acc, s.k[c & 1], s.v[c & 1], gates.tail);
+        state_add<2, 4>(acc, 0, s.k[c & 1], s.v[c & 1], gates.tail);
         ok = warp_wait(&s.d_full, it & 1, abort_flag, p.status);   // the chunk's last Q S_in is done
         if (!ok) break;
-        state_round(acc, s.state);
+        state_round(acc, 0, s.state);
       }
       ok = warp_wait(&s.y_full, it & 1, abort_flag, p.status);
       if (!ok) break;
@@ -501,7 +502,7 @@ gated_tc_out_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
       }
     }
     if (lane == 0) bulk_wait_all();
-    if (seg == last && ok) state_store(acc, p.state_out + (size_t)bh * kGS);
+    if (seg == last && ok) state_store(acc, 0, p.state_out + (size_t)bh * kGS);
   }
   tc_fence_before();
   __syncthreads();
