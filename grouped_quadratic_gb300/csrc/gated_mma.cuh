@@ -40,36 +40,61 @@ struct StateAcc {
   float v[kNb][4];
 };
 
-// s += sum_j w_j a_j b_j^T over the 64 rows j of two tiles, w in shared
-// memory (kFrom, kTo: of the rows, 16 at a time).  w_j a_j is held as two bf16
-// terms, off by at most 2^-16 of it, so the sum keeps about 16 bits more than
-// a rounded factor would; b is exact.
+// A weight per token of a chunk as two bf16 terms (the sum is off by at most
+// 2^-16 of it), in pairs: word l has tokens 2l and 2l + 1.
+struct __align__(16) PairWeights {
+  uint32_t hi[kGC / 2], lo[kGC / 2];
+};
+__device__ __forceinline__ void weights_put(PairWeights &w, float x, float y) {
+  const int lane = threadIdx.x & 31;
+  const uint32_t hi = tc::pack_bf16x2(x, y);
+  w.hi[lane] = hi;
+  w.lo[lane] = tc::pack_bf16x2(x - __uint_as_float(hi << 16), y - __uint_as_float(hi & 0xFFFF0000u));
+}
+__device__ __forceinline__ uint32_t bf2_mul(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t bf2_fma(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+
+// s += sum_j w_j a_j b_j^T over the 64 rows j of two tiles (kFrom, kTo: of the
+// rows, 16 at a time).  w_j a_j goes in as two bf16 terms: hi = bf16(w_hi a),
+// whose rounding error w_hi a - hi is a bf16 number itself, and
+// lo = bf16(w_lo a + that), three packed products for two values; the terms'
+// sum is off by at most 2^-15 of w a where one rounded factor would be off by
+// 2^-8.  b is exact.
 // The two terms of one accumulator are kNb products apart, and the next
 // 16 rows' operand is under way while these multiply.
 template <int kFrom, int kTo, int kNb>
 __device__ __forceinline__ void state_add(StateAcc<kNb> &s, int nb0, const void *a_tile, const void *b_tile,
-                                          const float *w) {
+                                          const PairWeights &w) {
   const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3;
-  const uint32_t at = tc::smem_u32(a_tile), bt = tc::smem_u32(b_tile);
   const int mat = lane >> 3, r = lane & 7, q = lane & 3;
+  // (16 rows further on is 2048 bytes: the swizzle goes by the row's low three bits)
+  const uint32_t at = tc::smem_u32(a_tile) + tile_at(8 * (mat >> 1) + r, 2 * warp + (mat & 1));
+  uint32_t bt[kNb / 2];
+#pragma unroll
+  for (int np = 0; np < kNb / 2; ++np)
+    bt[np] = tc::smem_u32(b_tile) + tile_at(8 * (mat & 1) + r, nb0 + 2 * np + (mat >> 1));
   uint32_t a[4], b[kNb / 2][4];
-  ldsm4t(at + tile_at(16 * kFrom + 8 * (mat >> 1) + r, 2 * warp + (mat & 1)), a);
+  ldsm4t(at + 2048 * kFrom, a);
 #pragma unroll
   for (int ks = kFrom; ks < kTo; ++ks) {
 #pragma unroll
-    for (int np = 0; np < kNb / 2; ++np)
-      ldsm4t(bt + tile_at(16 * ks + 8 * (mat & 1) + r, nb0 + 2 * np + (mat >> 1)), b[np]);
+    for (int np = 0; np < kNb / 2; ++np) ldsm4t(bt[np] + 2048 * ks, b[np]);
     uint32_t hi[4], lo[4];
-    const float2 w0 = *reinterpret_cast<const float2 *>(w + 16 * ks + 2 * q);
-    const float2 w1 = *reinterpret_cast<const float2 *>(w + 16 * ks + 8 + 2 * q);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const float2 f = e < 2 ? w0 : w1;
-      const float x = __uint_as_float(a[e] << 16) * f.x, y = __uint_as_float(a[e] & 0xFFFF0000u) * f.y;
-      hi[e] = tc::pack_bf16x2(x, y);
-      lo[e] = tc::pack_bf16x2(x - __uint_as_float(hi[e] << 16), y - __uint_as_float(hi[e] & 0xFFFF0000u));
+      const uint32_t wh = w.hi[8 * ks + 4 * (e >> 1) + q], wl = w.lo[8 * ks + 4 * (e >> 1) + q];
+      hi[e] = bf2_mul(wh, a[e]);
+      lo[e] = bf2_fma(wl, a[e], bf2_fma(wh, a[e], hi[e] ^ 0x80008000u));
     }
-    if (ks + 1 < kTo) ldsm4t(at + tile_at(16 * (ks + 1) + 8 * (mat >> 1) + r, 2 * warp + (mat & 1)), a);
+    if (ks + 1 < kTo) ldsm4t(at + 2048 * (ks + 1), a);
 #pragma unroll
     for (int nb = 0; nb < kNb; ++nb) mma16816(s.v[nb], hi, b[nb >> 1][2 * (nb & 1)], b[nb >> 1][2 * (nb & 1) + 1]);
 #pragma unroll
@@ -119,15 +144,13 @@ __device__ __forceinline__ void state_round(const StateAcc<kNb> &s, int nb0, voi
           tc::pack_bf16x2(s.v[nb][2 * h], s.v[nb][2 * h + 1]);
 }
 
-// Decays from behind each token to the end of the chunk (out, 64 floats of
-// this warp's own) and over the whole chunk (returned).
-__device__ __forceinline__ float gate_tails(const GateLane &x, float *out) {
+// Decays from behind each token to the end of the chunk (out) and over the
+// whole chunk (returned).
+__device__ __forceinline__ float gate_tails(const GateLane &x, PairWeights &out) {
   const float eh = __shfl_sync(0xffffffffu, x.hi[1], 31), el = __shfl_sync(0xffffffffu, x.lo[1], 31);
   const int ec = __shfl_sync(0xffffffffu, x.cuts[1], 31);
-  float t[2];
-#pragma unroll
-  for (int e = 0; e < 2; ++e) t[e] = gate_exp_fast(x.cuts[e] == ec, (eh - x.hi[e]) + (el - x.lo[e]));
-  *reinterpret_cast<float2 *>(out + 2 * (threadIdx.x & 31)) = make_float2(t[0], t[1]);
+  weights_put(out, gate_exp_fast(x.cuts[0] == ec, (eh - x.hi[0]) + (el - x.lo[0])),
+              gate_exp_fast(x.cuts[1] == ec, (eh - x.hi[1]) + (el - x.lo[1])));
   return gate_exp_fast(ec == 0, eh + el);
 }
 

@@ -79,12 +79,16 @@ __device__ __forceinline__ void clear_rows(void *tile, int rows) {
 
 struct SegSmem {
   uint8_t a[kStages][kTileBytes], b[kStages][kTileBytes];
-  float tail[4][kGC];
+  struct {
+    PairWeights tail;
+    float whole;
+  } gates[2];
   uint64_t full[kStages];
   int abort_flag;
 };
 
-// Own state of each segment but a sequence's last.  HBM-bound: K and V once.
+// Own state of each segment but a sequence's last: K and V once, the four
+// warps' decays by one of them in turn, a chunk ahead.
 __global__ void __launch_bounds__(kSegThreads)
 gated_tc_segment_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                         GatedArgs p) {
@@ -113,20 +117,30 @@ gated_tc_segment_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_co
   if (tid == 0)
     for (int c = 0; c < min(kStages, nc); ++c) load(c);
   const float *g = p.g + (size_t)bh * p.T;
-  float2 gate = gate_load(g, c0 * kGC, n);
+  auto make_gates = [&](int c, float2 gate) {
+    const float whole = gate_tails(gate_sums(gate), s.gates[c & 1].tail);
+    if ((tid & 31) == 0) s.gates[c & 1].whole = whole;
+  };
+  // warp w has the gates of its next chunk in hand: the first c > 0 with c % 4 = w, then every fourth
+  const int own = warp ? warp : 4;
+  if (warp == 0) make_gates(0, gate_load(g, c0 * kGC, n));
+  float2 gate = gate_load(g, (c0 + own) * kGC, own < nc ? n : 0);
+  __syncthreads();
   StateAcc<8> acc;
   state_load(acc, 0, nullptr);
   float decay = 1.f;
   bool ok = true;
   for (int c = 0; c < nc; ++c) {
-    const GateLane sums = gate_sums(gate);
-    if (c + 1 < nc) gate = gate_load(g, (c0 + c + 1) * kGC, n);
-    const float whole = gate_tails(sums, s.tail[warp]);
+    const float whole = s.gates[c & 1].whole;
     decay *= whole;
     state_scale(acc, whole);
-    __syncwarp();
+    if ((c + 1) % 4 == warp && c + 1 < nc) {
+      make_gates(c + 1, gate);
+      gate = gate_load(g, (c0 + c + 5) * kGC, c + 5 < nc ? n : 0);
+    }
     ok = ok && mbar_wait(&s.full[c % kStages], (c / kStages) & 1, abort_flag, p.status);
-    if (ok) state_add<0, 4>(acc, 0, s.a[c % kStages], s.b[c % kStages], s.tail[warp]);
+    ok = __all_sync(0xffffffffu, ok);
+    if (ok) state_add<0, 4>(acc, 0, s.a[c % kStages], s.b[c % kStages], s.gates[c & 1].tail);
     __syncthreads();
     if (tid == 0 && ok && c + kStages < nc) load(c + kStages);
   }
@@ -144,7 +158,8 @@ struct OutSmem {
   uint8_t q[2][2 * kTileBytes];          // two heads' queries, then their outputs
   uint8_t state[kTileBytes];             // the state before the chunk, bf16
   struct alignas(16) Gates {             // of a chunk, by the issuing warp
-    float tail[kGC], rest[kGC], row[kGC];   // e^{G_63-G_j}, e^{R-G_j}, e^{G_i-R}
+    PairWeights tail;                       // e^{G_63-G_j}
+    float rest[kGC], row[kGC];              // e^{R-G_j}, e^{G_i-R}
     float whole, first;                     // e^{G_63} (0 if cut), e^{G_31}
     uint32_t cut_even, cut_odd;             // bit l: the gate of token 2l (2l + 1) is cut
     int mode;
