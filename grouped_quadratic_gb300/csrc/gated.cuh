@@ -37,6 +37,7 @@ struct GatedArgs {
   int seg_chunks, nseg;                 // chunks of a segment, segments of T tokens
   float *seg_state, *seg_decay;         // [B Hkv][nseg][64 64], [B Hkv][nseg]
   float *seg_grad;                      // backward: the same for the state's gradient
+  uint8_t *state_tiles, *grad_tiles;    // backward (bf16): S and R of each chunk, two 8 KB tiles each
   int *status;
 };
 
@@ -170,3 +171,9 @@ __device__ __forceinline__ void gated_load8(const float *p, float (&o)[8]) {
 }
 
 }  // namespace oal
+
+#define GATED_TRY(x)             \
+  do {                           \
+    const oal_status _s = (x);   \
+    if (_s != OAL_OK) return _s; \
+  } while (0)

@@ -472,12 +472,6 @@ __global__ void __launch_bounds__(kThreads) gated_grad_kernel(GatedArgs p) {
   }
 }
 
-#define GATED_TRY(x)             \
-  do {                           \
-    const oal_status _s = (x);   \
-    if (_s != OAL_OK) return _s; \
-  } while (0)
-
 }  // namespace
 
 oal_status gated_need_smem(const void *kernel, size_t bytes, bool (&done)[kMaxDevices]) {

@@ -18,62 +18,18 @@
 // scores and S_in instead.  Other chunks form every decay exp(G_i - G_j) by
 // itself.
 #include <algorithm>
-#include <mutex>
 
-#include <cudaTypedefs.h>
-
-#include "gated_mma.cuh"
+#include "gated_tc.cuh"
 
 namespace oal {
 namespace {
-using namespace tc;
+using namespace gated;
 
 constexpr int kStages = 4;                  // chunks in flight of the segment kernel
 constexpr int kSegThreads = 128;
 constexpr int kOutThreads = 160;            // four computing warps and one that issues
 constexpr uint32_t kOutCols = 128;          // tensor memory: X (then P) 64, D 64
 constexpr uint32_t kColX = 0, kColD = 64;
-
-__device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, const void *src, int x, int y, int z) {
-  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
-                   reinterpret_cast<uint64_t>(map)),
-               "r"(smem_u32(src)), "r"(x), "r"(y), "r"(z)
-               : "memory");
-}
-__device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap *map, int x, int y, int z) {
-  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(
-                   reinterpret_cast<uint64_t>(map)),
-               "r"(x), "r"(y), "r"(z)
-               : "memory");
-}
-__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
-__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
-__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t *r) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
-               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-               : "memory");
-}
-// mbar_wait by a whole warp, whose lanes agree on the outcome (the tensor-
-// memory instructions that follow want all of them).
-__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort, int *status) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, status));
-}
-// The first 1024-byte boundary of the dynamic shared memory.  (By an offset: a
-// pointer rounded as an integer is one the compiler no longer knows to be
-// shared, and every access through it a generic one.)
-__device__ __forceinline__ uint8_t *align1024(uint8_t *p) { return p + ((1024u - (smem_u32(p) & 1023u)) & 1023u); }
-
-// What a chunk's gates ask for: nothing (R = 0, no cuts), R per half and
-// masks, or every decay by itself.
-constexpr int kPlain = 0, kHalves = 1, kEach = 2;
-constexpr float kSpan = 60.f;
-
-// Rows from `rows` on of a tile become zeros (threads 0 .. 127).
-__device__ __forceinline__ void clear_rows(void *tile, int rows) {
-  for (int x = threadIdx.x; x < 64 * 8; x += 128)
-    if ((x >> 3) >= rows) reinterpret_cast<uint4 *>(tile)[x] = make_uint4(0u, 0u, 0u, 0u);
-}
 
 // ---------------------------------------------------------------- segments
 
@@ -157,13 +113,7 @@ struct OutSmem {
   uint8_t k[2][kTileBytes], v[2][kTileBytes];
   uint8_t q[2][2 * kTileBytes];          // two heads' queries, then their outputs
   uint8_t state[kTileBytes];             // the state before the chunk, bf16
-  struct alignas(16) Gates {             // of a chunk, by the issuing warp
-    PairWeights tail;                       // e^{G_63-G_j}
-    float rest[kGC], row[kGC];              // e^{R-G_j}, e^{G_i-R}
-    float whole, first;                     // e^{G_63} (0 if cut), e^{G_31}
-    uint32_t cut_even, cut_odd;             // bit l: the gate of token 2l (2l + 1) is cut
-    int mode;
-  } gates[2];
+  ChunkGates gates[2];                   // by the issuing warp
   uint64_t kv_full[2], q_full[2], gate_full, x_full, d_full, p_full, y_full, go, meet, drain;
   uint32_t tmem;
   int abort_flag;
@@ -284,28 +234,9 @@ gated_tc_out_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
     const float *g = p.g + (size_t)bh * p.T;
     float2 gate = gate_load(g, c0 * kGC, n);
     auto make_gates = [&](int c) {
-      const GateLane sums = gate_sums(gate);
-      OutSmem::Gates &to = s.gates[c & 1];
-      const uint32_t even = __ballot_sync(0xffffffffu, gate.x <= kGateCut);
-      const uint32_t odd = __ballot_sync(0xffffffffu, gate.y <= kGateCut);
+      const float2 now = gate;
       if (c + 1 < nc) gate = gate_load(g, (c0 + c + 1) * kGC, n);
-      const float whole = gate_tails(sums, to.tail);
-      const float mh = __shfl_sync(0xffffffffu, sums.hi[1], 15), ml = __shfl_sync(0xffffffffu, sums.lo[1], 15);
-      const float span = fmaxf(fabsf(sums.hi[0]), fabsf(sums.hi[1]));
-      const bool plain = __all_sync(0xffffffffu, span <= kSpan) && (even | odd) == 0u;
-      const float rh = plain || lane < 16 ? 0.f : mh, rl = plain || lane < 16 ? 0.f : ml;
-      const float near = fmaxf(fabsf(sums.hi[0] - rh), fabsf(sums.hi[1] - rh));
-      const bool halves = __all_sync(0xffffffffu, near <= kSpan);
-      const float x0 = (sums.hi[0] - rh) + (sums.lo[0] - rl), x1 = (sums.hi[1] - rh) + (sums.lo[1] - rl);
-      reinterpret_cast<float2 *>(to.rest)[lane] = make_float2(__expf(-x0), __expf(-x1));
-      reinterpret_cast<float2 *>(to.row)[lane] = make_float2(__expf(x0), __expf(x1));
-      if (lane == 0) {
-        to.whole = whole;
-        to.first = __expf(mh + ml);
-        to.cut_even = even;
-        to.cut_odd = odd;
-        to.mode = plain ? kPlain : halves ? kHalves : kEach;
-      }
+      chunk_gates(now, gate_sums(now), s.gates[c & 1]);
       __syncwarp();
       if (lane == 0) mbar_arrive(&s.gate_full);
     };
@@ -372,7 +303,7 @@ gated_tc_out_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
     };
     for (int it = 0; it < steps && ok; ++it) {
       const int c = it / npair, pr = it % npair, t0 = (c0 + c) * kGC;
-      const OutSmem::Gates &gates = s.gates[c & 1];
+      const ChunkGates &gates = s.gates[c & 1];
       if (pr == 0) {
         ok = warp_wait(&s.gate_full, c & 1, abort_flag, p.status);
         if (!ok) break;
@@ -380,20 +311,15 @@ gated_tc_out_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
         row = mode == kEach ? p.scale : p.scale * gates.row[i];
         begin = 0;
         into = half && mode == kHalves ? gates.first : 1.f;
-        const uint32_t upto = (2u << (i >> 1)) - 1u;     // bits l with 2 l <= i
-        const uint32_t even = gates.cut_even & upto, odd = gates.cut_odd & (i & 1 ? upto : upto >> 1);
-        if (even | odd) {                                // keys from the row's last cut gate on, nothing from S_in
-          begin = max(2 * (31 - __clz(even)), 2 * (31 - __clz(odd)) + 1);
-          into = 0.f;
-        }
+        if (cut_before(gates, i, begin)) into = 0.f;     // keys from the row's last cut gate on, nothing from S_in
         ok = warp_wait(&s.kv_full[c & 1], (c >> 1) & 1, abort_flag, p.status);
       }
       ok = ok && warp_wait(&s.x_full, it & 1, abort_flag, p.status);
       if (!ok) break;
       tc_fence_after();
       if (pr == 0 && t0 + kGC > n) {                     // rows behind the sequence count as zeros
-        clear_rows(s.k[c & 1], n - t0);
-        clear_rows(s.v[c & 1], n - t0);
+        clear_rows(s.k[c & 1], n - t0, tid, 128);
+        clear_rows(s.v[c & 1], n - t0, tid, 128);
         fence_proxy_async();
         ok = meet();
         if (!ok) break;
@@ -526,41 +452,6 @@ gated_tc_out_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
     tmem_dealloc(tb, kOutCols);
   }
 }
-
-// ---------------------------------------------------------------- host side
-
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
-    void *f = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      f = nullptr;
-    return (PFN_cuTensorMapEncodeTiled_v12000)f;
-  }();
-  return fn;
-}
-
-// [heads][T][64] bf16 in boxes of 64 columns, 128-byte swizzle; rows from T on
-// read as zeros and are not written.
-oal_status make_map(CUtensorMap *m, const void *ptr, int T, long long heads, int rows = kGC) {
-  auto fn = encode_fn();
-  if (!fn) return oal_fail(OAL_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
-  const cuuint64_t dims[3] = {64, (cuuint64_t)T, (cuuint64_t)heads};
-  const cuuint64_t strides[2] = {128, (cuuint64_t)T * 128};
-  const cuuint32_t box[3] = {64, (cuuint32_t)rows, 1}, es[3] = {1, 1, 1};
-  if (fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(ptr), dims, strides, box, es,
-         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-    return oal_fail(OAL_ERR_CUDA, "cuTensorMapEncodeTiled failed");
-  return OAL_OK;
-}
-
-#define GATED_TRY(x)             \
-  do {                           \
-    const oal_status _s = (x);   \
-    if (_s != OAL_OK) return _s; \
-  } while (0)
 
 }  // namespace
 

@@ -1,0 +1,126 @@
+// gated_tc.cuh -- what the gated recurrence's tensor-core kernels share: bulk
+// stores, warp-wide waits, the modes of a chunk's gates, tensor maps.
+#pragma once
+#include <cudaTypedefs.h>
+
+#include "gated_mma.cuh"
+
+namespace oal {
+namespace gated {
+using namespace tc;
+
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, const void *src, int x, int y, int z) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(smem_u32(src)), "r"(x), "r"(y), "r"(z)
+               : "memory");
+}
+__device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap *map, int x, int y, int z) {
+  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(x), "r"(y), "r"(z)
+               : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t *r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+// mbar_wait by a whole warp, whose lanes agree on the outcome (the tensor-
+// memory instructions that follow want all of them).
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort, int *status) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, status));
+}
+// The first 1024-byte boundary of the dynamic shared memory.  (By an offset: a
+// pointer rounded as an integer is one the compiler no longer knows to be
+// shared, and every access through it a generic one.)
+__device__ __forceinline__ uint8_t *align1024(uint8_t *p) { return p + ((1024u - (smem_u32(p) & 1023u)) & 1023u); }
+
+// What a chunk's gates ask for: nothing (R = 0, no cuts), R per half and
+// masks, or every decay by itself.
+constexpr int kPlain = 0, kHalves = 1, kEach = 2;
+constexpr float kSpan = 60.f;
+
+struct alignas(16) ChunkGates {
+  PairWeights tail;                       // e^{G_63-G_j}
+  float rest[kGC], row[kGC];              // e^{R-G_j}, e^{G_i-R}
+  float whole, first;                     // e^{G_63} (0 if cut), e^{G_31}
+  uint32_t cut_even, cut_odd;             // bit l: the gate of token 2l (2l + 1) is cut
+  int mode;
+};
+// Fills them (one warp; `gate` as loaded, `sums` of it).
+__device__ __forceinline__ void chunk_gates(float2 gate, const GateLane &sums, ChunkGates &to) {
+  const int lane = threadIdx.x & 31;
+  const uint32_t even = __ballot_sync(0xffffffffu, gate.x <= kGateCut);
+  const uint32_t odd = __ballot_sync(0xffffffffu, gate.y <= kGateCut);
+  const float whole = gate_tails(sums, to.tail);
+  const float mh = __shfl_sync(0xffffffffu, sums.hi[1], 15), ml = __shfl_sync(0xffffffffu, sums.lo[1], 15);
+  const float span = fmaxf(fabsf(sums.hi[0]), fabsf(sums.hi[1]));
+  const bool plain = __all_sync(0xffffffffu, span <= kSpan) && (even | odd) == 0u;
+  const float rh = plain || lane < 16 ? 0.f : mh, rl = plain || lane < 16 ? 0.f : ml;
+  const float near = fmaxf(fabsf(sums.hi[0] - rh), fabsf(sums.hi[1] - rh));
+  const bool halves = __all_sync(0xffffffffu, near <= kSpan);
+  const float x0 = (sums.hi[0] - rh) + (sums.lo[0] - rl), x1 = (sums.hi[1] - rh) + (sums.lo[1] - rl);
+  reinterpret_cast<float2 *>(to.rest)[lane] = make_float2(__expf(-x0), __expf(-x1));
+  reinterpret_cast<float2 *>(to.row)[lane] = make_float2(__expf(x0), __expf(x1));
+  if (lane == 0) {
+    to.whole = whole;
+    to.first = __expf(mh + ml);
+    to.cut_even = even;
+    to.cut_odd = odd;
+    to.mode = plain ? kPlain : halves ? kHalves : kEach;
+  }
+}
+// Whether a gate up to token i's is cut; `begin` then becomes the last such token.
+__device__ __forceinline__ bool cut_before(const ChunkGates &gates, int i, int &begin) {
+  const uint32_t upto = (2u << (i >> 1)) - 1u;     // bits l with 2 l <= i
+  const uint32_t even = gates.cut_even & upto, odd = gates.cut_odd & (i & 1 ? upto : upto >> 1);
+  if ((even | odd) == 0u) return false;
+  begin = max(2 * (31 - __clz(even)), 2 * (31 - __clz(odd)) + 1);
+  return true;
+}
+
+// Rows from `rows` on of a tile become zeros; thread `at` of `threads`.
+__device__ __forceinline__ void clear_rows(void *tile, int rows, int at, int threads) {
+  for (int x = at; x < 64 * 8; x += threads)
+    if ((x >> 3) >= rows) reinterpret_cast<uint4 *>(tile)[x] = make_uint4(0u, 0u, 0u, 0u);
+}
+
+inline PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void *f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return (PFN_cuTensorMapEncodeTiled_v12000)f;
+  }();
+  return fn;
+}
+
+// [heads][T][64] bf16 in boxes of 64 columns, 128-byte swizzle; rows from T on
+// read as zeros and are not written.
+inline oal_status make_map(CUtensorMap *m, const void *ptr, int T, long long heads, int rows = kGC) {
+  auto fn = encode_fn();
+  if (!fn) return oal_fail(OAL_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
+  const cuuint64_t dims[3] = {64, (cuuint64_t)T, (cuuint64_t)heads};
+  const cuuint64_t strides[2] = {128, (cuuint64_t)T * 128};
+  const cuuint32_t box[3] = {64, (cuuint32_t)rows, 1}, es[3] = {1, 1, 1};
+  if (fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(ptr), dims, strides, box, es,
+         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return oal_fail(OAL_ERR_CUDA, "cuTensorMapEncodeTiled failed");
+  return OAL_OK;
+}
+
+}  // namespace gated
+
+}  // namespace oal

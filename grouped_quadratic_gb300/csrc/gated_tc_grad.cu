@@ -1,0 +1,663 @@
+// gated_tc_grad.cu -- the backward of the gated recurrence for bf16 on the
+// tensor cores.
+//
+// With f_ij = scale e^{G_i-G_j} for j <= i of a chunk, S the state before it
+// and R the gradient of the state behind it,
+//     X = Q K^T, Z = dY V^T,  p = f o X, z = f o Z  (rounded to bf16)
+//     dQ = z K + scale e^{G_i} dY S^T
+//     dK = z^T Q + e^{G_63-G_j} V R^T,   dV = p^T dY + e^{G_63-G_j} K R
+//     dg_t = sum_{j<t<=l} X_lj (f o Z)_lj + sum_{l>=t} q_l.dq_l' + sum_{j<t} k_j.dk_j' + e^{G_63} <S, R>
+// (dq', dk': the terms with S and R; they and X, Z enter dg unrounded).
+//   gated_tc_own_kernel   a chunk's own state (K, V) and own gradient of the
+//                         state before it (Q, dY of all heads), registers
+//   gated_tc_scan_kernel  S and R of every chunk from those, as two bf16 tiles
+//                         hi + lo each (off by at most 2^-16)
+//   gated_tc_grad_kernel  the gradients, chunks in any order: a pair of query
+//                         heads is 128 rows; two blocks per SM.
+// Tensor memory of a block: X, then dY S^T | Z, then z K | 128 columns of
+// [p | z]^T [dY | Q], of which the upper left quarter is dV and the lower
+// right one dK, on top of K R and V R^T.
+#include <algorithm>
+
+#include "gated_tc.cuh"
+
+namespace oal {
+namespace {
+using namespace gated;
+
+// ---------------------------------------------------------------- own states
+
+constexpr int kOwnThreads = 128, kOwnStages = 2;
+struct OwnSmem {
+  uint8_t a[kOwnStages][kTileBytes], b[kOwnStages][kTileBytes];
+  PairWeights w;
+  uint64_t full[kOwnStages];
+  int abort_flag;
+};
+
+// blockIdx.y = 0: sum_j e^{G_63-G_j} k_j v_j^T of the chunk, and its decay;
+// 1: scale sum_i e^{G_i} q_i dy_i^T over the query heads of the KV head.
+__global__ void __launch_bounds__(kOwnThreads)
+gated_tc_own_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                    const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO, GatedArgs p) {
+  pdl_trigger();
+  extern __shared__ uint8_t smem_raw[];
+  OwnSmem &s = *reinterpret_cast<OwnSmem *>(align1024(smem_raw));
+  const int bh = blockIdx.x / p.nseg, c = blockIdx.x % p.nseg, b = bh / p.Hkv, kv = bh % p.Hkv;
+  const int tid = threadIdx.x, rho = p.Hq / p.Hkv, t0 = c * kGC;
+  const bool grad = blockIdx.y != 0;
+  if (tid == 0) {
+    s.abort_flag = 0;
+    for (int i = 0; i < kOwnStages; ++i) mbar_init(&s.full[i], 1);
+    fence_mbar_init();
+  }
+  pdl_wait();
+  const int n = gated_len(p, b);
+  if (t0 >= n) return;
+  __syncthreads();
+  volatile int *abort_flag = &s.abort_flag;
+  const int count = grad ? rho : 1;
+  auto load = [&](int r) {
+    const int st = r % kOwnStages;
+    mbar_arrive_expect_tx(&s.full[st], 2 * kTileBytes);
+    tma_load_3d(s.a[st], grad ? &tmQ : &tmK, &s.full[st], 0, t0, grad ? b * p.Hq + kv * rho + r : bh);
+    tma_load_3d(s.b[st], grad ? &tmO : &tmV, &s.full[st], 0, t0, grad ? b * p.Hq + kv * rho + r : bh);
+  };
+  if (tid == 0)
+    for (int r = 0; r < min(kOwnStages, count); ++r) load(r);
+  if (tid < 32) {
+    const GateLane sums = gate_sums(gate_load(p.g + (size_t)bh * p.T, t0, n));
+    if (!grad) {
+      const float whole = gate_tails(sums, s.w);
+      if (tid == 0) p.seg_decay[(size_t)bh * p.nseg + c] = whole;
+    } else {
+      weights_put(s.w, p.scale * gate_exp_fast(sums.cuts[0] == 0, sums.hi[0] + sums.lo[0]),
+                  p.scale * gate_exp_fast(sums.cuts[1] == 0, sums.hi[1] + sums.lo[1]));
+    }
+  }
+  __syncthreads();
+  StateAcc<8> acc;
+  state_load(acc, 0, nullptr);
+  bool ok = true;
+  for (int r = 0; r < count; ++r) {
+    const int st = r % kOwnStages;
+    ok = ok && mbar_wait(&s.full[st], (r / kOwnStages) & 1, abort_flag, p.status);
+    ok = __all_sync(0xffffffffu, ok);
+    if (t0 + kGC > n && n < p.T) {   // rows behind the sequence count as zeros
+      clear_rows(s.a[st], n - t0, tid, kOwnThreads);
+      clear_rows(s.b[st], n - t0, tid, kOwnThreads);
+      fence_proxy_async();
+      __syncthreads();
+    }
+    if (ok) state_add<0, 4>(acc, 0, s.a[st], s.b[st], s.w);
+    __syncthreads();
+    if (tid == 0 && ok && r + kOwnStages < count) load(r + kOwnStages);
+  }
+  if (tid == 0 && !ok)   // copies still in flight land before the block ends
+    for (int i = 0; i < min(kOwnStages, count); ++i)
+      for (int ph = 0; ph < 2; ++ph) mbar_wait_teardown(&s.full[i], ph, p.status);
+  state_store(acc, 0, (grad ? p.seg_grad : p.seg_state) + ((size_t)bh * p.nseg + c) * kGS);
+}
+
+// ---------------------------------------------------------------- scan
+
+constexpr int kScanThreads = 256, kAhead = 8;
+
+// The thread's four values of a state as hi and lo words of the two tiles.
+__device__ __forceinline__ void put_tiles(uint8_t *tiles, int x, float4 v) {
+  uint8_t *at = tiles + tile_at(x >> 4, (x & 15) >> 1) + 8 * (x & 1);
+  const uint32_t h0 = pack_bf16x2(v.x, v.y), h1 = pack_bf16x2(v.z, v.w);
+  *reinterpret_cast<uint2 *>(at) = make_uint2(h0, h1);
+  *reinterpret_cast<uint2 *>(at + kTileBytes) =
+      make_uint2(pack_bf16x2(v.x - __uint_as_float(h0 << 16), v.y - __uint_as_float(h0 & 0xFFFF0000u)),
+                 pack_bf16x2(v.z - __uint_as_float(h1 << 16), v.w - __uint_as_float(h1 & 0xFFFF0000u)));
+}
+
+// z = 0: the state before each chunk, forwards; 1: the gradient of the state
+// behind each, backwards, and dstate0.
+__global__ void __launch_bounds__(kScanThreads) gated_tc_scan_kernel(GatedArgs p) {
+  pdl_trigger();
+  pdl_wait();
+  const int bh = blockIdx.x, x = blockIdx.y * kScanThreads + threadIdx.x;
+  const bool grad = blockIdx.z != 0;
+  const int n = gated_len(p, bh / p.Hkv), count = (n + kGC - 1) / kGC;
+  const float *decay = p.seg_decay + (size_t)bh * p.nseg;
+  const float4 *own = reinterpret_cast<const float4 *>((grad ? p.seg_grad : p.seg_state) + (size_t)bh * p.nseg * kGS) + x;
+  uint8_t *tiles = (grad ? p.grad_tiles : p.state_tiles) + (size_t)bh * p.nseg * 2 * kTileBytes;
+  const float *from = grad ? p.dstate : p.state_in;
+  float4 run = from ? reinterpret_cast<const float4 *>(from + (size_t)bh * kGS)[x] : make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i0 = 0; i0 < count; i0 += kAhead) {
+    float4 v[kAhead];
+    float f[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int i = grad ? count - 1 - i0 - k : i0 + k;
+      const bool on = i0 + k < count;
+      v[k] = on ? __ldg(own + (size_t)i * (kGS / 4)) : make_float4(0.f, 0.f, 0.f, 0.f);
+      f[k] = on ? __ldg(decay + i) : 0.f;
+    }
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int i = grad ? count - 1 - i0 - k : i0 + k;
+      if (i0 + k < count) {
+        put_tiles(tiles + (size_t)i * 2 * kTileBytes, x, run);
+        run.x = fmaf(f[k], run.x, v[k].x), run.y = fmaf(f[k], run.y, v[k].y);
+        run.z = fmaf(f[k], run.z, v[k].z), run.w = fmaf(f[k], run.w, v[k].w);
+      }
+    }
+  }
+  if (grad && p.dstate0) reinterpret_cast<float4 *>(p.dstate0 + (size_t)bh * kGS)[x] = run;
+}
+
+// ---------------------------------------------------------------- gradients
+
+constexpr int kGradThreads = 288;              // eight computing warps and one that issues
+constexpr uint32_t kGradCols = 256;
+struct GradSmem {
+  uint8_t kv[2 * kTileBytes];                  // K, V; at the end dV, dK
+  uint8_t oq[4 * kTileBytes];                  // dY of two heads, Q of two heads
+  uint8_t pz[4 * kTileBytes];                  // R hi, R lo; then p (later dQ) and z, 128 rows each
+  uint8_t st[2 * kTileBytes];                  // S hi, lo
+  ChunkGates gates;
+  float tail[kGC], head[kGC];                  // e^{G_63-G_j}, e^{G_i}
+  float rows[2][2 * kGC], cols[4][kGC], far[2][kGC], dots[8];   // parts of dg
+  uint64_t kv_full, gate_full, far_full, q_full, clean, go, xz_full, pz_full, dq_full, pair[4], meet, chunk_done, drain;
+  uint32_t tmem;
+  int abort_flag;
+};
+static_assert(2 * (sizeof(GradSmem) + 2 * 1024) <= 228 * 1024, "two blocks per SM");
+
+__global__ void __launch_bounds__(kGradThreads, 2)
+gated_tc_grad_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
+                     const __grid_constant__ CUtensorMap tmDQ, const __grid_constant__ CUtensorMap tmDK,
+                     const __grid_constant__ CUtensorMap tmDV, GatedArgs p) {
+  pdl_trigger();
+  extern __shared__ uint8_t smem_raw[];
+  GradSmem &s = *reinterpret_cast<GradSmem *>(align1024(smem_raw));
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rho = p.Hq / p.Hkv, npair = (rho + 1) / 2;
+  if (tid == 0) {
+    s.abort_flag = 0;
+    mbar_init(&s.kv_full, 1), mbar_init(&s.gate_full, 1), mbar_init(&s.far_full, 1), mbar_init(&s.q_full, 1);
+    mbar_init(&s.clean, 8), mbar_init(&s.go, 8), mbar_init(&s.xz_full, 1), mbar_init(&s.pz_full, 8);
+    mbar_init(&s.dq_full, 1), mbar_init(&s.meet, 8), mbar_init(&s.chunk_done, 8), mbar_init(&s.drain, 1);
+    for (int i = 0; i < 4; ++i) mbar_init(&s.pair[i], 2);
+    fence_mbar_init();
+  }
+  if (warp == 8) {
+    tmem_alloc(&s.tmem, kGradCols);
+    tmem_relinquish();
+  }
+  pdl_wait();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tb = s.tmem, tx = tb, tz = tb + 64, tkv = tb + 128;
+  volatile int *abort_flag = &s.abort_flag;
+  auto wait = [&](uint64_t *bar, int phase) { return warp_wait(bar, phase & 1, abort_flag, p.status); };
+  auto arrive = [&](uint64_t *bar) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
+  };
+  const int total = p.nseg * p.B * p.Hkv;
+  bool ok = true;
+  // Both sides count alike: k chunks begun, it steps (a chunk's pairs of
+  // heads), cl cleanings.  Every barrier completes once per what it counts and
+  // all who wait on it wait every time, so none is ever two phases ahead.
+  int k = 0, it = 0, cl = 0;
+  // Tiles of heads that do not exist, or rows behind a sequence, are cleared
+  // before the tensor cores read them (they are summed over).
+  auto cleans = [&](int pr, bool tail) { return tail || (rho - 2 * pr == 1 && (rho > 1 || it == 0)); };
+
+  if (warp == 8) {
+    const uint32_t id_k = idesc_bf16_f32(128, 64, 0), id_mn = idesc_bf16_f32(128, 64, 1);
+    const uint32_t id_kv = idesc_bf16_f32(128, 128, 1) | (1u << 15);   // A with rows along its minor axis too
+    const uint64_t od = sdesc_sw128(smem_u32(s.oq), 16, 1024), qd = sdesc_sw128(smem_u32(s.oq) + 2 * kTileBytes, 16, 1024);
+    const uint64_t kd = sdesc_sw128(smem_u32(s.kv), 16, 1024), vd = sdesc_sw128(smem_u32(s.kv) + kTileBytes, 16, 1024);
+    const uint64_t sh = sdesc_sw128(smem_u32(s.st), 16, 1024), sl = sdesc_sw128(smem_u32(s.st) + kTileBytes, 16, 1024);
+    const uint64_t rh = sdesc_sw128(smem_u32(s.pz), 16, 1024), rl = sdesc_sw128(smem_u32(s.pz) + kTileBytes, 16, 1024);
+    const uint64_t zd = sdesc_sw128(smem_u32(s.pz) + 2 * kTileBytes, 16, 1024);
+    // [p | z] and [dY | Q]: two 64-column atoms, 16 KB apart
+    const uint64_t pzd = sdesc_sw128(smem_u32(s.pz), 2 * kTileBytes, 1024);
+    const uint64_t oqd = sdesc_sw128(smem_u32(s.oq), 2 * kTileBytes, 1024);
+    int loads = 0;
+    for (int idx = blockIdx.x; idx < total && ok; idx += gridDim.x) {
+      const int bh = idx / p.nseg, c = idx % p.nseg, b = bh / p.Hkv, kv = bh % p.Hkv, t0 = c * kGC;
+      const int n = gated_len(p, b), h0 = b * p.Hq + kv * rho;
+      if (t0 >= n) continue;
+      const bool tail = t0 + kGC > n && n < p.T;
+      const float2 gate = gate_load(p.g + (size_t)bh * p.T, t0, n);
+      auto load_q = [&](int pr) {
+        const int heads = min(2, rho - 2 * pr);
+        mbar_arrive_expect_tx(&s.q_full, 2 * heads * kTileBytes);
+        for (int h = 0; h < heads; ++h) {
+          tma_load_3d(s.oq + h * kTileBytes, &tmO, &s.q_full, 0, t0, h0 + 2 * pr + h);
+          tma_load_3d(s.oq + (2 + h) * kTileBytes, &tmQ, &s.q_full, 0, t0, h0 + 2 * pr + h);
+        }
+      };
+      if (k > 0) ok = wait(&s.chunk_done, k - 1);
+      if (!ok) break;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&s.kv_full, 6 * kTileBytes);
+        tma_load_3d(s.kv, &tmK, &s.kv_full, 0, t0, bh);
+        tma_load_3d(s.kv + kTileBytes, &tmV, &s.kv_full, 0, t0, bh);
+        bulk_load(s.st, p.state_tiles + (size_t)idx * 2 * kTileBytes, 2 * kTileBytes, &s.kv_full);
+        bulk_load(s.pz, p.grad_tiles + (size_t)idx * 2 * kTileBytes, 2 * kTileBytes, &s.kv_full);
+        load_q(0), ++loads;
+        for (int h = 2; h < min(4, rho); ++h) {
+          tma_prefetch_3d(&tmO, 0, t0, h0 + h);
+          tma_prefetch_3d(&tmQ, 0, t0, h0 + h);
+        }
+        const int next = idx + gridDim.x;
+        if (next < total) {
+          const int nbh = next / p.nseg, nt = (next % p.nseg) * kGC, nh = (nbh / p.Hkv) * p.Hq + (nbh % p.Hkv) * rho;
+          tma_prefetch_3d(&tmK, 0, nt, nbh);
+          tma_prefetch_3d(&tmV, 0, nt, nbh);
+          prefetch_l2(p.state_tiles + (size_t)next * 2 * kTileBytes, 2 * kTileBytes);
+          prefetch_l2(p.grad_tiles + (size_t)next * 2 * kTileBytes, 2 * kTileBytes);
+          for (int h = 0; h < min(2, rho); ++h) {
+            tma_prefetch_3d(&tmO, 0, nt, nh + h);
+            tma_prefetch_3d(&tmQ, 0, nt, nh + h);
+          }
+        }
+      }
+      __syncwarp();
+      {
+        const GateLane sums = gate_sums(gate);
+        chunk_gates(gate, sums, s.gates);
+        const float eh = __shfl_sync(0xffffffffu, sums.hi[1], 31), el = __shfl_sync(0xffffffffu, sums.lo[1], 31);
+        const int ec = __shfl_sync(0xffffffffu, sums.cuts[1], 31);
+        float2 tl, hd;
+        tl.x = gate_exp_fast(sums.cuts[0] == ec, (eh - sums.hi[0]) + (el - sums.lo[0]));
+        tl.y = gate_exp_fast(sums.cuts[1] == ec, (eh - sums.hi[1]) + (el - sums.lo[1]));
+        hd.x = gate_exp_fast(sums.cuts[0] == 0, sums.hi[0] + sums.lo[0]);
+        hd.y = gate_exp_fast(sums.cuts[1] == 0, sums.hi[1] + sums.lo[1]);
+        reinterpret_cast<float2 *>(s.tail)[lane] = tl;
+        reinterpret_cast<float2 *>(s.head)[lane] = hd;
+      }
+      arrive(&s.gate_full);
+      ok = wait(&s.kv_full, k);
+      if (ok && tail) ok = wait(&s.clean, cl++);
+      if (!ok) break;
+      tc_fence_after();
+      // [K; V] R and [K; V] R^T side by side: K R above on the left, V R^T below on the right
+#pragma unroll
+      for (int j = 0; j < 4; ++j) umma_ss_warp(tkv, kd + 2 * j, rh + 128 * j, id_mn, j > 0);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) umma_ss_warp(tkv, kd + 2 * j, rl + 128 * j, id_mn, 1u);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) umma_ss_warp(tkv + 64, kd + 2 * j, rh + 2 * j, id_k, j > 0);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) umma_ss_warp(tkv + 64, kd + 2 * j, rl + 2 * j, id_k, 1u);
+      umma_commit_warp(&s.far_full);
+      ++k;
+      for (int pr = 0; pr < npair && ok; ++pr) {
+        ok = wait(&s.q_full, it);
+        if (ok && cleans(pr, tail)) ok = wait(&s.clean, cl++);
+        ok = ok && wait(&s.go, it);       // X and Z are free
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int j = 0; j < 4; ++j) umma_ss_warp(tx, qd + 2 * j, kd + 2 * j, id_k, j > 0);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) umma_ss_warp(tz, od + 2 * j, vd + 2 * j, id_k, j > 0);
+        umma_commit_warp(&s.xz_full);
+        ok = wait(&s.pz_full, it);        // p and z are there, X and Z are read
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int j = 0; j < 4; ++j) umma_ss_warp(tx, od + 2 * j, sh + 2 * j, id_k, j > 0);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) umma_ss_warp(tx, od + 2 * j, sl + 2 * j, id_k, 1u);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) umma_ss_warp(tz, zd + 2 * j, kd + 128 * j, id_mn, j > 0);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) umma_ss_warp(tkv, pzd + 128 * j, oqd + 128 * j, id_kv, 1u);
+        umma_commit_warp(&s.dq_full);
+        ok = wait(&s.dq_full, it);
+        ++it;
+        if (ok && pr + 1 < npair) {
+          if (lane == 0) {
+            load_q(pr + 1), ++loads;
+            for (int h = 2 * pr + 4; h < min(2 * pr + 6, rho); ++h) {
+              tma_prefetch_3d(&tmO, 0, t0, h0 + h);
+              tma_prefetch_3d(&tmQ, 0, t0, h0 + h);
+            }
+          }
+          __syncwarp();
+        }
+      }
+    }
+    umma_commit_warp(&s.drain);
+    if (lane == 0) {   // nothing in flight at the block's end
+      mbar_wait_teardown(&s.drain, 0, p.status);
+      if (!ok) {       // (the last loads may not have been waited for)
+        mbar_wait_teardown(&s.kv_full, k & 1, p.status);
+        mbar_wait_teardown(&s.kv_full, (k + 1) & 1, p.status);
+        if (loads > 0) mbar_wait_teardown(&s.q_full, (loads - 1) & 1, p.status);
+      }
+    }
+    __syncwarp();
+  } else {
+    const int quad = warp & 3, hf = warp >> 2;                 // lanes of tensor memory; keys (dims) 32 hf .. + 31
+    const int m = 32 * quad + lane, i = m & 63;                // row: head m / 64 of the pair, token i
+    const bool own = hf == (quad & 1), pre = !hf && (quad & 1);   // keys of the row's half of the chunk; of the half before
+    const uint32_t lanes = (uint32_t)(32 * quad) << 16;
+    int met = 0, paired = 0;
+    arrive(&s.go);
+    for (int idx = blockIdx.x; idx < total && ok; idx += gridDim.x) {
+      const int bh = idx / p.nseg, c = idx % p.nseg, b = bh / p.Hkv, kv = bh % p.Hkv, t0 = c * kGC;
+      const int n = gated_len(p, b), h0 = b * p.Hq + kv * rho;
+      if (t0 >= n) continue;
+      const bool tail = t0 + kGC > n && n < p.T;
+      ok = wait(&s.gate_full, k) && wait(&s.kv_full, k);
+      if (!ok) break;
+      if (tail) {
+        clear_rows(s.kv, n - t0, tid, 256);
+        clear_rows(s.kv + kTileBytes, n - t0, tid, 256);
+        fence_proxy_async();
+        arrive(&s.clean);
+        ++cl;
+      }
+      float cfar = 0.f;
+      {
+        // <S, R>: all four tiles hold an element at the same place
+        const uint32_t *a = reinterpret_cast<const uint32_t *>(s.st), *r = reinterpret_cast<const uint32_t *>(s.pz);
+        float dot = 0.f;
+#pragma unroll
+        for (int z = 0; z < 8; ++z) {
+          const int x = tid + 256 * z;
+          const uint32_t ah = a[x], al = a[x + kTileBytes / 4], gh = r[x], gl = r[x + kTileBytes / 4];
+          dot = fmaf(__uint_as_float(ah << 16) + __uint_as_float(al << 16),
+                     __uint_as_float(gh << 16) + __uint_as_float(gl << 16), dot);
+          dot = fmaf(__uint_as_float(ah & 0xFFFF0000u) + __uint_as_float(al & 0xFFFF0000u),
+                     __uint_as_float(gh & 0xFFFF0000u) + __uint_as_float(gl & 0xFFFF0000u), dot);
+        }
+#pragma unroll
+        for (int d = 16; d; d >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, d);
+        if (lane == 0) s.dots[warp] = dot;
+        // K R (rows 0 .. 63) and V R^T (64 .. 127) times the keys' decays to the chunk's end
+        ok = wait(&s.far_full, k);
+        if (!ok) break;
+        tc_fence_after();
+        const float tj = s.tail[i];
+        const uint32_t from = tkv + (quad & 2 ? 64u : 0u) + 32u * hf + lanes;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t x[16];
+          tmem_ld16(from + 16 * h, x);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 16; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * tj);
+          if (quad & 2) {
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {
+              const uint4 kk = *reinterpret_cast<const uint4 *>(s.kv + tile_at(i, 4 * hf + 2 * h + z));
+              const uint32_t u[4] = {kk.x, kk.y, kk.z, kk.w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                cfar = fmaf(__uint_as_float(u[e] << 16), __uint_as_float(x[8 * z + 2 * e]), cfar);
+                cfar = fmaf(__uint_as_float(u[e] & 0xFFFF0000u), __uint_as_float(x[8 * z + 2 * e + 1]), cfar);
+              }
+            }
+          }
+          tmem_st16(from + 16 * h, x);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+      }
+      arrive(&s.meet);
+      ok = wait(&s.meet, met++);                               // R is read by all: p takes its place
+      if (!ok) break;
+      ++k;
+      const int mode = s.gates.mode;
+      const float fq = p.scale * s.head[i];
+      const float fr = p.scale * s.gates.row[i] * (pre && mode == kHalves ? s.gates.first : 1.f);
+      int begin = 0;
+      cut_before(s.gates, i, begin);
+      const uint32_t live = 0xFFFFFFFFu << min(31, max(0, begin - 32 * hf));
+      const uint32_t mask = own ? live & (0xFFFFFFFFu >> (31 - lane)) : pre && begin < 32 ? live : 0u;
+      const uint32_t strict = own ? mask & ~(1u << lane) : mask;
+      GateLane es;
+      if (mode == kEach) es = gate_sums(gate_load(p.g + (size_t)bh * p.T, t0, n));
+      float w[32], racc = 0.f;
+#pragma unroll
+      for (int e = 0; e < 32; ++e) w[e] = 0.f;
+      for (int pr = 0; pr < npair; ++pr) {
+        const bool single = rho - 2 * pr == 1;
+        ok = wait(&s.q_full, it);
+        if (!ok) break;
+        if (cleans(pr, tail)) {
+          const int keep = tail ? n - t0 : 64, keep1 = single ? 0 : keep;
+          clear_rows(s.oq, keep, tid, 256);
+          clear_rows(s.oq + kTileBytes, keep1, tid, 256);
+          clear_rows(s.oq + 2 * kTileBytes, keep, tid, 256);
+          clear_rows(s.oq + 3 * kTileBytes, keep1, tid, 256);
+          fence_proxy_async();
+          arrive(&s.clean);
+          ++cl;
+        }
+        ok = wait(&s.xz_full, it);
+        if (!ok) break;
+        tc_fence_after();
+        if (own || pre) {
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {
+            uint32_t x[8], y[8];
+            tmem_ld8(tx + lanes + 32 * hf + 8 * h, x);
+            tmem_ld8(tz + lanes + 32 * hf + 8 * h, y);
+            float f[8];
+            if (mode != kEach) {
+#pragma unroll
+              for (int e = 0; e < 8; e += 4) {
+                const float4 r = *reinterpret_cast<const float4 *>(s.gates.rest + 32 * hf + 8 * h + e);
+                f[e] = fr * r.x, f[e + 1] = fr * r.y, f[e + 2] = fr * r.z, f[e + 3] = fr * r.w;
+              }
+            } else {
+              const float ih = __shfl_sync(0xffffffffu, es.hi[0], i >> 1), ih1 = __shfl_sync(0xffffffffu, es.hi[1], i >> 1);
+              const float il = __shfl_sync(0xffffffffu, es.lo[0], i >> 1), il1 = __shfl_sync(0xffffffffu, es.lo[1], i >> 1);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const int from = 16 * hf + 4 * h + (e >> 1);
+                const float hj = __shfl_sync(0xffffffffu, es.hi[e & 1], from), lj = __shfl_sync(0xffffffffu, es.lo[e & 1], from);
+                f[e] = p.scale * gate_exp_fast(mask & (1u << (8 * h + e)), ((i & 1 ? ih1 : ih) - hj) + ((i & 1 ? il1 : il) - lj));
+              }
+            }
+            tmem_wait_ld();
+            uint32_t pw[4], zw[4];
+#pragma unroll
+            for (int e = 0; e < 8; e += 2) {
+              float pv[2], zv[2];
+#pragma unroll
+              for (int d = 0; d < 2; ++d) {
+                const int j = 8 * h + e + d;
+                const float xv = __uint_as_float(x[e + d]);
+                zv[d] = mask & (1u << j) ? f[e + d] * __uint_as_float(y[e + d]) : 0.f;
+                pv[d] = mask & (1u << j) ? f[e + d] * xv : 0.f;
+                w[j] = fmaf(strict & (1u << j) ? xv : 0.f, zv[d], w[j]);
+              }
+              pw[e >> 1] = pack_bf16x2(pv[0], pv[1]);
+              zw[e >> 1] = pack_bf16x2(zv[0], zv[1]);
+            }
+            *reinterpret_cast<uint4 *>(s.pz + tile_at(m, 4 * hf + h)) = make_uint4(pw[0], pw[1], pw[2], pw[3]);
+            *reinterpret_cast<uint4 *>(s.pz + 2 * kTileBytes + tile_at(m, 4 * hf + h)) = make_uint4(zw[0], zw[1], zw[2], zw[3]);
+          }
+        } else {                                               // later keys: nothing
+#pragma unroll
+          for (int z = 0; z < 4; ++z) {
+            *reinterpret_cast<uint4 *>(s.pz + tile_at(m, 4 * hf + z)) = make_uint4(0u, 0u, 0u, 0u);
+            *reinterpret_cast<uint4 *>(s.pz + 2 * kTileBytes + tile_at(m, 4 * hf + z)) = make_uint4(0u, 0u, 0u, 0u);
+          }
+        }
+        uint4 q[4];                                            // the row's queries, before their buffer is refilled
+#pragma unroll
+        for (int z = 0; z < 4; ++z) q[z] = *reinterpret_cast<const uint4 *>(s.oq + 2 * kTileBytes + tile_at(m, 4 * hf + z));
+        fence_proxy_async();
+        tc_fence_before();
+        arrive(&s.pz_full);
+        ok = wait(&s.dq_full, it);
+        if (!ok) break;
+        tc_fence_after();
+        ++it;
+        const int hd = 2 * pr + (m >> 6);
+        uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.dQ) + ((size_t)(h0 + hd) * p.T + t0 + i) * 64) + 4 * hf;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t x[16], y[16];
+          tmem_ld16(tx + lanes + 32 * hf + 16 * h, x);
+          tmem_ld16(tz + lanes + 32 * hf + 16 * h, y);
+          tmem_wait_ld();
+#pragma unroll
+          for (int z = 0; z < 2; ++z) {
+            const uint4 qq = q[2 * h + z];
+            const uint32_t u[4] = {qq.x, qq.y, qq.z, qq.w};
+            uint32_t o[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float a = fq * __uint_as_float(x[8 * z + 2 * e]), d = fq * __uint_as_float(x[8 * z + 2 * e + 1]);
+              racc = fmaf(__uint_as_float(u[e] << 16), a, racc);
+              racc = fmaf(__uint_as_float(u[e] & 0xFFFF0000u), d, racc);
+              o[e] = pack_bf16x2(a + __uint_as_float(y[8 * z + 2 * e]), d + __uint_as_float(y[8 * z + 2 * e + 1]));
+            }
+            const uint4 out = make_uint4(o[0], o[1], o[2], o[3]);
+            if (!tail) *reinterpret_cast<uint4 *>(s.pz + tile_at(m, 4 * hf + 2 * h + z)) = out;   // p has been read
+            else if (hd < rho && t0 + i < n) dst[2 * h + z] = out;
+          }
+        }
+        fence_proxy_async();
+        tc_fence_before();
+        arrive(&s.pair[quad]);
+        if (hf == 0) {                                         // both halves of these 32 rows are there
+          ok = wait(&s.pair[quad], paired);
+          if (!ok) break;
+          if (lane == 0) {
+            const int row = 32 * (quad & 1);
+            if (!tail && hd < rho && t0 + row < n) tma_store_3d(&tmDQ, s.pz + 32 * quad * 128, 0, t0 + row, h0 + hd);
+            bulk_commit();
+            bulk_wait_read();
+          }
+        }
+        ++paired;
+        arrive(&s.go);
+      }
+      if (!ok) break;
+      // dV from rows 0 .. 63, dK from rows 64 .. 127; the sums for dg
+      {
+        const uint32_t from = tkv + (quad & 2 ? 64u : 0u) + 32u * hf + lanes;
+        uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(quad & 2 ? p.dK : p.dV) + ((size_t)bh * p.T + t0 + i) * 64) + 4 * hf;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t x[16];
+          tmem_ld16(from + 16 * h, x);
+          tmem_wait_ld();
+#pragma unroll
+          for (int z = 0; z < 2; ++z) {
+            uint32_t o[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              o[e] = pack_bf16x2(__uint_as_float(x[8 * z + 2 * e]), __uint_as_float(x[8 * z + 2 * e + 1]));
+            const uint4 out = make_uint4(o[0], o[1], o[2], o[3]);
+            if (!tail) *reinterpret_cast<uint4 *>(s.kv + tile_at(m, 4 * hf + 2 * h + z)) = out;
+            else if (t0 + i < n) dst[2 * h + z] = out;
+          }
+        }
+        fence_proxy_async();
+        tc_fence_before();
+        arrive(&s.pair[quad]);
+        if (hf == 0) {
+          ok = wait(&s.pair[quad], paired);
+          if (!ok) break;
+          if (lane == 0) {
+            const int row = 32 * (quad & 1);
+            if (!tail && t0 + row < n) tma_store_3d(quad & 2 ? &tmDK : &tmDV, s.kv + 32 * quad * 128, 0, t0 + row, bh);
+            bulk_commit();
+          }
+        }
+        ++paired;
+        float sum = racc;
+#pragma unroll
+        for (int e = 0; e < 32; ++e) sum += w[e];
+        s.rows[hf][m] = sum;
+        // lane l ends with the sum over the warp's rows of column l
+#pragma unroll
+        for (int d = 16; d; d >>= 1)
+#pragma unroll
+          for (int e = 0; e < d; ++e) {
+            const float keep = lane & d ? w[e + d] : w[e], give = lane & d ? w[e] : w[e + d];
+            w[e] = keep + __shfl_xor_sync(0xffffffffu, give, d);
+          }
+        s.cols[quad][32 * hf + lane] = w[0];
+        if (quad & 2) s.far[hf][i] = cfar;
+      }
+      arrive(&s.meet);
+      ok = wait(&s.meet, met++);
+      if (!ok) break;
+      if (warp == 7) {
+        float x = 0.f, r[2], f[2];
+#pragma unroll
+        for (int z = 0; z < 8; ++z) x += s.dots[z];
+        x *= s.gates.whole;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int t = 2 * lane + e;
+          r[e] = (s.rows[0][t] + s.rows[1][t]) + (s.rows[0][64 + t] + s.rows[1][64 + t]) -
+                 ((s.cols[0][t] + s.cols[1][t]) + (s.cols[2][t] + s.cols[3][t]));
+          f[e] = s.far[0][t] + s.far[1][t];
+        }
+        float down = r[0] + r[1], up = f[0] + f[1];            // sums from this lane on; up to it
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const float a = __shfl_down_sync(0xffffffffu, down, d), u = __shfl_up_sync(0xffffffffu, up, d);
+          if (lane + d < 32) down += a;
+          if (lane >= d) up += u;
+        }
+        up = __shfl_up_sync(0xffffffffu, up, 1);
+        if (lane == 0) up = 0.f;
+        float after = __shfl_down_sync(0xffffffffu, down, 1);
+        if (lane == 31) after = 0.f;
+        float *dg = p.dg + (size_t)bh * p.T + t0 + 2 * lane;
+        const float d0 = x + (after + r[1] + r[0]) + up, d1 = x + (after + r[1]) + (up + f[0]);
+        if (t0 + 2 * lane < n) dg[0] = s.gates.cut_even >> lane & 1u ? 0.f : d0;
+        if (t0 + 2 * lane + 1 < n) dg[1] = s.gates.cut_odd >> lane & 1u ? 0.f : d1;
+      }
+      if (hf == 0 && lane == 0) bulk_wait_read();
+      arrive(&s.chunk_done);
+    }
+    if (lane == 0) bulk_wait_all();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 8) {
+    tc_fence_after();
+    tmem_dealloc(tb, kGradCols);
+  }
+}
+
+}  // namespace
+
+oal_status launch_gated_backward_tc(const GatedArgs &p, cudaStream_t stream) {
+  static bool done_own[kMaxDevices], done_grad[kMaxDevices];
+  const size_t own_smem = sizeof(OwnSmem) + 1024, grad_smem = sizeof(GradSmem) + 1024;
+  GATED_TRY(gated_need_smem(reinterpret_cast<const void *>(gated_tc_own_kernel), own_smem, done_own));
+  GATED_TRY(gated_need_smem(reinterpret_cast<const void *>(gated_tc_grad_kernel), grad_smem, done_grad));
+  const long long hq = (long long)p.B * p.Hq, hkv = (long long)p.B * p.Hkv;
+  CUtensorMap tmQ, tmK, tmV, tmO, tmDQ, tmDK, tmDV;
+  GATED_TRY(make_map(&tmQ, p.Q, p.T, hq));
+  GATED_TRY(make_map(&tmK, p.K, p.T, hkv));
+  GATED_TRY(make_map(&tmV, p.V, p.T, hkv));
+  GATED_TRY(make_map(&tmO, p.dY, p.T, hq));
+  GATED_TRY(make_map(&tmDQ, p.dQ, p.T, hq, 32));
+  GATED_TRY(make_map(&tmDK, p.dK, p.T, hkv, 32));
+  GATED_TRY(make_map(&tmDV, p.dV, p.T, hkv, 32));
+  const int total = p.nseg * p.B * p.Hkv;
+  launch_pdl(gated_tc_own_kernel, dim3(total, 2), dim3(kOwnThreads), own_smem, stream, tmQ, tmK, tmV, tmO, p);
+  GATED_TRY(oal_after_launch("gated_tc_own_kernel", stream));
+  launch_pdl(gated_tc_scan_kernel, dim3(p.B * p.Hkv, kGS / 4 / kScanThreads, 2), dim3(kScanThreads), 0, stream, p);
+  GATED_TRY(oal_after_launch("gated_tc_scan_kernel", stream));
+  launch_pdl(gated_tc_grad_kernel, dim3(std::min(total, 2 * 152)), dim3(kGradThreads), grad_smem, stream, tmQ, tmK, tmV,
+             tmO, tmDQ, tmDK, tmDV, p);
+  return oal_after_launch("gated_tc_grad_kernel", stream);
+}
+
+}  // namespace oal

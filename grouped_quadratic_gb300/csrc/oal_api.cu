@@ -49,6 +49,7 @@ oal_status group_dims_host(const float *chi_p, int P, int d, const int32_t *boot
 oal_status launch_gated_prefill_simt(const GatedArgs &p, int is_bf16, cudaStream_t stream);
 oal_status launch_gated_prefill_tc(const GatedArgs &p, cudaStream_t stream);
 oal_status launch_gated_backward_simt(const GatedArgs &p, int is_bf16, cudaStream_t stream);
+oal_status launch_gated_backward_tc(const GatedArgs &p, cudaStream_t stream);
 oal_status launch_gated_decode(const void *q, const void *k, const void *v, int is_bf16,
                                const float *g, int B, int Hq, int Hkv, float scale,
                                const int32_t *slots, int n_slots, float *state, void *y,
@@ -521,7 +522,9 @@ size_t oal_gated_backward_workspace_bytes(int B, int Hq, int Hkv, int T, int d, 
   if (check_gated(B, Hq, Hkv, T, d, dv, dtype, 1.f) != OAL_OK) return 0;
   if (B == 0 || T == 0) return 256;
   const int nseg = oal::gated_segments(T, oal::gated_backward_segment(dtype == OAL_BF16));
-  return 2 * gated_states_bytes(B, Hkv, nseg) + round256((size_t)B * Hkv * nseg * sizeof(float));
+  // (bf16: and both once more, as pairs of bf16 tiles)
+  return (dtype == OAL_BF16 ? 4 : 2) * gated_states_bytes(B, Hkv, nseg) +
+         round256((size_t)B * Hkv * nseg * sizeof(float));
 }
 
 oal_status oal_gated_backward(const void *Q, const void *K, const void *V, oal_dtype dtype,
@@ -566,11 +569,14 @@ oal_status oal_gated_backward(const void *Q, const void *K, const void *V, oal_d
   const size_t states = gated_states_bytes(B, Hkv, p.nseg);
   p.seg_state = static_cast<float *>(workspace);
   p.seg_grad = reinterpret_cast<float *>(static_cast<char *>(workspace) + states);
-  p.seg_decay = reinterpret_cast<float *>(static_cast<char *>(workspace) + 2 * states);
+  uint8_t *rest = static_cast<uint8_t *>(workspace) + 2 * states;
+  if (dtype == OAL_BF16) p.state_tiles = rest, p.grad_tiles = rest + states, rest += 2 * states;
+  p.seg_decay = reinterpret_cast<float *>(rest);
   p.status = oal_device_status_word();
   if (!p.status) return oal_fail(OAL_ERR_CUDA, "no device status word");
   oal_begin_call(stream);
-  return oal::launch_gated_backward_simt(p, dtype == OAL_BF16, stream);
+  if (dtype == OAL_BF16) return oal::launch_gated_backward_tc(p, stream);
+  return oal::launch_gated_backward_simt(p, 0, stream);
 }
 
 oal_status oal_gated_decode_step(const void *q, const void *k, const void *v, oal_dtype dtype,
