@@ -161,7 +161,7 @@ gated_tc_out_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
   extern __shared__ uint8_t smem_raw[];
   OutSmem &s = *reinterpret_cast<OutSmem *>(align1024(smem_raw));
   const int bh = blockIdx.x / p.nseg, seg = blockIdx.x % p.nseg, b = bh / p.Hkv, kv = bh % p.Hkv;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
   const int rho = p.Hq / p.Hkv, npair = (rho + 1) / 2;
   if (tid == 0) {
     s.abort_flag = 0;
@@ -186,7 +186,7 @@ gated_tc_out_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tb = s.tmem;
+  const uint32_t tb = uniform(s.tmem);
   const int c0 = seg * p.seg_chunks, nc = max(0, min((n + kGC - 1) / kGC - c0, p.seg_chunks));
   const int steps = nc * npair;              // step it: chunk it / npair, heads 2 (it % npair), + 1
   volatile int *abort_flag = &s.abort_flag;

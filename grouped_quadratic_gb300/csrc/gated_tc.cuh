@@ -34,6 +34,11 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t *r) {
                "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                : "memory");
 }
+// A value that is the same in all lanes, as one the compiler knows to be so:
+// branches on it are uniform, and what follows from it (descriptors, tensor-
+// memory addresses) stays in uniform registers, where an MMA wants it.
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
+__device__ __forceinline__ int warp_index() { return (int)uniform(threadIdx.x >> 5); }
 // mbar_wait by a whole warp, whose lanes agree on the outcome (the tensor-
 // memory instructions that follow want all of them).
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort, int *status) {

@@ -175,7 +175,7 @@ gated_tc_grad_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
   pdl_trigger();
   extern __shared__ uint8_t smem_raw[];
   GradSmem &s = *reinterpret_cast<GradSmem *>(align1024(smem_raw));
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
   const int rho = p.Hq / p.Hkv, npair = (rho + 1) / 2;
   if (tid == 0) {
     s.abort_flag = 0;
@@ -193,7 +193,7 @@ gated_tc_grad_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tb = s.tmem, tx = tb, tz = tb + 64, tkv = tb + 128;
+  const uint32_t tb = uniform(s.tmem), tx = tb, tz = tb + 64, tkv = tb + 128;
   volatile int *abort_flag = &s.abort_flag;
   auto wait = [&](uint64_t *bar, int phase) { return warp_wait(bar, phase & 1, abort_flag, p.status); };
   auto arrive = [&](uint64_t *bar) {
