@@ -67,10 +67,11 @@ __device__ __forceinline__ uint32_t bf2_fma(uint32_t a, uint32_t b, uint32_t c) 
 // whose rounding error w_hi a - hi is a bf16 number itself, and
 // lo = bf16(w_lo a + that), three packed products for two values; the terms'
 // sum is off by at most 2^-15 of w a where one rounded factor would be off by
-// 2^-8.  b is exact.
-// The two terms of one accumulator are kNb products apart, and the next
+// 2^-8.  With kTerms = 3 the error and bf16(w_lo a) go in apart: off by 2^-16
+// at most, mostly by the weight's own second rounding.  b is exact.
+// The terms of one accumulator are kNb products apart, and the next
 // 16 rows' operand is under way while these multiply.
-template <int kFrom, int kTo, int kNb>
+template <int kFrom, int kTo, int kTerms = 2, int kNb>
 __device__ __forceinline__ void state_add(StateAcc<kNb> &s, int nb0, const void *a_tile, const void *b_tile,
                                           const PairWeights &w) {
   const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3;
@@ -87,18 +88,23 @@ __device__ __forceinline__ void state_add(StateAcc<kNb> &s, int nb0, const void 
   for (int ks = kFrom; ks < kTo; ++ks) {
 #pragma unroll
     for (int np = 0; np < kNb / 2; ++np) ldsm4t(bt[np] + 2048 * ks, b[np]);
-    uint32_t hi[4], lo[4];
+    uint32_t hi[4], lo[4], rest[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const uint32_t wh = w.hi[8 * ks + 4 * (e >> 1) + q], wl = w.lo[8 * ks + 4 * (e >> 1) + q];
       hi[e] = bf2_mul(wh, a[e]);
-      lo[e] = bf2_fma(wl, a[e], bf2_fma(wh, a[e], hi[e] ^ 0x80008000u));
+      lo[e] = bf2_fma(wh, a[e], hi[e] ^ 0x80008000u);
+      if (kTerms == 3) rest[e] = bf2_mul(wl, a[e]);
+      else lo[e] = bf2_fma(wl, a[e], lo[e]);
     }
     if (ks + 1 < kTo) ldsm4t(at + 2048 * (ks + 1), a);
 #pragma unroll
     for (int nb = 0; nb < kNb; ++nb) mma16816(s.v[nb], hi, b[nb >> 1][2 * (nb & 1)], b[nb >> 1][2 * (nb & 1) + 1]);
 #pragma unroll
     for (int nb = 0; nb < kNb; ++nb) mma16816(s.v[nb], lo, b[nb >> 1][2 * (nb & 1)], b[nb >> 1][2 * (nb & 1) + 1]);
+    if (kTerms == 3)
+#pragma unroll
+      for (int nb = 0; nb < kNb; ++nb) mma16816(s.v[nb], rest, b[nb >> 1][2 * (nb & 1)], b[nb >> 1][2 * (nb & 1) + 1]);
   }
 }
 template <int kNb>

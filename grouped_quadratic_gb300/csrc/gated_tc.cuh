@@ -39,10 +39,28 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t *r) {
 // memory addresses) stays in uniform registers, where an MMA wants it.
 __device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
 __device__ __forceinline__ int warp_index() { return (int)uniform(threadIdx.x >> 5); }
-// mbar_wait by a whole warp, whose lanes agree on the outcome (the tensor-
-// memory instructions that follow want all of them).
+// A bounded wait like mbar_wait by a whole warp, whose lanes agree on the
+// outcome (the tensor-memory instructions that follow want all of them).  The
+// abort flag and the clock are looked at every 16th time: most waits here end
+// within a microsecond, and a waiting warp's loop takes issue slots from the
+// warps that it waits for.
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort, int *status) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, status));
+  bool ok = mbar_try_wait(bar, parity);
+  if (!ok) {
+    const uint64_t t0 = cycles_now();
+    while (true) {
+#pragma unroll 1
+      for (int i = 0; i < 16 && !ok; ++i) ok = mbar_try_wait(bar, parity);
+      if (ok || *abort) break;
+      const uint64_t el = cycles_now() - t0;
+      if (el > kWaitFloorCycles && el > wait_limit(status)) {
+        *abort = 1;
+        if (status) atomicCAS(status, 0, 4 /* OAL_ERR_TIMEOUT */);
+        break;
+      }
+    }
+  }
+  return __all_sync(0xffffffffu, ok);
 }
 // The first 1024-byte boundary of the dynamic shared memory.  (By an offset: a
 // pointer rounded as an integer is one the compiler no longer knows to be

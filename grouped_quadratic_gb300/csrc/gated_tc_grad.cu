@@ -89,7 +89,7 @@ gated_tc_own_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
       fence_proxy_async();
       __syncthreads();
     }
-    if (ok) state_add<0, 4>(acc, 0, s.a[st], s.b[st], s.w);
+    if (ok) state_add<0, 4, 3>(acc, 0, s.a[st], s.b[st], s.w);
     __syncthreads();
     if (tid == 0 && ok && r + kOwnStages < count) load(r + kOwnStages);
   }
@@ -151,17 +151,22 @@ __global__ void __launch_bounds__(kScanThreads) gated_tc_scan_kernel(GatedArgs p
 
 // ---------------------------------------------------------------- gradients
 
-constexpr int kGradThreads = 288;              // eight computing warps and one that issues
+constexpr int kGradThreads = 320;              // eight computing warps, one for the MMAs, one for loads and gates
 constexpr uint32_t kGradCols = 256;
 struct GradSmem {
-  uint8_t kv[2 * kTileBytes];                  // K, V; at the end dV, dK
+  uint8_t kv[2 * kTileBytes];                  // K, V
   uint8_t oq[4 * kTileBytes];                  // dY of two heads, Q of two heads
-  uint8_t pz[4 * kTileBytes];                  // R hi, R lo; then p (later dQ) and z, 128 rows each
+  uint8_t pz[4 * kTileBytes];                  // p, z of 128 rows; R hi, R lo before p, dQ after it; dV, dK after z
   uint8_t st[2 * kTileBytes];                  // S hi, lo
-  ChunkGates gates;
-  float tail[kGC], head[kGC];                  // e^{G_63-G_j}, e^{G_i}
-  float rows[2][2 * kGC], cols[4][kGC], far[2][kGC], dots[8];   // parts of dg
-  uint64_t kv_full, gate_full, far_full, q_full, clean, go, xz_full, pz_full, dq_full, pair[4], meet, chunk_done, drain;
+  struct alignas(16) Gates {
+    ChunkGates c;
+    float tail[kGC], head[kGC];                // e^{G_63-G_j}, e^{G_i}
+  } gates[2];
+  struct Sums {                                // parts of dg
+    float rows[2][2 * kGC], cols[4][kGC], far[2][kGC], dots[8];
+  } sums[2];
+  uint64_t kv_full, r_full, gate_full, far_full, q_full, clean, go, xz_full, pz_full, dq_full, p_free, pair[4], meet,
+      chunk_done[2], drain;
   uint32_t tmem;
   int abort_flag;
 };
@@ -179,9 +184,10 @@ gated_tc_grad_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
   const int rho = p.Hq / p.Hkv, npair = (rho + 1) / 2;
   if (tid == 0) {
     s.abort_flag = 0;
-    mbar_init(&s.kv_full, 1), mbar_init(&s.gate_full, 1), mbar_init(&s.far_full, 1), mbar_init(&s.q_full, 1);
-    mbar_init(&s.clean, 8), mbar_init(&s.go, 8), mbar_init(&s.xz_full, 1), mbar_init(&s.pz_full, 8);
-    mbar_init(&s.dq_full, 1), mbar_init(&s.meet, 8), mbar_init(&s.chunk_done, 8), mbar_init(&s.drain, 1);
+    mbar_init(&s.kv_full, 1), mbar_init(&s.r_full, 1), mbar_init(&s.gate_full, 1), mbar_init(&s.far_full, 1);
+    mbar_init(&s.q_full, 1), mbar_init(&s.clean, 8), mbar_init(&s.go, 8), mbar_init(&s.xz_full, 1);
+    mbar_init(&s.pz_full, 8), mbar_init(&s.dq_full, 1), mbar_init(&s.p_free, 4), mbar_init(&s.meet, 8);
+    mbar_init(&s.chunk_done[0], 8), mbar_init(&s.chunk_done[1], 8), mbar_init(&s.drain, 1);
     for (int i = 0; i < 4; ++i) mbar_init(&s.pair[i], 2);
     fence_mbar_init();
   }
@@ -202,15 +208,136 @@ gated_tc_grad_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
   };
   const int total = p.nseg * p.B * p.Hkv;
   bool ok = true;
-  // Both sides count alike: k chunks begun, it steps (a chunk's pairs of
-  // heads), cl cleanings.  Every barrier completes once per what it counts and
-  // all who wait on it wait every time, so none is ever two phases ahead.
+  // All sides count alike: k chunks, it steps (a chunk's pairs of heads), cl
+  // cleanings.  Every barrier completes once per what it counts, and whoever
+  // waits on it is never more than a phase behind: the next but one needs
+  // what comes after that wait (chunk_done is a pair for that).
   int k = 0, it = 0, cl = 0;
   // Tiles of heads that do not exist, or rows behind a sequence, are cleared
   // before the tensor cores read them (they are summed over).
   auto cleans = [&](int pr, bool tail) { return tail || (rho - 2 * pr == 1 && (rho > 1 || it == 0)); };
 
-  if (warp == 8) {
+  if (warp == 9) {
+    // ---- loads and gates, ahead of the rest; dg behind it
+    auto load_q = [&](int t0, int h0, int pr) {
+      const int heads = min(2, rho - 2 * pr);
+      mbar_arrive_expect_tx(&s.q_full, 2 * heads * kTileBytes);
+      for (int h = 0; h < heads; ++h) {
+        tma_load_3d(s.oq + h * kTileBytes, &tmO, &s.q_full, 0, t0, h0 + 2 * pr + h);
+        tma_load_3d(s.oq + (2 + h) * kTileBytes, &tmQ, &s.q_full, 0, t0, h0 + 2 * pr + h);
+      }
+    };
+    auto prefetch_q = [&](int t0, int h0, int pr) {
+      for (int h = 2 * pr; h < min(2 * pr + 2, rho); ++h) {
+        tma_prefetch_3d(&tmO, 0, t0, h0 + h);
+        tma_prefetch_3d(&tmQ, 0, t0, h0 + h);
+      }
+    };
+    // dg of the chunk before: its parts are there once all warps are done with it
+    float *dg = nullptr;
+    int dg_rows = 0;
+    auto finish = [&]() {
+      if (!wait(&s.chunk_done[(k - 1) & 1], (k - 1) >> 1)) return false;
+      const GradSmem::Sums &u = s.sums[(k - 1) & 1];
+      const ChunkGates &gates = s.gates[(k - 1) & 1].c;
+      float x = 0.f, r[2], f[2];
+#pragma unroll
+      for (int z = 0; z < 8; ++z) x += u.dots[z];
+      x *= gates.whole;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int t = 2 * lane + e;
+        r[e] = (u.rows[0][t] + u.rows[1][t]) + (u.rows[0][64 + t] + u.rows[1][64 + t]) -
+               ((u.cols[0][t] + u.cols[1][t]) + (u.cols[2][t] + u.cols[3][t]));
+        f[e] = u.far[0][t] + u.far[1][t];
+      }
+      float down = r[0] + r[1], up = f[0] + f[1];              // sums from this lane on; up to it
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const float a = __shfl_down_sync(0xffffffffu, down, d), v = __shfl_up_sync(0xffffffffu, up, d);
+        if (lane + d < 32) down += a;
+        if (lane >= d) up += v;
+      }
+      up = __shfl_up_sync(0xffffffffu, up, 1);
+      if (lane == 0) up = 0.f;
+      float after = __shfl_down_sync(0xffffffffu, down, 1);
+      if (lane == 31) after = 0.f;
+      const float d0 = x + (after + r[1] + r[0]) + up, d1 = x + (after + r[1]) + (up + f[0]);
+      if (2 * lane < dg_rows) dg[2 * lane] = gates.cut_even >> lane & 1u ? 0.f : d0;
+      if (2 * lane + 1 < dg_rows) dg[2 * lane + 1] = gates.cut_odd >> lane & 1u ? 0.f : d1;
+      return true;
+    };
+    int q_loads = 0;
+    for (int idx = blockIdx.x; idx < total && ok; idx += gridDim.x) {
+      const int bh = idx / p.nseg, c = idx % p.nseg, b = bh / p.Hkv, kv = bh % p.Hkv, t0 = c * kGC;
+      const int n = gated_len(p, b), h0 = b * p.Hq + kv * rho;
+      if (t0 >= n) continue;
+      // the last step's MMAs have read K, V, S and the pair of heads (waited for below)
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&s.kv_full, 4 * kTileBytes);
+        tma_load_3d(s.kv, &tmK, &s.kv_full, 0, t0, bh);
+        tma_load_3d(s.kv + kTileBytes, &tmV, &s.kv_full, 0, t0, bh);
+        bulk_load(s.st, p.state_tiles + (size_t)idx * 2 * kTileBytes, 2 * kTileBytes, &s.kv_full);
+        load_q(t0, h0, 0), ++q_loads;
+      }
+      __syncwarp();
+      // (two chunks back, these gates were read for the last time before that dg)
+      const float2 gate = gate_load(p.g + (size_t)bh * p.T, t0, n);
+      const GateLane sums = gate_sums(gate);
+      GradSmem::Gates &to = s.gates[k & 1];
+      chunk_gates(gate, sums, to.c);
+      const float eh = __shfl_sync(0xffffffffu, sums.hi[1], 31), el = __shfl_sync(0xffffffffu, sums.lo[1], 31);
+      const int ec = __shfl_sync(0xffffffffu, sums.cuts[1], 31);
+      reinterpret_cast<float2 *>(to.tail)[lane] =
+          make_float2(gate_exp_fast(sums.cuts[0] == ec, (eh - sums.hi[0]) + (el - sums.lo[0])),
+                      gate_exp_fast(sums.cuts[1] == ec, (eh - sums.hi[1]) + (el - sums.lo[1])));
+      reinterpret_cast<float2 *>(to.head)[lane] = make_float2(gate_exp_fast(sums.cuts[0] == 0, sums.hi[0] + sums.lo[0]),
+                                                              gate_exp_fast(sums.cuts[1] == 0, sums.hi[1] + sums.lo[1]));
+      arrive(&s.gate_full);
+      // R goes where the last outputs dQ were: they have left
+      ok = k == 0 || wait(&s.p_free, it - 1);
+      if (!ok) break;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&s.r_full, 2 * kTileBytes);
+        bulk_load(s.pz, p.grad_tiles + (size_t)idx * 2 * kTileBytes, 2 * kTileBytes, &s.r_full);
+        if (npair > 1) prefetch_q(t0, h0, 1);
+      }
+      __syncwarp();
+      if (k > 0 && !finish()) ok = false;
+      if (!ok) break;
+      dg = p.dg + (size_t)bh * p.T + t0;
+      dg_rows = n - t0;
+      ++k;
+      for (int pr = 0; pr < npair && ok; ++pr, ++it) {
+        if (lane == 0) {
+          if (pr + 2 < npair) prefetch_q(t0, h0, pr + 2);
+          const int next = idx + gridDim.x;
+          if (pr == npair - 1 && next < total) {
+            const int nbh = next / p.nseg, nt = (next % p.nseg) * kGC;
+            tma_prefetch_3d(&tmK, 0, nt, nbh);
+            tma_prefetch_3d(&tmV, 0, nt, nbh);
+            prefetch_l2(p.state_tiles + (size_t)next * 2 * kTileBytes, 2 * kTileBytes);
+            prefetch_l2(p.grad_tiles + (size_t)next * 2 * kTileBytes, 2 * kTileBytes);
+            prefetch_q(nt, (nbh / p.Hkv) * p.Hq + (nbh % p.Hkv) * rho, 0);
+          }
+        }
+        __syncwarp();
+        ok = wait(&s.dq_full, it);
+        if (ok && lane == 0 && pr + 1 < npair) load_q(t0, h0, pr + 1), ++q_loads;
+        __syncwarp();
+      }
+    }
+    if (ok && k > 0) finish();
+    if (lane == 0 && !ok) {   // the last loads may not have been waited for
+      for (int ph = 0; ph < 2; ++ph) {
+        mbar_wait_teardown(&s.kv_full, ph, p.status);
+        mbar_wait_teardown(&s.r_full, ph, p.status);
+      }
+      if (q_loads > 0) mbar_wait_teardown(&s.q_full, (q_loads - 1) & 1, p.status);
+    }
+    __syncwarp();
+  } else if (warp == 8) {
+    // ---- the MMAs
     const uint32_t id_k = idesc_bf16_f32(128, 64, 0), id_mn = idesc_bf16_f32(128, 64, 1);
     const uint32_t id_kv = idesc_bf16_f32(128, 128, 1) | (1u << 15);   // A with rows along its minor axis too
     const uint64_t od = sdesc_sw128(smem_u32(s.oq), 16, 1024), qd = sdesc_sw128(smem_u32(s.oq) + 2 * kTileBytes, 16, 1024);
@@ -221,77 +348,11 @@ gated_tc_grad_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
     // [p | z] and [dY | Q]: two 64-column atoms, 16 KB apart
     const uint64_t pzd = sdesc_sw128(smem_u32(s.pz), 2 * kTileBytes, 1024);
     const uint64_t oqd = sdesc_sw128(smem_u32(s.oq), 2 * kTileBytes, 1024);
-    int loads = 0;
     for (int idx = blockIdx.x; idx < total && ok; idx += gridDim.x) {
-      const int bh = idx / p.nseg, c = idx % p.nseg, b = bh / p.Hkv, kv = bh % p.Hkv, t0 = c * kGC;
-      const int n = gated_len(p, b), h0 = b * p.Hq + kv * rho;
+      const int t0 = (idx % p.nseg) * kGC, n = gated_len(p, idx / p.nseg / p.Hkv);
       if (t0 >= n) continue;
       const bool tail = t0 + kGC > n && n < p.T;
-      const float2 gate = gate_load(p.g + (size_t)bh * p.T, t0, n);
-      auto load_q = [&](int pr) {
-        const int heads = min(2, rho - 2 * pr);
-        mbar_arrive_expect_tx(&s.q_full, 2 * heads * kTileBytes);
-        for (int h = 0; h < heads; ++h) {
-          tma_load_3d(s.oq + h * kTileBytes, &tmO, &s.q_full, 0, t0, h0 + 2 * pr + h);
-          tma_load_3d(s.oq + (2 + h) * kTileBytes, &tmQ, &s.q_full, 0, t0, h0 + 2 * pr + h);
-        }
-      };
-      if (k > 0) ok = wait(&s.chunk_done, k - 1);
-      if (!ok) break;
-      if (lane == 0) {
-        mbar_arrive_expect_tx(&s.kv_full, 6 * kTileBytes);
-        tma_load_3d(s.kv, &tmK, &s.kv_full, 0, t0, bh);
-        tma_load_3d(s.kv + kTileBytes, &tmV, &s.kv_full, 0, t0, bh);
-        bulk_load(s.st, p.state_tiles + (size_t)idx * 2 * kTileBytes, 2 * kTileBytes, &s.kv_full);
-        bulk_load(s.pz, p.grad_tiles + (size_t)idx * 2 * kTileBytes, 2 * kTileBytes, &s.kv_full);
-        load_q(0), ++loads;
-        for (int h = 2; h < min(4, rho); ++h) {
-          tma_prefetch_3d(&tmO, 0, t0, h0 + h);
-          tma_prefetch_3d(&tmQ, 0, t0, h0 + h);
-        }
-        const int next = idx + gridDim.x;
-        if (next < total) {
-          const int nbh = next / p.nseg, nt = (next % p.nseg) * kGC, nh = (nbh / p.Hkv) * p.Hq + (nbh % p.Hkv) * rho;
-          tma_prefetch_3d(&tmK, 0, nt, nbh);
-          tma_prefetch_3d(&tmV, 0, nt, nbh);
-          prefetch_l2(p.state_tiles + (size_t)next * 2 * kTileBytes, 2 * kTileBytes);
-          prefetch_l2(p.grad_tiles + (size_t)next * 2 * kTileBytes, 2 * kTileBytes);
-          for (int h = 0; h < min(2, rho); ++h) {
-            tma_prefetch_3d(&tmO, 0, nt, nh + h);
-            tma_prefetch_3d(&tmQ, 0, nt, nh + h);
-          }
-        }
-      }
-      __syncwarp();
-      {
-        const GateLane sums = gate_sums(gate);
-        chunk_gates(gate, sums, s.gates);
-        const float eh = __shfl_sync(0xffffffffu, sums.hi[1], 31), el = __shfl_sync(0xffffffffu, sums.lo[1], 31);
-        const int ec = __shfl_sync(0xffffffffu, sums.cuts[1], 31);
-        float2 tl, hd;
-        tl.x = gate_exp_fast(sums.cuts[0] == ec, (eh - sums.hi[0]) + (el - sums.lo[0]));
-        tl.y = gate_exp_fast(sums.cuts[1] == ec, (eh - sums.hi[1]) + (el - sums.lo[1]));
-        hd.x = gate_exp_fast(sums.cuts[0] == 0, sums.hi[0] + sums.lo[0]);
-        hd.y = gate_exp_fast(sums.cuts[1] == 0, sums.hi[1] + sums.lo[1]);
-        reinterpret_cast<float2 *>(s.tail)[lane] = tl;
-        reinterpret_cast<float2 *>(s.head)[lane] = hd;
-      }
-      arrive(&s.gate_full);
       ok = wait(&s.kv_full, k);
-      if (ok && tail) ok = wait(&s.clean, cl++);
-      if (!ok) break;
-      tc_fence_after();
-      // [K; V] R and [K; V] R^T side by side: K R above on the left, V R^T below on the right
-#pragma unroll
-      for (int j = 0; j < 4; ++j) umma_ss_warp(tkv, kd + 2 * j, rh + 128 * j, id_mn, j > 0);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) umma_ss_warp(tkv, kd + 2 * j, rl + 128 * j, id_mn, 1u);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) umma_ss_warp(tkv + 64, kd + 2 * j, rh + 2 * j, id_k, j > 0);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) umma_ss_warp(tkv + 64, kd + 2 * j, rl + 2 * j, id_k, 1u);
-      umma_commit_warp(&s.far_full);
-      ++k;
       for (int pr = 0; pr < npair && ok; ++pr) {
         ok = wait(&s.q_full, it);
         if (ok && cleans(pr, tail)) ok = wait(&s.clean, cl++);
@@ -303,6 +364,22 @@ gated_tc_grad_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
 #pragma unroll
         for (int j = 0; j < 4; ++j) umma_ss_warp(tz, od + 2 * j, vd + 2 * j, id_k, j > 0);
         umma_commit_warp(&s.xz_full);
+        if (pr == 0) {
+          // [K; V] R and [K; V] R^T side by side: K R above on the left, V R^T below on the right
+          ok = wait(&s.r_full, k) && (k == 0 || wait(&s.chunk_done[(k - 1) & 1], (k - 1) >> 1));
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int j = 0; j < 4; ++j) umma_ss_warp(tkv, kd + 2 * j, rh + 128 * j, id_mn, j > 0);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) umma_ss_warp(tkv, kd + 2 * j, rl + 128 * j, id_mn, 1u);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) umma_ss_warp(tkv + 64, kd + 2 * j, rh + 2 * j, id_k, j > 0);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) umma_ss_warp(tkv + 64, kd + 2 * j, rl + 2 * j, id_k, 1u);
+          umma_commit_warp(&s.far_full);
+          ++k;
+        }
         ok = wait(&s.pz_full, it);        // p and z are there, X and Z are read
         if (!ok) break;
         tc_fence_after();
@@ -315,29 +392,11 @@ gated_tc_grad_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
 #pragma unroll
         for (int j = 0; j < 8; ++j) umma_ss_warp(tkv, pzd + 128 * j, oqd + 128 * j, id_kv, 1u);
         umma_commit_warp(&s.dq_full);
-        ok = wait(&s.dq_full, it);
         ++it;
-        if (ok && pr + 1 < npair) {
-          if (lane == 0) {
-            load_q(pr + 1), ++loads;
-            for (int h = 2 * pr + 4; h < min(2 * pr + 6, rho); ++h) {
-              tma_prefetch_3d(&tmO, 0, t0, h0 + h);
-              tma_prefetch_3d(&tmQ, 0, t0, h0 + h);
-            }
-          }
-          __syncwarp();
-        }
       }
     }
     umma_commit_warp(&s.drain);
-    if (lane == 0) {   // nothing in flight at the block's end
-      mbar_wait_teardown(&s.drain, 0, p.status);
-      if (!ok) {       // (the last loads may not have been waited for)
-        mbar_wait_teardown(&s.kv_full, k & 1, p.status);
-        mbar_wait_teardown(&s.kv_full, (k + 1) & 1, p.status);
-        if (loads > 0) mbar_wait_teardown(&s.q_full, (loads - 1) & 1, p.status);
-      }
-    }
+    if (lane == 0) mbar_wait_teardown(&s.drain, 0, p.status);   // no MMA in flight at the block's end
     __syncwarp();
   } else {
     const int quad = warp & 3, hf = warp >> 2;                 // lanes of tensor memory; keys (dims) 32 hf .. + 31
@@ -351,16 +410,31 @@ gated_tc_grad_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
       const int n = gated_len(p, b), h0 = b * p.Hq + kv * rho;
       if (t0 >= n) continue;
       const bool tail = t0 + kGC > n && n < p.T;
+      const GradSmem::Gates &gates = s.gates[k & 1];
+      GradSmem::Sums &sums = s.sums[k & 1];
       ok = wait(&s.gate_full, k) && wait(&s.kv_full, k);
       if (!ok) break;
-      if (tail) {
-        clear_rows(s.kv, n - t0, tid, 256);
-        clear_rows(s.kv + kTileBytes, n - t0, tid, 256);
+      auto clean = [&](int pr) {
+        const int keep = tail ? n - t0 : 64, keep1 = rho - 2 * pr == 1 ? 0 : keep;
+        clear_rows(s.oq, keep, tid, 256);
+        clear_rows(s.oq + kTileBytes, keep1, tid, 256);
+        clear_rows(s.oq + 2 * kTileBytes, keep, tid, 256);
+        clear_rows(s.oq + 3 * kTileBytes, keep1, tid, 256);
         fence_proxy_async();
         arrive(&s.clean);
-        ++cl;
+      };
+      if (cleans(0, tail)) {                                   // with the first pair: K and V too
+        ok = wait(&s.q_full, it);
+        if (!ok) break;
+        if (tail) {
+          clear_rows(s.kv, n - t0, tid, 256);
+          clear_rows(s.kv + kTileBytes, n - t0, tid, 256);
+        }
+        clean(0);
       }
       float cfar = 0.f;
+      ok = wait(&s.r_full, k);
+      if (!ok) break;
       {
         // <S, R>: all four tiles hold an element at the same place
         const uint32_t *a = reinterpret_cast<const uint32_t *>(s.st), *r = reinterpret_cast<const uint32_t *>(s.pz);
@@ -376,12 +450,12 @@ gated_tc_grad_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
         }
 #pragma unroll
         for (int d = 16; d; d >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, d);
-        if (lane == 0) s.dots[warp] = dot;
+        if (lane == 0) sums.dots[warp] = dot;
         // K R (rows 0 .. 63) and V R^T (64 .. 127) times the keys' decays to the chunk's end
         ok = wait(&s.far_full, k);
         if (!ok) break;
         tc_fence_after();
-        const float tj = s.tail[i];
+        const float tj = gates.tail[i];
         const uint32_t from = tkv + (quad & 2 ? 64u : 0u) + 32u * hf + lanes;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -407,15 +481,16 @@ gated_tc_grad_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
         tmem_wait_st();
         tc_fence_before();
       }
+      if (hf == 0 && lane == 0) bulk_wait_read();              // the chunk before's dV, dK have left the place of z
       arrive(&s.meet);
       ok = wait(&s.meet, met++);                               // R is read by all: p takes its place
       if (!ok) break;
       ++k;
-      const int mode = s.gates.mode;
-      const float fq = p.scale * s.head[i];
-      const float fr = p.scale * s.gates.row[i] * (pre && mode == kHalves ? s.gates.first : 1.f);
+      const int mode = gates.c.mode;
+      const float fq = p.scale * gates.head[i];
+      const float fr = p.scale * gates.c.row[i] * (pre && mode == kHalves ? gates.c.first : 1.f);
       int begin = 0;
-      cut_before(s.gates, i, begin);
+      cut_before(gates.c, i, begin);
       const uint32_t live = 0xFFFFFFFFu << min(31, max(0, begin - 32 * hf));
       const uint32_t mask = own ? live & (0xFFFFFFFFu >> (31 - lane)) : pre && begin < 32 ? live : 0u;
       const uint32_t strict = own ? mask & ~(1u << lane) : mask;
@@ -425,22 +500,16 @@ gated_tc_grad_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
 #pragma unroll
       for (int e = 0; e < 32; ++e) w[e] = 0.f;
       for (int pr = 0; pr < npair; ++pr) {
-        const bool single = rho - 2 * pr == 1;
         ok = wait(&s.q_full, it);
         if (!ok) break;
-        if (cleans(pr, tail)) {
-          const int keep = tail ? n - t0 : 64, keep1 = single ? 0 : keep;
-          clear_rows(s.oq, keep, tid, 256);
-          clear_rows(s.oq + kTileBytes, keep1, tid, 256);
-          clear_rows(s.oq + 2 * kTileBytes, keep, tid, 256);
-          clear_rows(s.oq + 3 * kTileBytes, keep1, tid, 256);
-          fence_proxy_async();
-          arrive(&s.clean);
-          ++cl;
-        }
+        if (pr > 0 && cleans(pr, tail)) clean(pr);
         ok = wait(&s.xz_full, it);
         if (!ok) break;
         tc_fence_after();
+        if (pr > 0) {                                          // the outputs of the step before have left the place of p
+          ok = wait(&s.p_free, it - 1);
+          if (!ok) break;
+        }
         if (own || pre) {
 #pragma unroll
           for (int h = 0; h < 4; ++h) {
@@ -451,7 +520,7 @@ gated_tc_grad_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
             if (mode != kEach) {
 #pragma unroll
               for (int e = 0; e < 8; e += 4) {
-                const float4 r = *reinterpret_cast<const float4 *>(s.gates.rest + 32 * hf + 8 * h + e);
+                const float4 r = *reinterpret_cast<const float4 *>(gates.c.rest + 32 * hf + 8 * h + e);
                 f[e] = fr * r.x, f[e + 1] = fr * r.y, f[e + 2] = fr * r.z, f[e + 3] = fr * r.w;
               }
             } else {
@@ -527,6 +596,7 @@ gated_tc_grad_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
         }
         fence_proxy_async();
         tc_fence_before();
+        arrive(&s.go);
         arrive(&s.pair[quad]);
         if (hf == 0) {                                         // both halves of these 32 rows are there
           ok = wait(&s.pair[quad], paired);
@@ -536,10 +606,11 @@ gated_tc_grad_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
             if (!tail && hd < rho && t0 + row < n) tma_store_3d(&tmDQ, s.pz + 32 * quad * 128, 0, t0 + row, h0 + hd);
             bulk_commit();
             bulk_wait_read();
+            mbar_arrive(&s.p_free);
           }
+          __syncwarp();
         }
         ++paired;
-        arrive(&s.go);
       }
       if (!ok) break;
       // dV from rows 0 .. 63, dK from rows 64 .. 127; the sums for dg
@@ -558,7 +629,7 @@ gated_tc_grad_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
             for (int e = 0; e < 4; ++e)
               o[e] = pack_bf16x2(__uint_as_float(x[8 * z + 2 * e]), __uint_as_float(x[8 * z + 2 * e + 1]));
             const uint4 out = make_uint4(o[0], o[1], o[2], o[3]);
-            if (!tail) *reinterpret_cast<uint4 *>(s.kv + tile_at(m, 4 * hf + 2 * h + z)) = out;
+            if (!tail) *reinterpret_cast<uint4 *>(s.pz + 2 * kTileBytes + tile_at(m, 4 * hf + 2 * h + z)) = out;   // z has been read
             else if (t0 + i < n) dst[2 * h + z] = out;
           }
         }
@@ -570,7 +641,7 @@ gated_tc_grad_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
           if (!ok) break;
           if (lane == 0) {
             const int row = 32 * (quad & 1);
-            if (!tail && t0 + row < n) tma_store_3d(quad & 2 ? &tmDK : &tmDV, s.kv + 32 * quad * 128, 0, t0 + row, bh);
+            if (!tail && t0 + row < n) tma_store_3d(quad & 2 ? &tmDK : &tmDV, s.pz + 2 * kTileBytes + 32 * quad * 128, 0, t0 + row, bh);
             bulk_commit();
           }
         }
@@ -578,7 +649,7 @@ gated_tc_grad_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
         float sum = racc;
 #pragma unroll
         for (int e = 0; e < 32; ++e) sum += w[e];
-        s.rows[hf][m] = sum;
+        sums.rows[hf][m] = sum;
         // lane l ends with the sum over the warp's rows of column l
 #pragma unroll
         for (int d = 16; d; d >>= 1)
@@ -587,42 +658,10 @@ gated_tc_grad_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
             const float keep = lane & d ? w[e + d] : w[e], give = lane & d ? w[e] : w[e + d];
             w[e] = keep + __shfl_xor_sync(0xffffffffu, give, d);
           }
-        s.cols[quad][32 * hf + lane] = w[0];
-        if (quad & 2) s.far[hf][i] = cfar;
+        sums.cols[quad][32 * hf + lane] = w[0];
+        if (quad & 2) sums.far[hf][i] = cfar;
       }
-      arrive(&s.meet);
-      ok = wait(&s.meet, met++);
-      if (!ok) break;
-      if (warp == 7) {
-        float x = 0.f, r[2], f[2];
-#pragma unroll
-        for (int z = 0; z < 8; ++z) x += s.dots[z];
-        x *= s.gates.whole;
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int t = 2 * lane + e;
-          r[e] = (s.rows[0][t] + s.rows[1][t]) + (s.rows[0][64 + t] + s.rows[1][64 + t]) -
-                 ((s.cols[0][t] + s.cols[1][t]) + (s.cols[2][t] + s.cols[3][t]));
-          f[e] = s.far[0][t] + s.far[1][t];
-        }
-        float down = r[0] + r[1], up = f[0] + f[1];            // sums from this lane on; up to it
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-          const float a = __shfl_down_sync(0xffffffffu, down, d), u = __shfl_up_sync(0xffffffffu, up, d);
-          if (lane + d < 32) down += a;
-          if (lane >= d) up += u;
-        }
-        up = __shfl_up_sync(0xffffffffu, up, 1);
-        if (lane == 0) up = 0.f;
-        float after = __shfl_down_sync(0xffffffffu, down, 1);
-        if (lane == 31) after = 0.f;
-        float *dg = p.dg + (size_t)bh * p.T + t0 + 2 * lane;
-        const float d0 = x + (after + r[1] + r[0]) + up, d1 = x + (after + r[1]) + (up + f[0]);
-        if (t0 + 2 * lane < n) dg[0] = s.gates.cut_even >> lane & 1u ? 0.f : d0;
-        if (t0 + 2 * lane + 1 < n) dg[1] = s.gates.cut_odd >> lane & 1u ? 0.f : d1;
-      }
-      if (hf == 0 && lane == 0) bulk_wait_read();
-      arrive(&s.chunk_done);
+      arrive(&s.chunk_done[(k - 1) & 1]);
     }
     if (lane == 0) bulk_wait_all();
   }
