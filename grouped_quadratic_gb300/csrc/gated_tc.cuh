@@ -39,27 +39,38 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t *r) {
 // memory addresses) stays in uniform registers, where an MMA wants it.
 __device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
 __device__ __forceinline__ int warp_index() { return (int)uniform(threadIdx.x >> 5); }
-// A bounded wait like mbar_wait by a whole warp, whose lanes agree on the
-// outcome (the tensor-memory instructions that follow want all of them).  The
-// abort flag and the clock are looked at every 16th time: most waits here end
-// within a microsecond, and a waiting warp's loop takes issue slots from the
-// warps that it waits for.
-__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort, int *status) {
-  bool ok = mbar_try_wait(bar, parity);
-  if (!ok) {
-    const uint64_t t0 = cycles_now();
-    while (true) {
-#pragma unroll 1
-      for (int i = 0; i < 16 && !ok; ++i) ok = mbar_try_wait(bar, parity);
-      if (ok || *abort) break;
-      const uint64_t el = cycles_now() - t0;
-      if (el > kWaitFloorCycles && el > wait_limit(status)) {
-        *abort = 1;
-        if (status) atomicCAS(status, 0, 4 /* OAL_ERR_TIMEOUT */);
-        break;
-      }
+// Without a time hint the hardware puts a waiting warp to sleep until the phase
+// completes (or a while has passed); with one the wait is a loop of probes and
+// naps, which takes issue slots and instruction fetches from the others.
+__device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// The rest of a wait that did not end at once (out of line: these kernels'
+// instructions barely fit the caches).  Bounded like mbar_wait.
+static __device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile int *abort, int *status) {
+  const uint64_t t0 = cycles_now();
+  while (!try_wait(bar, parity)) {
+    if (*abort) return false;
+    const uint64_t el = cycles_now() - t0;
+    if (el > kWaitFloorCycles && el > wait_limit(status)) {
+      *abort = 1;
+      if (status) atomicCAS(status, 0, 4 /* OAL_ERR_TIMEOUT */);
+      return false;
     }
   }
+  return true;
+}
+// A wait by a whole warp, whose lanes agree on the outcome (the tensor-memory
+// instructions that follow want all of them).
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort, int *status) {
+  bool ok = try_wait(smem_u32(bar), parity);
+  if (!ok) ok = wait_on(smem_u32(bar), parity, abort, status);
   return __all_sync(0xffffffffu, ok);
 }
 // The first 1024-byte boundary of the dynamic shared memory.  (By an offset: a

@@ -156,7 +156,7 @@ constexpr uint32_t kGradCols = 256;
 struct GradSmem {
   uint8_t kv[2 * kTileBytes];                  // K, V
   uint8_t oq[4 * kTileBytes];                  // dY of two heads, Q of two heads
-  uint8_t pz[4 * kTileBytes];                  // p, z of 128 rows; R hi, R lo before p, dQ after it; dV, dK after z
+  uint8_t pz[4 * kTileBytes];                  // p, z of 128 rows; dQ after p, R hi, R lo before z
   uint8_t st[2 * kTileBytes];                  // S hi, lo
   struct alignas(16) Gates {
     ChunkGates c;
@@ -175,8 +175,7 @@ static_assert(2 * (sizeof(GradSmem) + 2 * 1024) <= 228 * 1024, "two blocks per S
 __global__ void __launch_bounds__(kGradThreads, 2)
 gated_tc_grad_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                      const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
-                     const __grid_constant__ CUtensorMap tmDQ, const __grid_constant__ CUtensorMap tmDK,
-                     const __grid_constant__ CUtensorMap tmDV, GatedArgs p) {
+                     const __grid_constant__ CUtensorMap tmDQ, GatedArgs p) {
   pdl_trigger();
   extern __shared__ uint8_t smem_raw[];
   GradSmem &s = *reinterpret_cast<GradSmem *>(align1024(smem_raw));
@@ -272,13 +271,16 @@ gated_tc_grad_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
       const int bh = idx / p.nseg, c = idx % p.nseg, b = bh / p.Hkv, kv = bh % p.Hkv, t0 = c * kGC;
       const int n = gated_len(p, b), h0 = b * p.Hq + kv * rho;
       if (t0 >= n) continue;
-      // the last step's MMAs have read K, V, S and the pair of heads (waited for below)
+      // the last step's MMAs have read K, V, S, z and the pair of heads (waited for below)
       if (lane == 0) {
         mbar_arrive_expect_tx(&s.kv_full, 4 * kTileBytes);
         tma_load_3d(s.kv, &tmK, &s.kv_full, 0, t0, bh);
         tma_load_3d(s.kv + kTileBytes, &tmV, &s.kv_full, 0, t0, bh);
         bulk_load(s.st, p.state_tiles + (size_t)idx * 2 * kTileBytes, 2 * kTileBytes, &s.kv_full);
+        mbar_arrive_expect_tx(&s.r_full, 2 * kTileBytes);
+        bulk_load(s.pz + 2 * kTileBytes, p.grad_tiles + (size_t)idx * 2 * kTileBytes, 2 * kTileBytes, &s.r_full);
         load_q(t0, h0, 0), ++q_loads;
+        if (npair > 1) prefetch_q(t0, h0, 1);
       }
       __syncwarp();
       // (two chunks back, these gates were read for the last time before that dg)
@@ -294,15 +296,6 @@ gated_tc_grad_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
       reinterpret_cast<float2 *>(to.head)[lane] = make_float2(gate_exp_fast(sums.cuts[0] == 0, sums.hi[0] + sums.lo[0]),
                                                               gate_exp_fast(sums.cuts[1] == 0, sums.hi[1] + sums.lo[1]));
       arrive(&s.gate_full);
-      // R goes where the last outputs dQ were: they have left
-      ok = k == 0 || wait(&s.p_free, it - 1);
-      if (!ok) break;
-      if (lane == 0) {
-        mbar_arrive_expect_tx(&s.r_full, 2 * kTileBytes);
-        bulk_load(s.pz, p.grad_tiles + (size_t)idx * 2 * kTileBytes, 2 * kTileBytes, &s.r_full);
-        if (npair > 1) prefetch_q(t0, h0, 1);
-      }
-      __syncwarp();
       if (k > 0 && !finish()) ok = false;
       if (!ok) break;
       dg = p.dg + (size_t)bh * p.T + t0;
@@ -343,8 +336,8 @@ gated_tc_grad_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
     const uint64_t od = sdesc_sw128(smem_u32(s.oq), 16, 1024), qd = sdesc_sw128(smem_u32(s.oq) + 2 * kTileBytes, 16, 1024);
     const uint64_t kd = sdesc_sw128(smem_u32(s.kv), 16, 1024), vd = sdesc_sw128(smem_u32(s.kv) + kTileBytes, 16, 1024);
     const uint64_t sh = sdesc_sw128(smem_u32(s.st), 16, 1024), sl = sdesc_sw128(smem_u32(s.st) + kTileBytes, 16, 1024);
-    const uint64_t rh = sdesc_sw128(smem_u32(s.pz), 16, 1024), rl = sdesc_sw128(smem_u32(s.pz) + kTileBytes, 16, 1024);
-    const uint64_t zd = sdesc_sw128(smem_u32(s.pz) + 2 * kTileBytes, 16, 1024);
+    const uint64_t rh = sdesc_sw128(smem_u32(s.pz) + 2 * kTileBytes, 16, 1024);
+    const uint64_t rl = sdesc_sw128(smem_u32(s.pz) + 3 * kTileBytes, 16, 1024), zd = rh;
     // [p | z] and [dY | Q]: two 64-column atoms, 16 KB apart
     const uint64_t pzd = sdesc_sw128(smem_u32(s.pz), 2 * kTileBytes, 1024);
     const uint64_t oqd = sdesc_sw128(smem_u32(s.oq), 2 * kTileBytes, 1024);
@@ -437,7 +430,7 @@ gated_tc_grad_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
       if (!ok) break;
       {
         // <S, R>: all four tiles hold an element at the same place
-        const uint32_t *a = reinterpret_cast<const uint32_t *>(s.st), *r = reinterpret_cast<const uint32_t *>(s.pz);
+        const uint32_t *a = reinterpret_cast<const uint32_t *>(s.st), *r = reinterpret_cast<const uint32_t *>(s.pz + 2 * kTileBytes);
         float dot = 0.f;
 #pragma unroll
         for (int z = 0; z < 8; ++z) {
@@ -481,9 +474,8 @@ gated_tc_grad_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
         tmem_wait_st();
         tc_fence_before();
       }
-      if (hf == 0 && lane == 0) bulk_wait_read();              // the chunk before's dV, dK have left the place of z
       arrive(&s.meet);
-      ok = wait(&s.meet, met++);                               // R is read by all: p takes its place
+      ok = wait(&s.meet, met++);                               // R is read by all: z takes its place
       if (!ok) break;
       ++k;
       const int mode = gates.c.mode;
@@ -506,7 +498,7 @@ gated_tc_grad_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
         ok = wait(&s.xz_full, it);
         if (!ok) break;
         tc_fence_after();
-        if (pr > 0) {                                          // the outputs of the step before have left the place of p
+        if (it > 0) {                                          // the outputs of the step before have left the place of p
           ok = wait(&s.p_free, it - 1);
           if (!ok) break;
         }
@@ -629,23 +621,10 @@ gated_tc_grad_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
             for (int e = 0; e < 4; ++e)
               o[e] = pack_bf16x2(__uint_as_float(x[8 * z + 2 * e]), __uint_as_float(x[8 * z + 2 * e + 1]));
             const uint4 out = make_uint4(o[0], o[1], o[2], o[3]);
-            if (!tail) *reinterpret_cast<uint4 *>(s.pz + 2 * kTileBytes + tile_at(m, 4 * hf + 2 * h + z)) = out;   // z has been read
-            else if (t0 + i < n) dst[2 * h + z] = out;
+            if (t0 + i < n) dst[2 * h + z] = out;              // (not by way of shared memory: R is on its way there)
           }
         }
-        fence_proxy_async();
         tc_fence_before();
-        arrive(&s.pair[quad]);
-        if (hf == 0) {
-          ok = wait(&s.pair[quad], paired);
-          if (!ok) break;
-          if (lane == 0) {
-            const int row = 32 * (quad & 1);
-            if (!tail && t0 + row < n) tma_store_3d(quad & 2 ? &tmDK : &tmDV, s.pz + 2 * kTileBytes + 32 * quad * 128, 0, t0 + row, bh);
-            bulk_commit();
-          }
-        }
-        ++paired;
         float sum = racc;
 #pragma unroll
         for (int e = 0; e < 32; ++e) sum += w[e];
@@ -681,21 +660,19 @@ oal_status launch_gated_backward_tc(const GatedArgs &p, cudaStream_t stream) {
   GATED_TRY(gated_need_smem(reinterpret_cast<const void *>(gated_tc_own_kernel), own_smem, done_own));
   GATED_TRY(gated_need_smem(reinterpret_cast<const void *>(gated_tc_grad_kernel), grad_smem, done_grad));
   const long long hq = (long long)p.B * p.Hq, hkv = (long long)p.B * p.Hkv;
-  CUtensorMap tmQ, tmK, tmV, tmO, tmDQ, tmDK, tmDV;
+  CUtensorMap tmQ, tmK, tmV, tmO, tmDQ;
   GATED_TRY(make_map(&tmQ, p.Q, p.T, hq));
   GATED_TRY(make_map(&tmK, p.K, p.T, hkv));
   GATED_TRY(make_map(&tmV, p.V, p.T, hkv));
   GATED_TRY(make_map(&tmO, p.dY, p.T, hq));
   GATED_TRY(make_map(&tmDQ, p.dQ, p.T, hq, 32));
-  GATED_TRY(make_map(&tmDK, p.dK, p.T, hkv, 32));
-  GATED_TRY(make_map(&tmDV, p.dV, p.T, hkv, 32));
   const int total = p.nseg * p.B * p.Hkv;
   launch_pdl(gated_tc_own_kernel, dim3(total, 2), dim3(kOwnThreads), own_smem, stream, tmQ, tmK, tmV, tmO, p);
   GATED_TRY(oal_after_launch("gated_tc_own_kernel", stream));
   launch_pdl(gated_tc_scan_kernel, dim3(p.B * p.Hkv, kGS / 4 / kScanThreads, 2), dim3(kScanThreads), 0, stream, p);
   GATED_TRY(oal_after_launch("gated_tc_scan_kernel", stream));
   launch_pdl(gated_tc_grad_kernel, dim3(std::min(total, 2 * 152)), dim3(kGradThreads), grad_smem, stream, tmQ, tmK, tmV,
-             tmO, tmDQ, tmDK, tmDV, p);
+             tmO, tmDQ, p);
   return oal_after_launch("gated_tc_grad_kernel", stream);
 }
 
