@@ -116,7 +116,7 @@ struct OutSmem {
   ChunkGates gates[2];                   // by the issuing warp
   uint64_t kv_full[2], q_full[2], gate_full, x_full, d_full, p_full, y_full, go, meet, drain;
   uint32_t tmem;
-  int abort_flag;
+  WaitState wait;
 };
 static_assert(3 * (sizeof(OutSmem) + 2 * 1024) <= 228 * 1024, "three blocks per SM");
 
@@ -164,7 +164,8 @@ gated_tc_out_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
   const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
   const int rho = p.Hq / p.Hkv, npair = (rho + 1) / 2;
   if (tid == 0) {
-    s.abort_flag = 0;
+    s.wait.abort = 0;
+    s.wait.status = p.status;
     for (int i = 0; i < 2; ++i) mbar_init(&s.kv_full[i], 1), mbar_init(&s.q_full[i], 1);
     mbar_init(&s.gate_full, 1);
     mbar_init(&s.x_full, 1);
@@ -189,7 +190,6 @@ gated_tc_out_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
   const uint32_t tb = uniform(s.tmem);
   const int c0 = seg * p.seg_chunks, nc = max(0, min((n + kGC - 1) / kGC - c0, p.seg_chunks));
   const int steps = nc * npair;              // step it: chunk it / npair, heads 2 (it % npair), + 1
-  volatile int *abort_flag = &s.abort_flag;
   const int h0 = b * p.Hq + kv * rho;
   // rows behind a sequence that ends before T must stay: its last tile is
   // stored row by row instead of by TMA (which drops rows from T on)
@@ -221,8 +221,8 @@ gated_tc_out_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
     // X of step it, while the step before writes its outputs
     auto issue_x = [&](int it) {
       const int c = it / npair;
-      if (!warp_wait(&s.q_full[it & 1], (it >> 1) & 1, abort_flag, p.status) ||
-          !warp_wait(&s.kv_full[c & 1], (c >> 1) & 1, abort_flag, p.status))
+      if (!warp_wait(&s.q_full[it & 1], (it >> 1) & 1, &s.wait) ||
+          !warp_wait(&s.kv_full[c & 1], (c >> 1) & 1, &s.wait))
         return false;
       const uint64_t qd = sdesc_sw128(smem_u32(s.q[it & 1]), 16, 1024);
       const uint64_t kd = sdesc_sw128(smem_u32(s.k[c & 1]), 16, 1024);
@@ -243,11 +243,12 @@ gated_tc_out_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
     __syncwarp();
     if (nc > 0) make_gates(0);
     bool ok = steps == 0 || issue_x(0);
+#pragma unroll 1
     for (int it = 0; it < steps && ok; ++it) {
       const int c = it / npair, pr = it % npair;
       // the step before is done: its D is read, its outputs and (a new chunk)
       // the state are in shared memory
-      ok = warp_wait(&s.go, it & 1, abort_flag, p.status);
+      ok = warp_wait(&s.go, it & 1, &s.wait);
       if (!ok) break;
       tc_fence_after();
       const uint64_t qd = sdesc_sw128(smem_u32(s.q[it & 1]), 16, 1024);
@@ -260,7 +261,7 @@ gated_tc_out_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
         if (it + 2 < steps) prefetch_q(it + 2);
       }
       __syncwarp();
-      ok = warp_wait(&s.p_full, it & 1, abort_flag, p.status);
+      ok = warp_wait(&s.p_full, it & 1, &s.wait);
       if (!ok) break;
       tc_fence_after();
 #pragma unroll
@@ -270,7 +271,7 @@ gated_tc_out_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
       if (lane == 0 && it > 0 && it + 1 < steps) load_q(it + 1), ++q_loads;
       __syncwarp();
       // P, which lies in X, has been read
-      if (it + 1 < steps) ok = warp_wait(&s.y_full, it & 1, abort_flag, p.status) && issue_x(it + 1);
+      if (it + 1 < steps) ok = warp_wait(&s.y_full, it & 1, &s.wait) && issue_x(it + 1);
       if (pr == 0 && c + 1 < nc) make_gates(c + 1);
     }
     umma_commit_warp(&s.drain);
@@ -299,22 +300,23 @@ gated_tc_out_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
     auto meet = [&]() {
       __syncwarp();
       if (lane == 0) mbar_arrive(&s.meet);
-      return warp_wait(&s.meet, met++ & 1, abort_flag, p.status);
+      return warp_wait(&s.meet, met++ & 1, &s.wait);
     };
+#pragma unroll 1
     for (int it = 0; it < steps && ok; ++it) {
       const int c = it / npair, pr = it % npair, t0 = (c0 + c) * kGC;
       const ChunkGates &gates = s.gates[c & 1];
       if (pr == 0) {
-        ok = warp_wait(&s.gate_full, c & 1, abort_flag, p.status);
+        ok = warp_wait(&s.gate_full, c & 1, &s.wait);
         if (!ok) break;
         mode = gates.mode;
         row = mode == kEach ? p.scale : p.scale * gates.row[i];
         begin = 0;
         into = half && mode == kHalves ? gates.first : 1.f;
         if (cut_before(gates, i, begin)) into = 0.f;     // keys from the row's last cut gate on, nothing from S_in
-        ok = warp_wait(&s.kv_full[c & 1], (c >> 1) & 1, abort_flag, p.status);
+        ok = warp_wait(&s.kv_full[c & 1], (c >> 1) & 1, &s.wait);
       }
-      ok = ok && warp_wait(&s.x_full, it & 1, abort_flag, p.status);
+      ok = ok && warp_wait(&s.x_full, it & 1, &s.wait);
       if (!ok) break;
       tc_fence_after();
       if (pr == 0 && t0 + kGC > n) {                     // rows behind the sequence count as zeros
@@ -370,13 +372,13 @@ gated_tc_out_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
           tmem_st16(tm + kColX + 16, pk);
         }
       } else {
-        ok = warp_wait(&s.d_full, it & 1, abort_flag, p.status);
+        ok = warp_wait(&s.d_full, it & 1, &s.wait);
         if (!ok) break;
         tc_fence_after();
         slow_scores(p.g + (size_t)bh * p.T, t0, n, i, tm);
       }
       if (mode == kHalves) {
-        ok = warp_wait(&s.d_full, it & 1, abort_flag, p.status);
+        ok = warp_wait(&s.d_full, it & 1, &s.wait);
         if (!ok) break;
         tc_fence_after();
 #pragma unroll 1
@@ -403,11 +405,11 @@ gated_tc_out_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
       }
       if (pr == npair - 1) {
         state_add<2, 4>(acc, 0, s.k[c & 1], s.v[c & 1], gates.tail);
-        ok = warp_wait(&s.d_full, it & 1, abort_flag, p.status);   // the chunk's last Q S_in is done
+        ok = warp_wait(&s.d_full, it & 1, &s.wait);   // the chunk's last Q S_in is done
         if (!ok) break;
         state_round(acc, 0, s.state);
       }
-      ok = warp_wait(&s.y_full, it & 1, abort_flag, p.status);
+      ok = warp_wait(&s.y_full, it & 1, &s.wait);
       if (!ok) break;
       tc_fence_after();
       const int hd = 2 * pr + (warp >> 1);

@@ -51,16 +51,22 @@ __device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
+// What every wait of a block shares, in shared memory.
+struct WaitState {
+  int *status;                            // the device status word
+  int abort;                              // a wait gave up: the others give up too
+};
 // The rest of a wait that did not end at once (out of line: these kernels'
 // instructions barely fit the caches).  Bounded like mbar_wait.
-static __device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile int *abort, int *status) {
+static __device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, WaitState *w) {
   const uint64_t t0 = cycles_now();
+  volatile int *abort = &w->abort;
   while (!try_wait(bar, parity)) {
     if (*abort) return false;
     const uint64_t el = cycles_now() - t0;
-    if (el > kWaitFloorCycles && el > wait_limit(status)) {
+    if (el > kWaitFloorCycles && el > wait_limit(w->status)) {
       *abort = 1;
-      if (status) atomicCAS(status, 0, 4 /* OAL_ERR_TIMEOUT */);
+      atomicCAS(w->status, 0, 4 /* OAL_ERR_TIMEOUT */);
       return false;
     }
   }
@@ -68,9 +74,9 @@ static __device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, volat
 }
 // A wait by a whole warp, whose lanes agree on the outcome (the tensor-memory
 // instructions that follow want all of them).
-__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort, int *status) {
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, WaitState *w) {
   bool ok = try_wait(smem_u32(bar), parity);
-  if (!ok) ok = wait_on(smem_u32(bar), parity, abort, status);
+  if (!ok) ok = wait_on(smem_u32(bar), parity, w);
   return __all_sync(0xffffffffu, ok);
 }
 // The first 1024-byte boundary of the dynamic shared memory.  (By an offset: a
@@ -123,7 +129,7 @@ __device__ __forceinline__ bool cut_before(const ChunkGates &gates, int i, int &
 }
 
 // Rows from `rows` on of a tile become zeros; thread `at` of `threads`.
-__device__ __forceinline__ void clear_rows(void *tile, int rows, int at, int threads) {
+static __device__ __noinline__ void clear_rows(void *tile, int rows, int at, int threads) {
   for (int x = at; x < 64 * 8; x += threads)
     if ((x >> 3) >= rows) reinterpret_cast<uint4 *>(tile)[x] = make_uint4(0u, 0u, 0u, 0u);
 }

@@ -151,6 +151,26 @@ __global__ void __launch_bounds__(kScanThreads) gated_tc_scan_kernel(GatedArgs p
 
 // ---------------------------------------------------------------- gradients
 
+// Factors f of keys j0 .. j0 + 7 of the chunk for row i by themselves, where
+// `on` has a bit, into two places (a chunk whose gates drop too far for factors; out of line,
+// as its instructions would push the others out of the cache).
+__device__ __noinline__ void each_decay(const float *g, int t0, int n, int i, int j0, uint32_t on, float scale, float4 *to0,
+                                        float4 *to1) {
+  const GateLane s = gate_sums(gate_load(g, t0, n));
+  const float h0 = __shfl_sync(0xffffffffu, s.hi[0], i >> 1), h1 = __shfl_sync(0xffffffffu, s.hi[1], i >> 1);
+  const float l0 = __shfl_sync(0xffffffffu, s.lo[0], i >> 1), l1 = __shfl_sync(0xffffffffu, s.lo[1], i >> 1);
+  const float hi = i & 1 ? h1 : h0, lo = i & 1 ? l1 : l0;
+  float f[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const int from = (j0 + e) >> 1;
+    const float hj = __shfl_sync(0xffffffffu, s.hi[e & 1], from), lj = __shfl_sync(0xffffffffu, s.lo[e & 1], from);
+    f[e] = scale * gate_exp_fast(on & (1u << e), (hi - hj) + (lo - lj));
+  }
+  *to0 = make_float4(f[0], f[1], f[2], f[3]);
+  *to1 = make_float4(f[4], f[5], f[6], f[7]);
+}
+
 constexpr int kGradThreads = 320;              // eight computing warps, one for the MMAs, one for loads and gates
 constexpr uint32_t kGradCols = 256;
 struct GradSmem {
@@ -168,9 +188,55 @@ struct GradSmem {
   uint64_t kv_full, r_full, gate_full, far_full, q_full, clean, go, xz_full, pz_full, dq_full, p_free, pair[4], meet,
       chunk_done[2], drain;
   uint32_t tmem;
-  int abort_flag;
+  WaitState wait;
 };
 static_assert(2 * (sizeof(GradSmem) + 2 * 1024) <= 228 * 1024, "two blocks per SM");
+
+// dg of a chunk from its parts (one warp, two tokens a lane).
+__device__ __noinline__ void chunk_dg(const GradSmem::Sums &u, const ChunkGates &gates, float *dg, int rows) {
+  const int lane = threadIdx.x & 31;
+  float x = 0.f, r[2], f[2];
+#pragma unroll
+  for (int z = 0; z < 8; ++z) x += u.dots[z];
+  x *= gates.whole;
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const int t = 2 * lane + e;
+    r[e] = (u.rows[0][t] + u.rows[1][t]) + (u.rows[0][64 + t] + u.rows[1][64 + t]) -
+           ((u.cols[0][t] + u.cols[1][t]) + (u.cols[2][t] + u.cols[3][t]));
+    f[e] = u.far[0][t] + u.far[1][t];
+  }
+  float down = r[0] + r[1], up = f[0] + f[1];              // sums from this lane on; up to it
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const float a = __shfl_down_sync(0xffffffffu, down, d), v = __shfl_up_sync(0xffffffffu, up, d);
+    if (lane + d < 32) down += a;
+    if (lane >= d) up += v;
+  }
+  up = __shfl_up_sync(0xffffffffu, up, 1);
+  if (lane == 0) up = 0.f;
+  float after = __shfl_down_sync(0xffffffffu, down, 1);
+  if (lane == 31) after = 0.f;
+  const float d0 = x + (after + r[1] + r[0]) + up, d1 = x + (after + r[1]) + (up + f[0]);
+  if (2 * lane < rows) dg[2 * lane] = gates.cut_even >> lane & 1u ? 0.f : d0;
+  if (2 * lane + 1 < rows) dg[2 * lane + 1] = gates.cut_odd >> lane & 1u ? 0.f : d1;
+}
+
+// dY and Q of heads head .. head + heads - 1 into their tiles, or (to null) into L2.
+__device__ __noinline__ void fetch_heads(const CUtensorMap *tmO, const CUtensorMap *tmQ, uint8_t *to, uint64_t *bar, int t0,
+                                         int head, int heads) {
+  if (to) mbar_arrive_expect_tx(bar, 2 * heads * kTileBytes);
+#pragma unroll 1
+  for (int h = 0; h < heads; ++h) {
+    if (to) {
+      tma_load_3d(to + h * kTileBytes, tmO, bar, 0, t0, head + h);
+      tma_load_3d(to + (2 + h) * kTileBytes, tmQ, bar, 0, t0, head + h);
+    } else {
+      tma_prefetch_3d(tmO, 0, t0, head + h);
+      tma_prefetch_3d(tmQ, 0, t0, head + h);
+    }
+  }
+}
 
 __global__ void __launch_bounds__(kGradThreads, 2)
 gated_tc_grad_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -182,7 +248,8 @@ gated_tc_grad_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
   const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
   const int rho = p.Hq / p.Hkv, npair = (rho + 1) / 2;
   if (tid == 0) {
-    s.abort_flag = 0;
+    s.wait.abort = 0;
+    s.wait.status = p.status;
     mbar_init(&s.kv_full, 1), mbar_init(&s.r_full, 1), mbar_init(&s.gate_full, 1), mbar_init(&s.far_full, 1);
     mbar_init(&s.q_full, 1), mbar_init(&s.clean, 8), mbar_init(&s.go, 8), mbar_init(&s.xz_full, 1);
     mbar_init(&s.pz_full, 8), mbar_init(&s.dq_full, 1), mbar_init(&s.p_free, 4), mbar_init(&s.meet, 8);
@@ -199,13 +266,25 @@ gated_tc_grad_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
   __syncthreads();
   tc_fence_after();
   const uint32_t tb = uniform(s.tmem), tx = tb, tz = tb + 64, tkv = tb + 128;
-  volatile int *abort_flag = &s.abort_flag;
-  auto wait = [&](uint64_t *bar, int phase) { return warp_wait(bar, phase & 1, abort_flag, p.status); };
+  auto wait = [&](uint64_t *bar, int phase) { return warp_wait(bar, phase & 1, &s.wait); };
   auto arrive = [&](uint64_t *bar) {
     __syncwarp();
     if (lane == 0) mbar_arrive(bar);
   };
-  const int total = p.nseg * p.B * p.Hkv;
+  // The block's chunks: every gridDim.x-th of (batch, KV head, chunk), the last
+  // fastest, counted up digit by digit (a division costs more than the rest).
+  struct Place {
+    int b, kv, c;
+  };
+  const int per = p.nseg * p.Hkv;
+  const Place by = {(int)gridDim.x / per, (int)gridDim.x % per / p.nseg, (int)gridDim.x % p.nseg};
+  auto next_of = [&](Place x) {
+    x.c += by.c, x.kv += by.kv, x.b += by.b;
+    if (x.c >= p.nseg) x.c -= p.nseg, ++x.kv;
+    if (x.kv >= p.Hkv) x.kv -= p.Hkv, ++x.b;
+    return x;
+  };
+  const Place begin_at = {(int)blockIdx.x / per, (int)blockIdx.x % per / p.nseg, (int)blockIdx.x % p.nseg};
   bool ok = true;
   // All sides count alike: k chunks, it steps (a chunk's pairs of heads), cl
   // cleanings.  Every barrier completes once per what it counts, and whoever
@@ -219,66 +298,32 @@ gated_tc_grad_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
   if (warp == 9) {
     // ---- loads and gates, ahead of the rest; dg behind it
     auto load_q = [&](int t0, int h0, int pr) {
-      const int heads = min(2, rho - 2 * pr);
-      mbar_arrive_expect_tx(&s.q_full, 2 * heads * kTileBytes);
-      for (int h = 0; h < heads; ++h) {
-        tma_load_3d(s.oq + h * kTileBytes, &tmO, &s.q_full, 0, t0, h0 + 2 * pr + h);
-        tma_load_3d(s.oq + (2 + h) * kTileBytes, &tmQ, &s.q_full, 0, t0, h0 + 2 * pr + h);
-      }
+      fetch_heads(&tmO, &tmQ, s.oq, &s.q_full, t0, h0 + 2 * pr, min(2, rho - 2 * pr));
     };
     auto prefetch_q = [&](int t0, int h0, int pr) {
-      for (int h = 2 * pr; h < min(2 * pr + 2, rho); ++h) {
-        tma_prefetch_3d(&tmO, 0, t0, h0 + h);
-        tma_prefetch_3d(&tmQ, 0, t0, h0 + h);
-      }
+      fetch_heads(&tmO, &tmQ, nullptr, nullptr, t0, h0 + 2 * pr, min(2, rho - 2 * pr));
     };
     // dg of the chunk before: its parts are there once all warps are done with it
     float *dg = nullptr;
     int dg_rows = 0;
     auto finish = [&]() {
       if (!wait(&s.chunk_done[(k - 1) & 1], (k - 1) >> 1)) return false;
-      const GradSmem::Sums &u = s.sums[(k - 1) & 1];
-      const ChunkGates &gates = s.gates[(k - 1) & 1].c;
-      float x = 0.f, r[2], f[2];
-#pragma unroll
-      for (int z = 0; z < 8; ++z) x += u.dots[z];
-      x *= gates.whole;
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int t = 2 * lane + e;
-        r[e] = (u.rows[0][t] + u.rows[1][t]) + (u.rows[0][64 + t] + u.rows[1][64 + t]) -
-               ((u.cols[0][t] + u.cols[1][t]) + (u.cols[2][t] + u.cols[3][t]));
-        f[e] = u.far[0][t] + u.far[1][t];
-      }
-      float down = r[0] + r[1], up = f[0] + f[1];              // sums from this lane on; up to it
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const float a = __shfl_down_sync(0xffffffffu, down, d), v = __shfl_up_sync(0xffffffffu, up, d);
-        if (lane + d < 32) down += a;
-        if (lane >= d) up += v;
-      }
-      up = __shfl_up_sync(0xffffffffu, up, 1);
-      if (lane == 0) up = 0.f;
-      float after = __shfl_down_sync(0xffffffffu, down, 1);
-      if (lane == 31) after = 0.f;
-      const float d0 = x + (after + r[1] + r[0]) + up, d1 = x + (after + r[1]) + (up + f[0]);
-      if (2 * lane < dg_rows) dg[2 * lane] = gates.cut_even >> lane & 1u ? 0.f : d0;
-      if (2 * lane + 1 < dg_rows) dg[2 * lane + 1] = gates.cut_odd >> lane & 1u ? 0.f : d1;
+      chunk_dg(s.sums[(k - 1) & 1], s.gates[(k - 1) & 1].c, dg, dg_rows);
       return true;
     };
     int q_loads = 0;
-    for (int idx = blockIdx.x; idx < total && ok; idx += gridDim.x) {
-      const int bh = idx / p.nseg, c = idx % p.nseg, b = bh / p.Hkv, kv = bh % p.Hkv, t0 = c * kGC;
-      const int n = gated_len(p, b), h0 = b * p.Hq + kv * rho;
+#pragma unroll 1
+    for (Place x = begin_at; x.b < p.B && ok; x = next_of(x)) {
+      const int bh = x.b * p.Hkv + x.kv, t0 = x.c * kGC, n = gated_len(p, x.b), h0 = x.b * p.Hq + x.kv * rho;
       if (t0 >= n) continue;
       // the last step's MMAs have read K, V, S, z and the pair of heads (waited for below)
       if (lane == 0) {
         mbar_arrive_expect_tx(&s.kv_full, 4 * kTileBytes);
         tma_load_3d(s.kv, &tmK, &s.kv_full, 0, t0, bh);
         tma_load_3d(s.kv + kTileBytes, &tmV, &s.kv_full, 0, t0, bh);
-        bulk_load(s.st, p.state_tiles + (size_t)idx * 2 * kTileBytes, 2 * kTileBytes, &s.kv_full);
+        bulk_load(s.st, p.state_tiles + ((size_t)bh * p.nseg + x.c) * 2 * kTileBytes, 2 * kTileBytes, &s.kv_full);
         mbar_arrive_expect_tx(&s.r_full, 2 * kTileBytes);
-        bulk_load(s.pz + 2 * kTileBytes, p.grad_tiles + (size_t)idx * 2 * kTileBytes, 2 * kTileBytes, &s.r_full);
+        bulk_load(s.pz + 2 * kTileBytes, p.grad_tiles + ((size_t)bh * p.nseg + x.c) * 2 * kTileBytes, 2 * kTileBytes, &s.r_full);
         load_q(t0, h0, 0), ++q_loads;
         if (npair > 1) prefetch_q(t0, h0, 1);
       }
@@ -301,17 +346,19 @@ gated_tc_grad_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
       dg = p.dg + (size_t)bh * p.T + t0;
       dg_rows = n - t0;
       ++k;
+#pragma unroll 1
       for (int pr = 0; pr < npair && ok; ++pr, ++it) {
         if (lane == 0) {
           if (pr + 2 < npair) prefetch_q(t0, h0, pr + 2);
-          const int next = idx + gridDim.x;
-          if (pr == npair - 1 && next < total) {
-            const int nbh = next / p.nseg, nt = (next % p.nseg) * kGC;
-            tma_prefetch_3d(&tmK, 0, nt, nbh);
-            tma_prefetch_3d(&tmV, 0, nt, nbh);
-            prefetch_l2(p.state_tiles + (size_t)next * 2 * kTileBytes, 2 * kTileBytes);
-            prefetch_l2(p.grad_tiles + (size_t)next * 2 * kTileBytes, 2 * kTileBytes);
-            prefetch_q(nt, (nbh / p.Hkv) * p.Hq + (nbh % p.Hkv) * rho, 0);
+          const Place y = next_of(x);
+          if (pr == npair - 1 && y.b < p.B) {
+            const int nbh = y.b * p.Hkv + y.kv;
+            const size_t tiles = ((size_t)nbh * p.nseg + y.c) * 2 * kTileBytes;
+            tma_prefetch_3d(&tmK, 0, y.c * kGC, nbh);
+            tma_prefetch_3d(&tmV, 0, y.c * kGC, nbh);
+            prefetch_l2(p.state_tiles + tiles, 2 * kTileBytes);
+            prefetch_l2(p.grad_tiles + tiles, 2 * kTileBytes);
+            prefetch_q(y.c * kGC, y.b * p.Hq + y.kv * rho, 0);
           }
         }
         __syncwarp();
@@ -341,11 +388,13 @@ gated_tc_grad_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
     // [p | z] and [dY | Q]: two 64-column atoms, 16 KB apart
     const uint64_t pzd = sdesc_sw128(smem_u32(s.pz), 2 * kTileBytes, 1024);
     const uint64_t oqd = sdesc_sw128(smem_u32(s.oq), 2 * kTileBytes, 1024);
-    for (int idx = blockIdx.x; idx < total && ok; idx += gridDim.x) {
-      const int t0 = (idx % p.nseg) * kGC, n = gated_len(p, idx / p.nseg / p.Hkv);
+#pragma unroll 1
+    for (Place x = begin_at; x.b < p.B && ok; x = next_of(x)) {
+      const int t0 = x.c * kGC, n = gated_len(p, x.b);
       if (t0 >= n) continue;
       const bool tail = t0 + kGC > n && n < p.T;
       ok = wait(&s.kv_full, k);
+#pragma unroll 1
       for (int pr = 0; pr < npair && ok; ++pr) {
         ok = wait(&s.q_full, it);
         if (ok && cleans(pr, tail)) ok = wait(&s.clean, cl++);
@@ -398,9 +447,9 @@ gated_tc_grad_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
     const uint32_t lanes = (uint32_t)(32 * quad) << 16;
     int met = 0, paired = 0;
     arrive(&s.go);
-    for (int idx = blockIdx.x; idx < total && ok; idx += gridDim.x) {
-      const int bh = idx / p.nseg, c = idx % p.nseg, b = bh / p.Hkv, kv = bh % p.Hkv, t0 = c * kGC;
-      const int n = gated_len(p, b), h0 = b * p.Hq + kv * rho;
+#pragma unroll 1
+    for (Place x = begin_at; x.b < p.B && ok; x = next_of(x)) {
+      const int bh = x.b * p.Hkv + x.kv, t0 = x.c * kGC, n = gated_len(p, x.b), h0 = x.b * p.Hq + x.kv * rho;
       if (t0 >= n) continue;
       const bool tail = t0 + kGC > n && n < p.T;
       const GradSmem::Gates &gates = s.gates[k & 1];
@@ -432,7 +481,7 @@ gated_tc_grad_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
         // <S, R>: all four tiles hold an element at the same place
         const uint32_t *a = reinterpret_cast<const uint32_t *>(s.st), *r = reinterpret_cast<const uint32_t *>(s.pz + 2 * kTileBytes);
         float dot = 0.f;
-#pragma unroll
+#pragma unroll 2
         for (int z = 0; z < 8; ++z) {
           const int x = tid + 256 * z;
           const uint32_t ah = a[x], al = a[x + kTileBytes / 4], gh = r[x], gl = r[x + kTileBytes / 4];
@@ -450,7 +499,7 @@ gated_tc_grad_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
         tc_fence_after();
         const float tj = gates.tail[i];
         const uint32_t from = tkv + (quad & 2 ? 64u : 0u) + 32u * hf + lanes;
-#pragma unroll
+#pragma unroll 1
         for (int h = 0; h < 2; ++h) {
           uint32_t x[16];
           tmem_ld16(from + 16 * h, x);
@@ -485,12 +534,10 @@ gated_tc_grad_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
       cut_before(gates.c, i, begin);
       const uint32_t live = 0xFFFFFFFFu << min(31, max(0, begin - 32 * hf));
       const uint32_t mask = own ? live & (0xFFFFFFFFu >> (31 - lane)) : pre && begin < 32 ? live : 0u;
-      const uint32_t strict = own ? mask & ~(1u << lane) : mask;
-      GateLane es;
-      if (mode == kEach) es = gate_sums(gate_load(p.g + (size_t)bh * p.T, t0, n));
       float w[32], racc = 0.f;
 #pragma unroll
       for (int e = 0; e < 32; ++e) w[e] = 0.f;
+#pragma unroll 1
       for (int pr = 0; pr < npair; ++pr) {
         ok = wait(&s.q_full, it);
         if (!ok) break;
@@ -503,6 +550,12 @@ gated_tc_grad_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
           if (!ok) break;
         }
         if (own || pre) {
+          if (mode == kEach)   // the factors lie where their p and z will
+#pragma unroll 1
+            for (int h = 0; h < 4; ++h)
+              each_decay(p.g + (size_t)bh * p.T, t0, n, i, 32 * hf + 8 * h, mask >> (8 * h), p.scale,
+                         reinterpret_cast<float4 *>(s.pz + tile_at(m, 4 * hf + h)),
+                         reinterpret_cast<float4 *>(s.pz + 2 * kTileBytes + tile_at(m, 4 * hf + h)));
 #pragma unroll
           for (int h = 0; h < 4; ++h) {
             uint32_t x[8], y[8];
@@ -516,14 +569,10 @@ gated_tc_grad_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
                 f[e] = fr * r.x, f[e + 1] = fr * r.y, f[e + 2] = fr * r.z, f[e + 3] = fr * r.w;
               }
             } else {
-              const float ih = __shfl_sync(0xffffffffu, es.hi[0], i >> 1), ih1 = __shfl_sync(0xffffffffu, es.hi[1], i >> 1);
-              const float il = __shfl_sync(0xffffffffu, es.lo[0], i >> 1), il1 = __shfl_sync(0xffffffffu, es.lo[1], i >> 1);
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const int from = 16 * hf + 4 * h + (e >> 1);
-                const float hj = __shfl_sync(0xffffffffu, es.hi[e & 1], from), lj = __shfl_sync(0xffffffffu, es.lo[e & 1], from);
-                f[e] = p.scale * gate_exp_fast(mask & (1u << (8 * h + e)), ((i & 1 ? ih1 : ih) - hj) + ((i & 1 ? il1 : il) - lj));
-              }
+              const float4 r0 = *reinterpret_cast<const float4 *>(s.pz + tile_at(m, 4 * hf + h));
+              const float4 r1 = *reinterpret_cast<const float4 *>(s.pz + 2 * kTileBytes + tile_at(m, 4 * hf + h));
+              f[0] = r0.x, f[1] = r0.y, f[2] = r0.z, f[3] = r0.w;
+              f[4] = r1.x, f[5] = r1.y, f[6] = r1.z, f[7] = r1.w;
             }
             tmem_wait_ld();
             uint32_t pw[4], zw[4];
@@ -533,10 +582,10 @@ gated_tc_grad_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
 #pragma unroll
               for (int d = 0; d < 2; ++d) {
                 const int j = 8 * h + e + d;
-                const float xv = __uint_as_float(x[e + d]);
-                zv[d] = mask & (1u << j) ? f[e + d] * __uint_as_float(y[e + d]) : 0.f;
-                pv[d] = mask & (1u << j) ? f[e + d] * xv : 0.f;
-                w[j] = fmaf(strict & (1u << j) ? xv : 0.f, zv[d], w[j]);
+                const float fv = mask & (1u << j) ? f[e + d] : 0.f, xv = __uint_as_float(x[e + d]);
+                zv[d] = fv * __uint_as_float(y[e + d]);
+                pv[d] = fv * xv;
+                w[j] = fmaf(xv, zv[d], w[j]);
               }
               pw[e >> 1] = pack_bf16x2(pv[0], pv[1]);
               zw[e >> 1] = pack_bf16x2(zv[0], zv[1]);
@@ -563,7 +612,7 @@ gated_tc_grad_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
         ++it;
         const int hd = 2 * pr + (m >> 6);
         uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.dQ) + ((size_t)(h0 + hd) * p.T + t0 + i) * 64) + 4 * hf;
-#pragma unroll
+#pragma unroll 1
         for (int h = 0; h < 2; ++h) {
           uint32_t x[16], y[16];
           tmem_ld16(tx + lanes + 32 * hf + 16 * h, x);
@@ -571,7 +620,7 @@ gated_tc_grad_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
           tmem_wait_ld();
 #pragma unroll
           for (int z = 0; z < 2; ++z) {
-            const uint4 qq = q[2 * h + z];
+            const uint4 qq = q[z];
             const uint32_t u[4] = {qq.x, qq.y, qq.z, qq.w};
             uint32_t o[4];
 #pragma unroll
@@ -585,6 +634,7 @@ gated_tc_grad_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
             if (!tail) *reinterpret_cast<uint4 *>(s.pz + tile_at(m, 4 * hf + 2 * h + z)) = out;   // p has been read
             else if (hd < rho && t0 + i < n) dst[2 * h + z] = out;
           }
+          q[0] = q[2], q[1] = q[3];
         }
         fence_proxy_async();
         tc_fence_before();
@@ -609,7 +659,7 @@ gated_tc_grad_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
       {
         const uint32_t from = tkv + (quad & 2 ? 64u : 0u) + 32u * hf + lanes;
         uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(quad & 2 ? p.dK : p.dV) + ((size_t)bh * p.T + t0 + i) * 64) + 4 * hf;
-#pragma unroll
+#pragma unroll 1
         for (int h = 0; h < 2; ++h) {
           uint32_t x[16];
           tmem_ld16(from + 16 * h, x);
@@ -627,7 +677,10 @@ gated_tc_grad_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
         tc_fence_before();
         float sum = racc;
 #pragma unroll
-        for (int e = 0; e < 32; ++e) sum += w[e];
+        for (int e = 0; e < 32; ++e) {
+          w[e] = own && e == lane ? 0.f : w[e];                // a token's own pair decays by nothing
+          sum += w[e];
+        }
         sums.rows[hf][m] = sum;
         // lane l ends with the sum over the warp's rows of column l
 #pragma unroll
