@@ -43,7 +43,6 @@ struct GatedArgs {
 
 // Segment sizes in chunks (gated_simt.cu), and how many of them T tokens have.
 int gated_prefill_segment(int B, int Hkv, int T, int is_bf16);
-int gated_backward_segment(int is_bf16);
 inline int gated_segments(int T, int seg_chunks) {
   const int chunks = (int)(((long long)T + kGC - 1) / kGC);
   return (chunks + seg_chunks - 1) / seg_chunks;
@@ -153,22 +152,64 @@ __device__ __forceinline__ float gate_tail(const GateSums &s, int j) {
   return gate_pair(s, kGC - 1, j);
 }
 
-// Eight elements of a row as fp32.
-__device__ __forceinline__ void gated_load8(const __nv_bfloat16 *p, float (&o)[8]) {
-  const uint4 w = __ldg(reinterpret_cast<const uint4 *>(p));
-  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    o[2 * e] = __uint_as_float(u[e] << 16);
-    o[2 * e + 1] = __uint_as_float(u[e] & 0xFFFF0000u);
+// The walk over a sequence's segments (chunks in the backward): a thread takes
+// kVec values of the state and has the loads of kAhead segments in flight,
+// which is all that hides the walk's own chain.  put(i, run) gets the value
+// before segment i (walking back: behind it).
+template <int kVec>
+struct ScanVec {
+  float v[kVec];
+};
+template <int kVec>
+__device__ __forceinline__ ScanVec<kVec> scan_load(const float *p) {
+  ScanVec<kVec> r;
+  if (kVec == 4) {
+    const float4 x = *reinterpret_cast<const float4 *>(p);
+    r.v[0] = x.x, r.v[1] = x.y, r.v[kVec - 2] = x.z, r.v[kVec - 1] = x.w;
+  } else {
+    const float2 x = *reinterpret_cast<const float2 *>(p);
+    r.v[0] = x.x, r.v[1] = x.y;
   }
+  return r;
 }
-__device__ __forceinline__ void gated_load8(const float *p, float (&o)[8]) {
-  const float4 a = __ldg(reinterpret_cast<const float4 *>(p));
-  const float4 b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
-  o[0] = a.x, o[1] = a.y, o[2] = a.z, o[3] = a.w;
-  o[4] = b.x, o[5] = b.y, o[6] = b.z, o[7] = b.w;
+template <int kVec>
+__device__ __forceinline__ void scan_store(float *p, const ScanVec<kVec> &r) {
+  if (kVec == 4) *reinterpret_cast<float4 *>(p) = make_float4(r.v[0], r.v[1], r.v[kVec - 2], r.v[kVec - 1]);
+  else *reinterpret_cast<float2 *>(p) = make_float2(r.v[0], r.v[1]);
 }
+// own: the thread's values of segment 0's own state; count segments, of which
+// the first `formed` in walking order have one; back: from the last to the first.
+template <int kVec, int kAhead, typename Put>
+__device__ __forceinline__ ScanVec<kVec> scan_walk(const float *own, const float *decay, const float *from, int count,
+                                                   int formed, bool back, Put put) {
+  ScanVec<kVec> run = {};
+  if (from) run = scan_load<kVec>(from);
+  for (int i0 = 0; i0 < count; i0 += kAhead) {
+    ScanVec<kVec> v[kAhead];
+    float f[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int i = back ? count - 1 - i0 - k : i0 + k;
+      v[k] = {};
+      f[k] = 0.f;
+      if (i0 + k < formed) v[k] = scan_load<kVec>(own + (size_t)i * kGS), f[k] = decay[i];
+    }
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+      if (i0 + k < count) {
+        put(back ? count - 1 - i0 - k : i0 + k, run);
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) run.v[e] = fmaf(f[k], run.v[e], v[k].v[e]);
+      }
+  }
+  return run;
+}
+// Few states and many segments: more threads a state and more loads ahead (205
+// segments of 2 states: 16 us against 22 with loads of 8 ahead); otherwise the
+// states' own number fills the GPU (64 chunks of 32 states, both ways: 22 us
+// against 27 the other way).
+inline bool scan_deep(int states, int segments) { return states <= 16 && segments > 16; }
+constexpr int kScanThreads = 128;
 
 }  // namespace oal
 

@@ -88,15 +88,17 @@ __device__ __forceinline__ void mm_tn(const float *A, const float *B, const floa
 }
 
 // Rows t0 .. t0 + 63 of a [T][64] matrix into a tile; rows from n on are 0.
-template <typename T>
-__device__ __forceinline__ void load_tile(const T *src, int t0, int n, float *tile) {
+__device__ __forceinline__ void load_tile(const float *src, int t0, int n, float *tile) {
+  float4 v[4];
 #pragma unroll
-  for (int it = 0; it < 2; ++it) {
-    const int x = threadIdx.x + it * kThreads, r = x >> 3, c = (x & 7) * 8;
-    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (t0 + r < n) gated_load8(src + (size_t)(t0 + r) * 64 + c, v);
-    *reinterpret_cast<float4 *>(tile + r * kP + c) = make_float4(v[0], v[1], v[2], v[3]);
-    *reinterpret_cast<float4 *>(tile + r * kP + c + 4) = make_float4(v[4], v[5], v[6], v[7]);
+  for (int it = 0; it < 4; ++it) {
+    const int x = threadIdx.x + it * kThreads, r = x >> 4, c = (x & 15) * 4;
+    v[it] = t0 + r < n ? __ldg(reinterpret_cast<const float4 *>(src + (size_t)(t0 + r) * 64 + c)) : make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+#pragma unroll
+  for (int it = 0; it < 4; ++it) {
+    const int x = threadIdx.x + it * kThreads, r = x >> 4, c = (x & 15) * 4;
+    *reinterpret_cast<float4 *>(tile + r * kP + c) = v[it];
   }
 }
 __device__ __forceinline__ void load_state(const float *src, float *tile) {
@@ -113,14 +115,13 @@ __device__ __forceinline__ void put(const Acc &a, int ty, int tx, float *tile) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) tile[(4 * ty + i) * kP + tx + 16 * j] = a.v[i][j];
 }
-template <typename T>
-__device__ __forceinline__ void store_rows(const Acc &a, int ty, int tx, T *dst, int t0, int n) {
+__device__ __forceinline__ void store_rows(const Acc &a, int ty, int tx, float *dst, int t0, int n) {
 #pragma unroll
   for (int i = 0; i < 4; ++i)
     if (t0 + 4 * ty + i < n)
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        dst[(size_t)(t0 + 4 * ty + i) * 64 + tx + 16 * j] = from_f32<T>(a.v[i][j]);
+        dst[(size_t)(t0 + 4 * ty + i) * 64 + tx + 16 * j] = a.v[i][j];
 }
 
 // The decays of a chunk that every thread reads.
@@ -142,7 +143,6 @@ __device__ __forceinline__ void chunk_decays(const float *g, int t0, int n, Deca
 // backward, own gradient of the state before each segment but the first
 // (y = 1):  sum_i e^{G_i} scale q_i dy_i^T over the segment's tokens and the
 // query heads of the KV head.
-template <typename T>
 __global__ void __launch_bounds__(kThreads) gated_segment_kernel(GatedArgs p) {
   pdl_trigger();
   pdl_wait();
@@ -171,8 +171,8 @@ __global__ void __launch_bounds__(kThreads) gated_segment_kernel(GatedArgs p) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) acc.v[i][j] *= whole;
     if (!grad) {
-      load_tile(static_cast<const T *>(p.K) + (size_t)bh * p.T * 64, t0, n, A);
-      load_tile(static_cast<const T *>(p.V) + (size_t)bh * p.T * 64, t0, n, B);
+      load_tile(static_cast<const float *>(p.K) + (size_t)bh * p.T * 64, t0, n, A);
+      load_tile(static_cast<const float *>(p.V) + (size_t)bh * p.T * 64, t0, n, B);
       __syncthreads();
       mm_tn(A, B, dec.tail, ty, tx, acc);
     } else {
@@ -180,8 +180,8 @@ __global__ void __launch_bounds__(kThreads) gated_segment_kernel(GatedArgs p) {
       for (int r = 0; r < rho; ++r) {
         const size_t row = ((size_t)b * p.Hq + kv * rho + r) * p.T * 64;
         __syncthreads();
-        load_tile(static_cast<const T *>(p.Q) + row, t0, n, A);
-        load_tile(static_cast<const T *>(p.dY) + row, t0, n, B);
+        load_tile(static_cast<const float *>(p.Q) + row, t0, n, A);
+        load_tile(static_cast<const float *>(p.dY) + row, t0, n, B);
         __syncthreads();
         mm_tn(A, B, dec.tail, ty, tx, acc);
       }
@@ -195,67 +195,26 @@ __global__ void __launch_bounds__(kThreads) gated_segment_kernel(GatedArgs p) {
   if (threadIdx.x == 0 && (grad || gridDim.y == 1)) p.seg_decay[(size_t)bh * p.nseg + seg] = decay;
 }
 
-__device__ __forceinline__ float4 fma4(float f, float4 a, float4 b) {
-  return make_float4(fmaf(f, a.x, b.x), fmaf(f, a.y, b.y), fmaf(f, a.z, b.z), fmaf(f, a.w, b.w));
-}
-
-// z = 0: own states -> the state before each segment.  z = 1: own gradients ->
-// the gradient of the state behind each segment, and dstate0.  A thread walks
-// one float4 of the state over the segments; the loads of kAhead of them are
-// in flight at a time (the walk is a chain of loads that nothing else hides).
-constexpr int kAhead = 8;
-__global__ void __launch_bounds__(kThreads) gated_scan_kernel(GatedArgs p) {
+// z = 0: own states -> the state before each segment, forwards.  z = 1: own
+// gradients -> the gradient of the state behind each segment, backwards, and
+// dstate0.  In place.
+template <int kVec, int kAhead>
+__global__ void __launch_bounds__(kScanThreads) gated_scan_kernel(GatedArgs p) {
   pdl_trigger();
   pdl_wait();
-  const int bh = blockIdx.x, x = blockIdx.y * kThreads + threadIdx.x;   // one float4 of a state
+  const int bh = blockIdx.x, x = kVec * (blockIdx.y * kScanThreads + threadIdx.x);
   const int n = gated_len(p, bh / p.Hkv), last = gated_last_seg(n, p.seg_chunks * kGC);
-  const float *decay = p.seg_decay + (size_t)bh * p.nseg;
   const bool grad = blockIdx.z != 0;
-  float4 *s = reinterpret_cast<float4 *>((grad ? p.seg_grad : p.seg_state) + (size_t)bh * p.nseg * kGS) + x;
+  float *s = (grad ? p.seg_grad : p.seg_state) + (size_t)bh * p.nseg * kGS + x;
   const float *from = grad ? p.dstate : p.state_in;
-  float4 run = from ? reinterpret_cast<const float4 *>(from + (size_t)bh * kGS)[x]
-                    : make_float4(0.f, 0.f, 0.f, 0.f);
-  constexpr int kStep = kGS / 4;
-  if (!grad) {
-    for (int i0 = 0; i0 <= last; i0 += kAhead) {
-      float4 own[kAhead];
-      float f[kAhead];
-#pragma unroll
-      for (int k = 0; k < kAhead; ++k) {   // the last segment's own state is not needed
-        const bool on = i0 + k < last;
-        own[k] = on ? s[(size_t)(i0 + k) * kStep] : make_float4(0.f, 0.f, 0.f, 0.f);
-        f[k] = on ? decay[i0 + k] : 0.f;
-      }
-#pragma unroll
-      for (int k = 0; k < kAhead; ++k)
-        if (i0 + k <= last) {
-          s[(size_t)(i0 + k) * kStep] = run;
-          run = fma4(f[k], run, own[k]);
-        }
-    }
-  } else {
-    for (int i0 = n > 0 ? last : -1; i0 >= 0; i0 -= kAhead) {
-      float4 own[kAhead];
-      float f[kAhead];
-#pragma unroll
-      for (int k = 0; k < kAhead; ++k) {
-        const bool on = i0 - k >= 0;
-        own[k] = on ? s[(size_t)(i0 - k) * kStep] : make_float4(0.f, 0.f, 0.f, 0.f);
-        f[k] = on ? decay[i0 - k] : 0.f;
-      }
-#pragma unroll
-      for (int k = 0; k < kAhead; ++k)
-        if (i0 - k >= 0) {
-          s[(size_t)(i0 - k) * kStep] = run;
-          run = fma4(f[k], run, own[k]);
-        }
-    }
-    if (p.dstate0) reinterpret_cast<float4 *>(p.dstate0 + (size_t)bh * kGS)[x] = run;
-  }
+  const int count = grad && n == 0 ? 0 : last + 1;
+  const auto run = scan_walk<kVec, kAhead>(s, p.seg_decay + (size_t)bh * p.nseg, from ? from + (size_t)bh * kGS + x : nullptr,
+                                           count, grad ? count : last, grad,   // (the last segment's own state is not formed)
+                                           [&](int i, const ScanVec<kVec> &v) { scan_store(s + (size_t)i * kGS, v); });
+  if (grad && p.dstate0) scan_store(p.dstate0 + (size_t)bh * kGS + x, run);
 }
 
 // Outputs of a segment, and the state behind the sequence's last one.
-template <typename T>
 __global__ void __launch_bounds__(kThreads) gated_out_kernel(GatedArgs p) {
   pdl_trigger();
   pdl_wait();
@@ -275,8 +234,8 @@ __global__ void __launch_bounds__(kThreads) gated_out_kernel(GatedArgs p) {
     const int t0 = c * kGC;
     __syncthreads();
     chunk_decays(g, t0, n, dec);
-    load_tile(static_cast<const T *>(p.K) + (size_t)bh * p.T * 64, t0, n, K);
-    load_tile(static_cast<const T *>(p.V) + (size_t)bh * p.T * 64, t0, n, V);
+    load_tile(static_cast<const float *>(p.K) + (size_t)bh * p.T * 64, t0, n, K);
+    load_tile(static_cast<const float *>(p.V) + (size_t)bh * p.T * 64, t0, n, V);
     float pair[4][4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -286,7 +245,7 @@ __global__ void __launch_bounds__(kThreads) gated_out_kernel(GatedArgs p) {
     for (int r = 0; r < rho; ++r) {
       const size_t row = ((size_t)b * p.Hq + kv * rho + r) * p.T * 64;
       __syncthreads();
-      load_tile(static_cast<const T *>(p.Q) + row, t0, n, Q);
+      load_tile(static_cast<const float *>(p.Q) + row, t0, n, Q);
       __syncthreads();
       Acc a;
       clear(a);
@@ -308,7 +267,7 @@ __global__ void __launch_bounds__(kThreads) gated_out_kernel(GatedArgs p) {
       for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) a.v[i][j] *= p.scale;
-      store_rows(a, ty, tx, static_cast<T *>(p.Y) + row, t0, n);
+      store_rows(a, ty, tx, static_cast<float *>(p.Y) + row, t0, n);
     }
     Acc s;
     const float whole = dec.head[kGC - 1];
@@ -340,7 +299,6 @@ __global__ void __launch_bounds__(kThreads) gated_out_kernel(GatedArgs p) {
 //   dg_t = sum_{j<t<=l} w_lj + sum_{l>=t} q_l.dq_l' + sum_{j<t} k_j.dk_j' + e^{G_63} <S_in, R>
 // with w = p scale dy.v, and dq', dk' the terms with S_in and R: every path
 // from a token before t to one at or behind t decays by exp(g_t).
-template <typename T>
 __global__ void __launch_bounds__(kThreads) gated_grad_kernel(GatedArgs p) {
   pdl_trigger();
   pdl_wait();
@@ -355,8 +313,8 @@ __global__ void __launch_bounds__(kThreads) gated_grad_kernel(GatedArgs p) {
   const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
   const size_t kvrow = (size_t)bh * p.T * 64;
   chunk_decays(p.g + (size_t)bh * p.T, t0, n, dec);
-  load_tile(static_cast<const T *>(p.K) + kvrow, t0, n, K);
-  load_tile(static_cast<const T *>(p.V) + kvrow, t0, n, V);
+  load_tile(static_cast<const float *>(p.K) + kvrow, t0, n, K);
+  load_tile(static_cast<const float *>(p.V) + kvrow, t0, n, V);
   load_state(p.seg_state + ((size_t)bh * p.nseg + c) * kGS, S);
   load_state(p.seg_grad + ((size_t)bh * p.nseg + c) * kGS, R);
   float pair[4][4], w[4][4], rows[4] = {0.f, 0.f, 0.f, 0.f};
@@ -373,8 +331,8 @@ __global__ void __launch_bounds__(kThreads) gated_grad_kernel(GatedArgs p) {
   for (int r = 0; r < rho; ++r) {
     const size_t row = ((size_t)b * p.Hq + kv * rho + r) * p.T * 64;
     __syncthreads();
-    load_tile(static_cast<const T *>(p.Q) + row, t0, n, Q);
-    load_tile(static_cast<const T *>(p.dY) + row, t0, n, O);
+    load_tile(static_cast<const float *>(p.Q) + row, t0, n, Q);
+    load_tile(static_cast<const float *>(p.dY) + row, t0, n, O);
     __syncthreads();
     Acc a, z;
     clear(a);
@@ -404,7 +362,7 @@ __global__ void __launch_bounds__(kThreads) gated_grad_kernel(GatedArgs p) {
       }
     __syncthreads();
     mm_nn(Z, K, ty, tx, a);
-    store_rows(a, ty, tx, static_cast<T *>(p.dQ) + row, t0, n);
+    store_rows(a, ty, tx, static_cast<float *>(p.dQ) + row, t0, n);
     mm_tn(P, O, nullptr, ty, tx, dV);
     mm_tn(Z, Q, nullptr, ty, tx, dK);
   }
@@ -426,8 +384,8 @@ __global__ void __launch_bounds__(kThreads) gated_grad_kernel(GatedArgs p) {
   for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) dV.v[i][j] = fmaf(dec.tail[4 * ty + i], a.v[i][j], dV.v[i][j]);
-  store_rows(dK, ty, tx, static_cast<T *>(p.dK) + kvrow, t0, n);
-  store_rows(dV, ty, tx, static_cast<T *>(p.dV) + kvrow, t0, n);
+  store_rows(dK, ty, tx, static_cast<float *>(p.dK) + kvrow, t0, n);
+  store_rows(dV, ty, tx, static_cast<float *>(p.dV) + kvrow, t0, n);
 
   // dg: row and column sums of w, the far terms and <S_in, R>
   float dot = 0.f;
@@ -493,49 +451,39 @@ int gated_prefill_segment(int B, int Hkv, int T, int is_bf16) {
   const long long want = std::max<long long>(1, 3 * 152 / units);
   return (int)std::max<long long>(1, (chunks + want - 1) / want);
 }
-int gated_backward_segment(int is_bf16) {
-  (void)is_bf16;
-  return 1;
-}
-
 oal_status launch_gated_scan(const GatedArgs &p, int both, cudaStream_t stream) {
-  launch_pdl(gated_scan_kernel, dim3(p.B * p.Hkv, kGS / 4 / kThreads, both ? 2 : 1), dim3(kThreads), 0, stream, p);
+  const int units = p.B * p.Hkv, ways = both ? 2 : 1;
+  if (scan_deep(units * ways, p.nseg))
+    launch_pdl(gated_scan_kernel<2, 32>, dim3(units, kGS / 2 / kScanThreads, ways), dim3(kScanThreads), 0, stream, p);
+  else
+    launch_pdl(gated_scan_kernel<4, 8>, dim3(units, kGS / 4 / kScanThreads, ways), dim3(kScanThreads), 0, stream, p);
   return oal_after_launch("gated_scan_kernel", stream);
 }
 
-template <typename T>
-static oal_status prefill_simt(const GatedArgs &p, cudaStream_t stream) {
+oal_status launch_gated_prefill_simt(const GatedArgs &p, cudaStream_t stream) {
   static bool done_seg[kMaxDevices], done_out[kMaxDevices];
   const size_t seg_smem = 2 * kTile * sizeof(float), out_smem = 5 * kTile * sizeof(float);
-  GATED_TRY(gated_need_smem(reinterpret_cast<const void *>(gated_segment_kernel<T>), seg_smem, done_seg));
-  GATED_TRY(gated_need_smem(reinterpret_cast<const void *>(gated_out_kernel<T>), out_smem, done_out));
+  GATED_TRY(gated_need_smem(reinterpret_cast<const void *>(gated_segment_kernel), seg_smem, done_seg));
+  GATED_TRY(gated_need_smem(reinterpret_cast<const void *>(gated_out_kernel), out_smem, done_out));
   if (p.nseg > 1) {
-    launch_pdl(gated_segment_kernel<T>, dim3(p.nseg * p.B * p.Hkv), dim3(kThreads), seg_smem, stream, p);
+    launch_pdl(gated_segment_kernel, dim3(p.nseg * p.B * p.Hkv), dim3(kThreads), seg_smem, stream, p);
     GATED_TRY(oal_after_launch("gated_segment_kernel", stream));
     GATED_TRY(launch_gated_scan(p, 0, stream));
   }
-  launch_pdl(gated_out_kernel<T>, dim3(p.nseg * p.B * p.Hkv), dim3(kThreads), out_smem, stream, p);
+  launch_pdl(gated_out_kernel, dim3(p.nseg * p.B * p.Hkv), dim3(kThreads), out_smem, stream, p);
   return oal_after_launch("gated_out_kernel", stream);
 }
 
-template <typename T>
-static oal_status backward_simt(const GatedArgs &p, cudaStream_t stream) {
+oal_status launch_gated_backward_simt(const GatedArgs &p, cudaStream_t stream) {
   static bool done_seg[kMaxDevices], done_grad[kMaxDevices];
   const size_t seg_smem = 2 * kTile * sizeof(float), grad_smem = 8 * kTile * sizeof(float);
-  GATED_TRY(gated_need_smem(reinterpret_cast<const void *>(gated_segment_kernel<T>), seg_smem, done_seg));
-  GATED_TRY(gated_need_smem(reinterpret_cast<const void *>(gated_grad_kernel<T>), grad_smem, done_grad));
-  launch_pdl(gated_segment_kernel<T>, dim3(p.nseg * p.B * p.Hkv, 2), dim3(kThreads), seg_smem, stream, p);
+  GATED_TRY(gated_need_smem(reinterpret_cast<const void *>(gated_segment_kernel), seg_smem, done_seg));
+  GATED_TRY(gated_need_smem(reinterpret_cast<const void *>(gated_grad_kernel), grad_smem, done_grad));
+  launch_pdl(gated_segment_kernel, dim3(p.nseg * p.B * p.Hkv, 2), dim3(kThreads), seg_smem, stream, p);
   GATED_TRY(oal_after_launch("gated_segment_kernel", stream));
   GATED_TRY(launch_gated_scan(p, 1, stream));
-  launch_pdl(gated_grad_kernel<T>, dim3(p.nseg * p.B * p.Hkv), dim3(kThreads), grad_smem, stream, p);
+  launch_pdl(gated_grad_kernel, dim3(p.nseg * p.B * p.Hkv), dim3(kThreads), grad_smem, stream, p);
   return oal_after_launch("gated_grad_kernel", stream);
-}
-
-oal_status launch_gated_prefill_simt(const GatedArgs &p, int is_bf16, cudaStream_t stream) {
-  return is_bf16 ? prefill_simt<__nv_bfloat16>(p, stream) : prefill_simt<float>(p, stream);
-}
-oal_status launch_gated_backward_simt(const GatedArgs &p, int is_bf16, cudaStream_t stream) {
-  return is_bf16 ? backward_simt<__nv_bfloat16>(p, stream) : backward_simt<float>(p, stream);
 }
 
 }  // namespace oal

@@ -101,52 +101,39 @@ gated_tc_own_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
 
 // ---------------------------------------------------------------- scan
 
-constexpr int kScanThreads = 256, kAhead = 8;
-
-// The thread's four values of a state as hi and lo words of the two tiles.
-__device__ __forceinline__ void put_tiles(uint8_t *tiles, int x, float4 v) {
-  uint8_t *at = tiles + tile_at(x >> 4, (x & 15) >> 1) + 8 * (x & 1);
-  const uint32_t h0 = pack_bf16x2(v.x, v.y), h1 = pack_bf16x2(v.z, v.w);
-  *reinterpret_cast<uint2 *>(at) = make_uint2(h0, h1);
-  *reinterpret_cast<uint2 *>(at + kTileBytes) =
-      make_uint2(pack_bf16x2(v.x - __uint_as_float(h0 << 16), v.y - __uint_as_float(h0 & 0xFFFF0000u)),
-                 pack_bf16x2(v.z - __uint_as_float(h1 << 16), v.w - __uint_as_float(h1 & 0xFFFF0000u)));
-}
-
 // z = 0: the state before each chunk, forwards; 1: the gradient of the state
-// behind each, backwards, and dstate0.
+// behind each, backwards, and dstate0; as a word each of the hi and lo tiles
+// for two neighbouring values.
+template <int kVec, int kAhead>
 __global__ void __launch_bounds__(kScanThreads) gated_tc_scan_kernel(GatedArgs p) {
   pdl_trigger();
   pdl_wait();
-  const int bh = blockIdx.x, x = blockIdx.y * kScanThreads + threadIdx.x;
+  const int bh = blockIdx.x, x = kVec * (blockIdx.y * kScanThreads + threadIdx.x);
   const bool grad = blockIdx.z != 0;
   const int n = gated_len(p, bh / p.Hkv), count = (n + kGC - 1) / kGC;
-  const float *decay = p.seg_decay + (size_t)bh * p.nseg;
-  const float4 *own = reinterpret_cast<const float4 *>((grad ? p.seg_grad : p.seg_state) + (size_t)bh * p.nseg * kGS) + x;
-  uint8_t *tiles = (grad ? p.grad_tiles : p.state_tiles) + (size_t)bh * p.nseg * 2 * kTileBytes;
+  const float *own = (grad ? p.seg_grad : p.seg_state) + (size_t)bh * p.nseg * kGS + x;
+  uint8_t *tiles = (grad ? p.grad_tiles : p.state_tiles) + (size_t)bh * p.nseg * 2 * kTileBytes +
+                   tile_at(x >> 6, (x & 63) >> 3) + 2 * (x & 7);
   const float *from = grad ? p.dstate : p.state_in;
-  float4 run = from ? reinterpret_cast<const float4 *>(from + (size_t)bh * kGS)[x] : make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int i0 = 0; i0 < count; i0 += kAhead) {
-    float4 v[kAhead];
-    float f[kAhead];
+  const auto run = scan_walk<kVec, kAhead>(
+      own, p.seg_decay + (size_t)bh * p.nseg, from ? from + (size_t)bh * kGS + x : nullptr, count, count, grad,
+      [&](int i, const ScanVec<kVec> &v) {
+        uint8_t *at = tiles + (size_t)i * 2 * kTileBytes;
+        uint32_t hi[kVec / 2], lo[kVec / 2];
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      const int i = grad ? count - 1 - i0 - k : i0 + k;
-      const bool on = i0 + k < count;
-      v[k] = on ? __ldg(own + (size_t)i * (kGS / 4)) : make_float4(0.f, 0.f, 0.f, 0.f);
-      f[k] = on ? __ldg(decay + i) : 0.f;
-    }
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      const int i = grad ? count - 1 - i0 - k : i0 + k;
-      if (i0 + k < count) {
-        put_tiles(tiles + (size_t)i * 2 * kTileBytes, x, run);
-        run.x = fmaf(f[k], run.x, v[k].x), run.y = fmaf(f[k], run.y, v[k].y);
-        run.z = fmaf(f[k], run.z, v[k].z), run.w = fmaf(f[k], run.w, v[k].w);
-      }
-    }
-  }
-  if (grad && p.dstate0) reinterpret_cast<float4 *>(p.dstate0 + (size_t)bh * kGS)[x] = run;
+        for (int e = 0; e < kVec / 2; ++e) {
+          hi[e] = pack_bf16x2(v.v[2 * e], v.v[2 * e + 1]);
+          lo[e] = pack_bf16x2(v.v[2 * e] - __uint_as_float(hi[e] << 16), v.v[2 * e + 1] - __uint_as_float(hi[e] & 0xFFFF0000u));
+        }
+        if (kVec == 4) {
+          *reinterpret_cast<uint2 *>(at) = make_uint2(hi[0], hi[kVec / 2 - 1]);
+          *reinterpret_cast<uint2 *>(at + kTileBytes) = make_uint2(lo[0], lo[kVec / 2 - 1]);
+        } else {
+          *reinterpret_cast<uint32_t *>(at) = hi[0];
+          *reinterpret_cast<uint32_t *>(at + kTileBytes) = lo[0];
+        }
+      });
+  if (grad && p.dstate0) scan_store(p.dstate0 + (size_t)bh * kGS + x, run);
 }
 
 // ---------------------------------------------------------------- gradients
@@ -722,7 +709,11 @@ oal_status launch_gated_backward_tc(const GatedArgs &p, cudaStream_t stream) {
   const int total = p.nseg * p.B * p.Hkv;
   launch_pdl(gated_tc_own_kernel, dim3(total, 2), dim3(kOwnThreads), own_smem, stream, tmQ, tmK, tmV, tmO, p);
   GATED_TRY(oal_after_launch("gated_tc_own_kernel", stream));
-  launch_pdl(gated_tc_scan_kernel, dim3(p.B * p.Hkv, kGS / 4 / kScanThreads, 2), dim3(kScanThreads), 0, stream, p);
+  const int units = p.B * p.Hkv;
+  if (scan_deep(2 * units, p.nseg))
+    launch_pdl(gated_tc_scan_kernel<2, 32>, dim3(units, kGS / 2 / kScanThreads, 2), dim3(kScanThreads), 0, stream, p);
+  else
+    launch_pdl(gated_tc_scan_kernel<4, 8>, dim3(units, kGS / 4 / kScanThreads, 2), dim3(kScanThreads), 0, stream, p);
   GATED_TRY(oal_after_launch("gated_tc_scan_kernel", stream));
   launch_pdl(gated_tc_grad_kernel, dim3(std::min(total, 2 * 152)), dim3(kGradThreads), grad_smem, stream, tmQ, tmK, tmV,
              tmO, tmDQ, p);

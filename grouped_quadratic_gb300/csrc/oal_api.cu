@@ -46,9 +46,9 @@ oal_status group_dims_host(const float *chi_p, int P, int d, const int32_t *boot
                            int nboot, double alpha, double tau, double gamma, int g_min,
                            double eps, int32_t *group, int *G);
 
-oal_status launch_gated_prefill_simt(const GatedArgs &p, int is_bf16, cudaStream_t stream);
+oal_status launch_gated_prefill_simt(const GatedArgs &p, cudaStream_t stream);
 oal_status launch_gated_prefill_tc(const GatedArgs &p, cudaStream_t stream);
-oal_status launch_gated_backward_simt(const GatedArgs &p, int is_bf16, cudaStream_t stream);
+oal_status launch_gated_backward_simt(const GatedArgs &p, cudaStream_t stream);
 oal_status launch_gated_backward_tc(const GatedArgs &p, cudaStream_t stream);
 oal_status launch_gated_decode(const void *q, const void *k, const void *v, int is_bf16,
                                const float *g, int B, int Hq, int Hkv, float scale,
@@ -514,14 +514,14 @@ oal_status oal_gated_prefill(const void *Q, const void *K, const void *V, oal_dt
   if (!p.status) return oal_fail(OAL_ERR_CUDA, "no device status word");
   oal_begin_call(stream);
   if (dtype == OAL_BF16) return oal::launch_gated_prefill_tc(p, stream);
-  return oal::launch_gated_prefill_simt(p, 0, stream);
+  return oal::launch_gated_prefill_simt(p, stream);
 }
 
 size_t oal_gated_backward_workspace_bytes(int B, int Hq, int Hkv, int T, int d, int dv,
                                           oal_dtype dtype) {
   if (check_gated(B, Hq, Hkv, T, d, dv, dtype, 1.f) != OAL_OK) return 0;
   if (B == 0 || T == 0) return 256;
-  const int nseg = oal::gated_segments(T, oal::gated_backward_segment(dtype == OAL_BF16));
+  const int nseg = oal::gated_segments(T, 1);   // a segment is a chunk
   // (bf16: and both once more, as pairs of bf16 tiles)
   return (dtype == OAL_BF16 ? 4 : 2) * gated_states_bytes(B, Hkv, nseg) +
          round256((size_t)B * Hkv * nseg * sizeof(float));
@@ -564,7 +564,7 @@ oal_status oal_gated_backward(const void *Q, const void *K, const void *V, oal_d
   p.B = B, p.Hq = Hq, p.Hkv = Hkv, p.T = T, p.scale = scale, p.lengths = lengths;
   p.state_in = state0, p.dstate = dstate, p.dstate0 = dstate0;
   p.dQ = dQ, p.dK = dK, p.dV = dV, p.dg = dg;
-  p.seg_chunks = oal::gated_backward_segment(dtype == OAL_BF16);
+  p.seg_chunks = 1;
   p.nseg = oal::gated_segments(T, p.seg_chunks);
   const size_t states = gated_states_bytes(B, Hkv, p.nseg);
   p.seg_state = static_cast<float *>(workspace);
@@ -576,7 +576,7 @@ oal_status oal_gated_backward(const void *Q, const void *K, const void *V, oal_d
   if (!p.status) return oal_fail(OAL_ERR_CUDA, "no device status word");
   oal_begin_call(stream);
   if (dtype == OAL_BF16) return oal::launch_gated_backward_tc(p, stream);
-  return oal::launch_gated_backward_simt(p, 0, stream);
+  return oal::launch_gated_backward_simt(p, stream);
 }
 
 oal_status oal_gated_decode_step(const void *q, const void *k, const void *v, oal_dtype dtype,

@@ -2,12 +2,13 @@
 // pool of states in place: new[i] = old[map[i]], zeros where map[i] is -1.
 //
 // Every source has to be read before any target is written, whatever cycles
-// the map holds.  The slots are cut into slices of a few words; a
-// block takes a slice of ALL slots that change, holds their old words in
-// registers, waits for its threads and writes them to their new places.
-// Slices do not meet, so no block waits for another, and no workspace is
-// needed.  Each changed slot's source is read once and its target written
-// once: HBM-bound.
+// the map holds.  The slots are cut into slices of a few words; a block takes
+// a slice of ALL slots that change, holds the old words that move in
+// registers, waits for its threads, and writes them and the zeros.  Slices do
+// not meet, so no block waits for another, and no workspace is needed.  Each
+// moved slot's source is read once and its target written once: HBM-bound.
+// The fewer slots move, the longer the runs of a slice: 512 moving slots leave
+// runs of 256 bytes, 64 of 2 KB.
 #include <algorithm>
 
 #include "gated.cuh"
@@ -26,40 +27,45 @@ __global__ void __launch_bounds__(kMoveThreads)
 state_remap_kernel(Word *pool, long long slot_words, int n, const int32_t *__restrict__ map, int *status) {
   pdl_trigger();
   pdl_wait();
-  extern __shared__ int2 s_move[];      // (target, source) of the slots that change
-  __shared__ int s_count;
-  if (threadIdx.x == 0) s_count = 0;
+  extern __shared__ int2 s_move[];      // (target, source) of the slots that move; from the end: those to be zeroed
+  __shared__ int s_count, s_zeros;
+  if (threadIdx.x == 0) s_count = s_zeros = 0;
   __syncthreads();
   for (int i = threadIdx.x; i < n; i += kMoveThreads) {
     const int from = map[i];
     if (from < -1 || from >= n) {
       atomicCAS(status, kStatusOk, (int)OAL_ERR_INVALID_ARG);
+    } else if (from == -1) {
+      s_move[n - 1 - atomicAdd(&s_zeros, 1)].x = i;          // (any order: targets differ)
     } else if (from != i) {
-      s_move[atomicAdd(&s_count, 1)] = make_int2(i, from);   // any order: targets differ
+      s_move[atomicAdd(&s_count, 1)] = make_int2(i, from);
     }
   }
   __syncthreads();
-  const int count = s_count;
-  if (count == 0) return;
+  const int count = s_count, zeros = s_zeros;
+  if (count + zeros == 0) return;
   // words of a slice: as many as the block holds, at most what spreads the
   // slot over the grid
   const long long spread = (slot_words + gridDim.x - 1) / gridDim.x;
-  const int width = (int)min((long long)(kMoveMost / count), spread);
+  const int width = (int)min((long long)(kMoveMost / max(count, 1)), spread);
   const int total = width * count;
   for (long long w0 = (long long)blockIdx.x * width; w0 < slot_words; w0 += (long long)gridDim.x * width) {
+    const int wide = (int)min((long long)width, slot_words - w0);
     Word held[kMoveWords];
 #pragma unroll
     for (int k = 0; k < kMoveWords; ++k) {
       const int x = threadIdx.x + k * kMoveThreads, m = x / width, w = x - m * width;
-      held[k] = Word();
-      if (x < total && w0 + w < slot_words && s_move[m].y >= 0)
-        held[k] = pool[(long long)s_move[m].y * slot_words + w0 + w];
+      if (x < total && w < wide) held[k] = pool[(long long)s_move[m].y * slot_words + w0 + w];
     }
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < kMoveWords; ++k) {
       const int x = threadIdx.x + k * kMoveThreads, m = x / width, w = x - m * width;
-      if (x < total && w0 + w < slot_words) pool[(long long)s_move[m].x * slot_words + w0 + w] = held[k];
+      if (x < total && w < wide) pool[(long long)s_move[m].x * slot_words + w0 + w] = held[k];
+    }
+    for (int x = threadIdx.x; x < zeros * width; x += kMoveThreads) {
+      const int m = x / width, w = x - m * width;
+      if (w < wide) pool[(long long)s_move[n - 1 - m].x * slot_words + w0 + w] = Word();
     }
   }
 }

@@ -344,7 +344,7 @@ def _need(ok, what):
 
 
 def _need_tensor(t, name, dtype, shape, dev):
-    if t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous():
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.device == dev:
         return
     if t.dtype != dtype or t.shape != shape:
         raise OALError(OAL_ERR_INVALID_ARG, "%s must be %s %s (got %s %s)"
