@@ -129,8 +129,10 @@ struct Decays {
   GateSums sums;
   float head[kGC], tail[kGC];
 };
-__device__ __forceinline__ void chunk_decays(const float *g, int t0, int n, Decays &d) {
-  if (threadIdx.x < 32) gate_store(gate_sums(gate_load(g, t0, n)), d.sums);
+// (`gate` as warp 0 loaded it, early, so that its way to memory is not in
+// front of the tiles')
+__device__ __forceinline__ void chunk_decays(float2 gate, Decays &d) {
+  if (threadIdx.x < 32) gate_store(gate_sums(gate), d.sums);
   __syncthreads();
   if (threadIdx.x < kGC) {
     d.head[threadIdx.x] = gate_head(d.sums, threadIdx.x);
@@ -162,8 +164,16 @@ __global__ void __launch_bounds__(kThreads) gated_segment_kernel(GatedArgs p) {
   float decay = 1.f;
   for (int s = 0; s < c1 - c0; ++s) {
     const int t0 = (grad ? c1 - 1 - s : c0 + s) * kGC;
+    const float2 gate = gate_load(g, t0, n);
     __syncthreads();
-    chunk_decays(g, t0, n, dec);
+    if (!grad) {
+      load_tile(static_cast<const float *>(p.K) + (size_t)bh * p.T * 64, t0, n, A);
+      load_tile(static_cast<const float *>(p.V) + (size_t)bh * p.T * 64, t0, n, B);
+    } else {
+      load_tile(static_cast<const float *>(p.Q) + ((size_t)b * p.Hq + kv * rho) * p.T * 64, t0, n, A);
+      load_tile(static_cast<const float *>(p.dY) + ((size_t)b * p.Hq + kv * rho) * p.T * 64, t0, n, B);
+    }
+    chunk_decays(gate, dec);
     const float whole = dec.head[kGC - 1];
     decay *= whole;
 #pragma unroll
@@ -171,18 +181,17 @@ __global__ void __launch_bounds__(kThreads) gated_segment_kernel(GatedArgs p) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) acc.v[i][j] *= whole;
     if (!grad) {
-      load_tile(static_cast<const float *>(p.K) + (size_t)bh * p.T * 64, t0, n, A);
-      load_tile(static_cast<const float *>(p.V) + (size_t)bh * p.T * 64, t0, n, B);
-      __syncthreads();
       mm_tn(A, B, dec.tail, ty, tx, acc);
     } else {
       if (threadIdx.x < kGC) dec.tail[threadIdx.x] = p.scale * dec.head[threadIdx.x];
       for (int r = 0; r < rho; ++r) {
         const size_t row = ((size_t)b * p.Hq + kv * rho + r) * p.T * 64;
         __syncthreads();
-        load_tile(static_cast<const float *>(p.Q) + row, t0, n, A);
-        load_tile(static_cast<const float *>(p.dY) + row, t0, n, B);
-        __syncthreads();
+        if (r > 0) {
+          load_tile(static_cast<const float *>(p.Q) + row, t0, n, A);
+          load_tile(static_cast<const float *>(p.dY) + row, t0, n, B);
+          __syncthreads();
+        }
         mm_tn(A, B, dec.tail, ty, tx, acc);
       }
     }
@@ -232,10 +241,12 @@ __global__ void __launch_bounds__(kThreads) gated_out_kernel(GatedArgs p) {
   const int c0 = seg * p.seg_chunks, c1 = min((n + kGC - 1) / kGC, c0 + p.seg_chunks);
   for (int c = c0; c < c1; ++c) {
     const int t0 = c * kGC;
+    const float2 gate = gate_load(g, t0, n);
     __syncthreads();
-    chunk_decays(g, t0, n, dec);
     load_tile(static_cast<const float *>(p.K) + (size_t)bh * p.T * 64, t0, n, K);
+    load_tile(static_cast<const float *>(p.Q) + ((size_t)b * p.Hq + kv * rho) * p.T * 64, t0, n, Q);
     load_tile(static_cast<const float *>(p.V) + (size_t)bh * p.T * 64, t0, n, V);
+    chunk_decays(gate, dec);
     float pair[4][4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -244,9 +255,11 @@ __global__ void __launch_bounds__(kThreads) gated_out_kernel(GatedArgs p) {
         pair[i][j] = gate_pair(dec.sums, 4 * ty + i, min(tx + 16 * j, 4 * ty + i));
     for (int r = 0; r < rho; ++r) {
       const size_t row = ((size_t)b * p.Hq + kv * rho + r) * p.T * 64;
-      __syncthreads();
-      load_tile(static_cast<const float *>(p.Q) + row, t0, n, Q);
-      __syncthreads();
+      if (r > 0) {
+        __syncthreads();
+        load_tile(static_cast<const float *>(p.Q) + row, t0, n, Q);
+        __syncthreads();
+      }
       Acc a;
       clear(a);
       mm_nt(Q, K, ty, tx, a);
@@ -312,11 +325,14 @@ __global__ void __launch_bounds__(kThreads) gated_grad_kernel(GatedArgs p) {
   if (t0 >= n) return;
   const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
   const size_t kvrow = (size_t)bh * p.T * 64;
-  chunk_decays(p.g + (size_t)bh * p.T, t0, n, dec);
+  const float2 gate = gate_load(p.g + (size_t)bh * p.T, t0, n);
   load_tile(static_cast<const float *>(p.K) + kvrow, t0, n, K);
   load_tile(static_cast<const float *>(p.V) + kvrow, t0, n, V);
+  load_tile(static_cast<const float *>(p.Q) + ((size_t)b * p.Hq + kv * rho) * p.T * 64, t0, n, Q);
+  load_tile(static_cast<const float *>(p.dY) + ((size_t)b * p.Hq + kv * rho) * p.T * 64, t0, n, O);
   load_state(p.seg_state + ((size_t)bh * p.nseg + c) * kGS, S);
   load_state(p.seg_grad + ((size_t)bh * p.nseg + c) * kGS, R);
+  chunk_decays(gate, dec);
   float pair[4][4], w[4][4], rows[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int i = 0; i < 4; ++i)
@@ -330,10 +346,12 @@ __global__ void __launch_bounds__(kThreads) gated_grad_kernel(GatedArgs p) {
   clear(dV);
   for (int r = 0; r < rho; ++r) {
     const size_t row = ((size_t)b * p.Hq + kv * rho + r) * p.T * 64;
-    __syncthreads();
-    load_tile(static_cast<const float *>(p.Q) + row, t0, n, Q);
-    load_tile(static_cast<const float *>(p.dY) + row, t0, n, O);
-    __syncthreads();
+    if (r > 0) {
+      __syncthreads();
+      load_tile(static_cast<const float *>(p.Q) + row, t0, n, Q);
+      load_tile(static_cast<const float *>(p.dY) + row, t0, n, O);
+      __syncthreads();
+    }
     Acc a, z;
     clear(a);
     clear(z);

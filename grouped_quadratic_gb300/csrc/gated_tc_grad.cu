@@ -27,7 +27,8 @@ using namespace gated;
 
 // ---------------------------------------------------------------- own states
 
-constexpr int kOwnThreads = 128, kOwnStages = 2;
+constexpr int kOwnThreads = 128;
+template <int kOwnStages>
 struct OwnSmem {
   uint8_t a[kOwnStages][kTileBytes], b[kOwnStages][kTileBytes];
   PairWeights w;
@@ -37,12 +38,13 @@ struct OwnSmem {
 
 // blockIdx.y = 0: sum_j e^{G_63-G_j} k_j v_j^T of the chunk, and its decay;
 // 1: scale sum_i e^{G_i} q_i dy_i^T over the query heads of the KV head.
+template <int kOwnStages>
 __global__ void __launch_bounds__(kOwnThreads)
 gated_tc_own_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO, GatedArgs p) {
   pdl_trigger();
   extern __shared__ uint8_t smem_raw[];
-  OwnSmem &s = *reinterpret_cast<OwnSmem *>(align1024(smem_raw));
+  OwnSmem<kOwnStages> &s = *reinterpret_cast<OwnSmem<kOwnStages> *>(align1024(smem_raw));
   const int bh = blockIdx.x / p.nseg, c = blockIdx.x % p.nseg, b = bh / p.Hkv, kv = bh % p.Hkv;
   const int tid = threadIdx.x, rho = p.Hq / p.Hkv, t0 = c * kGC;
   const bool grad = blockIdx.y != 0;
@@ -695,9 +697,15 @@ gated_tc_grad_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
 }  // namespace
 
 oal_status launch_gated_backward_tc(const GatedArgs &p, cudaStream_t stream) {
-  static bool done_own[kMaxDevices], done_grad[kMaxDevices];
-  const size_t own_smem = sizeof(OwnSmem) + 1024, grad_smem = sizeof(GradSmem) + 1024;
-  GATED_TRY(gated_need_smem(reinterpret_cast<const void *>(gated_tc_own_kernel), own_smem, done_own));
+  static bool done_own[2][kMaxDevices], done_grad[kMaxDevices];
+  const int total = p.nseg * p.B * p.Hkv;
+  // Few chunks: more heads of each in flight (256 chunks of 7 heads: 46 us a
+  // backward against 57); many: more blocks per SM (2048 chunks of 4 heads:
+  // 50 us this kernel against 58).
+  const bool few = total <= 3 * 152;
+  const auto own = few ? gated_tc_own_kernel<4> : gated_tc_own_kernel<2>;
+  const size_t own_smem = (few ? sizeof(OwnSmem<4>) : sizeof(OwnSmem<2>)) + 1024, grad_smem = sizeof(GradSmem) + 1024;
+  GATED_TRY(gated_need_smem(reinterpret_cast<const void *>(own), own_smem, done_own[few]));
   GATED_TRY(gated_need_smem(reinterpret_cast<const void *>(gated_tc_grad_kernel), grad_smem, done_grad));
   const long long hq = (long long)p.B * p.Hq, hkv = (long long)p.B * p.Hkv;
   CUtensorMap tmQ, tmK, tmV, tmO, tmDQ;
@@ -706,8 +714,7 @@ oal_status launch_gated_backward_tc(const GatedArgs &p, cudaStream_t stream) {
   GATED_TRY(make_map(&tmV, p.V, p.T, hkv));
   GATED_TRY(make_map(&tmO, p.dY, p.T, hq));
   GATED_TRY(make_map(&tmDQ, p.dQ, p.T, hq, 32));
-  const int total = p.nseg * p.B * p.Hkv;
-  launch_pdl(gated_tc_own_kernel, dim3(total, 2), dim3(kOwnThreads), own_smem, stream, tmQ, tmK, tmV, tmO, p);
+  launch_pdl(own, dim3(total, 2), dim3(kOwnThreads), own_smem, stream, tmQ, tmK, tmV, tmO, p);
   GATED_TRY(oal_after_launch("gated_tc_own_kernel", stream));
   const int units = p.B * p.Hkv;
   if (scan_deep(2 * units, p.nseg))

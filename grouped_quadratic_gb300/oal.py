@@ -502,12 +502,20 @@ def oal_gated_decode_step(q, k, v, g, state, scale=0.125, slots=None, y=None, st
           "q, k and v must have 3 dimensions, state 4")
     B, Hq, d = q.shape
     Hkv, dv = k.shape[1], v.shape[2]
-    dt, dev, n = _dtype_code(q), q.device, state.shape[0]
-    _need_tensor(q, "q", q.dtype, (B, Hq, d), dev)
-    _need_tensor(k, "k", q.dtype, (B, Hkv, d), dev)
-    _need_tensor(v, "v", q.dtype, (B, Hkv, dv), dev)
-    _need_tensor(g, "g", torch.float32, (B, Hkv), dev)
-    _need_tensor(state, "state", torch.float32, (n, Hkv, d, dv), dev)
+    dt, dev, n, t = _dtype_code(q), q.device, state.shape[0], q.dtype
+    at = q.get_device()
+    # (one expression: a token's call is worth a few microseconds)
+    if not (k.dtype is t and v.dtype is t and g.dtype is torch.float32
+            and state.dtype is torch.float32 and k.shape == (B, Hkv, d) and v.shape == (B, Hkv, dv)
+            and g.shape == (B, Hkv) and state.shape == (n, Hkv, d, dv)
+            and k.get_device() == at and v.get_device() == at and g.get_device() == at
+            and state.get_device() == at and q.is_contiguous() and k.is_contiguous()
+            and v.is_contiguous() and g.is_contiguous() and state.is_contiguous()):
+        _need_tensor(q, "q", t, (B, Hq, d), dev)
+        _need_tensor(k, "k", t, (B, Hkv, d), dev)
+        _need_tensor(v, "v", t, (B, Hkv, dv), dev)
+        _need_tensor(g, "g", torch.float32, (B, Hkv), dev)
+        _need_tensor(state, "state", torch.float32, (n, Hkv, d, dv), dev)
     if slots is not None:
         _need_tensor(slots, "slots", torch.int32, (B,), dev)
     if _elsewhere(dev):
