@@ -33,18 +33,21 @@ constexpr uint32_t kColX = 0, kColD = 64;
 
 // ---------------------------------------------------------------- segments
 
+constexpr int kGateBatch = 8;               // chunks whose decays are formed together, two a warp
 struct SegSmem {
   uint8_t a[kStages][kTileBytes], b[kStages][kTileBytes];
   struct {
     PairWeights tail;
     float whole;
-  } gates[2];
+  } gates[kGateBatch];
   uint64_t full[kStages];
   int abort_flag;
 };
 
-// Own state of each segment but a sequence's last: K and V once, the four
-// warps' decays by one of them in turn, a chunk ahead.
+// Own state of each segment but a sequence's last: K and V once.  A chunk's
+// decays are a chain of shuffles as long as its products: eight chunks' are
+// formed side by side, or every chunk would wait for its own (22 us at
+// 4 x 8192 tokens, 8 KV heads, that way).
 __global__ void __launch_bounds__(kSegThreads)
 gated_tc_segment_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                         GatedArgs p) {
@@ -73,30 +76,27 @@ gated_tc_segment_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_co
   if (tid == 0)
     for (int c = 0; c < min(kStages, nc); ++c) load(c);
   const float *g = p.g + (size_t)bh * p.T;
-  auto make_gates = [&](int c, float2 gate) {
-    const float whole = gate_tails(gate_sums(gate), s.gates[c & 1].tail);
-    if ((tid & 31) == 0) s.gates[c & 1].whole = whole;
-  };
-  // warp w has the gates of its next chunk in hand: the first c > 0 with c % 4 = w, then every fourth
-  const int own = warp ? warp : 4;
-  if (warp == 0) make_gates(0, gate_load(g, c0 * kGC, n));
-  float2 gate = gate_load(g, (c0 + own) * kGC, own < nc ? n : 0);
-  __syncthreads();
+  auto gate_of = [&](int c) { return gate_load(g, (c0 + c) * kGC, c < nc ? n : 0); };
+  float2 gate0 = gate_of(warp), gate1 = gate_of(warp + 4);
   StateAcc<8> acc;
   state_load(acc, 0, nullptr);
   float decay = 1.f;
   bool ok = true;
   for (int c = 0; c < nc; ++c) {
-    const float whole = s.gates[c & 1].whole;
-    decay *= whole;
-    state_scale(acc, whole);
-    if ((c + 1) % 4 == warp && c + 1 < nc) {
-      make_gates(c + 1, gate);
-      gate = gate_load(g, (c0 + c + 5) * kGC, c + 5 < nc ? n : 0);
+    if (c % kGateBatch == 0) {   // (the chunk before ended in a barrier)
+      const GateLane s0 = gate_sums(gate0), s1 = gate_sums(gate1);
+      auto &to0 = s.gates[warp], &to1 = s.gates[warp + 4];
+      to0.whole = gate_tails(s0, to0.tail);
+      to1.whole = gate_tails(s1, to1.tail);
+      gate0 = gate_of(c + kGateBatch + warp), gate1 = gate_of(c + kGateBatch + warp + 4);
+      __syncthreads();
     }
+    const auto &gates = s.gates[c % kGateBatch];
+    decay *= gates.whole;
+    state_scale(acc, gates.whole);
     ok = ok && mbar_wait(&s.full[c % kStages], (c / kStages) & 1, abort_flag, p.status);
     ok = __all_sync(0xffffffffu, ok);
-    if (ok) state_add<0, 4>(acc, 0, s.a[c % kStages], s.b[c % kStages], s.gates[c & 1].tail);
+    if (ok) state_add<0, 4>(acc, 0, s.a[c % kStages], s.b[c % kStages], gates.tail);
     __syncthreads();
     if (tid == 0 && ok && c + kStages < nc) load(c + kStages);
   }
