@@ -67,11 +67,11 @@ __device__ __forceinline__ uint32_t bf2_fma(uint32_t a, uint32_t b, uint32_t c) 
 // whose rounding error w_hi a - hi is a bf16 number itself, and
 // lo = bf16(w_lo a + that), three packed products for two values; the terms'
 // sum is off by at most 2^-15 of w a where one rounded factor would be off by
-// 2^-8.  With kTerms = 3 the error and bf16(w_lo a) go in apart: off by 2^-16
-// at most, mostly by the weight's own second rounding.  b is exact.
+// 2^-8.  b is exact.  (For a state that is rounded to bf16 before it is read;
+// state_step is the exact one.)
 // The terms of one accumulator are kNb products apart, and the next
 // 16 rows' operand is under way while these multiply.
-template <int kFrom, int kTo, int kTerms = 2, int kNb>
+template <int kFrom, int kTo, int kNb>
 __device__ __forceinline__ void state_add(StateAcc<kNb> &s, int nb0, const void *a_tile, const void *b_tile,
                                           const PairWeights &w) {
   const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3;
@@ -88,24 +88,68 @@ __device__ __forceinline__ void state_add(StateAcc<kNb> &s, int nb0, const void 
   for (int ks = kFrom; ks < kTo; ++ks) {
 #pragma unroll
     for (int np = 0; np < kNb / 2; ++np) ldsm4t(bt[np] + 2048 * ks, b[np]);
-    uint32_t hi[4], lo[4], rest[4];
+    uint32_t hi[4], lo[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const uint32_t wh = w.hi[8 * ks + 4 * (e >> 1) + q], wl = w.lo[8 * ks + 4 * (e >> 1) + q];
       hi[e] = bf2_mul(wh, a[e]);
-      lo[e] = bf2_fma(wh, a[e], hi[e] ^ 0x80008000u);
-      if (kTerms == 3) rest[e] = bf2_mul(wl, a[e]);
-      else lo[e] = bf2_fma(wl, a[e], lo[e]);
+      lo[e] = bf2_fma(wl, a[e], bf2_fma(wh, a[e], hi[e] ^ 0x80008000u));
     }
     if (ks + 1 < kTo) ldsm4t(at + 2048 * (ks + 1), a);
 #pragma unroll
     for (int nb = 0; nb < kNb; ++nb) mma16816(s.v[nb], hi, b[nb >> 1][2 * (nb & 1)], b[nb >> 1][2 * (nb & 1) + 1]);
 #pragma unroll
     for (int nb = 0; nb < kNb; ++nb) mma16816(s.v[nb], lo, b[nb >> 1][2 * (nb & 1)], b[nb >> 1][2 * (nb & 1) + 1]);
-    if (kTerms == 3)
-#pragma unroll
-      for (int nb = 0; nb < kNb; ++nb) mma16816(s.v[nb], rest, b[nb >> 1][2 * (nb & 1)], b[nb >> 1][2 * (nb & 1) + 1]);
   }
+}
+// s = f s + sum_j w_j a_j b_j^T over the 64 rows j of two tiles, w in fp32 in
+// shared memory, as a sum of fp32 products: w_j a_j is formed in fp32 and goes
+// in as three bf16 terms, which hold all of its 24 bits, and the tiles' sum
+// starts from zero, because the tensor cores cut what they add to an
+// accumulator instead of rounding it (a state of 2,000 tokens was off by 3e-6
+// when they added to it, by 2e-7 this way).
+__device__ __forceinline__ void split3(float x, float y, uint32_t &hi, uint32_t &mid, uint32_t &lo) {
+  hi = tc::pack_bf16x2(x, y);
+  x -= __uint_as_float(hi << 16), y -= __uint_as_float(hi & 0xFFFF0000u);
+  mid = tc::pack_bf16x2(x, y);
+  x -= __uint_as_float(mid << 16), y -= __uint_as_float(mid & 0xFFFF0000u);
+  lo = tc::pack_bf16x2(x, y);
+}
+template <int kNb>
+__device__ __forceinline__ void state_step(StateAcc<kNb> &s, float f, int nb0, const void *a_tile, const void *b_tile,
+                                           const float *w) {
+  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3;
+  const int mat = lane >> 3, r = lane & 7, q = lane & 3;
+  const uint32_t at = tc::smem_u32(a_tile) + tile_at(8 * (mat >> 1) + r, 2 * warp + (mat & 1));
+  uint32_t bt[kNb / 2];
+#pragma unroll
+  for (int np = 0; np < kNb / 2; ++np)
+    bt[np] = tc::smem_u32(b_tile) + tile_at(8 * (mat & 1) + r, nb0 + 2 * np + (mat >> 1));
+  StateAcc<kNb> d = {};
+  uint32_t a[4], b[kNb / 2][4];
+  ldsm4t(at, a);
+#pragma unroll
+  for (int ks = 0; ks < 4; ++ks) {
+#pragma unroll
+    for (int np = 0; np < kNb / 2; ++np) ldsm4t(bt[np] + 2048 * ks, b[np]);
+    uint32_t t[3][4];
+    const float2 w0 = *reinterpret_cast<const float2 *>(w + 16 * ks + 2 * q);
+    const float2 w1 = *reinterpret_cast<const float2 *>(w + 16 * ks + 8 + 2 * q);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 x = e < 2 ? w0 : w1;
+      split3(__uint_as_float(a[e] << 16) * x.x, __uint_as_float(a[e] & 0xFFFF0000u) * x.y, t[0][e], t[1][e], t[2][e]);
+    }
+    if (ks < 3) ldsm4t(at + 2048 * (ks + 1), a);
+#pragma unroll
+    for (int z = 0; z < 3; ++z)
+#pragma unroll
+      for (int nb = 0; nb < kNb; ++nb) mma16816(d.v[nb], t[z], b[nb >> 1][2 * (nb & 1)], b[nb >> 1][2 * (nb & 1) + 1]);
+  }
+#pragma unroll
+  for (int nb = 0; nb < kNb; ++nb)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s.v[nb][e] = fmaf(f, s.v[nb][e], d.v[nb][e]);
 }
 template <int kNb>
 __device__ __forceinline__ void state_scale(StateAcc<kNb> &s, float f) {
@@ -150,13 +194,13 @@ __device__ __forceinline__ void state_round(const StateAcc<kNb> &s, int nb0, voi
           tc::pack_bf16x2(s.v[nb][2 * h], s.v[nb][2 * h + 1]);
 }
 
-// Decays from behind each token to the end of the chunk (out) and over the
+// Decays from behind a lane's two tokens to the end of the chunk, and over the
 // whole chunk (returned).
-__device__ __forceinline__ float gate_tails(const GateLane &x, PairWeights &out) {
+__device__ __forceinline__ float gate_tails(const GateLane &x, float2 &out) {
   const float eh = __shfl_sync(0xffffffffu, x.hi[1], 31), el = __shfl_sync(0xffffffffu, x.lo[1], 31);
   const int ec = __shfl_sync(0xffffffffu, x.cuts[1], 31);
-  weights_put(out, gate_exp_fast(x.cuts[0] == ec, (eh - x.hi[0]) + (el - x.lo[0])),
-              gate_exp_fast(x.cuts[1] == ec, (eh - x.hi[1]) + (el - x.lo[1])));
+  out = make_float2(gate_exp_fast(x.cuts[0] == ec, (eh - x.hi[0]) + (el - x.lo[0])),
+                    gate_exp_fast(x.cuts[1] == ec, (eh - x.hi[1]) + (el - x.lo[1])));
   return gate_exp_fast(ec == 0, eh + el);
 }
 

@@ -206,8 +206,9 @@ __global__ void __launch_bounds__(kThreads) gated_segment_kernel(GatedArgs p) {
 
 // z = 0: own states -> the state before each segment, forwards.  z = 1: own
 // gradients -> the gradient of the state behind each segment, backwards, and
-// dstate0.  In place.
-template <int kVec, int kAhead>
+// dstate0.  In place.  kLast: the last segment has its own state too, and the
+// state behind it is the result.
+template <int kVec, int kAhead, bool kLast>
 __global__ void __launch_bounds__(kScanThreads) gated_scan_kernel(GatedArgs p) {
   pdl_trigger();
   pdl_wait();
@@ -218,9 +219,10 @@ __global__ void __launch_bounds__(kScanThreads) gated_scan_kernel(GatedArgs p) {
   const float *from = grad ? p.dstate : p.state_in;
   const int count = grad && n == 0 ? 0 : last + 1;
   const auto run = scan_walk<kVec, kAhead>(s, p.seg_decay + (size_t)bh * p.nseg, from ? from + (size_t)bh * kGS + x : nullptr,
-                                           count, grad ? count : last, grad,   // (the last segment's own state is not formed)
+                                           count, grad || kLast ? count : last, grad,
                                            [&](int i, const ScanVec<kVec> &v) { scan_store(s + (size_t)i * kGS, v); });
   if (grad && p.dstate0) scan_store(p.dstate0 + (size_t)bh * kGS + x, run);
+  if (!grad && kLast) scan_store(p.state_out + (size_t)bh * kGS + x, run);
 }
 
 // Outputs of a segment, and the state behind the sequence's last one.
@@ -469,14 +471,17 @@ int gated_prefill_segment(int B, int Hkv, int T, int is_bf16) {
   const long long want = std::max<long long>(1, 3 * 152 / units);
   return (int)std::max<long long>(1, (chunks + want - 1) / want);
 }
-oal_status launch_gated_scan(const GatedArgs &p, int both, cudaStream_t stream) {
-  const int units = p.B * p.Hkv, ways = both ? 2 : 1;
+template <bool kLast>
+static oal_status launch_scan(const GatedArgs &p, int ways, cudaStream_t stream) {
+  const int units = p.B * p.Hkv;
   if (scan_deep(units * ways, p.nseg))
-    launch_pdl(gated_scan_kernel<2, 32>, dim3(units, kGS / 2 / kScanThreads, ways), dim3(kScanThreads), 0, stream, p);
+    launch_pdl(gated_scan_kernel<2, 32, kLast>, dim3(units, kGS / 2 / kScanThreads, ways), dim3(kScanThreads), 0, stream, p);
   else
-    launch_pdl(gated_scan_kernel<4, 8>, dim3(units, kGS / 4 / kScanThreads, ways), dim3(kScanThreads), 0, stream, p);
+    launch_pdl(gated_scan_kernel<4, 8, kLast>, dim3(units, kGS / 4 / kScanThreads, ways), dim3(kScanThreads), 0, stream, p);
   return oal_after_launch("gated_scan_kernel", stream);
 }
+// From the segments' own states to those before them and the last one.
+oal_status launch_gated_scan(const GatedArgs &p, cudaStream_t stream) { return launch_scan<true>(p, 1, stream); }
 
 oal_status launch_gated_prefill_simt(const GatedArgs &p, cudaStream_t stream) {
   static bool done_seg[kMaxDevices], done_out[kMaxDevices];
@@ -486,7 +491,7 @@ oal_status launch_gated_prefill_simt(const GatedArgs &p, cudaStream_t stream) {
   if (p.nseg > 1) {
     launch_pdl(gated_segment_kernel, dim3(p.nseg * p.B * p.Hkv), dim3(kThreads), seg_smem, stream, p);
     GATED_TRY(oal_after_launch("gated_segment_kernel", stream));
-    GATED_TRY(launch_gated_scan(p, 0, stream));
+    GATED_TRY(launch_scan<false>(p, 1, stream));
   }
   launch_pdl(gated_out_kernel, dim3(p.nseg * p.B * p.Hkv), dim3(kThreads), out_smem, stream, p);
   return oal_after_launch("gated_out_kernel", stream);
@@ -499,7 +504,7 @@ oal_status launch_gated_backward_simt(const GatedArgs &p, cudaStream_t stream) {
   GATED_TRY(gated_need_smem(reinterpret_cast<const void *>(gated_grad_kernel), grad_smem, done_grad));
   launch_pdl(gated_segment_kernel, dim3(p.nseg * p.B * p.Hkv, 2), dim3(kThreads), seg_smem, stream, p);
   GATED_TRY(oal_after_launch("gated_segment_kernel", stream));
-  GATED_TRY(launch_gated_scan(p, 1, stream));
+  GATED_TRY(launch_scan<false>(p, 2, stream));
   launch_pdl(gated_grad_kernel, dim3(p.nseg * p.B * p.Hkv), dim3(kThreads), grad_smem, stream, p);
   return oal_after_launch("gated_grad_kernel", stream);
 }

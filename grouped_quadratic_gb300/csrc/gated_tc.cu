@@ -1,8 +1,8 @@
 // gated_tc.cu -- the gated linear recurrence for bf16 on the tensor cores.
 //
 // Prefill.  gated_tc_segment_kernel forms the segments' own states,
-// gated_scan_kernel (gated_simt.cu) the state before each segment, and
-// gated_tc_out_kernel walks every segment: per chunk of 64 tokens and pair of
+// gated_scan_kernel (gated_simt.cu) the state before each segment and the last
+// one, and gated_tc_out_kernel walks every segment: per chunk of 64 tokens and pair of
 // query heads of the KV head (128 rows: 64 tokens of each)
 //     X = Q K^T,  D = Q S_in           tcgen05, operands as TMA left them
 //     P = X o decays (bf16)            four warps, tensor memory -> registers -> tensor memory
@@ -36,15 +36,14 @@ constexpr uint32_t kColX = 0, kColD = 64;
 constexpr int kGateBatch = 8;               // chunks whose decays are formed together, two a warp
 struct SegSmem {
   uint8_t a[kStages][kTileBytes], b[kStages][kTileBytes];
-  struct {
-    PairWeights tail;
-    float whole;
+  struct alignas(16) {
+    float tail[kGC], whole;               // e^{G_63-G_j}, e^{G_63}
   } gates[kGateBatch];
   uint64_t full[kStages];
   int abort_flag;
 };
 
-// Own state of each segment but a sequence's last: K and V once.  A chunk's
+// Own state of each segment: K and V once.  A chunk's
 // decays are a chain of shuffles as long as its products: eight chunks' are
 // formed side by side, or every chunk would wait for its own (22 us at
 // 4 x 8192 tokens, 8 KV heads, that way).
@@ -63,9 +62,9 @@ gated_tc_segment_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_co
   }
   pdl_wait();
   const int n = gated_len(p, b);
-  if (seg >= gated_last_seg(n, p.seg_chunks * kGC)) return;
+  if (seg > gated_last_seg(n, p.seg_chunks * kGC)) return;
   __syncthreads();
-  const int c0 = seg * p.seg_chunks, nc = p.seg_chunks;   // whole chunks: not the last segment
+  const int c0 = seg * p.seg_chunks, nc = max(0, min((n + kGC - 1) / kGC - c0, p.seg_chunks));
   volatile int *abort_flag = &s.abort_flag;
   auto load = [&](int c) {
     const int st = c % kStages;
@@ -86,17 +85,21 @@ gated_tc_segment_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_co
     if (c % kGateBatch == 0) {   // (the chunk before ended in a barrier)
       const GateLane s0 = gate_sums(gate0), s1 = gate_sums(gate1);
       auto &to0 = s.gates[warp], &to1 = s.gates[warp + 4];
-      to0.whole = gate_tails(s0, to0.tail);
-      to1.whole = gate_tails(s1, to1.tail);
+      to0.whole = gate_tails(s0, reinterpret_cast<float2 *>(to0.tail)[tid & 31]);
+      to1.whole = gate_tails(s1, reinterpret_cast<float2 *>(to1.tail)[tid & 31]);
       gate0 = gate_of(c + kGateBatch + warp), gate1 = gate_of(c + kGateBatch + warp + 4);
       __syncthreads();
     }
     const auto &gates = s.gates[c % kGateBatch];
     decay *= gates.whole;
-    state_scale(acc, gates.whole);
     ok = ok && mbar_wait(&s.full[c % kStages], (c / kStages) & 1, abort_flag, p.status);
     ok = __all_sync(0xffffffffu, ok);
-    if (ok) state_add<0, 4>(acc, 0, s.a[c % kStages], s.b[c % kStages], gates.tail);
+    if (n < p.T && (c0 + c + 1) * kGC > n) {   // rows behind the sequence count as zeros
+      clear_rows(s.a[c % kStages], n - (c0 + c) * kGC, tid, kSegThreads);
+      clear_rows(s.b[c % kStages], n - (c0 + c) * kGC, tid, kSegThreads);
+      __syncthreads();
+    }
+    if (ok) state_step(acc, gates.whole, 0, s.a[c % kStages], s.b[c % kStages], gates.tail);
     __syncthreads();
     if (tid == 0 && ok && c + kStages < nc) load(c + kStages);
   }
@@ -285,8 +288,7 @@ gated_tc_out_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
     const int i = tid & 63, half = warp & 1;            // token of this thread's row, its 32-token half
     const uint32_t tm = tb + ((uint32_t)(32 * warp) << 16);
     StateAcc<8> acc;
-    state_load(acc, 0, p.nseg > 1 ? p.seg_state + ((size_t)bh * p.nseg + seg) * kGS
-                               : p.state_in ? p.state_in + (size_t)bh * kGS : nullptr);
+    state_load(acc, 0, p.seg_state + ((size_t)bh * p.nseg + seg) * kGS);
     state_round(acc, 0, s.state);
     fence_proxy_async();
     __syncwarp();
@@ -445,7 +447,6 @@ gated_tc_out_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
       }
     }
     if (lane == 0) bulk_wait_all();
-    if (seg == last && ok) state_store(acc, 0, p.state_out + (size_t)bh * kGS);
   }
   tc_fence_before();
   __syncthreads();
@@ -457,7 +458,7 @@ gated_tc_out_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
 
 }  // namespace
 
-oal_status launch_gated_scan(const GatedArgs &p, int both, cudaStream_t stream);
+oal_status launch_gated_scan(const GatedArgs &p, cudaStream_t stream);
 
 oal_status launch_gated_prefill_tc(const GatedArgs &p, cudaStream_t stream) {
   static bool done_seg[kMaxDevices], done_out[kMaxDevices];
@@ -470,11 +471,9 @@ oal_status launch_gated_prefill_tc(const GatedArgs &p, cudaStream_t stream) {
   GATED_TRY(make_map(&tmV, p.V, p.T, (long long)p.B * p.Hkv));
   GATED_TRY(make_map(&tmY, p.Y, p.T, (long long)p.B * p.Hq, 32));
   const dim3 grid(p.nseg * p.B * p.Hkv);
-  if (p.nseg > 1) {
-    launch_pdl(gated_tc_segment_kernel, grid, dim3(kSegThreads), seg_smem, stream, tmK, tmV, p);
-    GATED_TRY(oal_after_launch("gated_tc_segment_kernel", stream));
-    GATED_TRY(launch_gated_scan(p, 0, stream));
-  }
+  launch_pdl(gated_tc_segment_kernel, grid, dim3(kSegThreads), seg_smem, stream, tmK, tmV, p);
+  GATED_TRY(oal_after_launch("gated_tc_segment_kernel", stream));
+  GATED_TRY(launch_gated_scan(p, stream));
   launch_pdl(gated_tc_out_kernel, grid, dim3(kOutThreads), out_smem, stream, tmQ, tmK, tmV, tmY, p);
   return oal_after_launch("gated_tc_out_kernel", stream);
 }

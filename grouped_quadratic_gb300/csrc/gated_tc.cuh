@@ -101,7 +101,9 @@ __device__ __forceinline__ void chunk_gates(float2 gate, const GateLane &sums, C
   const int lane = threadIdx.x & 31;
   const uint32_t even = __ballot_sync(0xffffffffu, gate.x <= kGateCut);
   const uint32_t odd = __ballot_sync(0xffffffffu, gate.y <= kGateCut);
-  const float whole = gate_tails(sums, to.tail);
+  float2 tail;
+  const float whole = gate_tails(sums, tail);
+  weights_put(to.tail, tail.x, tail.y);
   const float mh = __shfl_sync(0xffffffffu, sums.hi[1], 15), ml = __shfl_sync(0xffffffffu, sums.lo[1], 15);
   const float span = fmaxf(fabsf(sums.hi[0]), fabsf(sums.hi[1]));
   const bool plain = __all_sync(0xffffffffu, span <= kSpan) && (even | odd) == 0u;

@@ -31,7 +31,7 @@ constexpr int kOwnThreads = 128;
 template <int kOwnStages>
 struct OwnSmem {
   uint8_t a[kOwnStages][kTileBytes], b[kOwnStages][kTileBytes];
-  PairWeights w;
+  alignas(16) float w[kGC];
   uint64_t full[kOwnStages];
   int abort_flag;
 };
@@ -70,11 +70,12 @@ gated_tc_own_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
   if (tid < 32) {
     const GateLane sums = gate_sums(gate_load(p.g + (size_t)bh * p.T, t0, n));
     if (!grad) {
-      const float whole = gate_tails(sums, s.w);
+      const float whole = gate_tails(sums, reinterpret_cast<float2 *>(s.w)[tid]);
       if (tid == 0) p.seg_decay[(size_t)bh * p.nseg + c] = whole;
     } else {
-      weights_put(s.w, p.scale * gate_exp_fast(sums.cuts[0] == 0, sums.hi[0] + sums.lo[0]),
-                  p.scale * gate_exp_fast(sums.cuts[1] == 0, sums.hi[1] + sums.lo[1]));
+      reinterpret_cast<float2 *>(s.w)[tid] =
+          make_float2(p.scale * gate_exp_fast(sums.cuts[0] == 0, sums.hi[0] + sums.lo[0]),
+                      p.scale * gate_exp_fast(sums.cuts[1] == 0, sums.hi[1] + sums.lo[1]));
     }
   }
   __syncthreads();
@@ -91,7 +92,7 @@ gated_tc_own_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
       fence_proxy_async();
       __syncthreads();
     }
-    if (ok) state_add<0, 4, 3>(acc, 0, s.a[st], s.b[st], s.w);
+    if (ok) state_step(acc, 1.f, 0, s.a[st], s.b[st], s.w);
     __syncthreads();
     if (tid == 0 && ok && r + kOwnStages < count) load(r + kOwnStages);
   }
@@ -322,11 +323,7 @@ gated_tc_grad_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
       const GateLane sums = gate_sums(gate);
       GradSmem::Gates &to = s.gates[k & 1];
       chunk_gates(gate, sums, to.c);
-      const float eh = __shfl_sync(0xffffffffu, sums.hi[1], 31), el = __shfl_sync(0xffffffffu, sums.lo[1], 31);
-      const int ec = __shfl_sync(0xffffffffu, sums.cuts[1], 31);
-      reinterpret_cast<float2 *>(to.tail)[lane] =
-          make_float2(gate_exp_fast(sums.cuts[0] == ec, (eh - sums.hi[0]) + (el - sums.lo[0])),
-                      gate_exp_fast(sums.cuts[1] == ec, (eh - sums.hi[1]) + (el - sums.lo[1])));
+      gate_tails(sums, reinterpret_cast<float2 *>(to.tail)[lane]);
       reinterpret_cast<float2 *>(to.head)[lane] = make_float2(gate_exp_fast(sums.cuts[0] == 0, sums.hi[0] + sums.lo[0]),
                                                               gate_exp_fast(sums.cuts[1] == 0, sums.hi[1] + sums.lo[1]));
       arrive(&s.gate_full);

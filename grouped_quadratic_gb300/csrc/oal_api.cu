@@ -472,7 +472,6 @@ size_t oal_gated_prefill_workspace_bytes(int B, int Hq, int Hkv, int T, int d, i
   if (B == 0 || T == 0) return 256;
   const int chunks = oal::gated_prefill_segment(B, Hkv, T, dtype == OAL_BF16);
   const int nseg = oal::gated_segments(T, chunks);
-  if (nseg == 1) return 256;
   return gated_states_bytes(B, Hkv, nseg) + round256((size_t)B * Hkv * nseg * sizeof(float));
 }
 
