@@ -3,8 +3,8 @@
 // 16-byte chunk c of row r at chunk c ^ (r & 7), as a 128-byte-swizzled TMA
 // copy leaves it).
 //
-// The states live in registers, split over four or eight warps (warp w owns
-// rows 16 (w % 4) .. + 15 of all columns or of half of them), because every chunk scales them by a decay and adds a
+// The states live in registers, split over four warps (warp w owns rows
+// 16 w .. 16 w + 15), because every chunk scales them by a decay and adds a
 // product: in tensor memory that would be a read and a write of the state per
 // chunk besides the product.
 #pragma once

@@ -252,8 +252,11 @@ oal_status oal_decode_step(const void *q, const void *k, const void *v,
  *  workspace  >= oal_gated_prefill_workspace_bytes(...) bytes, 256-byte
  *           aligned, contents need not be initialised.  Calls that may
  *           overlap on the GPU (streams, captured graphs) need one each.
- * Arithmetic: fp32 sums and states.  T == 0 leaves Y untouched and zeroes
- * the state unless continue_from_state != 0.
+ * Arithmetic: OAL_F32 in fp32 on the CUDA cores.  OAL_BF16 on the tensor
+ * cores with fp32 accumulation: the states are sums of fp32 products; the
+ * decayed scores and the state a chunk reads are rounded to bf16 once each.
+ * Deterministic.  T == 0 leaves Y untouched and zeroes the state unless
+ * continue_from_state != 0.
  */
 size_t oal_gated_prefill_workspace_bytes(int B, int Hq, int Hkv, int T, int d, int dv,
                                          oal_dtype dtype);
@@ -276,7 +279,10 @@ oal_status oal_gated_prefill(const void *Q, const void *K, const void *V, oal_dt
  *           state0, or NULL if not wanted.  No output may overlap an input or
  *           another output.  Rows behind a sequence's length
  *           are neither read nor written.
- * Deterministic: no atomics on the outputs.  T == 0: dstate0 = dstate.
+ * Arithmetic: as for the prefill; bf16: the decayed score gradients are
+ * rounded to bf16 for dQ and dK, the decayed scores for dV, and the states and
+ * their gradients enter as two bf16 terms (2^-16); dg is formed from unrounded
+ * scores.  Deterministic: no atomics on the outputs.  T == 0: dstate0 = dstate.
  */
 size_t oal_gated_backward_workspace_bytes(int B, int Hq, int Hkv, int T, int d, int dv,
                                           oal_dtype dtype);
