@@ -204,12 +204,64 @@ __device__ __forceinline__ ScanVec<kVec> scan_walk(const float *own, const float
   }
   return run;
 }
-// Few states and many segments: more threads a state and more loads ahead (205
-// segments of 2 states: 16 us against 22 with loads of 8 ahead); otherwise the
-// states' own number fills the GPU (64 chunks of 32 states, both ways: 22 us
-// against 27 the other way).
-inline bool scan_deep(int states, int segments) { return states <= 16 && segments > 16; }
+// The same walk by kChains threads a value, each over kAhead segments of a
+// round at a time: its part's decay and sum first, then, from the parts before
+// it, the states.  All of a round's loads are in flight together.  The threads
+// of a block are kChains groups of kScanThreads / kChains; all get the result.
 constexpr int kScanThreads = 128;
+template <int kVec, int kAhead, int kChains, typename Put>
+__device__ __forceinline__ ScanVec<kVec> scan_split(const float *own, const float *decay, const float *from, int count,
+                                                    int formed, bool back, Put put) {
+  constexpr int kLanes = kScanThreads / kChains;
+  __shared__ float s_decay[kChains];
+  __shared__ ScanVec<kVec> s_sum[kChains][kLanes];
+  const int chain = threadIdx.x / kLanes, lane = threadIdx.x % kLanes;
+  ScanVec<kVec> run = {};
+  if (from) run = scan_load<kVec>(from);
+  for (int i0 = 0; i0 < count; i0 += kAhead * kChains) {
+    const int first = i0 + chain * kAhead;
+    ScanVec<kVec> v[kAhead], sum = {};
+    float f[kAhead], all = 1.f;
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int i = back ? count - 1 - first - k : first + k;
+      v[k] = {};
+      f[k] = 1.f;
+      if (first + k < formed) v[k] = scan_load<kVec>(own + (size_t)i * kGS), f[k] = decay[i];
+    }
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+#pragma unroll
+      for (int e = 0; e < kVec; ++e) sum.v[e] = fmaf(f[k], sum.v[e], v[k].v[e]);
+      all *= f[k];
+    }
+    __syncthreads();
+    if (lane == 0) s_decay[chain] = all;
+    s_sum[chain][lane] = sum;
+    __syncthreads();
+    ScanVec<kVec> in = run;
+#pragma unroll
+    for (int z = 0; z < kChains; ++z) {
+      if (z == chain) in = run;
+      const ScanVec<kVec> part = s_sum[z][lane];
+#pragma unroll
+      for (int e = 0; e < kVec; ++e) run.v[e] = fmaf(s_decay[z], run.v[e], part.v[e]);
+    }
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+      if (first + k < count) {
+        put(back ? count - 1 - first - k : first + k, in);
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) in.v[e] = fmaf(f[k], in.v[e], v[k].v[e]);
+      }
+  }
+  return run;
+}
+// Few states and many segments: the split walk (205 segments of 2 states: 8 us
+// against 16 by one thread a value with 32 loads ahead, 22 with 8); otherwise
+// the states' own number fills the GPU.
+inline bool scan_deep(int states, int segments) { return states <= 16 && segments > 16; }
+constexpr int kScanChains = 8;
 
 }  // namespace oal
 

@@ -208,19 +208,23 @@ __global__ void __launch_bounds__(kThreads) gated_segment_kernel(GatedArgs p) {
 // gradients -> the gradient of the state behind each segment, backwards, and
 // dstate0.  In place.  kLast: the last segment has its own state too, and the
 // state behind it is the result.
-template <int kVec, int kAhead, bool kLast>
+template <int kVec, int kAhead, int kChains, bool kLast>
 __global__ void __launch_bounds__(kScanThreads) gated_scan_kernel(GatedArgs p) {
   pdl_trigger();
   pdl_wait();
-  const int bh = blockIdx.x, x = kVec * (blockIdx.y * kScanThreads + threadIdx.x);
+  constexpr int kLanes = kScanThreads / kChains;
+  const int bh = blockIdx.x, x = kVec * (blockIdx.y * kLanes + threadIdx.x % kLanes);
   const int n = gated_len(p, bh / p.Hkv), last = gated_last_seg(n, p.seg_chunks * kGC);
   const bool grad = blockIdx.z != 0;
   float *s = (grad ? p.seg_grad : p.seg_state) + (size_t)bh * p.nseg * kGS + x;
-  const float *from = grad ? p.dstate : p.state_in;
-  const int count = grad && n == 0 ? 0 : last + 1;
-  const auto run = scan_walk<kVec, kAhead>(s, p.seg_decay + (size_t)bh * p.nseg, from ? from + (size_t)bh * kGS + x : nullptr,
-                                           count, grad || kLast ? count : last, grad,
-                                           [&](int i, const ScanVec<kVec> &v) { scan_store(s + (size_t)i * kGS, v); });
+  const float *from = grad ? p.dstate : p.state_in, *decay = p.seg_decay + (size_t)bh * p.nseg;
+  if (from) from += (size_t)bh * kGS + x;
+  const int count = grad && n == 0 ? 0 : last + 1, formed = grad || kLast ? count : last;
+  auto put = [&](int i, const ScanVec<kVec> &v) { scan_store(s + (size_t)i * kGS, v); };
+  ScanVec<kVec> run;
+  if constexpr (kChains == 1) run = scan_walk<kVec, kAhead>(s, decay, from, count, formed, grad, put);
+  else run = scan_split<kVec, kAhead, kChains>(s, decay, from, count, formed, grad, put);
+  if (threadIdx.x >= kLanes) return;
   if (grad && p.dstate0) scan_store(p.dstate0 + (size_t)bh * kGS + x, run);
   if (!grad && kLast) scan_store(p.state_out + (size_t)bh * kGS + x, run);
 }
@@ -475,9 +479,10 @@ template <bool kLast>
 static oal_status launch_scan(const GatedArgs &p, int ways, cudaStream_t stream) {
   const int units = p.B * p.Hkv;
   if (scan_deep(units * ways, p.nseg))
-    launch_pdl(gated_scan_kernel<2, 32, kLast>, dim3(units, kGS / 2 / kScanThreads, ways), dim3(kScanThreads), 0, stream, p);
+    launch_pdl(gated_scan_kernel<2, 32, kScanChains, kLast>, dim3(units, kGS / 2 * kScanChains / kScanThreads, ways),
+               dim3(kScanThreads), 0, stream, p);
   else
-    launch_pdl(gated_scan_kernel<4, 8, kLast>, dim3(units, kGS / 4 / kScanThreads, ways), dim3(kScanThreads), 0, stream, p);
+    launch_pdl(gated_scan_kernel<4, 8, 1, kLast>, dim3(units, kGS / 4 / kScanThreads, ways), dim3(kScanThreads), 0, stream, p);
   return oal_after_launch("gated_scan_kernel", stream);
 }
 // From the segments' own states to those before them and the last one.

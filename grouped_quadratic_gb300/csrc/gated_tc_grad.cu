@@ -107,36 +107,39 @@ gated_tc_own_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
 // z = 0: the state before each chunk, forwards; 1: the gradient of the state
 // behind each, backwards, and dstate0; as a word each of the hi and lo tiles
 // for two neighbouring values.
-template <int kVec, int kAhead>
+template <int kVec, int kAhead, int kChains>
 __global__ void __launch_bounds__(kScanThreads) gated_tc_scan_kernel(GatedArgs p) {
   pdl_trigger();
   pdl_wait();
-  const int bh = blockIdx.x, x = kVec * (blockIdx.y * kScanThreads + threadIdx.x);
+  constexpr int kLanes = kScanThreads / kChains;
+  const int bh = blockIdx.x, x = kVec * (blockIdx.y * kLanes + threadIdx.x % kLanes);
   const bool grad = blockIdx.z != 0;
   const int n = gated_len(p, bh / p.Hkv), count = (n + kGC - 1) / kGC;
   const float *own = (grad ? p.seg_grad : p.seg_state) + (size_t)bh * p.nseg * kGS + x;
   uint8_t *tiles = (grad ? p.grad_tiles : p.state_tiles) + (size_t)bh * p.nseg * 2 * kTileBytes +
                    tile_at(x >> 6, (x & 63) >> 3) + 2 * (x & 7);
-  const float *from = grad ? p.dstate : p.state_in;
-  const auto run = scan_walk<kVec, kAhead>(
-      own, p.seg_decay + (size_t)bh * p.nseg, from ? from + (size_t)bh * kGS + x : nullptr, count, count, grad,
-      [&](int i, const ScanVec<kVec> &v) {
-        uint8_t *at = tiles + (size_t)i * 2 * kTileBytes;
-        uint32_t hi[kVec / 2], lo[kVec / 2];
+  const float *from = grad ? p.dstate : p.state_in, *decay = p.seg_decay + (size_t)bh * p.nseg;
+  if (from) from += (size_t)bh * kGS + x;
+  auto put = [&](int i, const ScanVec<kVec> &v) {
+    uint8_t *at = tiles + (size_t)i * 2 * kTileBytes;
+    uint32_t hi[kVec / 2], lo[kVec / 2];
 #pragma unroll
-        for (int e = 0; e < kVec / 2; ++e) {
-          hi[e] = pack_bf16x2(v.v[2 * e], v.v[2 * e + 1]);
-          lo[e] = pack_bf16x2(v.v[2 * e] - __uint_as_float(hi[e] << 16), v.v[2 * e + 1] - __uint_as_float(hi[e] & 0xFFFF0000u));
-        }
-        if (kVec == 4) {
-          *reinterpret_cast<uint2 *>(at) = make_uint2(hi[0], hi[kVec / 2 - 1]);
-          *reinterpret_cast<uint2 *>(at + kTileBytes) = make_uint2(lo[0], lo[kVec / 2 - 1]);
-        } else {
-          *reinterpret_cast<uint32_t *>(at) = hi[0];
-          *reinterpret_cast<uint32_t *>(at + kTileBytes) = lo[0];
-        }
-      });
-  if (grad && p.dstate0) scan_store(p.dstate0 + (size_t)bh * kGS + x, run);
+    for (int e = 0; e < kVec / 2; ++e) {
+      hi[e] = pack_bf16x2(v.v[2 * e], v.v[2 * e + 1]);
+      lo[e] = pack_bf16x2(v.v[2 * e] - __uint_as_float(hi[e] << 16), v.v[2 * e + 1] - __uint_as_float(hi[e] & 0xFFFF0000u));
+    }
+    if (kVec == 4) {
+      *reinterpret_cast<uint2 *>(at) = make_uint2(hi[0], hi[kVec / 2 - 1]);
+      *reinterpret_cast<uint2 *>(at + kTileBytes) = make_uint2(lo[0], lo[kVec / 2 - 1]);
+    } else {
+      *reinterpret_cast<uint32_t *>(at) = hi[0];
+      *reinterpret_cast<uint32_t *>(at + kTileBytes) = lo[0];
+    }
+  };
+  ScanVec<kVec> run;
+  if constexpr (kChains == 1) run = scan_walk<kVec, kAhead>(own, decay, from, count, count, grad, put);
+  else run = scan_split<kVec, kAhead, kChains>(own, decay, from, count, count, grad, put);
+  if (grad && p.dstate0 && threadIdx.x < kLanes) scan_store(p.dstate0 + (size_t)bh * kGS + x, run);
 }
 
 // ---------------------------------------------------------------- gradients
@@ -715,9 +718,10 @@ oal_status launch_gated_backward_tc(const GatedArgs &p, cudaStream_t stream) {
   GATED_TRY(oal_after_launch("gated_tc_own_kernel", stream));
   const int units = p.B * p.Hkv;
   if (scan_deep(2 * units, p.nseg))
-    launch_pdl(gated_tc_scan_kernel<2, 32>, dim3(units, kGS / 2 / kScanThreads, 2), dim3(kScanThreads), 0, stream, p);
+    launch_pdl(gated_tc_scan_kernel<2, 32, kScanChains>, dim3(units, kGS / 2 * kScanChains / kScanThreads, 2),
+               dim3(kScanThreads), 0, stream, p);
   else
-    launch_pdl(gated_tc_scan_kernel<4, 8>, dim3(units, kGS / 4 / kScanThreads, 2), dim3(kScanThreads), 0, stream, p);
+    launch_pdl(gated_tc_scan_kernel<4, 8, 1>, dim3(units, kGS / 4 / kScanThreads, 2), dim3(kScanThreads), 0, stream, p);
   GATED_TRY(oal_after_launch("gated_tc_scan_kernel", stream));
   launch_pdl(gated_tc_grad_kernel, dim3(std::min(total, 2 * 152)), dim3(kGradThreads), grad_smem, stream, tmQ, tmK, tmV,
              tmO, tmDQ, p);
