@@ -17,12 +17,11 @@ namespace oal {
 namespace {
 
 constexpr int kMoveThreads = 1024;
-constexpr int kMoveWords = 8;                           // words a thread holds
-constexpr int kMoveMost = kMoveThreads * kMoveWords;    // words a block holds
+constexpr int kMoveMost = OAL_REMAP_MAX_SLOTS;           // one word of each slot at least
 
 // Word: the widest type that slot_bytes is a multiple of (a packed prefix
 // state has 557,700 bytes a head, so slots need not start on 16).
-template <typename Word>
+template <typename Word, int kWords, bool kAhead>
 __global__ void __launch_bounds__(kMoveThreads)
 state_remap_kernel(Word *pool, long long slot_words, int n, const int32_t *__restrict__ map, int *status) {
   pdl_trigger();
@@ -47,44 +46,69 @@ state_remap_kernel(Word *pool, long long slot_words, int n, const int32_t *__res
   // words of a slice: as many as the block holds, at most what spreads the
   // slot over the grid
   const long long spread = (slot_words + gridDim.x - 1) / gridDim.x;
-  const int width = (int)min((long long)(kMoveMost / max(count, 1)), spread);
-  const int total = width * count;
-  for (long long w0 = (long long)blockIdx.x * width; w0 < slot_words; w0 += (long long)gridDim.x * width) {
+  const int width = (int)min((long long)(kWords * kMoveThreads / max(count, 1)), spread);
+  const long long step = (long long)gridDim.x * width;
+  // this thread's words of every slice: the move, and the place in the slice
+  // (16 bits each; past the last move: past the slice)
+  uint32_t at[kWords];
+#pragma unroll
+  for (int k = 0; k < kWords; ++k) {
+    const int x = threadIdx.x + k * kMoveThreads, m = x / width;
+    at[k] = m < count ? (uint32_t)m << 16 | (uint32_t)(x - m * width) : 0xFFFFu;
+  }
+  auto gather = [&](long long w0, Word (&held)[kWords]) {
+    const int wide = (int)max(0LL, min((long long)width, slot_words - w0));
+#pragma unroll
+    for (int k = 0; k < kWords; ++k)
+      if ((int)(at[k] & 0xFFFFu) < wide) held[k] = pool[s_move[at[k] >> 16].y * slot_words + (w0 + (at[k] & 0xFFFFu))];
+  };
+  auto scatter = [&](long long w0, const Word (&held)[kWords]) {
     const int wide = (int)min((long long)width, slot_words - w0);
-    Word held[kMoveWords];
 #pragma unroll
-    for (int k = 0; k < kMoveWords; ++k) {
-      const int x = threadIdx.x + k * kMoveThreads, m = x / width, w = x - m * width;
-      if (x < total && w < wide) held[k] = pool[(long long)s_move[m].y * slot_words + w0 + w];
-    }
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < kMoveWords; ++k) {
-      const int x = threadIdx.x + k * kMoveThreads, m = x / width, w = x - m * width;
-      if (x < total && w < wide) pool[(long long)s_move[m].x * slot_words + w0 + w] = held[k];
-    }
+    for (int k = 0; k < kWords; ++k)
+      if ((int)(at[k] & 0xFFFFu) < wide) pool[s_move[at[k] >> 16].x * slot_words + (w0 + (at[k] & 0xFFFFu))] = held[k];
     for (int x = threadIdx.x; x < zeros * width; x += kMoveThreads) {
       const int m = x / width, w = x - m * width;
-      if (w < wide) pool[(long long)s_move[n - 1 - m].x * slot_words + w0 + w] = Word();
+      if (w < wide) pool[s_move[n - 1 - m].x * slot_words + w0 + w] = Word();
     }
+  };
+  // (kAhead: the next slice is on its way while this one is written)
+  Word held[kAhead ? 2 : 1][kWords];
+  long long w0 = (long long)blockIdx.x * width;
+  if (kAhead) gather(w0, held[0]);
+  for (; w0 < slot_words; w0 += step) {
+    if (!kAhead) gather(w0, held[0]);
+    __syncthreads();                     // the slice at w0 is read by all
+    if (kAhead) gather(w0 + step, held[kAhead]);
+    scatter(w0, held[0]);
+    if (!kAhead) continue;
+    w0 += step;
+    if (w0 >= slot_words) break;
+    __syncthreads();
+    gather(w0 + step, held[0]);
+    scatter(w0, held[kAhead]);
   }
 }
 
 template <typename Word>
 oal_status remap(void *pool, size_t slot_bytes, int n, const int32_t *map, int *status, cudaStream_t stream) {
-  static bool done[kMaxDevices];
+  static bool done[2][kMaxDevices];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices)
     return oal_fail(OAL_ERR_CUDA, "no current device");
-  if (!done[dev]) {
-    if (cudaFuncSetAttribute(state_remap_kernel<Word>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)(kMoveMost * sizeof(int2))) != cudaSuccess)
+  // Four words a thread and two slices in flight; more slots than that has
+  // words for take eight and one slice.
+  const bool few = n <= 4 * kMoveThreads;
+  const auto kernel = few ? state_remap_kernel<Word, 4, true> : state_remap_kernel<Word, 8, false>;
+  if (!done[few][dev]) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(kMoveMost * sizeof(int2))) !=
+        cudaSuccess)
       return oal_check_launch("shared memory of the remap kernel");
-    done[dev] = true;
+    done[few][dev] = true;
   }
   const long long words = (long long)(slot_bytes / sizeof(Word));
-  const int blocks = (int)std::min<long long>(words, 2 * 152);
-  launch_pdl(state_remap_kernel<Word>, dim3(blocks), dim3(kMoveThreads), (size_t)n * sizeof(int2), stream,
+  const int blocks = (int)std::min<long long>(words, 152);
+  launch_pdl(kernel, dim3(blocks), dim3(kMoveThreads), (size_t)n * sizeof(int2), stream,
              static_cast<Word *>(pool), words, n, map, status);
   return oal_after_launch("state_remap_kernel", stream);
 }
