@@ -3,7 +3,8 @@
 // per (sequence, KV head), the state of sequence b in slot slots[b] of a pool.
 //
 // The state is read and written once (32 KB a unit), q, k, v and y are small:
-// HBM-bound for a batch, a few dependent loads long for one sequence.  A
+// HBM-bound for a batch, a few dependent loads long for one sequence (3.1 us
+// for 2 units, 5.0 for 512, 10.5 for 2408: 77 MB that stay in L2).  A
 // block holds its part of the state in registers: thread (row group, column
 // group) owns kRows rows of 4 columns, all of whose loads are in flight
 // before the first use.

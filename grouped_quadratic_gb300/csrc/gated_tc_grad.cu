@@ -38,6 +38,9 @@ struct OwnSmem {
 
 // blockIdx.y = 0: sum_j e^{G_63-G_j} k_j v_j^T of the chunk, and its decay;
 // 1: scale sum_i e^{G_i} q_i dy_i^T over the query heads of the KV head.
+// 51 us for 4 x 4096 tokens, 32/8 heads (168 MB in, 67 MB out: 4.6 TB/s); the
+// products (mma.sync at a quarter of tcgen05's rate) and the splitting of
+// their factors take about as long as the memory does.
 template <int kOwnStages>
 __global__ void __launch_bounds__(kOwnThreads)
 gated_tc_own_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -106,7 +109,8 @@ gated_tc_own_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
 
 // z = 0: the state before each chunk, forwards; 1: the gradient of the state
 // behind each, backwards, and dstate0; as a word each of the hi and lo tiles
-// for two neighbouring values.
+// for two neighbouring values.  HBM-bound: 20 us for 2048 chunks both ways
+// (134 MB, 6.7 TB/s).
 template <int kVec, int kAhead, int kChains>
 __global__ void __launch_bounds__(kScanThreads) gated_tc_scan_kernel(GatedArgs p) {
   pdl_trigger();
@@ -231,6 +235,12 @@ __device__ __noinline__ void fetch_heads(const CUtensorMap *tmO, const CUtensorM
   }
 }
 
+// 88 us for 4 x 4096 tokens, 32/8 heads (306 MB: 3.5 TB/s).  Bound by the chain
+// of a step - tile loads, X and Z, p and z, 20 MMAs, dQ - about 10,000 cycles a
+// pair of heads where two blocks per SM leave 5,000; tensor pipe 23% busy,
+// shared memory 30%, instruction fetches from behind the SM's cache 40% of what
+// that path can do (66% at 68 KB of code, before its rare paths went out of
+// line).
 __global__ void __launch_bounds__(kGradThreads, 2)
 gated_tc_grad_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                      const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,

@@ -8,7 +8,10 @@
 // not meet, so no block waits for another, and no workspace is needed.  Each
 // moved slot's source is read once and its target written once: HBM-bound.
 // The fewer slots move, the longer the runs of a slice: 512 moving slots leave
-// runs of 256 bytes, 64 of 2 KB.
+// runs of 128 bytes, 64 of 1 KB.  26 us for 64 slots of 1.1 MB (4.5 TB/s, in
+// 8-byte words, as such slots start on 8), 37 us for 512 moves and 512 zeros
+// of 131 KB (5.4 TB/s).  Words placed anew for every slice, with a division
+// each, cost 20% more.
 #include <algorithm>
 
 #include "gated.cuh"

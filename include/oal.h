@@ -249,6 +249,7 @@ oal_status oal_decode_step(const void *q, const void *k, const void *v,
  *           clamped and recorded in the device status word
  *           (OAL_ERR_INVALID_ARG at oal_sync_status).
  *  state    in/out; continue_from_state != 0 starts from it, 0 from zeros.
+ *           Neither it nor Y may overlap an input or the other.
  *  workspace  >= oal_gated_prefill_workspace_bytes(...) bytes, 256-byte
  *           aligned, contents need not be initialised.  Calls that may
  *           overlap on the GPU (streams, captured graphs) need one each.
