@@ -42,7 +42,7 @@ struct GatedArgs {
 };
 
 // Segment sizes in chunks (gated_simt.cu), and how many of them T tokens have.
-int gated_prefill_segment(int B, int Hkv, int T, int is_bf16);
+int gated_prefill_segment(int B, int Hkv, int T);
 inline int gated_segments(int T, int seg_chunks) {
   const int chunks = (int)(((long long)T + kGC - 1) / kGC);
   return (chunks + seg_chunks - 1) / seg_chunks;

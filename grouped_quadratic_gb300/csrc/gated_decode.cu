@@ -3,11 +3,12 @@
 // per (sequence, KV head), the state of sequence b in slot slots[b] of a pool.
 //
 // The state is read and written once (32 KB a unit), q, k, v and y are small:
-// HBM-bound for a batch, a few dependent loads long for one sequence (3.1 us
-// for 2 units, 5.0 for 512, 10.5 for 2408: 77 MB that stay in L2).  A
-// block holds its part of the state in registers: thread (row group, column
+// HBM-bound for a batch, a few dependent loads long for one sequence.  One
+// block a unit holds the state in registers: thread (row group, column
 // group) owns kRows rows of 4 columns, all of whose loads are in flight
-// before the first use.
+// before the first use.  Replayed with the states in L2: 2.6 us for 2 units,
+// 4.9 for 512, 18 for 4096; four blocks a unit, 16 columns each, took 2.9,
+// 6.8 and 37, and with cold states were ahead at no number of units either.
 #include "gated.cuh"
 
 namespace oal {
@@ -16,8 +17,7 @@ namespace {
 constexpr int kDecThreads = 128;
 constexpr int kHeads = 8;                // query heads read out together
 
-// Split: blocks a state is cut into, by columns of the state (values).
-template <typename T, int kSplit>
+template <typename T>
 __global__ void __launch_bounds__(kDecThreads)
 gated_decode_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ v,
                     const float *__restrict__ g, int B, int Hq, int Hkv, float scale,
@@ -25,11 +25,11 @@ gated_decode_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *_
                     T *__restrict__ y, int *status) {
   pdl_trigger();
   pdl_wait();
-  constexpr int kCols = kDv / kSplit, kCg = kCols / 4, kRg = kDecThreads / kCg, kRows = kD / kRg;
+  constexpr int kCols = kDv, kCg = kCols / 4, kRg = kDecThreads / kCg, kRows = kD / kRg;
   constexpr int kWarps = kDecThreads / 32;
   __shared__ float s_q[kHeads][kD];
   __shared__ float s_red[kWarps][kHeads][kCols];
-  const int unit = blockIdx.x / kSplit, part = blockIdx.x % kSplit;
+  const int unit = blockIdx.x;
   const int b = unit / Hkv, kv = unit % Hkv, rho = Hq / Hkv;
   const int tid = threadIdx.x, cg = tid % kCg, rg = tid / kCg;
   int slot = b;
@@ -43,11 +43,11 @@ gated_decode_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *_
     if (bad && tid == 0) atomicCAS(status, kStatusOk, (int)OAL_ERR_INVALID_ARG);
     if (bad || slot == -1) {   // no state: zeros
       for (int x = tid; x < rho * kCols; x += kDecThreads)
-        y[((size_t)b * Hq + kv * rho + x / kCols) * 64 + part * kCols + x % kCols] = from_f32<T>(0.f);
+        y[((size_t)b * Hq + kv * rho + x / kCols) * 64 + x % kCols] = from_f32<T>(0.f);
       return;
     }
   }
-  float *s = state + ((size_t)slot * Hkv + kv) * kGS + part * kCols + 4 * cg;
+  float *s = state + ((size_t)slot * Hkv + kv) * kGS + 4 * cg;
   float4 S[kRows];
 #pragma unroll
   for (int r = 0; r < kRows; ++r) S[r] = *reinterpret_cast<const float4 *>(s + (rg * kRows + r) * 64);
@@ -55,7 +55,7 @@ gated_decode_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *_
   const float a = expf(__ldg(g + unit));
   float vv[4], kk[kRows];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) vv[e] = to_f32(v[kvrow + part * kCols + 4 * cg + e]);
+  for (int e = 0; e < 4; ++e) vv[e] = to_f32(v[kvrow + 4 * cg + e]);
 #pragma unroll
   for (int r = 0; r < kRows; ++r) kk[r] = to_f32(k[kvrow + rg * kRows + r]);
 #pragma unroll
@@ -93,15 +93,12 @@ gated_decode_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *_
       float o = 0.f;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) o += s_red[w][h][c];
-      y[qrow + h * 64 + part * kCols + c] = from_f32<T>(scale * o);
+      y[qrow + h * 64 + c] = from_f32<T>(scale * o);
     }
   }
 }
 
 }  // namespace
-
-// Four blocks a state where one block each would leave most SMs idle.
-static int decode_split(int units) { return units <= 152 ? 4 : 1; }
 
 template <typename T>
 static oal_status run(const void *q, const void *k, const void *v, const float *g, int B, int Hq, int Hkv,
@@ -109,9 +106,7 @@ static oal_status run(const void *q, const void *k, const void *v, const float *
                       cudaStream_t stream) {
   int *status = oal_device_status_word();
   if (!status) return oal_fail(OAL_ERR_CUDA, "no device status word");
-  const int units = B * Hkv, split = decode_split(units);
-  auto kernel = split == 4 ? gated_decode_kernel<T, 4> : gated_decode_kernel<T, 1>;
-  launch_pdl(kernel, dim3(units * split), dim3(kDecThreads), 0, stream, static_cast<const T *>(q),
+  launch_pdl(gated_decode_kernel<T>, dim3(B * Hkv), dim3(kDecThreads), 0, stream, static_cast<const T *>(q),
              static_cast<const T *>(k), static_cast<const T *>(v), g, B, Hq, Hkv, scale, slots, n_slots,
              state, static_cast<T *>(y), status);
   return oal_after_launch("gated_decode_kernel", stream);

@@ -470,10 +470,13 @@ oal_status gated_need_smem(const void *kernel, size_t bytes, bool (&done)[kMaxDe
   return OAL_OK;
 }
 
-// As many segments as give three blocks per SM one wave; one segment, and so
-// one launch, where the (batch, KV head) units alone are that many.
-int gated_prefill_segment(int B, int Hkv, int T, int is_bf16) {
-  (void)is_bf16;
+// As many segments as give three blocks per SM one wave: what is resident in
+// the bf16 output kernel.  Blocks a segment at 2, 2.5, 3, 4 and 6 per SM, us:
+// 4 x 32/8 heads x 8192 tokens 97, 92, 84, 95, 87; 65536 tokens 77, 76, 68,
+// 84, 76; 4 x 16/16 x 4096 75, 73, 63, 70, 66; 8 x 32/8 x 512 20, 20, 20, 23,
+// 23.  Fewer lose more (1 per SM 164, 112, 107, 25).  Only small ragged
+// batches gain from more (14/2 heads, 201 tokens: 28 -> 25 with 4).
+int gated_prefill_segment(int B, int Hkv, int T) {
   const long long units = (long long)B * Hkv, chunks = ((long long)T + kGC - 1) / kGC;
   const long long want = std::max<long long>(1, 3 * 152 / units);
   return (int)std::max<long long>(1, (chunks + want - 1) / want);

@@ -470,7 +470,7 @@ size_t oal_gated_prefill_workspace_bytes(int B, int Hq, int Hkv, int T, int d, i
                                          oal_dtype dtype) {
   if (check_gated(B, Hq, Hkv, T, d, dv, dtype, 1.f) != OAL_OK) return 0;
   if (B == 0 || T == 0) return 256;
-  const int chunks = oal::gated_prefill_segment(B, Hkv, T, dtype == OAL_BF16);
+  const int chunks = oal::gated_prefill_segment(B, Hkv, T);
   const int nseg = oal::gated_segments(T, chunks);
   return gated_states_bytes(B, Hkv, nseg) + round256((size_t)B * Hkv * nseg * sizeof(float));
 }
@@ -504,7 +504,7 @@ oal_status oal_gated_prefill(const void *Q, const void *K, const void *V, oal_dt
   p.B = B, p.Hq = Hq, p.Hkv = Hkv, p.T = T, p.scale = scale, p.lengths = lengths;
   p.state_in = continue_from_state ? state : nullptr;
   p.state_out = state;
-  p.seg_chunks = oal::gated_prefill_segment(B, Hkv, T, dtype == OAL_BF16);
+  p.seg_chunks = oal::gated_prefill_segment(B, Hkv, T);
   p.nseg = oal::gated_segments(T, p.seg_chunks);
   p.seg_state = static_cast<float *>(workspace);
   p.seg_decay = reinterpret_cast<float *>(static_cast<char *>(workspace) +
