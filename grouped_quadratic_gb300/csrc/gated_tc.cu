@@ -47,7 +47,11 @@ struct SegSmem {
 // A chunk's decays are a chain of shuffles as long as its products: eight
 // chunks' are formed side by side, or every chunk would wait for its own.
 // 25 us for 4 x 8192 tokens of 8 KV heads (2.7 TB/s): bound by the factors'
-// splitting and the 96 products a warp and chunk they take.
+// splitting and the 96 products a warp and chunk they take, and 7,000 of its
+// 40,000 cycles pass before the first chunk is there.  tcgen05 in place of
+// mma.sync, the split factors by way of shared memory, took as long (26 us,
+// and 57 where gated_tc_own_kernel takes 51): a step's barrier, MMAs and read
+// of tensor memory stand in a row there.
 __global__ void __launch_bounds__(kSegThreads)
 gated_tc_segment_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                         GatedArgs p) {
@@ -167,7 +171,6 @@ __global__ void __launch_bounds__(kOutThreads, 3)
 gated_tc_out_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmY,
                     GatedArgs p) {
-  pdl_trigger();
   extern __shared__ uint8_t smem_raw[];
   OutSmem &s = *reinterpret_cast<OutSmem *>(align1024(smem_raw));
   const int bh = blockIdx.x / p.nseg, seg = blockIdx.x % p.nseg, b = bh / p.Hkv, kv = bh % p.Hkv;
@@ -197,6 +200,7 @@ gated_tc_out_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  pdl_trigger();   // (not before: what comes behind must not hold tensor memory that this block waits for)
   const uint32_t tb = uniform(s.tmem);
   const int c0 = seg * p.seg_chunks, nc = max(0, min((n + kGC - 1) / kGC - c0, p.seg_chunks));
   const int steps = nc * npair;              // step it: chunk it / npair, heads 2 (it % npair), + 1

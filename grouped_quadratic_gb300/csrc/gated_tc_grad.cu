@@ -245,7 +245,6 @@ __global__ void __launch_bounds__(kGradThreads, 2)
 gated_tc_grad_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                      const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
                      const __grid_constant__ CUtensorMap tmDQ, GatedArgs p) {
-  pdl_trigger();
   extern __shared__ uint8_t smem_raw[];
   GradSmem &s = *reinterpret_cast<GradSmem *>(align1024(smem_raw));
   const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
@@ -260,14 +259,15 @@ gated_tc_grad_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
     for (int i = 0; i < 4; ++i) mbar_init(&s.pair[i], 2);
     fence_mbar_init();
   }
-  if (warp == 8) {
+  pdl_wait();
+  if (warp == 8) {   // (not before: this block must not hold tensor memory that what it waits for may want)
     tmem_alloc(&s.tmem, kGradCols);
     tmem_relinquish();
   }
-  pdl_wait();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  pdl_trigger();
   const uint32_t tb = uniform(s.tmem), tx = tb, tz = tb + 64, tkv = tb + 128;
   auto wait = [&](uint64_t *bar, int phase) { return warp_wait(bar, phase & 1, &s.wait); };
   auto arrive = [&](uint64_t *bar) {
