@@ -25,7 +25,7 @@ namespace oal {
 namespace {
 using namespace gated;
 
-constexpr int kStages = 4;                  // chunks in flight of the segment kernel
+constexpr int kStages = 3;                  // chunks in flight of the segment kernel
 constexpr int kSegThreads = 128;
 constexpr int kOutThreads = 160;            // four computing warps and one that issues
 constexpr uint32_t kOutCols = 128;          // tensor memory: X (then P) 64, D 64
@@ -33,61 +33,175 @@ constexpr uint32_t kColX = 0, kColD = 64;
 
 // ---------------------------------------------------------------- segments
 
+// sum_j w_j a_j b_j^T over the 64 rows j of two bf16 tiles, as a sum of fp32
+// products: w_j a_j is formed in fp32 and goes in as three bf16 terms, which
+// hold all of its 24 bits.  The terms lie in shared memory as the tiles do, the
+// first in the place of a: one MMA of 128 rows takes the first two (64 rows of
+// the state each), another the second again and the third.  Every sum starts
+// from zero, because the tensor cores cut what they add to an accumulator; the
+// state is in registers, thread m (of 128) holding row m % 64 as the first
+// term's sum or that of the other two.
+constexpr uint32_t kSumCols = 128;
+constexpr int kSumIssuer = 3;               // the warp that issues (the first one loads)
+// Threads 0 .. 127; `terms` has room for two tiles.
+__device__ __forceinline__ void sum_split(uint8_t *a, uint8_t *terms, const float *w) {
+#pragma unroll
+  for (int z = 0; z < 4; ++z) {
+    const int row = (threadIdx.x >> 3) + 16 * z;
+    const uint32_t at = tile_at(row, threadIdx.x & 7);
+    const float f = w[row];
+    const uint4 x4 = *reinterpret_cast<const uint4 *>(a + at);
+    const uint32_t x[4] = {x4.x, x4.y, x4.z, x4.w};
+    uint32_t t[3][4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      float lo = f * __uint_as_float(x[e] << 16), hi = f * __uint_as_float(x[e] & 0xFFFF0000u);
+#pragma unroll
+      for (int q = 0; q < 3; ++q) {
+        const uint32_t word = pack_bf16x2(lo, hi);
+        lo -= __uint_as_float(word << 16), hi -= __uint_as_float(word & 0xFFFF0000u);
+        t[q][e] = word;
+      }
+    }
+    *reinterpret_cast<uint4 *>(a + at) = make_uint4(t[0][0], t[0][1], t[0][2], t[0][3]);
+    *reinterpret_cast<uint4 *>(terms + at) = make_uint4(t[1][0], t[1][1], t[1][2], t[1][3]);
+    *reinterpret_cast<uint4 *>(terms + kTileBytes + at) = make_uint4(t[2][0], t[2][1], t[2][2], t[2][3]);
+  }
+  fence_proxy_async();
+}
+// The products (one warp); `bar` completes with them.  `terms` lies behind `a`.
+__device__ __forceinline__ void sum_issue(uint32_t tm, const uint8_t *a, const uint8_t *b, const uint8_t *terms, uint64_t *bar) {
+  const uint32_t id = idesc_bf16_f32(128, 64, 1) | (1u << 15);   // both with rows along their minor axis
+  const uint64_t ad = sdesc_sw128(smem_u32(a), smem_u32(terms) - smem_u32(a), 1024);
+  const uint64_t td = sdesc_sw128(smem_u32(terms), kTileBytes, 1024), bd = sdesc_sw128(smem_u32(b), 16, 1024);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) umma_ss_warp(tm, ad + 128 * j, bd + 128 * j, id, j > 0);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) umma_ss_warp(tm + 64, td + 128 * j, bd + 128 * j, id, j > 0);
+  umma_commit_warp(bar);
+}
+// s = f s + the sums.
+__device__ __forceinline__ void sum_add(float (&s)[64], float f, uint32_t tm) {
+  const int warp = threadIdx.x >> 5;
+  const uint32_t from = tm + ((uint32_t)(32 * warp) << 16);
+#pragma unroll
+  for (int h = 0; h < 4; ++h) {
+    uint32_t x[16];
+    tmem_ld16(from + 16 * h, x);
+    tmem_wait_ld();
+#pragma unroll
+    for (int e = 0; e < 16; ++e) s[16 * h + e] = fmaf(f, s[16 * h + e], __uint_as_float(x[e]));
+  }
+  if (warp >= 2) {
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+      uint32_t x[16];
+      tmem_ld16(from + 64 + 16 * h, x);
+      tmem_wait_ld();
+#pragma unroll
+      for (int e = 0; e < 16; ++e) s[16 * h + e] += __uint_as_float(x[e]);
+    }
+  }
+}
+// The state, by way of 64 x 68 floats of shared memory that nothing else uses now (all 128 threads).
+__device__ __forceinline__ void sum_store(const float (&s)[64], float *room, float *dst) {
+  float *row = room + (threadIdx.x & 63) * 68;
+  if (threadIdx.x >= 64)
+#pragma unroll
+    for (int h = 0; h < 16; ++h) *reinterpret_cast<float4 *>(row + 4 * h) = make_float4(s[4 * h], s[4 * h + 1], s[4 * h + 2], s[4 * h + 3]);
+  __syncthreads();
+  if (threadIdx.x < 64)
+#pragma unroll
+    for (int h = 0; h < 16; ++h) {
+      const float4 x = *reinterpret_cast<const float4 *>(row + 4 * h);
+      *reinterpret_cast<float4 *>(row + 4 * h) =
+          make_float4(s[4 * h] + x.x, s[4 * h + 1] + x.y, s[4 * h + 2] + x.z, s[4 * h + 3] + x.w);
+    }
+  __syncthreads();
+#pragma unroll
+  for (int z = 0; z < 8; ++z) {
+    const int x = threadIdx.x + 128 * z;
+    reinterpret_cast<float4 *>(dst)[x] = *reinterpret_cast<const float4 *>(room + (x >> 4) * 68 + 4 * (x & 15));
+  }
+}
+
 constexpr int kGateBatch = 8;               // chunks whose decays are formed together, two a warp
 struct SegSmem {
   uint8_t a[kStages][kTileBytes], b[kStages][kTileBytes];
+  uint8_t terms[2][kTileBytes];
   struct alignas(16) {
     float tail[kGC], whole;               // e^{G_63-G_j}, e^{G_63}
   } gates[kGateBatch];
-  uint64_t full[kStages];
-  int abort_flag;
+  uint64_t full[kStages], done, drain;
+  uint32_t tmem;
+  WaitState wait;
 };
+static_assert(3 * (sizeof(SegSmem) + 2 * 1024) <= 228 * 1024, "three blocks per SM");
 
-// Own state of each segment: K and V once, four warps of 16 rows of the state.
+// Own state of each segment: K and V once.
 // A chunk's decays are a chain of shuffles as long as its products: eight
 // chunks' are formed side by side, or every chunk would wait for its own.
-// 25 us for 4 x 8192 tokens of 8 KV heads (2.7 TB/s): bound by the factors'
-// splitting and the 96 products a warp and chunk they take, and 7,000 of its
-// 40,000 cycles pass before the first chunk is there.  tcgen05 in place of
-// mma.sync, the split factors by way of shared memory, took as long (26 us,
-// and 57 where gated_tc_own_kernel takes 51): a step's barrier, MMAs and read
-// of tensor memory stand in a row there.
-__global__ void __launch_bounds__(kSegThreads)
+// 4 x 8192 tokens of 8 KV heads, 32 query heads: 80.5 us a prefill (this
+// kernel alone 25, 2.7 TB/s), where mma.sync, 96 products a warp and chunk, took
+// 85.9.  A chunk is 2,500 cycles of a block, three of which share the SM -
+// splitting 500, MMAs 800, their sums 300, waits - after 5,000 until the first
+// one is there.  A warp of its own for loads, decays and MMAs with two places
+// for the sums took 2 us more: the decays, 2,000 cycles a chunk there, were in
+// its way.
+__global__ void __launch_bounds__(kSegThreads, 3)
 gated_tc_segment_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                         GatedArgs p) {
-  pdl_trigger();
   extern __shared__ uint8_t smem_raw[];
   SegSmem &s = *reinterpret_cast<SegSmem *>(align1024(smem_raw));
   const int bh = blockIdx.x / p.nseg, seg = blockIdx.x % p.nseg, b = bh / p.Hkv;
-  const int tid = threadIdx.x, warp = tid >> 5;
+  const int tid = threadIdx.x, warp = warp_index();
   if (tid == 0) {
-    s.abort_flag = 0;
+    s.wait.abort = 0;
+    s.wait.status = p.status;
     for (int i = 0; i < kStages; ++i) mbar_init(&s.full[i], 1);
+    mbar_init(&s.done, 1), mbar_init(&s.drain, 1);
     fence_mbar_init();
   }
   pdl_wait();
   const int n = gated_len(p, b);
   if (seg > gated_last_seg(n, p.seg_chunks * kGC)) return;
-  __syncthreads();
   const int c0 = seg * p.seg_chunks, nc = max(0, min((n + kGC - 1) / kGC - c0, p.seg_chunks));
-  volatile int *abort_flag = &s.abort_flag;
-  auto load = [&](int c) {
-    const int st = c % kStages;
-    mbar_arrive_expect_tx(&s.full[st], 2 * kTileBytes);
-    tma_load_3d(s.a[st], &tmK, &s.full[st], 0, (c0 + c) * kGC, bh);
-    tma_load_3d(s.b[st], &tmV, &s.full[st], 0, (c0 + c) * kGC, bh);
-  };
-  if (tid == 0)
-    for (int c = 0; c < min(kStages, nc); ++c) load(c);
   const float *g = p.g + (size_t)bh * p.T;
   auto gate_of = [&](int c) { return gate_load(g, (c0 + c) * kGC, c < nc ? n : 0); };
   float2 gate0 = gate_of(warp), gate1 = gate_of(warp + 4);
-  StateAcc<8> acc;
-  state_load(acc, 0, nullptr);
-  float decay = 1.f;
+  int loads = 0;
+  auto load = [&]() {
+    const int st = loads % kStages;
+    mbar_arrive_expect_tx(&s.full[st], 2 * kTileBytes);
+    tma_load_3d(s.a[st], &tmK, &s.full[st], 0, (c0 + loads) * kGC, bh);
+    tma_load_3d(s.b[st], &tmV, &s.full[st], 0, (c0 + loads) * kGC, bh);
+    ++loads;
+  };
+  if (tid == 0)
+    while (loads < min(kStages, nc)) load();
+  if (warp == kSumIssuer) {
+    tmem_alloc(&s.tmem, kSumCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  pdl_trigger();   // (not before: what comes behind must not hold tensor memory that this block waits for)
+  const uint32_t tm = uniform(s.tmem);
+  float acc[64], decay = 1.f, whole = 1.f;   // whole: of the chunk whose sums come next
+#pragma unroll
+  for (int e = 0; e < 64; ++e) acc[e] = 0.f;
   bool ok = true;
-  for (int c = 0; c < nc; ++c) {
-    if (c % kGateBatch == 0) {   // (the chunk before ended in a barrier)
+  auto take = [&](int c) {
+    ok = ok && warp_wait(&s.done, c & 1, &s.wait);
+    if (!ok) return;
+    tc_fence_after();
+    sum_add(acc, whole, tm);
+    tc_fence_before();
+  };
+#pragma unroll 1
+  for (int c = 0, st = 0, turn = 0; c < nc; ++c) {
+    if (c % kGateBatch == 0) {   // (the chunk before is behind a barrier)
       const GateLane s0 = gate_sums(gate0), s1 = gate_sums(gate1);
       auto &to0 = s.gates[warp], &to1 = s.gates[warp + 4];
       to0.whole = gate_tails(s0, reinterpret_cast<float2 *>(to0.tail)[tid & 31]);
@@ -96,23 +210,44 @@ gated_tc_segment_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_co
       __syncthreads();
     }
     const auto &gates = s.gates[c % kGateBatch];
-    decay *= gates.whole;
-    ok = ok && mbar_wait(&s.full[c % kStages], (c / kStages) & 1, abort_flag, p.status);
-    ok = __all_sync(0xffffffffu, ok);
+    ok = ok && warp_wait(&s.full[st], turn & 1, &s.wait);
+    if (c > 0) {
+      take(c - 1);               // its tiles and terms have been read
+      if (tid == 0 && ok && loads < nc) load();
+    }
+    whole = gates.whole;
+    decay *= whole;
     if (n < p.T && (c0 + c + 1) * kGC > n) {   // rows behind the sequence count as zeros
-      clear_rows(s.a[c % kStages], n - (c0 + c) * kGC, tid, kSegThreads);
-      clear_rows(s.b[c % kStages], n - (c0 + c) * kGC, tid, kSegThreads);
+      clear_rows(s.a[st], n - (c0 + c) * kGC, tid, kSegThreads);
+      clear_rows(s.b[st], n - (c0 + c) * kGC, tid, kSegThreads);
       __syncthreads();
     }
-    if (ok) state_step(acc, gates.whole, 0, s.a[c % kStages], s.b[c % kStages], gates.tail);
+    if (ok) sum_split(s.a[st], s.terms[0], gates.tail);
+    tc_fence_before();
     __syncthreads();
-    if (tid == 0 && ok && c + kStages < nc) load(c + kStages);
+    if (warp == kSumIssuer && ok) {
+      tc_fence_after();
+      sum_issue(tm, s.a[st], s.b[st], s.terms[0], &s.done);
+    }
+    if (++st == kStages) st = 0, ++turn;
   }
-  if (tid == 0 && !ok)   // copies still in flight land before the block ends
-    for (int i = 0; i < min(kStages, nc); ++i)
-      for (int ph = 0; ph < 2; ++ph) mbar_wait_teardown(&s.full[i], ph, p.status);
-  state_store(acc, 0, p.seg_state + ((size_t)bh * p.nseg + seg) * kGS);
+  if (nc > 0) take(nc - 1);
+  if (warp == kSumIssuer) {   // nothing in flight at the block's end
+    umma_commit_warp(&s.drain);
+    if ((tid & 31) == 0) mbar_wait_teardown(&s.drain, 0, p.status);
+    __syncwarp();
+  }
+  if (tid == 0 && !ok)
+    for (int i = max(0, loads - kStages); i < loads; ++i)
+      mbar_wait_teardown(&s.full[i % kStages], (i / kStages) & 1, p.status);
+  tc_fence_before();
+  __syncthreads();
+  sum_store(acc, reinterpret_cast<float *>(s.a), p.seg_state + ((size_t)bh * p.nseg + seg) * kGS);
   if (tid == 0) p.seg_decay[(size_t)bh * p.nseg + seg] = decay;
+  if (warp == kSumIssuer) {
+    tc_fence_after();
+    tmem_dealloc(tm, kSumCols);
+  }
 }
 
 // ---------------------------------------------------------------- outputs
