@@ -10,6 +10,9 @@ Tensor layouts (row-major, contiguous, CUDA):
   L [Hq,G+1,G+1] float32 (lower triangle), group [Hq,64] int32 in 1..G
   state [B,Hkv,F,65] float32 (F = 4161 FULL, 2145 PACKED)
   gated recurrence: g [B,Hkv,T] float32 (log decays), state [B,Hkv,64,64] float32
+
+A gated call given a `stream` waits there for the tensors that it makes itself
+(on the current stream); tensors given to it have to be ready on `stream`.
 """
 import ctypes
 import os
@@ -362,16 +365,22 @@ def _elsewhere(dev):
 
 def _stream_on(dev, stream, made):
     """The handle to launch on: that of `stream`, or of the current stream of
-    dev.  `made`: tensors this call allocated, from the current stream's pool;
-    their memory must not be handed out again before `stream` is done with it."""
+    dev.  `made`: tensors this call allocated from the current stream's pool.
+    Work queued there may still use their memory, and some are being zeroed
+    there, so `stream` waits for it; and the memory must not be handed out
+    again before `stream` is done with it.  Tensors the caller gives are the
+    caller's to order."""
     if stream is None:
         return torch._C._cuda_getCurrentRawStream(dev.index)
     if stream.device != dev:
         raise OALError(OAL_ERR_INVALID_ARG, "the stream is on %s, the tensors on %s"
                        % (stream.device, dev))
-    if stream != torch.cuda.current_stream(dev):
-        for t in made:
-            t.record_stream(stream)
+    if made:
+        current = torch.cuda.current_stream(dev)
+        if stream != current:
+            stream.wait_stream(current)
+            for t in made:
+                t.record_stream(stream)
     return stream.cuda_stream
 
 

@@ -118,3 +118,36 @@ def test_binding_refuses_wrong_tensors(lib):
         with pytest.raises(oal.OALError) as e:
             call()
         assert e.value.status == oal.OAL_ERR_INVALID_ARG
+
+
+class FakeStream:
+    """What the binding uses of a torch.cuda.Stream, with its calls in order."""
+    device = torch.device("cuda", 0)
+    cuda_stream = 4321
+
+    def __init__(self):
+        self.calls = []
+
+    def wait_stream(self, other):
+        self.calls.append(("wait", other))
+
+
+class FakeTensor:
+    def record_stream(self, stream):
+        stream.calls.append(("record", self))
+
+
+def test_tensors_made_in_a_call_are_ordered_before_its_stream(lib, monkeypatch):
+    """A call makes (and fills) its tensors on the current stream; the stream it
+    launches on has to wait for that, and the memory must live until it is done."""
+    from grouped_quadratic_gb300 import oal
+    now, side, made = FakeStream(), FakeStream(), [FakeTensor(), FakeTensor()]
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda dev=None: now)
+    assert oal._stream_on(now.device, side, made) == side.cuda_stream
+    assert ("wait", now) in side.calls
+    assert all(("record", t) in side.calls for t in made)
+    # nothing made, or the current stream itself: no order to add
+    side.calls.clear()
+    assert oal._stream_on(now.device, side, []) == side.cuda_stream
+    assert oal._stream_on(now.device, now, made) == now.cuda_stream
+    assert side.calls == [] and now.calls == []

@@ -524,3 +524,21 @@ def test_offsets_beyond_32_bits(oal):
     oal.oal_sync_status()
     assert rel(Y[:, :, T - tail:], y) <= OUT[torch.bfloat16]
     assert rel(S, s) <= STATE[torch.bfloat16]
+
+
+def test_outputs_made_in_a_call_on_another_stream(oal):
+    """The current stream is busy when the call makes its outputs (zeroed there,
+    as there are lengths): the kernels on the other stream come behind that."""
+    c = Case(torch.bfloat16, 2, 14, 2, 3000, seed=44, lengths=[3000, 1701])
+    grads = lambda **kw: oal.oal_gated_backward(c.Q, c.K, c.V, c.g, c.dY, lengths=c.lengths, state0=c.state0, **kw)
+    want = oal.oal_gated_prefill(c.Q, c.K, c.V, c.g, lengths=c.lengths) + grads()
+    work = torch.randn(8192, 8192, device="cuda", dtype=torch.bfloat16)
+    work @ work
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(5):                       # about 5 ms
+        work @ work
+    got = oal.oal_gated_prefill(c.Q, c.K, c.V, c.g, lengths=c.lengths, stream=side) + grads(stream=side)
+    torch.cuda.synchronize()
+    oal.oal_sync_status()
+    assert all(torch.equal(x, y) for x, y in zip(got, want))
