@@ -21,6 +21,28 @@ constexpr int kGS = kD * kDv;           // elements of a state
 // -inf does; it is counted instead of summed, which keeps the sums small.
 constexpr float kGateCut = -104.f;
 
+// A decay over a token, a chunk or a segment, e^x, as an unevaluated sum
+// hi + lo.  Many of them in a row multiply a state, and a slow gate's lie next
+// to 1, where half a step of fp32 is 2^-25: under a constant gate it would be
+// the same one each time, and grow with their number instead of its root
+// (4096 chunks: 6e-5 of the state, with the pair 5e-7).  From |x| = 0.5 on a
+// state is forgotten before that shows, and lo is 0.
+struct GateDecay {
+  float hi, lo;
+};
+__device__ __forceinline__ GateDecay decay_exp(float x) {
+  const float hi = expf(x);
+  return {hi, fabsf(x) < 0.5f ? expm1f(x) - (hi - 1.f) : 0.f};
+}
+__device__ __forceinline__ GateDecay decay_mul(GateDecay a, GateDecay b) {
+  const float p = a.hi * b.hi;
+  const float e = fmaf(a.hi, b.hi, -p) + fmaf(a.hi, b.lo, a.lo * b.hi);
+  const float hi = p + e;
+  return {hi, e - (hi - p)};
+}
+// f s + d
+__device__ __forceinline__ float decay_add(GateDecay f, float s, float d) { return fmaf(f.hi, s, fmaf(f.lo, s, d)); }
+
 struct GatedArgs {
   const void *Q, *K, *V, *dY;
   const float *g;
@@ -35,7 +57,8 @@ struct GatedArgs {
   void *dQ, *dK, *dV;
   float *dg;
   int seg_chunks, nseg;                 // chunks of a segment, segments of T tokens
-  float *seg_state, *seg_decay;         // [B Hkv][nseg][64 64], [B Hkv][nseg]
+  float *seg_state;                     // [B Hkv][nseg][64 64]
+  GateDecay *seg_decay;                 // [B Hkv][nseg]
   float *seg_grad;                      // backward: the same for the state's gradient
   uint8_t *state_tiles, *grad_tiles;    // backward (bf16): S and R of each chunk, two 8 KB tiles each
   int *status;
@@ -147,6 +170,10 @@ __device__ __forceinline__ float gate_pair(const GateSums &s, int i, int j) {
 __device__ __forceinline__ float gate_head(const GateSums &s, int i) {
   return gate_exp(s.cuts[i] == 0, s.hi[i] + s.lo[i]);
 }
+// Decay over the chunk.
+__device__ __forceinline__ GateDecay gate_whole(const GateSums &s) {
+  return decay_exp(s.cuts[kGC - 1] == 0 ? s.hi[kGC - 1] + s.lo[kGC - 1] : -INFINITY);
+}
 // Decay from behind token j to the chunk's end, exp(G_63 - G_j).
 __device__ __forceinline__ float gate_tail(const GateSums &s, int j) {
   return gate_pair(s, kGC - 1, j);
@@ -180,18 +207,18 @@ __device__ __forceinline__ void scan_store(float *p, const ScanVec<kVec> &r) {
 // own: the thread's values of segment 0's own state; count segments, of which
 // the first `formed` in walking order have one; back: from the last to the first.
 template <int kVec, int kAhead, typename Put>
-__device__ __forceinline__ ScanVec<kVec> scan_walk(const float *own, const float *decay, const float *from, int count,
+__device__ __forceinline__ ScanVec<kVec> scan_walk(const float *own, const GateDecay *decay, const float *from, int count,
                                                    int formed, bool back, Put put) {
   ScanVec<kVec> run = {};
   if (from) run = scan_load<kVec>(from);
   for (int i0 = 0; i0 < count; i0 += kAhead) {
     ScanVec<kVec> v[kAhead];
-    float f[kAhead];
+    GateDecay f[kAhead];
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
       const int i = back ? count - 1 - i0 - k : i0 + k;
       v[k] = {};
-      f[k] = 0.f;
+      f[k] = {};
       if (i0 + k < formed) v[k] = scan_load<kVec>(own + (size_t)i * kGS), f[k] = decay[i];
     }
 #pragma unroll
@@ -199,7 +226,7 @@ __device__ __forceinline__ ScanVec<kVec> scan_walk(const float *own, const float
       if (i0 + k < count) {
         put(back ? count - 1 - i0 - k : i0 + k, run);
 #pragma unroll
-        for (int e = 0; e < kVec; ++e) run.v[e] = fmaf(f[k], run.v[e], v[k].v[e]);
+        for (int e = 0; e < kVec; ++e) run.v[e] = decay_add(f[k], run.v[e], v[k].v[e]);
       }
   }
   return run;
@@ -210,10 +237,10 @@ __device__ __forceinline__ ScanVec<kVec> scan_walk(const float *own, const float
 // of a block are kChains groups of kScanThreads / kChains; all get the result.
 constexpr int kScanThreads = 128;
 template <int kVec, int kAhead, int kChains, typename Put>
-__device__ __forceinline__ ScanVec<kVec> scan_split(const float *own, const float *decay, const float *from, int count,
+__device__ __forceinline__ ScanVec<kVec> scan_split(const float *own, const GateDecay *decay, const float *from, int count,
                                                     int formed, bool back, Put put) {
   constexpr int kLanes = kScanThreads / kChains;
-  __shared__ float s_decay[kChains];
+  __shared__ GateDecay s_decay[kChains];
   __shared__ ScanVec<kVec> s_sum[kChains][kLanes];
   const int chain = threadIdx.x / kLanes, lane = threadIdx.x % kLanes;
   ScanVec<kVec> run = {};
@@ -221,19 +248,19 @@ __device__ __forceinline__ ScanVec<kVec> scan_split(const float *own, const floa
   for (int i0 = 0; i0 < count; i0 += kAhead * kChains) {
     const int first = i0 + chain * kAhead;
     ScanVec<kVec> v[kAhead], sum = {};
-    float f[kAhead], all = 1.f;
+    GateDecay f[kAhead], all = {1.f, 0.f};
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
       const int i = back ? count - 1 - first - k : first + k;
       v[k] = {};
-      f[k] = 1.f;
+      f[k] = {1.f, 0.f};
       if (first + k < formed) v[k] = scan_load<kVec>(own + (size_t)i * kGS), f[k] = decay[i];
     }
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
 #pragma unroll
-      for (int e = 0; e < kVec; ++e) sum.v[e] = fmaf(f[k], sum.v[e], v[k].v[e]);
-      all *= f[k];
+      for (int e = 0; e < kVec; ++e) sum.v[e] = decay_add(f[k], sum.v[e], v[k].v[e]);
+      all = decay_mul(all, f[k]);
     }
     __syncthreads();
     if (lane == 0) s_decay[chain] = all;
@@ -245,14 +272,14 @@ __device__ __forceinline__ ScanVec<kVec> scan_split(const float *own, const floa
       if (z == chain) in = run;
       const ScanVec<kVec> part = s_sum[z][lane];
 #pragma unroll
-      for (int e = 0; e < kVec; ++e) run.v[e] = fmaf(s_decay[z], run.v[e], part.v[e]);
+      for (int e = 0; e < kVec; ++e) run.v[e] = decay_add(s_decay[z], run.v[e], part.v[e]);
     }
 #pragma unroll
     for (int k = 0; k < kAhead; ++k)
       if (first + k < count) {
         put(back ? count - 1 - first - k : first + k, in);
 #pragma unroll
-        for (int e = 0; e < kVec; ++e) in.v[e] = fmaf(f[k], in.v[e], v[k].v[e]);
+        for (int e = 0; e < kVec; ++e) in.v[e] = decay_add(f[k], in.v[e], v[k].v[e]);
       }
   }
   return run;

@@ -52,7 +52,7 @@ gated_decode_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *_
 #pragma unroll
   for (int r = 0; r < kRows; ++r) S[r] = *reinterpret_cast<const float4 *>(s + (rg * kRows + r) * 64);
   const size_t kvrow = (size_t)unit * 64;
-  const float a = expf(__ldg(g + unit));
+  const GateDecay a = decay_exp(__ldg(g + unit));
   float vv[4], kk[kRows];
 #pragma unroll
   for (int e = 0; e < 4; ++e) vv[e] = to_f32(v[kvrow + 4 * cg + e]);
@@ -60,8 +60,8 @@ gated_decode_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *_
   for (int r = 0; r < kRows; ++r) kk[r] = to_f32(k[kvrow + rg * kRows + r]);
 #pragma unroll
   for (int r = 0; r < kRows; ++r) {
-    S[r].x = fmaf(a, S[r].x, kk[r] * vv[0]), S[r].y = fmaf(a, S[r].y, kk[r] * vv[1]);
-    S[r].z = fmaf(a, S[r].z, kk[r] * vv[2]), S[r].w = fmaf(a, S[r].w, kk[r] * vv[3]);
+    S[r].x = decay_add(a, S[r].x, kk[r] * vv[0]), S[r].y = decay_add(a, S[r].y, kk[r] * vv[1]);
+    S[r].z = decay_add(a, S[r].z, kk[r] * vv[2]), S[r].w = decay_add(a, S[r].w, kk[r] * vv[3]);
     *reinterpret_cast<float4 *>(s + (rg * kRows + r) * 64) = S[r];
   }
   for (int h0 = 0; h0 < rho; h0 += kHeads) {

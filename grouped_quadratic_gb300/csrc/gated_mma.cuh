@@ -152,11 +152,11 @@ __device__ __forceinline__ void state_step(StateAcc<kNb> &s, float f, int nb0, c
     for (int e = 0; e < 4; ++e) s.v[nb][e] = fmaf(f, s.v[nb][e], d.v[nb][e]);
 }
 template <int kNb>
-__device__ __forceinline__ void state_scale(StateAcc<kNb> &s, float f) {
+__device__ __forceinline__ void state_scale(StateAcc<kNb> &s, GateDecay f) {
 #pragma unroll
   for (int nb = 0; nb < kNb; ++nb)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) s.v[nb][e] *= f;
+    for (int e = 0; e < 4; ++e) s.v[nb][e] = decay_add(f, s.v[nb][e], 0.f);
 }
 template <int kNb>
 __device__ __forceinline__ void state_load(StateAcc<kNb> &s, int nb0, const float *src) {
@@ -196,12 +196,12 @@ __device__ __forceinline__ void state_round(const StateAcc<kNb> &s, int nb0, voi
 
 // Decays from behind a lane's two tokens to the end of the chunk, and over the
 // whole chunk (returned).
-__device__ __forceinline__ float gate_tails(const GateLane &x, float2 &out) {
+__device__ __forceinline__ GateDecay gate_tails(const GateLane &x, float2 &out) {
   const float eh = __shfl_sync(0xffffffffu, x.hi[1], 31), el = __shfl_sync(0xffffffffu, x.lo[1], 31);
   const int ec = __shfl_sync(0xffffffffu, x.cuts[1], 31);
   out = make_float2(gate_exp_fast(x.cuts[0] == ec, (eh - x.hi[0]) + (el - x.lo[0])),
                     gate_exp_fast(x.cuts[1] == ec, (eh - x.hi[1]) + (el - x.lo[1])));
-  return gate_exp_fast(ec == 0, eh + el);
+  return decay_exp(ec == 0 ? eh + el : -INFINITY);
 }
 
 }  // namespace oal

@@ -131,6 +131,7 @@ __device__ __forceinline__ void store_rows(const Acc &a, int ty, int tx, float *
 struct Decays {
   GateSums sums;
   float head[kGC], tail[kGC];
+  GateDecay whole;
 };
 // (`gate` as warp 0 loaded it, early, so that its way to memory is not in
 // front of the tiles')
@@ -141,6 +142,7 @@ __device__ __forceinline__ void chunk_decays(float2 gate, Decays &d) {
     d.head[threadIdx.x] = gate_head(d.sums, threadIdx.x);
     d.tail[threadIdx.x] = gate_tail(d.sums, threadIdx.x);
   }
+  if (threadIdx.x == kGC) d.whole = gate_whole(d.sums);
   __syncthreads();
 }
 
@@ -164,7 +166,8 @@ __global__ void __launch_bounds__(kThreads) gated_segment_kernel(GatedArgs p) {
   const int c0 = seg * p.seg_chunks, c1 = min((n + kGC - 1) / kGC, c0 + p.seg_chunks);
   Acc acc;
   clear(acc);
-  float decay = 1.f;
+  __shared__ GateDecay decay;                 // (the first thread's)
+  if (threadIdx.x == 0) decay = {1.f, 0.f};
   for (int s = 0; s < c1 - c0; ++s) {
     const int t0 = (grad ? c1 - 1 - s : c0 + s) * kGC;
     const float2 gate = gate_load(g, t0, n);
@@ -177,12 +180,12 @@ __global__ void __launch_bounds__(kThreads) gated_segment_kernel(GatedArgs p) {
       load_tile(static_cast<const float *>(p.dY) + ((size_t)b * p.Hq + kv * rho) * p.T * 64, t0, n, B);
     }
     chunk_decays(gate, dec);
-    const float whole = dec.head[kGC - 1];
-    decay *= whole;
+    const GateDecay whole = dec.whole;
+    if (threadIdx.x == 0) decay = decay_mul(decay, whole);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) acc.v[i][j] *= whole;
+      for (int j = 0; j < 4; ++j) acc.v[i][j] = decay_add(whole, acc.v[i][j], 0.f);
     if (!grad) {
       mm_tn(A, B, dec.tail, ty, tx, acc);
     } else {
@@ -220,7 +223,8 @@ __global__ void __launch_bounds__(kScanThreads) gated_scan_kernel(GatedArgs p) {
   const int n = gated_len(p, bh / p.Hkv), last = gated_last_seg(n, p.seg_chunks * kGC);
   const bool grad = blockIdx.z != 0;
   float *s = (grad ? p.seg_grad : p.seg_state) + (size_t)bh * p.nseg * kGS + x;
-  const float *from = grad ? p.dstate : p.state_in, *decay = p.seg_decay + (size_t)bh * p.nseg;
+  const float *from = grad ? p.dstate : p.state_in;
+  const GateDecay *decay = p.seg_decay + (size_t)bh * p.nseg;
   if (from) from += (size_t)bh * kGS + x;
   const int count = grad && n == 0 ? 0 : last + 1, formed = grad || kLast ? count : last;
   auto put = [&](int i, const ScanVec<kVec> &v) { scan_store(s + (size_t)i * kGS, v); };
@@ -292,11 +296,11 @@ __global__ void __launch_bounds__(kThreads) gated_out_kernel(GatedArgs p) {
       store_rows(a, ty, tx, static_cast<float *>(p.Y) + row, t0, n);
     }
     Acc s;
-    const float whole = dec.head[kGC - 1];
+    const GateDecay whole = dec.whole;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) s.v[i][j] = whole * S[(4 * ty + i) * kP + tx + 16 * j];
+      for (int j = 0; j < 4; ++j) s.v[i][j] = decay_add(whole, S[(4 * ty + i) * kP + tx + 16 * j], 0.f);
     mm_tn(K, V, dec.tail, ty, tx, s);
     __syncthreads();
     put(s, ty, tx, S);

@@ -81,7 +81,7 @@ __device__ __forceinline__ void sum_issue(uint32_t tm, const uint8_t *a, const u
   umma_commit_warp(bar);
 }
 // s = f s + the sums.
-__device__ __forceinline__ void sum_add(float (&s)[64], float f, uint32_t tm) {
+__device__ __forceinline__ void sum_add(float (&s)[64], GateDecay f, uint32_t tm) {
   const int warp = threadIdx.x >> 5;
   const uint32_t from = tm + ((uint32_t)(32 * warp) << 16);
 #pragma unroll
@@ -90,7 +90,7 @@ __device__ __forceinline__ void sum_add(float (&s)[64], float f, uint32_t tm) {
     tmem_ld16(from + 16 * h, x);
     tmem_wait_ld();
 #pragma unroll
-    for (int e = 0; e < 16; ++e) s[16 * h + e] = fmaf(f, s[16 * h + e], __uint_as_float(x[e]));
+    for (int e = 0; e < 16; ++e) s[16 * h + e] = decay_add(f, s[16 * h + e], __uint_as_float(x[e]));
   }
   if (warp >= 2) {
 #pragma unroll
@@ -130,7 +130,8 @@ struct SegSmem {
   uint8_t a[kStages][kTileBytes], b[kStages][kTileBytes];
   uint8_t terms[2][kTileBytes];
   struct alignas(16) {
-    float tail[kGC], whole;               // e^{G_63-G_j}, e^{G_63}
+    float tail[kGC];                      // e^{G_63-G_j}
+    GateDecay whole;                      // e^{G_63}
   } gates[kGateBatch];
   uint64_t full[kStages], done, drain;
   uint32_t tmem;
@@ -188,7 +189,8 @@ gated_tc_segment_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_co
   tc_fence_after();
   pdl_trigger();   // (not before: what comes behind must not hold tensor memory that this block waits for)
   const uint32_t tm = uniform(s.tmem);
-  float acc[64], decay = 1.f, whole = 1.f;   // whole: of the chunk whose sums come next
+  float acc[64];
+  GateDecay decay = {1.f, 0.f}, whole = decay;   // whole: of the chunk whose sums come next
 #pragma unroll
   for (int e = 0; e < 64; ++e) acc[e] = 0.f;
   bool ok = true;
@@ -216,7 +218,7 @@ gated_tc_segment_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_co
       if (tid == 0 && ok && loads < nc) load();
     }
     whole = gates.whole;
-    decay *= whole;
+    decay = decay_mul(decay, whole);
     if (n < p.T && (c0 + c + 1) * kGC > n) {   // rows behind the sequence count as zeros
       clear_rows(s.a[st], n - (c0 + c) * kGC, tid, kSegThreads);
       clear_rows(s.b[st], n - (c0 + c) * kGC, tid, kSegThreads);

@@ -92,7 +92,8 @@ constexpr float kSpan = 60.f;
 struct alignas(16) ChunkGates {
   PairWeights tail;                       // e^{G_63-G_j}
   float rest[kGC], row[kGC];              // e^{R-G_j}, e^{G_i-R}
-  float whole, first;                     // e^{G_63} (0 if cut), e^{G_31}
+  GateDecay whole;                        // e^{G_63} (0 if cut)
+  float first;                            // e^{G_31}
   uint32_t cut_even, cut_odd;             // bit l: the gate of token 2l (2l + 1) is cut
   int mode;
 };
@@ -102,7 +103,7 @@ __device__ __forceinline__ void chunk_gates(float2 gate, const GateLane &sums, C
   const uint32_t even = __ballot_sync(0xffffffffu, gate.x <= kGateCut);
   const uint32_t odd = __ballot_sync(0xffffffffu, gate.y <= kGateCut);
   float2 tail;
-  const float whole = gate_tails(sums, tail);
+  const GateDecay whole = gate_tails(sums, tail);
   weights_put(to.tail, tail.x, tail.y);
   const float mh = __shfl_sync(0xffffffffu, sums.hi[1], 15), ml = __shfl_sync(0xffffffffu, sums.lo[1], 15);
   const float span = fmaxf(fabsf(sums.hi[0]), fabsf(sums.hi[1]));

@@ -75,7 +75,7 @@ gated_tc_own_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
   if (tid < 32) {
     const GateLane sums = gate_sums(gate_load(p.g + (size_t)bh * p.T, t0, n));
     if (!grad) {
-      const float whole = gate_tails(sums, reinterpret_cast<float2 *>(s.w)[tid]);
+      const GateDecay whole = gate_tails(sums, reinterpret_cast<float2 *>(s.w)[tid]);
       if (tid == 0) p.seg_decay[(size_t)bh * p.nseg + c] = whole;
     } else {
       reinterpret_cast<float2 *>(s.w)[tid] =
@@ -124,7 +124,8 @@ __global__ void __launch_bounds__(kScanThreads) gated_tc_scan_kernel(GatedArgs p
   const float *own = (grad ? p.seg_grad : p.seg_state) + (size_t)bh * p.nseg * kGS + x;
   uint8_t *tiles = (grad ? p.grad_tiles : p.state_tiles) + (size_t)bh * p.nseg * 2 * kTileBytes +
                    tile_at(x >> 6, (x & 63) >> 3) + 2 * (x & 7);
-  const float *from = grad ? p.dstate : p.state_in, *decay = p.seg_decay + (size_t)bh * p.nseg;
+  const float *from = grad ? p.dstate : p.state_in;
+  const GateDecay *decay = p.seg_decay + (size_t)bh * p.nseg;
   if (from) from += (size_t)bh * kGS + x;
   auto put = [&](int i, const ScanVec<kVec> &v) {
     uint8_t *at = tiles + (size_t)i * 2 * kTileBytes;
@@ -197,7 +198,7 @@ __device__ __noinline__ void chunk_dg(const GradSmem::Sums &u, const ChunkGates 
   float x = 0.f, r[2], f[2];
 #pragma unroll
   for (int z = 0; z < 8; ++z) x += u.dots[z];
-  x *= gates.whole;
+  x *= gates.whole.hi;
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
     const int t = 2 * lane + e;

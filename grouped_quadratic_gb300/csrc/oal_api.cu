@@ -472,7 +472,7 @@ size_t oal_gated_prefill_workspace_bytes(int B, int Hq, int Hkv, int T, int d, i
   if (B == 0 || T == 0) return 256;
   const int chunks = oal::gated_prefill_segment(B, Hkv, T);
   const int nseg = oal::gated_segments(T, chunks);
-  return gated_states_bytes(B, Hkv, nseg) + round256((size_t)B * Hkv * nseg * sizeof(float));
+  return gated_states_bytes(B, Hkv, nseg) + round256((size_t)B * Hkv * nseg * sizeof(oal::GateDecay));
 }
 
 oal_status oal_gated_prefill(const void *Q, const void *K, const void *V, oal_dtype dtype,
@@ -507,8 +507,8 @@ oal_status oal_gated_prefill(const void *Q, const void *K, const void *V, oal_dt
   p.seg_chunks = oal::gated_prefill_segment(B, Hkv, T);
   p.nseg = oal::gated_segments(T, p.seg_chunks);
   p.seg_state = static_cast<float *>(workspace);
-  p.seg_decay = reinterpret_cast<float *>(static_cast<char *>(workspace) +
-                                          gated_states_bytes(B, Hkv, p.nseg));
+  p.seg_decay = reinterpret_cast<oal::GateDecay *>(static_cast<char *>(workspace) +
+                                                   gated_states_bytes(B, Hkv, p.nseg));
   p.status = oal_device_status_word();
   if (!p.status) return oal_fail(OAL_ERR_CUDA, "no device status word");
   oal_begin_call(stream);
@@ -523,7 +523,7 @@ size_t oal_gated_backward_workspace_bytes(int B, int Hq, int Hkv, int T, int d, 
   const int nseg = oal::gated_segments(T, 1);   // a segment is a chunk
   // (bf16: and both once more, as pairs of bf16 tiles)
   return (dtype == OAL_BF16 ? 4 : 2) * gated_states_bytes(B, Hkv, nseg) +
-         round256((size_t)B * Hkv * nseg * sizeof(float));
+         round256((size_t)B * Hkv * nseg * sizeof(oal::GateDecay));
 }
 
 oal_status oal_gated_backward(const void *Q, const void *K, const void *V, oal_dtype dtype,
@@ -570,7 +570,7 @@ oal_status oal_gated_backward(const void *Q, const void *K, const void *V, oal_d
   p.seg_grad = reinterpret_cast<float *>(static_cast<char *>(workspace) + states);
   uint8_t *rest = static_cast<uint8_t *>(workspace) + 2 * states;
   if (dtype == OAL_BF16) p.state_tiles = rest, p.grad_tiles = rest + states, rest += 2 * states;
-  p.seg_decay = reinterpret_cast<float *>(rest);
+  p.seg_decay = reinterpret_cast<oal::GateDecay *>(rest);
   p.status = oal_device_status_word();
   if (!p.status) return oal_fail(OAL_ERR_CUDA, "no device status word");
   oal_begin_call(stream);

@@ -542,3 +542,51 @@ def test_outputs_made_in_a_call_on_another_stream(oal):
     torch.cuda.synchronize()
     oal.oal_sync_status()
     assert all(torch.equal(x, y) for x, y in zip(got, want))
+
+
+# Constant gates whose decay over a chunk (the first two; over a token: the
+# third) lies nearly half way between two fp32 numbers: a decay carried as one
+# fp32 factor is off by the same 2^-25 every time, 3e-5 to 1e-4 of the state
+# after these many chunks.  Independent roundings are what the tolerances
+# count: 4096 chunks of 64 tokens, sqrt(4160) 2^-24 = 4e-6.
+SLOW = [-8.181881980817707e-07, -2.6682809561862086e-07, -1e-5, -3e-6]
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["f32", "bf16"])
+@pytest.mark.parametrize("gate", SLOW)
+@pytest.mark.parametrize("T", [65536, 262143])
+def test_slow_gates_over_many_chunks(oal, dtype, gate, T):
+    gen = torch.Generator(device="cuda").manual_seed(50)
+    n = lambda *s: torch.randn(*s, generator=gen, device="cuda")
+    Q, K, V, dY = (n(1, 1, T, 64).to(dtype) for _ in range(4))
+    state0, dstate = n(1, 1, 64, 64), n(1, 1, 64, 64)
+    g = torch.full((1, 1, T), gate, device="cuda")
+    # S_T = sum_t e^{(T-1-t) g} k_t v_t^T + e^{T g} S_0, and its like for the gradient
+    age = torch.arange(T, device="cuda", dtype=torch.float64) * float(g[0, 0, 0])
+    last = math.exp(T * float(g[0, 0, 0]))
+    S = (K[0, 0].double() * age.flip(0).exp()[:, None]).T @ V[0, 0].double() + last * state0[0, 0].double()
+    first = math.exp(float(g[0, 0, 0]))
+    R = SCALE * first * (Q[0, 0].double() * age.exp()[:, None]).T @ dY[0, 0].double() + last * dstate[0, 0].double()
+    _, state = oal.oal_gated_prefill(Q, K, V, g, SCALE, state=state0.clone(), continue_from_state=True)
+    grads = oal.oal_gated_backward(Q, K, V, g, dY, SCALE, state0=state0, dstate=dstate)
+    oal.oal_sync_status()
+    assert rel(state[0, 0], S) <= STATE[dtype]
+    assert rel(grads[4][0, 0], R) <= STATE[dtype]
+
+
+@pytest.mark.parametrize("gate", [-8.9e-8, -2.6682809561862086e-07, -1e-5])
+def test_slow_gates_over_many_steps(oal, gate):
+    """16384 decode steps: sqrt(16384) 2^-24 = 8e-6 from roundings that are
+    independent; half a step each time the same way would be 16384 2^-25 = 5e-4."""
+    steps = 16384
+    gen = torch.Generator(device="cuda").manual_seed(51)
+    q, k, v = (torch.randn(steps, 1, 1, 64, generator=gen, device="cuda") for _ in range(3))
+    state0 = torch.randn(1, 1, 64, 64, generator=gen, device="cuda")
+    g = torch.full((1, 1), gate, device="cuda")
+    state, y = state0.clone(), torch.empty(1, 1, 64, device="cuda")
+    for t in range(steps):
+        oal.oal_gated_decode_step(q[t], k[t], v[t], g, state, SCALE, y=y)
+    oal.oal_sync_status()
+    age = torch.arange(steps, device="cuda", dtype=torch.float64) * float(g)
+    S = (k[:, 0, 0].double() * age.flip(0).exp()[:, None]).T @ v[:, 0, 0].double() + math.exp(steps * float(g)) * state0[0, 0].double()
+    assert rel(state[0, 0], S) <= 1e-5
