@@ -40,8 +40,14 @@ __device__ __forceinline__ GateDecay decay_mul(GateDecay a, GateDecay b) {
   const float hi = p + e;
   return {hi, e - (hi - p)};
 }
-// f s + d
-__device__ __forceinline__ float decay_add(GateDecay f, float s, float d) { return fmaf(f.hi, s, fmaf(f.lo, s, d)); }
+// f s + d.  A decay of 0 (a cut gate) shuts out whatever s is, NaN and
+// infinities too.
+__device__ __forceinline__ float decay_add(GateDecay f, float s, float d) {
+  s = __uint_as_float(__float_as_uint(s) & (f.hi == 0.f ? 0u : ~0u));   // (a select would become a branch)
+  return fmaf(f.hi, s, fmaf(f.lo, s, d));
+}
+// The same for a factor by itself.
+__device__ __forceinline__ float decay_by(float f, float x) { return f == 0.f ? 0.f : f * x; }
 
 struct GatedArgs {
   const void *Q, *K, *V, *dY;

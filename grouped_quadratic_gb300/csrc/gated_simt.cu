@@ -286,7 +286,7 @@ __global__ void __launch_bounds__(kThreads) gated_out_kernel(GatedArgs p) {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) a.v[i][j] *= dec.head[4 * ty + i];
+        for (int j = 0; j < 4; ++j) a.v[i][j] = decay_by(dec.head[4 * ty + i], a.v[i][j]);
       __syncthreads();
       mm_nn(P, V, ty, tx, a);
 #pragma unroll
@@ -388,7 +388,7 @@ __global__ void __launch_bounds__(kThreads) gated_grad_kernel(GatedArgs p) {
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        a.v[i][j] *= p.scale * dec.head[4 * ty + i];
+        a.v[i][j] = decay_by(p.scale * dec.head[4 * ty + i], a.v[i][j]);
         rows[i] = fmaf(a.v[i][j], Q[(4 * ty + i) * kP + tx + 16 * j], rows[i]);
       }
     __syncthreads();
@@ -405,7 +405,7 @@ __global__ void __launch_bounds__(kThreads) gated_grad_kernel(GatedArgs p) {
   for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      a.v[i][j] *= dec.tail[4 * ty + i];
+      a.v[i][j] = decay_by(dec.tail[4 * ty + i], a.v[i][j]);
       far[i] = fmaf(a.v[i][j], K[(4 * ty + i) * kP + tx + 16 * j], far[i]);
       dK.v[i][j] += a.v[i][j];
     }
@@ -414,7 +414,7 @@ __global__ void __launch_bounds__(kThreads) gated_grad_kernel(GatedArgs p) {
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) dV.v[i][j] = fmaf(dec.tail[4 * ty + i], a.v[i][j], dV.v[i][j]);
+    for (int j = 0; j < 4; ++j) dV.v[i][j] += decay_by(dec.tail[4 * ty + i], a.v[i][j]);
   store_rows(dK, ty, tx, static_cast<float *>(p.dK) + kvrow, t0, n);
   store_rows(dV, ty, tx, static_cast<float *>(p.dV) + kvrow, t0, n);
 
@@ -453,7 +453,7 @@ __global__ void __launch_bounds__(kThreads) gated_grad_kernel(GatedArgs p) {
     float x = 0.f;
 #pragma unroll
     for (int k = 0; k < kThreads / 32; ++k) x += s_dot[k];
-    x *= dec.head[kGC - 1];
+    x = decay_by(dec.whole.hi, x);
     for (int l = kGC - 1; l >= t; --l) x += s_row[l];
     for (int j = 0; j < t; ++j) x += s_far[j];
     const bool cut = dec.sums.cuts[t] != (t ? dec.sums.cuts[t - 1] : 0);

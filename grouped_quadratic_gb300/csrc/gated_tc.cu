@@ -84,13 +84,17 @@ __device__ __forceinline__ void sum_issue(uint32_t tm, const uint8_t *a, const u
 __device__ __forceinline__ void sum_add(float (&s)[64], GateDecay f, uint32_t tm) {
   const int warp = threadIdx.x >> 5;
   const uint32_t from = tm + ((uint32_t)(32 * warp) << 16);
+  if (f.hi == 0.f) {   // a cut gate: as in decay_add, but one branch instead of 64 masks
+#pragma unroll
+    for (int e = 0; e < 64; ++e) s[e] = 0.f;
+  }
 #pragma unroll
   for (int h = 0; h < 4; ++h) {
     uint32_t x[16];
     tmem_ld16(from + 16 * h, x);
     tmem_wait_ld();
 #pragma unroll
-    for (int e = 0; e < 16; ++e) s[16 * h + e] = decay_add(f, s[16 * h + e], __uint_as_float(x[e]));
+    for (int e = 0; e < 16; ++e) s[16 * h + e] = fmaf(f.hi, s[16 * h + e], fmaf(f.lo, s[16 * h + e], __uint_as_float(x[e])));
   }
   if (warp >= 2) {
 #pragma unroll
@@ -289,7 +293,7 @@ __device__ __noinline__ void slow_scores(const float *g, int t0, int n, int i, u
       const int cj = __shfl_sync(0xffffffffu, s.cuts[e & 1], from);
       const float w = gate_exp_fast(j <= i && cj == cut, (hi - hj) + (lo - lj));
       f[e] = j <= i ? __uint_as_float(x[e]) * w : 0.f;
-      d[e] = __float_as_uint(__uint_as_float(d[e]) * head);
+      d[e] = __float_as_uint(decay_by(head, __uint_as_float(d[e])));
     }
 #pragma unroll
     for (int e = 0; e < 8; ++e) x[e] = pack_bf16x2(f[2 * e], f[2 * e + 1]);

@@ -198,7 +198,7 @@ __device__ __noinline__ void chunk_dg(const GradSmem::Sums &u, const ChunkGates 
   float x = 0.f, r[2], f[2];
 #pragma unroll
   for (int z = 0; z < 8; ++z) x += u.dots[z];
-  x *= gates.whole.hi;
+  x = decay_by(gates.whole.hi, x);
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
     const int t = 2 * lane + e;
@@ -507,7 +507,7 @@ gated_tc_grad_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
           tmem_ld16(from + 16 * h, x);
           tmem_wait_ld();
 #pragma unroll
-          for (int e = 0; e < 16; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * tj);
+          for (int e = 0; e < 16; ++e) x[e] = __float_as_uint(decay_by(tj, __uint_as_float(x[e])));
           if (quad & 2) {
 #pragma unroll
             for (int z = 0; z < 2; ++z) {
@@ -627,7 +627,7 @@ gated_tc_grad_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
             uint32_t o[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const float a = fq * __uint_as_float(x[8 * z + 2 * e]), d = fq * __uint_as_float(x[8 * z + 2 * e + 1]);
+              const float a = decay_by(fq, __uint_as_float(x[8 * z + 2 * e])), d = decay_by(fq, __uint_as_float(x[8 * z + 2 * e + 1]));
               racc = fmaf(__uint_as_float(u[e] << 16), a, racc);
               racc = fmaf(__uint_as_float(u[e] & 0xFFFF0000u), d, racc);
               o[e] = pack_bf16x2(a + __uint_as_float(y[8 * z + 2 * e]), d + __uint_as_float(y[8 * z + 2 * e + 1]));

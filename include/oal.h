@@ -236,8 +236,10 @@ oal_status oal_decode_step(const void *q, const void *k, const void *v,
  * Query heads share the state of their KV head as above.  g is the natural
  * logarithm of the gate, fp32, at most 0 in use; a value of -104 or less (-inf
  * among them), where exp gives 0 in fp32, starts from nothing, as at the
- * first token of a packed document.  NaN and +inf gates and inputs that are
- * not finite make the results of their sequence unspecified.
+ * first token of a packed document: the state before it has no part in what
+ * follows, even where it is not finite (nor the gradient of a state behind it
+ * in what is before it).  NaN and +inf gates and Q, K, V or dY that are not
+ * finite make the results of their sequence (all of its T tokens) unspecified.
  * Supported: d == dv == 64.  State layout: [B][Hkv][d][dv] fp32.
  *
  * oal_gated_prefill -- T tokens.

@@ -590,3 +590,47 @@ def test_slow_gates_over_many_steps(oal, gate):
     age = torch.arange(steps, device="cuda", dtype=torch.float64) * float(g)
     S = (k[:, 0, 0].double() * age.flip(0).exp()[:, None]).T @ v[:, 0, 0].double() + math.exp(steps * float(g)) * state0[0, 0].double()
     assert rel(state[0, 0], S) <= 1e-5
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+@pytest.mark.parametrize("dtype", DTYPES, ids=["f32", "bf16"])
+@pytest.mark.parametrize("B,Hq,Hkv,T,at", [
+    (1, 2, 1, 1, 0), (2, 3, 1, 130, 0), (1, 4, 2, 200, 70), (1, 2, 2, 5000, 3001), (160, 3, 3, 170, 100),
+    (1, 1, 1, 20000, 64)])
+def test_a_cut_shuts_out_a_state_that_is_not_finite(oal, dtype, bad, B, Hq, Hkv, T, at):
+    """Behind a cut gate a state starts from nothing, whatever was in it; the
+    gradient of the state does so in front of one."""
+    c = Case(dtype, B, Hq, Hkv, T, seed=60)
+    c.g[:, :, at] = -math.inf
+    c.g[:, :, 130::400] = -80.0                      # (chunks of every kind of gates behind it)
+    dirty = torch.full_like(c.state0, bad)
+    Y0, S0 = run_forward(oal, c, True)
+    G0 = oal.oal_gated_backward(c.Q, c.K, c.V, c.g, c.dY, SCALE, state0=c.state0, dstate=c.dstate)
+    clean = c.state0
+    c.state0 = dirty
+    Y1, S1 = run_forward(oal, c, True)
+    G1 = oal.oal_gated_backward(c.Q, c.K, c.V, c.g, c.dY, SCALE, state0=dirty, dstate=c.dstate)
+    G2 = oal.oal_gated_backward(c.Q, c.K, c.V, c.g, c.dY, SCALE, state0=clean, dstate=dirty)
+    oal.oal_sync_status()
+    assert torch.equal(S0, S1) and torch.equal(Y0[:, :, at:], Y1[:, :, at:])
+    assert torch.equal(G0[0][:, :, at:], G1[0][:, :, at:])                        # dQ behind the cut
+    assert torch.equal(G0[3][:, :, at:], G1[3][:, :, at:])                        # dg
+    for i in (1, 2, 4):                              # dK, dV and dstate0 do not see the state
+        assert torch.equal(G0[i], G1[i])
+    assert torch.equal(G0[0], G2[0])                                             # dQ does not see its gradient
+    for i in (1, 2, 3):
+        assert torch.equal(G0[i][:, :, :at], G2[i][:, :, :at])
+    assert torch.equal(G0[4], G2[4])
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["f32", "bf16"])
+def test_decode_cut_shuts_out_a_state_that_is_not_finite(oal, dtype):
+    c = Case(dtype, 3, 4, 2, 1, seed=61)
+    c.g[:] = torch.tensor([-math.inf, -104.0, -1e30]).cuda()[:, None, None]
+    args = [x[:, :, 0].contiguous() for x in (c.Q, c.K, c.V, c.g)]
+    want = oal.oal_gated_decode_step(*args, c.state0, SCALE)
+    for bad in (math.nan, math.inf, -math.inf):
+        state = torch.full_like(c.state0, bad)
+        assert torch.equal(oal.oal_gated_decode_step(*args, state, SCALE), want)
+        assert torch.equal(state, c.state0)
+    oal.oal_sync_status()
