@@ -92,8 +92,9 @@ constexpr float kSpan = 60.f;
 struct alignas(16) ChunkGates {
   PairWeights tail;                       // e^{G_63-G_j}
   float rest[kGC], row[kGC];              // e^{R-G_j}, e^{G_i-R}
+  float before[kGC / 2];                  // e^{R'-G_j}, R' that of the second half's rows
   GateDecay whole;                        // e^{G_63} (0 if cut)
-  float first;                            // e^{G_31}
+  float first;                            // e^{R'}
   uint32_t cut_even, cut_odd;             // bit l: the gate of token 2l (2l + 1) is cut
   int mode;
 };
@@ -114,9 +115,13 @@ __device__ __forceinline__ void chunk_gates(float2 gate, const GateLane &sums, C
   const float x0 = (sums.hi[0] - rh) + (sums.lo[0] - rl), x1 = (sums.hi[1] - rh) + (sums.lo[1] - rl);
   reinterpret_cast<float2 *>(to.rest)[lane] = make_float2(__expf(-x0), __expf(-x1));
   reinterpret_cast<float2 *>(to.row)[lane] = make_float2(__expf(x0), __expf(x1));
+  const float bh = plain ? 0.f : mh, bl = plain ? 0.f : ml;
+  if (lane < 16)
+    reinterpret_cast<float2 *>(to.before)[lane] =
+        make_float2(__expf((bh - sums.hi[0]) + (bl - sums.lo[0])), __expf((bh - sums.hi[1]) + (bl - sums.lo[1])));
   if (lane == 0) {
     to.whole = whole;
-    to.first = __expf(mh + ml);
+    to.first = __expf(bh + bl);
     to.cut_even = even;
     to.cut_odd = odd;
     to.mode = plain ? kPlain : halves ? kHalves : kEach;

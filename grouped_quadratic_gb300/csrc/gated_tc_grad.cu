@@ -531,7 +531,8 @@ gated_tc_grad_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
       ++k;
       const int mode = gates.c.mode;
       const float fq = p.scale * gates.head[i];
-      const float fr = p.scale * gates.c.row[i] * (pre && mode == kHalves ? gates.c.first : 1.f);
+      const float fr = p.scale * gates.c.row[i];
+      const float *rest = pre ? gates.c.before : gates.c.rest + 32 * hf;
       int begin = 0;
       cut_before(gates.c, i, begin);
       const uint32_t live = 0xFFFFFFFFu << min(31, max(0, begin - 32 * hf));
@@ -567,7 +568,7 @@ gated_tc_grad_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
             if (mode != kEach) {
 #pragma unroll
               for (int e = 0; e < 8; e += 4) {
-                const float4 r = *reinterpret_cast<const float4 *>(gates.c.rest + 32 * hf + 8 * h + e);
+                const float4 r = *reinterpret_cast<const float4 *>(rest + 8 * h + e);
                 f[e] = fr * r.x, f[e + 1] = fr * r.y, f[e + 2] = fr * r.z, f[e + 3] = fr * r.w;
               }
             } else {

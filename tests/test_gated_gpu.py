@@ -634,3 +634,27 @@ def test_decode_cut_shuts_out_a_state_that_is_not_finite(oal, dtype):
         assert torch.equal(oal.oal_gated_decode_step(*args, state, SCALE), want)
         assert torch.equal(state, c.state0)
     oal.oal_sync_status()
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["f32", "bf16"])
+@pytest.mark.parametrize("gate", [-1.8, -0.9, -0.3])
+def test_only_far_keys(oal, dtype, gate):
+    """Rows that see nothing but the last keys of the chunk's other half."""
+    c = Case(dtype, 1, 2, 1, 64, seed=71)
+    c.g = torch.full_like(c.g, gate)
+    c.K[:, :, :24] = 0
+    c.K[:, :, 32:] = 0
+    check_forward(oal, c, False)
+    Y, _ = run_forward(oal, c)
+    want, _ = oracle(c)
+    for t in range(64):                      # row by row: the first ones are 1e40 times the last
+        err, size = (float(x.norm()) for x in (Y[:, :, t].double().cpu() - want[:, :, t], want[:, :, t]))
+        if size > 1e-30:
+            assert err <= OUT[dtype] * size, t
+    got = oal.oal_gated_backward(c.Q, c.K, c.V, c.g, c.dY, SCALE)
+    oal.oal_sync_status()
+    grads = oracle(c, backward=True)
+    for t in range(64):
+        err, size = (float(x.norm()) for x in (got[0][:, :, t].double().cpu() - grads[0][:, :, t], grads[0][:, :, t]))
+        if size > 1e-30:
+            assert err <= OUT[dtype] * size, t
