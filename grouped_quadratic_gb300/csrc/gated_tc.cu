@@ -9,14 +9,19 @@
 //     D += P V                         tcgen05, P from tensor memory
 // and the state itself in registers (gated_mma.cuh).
 //
-// Where the sums G of each half chunk span at most 60, a row's factor is taken
-// out of its sum: with R = 0 for the first 32 rows, and G_31 for the others
-// unless the whole chunk spans at most 60,
-//     y_i = scale e^{G_i-R} [ e^R S_in^T q_i + sum_j (q_i.k_j) e^{R-G_j} v_j ],
-// one product a score and one a result; no factor exceeds e^60, and the terms
-// of a row keep their ratios.  A cut gate leaves the sums alone and masks the
-// scores and S_in instead.  Other chunks form every decay exp(G_i - G_j) by
-// itself.
+// Where the sums G of a chunk span at most 60, a row's factor is taken out of
+// its sum, one product a score and one a result:
+//     y_i = scale e^{G_i} [ S_in^T q_i + sum_j (q_i.k_j) e^{-G_j} v_j ].
+// The sum is up to e^60 = 1e26 times the result: where that leaves fp32 (results
+// of 3e12 and more), a block whose results are not finite takes its segment
+// again without this way (one more packed product per two results to see that;
+// the next way for every chunk cost 8% of a prefill).
+// Where each half spans at most 60, a decay is the product of two factors,
+//     e^{G_i-G_j} = e^{G_i-R} e^{R-G_j},
+// with R = 0 for the first 32 rows and G_31 for the others, which meet before a
+// score does, and S_in^T q_i takes e^{G_i} in tensor memory; a cut gate leaves
+// the sums alone and masks the scores and S_in instead.  Other chunks form every
+// decay exp(G_i - G_j) by itself.
 #include <algorithm>
 
 #include "gated_tc.cuh"
@@ -265,6 +270,7 @@ struct OutSmem {
   ChunkGates gates[2];                   // by the issuing warp
   uint64_t kv_full[2], q_full[2], gate_full, x_full, d_full, p_full, y_full, go, meet, drain;
   uint32_t tmem;
+  int again;                             // a result was not finite
   WaitState wait;
 };
 static_assert(3 * (sizeof(OutSmem) + 2 * 1024) <= 228 * 1024, "three blocks per SM");
@@ -317,9 +323,8 @@ gated_tc_out_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
   const int bh = blockIdx.x / p.nseg, seg = blockIdx.x % p.nseg, b = bh / p.Hkv, kv = bh % p.Hkv;
   const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
   const int rho = p.Hq / p.Hkv, npair = (rho + 1) / 2;
-  if (tid == 0) {
-    s.wait.abort = 0;
-    s.wait.status = p.status;
+  auto init = [&]() {
+    s.again = 0;
     for (int i = 0; i < 2; ++i) mbar_init(&s.kv_full[i], 1), mbar_init(&s.q_full[i], 1);
     mbar_init(&s.gate_full, 1);
     mbar_init(&s.x_full, 1);
@@ -330,6 +335,11 @@ gated_tc_out_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
     mbar_init(&s.meet, 4);
     mbar_init(&s.drain, 1);
     fence_mbar_init();
+  };
+  if (tid == 0) {
+    s.wait.abort = 0;
+    s.wait.status = p.status;
+    init();
   }
   pdl_wait();
   const int n = gated_len(p, b), last = gated_last_seg(n, p.seg_chunks * kGC);
@@ -350,258 +360,279 @@ gated_tc_out_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
   // stored row by row instead of by TMA (which drops rows from T on)
   auto by_rows = [&](int t0) { return t0 + kGC > n && n < p.T; };
 
-  if (warp == 4) {
-    const uint32_t id_k = idesc_bf16_f32(128, 64, 0), id_mn = idesc_bf16_f32(128, 64, 1);
-    auto load_q = [&](int it) {
-      const int pr = it % npair, heads = min(2, rho - 2 * pr), st = it & 1;
-      mbar_arrive_expect_tx(&s.q_full[st], heads * kTileBytes);
-      for (int h = 0; h < heads; ++h)
-        tma_load_3d(s.q[st] + h * kTileBytes, &tmQ, &s.q_full[st], 0, (c0 + it / npair) * kGC, h0 + 2 * pr + h);
-    };
-    auto prefetch_q = [&](int it) {
-      const int pr = it % npair, heads = min(2, rho - 2 * pr);
-      for (int h = 0; h < heads; ++h) tma_prefetch_3d(&tmQ, 0, (c0 + it / npair) * kGC, h0 + 2 * pr + h);
-    };
-    auto load_kv = [&](int c) {
-      mbar_arrive_expect_tx(&s.kv_full[c & 1], 2 * kTileBytes);
-      tma_load_3d(s.k[c & 1], &tmK, &s.kv_full[c & 1], 0, (c0 + c) * kGC, bh);
-      tma_load_3d(s.v[c & 1], &tmV, &s.kv_full[c & 1], 0, (c0 + c) * kGC, bh);
-    };
-    int kv_loads = 0, q_loads = 0;
-    if (lane == 0) {
-      for (; kv_loads < min(2, nc); ++kv_loads) load_kv(kv_loads);
-      for (; q_loads < min(2, steps); ++q_loads) load_q(q_loads);
-    }
-    const uint64_t sd = sdesc_sw128(smem_u32(s.state), 16, 1024);
-    // X of step it, while the step before writes its outputs
-    auto issue_x = [&](int it) {
-      const int c = it / npair;
-      if (!warp_wait(&s.q_full[it & 1], (it >> 1) & 1, &s.wait) ||
-          !warp_wait(&s.kv_full[c & 1], (c >> 1) & 1, &s.wait))
-        return false;
-      const uint64_t qd = sdesc_sw128(smem_u32(s.q[it & 1]), 16, 1024);
-      const uint64_t kd = sdesc_sw128(smem_u32(s.k[c & 1]), 16, 1024);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) umma_ss_warp(tb + kColX, qd + 2 * k, kd + 2 * k, id_k, k > 0);
-      umma_commit_warp(&s.x_full);
-      return true;
-    };
-    const float *g = p.g + (size_t)bh * p.T;
-    float2 gate = gate_load(g, c0 * kGC, n);
-    auto make_gates = [&](int c) {
-      const float2 now = gate;
-      if (c + 1 < nc) gate = gate_load(g, (c0 + c + 1) * kGC, n);
-      chunk_gates(now, gate_sums(now), s.gates[c & 1]);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&s.gate_full);
-    };
-    __syncwarp();
-    if (nc > 0) make_gates(0);
-    bool ok = steps == 0 || issue_x(0);
-#pragma unroll 1
-    for (int it = 0; it < steps && ok; ++it) {
-      const int c = it / npair, pr = it % npair;
-      // the step before is done: its D is read, its outputs and (a new chunk)
-      // the state are in shared memory
-      ok = warp_wait(&s.go, it & 1, &s.wait);
-      if (!ok) break;
-      tc_fence_after();
-      const uint64_t qd = sdesc_sw128(smem_u32(s.q[it & 1]), 16, 1024);
-      const uint64_t vd = sdesc_sw128(smem_u32(s.v[c & 1]), 16, 1024);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) umma_ss_warp(tb + kColD, qd + 2 * k, sd + 128 * k, id_mn, k > 0);
-      umma_commit_warp(&s.d_full);
+  for (bool careful = false;; careful = true) {
+    if (warp == 4) {
+      const uint32_t id_k = idesc_bf16_f32(128, 64, 0), id_mn = idesc_bf16_f32(128, 64, 1);
+      auto load_q = [&](int it) {
+        const int pr = it % npair, heads = min(2, rho - 2 * pr), st = it & 1;
+        mbar_arrive_expect_tx(&s.q_full[st], heads * kTileBytes);
+        for (int h = 0; h < heads; ++h)
+          tma_load_3d(s.q[st] + h * kTileBytes, &tmQ, &s.q_full[st], 0, (c0 + it / npair) * kGC, h0 + 2 * pr + h);
+      };
+      auto prefetch_q = [&](int it) {
+        const int pr = it % npair, heads = min(2, rho - 2 * pr);
+        for (int h = 0; h < heads; ++h) tma_prefetch_3d(&tmQ, 0, (c0 + it / npair) * kGC, h0 + 2 * pr + h);
+      };
+      auto load_kv = [&](int c) {
+        mbar_arrive_expect_tx(&s.kv_full[c & 1], 2 * kTileBytes);
+        tma_load_3d(s.k[c & 1], &tmK, &s.kv_full[c & 1], 0, (c0 + c) * kGC, bh);
+        tma_load_3d(s.v[c & 1], &tmV, &s.kv_full[c & 1], 0, (c0 + c) * kGC, bh);
+      };
+      int kv_loads = 0, q_loads = 0;
       if (lane == 0) {
-        if (pr == 0 && c > 0 && c + 1 < nc) load_kv(c + 1), ++kv_loads;
-        if (it + 2 < steps) prefetch_q(it + 2);
+        for (; kv_loads < min(2, nc); ++kv_loads) load_kv(kv_loads);
+        for (; q_loads < min(2, steps); ++q_loads) load_q(q_loads);
       }
-      __syncwarp();
-      ok = warp_wait(&s.p_full, it & 1, &s.wait);
-      if (!ok) break;
-      tc_fence_after();
+      const uint64_t sd = sdesc_sw128(smem_u32(s.state), 16, 1024);
+      // X of step it, while the step before writes its outputs
+      auto issue_x = [&](int it) {
+        const int c = it / npair;
+        if (!warp_wait(&s.q_full[it & 1], (it >> 1) & 1, &s.wait) ||
+            !warp_wait(&s.kv_full[c & 1], (c >> 1) & 1, &s.wait))
+          return false;
+        const uint64_t qd = sdesc_sw128(smem_u32(s.q[it & 1]), 16, 1024);
+        const uint64_t kd = sdesc_sw128(smem_u32(s.k[c & 1]), 16, 1024);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) umma_ts_warp(tb + kColD, tb + kColX + 8 * k, vd + 128 * k, id_mn, 1u);
-      umma_commit_warp(&s.y_full);
-      // the outputs of the step before have left their buffer (p_full says so)
-      if (lane == 0 && it > 0 && it + 1 < steps) load_q(it + 1), ++q_loads;
+        for (int k = 0; k < 4; ++k) umma_ss_warp(tb + kColX, qd + 2 * k, kd + 2 * k, id_k, k > 0);
+        umma_commit_warp(&s.x_full);
+        return true;
+      };
+      const float *g = p.g + (size_t)bh * p.T;
+      float2 gate = gate_load(g, c0 * kGC, n);
+      auto make_gates = [&](int c) {
+        const float2 now = gate;
+        if (c + 1 < nc) gate = gate_load(g, (c0 + c + 1) * kGC, n);
+        chunk_gates(now, gate_sums(now), s.gates[c & 1], careful);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s.gate_full);
+      };
       __syncwarp();
-      // P, which lies in X, has been read
-      if (it + 1 < steps) ok = warp_wait(&s.y_full, it & 1, &s.wait) && issue_x(it + 1);
-      if (pr == 0 && c + 1 < nc) make_gates(c + 1);
-    }
-    umma_commit_warp(&s.drain);
-    if (lane == 0) {   // nothing in flight at the block's end
-      mbar_wait_teardown(&s.drain, 0, p.status);
-      for (int i = max(0, kv_loads - 2); i < kv_loads; ++i) mbar_wait_teardown(&s.kv_full[i & 1], (i >> 1) & 1, p.status);
-      for (int i = max(0, q_loads - 2); i < q_loads; ++i) mbar_wait_teardown(&s.q_full[i & 1], (i >> 1) & 1, p.status);
-    }
-    __syncwarp();
-  } else {
-    const int i = tid & 63, half = warp & 1;            // token of this thread's row, its 32-token half
-    const uint32_t tm = tb + ((uint32_t)(32 * warp) << 16);
-    StateAcc<8> acc;
-    state_load(acc, 0, p.seg_state + ((size_t)bh * p.nseg + seg) * kGS);
-    state_round(acc, 0, s.state);
-    fence_proxy_async();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&s.go);
-    float row = 0.f;                                      // factor of the row's result
-    float into = 1.f;                                    // (kHalves) factor of S_in^T q_i
-    int begin = 0, mode = kPlain;                        // first key of the row
-    bool ok = true;
-    // the four computing warps meet (a wait that ends, unlike a barrier of threads)
-    int met = 0;
-    auto meet = [&]() {
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&s.meet);
-      return warp_wait(&s.meet, met++ & 1, &s.wait);
-    };
+      if (nc > 0) make_gates(0);
+      bool ok = steps == 0 || issue_x(0);
 #pragma unroll 1
-    for (int it = 0; it < steps && ok; ++it) {
-      const int c = it / npair, pr = it % npair, t0 = (c0 + c) * kGC;
-      const ChunkGates &gates = s.gates[c & 1];
-      if (pr == 0) {
-        ok = warp_wait(&s.gate_full, c & 1, &s.wait);
+      for (int it = 0; it < steps && ok; ++it) {
+        const int c = it / npair, pr = it % npair;
+        // the step before is done: its D is read, its outputs and (a new chunk)
+        // the state are in shared memory
+        ok = warp_wait(&s.go, it & 1, &s.wait);
         if (!ok) break;
-        mode = gates.mode;
-        row = mode == kEach ? p.scale : p.scale * gates.row[i];
-        begin = 0;
-        into = half && mode == kHalves ? gates.first : 1.f;
-        if (cut_before(gates, i, begin)) into = 0.f;     // keys from the row's last cut gate on, nothing from S_in
-        ok = warp_wait(&s.kv_full[c & 1], (c >> 1) & 1, &s.wait);
-      }
-      ok = ok && warp_wait(&s.x_full, it & 1, &s.wait);
-      if (!ok) break;
-      tc_fence_after();
-      if (pr == 0 && t0 + kGC > n) {                     // rows behind the sequence count as zeros
-        clear_rows(s.k[c & 1], n - t0, tid, 128);
-        clear_rows(s.v[c & 1], n - t0, tid, 128);
-        fence_proxy_async();
-        ok = meet();
-        if (!ok) break;
-      }
-      if (mode != kEach) {
-        // P's columns lie in front of the X still to be read: first the first
-        // half's keys for rows of the second, then the keys of the row's own half
-        uint32_t x[2][16], pk[16];
-        if (half) {
-          tmem_ld16(tm + kColX, x[0]);
-          tmem_ld16(tm + kColX + 16, x[1]);
-          tmem_wait_ld();
-          if (mode == kHalves) {
+        tc_fence_after();
+        const uint64_t qd = sdesc_sw128(smem_u32(s.q[it & 1]), 16, 1024);
+        const uint64_t vd = sdesc_sw128(smem_u32(s.v[c & 1]), 16, 1024);
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              x[e >> 4][e & 15] = e >= begin ? __float_as_uint(__uint_as_float(x[e >> 4][e & 15]) * gates.first) : 0u;
+        for (int k = 0; k < 4; ++k) umma_ss_warp(tb + kColD, qd + 2 * k, sd + 128 * k, id_mn, k > 0);
+        umma_commit_warp(&s.d_full);
+        if (lane == 0) {
+          if (pr == 0 && c > 0 && c + 1 < nc) load_kv(c + 1), ++kv_loads;
+          if (it + 2 < steps) prefetch_q(it + 2);
+        }
+        __syncwarp();
+        ok = warp_wait(&s.p_full, it & 1, &s.wait);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int k = 0; k < 4; ++k) umma_ts_warp(tb + kColD, tb + kColX + 8 * k, vd + 128 * k, id_mn, 1u);
+        umma_commit_warp(&s.y_full);
+        // the outputs of the step before have left their buffer (p_full says so)
+        if (lane == 0 && it > 0 && it + 1 < steps) load_q(it + 1), ++q_loads;
+        __syncwarp();
+        // P, which lies in X, has been read
+        if (it + 1 < steps) ok = warp_wait(&s.y_full, it & 1, &s.wait) && issue_x(it + 1);
+        if (pr == 0 && c + 1 < nc) make_gates(c + 1);
+      }
+      umma_commit_warp(&s.drain);
+      if (lane == 0) {   // nothing in flight at the block's end
+        mbar_wait_teardown(&s.drain, 0, p.status);
+        for (int i = max(0, kv_loads - 2); i < kv_loads; ++i) mbar_wait_teardown(&s.kv_full[i & 1], (i >> 1) & 1, p.status);
+        for (int i = max(0, q_loads - 2); i < q_loads; ++i) mbar_wait_teardown(&s.q_full[i & 1], (i >> 1) & 1, p.status);
+      }
+      __syncwarp();
+    } else {
+      const int i = tid & 63, half = warp & 1;            // token of this thread's row, its 32-token half
+      const uint32_t tm = tb + ((uint32_t)(32 * warp) << 16);
+      StateAcc<8> acc;
+      state_load(acc, 0, p.seg_state + ((size_t)bh * p.nseg + seg) * kGS);
+      state_round(acc, 0, s.state);
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s.go);
+      float row = 0.f;                                      // factor of the row's result
+      float in = 1.f, into = 1.f;                          // of its scores, and (kHalves) of S_in^T q_i
+      uint32_t wrong = 0u;                                 // 0, or NaN once a result was not finite
+      int begin = 0, mode = kPlain;                        // first key of the row
+      bool ok = true;
+      // the four computing warps meet (a wait that ends, unlike a barrier of threads)
+      int met = 0;
+      auto meet = [&]() {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s.meet);
+        return warp_wait(&s.meet, met++ & 1, &s.wait);
+      };
+#pragma unroll 1
+      for (int it = 0; it < steps && ok; ++it) {
+        const int c = it / npair, pr = it % npair, t0 = (c0 + c) * kGC;
+        const ChunkGates &gates = s.gates[c & 1];
+        if (pr == 0) {
+          ok = warp_wait(&s.gate_full, c & 1, &s.wait);
+          if (!ok) break;
+          mode = gates.mode;
+          const float r = gates.row[i];
+          row = mode == kPlain ? p.scale * r : p.scale;
+          in = mode == kPlain ? 1.f : r;
+          begin = 0;
+          into = half ? r * gates.first : r;
+          if (cut_before(gates, i, begin)) into = 0.f;     // keys from the row's last cut gate on, nothing from S_in
+          ok = warp_wait(&s.kv_full[c & 1], (c >> 1) & 1, &s.wait);
+        }
+        ok = ok && warp_wait(&s.x_full, it & 1, &s.wait);
+        if (!ok) break;
+        tc_fence_after();
+        if (pr == 0 && t0 + kGC > n) {                     // rows behind the sequence count as zeros
+          clear_rows(s.k[c & 1], n - t0, tid, 128);
+          clear_rows(s.v[c & 1], n - t0, tid, 128);
+          fence_proxy_async();
+          ok = meet();
+          if (!ok) break;
+        }
+        if (mode != kEach) {
+          // P's columns lie in front of the X still to be read: first the first
+          // half's keys for rows of the second, then the keys of the row's own half
+          uint32_t x[2][16], pk[16];
+          if (half) {
+            tmem_ld16(tm + kColX, x[0]);
+            tmem_ld16(tm + kColX + 16, x[1]);
+            tmem_wait_ld();
+            if (mode == kHalves) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e) x[e >> 4][e & 15] = e >= begin ? x[e >> 4][e & 15] : 0u;
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int e = 0; e < 16; e += 4) {
+                const float4 r = *reinterpret_cast<const float4 *>(gates.before + 16 * h + e);
+                pk[8 * h + (e >> 1)] =
+                    pack_bf16x2(__uint_as_float(x[h][e]) * (in * r.x), __uint_as_float(x[h][e + 1]) * (in * r.y));
+                pk[8 * h + (e >> 1) + 1] =
+                    pack_bf16x2(__uint_as_float(x[h][e + 2]) * (in * r.z), __uint_as_float(x[h][e + 3]) * (in * r.w));
+              }
+            tmem_st16(tm + kColX, pk);
           }
+          const uint32_t mask = (0xFFFFFFFFu >> (31 - lane)) & (0xFFFFFFFFu << max(0, begin - 32 * half));   // begin <= i
+          tmem_ld16(tm + kColX + 32 * half, x[0]);
+          tmem_ld16(tm + kColX + 32 * half + 16, x[1]);
+          tmem_wait_ld();
 #pragma unroll
           for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int e = 0; e < 16; e += 4) {
-              const float4 r = *reinterpret_cast<const float4 *>(gates.rest + 16 * h + e);
-              pk[8 * h + (e >> 1)] = pack_bf16x2(__uint_as_float(x[h][e]) * r.x, __uint_as_float(x[h][e + 1]) * r.y);
+              const float4 r = *reinterpret_cast<const float4 *>(gates.rest + 32 * half + 16 * h + e);
+              const int j = 16 * h + e;
+              pk[8 * h + (e >> 1)] = pack_bf16x2(mask & (1u << j) ? __uint_as_float(x[h][e]) * (in * r.x) : 0.f,
+                                                 mask & (1u << (j + 1)) ? __uint_as_float(x[h][e + 1]) * (in * r.y) : 0.f);
               pk[8 * h + (e >> 1) + 1] =
-                  pack_bf16x2(__uint_as_float(x[h][e + 2]) * r.z, __uint_as_float(x[h][e + 3]) * r.w);
+                  pack_bf16x2(mask & (1u << (j + 2)) ? __uint_as_float(x[h][e + 2]) * (in * r.z) : 0.f,
+                              mask & (1u << (j + 3)) ? __uint_as_float(x[h][e + 3]) * (in * r.w) : 0.f);
             }
-          tmem_st16(tm + kColX, pk);
+          tmem_st16(tm + kColX + 16 * half, pk);
+          if (!half) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) pk[e] = 0u;
+            tmem_st16(tm + kColX + 16, pk);
+          }
+        } else {
+          ok = warp_wait(&s.d_full, it & 1, &s.wait);
+          if (!ok) break;
+          tc_fence_after();
+          slow_scores(p.g + (size_t)bh * p.T, t0, n, i, tm);
         }
-        const uint32_t mask = (0xFFFFFFFFu >> (31 - lane)) & (0xFFFFFFFFu << max(0, begin - 32 * half));   // begin <= i
-        tmem_ld16(tm + kColX + 32 * half, x[0]);
-        tmem_ld16(tm + kColX + 32 * half + 16, x[1]);
+        if (mode == kHalves) {
+          ok = warp_wait(&s.d_full, it & 1, &s.wait);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll 1
+          for (int h = 0; h < 4; ++h) {
+            uint32_t x[16];
+            tmem_ld16(tm + kColD + 16 * h, x);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) x[e] = into == 0.f ? 0u : __float_as_uint(__uint_as_float(x[e]) * into);
+            tmem_st16(tm + kColD + 16 * h, x);
+          }
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          bulk_wait_read();                                // the outputs of the step before are out of shared memory
+          mbar_arrive(&s.p_full);
+        }
+        // the state, while P V runs: half of the chunk with its first pair, the rest with its last
+        if (pr == 0) {
+          state_scale(acc, gates.whole);
+          state_add<0, 2>(acc, 0, s.k[c & 1], s.v[c & 1], gates.tail);
+        }
+        if (pr == npair - 1) {
+          state_add<2, 4>(acc, 0, s.k[c & 1], s.v[c & 1], gates.tail);
+          ok = warp_wait(&s.d_full, it & 1, &s.wait);   // the chunk's last Q S_in is done
+          if (!ok) break;
+          state_round(acc, 0, s.state);
+        }
+        ok = warp_wait(&s.y_full, it & 1, &s.wait);
+        if (!ok) break;
+        tc_fence_after();
+        const int hd = 2 * pr + (warp >> 1);
+        const bool rows = by_rows(t0);
+        uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.Y) + ((size_t)(h0 + hd) * p.T + t0 + i) * 64);
+        uint8_t *tile = s.q[it & 1] + (warp >> 1) * kTileBytes;
+        uint32_t x[4][16];
+#pragma unroll
+        for (int h = 0; h < 4; ++h) tmem_ld16(tm + kColD + 16 * h, x[h]);
         tmem_wait_ld();
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int e = 0; e < 16; e += 4) {
-            const float4 r = *reinterpret_cast<const float4 *>(gates.rest + 32 * half + 16 * h + e);
-            const int j = 16 * h + e;
-            pk[8 * h + (e >> 1)] = pack_bf16x2(mask & (1u << j) ? __uint_as_float(x[h][e]) * r.x : 0.f,
-                                               mask & (1u << (j + 1)) ? __uint_as_float(x[h][e + 1]) * r.y : 0.f);
-            pk[8 * h + (e >> 1) + 1] = pack_bf16x2(mask & (1u << (j + 2)) ? __uint_as_float(x[h][e + 2]) * r.z : 0.f,
-                                                   mask & (1u << (j + 3)) ? __uint_as_float(x[h][e + 3]) * r.w : 0.f);
-          }
-        tmem_st16(tm + kColX + 16 * half, pk);
-        if (!half) {
-#pragma unroll
-          for (int e = 0; e < 16; ++e) pk[e] = 0u;
-          tmem_st16(tm + kColX + 16, pk);
-        }
-      } else {
-        ok = warp_wait(&s.d_full, it & 1, &s.wait);
-        if (!ok) break;
-        tc_fence_after();
-        slow_scores(p.g + (size_t)bh * p.T, t0, n, i, tm);
-      }
-      if (mode == kHalves) {
-        ok = warp_wait(&s.d_full, it & 1, &s.wait);
-        if (!ok) break;
-        tc_fence_after();
-#pragma unroll 1
         for (int h = 0; h < 4; ++h) {
-          uint32_t x[16];
-          tmem_ld16(tm + kColD + 16 * h, x);
-          tmem_wait_ld();
+          uint32_t y[8];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) x[e] = into == 0.f ? 0u : __float_as_uint(__uint_as_float(x[e]) * into);
-          tmem_st16(tm + kColD + 16 * h, x);
+          for (int e = 0; e < 8; ++e)
+            y[e] = pack_bf16x2(__uint_as_float(x[h][2 * e]) * row, __uint_as_float(x[h][2 * e + 1]) * row);
+          if (hd < rho && t0 + i < n)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) wrong = bf2_fma(y[e], 0u, wrong);
+          const uint4 lo = make_uint4(y[0], y[1], y[2], y[3]), hi = make_uint4(y[4], y[5], y[6], y[7]);
+          if (!rows) {
+            *reinterpret_cast<uint4 *>(tile + tile_at(i, 2 * h)) = lo;
+            *reinterpret_cast<uint4 *>(tile + tile_at(i, 2 * h + 1)) = hi;
+          } else if (hd < rho && t0 + i < n) {
+            dst[2 * h] = lo;
+            dst[2 * h + 1] = hi;
+          }
+        }
+        fence_proxy_async();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (!rows && hd < rho && t0 + 32 * half < n) tma_store_3d(&tmY, tile + 32 * half * 128, 0, t0 + 32 * half, h0 + hd);
+          bulk_commit();
+          mbar_arrive(&s.go);
         }
       }
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        bulk_wait_read();                                // the outputs of the step before are out of shared memory
-        mbar_arrive(&s.p_full);
-      }
-      // the state, while P V runs: half of the chunk with its first pair, the rest with its last
-      if (pr == 0) {
-        state_scale(acc, gates.whole);
-        state_add<0, 2>(acc, 0, s.k[c & 1], s.v[c & 1], gates.tail);
-      }
-      if (pr == npair - 1) {
-        state_add<2, 4>(acc, 0, s.k[c & 1], s.v[c & 1], gates.tail);
-        ok = warp_wait(&s.d_full, it & 1, &s.wait);   // the chunk's last Q S_in is done
-        if (!ok) break;
-        state_round(acc, 0, s.state);
-      }
-      ok = warp_wait(&s.y_full, it & 1, &s.wait);
-      if (!ok) break;
-      tc_fence_after();
-      const int hd = 2 * pr + (warp >> 1);
-      const bool rows = by_rows(t0);
-      uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.Y) + ((size_t)(h0 + hd) * p.T + t0 + i) * 64);
-      uint8_t *tile = s.q[it & 1] + (warp >> 1) * kTileBytes;
-      uint32_t x[4][16];
-#pragma unroll
-      for (int h = 0; h < 4; ++h) tmem_ld16(tm + kColD + 16 * h, x[h]);
-      tmem_wait_ld();
-#pragma unroll
-      for (int h = 0; h < 4; ++h) {
-        uint32_t y[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          y[e] = pack_bf16x2(__uint_as_float(x[h][2 * e]) * row, __uint_as_float(x[h][2 * e + 1]) * row);
-        const uint4 lo = make_uint4(y[0], y[1], y[2], y[3]), hi = make_uint4(y[4], y[5], y[6], y[7]);
-        if (!rows) {
-          *reinterpret_cast<uint4 *>(tile + tile_at(i, 2 * h)) = lo;
-          *reinterpret_cast<uint4 *>(tile + tile_at(i, 2 * h + 1)) = hi;
-        } else if (hd < rho && t0 + i < n) {
-          dst[2 * h] = lo;
-          dst[2 * h + 1] = hi;
-        }
-      }
-      fence_proxy_async();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        if (!rows && hd < rho && t0 + 32 * half < n) tma_store_3d(&tmY, tile + 32 * half * 128, 0, t0 + 32 * half, h0 + hd);
-        bulk_commit();
-        mbar_arrive(&s.go);
-      }
+      if (lane == 0) bulk_wait_all();
+      if (wrong & 0x7FFF7FFFu) s.again = 1;
     }
-    if (lane == 0) bulk_wait_all();
+    tc_fence_before();
+    __syncthreads();
+    if (careful || !s.again || s.wait.abort) break;
+    // once more, from the start: nothing is in flight, the barriers begin anew
+    tc_fence_after();
+    __syncthreads();
+    if (tid == 0) {
+      uint64_t *bars[] = {&s.kv_full[0], &s.kv_full[1], &s.q_full[0], &s.q_full[1], &s.gate_full, &s.x_full,
+                          &s.d_full,     &s.p_full,     &s.y_full,    &s.go,        &s.meet,      &s.drain};
+      for (uint64_t *bar : bars) mbar_inval(bar);
+      init();
+    }
+    __syncthreads();
   }
-  tc_fence_before();
-  __syncthreads();
   if (warp == 4) {
     tc_fence_after();
     tmem_dealloc(tb, kOutCols);

@@ -98,8 +98,8 @@ struct alignas(16) ChunkGates {
   uint32_t cut_even, cut_odd;             // bit l: the gate of token 2l (2l + 1) is cut
   int mode;
 };
-// Fills them (one warp; `gate` as loaded, `sums` of it).
-__device__ __forceinline__ void chunk_gates(float2 gate, const GateLane &sums, ChunkGates &to) {
+// Fills them (one warp; `gate` as loaded, `sums` of it); never as kPlain if so told.
+__device__ __forceinline__ void chunk_gates(float2 gate, const GateLane &sums, ChunkGates &to, bool not_plain = false) {
   const int lane = threadIdx.x & 31;
   const uint32_t even = __ballot_sync(0xffffffffu, gate.x <= kGateCut);
   const uint32_t odd = __ballot_sync(0xffffffffu, gate.y <= kGateCut);
@@ -108,7 +108,7 @@ __device__ __forceinline__ void chunk_gates(float2 gate, const GateLane &sums, C
   weights_put(to.tail, tail.x, tail.y);
   const float mh = __shfl_sync(0xffffffffu, sums.hi[1], 15), ml = __shfl_sync(0xffffffffu, sums.lo[1], 15);
   const float span = fmaxf(fabsf(sums.hi[0]), fabsf(sums.hi[1]));
-  const bool plain = __all_sync(0xffffffffu, span <= kSpan) && (even | odd) == 0u;
+  const bool plain = __all_sync(0xffffffffu, span <= kSpan) && (even | odd) == 0u && !not_plain;
   const float rh = plain || lane < 16 ? 0.f : mh, rl = plain || lane < 16 ? 0.f : ml;
   const float near = fmaxf(fabsf(sums.hi[0] - rh), fabsf(sums.hi[1] - rh));
   const bool halves = __all_sync(0xffffffffu, near <= kSpan);

@@ -256,8 +256,11 @@ oal_status oal_decode_step(const void *q, const void *k, const void *v,
  *           aligned, contents need not be initialised.  Calls that may
  *           overlap on the GPU (streams, captured graphs) need one each.
  * Arithmetic: OAL_F32 in fp32 on the CUDA cores.  OAL_BF16 on the tensor
- * cores with fp32 accumulation: the states are sums of fp32 products; the
- * decayed scores and the state a chunk reads are rounded to bf16 once each.
+ * cores with fp32 accumulation: the last state is a sum of fp32 products; for Y
+ * the decayed scores, and the state a chunk reads, are rounded to bf16 once
+ * each, and that state, inside a segment of chunks, adds keys scaled as two
+ * bf16 terms (2^-15).  A result overflows only where the sum of its decayed
+ * terms, before scale, does in fp32.
  * Deterministic.  T == 0 leaves Y untouched and zeroes the state unless
  * continue_from_state != 0.
  */

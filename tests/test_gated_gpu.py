@@ -658,3 +658,38 @@ def test_only_far_keys(oal, dtype, gate):
         err, size = (float(x.norm()) for x in (got[0][:, :, t].double().cpu() - grads[0][:, :, t], grads[0][:, :, t]))
         if size > 1e-30:
             assert err <= OUT[dtype] * size, t
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["f32", "bf16"])
+@pytest.mark.parametrize("size", [1e-8, 1e4, 1e8])
+@pytest.mark.parametrize("gate", [-1.8, -0.9, -0.4, -0.16, -0.01])
+def test_large_and_small_inputs(oal, dtype, size, gate):
+    """Results of up to 1e27 (and down to 1e-24) are inside the types' range,
+    whatever the gates: no factor on the way may leave it."""
+    c = Case(dtype, 1, 3, 1, 150, seed=70)
+    c.g = torch.full_like(c.g, gate)
+    c.g[:, :, 77] = -math.inf
+    for name, f in (("Q", size), ("K", size), ("V", size), ("state0", size * size)):
+        setattr(c, name, (getattr(c, name) * f).contiguous())
+    check_forward(oal, c, True)
+    check_backward(oal, c, True)
+
+
+def test_large_inputs_in_some_segments(oal):
+    """bf16, segments of three chunks, some of which outgrow the first way of
+    forming them: all come out as by themselves."""
+    c = Case(torch.bfloat16, 160, 9, 3, 170, seed=72, lengths=[170, 169, 128, 129, 5, 0, 64, 65] * 20)
+    c.g = torch.full_like(c.g, -0.9)
+    Y0, S0 = run_forward(oal, c, True)
+    for name, f in (("Q", 1e8), ("K", 1e8), ("V", 1e8), ("state0", 1e16)):
+        x = getattr(c, name)
+        x[::3] *= f
+    Y1, S1 = run_forward(oal, c, True)
+    small = torch.arange(160, device="cuda") % 3 != 0
+    assert torch.equal(Y0[small], Y1[small]) and torch.equal(S0[small], S1[small])
+    check_forward(oal, c, True)
+    for b in (0, 3, 6, 9):                   # by themselves, as the large ones hide the others in a norm
+        one = Case(torch.bfloat16, 1, 9, 3, 170, seed=72, lengths=[int(c.lengths[b])])
+        for name in ("Q", "K", "V", "g", "state0"):
+            setattr(one, name, getattr(c, name)[b:b + 1].clone())
+        check_forward(oal, one, True)
