@@ -693,3 +693,52 @@ def test_large_inputs_in_some_segments(oal):
         for name in ("Q", "K", "V", "g", "state0"):
             setattr(one, name, getattr(c, name)[b:b + 1].clone())
         check_forward(oal, one, True)
+
+
+# ---------------------------------------------------------------- row by row
+
+def rows_off(got, want, inside=None):
+    """The largest error of a row (of the last dimension), relative to the row's
+    norm or the tensor's root mean square of them, whichever is larger: the
+    roundings that a tensor's tolerance counts are those of the row's own terms,
+    which may cancel, but are of the size of other rows' terms."""
+    got, want = got.double().cpu(), want.double().cpu()
+    err, size = (got - want).norm(dim=-1), want.norm(dim=-1)
+    if inside is not None:
+        inside = inside[..., 0].cpu()
+        err, size = err[inside], size[inside]
+    assert torch.isfinite(err).all()
+    rms = float(size.square().mean().sqrt())
+    return float((err / size.clamp(min=max(rms, 1e-30))).max()) if err.numel() else 0.0
+
+
+def every_kind_of_gate(c):
+    """Chunk after chunk as drawn, four times, thirty times as steep, and with a cut."""
+    for i, t0 in enumerate(range(0, c.T, 64)):
+        c.g[:, :, t0:t0 + 64] *= (1.0, 30.0, 4.0, 1.0)[i % 4]
+        if i % 4 == 3:
+            c.g[:, :, t0 + i % 64] = -math.inf
+    return c
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=["f32", "bf16"])
+@pytest.mark.parametrize("B,Hq,Hkv,T,span,lengths", [
+    (2, 10, 2, 191, 30.0, [191, 17]), (1, 7, 1, 1000, 30.0, None), (3, 9, 1, 257, 3.0, [257, 256, 3]),
+    # several chunks a segment of the prefill and a block of the backward
+    (160, 3, 3, 170, 3.0, [170, 169, 128, 129, 5, 0, 64, 65] * 20), (60, 10, 2, 400, 3.0, None),
+    (100, 5, 5, 330, 30.0, list(range(231, 331))),
+    # many segments of few states, some sequences shorter; more than the split scan's round of 256
+    (3, 4, 2, 3000, 300.0, [3000, 0, 1101]), (2, 1, 1, 17000, 2000.0, [17000, 16383])])
+def test_row_by_row(oal, dtype, B, Hq, Hkv, T, span, lengths):
+    c = every_kind_of_gate(Case(dtype, B, Hq, Hkv, T, seed=80 + B, span=span, lengths=lengths))
+    Y, state = run_forward(oal, c, True)
+    want, S = oracle(c, c.state0)
+    assert rows_off(Y, want, c.rows(Y)) <= OUT[dtype]
+    assert rows_off(state.flatten(2), S.flatten(2)) <= STATE[dtype]
+    got = oal.oal_gated_backward(c.Q, c.K, c.V, c.g, c.dY, SCALE, lengths=c.lengths, state0=c.state0, dstate=c.dstate)
+    oal.oal_sync_status()
+    want = oracle(c, c.state0, c.dstate, backward=True)
+    for name, x, w in zip(("dQ", "dK", "dV"), got, want):
+        assert rows_off(x, w, c.rows(x)) <= OUT[dtype], name
+    assert rows_off(got[3], want[3]) <= DG[dtype]                       # (a row: a sequence and head)
+    assert rows_off(got[4].flatten(2), want[4].flatten(2)) <= STATE[dtype]
