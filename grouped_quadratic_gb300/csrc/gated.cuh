@@ -34,11 +34,11 @@ __device__ __forceinline__ GateDecay decay_exp(float x) {
   const float hi = expf(x);
   return {hi, fabsf(x) < 0.5f ? expm1f(x) - (hi - 1.f) : 0.f};
 }
+// (lo may outgrow half a step of hi; not renormalised, a row of these is as deep
+// as one of plain products)
 __device__ __forceinline__ GateDecay decay_mul(GateDecay a, GateDecay b) {
   const float p = a.hi * b.hi;
-  const float e = fmaf(a.hi, b.hi, -p) + fmaf(a.hi, b.lo, a.lo * b.hi);
-  const float hi = p + e;
-  return {hi, e - (hi - p)};
+  return {p, fmaf(a.lo, b.hi, fmaf(a.hi, b.lo, fmaf(a.hi, b.hi, -p)))};
 }
 // f s + d.  A decay of 0 (a cut gate) shuts out whatever s is, NaN and
 // infinities too.
