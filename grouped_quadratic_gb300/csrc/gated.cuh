@@ -66,7 +66,6 @@ struct GatedArgs {
   float *seg_state;                     // [B Hkv][nseg][64 64]
   GateDecay *seg_decay;                 // [B Hkv][nseg]
   float *seg_grad;                      // backward: the same for the state's gradient
-  uint8_t *state_tiles, *grad_tiles;    // backward (bf16): S and R of each chunk, two 8 KB tiles each
   int *status;
 };
 

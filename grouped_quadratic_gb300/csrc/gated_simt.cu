@@ -495,8 +495,11 @@ static oal_status launch_scan(const GatedArgs &p, int ways, cudaStream_t stream)
     launch_pdl(gated_scan_kernel<4, 8, 1, kLast>, dim3(units, kGS / 4 / kScanThreads, ways), dim3(kScanThreads), 0, stream, p);
   return oal_after_launch("gated_scan_kernel", stream);
 }
-// From the segments' own states to those before them and the last one.
-oal_status launch_gated_scan(const GatedArgs &p, cudaStream_t stream) { return launch_scan<true>(p, 1, stream); }
+// From the segments' own states to those before them and (last) the one behind
+// the last of them; with two ways, the gradients too.
+oal_status launch_gated_scan(const GatedArgs &p, int ways, bool last, cudaStream_t stream) {
+  return last ? launch_scan<true>(p, ways, stream) : launch_scan<false>(p, ways, stream);
+}
 
 oal_status launch_gated_prefill_simt(const GatedArgs &p, cudaStream_t stream) {
   static bool done_seg[kMaxDevices], done_out[kMaxDevices];

@@ -268,6 +268,7 @@ struct OutSmem {
   uint8_t q[2][2 * kTileBytes];          // two heads' queries, then their outputs
   uint8_t state[kTileBytes];             // the state before the chunk, bf16
   ChunkGates gates[2];                   // by the issuing warp
+  PairWeights tail[2];                   // e^{G_63-G_j}
   uint64_t kv_full[2], q_full[2], gate_full, x_full, d_full, p_full, y_full, go, meet, drain;
   uint32_t tmem;
   int again;                             // a result was not finite
@@ -402,7 +403,9 @@ gated_tc_out_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
       auto make_gates = [&](int c) {
         const float2 now = gate;
         if (c + 1 < nc) gate = gate_load(g, (c0 + c + 1) * kGC, n);
-        chunk_gates(now, gate_sums(now), s.gates[c & 1], careful);
+        float2 tail;
+        chunk_gates<false>(now, gate_sums(now), s.gates[c & 1], tail, careful);
+        weights_put(s.tail[c & 1], tail.x, tail.y);
         __syncwarp();
         if (lane == 0) mbar_arrive(&s.gate_full);
       };
@@ -570,10 +573,10 @@ gated_tc_out_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
         // the state, while P V runs: half of the chunk with its first pair, the rest with its last
         if (pr == 0) {
           state_scale(acc, gates.whole);
-          state_add<0, 2>(acc, 0, s.k[c & 1], s.v[c & 1], gates.tail);
+          state_add<0, 2>(acc, 0, s.k[c & 1], s.v[c & 1], s.tail[c & 1]);
         }
         if (pr == npair - 1) {
-          state_add<2, 4>(acc, 0, s.k[c & 1], s.v[c & 1], gates.tail);
+          state_add<2, 4>(acc, 0, s.k[c & 1], s.v[c & 1], s.tail[c & 1]);
           ok = warp_wait(&s.d_full, it & 1, &s.wait);   // the chunk's last Q S_in is done
           if (!ok) break;
           state_round(acc, 0, s.state);
@@ -641,7 +644,7 @@ gated_tc_out_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
 
 }  // namespace
 
-oal_status launch_gated_scan(const GatedArgs &p, cudaStream_t stream);
+oal_status launch_gated_scan(const GatedArgs &p, int ways, bool last, cudaStream_t stream);
 
 oal_status launch_gated_prefill_tc(const GatedArgs &p, cudaStream_t stream) {
   static bool done_seg[kMaxDevices], done_out[kMaxDevices];
@@ -656,7 +659,7 @@ oal_status launch_gated_prefill_tc(const GatedArgs &p, cudaStream_t stream) {
   const dim3 grid(p.nseg * p.B * p.Hkv);
   launch_pdl(gated_tc_segment_kernel, grid, dim3(kSegThreads), seg_smem, stream, tmK, tmV, p);
   GATED_TRY(oal_after_launch("gated_tc_segment_kernel", stream));
-  GATED_TRY(launch_gated_scan(p, stream));
+  GATED_TRY(launch_gated_scan(p, 1, true, stream));
   launch_pdl(gated_tc_out_kernel, grid, dim3(kOutThreads), out_smem, stream, tmQ, tmK, tmV, tmY, p);
   return oal_after_launch("gated_tc_out_kernel", stream);
 }

@@ -90,7 +90,6 @@ constexpr int kPlain = 0, kHalves = 1, kEach = 2;
 constexpr float kSpan = 60.f;
 
 struct alignas(16) ChunkGates {
-  PairWeights tail;                       // e^{G_63-G_j}
   float rest[kGC], row[kGC];              // e^{R-G_j}, e^{G_i-R}
   float before[kGC / 2];                  // e^{R'-G_j}, R' that of the second half's rows
   GateDecay whole;                        // e^{G_63} (0 if cut)
@@ -98,27 +97,40 @@ struct alignas(16) ChunkGates {
   uint32_t cut_even, cut_odd;             // bit l: the gate of token 2l (2l + 1) is cut
   int mode;
 };
-// Fills them (one warp; `gate` as loaded, `sums` of it); never as kPlain if so told.
-__device__ __forceinline__ void chunk_gates(float2 gate, const GateLane &sums, ChunkGates &to, bool not_plain = false) {
+// e^{a-b} of two sums hi + lo.  kExact: to fp32's last bits, which the fast
+// exponential of a sum rounded to fp32 is not where that is large (3e-6 at 60).
+template <bool kExact>
+__device__ __forceinline__ float gate_exp_sums(float ah, float al, float bh, float bl) {
+  if (!kExact) return __expf((ah - bh) + (al - bl));
+  float x, e;
+  two_sum(ah, -bh, x, e);
+  x = expf(x);
+  return fmaf(x, e + (al - bl), x);
+}
+// Fills them, and the lane's decays to the chunk's end (one warp; `gate` as
+// loaded, `sums` of it); never as kPlain if so told.
+template <bool kExact>
+__device__ __forceinline__ void chunk_gates(float2 gate, const GateLane &sums, ChunkGates &to, float2 &tail,
+                                            bool not_plain = false) {
   const int lane = threadIdx.x & 31;
   const uint32_t even = __ballot_sync(0xffffffffu, gate.x <= kGateCut);
   const uint32_t odd = __ballot_sync(0xffffffffu, gate.y <= kGateCut);
-  float2 tail;
   const GateDecay whole = gate_tails(sums, tail);
-  weights_put(to.tail, tail.x, tail.y);
   const float mh = __shfl_sync(0xffffffffu, sums.hi[1], 15), ml = __shfl_sync(0xffffffffu, sums.lo[1], 15);
   const float span = fmaxf(fabsf(sums.hi[0]), fabsf(sums.hi[1]));
   const bool plain = __all_sync(0xffffffffu, span <= kSpan) && (even | odd) == 0u && !not_plain;
-  const float rh = plain || lane < 16 ? 0.f : mh, rl = plain || lane < 16 ? 0.f : ml;
+  const float bh = plain ? 0.f : mh, bl = plain ? 0.f : ml;          // R'
+  const float rh = lane < 16 ? 0.f : bh, rl = lane < 16 ? 0.f : bl;   // R
   const float near = fmaxf(fabsf(sums.hi[0] - rh), fabsf(sums.hi[1] - rh));
   const bool halves = __all_sync(0xffffffffu, near <= kSpan);
-  const float x0 = (sums.hi[0] - rh) + (sums.lo[0] - rl), x1 = (sums.hi[1] - rh) + (sums.lo[1] - rl);
-  reinterpret_cast<float2 *>(to.rest)[lane] = make_float2(__expf(-x0), __expf(-x1));
-  reinterpret_cast<float2 *>(to.row)[lane] = make_float2(__expf(x0), __expf(x1));
-  const float bh = plain ? 0.f : mh, bl = plain ? 0.f : ml;
-  if (lane < 16)
-    reinterpret_cast<float2 *>(to.before)[lane] =
-        make_float2(__expf((bh - sums.hi[0]) + (bl - sums.lo[0])), __expf((bh - sums.hi[1]) + (bl - sums.lo[1])));
+  float2 rest, row, before;
+  rest.x = gate_exp_sums<kExact>(rh, rl, sums.hi[0], sums.lo[0]), rest.y = gate_exp_sums<kExact>(rh, rl, sums.hi[1], sums.lo[1]);
+  row.x = gate_exp_sums<kExact>(sums.hi[0], sums.lo[0], rh, rl), row.y = gate_exp_sums<kExact>(sums.hi[1], sums.lo[1], rh, rl);
+  before.x = gate_exp_sums<kExact>(bh, bl, sums.hi[0], sums.lo[0]);
+  before.y = gate_exp_sums<kExact>(bh, bl, sums.hi[1], sums.lo[1]);
+  reinterpret_cast<float2 *>(to.rest)[lane] = rest;
+  reinterpret_cast<float2 *>(to.row)[lane] = row;
+  if (lane < 16) reinterpret_cast<float2 *>(to.before)[lane] = before;
   if (lane == 0) {
     to.whole = whole;
     to.first = __expf(bh + bl);

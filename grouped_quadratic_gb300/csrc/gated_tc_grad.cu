@@ -10,10 +10,11 @@
 // (dq', dk': the terms with S and R; they and X, Z enter dg unrounded).
 //   gated_tc_own_kernel   a chunk's own state (K, V) and own gradient of the
 //                         state before it (Q, dY of all heads), registers
-//   gated_tc_scan_kernel  S and R of every chunk from those, as two bf16 tiles
-//                         hi + lo each (off by at most 2^-16)
+//   gated_scan_kernel     (gated_simt.cu) S and R of every chunk from those
 //   gated_tc_grad_kernel  the gradients, chunks in any order: a pair of query
-//                         heads is 128 rows; two blocks per SM.
+//                         heads is 128 rows; two blocks per SM.  S and R are
+//                         operands as three bf16 terms, which hold all of their
+//                         bits (R as two for dV, which is rounded to bf16).
 // Tensor memory of a block: X, then dY S^T | Z, then z K | 128 columns of
 // [p | z]^T [dY | Q], of which the upper left quarter is dV and the lower
 // right one dK, on top of K R and V R^T.
@@ -107,48 +108,6 @@ gated_tc_own_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
   state_store(acc, 0, (grad ? p.seg_grad : p.seg_state) + ((size_t)bh * p.nseg + c) * kGS);
 }
 
-// ---------------------------------------------------------------- scan
-
-// z = 0: the state before each chunk, forwards; 1: the gradient of the state
-// behind each, backwards, and dstate0; as a word each of the hi and lo tiles
-// for two neighbouring values.  HBM-bound: 20 us for 2048 chunks both ways
-// (134 MB, 6.7 TB/s).
-template <int kVec, int kAhead, int kChains>
-__global__ void __launch_bounds__(kScanThreads) gated_tc_scan_kernel(GatedArgs p) {
-  pdl_trigger();
-  pdl_wait();
-  constexpr int kLanes = kScanThreads / kChains;
-  const int bh = blockIdx.x, x = kVec * (blockIdx.y * kLanes + threadIdx.x % kLanes);
-  const bool grad = blockIdx.z != 0;
-  const int n = gated_len(p, bh / p.Hkv), count = (n + kGC - 1) / kGC;
-  const float *own = (grad ? p.seg_grad : p.seg_state) + (size_t)bh * p.nseg * kGS + x;
-  uint8_t *tiles = (grad ? p.grad_tiles : p.state_tiles) + (size_t)bh * p.nseg * 2 * kTileBytes +
-                   tile_at(x >> 6, (x & 63) >> 3) + 2 * (x & 7);
-  const float *from = grad ? p.dstate : p.state_in;
-  const GateDecay *decay = p.seg_decay + (size_t)bh * p.nseg;
-  if (from) from += (size_t)bh * kGS + x;
-  auto put = [&](int i, const ScanVec<kVec> &v) {
-    uint8_t *at = tiles + (size_t)i * 2 * kTileBytes;
-    uint32_t hi[kVec / 2], lo[kVec / 2];
-#pragma unroll
-    for (int e = 0; e < kVec / 2; ++e) {
-      hi[e] = pack_bf16x2(v.v[2 * e], v.v[2 * e + 1]);
-      lo[e] = pack_bf16x2(v.v[2 * e] - __uint_as_float(hi[e] << 16), v.v[2 * e + 1] - __uint_as_float(hi[e] & 0xFFFF0000u));
-    }
-    if (kVec == 4) {
-      *reinterpret_cast<uint2 *>(at) = make_uint2(hi[0], hi[kVec / 2 - 1]);
-      *reinterpret_cast<uint2 *>(at + kTileBytes) = make_uint2(lo[0], lo[kVec / 2 - 1]);
-    } else {
-      *reinterpret_cast<uint32_t *>(at) = hi[0];
-      *reinterpret_cast<uint32_t *>(at + kTileBytes) = lo[0];
-    }
-  };
-  ScanVec<kVec> run;
-  if constexpr (kChains == 1) run = scan_walk<kVec, kAhead>(own, decay, from, count, count, grad, put);
-  else run = scan_split<kVec, kAhead, kChains>(own, decay, from, count, count, grad, put);
-  if (grad && p.dstate0 && threadIdx.x < kLanes) scan_store(p.dstate0 + (size_t)bh * kGS + x, run);
-}
-
 // ---------------------------------------------------------------- gradients
 
 // Factors f of keys j0 .. j0 + 7 of the chunk for row i by themselves, where
@@ -176,8 +135,9 @@ constexpr uint32_t kGradCols = 256;
 struct GradSmem {
   uint8_t kv[2 * kTileBytes];                  // K, V
   uint8_t oq[4 * kTileBytes];                  // dY of two heads, Q of two heads
-  uint8_t pz[4 * kTileBytes];                  // p, z of 128 rows; dQ after p, R hi, R lo before z
-  uint8_t st[2 * kTileBytes];                  // S hi, lo
+  uint8_t pz[4 * kTileBytes];                  // p, z of 128 rows; dQ after p; before z R in fp32, then its
+                                               // first two terms, and the third before p
+  uint8_t st[3 * kTileBytes];                  // S in fp32, then its terms
   struct alignas(16) Gates {
     ChunkGates c;
     float tail[kGC], head[kGC];                // e^{G_63-G_j}, e^{G_i}
@@ -185,12 +145,22 @@ struct GradSmem {
   struct Sums {                                // parts of dg
     float rows[2][2 * kGC], cols[4][kGC], far[2][kGC], dots[8];
   } sums[2];
-  uint64_t kv_full, r_full, gate_full, far_full, q_full, clean, go, xz_full, pz_full, dq_full, p_free, pair[4], meet,
-      chunk_done[2], drain;
+  uint64_t kv_full, r_full, gate_full, split_full, far_full, q_full, clean, go, xz_full, pz_full, dq_full, p_free, pair[4],
+      meet, chunk_done[2], drain;
   uint32_t tmem;
   WaitState wait;
 };
 static_assert(2 * (sizeof(GradSmem) + 2 * 1024) <= 228 * 1024, "two blocks per SM");
+
+// Four values as three bf16 terms, which hold all of their 24 bits.
+__device__ __forceinline__ void split_put(float4 x, uint8_t *to0, uint8_t *to1, uint8_t *to2) {
+  uint2 t[3];
+  split3(x.x, x.y, t[0].x, t[1].x, t[2].x);
+  split3(x.z, x.w, t[0].y, t[1].y, t[2].y);
+  *reinterpret_cast<uint2 *>(to0) = t[0];
+  *reinterpret_cast<uint2 *>(to1) = t[1];
+  *reinterpret_cast<uint2 *>(to2) = t[2];
+}
 
 // dg of a chunk from its parts (one warp, two tokens a lane).
 __device__ __noinline__ void chunk_dg(const GradSmem::Sums &u, const ChunkGates &gates, float *dg, int rows) {
@@ -256,6 +226,7 @@ gated_tc_grad_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
     s.wait.abort = 0;
     s.wait.status = p.status;
     mbar_init(&s.kv_full, 1), mbar_init(&s.r_full, 1), mbar_init(&s.gate_full, 1), mbar_init(&s.far_full, 1);
+    mbar_init(&s.split_full, 8);
     mbar_init(&s.q_full, 1), mbar_init(&s.clean, 8), mbar_init(&s.go, 8), mbar_init(&s.xz_full, 1);
     mbar_init(&s.pz_full, 8), mbar_init(&s.dq_full, 1), mbar_init(&s.p_free, 4), mbar_init(&s.meet, 8);
     mbar_init(&s.chunk_done[0], 8), mbar_init(&s.chunk_done[1], 8), mbar_init(&s.drain, 1);
@@ -327,9 +298,9 @@ gated_tc_grad_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
         mbar_arrive_expect_tx(&s.kv_full, 4 * kTileBytes);
         tma_load_3d(s.kv, &tmK, &s.kv_full, 0, t0, bh);
         tma_load_3d(s.kv + kTileBytes, &tmV, &s.kv_full, 0, t0, bh);
-        bulk_load(s.st, p.state_tiles + ((size_t)bh * p.nseg + x.c) * 2 * kTileBytes, 2 * kTileBytes, &s.kv_full);
+        bulk_load(s.st, p.seg_state + ((size_t)bh * p.nseg + x.c) * kGS, kGS * sizeof(float), &s.kv_full);
         mbar_arrive_expect_tx(&s.r_full, 2 * kTileBytes);
-        bulk_load(s.pz + 2 * kTileBytes, p.grad_tiles + ((size_t)bh * p.nseg + x.c) * 2 * kTileBytes, 2 * kTileBytes, &s.r_full);
+        bulk_load(s.pz + 2 * kTileBytes, p.seg_grad + ((size_t)bh * p.nseg + x.c) * kGS, kGS * sizeof(float), &s.r_full);
         load_q(t0, h0, 0), ++q_loads;
         if (npair > 1) prefetch_q(t0, h0, 1);
       }
@@ -338,8 +309,7 @@ gated_tc_grad_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
       const float2 gate = gate_load(p.g + (size_t)bh * p.T, t0, n);
       const GateLane sums = gate_sums(gate);
       GradSmem::Gates &to = s.gates[k & 1];
-      chunk_gates(gate, sums, to.c);
-      gate_tails(sums, reinterpret_cast<float2 *>(to.tail)[lane]);
+      chunk_gates<true>(gate, sums, to.c, reinterpret_cast<float2 *>(to.tail)[lane]);
       reinterpret_cast<float2 *>(to.head)[lane] = make_float2(gate_exp_fast(sums.cuts[0] == 0, sums.hi[0] + sums.lo[0]),
                                                               gate_exp_fast(sums.cuts[1] == 0, sums.hi[1] + sums.lo[1]));
       arrive(&s.gate_full);
@@ -355,11 +325,11 @@ gated_tc_grad_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
           const Place y = next_of(x);
           if (pr == npair - 1 && y.b < p.B) {
             const int nbh = y.b * p.Hkv + y.kv;
-            const size_t tiles = ((size_t)nbh * p.nseg + y.c) * 2 * kTileBytes;
+            const size_t at = ((size_t)nbh * p.nseg + y.c) * kGS;
             tma_prefetch_3d(&tmK, 0, y.c * kGC, nbh);
             tma_prefetch_3d(&tmV, 0, y.c * kGC, nbh);
-            prefetch_l2(p.state_tiles + tiles, 2 * kTileBytes);
-            prefetch_l2(p.grad_tiles + tiles, 2 * kTileBytes);
+            prefetch_l2(p.seg_state + at, kGS * sizeof(float));
+            prefetch_l2(p.seg_grad + at, kGS * sizeof(float));
             prefetch_q(y.c * kGC, y.b * p.Hq + y.kv * rho, 0);
           }
         }
@@ -384,9 +354,11 @@ gated_tc_grad_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
     const uint32_t id_kv = idesc_bf16_f32(128, 128, 1) | (1u << 15);   // A with rows along its minor axis too
     const uint64_t od = sdesc_sw128(smem_u32(s.oq), 16, 1024), qd = sdesc_sw128(smem_u32(s.oq) + 2 * kTileBytes, 16, 1024);
     const uint64_t kd = sdesc_sw128(smem_u32(s.kv), 16, 1024), vd = sdesc_sw128(smem_u32(s.kv) + kTileBytes, 16, 1024);
-    const uint64_t sh = sdesc_sw128(smem_u32(s.st), 16, 1024), sl = sdesc_sw128(smem_u32(s.st) + kTileBytes, 16, 1024);
-    const uint64_t rh = sdesc_sw128(smem_u32(s.pz) + 2 * kTileBytes, 16, 1024);
-    const uint64_t rl = sdesc_sw128(smem_u32(s.pz) + 3 * kTileBytes, 16, 1024), zd = rh;
+    // the terms of S one behind the other, of R the first two at z, the third at p
+    constexpr uint64_t kNext = kTileBytes >> 4;
+    const uint64_t sd = sdesc_sw128(smem_u32(s.st), 16, 1024);
+    const uint64_t rd = sdesc_sw128(smem_u32(s.pz) + 2 * kTileBytes, 16, 1024), zd = rd;
+    const uint64_t rd3 = sdesc_sw128(smem_u32(s.pz), 16, 1024);
     // [p | z] and [dY | Q]: two 64-column atoms, 16 KB apart
     const uint64_t pzd = sdesc_sw128(smem_u32(s.pz), 2 * kTileBytes, 1024);
     const uint64_t oqd = sdesc_sw128(smem_u32(s.oq), 2 * kTileBytes, 1024);
@@ -410,17 +382,15 @@ gated_tc_grad_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
         umma_commit_warp(&s.xz_full);
         if (pr == 0) {
           // [K; V] R and [K; V] R^T side by side: K R above on the left, V R^T below on the right
-          ok = wait(&s.r_full, k) && (k == 0 || wait(&s.chunk_done[(k - 1) & 1], (k - 1) >> 1));
+          ok = wait(&s.split_full, k) && (k == 0 || wait(&s.chunk_done[(k - 1) & 1], (k - 1) >> 1));
           if (!ok) break;
           tc_fence_after();
 #pragma unroll
-          for (int j = 0; j < 4; ++j) umma_ss_warp(tkv, kd + 2 * j, rh + 128 * j, id_mn, j > 0);
+          for (int j = 0; j < 8; ++j) umma_ss_warp(tkv, kd + 2 * (j & 3), rd + kNext * (j >> 2) + 128 * (j & 3), id_mn, j > 0);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) umma_ss_warp(tkv, kd + 2 * j, rl + 128 * j, id_mn, 1u);
+          for (int j = 0; j < 8; ++j) umma_ss_warp(tkv + 64, kd + 2 * (j & 3), rd + kNext * (j >> 2) + 2 * (j & 3), id_k, j > 0);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) umma_ss_warp(tkv + 64, kd + 2 * j, rh + 2 * j, id_k, j > 0);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) umma_ss_warp(tkv + 64, kd + 2 * j, rl + 2 * j, id_k, 1u);
+          for (int j = 0; j < 4; ++j) umma_ss_warp(tkv + 64, kd + 2 * j, rd3 + 2 * j, id_k, 1u);
           umma_commit_warp(&s.far_full);
           ++k;
         }
@@ -428,9 +398,7 @@ gated_tc_grad_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
         if (!ok) break;
         tc_fence_after();
 #pragma unroll
-        for (int j = 0; j < 4; ++j) umma_ss_warp(tx, od + 2 * j, sh + 2 * j, id_k, j > 0);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) umma_ss_warp(tx, od + 2 * j, sl + 2 * j, id_k, 1u);
+        for (int j = 0; j < 12; ++j) umma_ss_warp(tx, od + 2 * (j & 3), sd + kNext * (j >> 2) + 2 * (j & 3), id_k, j > 0);
 #pragma unroll
         for (int j = 0; j < 4; ++j) umma_ss_warp(tz, zd + 2 * j, kd + 128 * j, id_mn, j > 0);
 #pragma unroll
@@ -480,18 +448,29 @@ gated_tc_grad_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
       ok = wait(&s.r_full, k);
       if (!ok) break;
       {
-        // <S, R>: all four tiles hold an element at the same place
-        const uint32_t *a = reinterpret_cast<const uint32_t *>(s.st), *r = reinterpret_cast<const uint32_t *>(s.pz + 2 * kTileBytes);
+        // S and R (row-major, as the scan left them) into their terms, in the same
+        // place: all of them read, then written.  <S, R> on the way.
+        float4 sv[4], rv[4];
         float dot = 0.f;
-#pragma unroll 2
-        for (int z = 0; z < 8; ++z) {
-          const int x = tid + 256 * z;
-          const uint32_t ah = a[x], al = a[x + kTileBytes / 4], gh = r[x], gl = r[x + kTileBytes / 4];
-          dot = fmaf(__uint_as_float(ah << 16) + __uint_as_float(al << 16),
-                     __uint_as_float(gh << 16) + __uint_as_float(gl << 16), dot);
-          dot = fmaf(__uint_as_float(ah & 0xFFFF0000u) + __uint_as_float(al & 0xFFFF0000u),
-                     __uint_as_float(gh & 0xFFFF0000u) + __uint_as_float(gl & 0xFFFF0000u), dot);
+#pragma unroll
+        for (int z = 0; z < 4; ++z) {
+          sv[z] = reinterpret_cast<const float4 *>(s.st)[tid + 256 * z];
+          rv[z] = reinterpret_cast<const float4 *>(s.pz + 2 * kTileBytes)[tid + 256 * z];
+          dot = fmaf(sv[z].x, rv[z].x, fmaf(sv[z].y, rv[z].y, dot));
+          dot = fmaf(sv[z].z, rv[z].z, fmaf(sv[z].w, rv[z].w, dot));
         }
+        arrive(&s.meet);
+        ok = wait(&s.meet, met++) && (it == 0 || wait(&s.p_free, it - 1));   // (dQ has left the third term's place)
+        if (!ok) break;
+#pragma unroll
+        for (int z = 0; z < 4; ++z) {
+          const int f = tid + 256 * z;
+          const uint32_t at = tile_at(f >> 4, (f & 15) >> 1) + 8 * (f & 1);
+          split_put(sv[z], s.st + at, s.st + kTileBytes + at, s.st + 2 * kTileBytes + at);
+          split_put(rv[z], s.pz + 2 * kTileBytes + at, s.pz + 3 * kTileBytes + at, s.pz + at);
+        }
+        fence_proxy_async();
+        arrive(&s.split_full);
 #pragma unroll
         for (int d = 16; d; d >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, d);
         if (lane == 0) sums.dots[warp] = dot;
@@ -525,10 +504,7 @@ gated_tc_grad_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
         tmem_wait_st();
         tc_fence_before();
       }
-      arrive(&s.meet);
-      ok = wait(&s.meet, met++);                               // R is read by all: z takes its place
-      if (!ok) break;
-      ++k;
+      ++k;                                                     // (R has been read: p and z take its place)
       const int mode = gates.c.mode;
       const float fq = p.scale * gates.head[i];
       const float fr = p.scale * gates.c.row[i];
@@ -710,6 +686,8 @@ gated_tc_grad_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
 
 }  // namespace
 
+oal_status launch_gated_scan(const GatedArgs &p, int ways, bool last, cudaStream_t stream);
+
 oal_status launch_gated_backward_tc(const GatedArgs &p, cudaStream_t stream) {
   static bool done_own[2][kMaxDevices], done_grad[kMaxDevices];
   const int total = p.nseg * p.B * p.Hkv;
@@ -730,13 +708,7 @@ oal_status launch_gated_backward_tc(const GatedArgs &p, cudaStream_t stream) {
   GATED_TRY(make_map(&tmDQ, p.dQ, p.T, hq, 32));
   launch_pdl(own, dim3(total, 2), dim3(kOwnThreads), own_smem, stream, tmQ, tmK, tmV, tmO, p);
   GATED_TRY(oal_after_launch("gated_tc_own_kernel", stream));
-  const int units = p.B * p.Hkv;
-  if (scan_deep(2 * units, p.nseg))
-    launch_pdl(gated_tc_scan_kernel<2, 32, kScanChains>, dim3(units, kGS / 2 * kScanChains / kScanThreads, 2),
-               dim3(kScanThreads), 0, stream, p);
-  else
-    launch_pdl(gated_tc_scan_kernel<4, 8, 1>, dim3(units, kGS / 4 / kScanThreads, 2), dim3(kScanThreads), 0, stream, p);
-  GATED_TRY(oal_after_launch("gated_tc_scan_kernel", stream));
+  GATED_TRY(launch_gated_scan(p, 2, false, stream));
   launch_pdl(gated_tc_grad_kernel, dim3(std::min(total, 2 * 152)), dim3(kGradThreads), grad_smem, stream, tmQ, tmK, tmV,
              tmO, tmDQ, p);
   return oal_after_launch("gated_tc_grad_kernel", stream);

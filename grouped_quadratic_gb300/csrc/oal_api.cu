@@ -521,8 +521,7 @@ size_t oal_gated_backward_workspace_bytes(int B, int Hq, int Hkv, int T, int d, 
   if (check_gated(B, Hq, Hkv, T, d, dv, dtype, 1.f) != OAL_OK) return 0;
   if (B == 0 || T == 0) return 256;
   const int nseg = oal::gated_segments(T, 1);   // a segment is a chunk
-  // (bf16: and both once more, as pairs of bf16 tiles)
-  return (dtype == OAL_BF16 ? 4 : 2) * gated_states_bytes(B, Hkv, nseg) +
+  return 2 * gated_states_bytes(B, Hkv, nseg) +
          round256((size_t)B * Hkv * nseg * sizeof(oal::GateDecay));
 }
 
@@ -568,9 +567,7 @@ oal_status oal_gated_backward(const void *Q, const void *K, const void *V, oal_d
   const size_t states = gated_states_bytes(B, Hkv, p.nseg);
   p.seg_state = static_cast<float *>(workspace);
   p.seg_grad = reinterpret_cast<float *>(static_cast<char *>(workspace) + states);
-  uint8_t *rest = static_cast<uint8_t *>(workspace) + 2 * states;
-  if (dtype == OAL_BF16) p.state_tiles = rest, p.grad_tiles = rest + states, rest += 2 * states;
-  p.seg_decay = reinterpret_cast<oal::GateDecay *>(rest);
+  p.seg_decay = reinterpret_cast<oal::GateDecay *>(static_cast<char *>(workspace) + 2 * states);
   p.status = oal_device_status_word();
   if (!p.status) return oal_fail(OAL_ERR_CUDA, "no device status word");
   oal_begin_call(stream);

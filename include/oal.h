@@ -286,9 +286,9 @@ oal_status oal_gated_prefill(const void *Q, const void *K, const void *V, oal_dt
  *           another output.  Rows behind a sequence's length
  *           are neither read nor written.
  * Arithmetic: as for the prefill; bf16: the decayed score gradients are
- * rounded to bf16 for dQ and dK, the decayed scores for dV, and the states and
- * their gradients enter as two bf16 terms (2^-16); dg is formed from unrounded
- * scores.  Deterministic: no atomics on the outputs.  T == 0: dstate0 = dstate.
+ * rounded to bf16 for dQ and dK, the decayed scores for dV; dg is a sum of fp32
+ * products of unrounded scores and states.  Deterministic: no atomics on the
+ * outputs.  T == 0: dstate0 = dstate.
  */
 size_t oal_gated_backward_workspace_bytes(int B, int Hq, int Hkv, int T, int d, int dv,
                                           oal_dtype dtype);

@@ -742,3 +742,15 @@ def test_row_by_row(oal, dtype, B, Hq, Hkv, T, span, lengths):
         assert rows_off(x, w, c.rows(x)) <= OUT[dtype], name
     assert rows_off(got[3], want[3]) <= DG[dtype]                       # (a row: a sequence and head)
     assert rows_off(got[4].flatten(2), want[4].flatten(2)) <= STATE[dtype]
+
+
+@pytest.mark.parametrize("span", [30.0, 300.0, 2000.0])
+def test_gate_gradients_as_sums_of_fp32_products(oal, span):
+    """dg of bf16 inputs: products of states in all of their bits.  A sum takes
+    at most 12 steps in the tensor cores, which cut: 12 * 2^-23 = 1.4e-6; the
+    sums over a chunk's tokens behind that add sqrt(128) 2^-24 = 7e-7."""
+    c = Case(torch.bfloat16, 1, 4, 1, 4096, seed=90, span=span)
+    got = oal.oal_gated_backward(c.Q, c.K, c.V, c.g, c.dY, SCALE, state0=c.state0, dstate=c.dstate)
+    oal.oal_sync_status()
+    want = oracle(c, c.state0, c.dstate, backward=True)
+    assert rel(got[3], want[3]) <= 2.1e-6
