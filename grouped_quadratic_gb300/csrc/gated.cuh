@@ -289,9 +289,9 @@ __device__ __forceinline__ ScanVec<kVec> scan_split(const float *own, const Gate
   }
   return run;
 }
-// Few states and many segments: the split walk (205 segments of 2 states: 8 us
-// against 16 by one thread a value with 32 loads ahead, 22 with 8); otherwise
-// the states' own number fills the GPU.
+// Few states and many segments: the split walk (205 segments of 2 states: 7 us;
+// one thread a value took 16 with 32 loads ahead, 22 with 8, when this one took
+// 8); otherwise the states' own number fills the GPU.
 inline bool scan_deep(int states, int segments) { return states <= 16 && segments > 16; }
 constexpr int kScanChains = 8;
 

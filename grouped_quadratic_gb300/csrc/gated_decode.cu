@@ -9,6 +9,9 @@
 // before the first use.  Replayed with the states in L2: 2.6 us for 2 units,
 // 4.9 for 512, 18 for 4096; four blocks a unit, 16 columns each, took 2.9,
 // 6.8 and 37, and with cold states were ahead at no number of units either.
+// Before its state a block looks through the slots of the sequences before its
+// own, work that grows with the square of the batch: at 4096 sequences of 8
+// heads the call takes 179 us, the bytes alone 158.
 #include "gated.cuh"
 
 namespace oal {

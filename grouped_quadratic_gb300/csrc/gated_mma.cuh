@@ -68,7 +68,8 @@ __device__ __forceinline__ uint32_t bf2_fma(uint32_t a, uint32_t b, uint32_t c) 
 // lo = bf16(w_lo a + that), three packed products for two values; the terms'
 // sum is off by at most 2^-15 of w a where one rounded factor would be off by
 // 2^-8.  b is exact.  (For a state that is rounded to bf16 before it is read;
-// state_step is the exact one.)
+// state_step is the exact one.  Here the tensor cores add to the state itself
+// and cut: 1.3e-4 low after 1024 chunks.)
 // The terms of one accumulator are kNb products apart, and the next
 // 16 rows' operand is under way while these multiply.
 template <int kFrom, int kTo, int kNb>

@@ -5,7 +5,7 @@
 // owns rows 4 ty .. 4 ty + 3 and columns tx, tx + 16, tx + 32, tx + 48 of a
 // product, so a warp's reads of the left tile are broadcasts and those of the
 // right tile meet no bank twice (pitch 68: four words past a row of 64).
-// fp32 inputs only.  Bound by the latency of a chunk where there are few: 28 us
+// fp32 inputs only.  Bound by the latency of a chunk where there are few: 32 us
 // for 2 x 777 tokens of 4 heads in three launches, 44 us for the backward of
 // 2 x 513 tokens, 4/2 heads; by the fp32 pipes where there are many.
 #include <algorithm>
@@ -479,7 +479,8 @@ oal_status gated_need_smem(const void *kernel, size_t bytes, bool (&done)[kMaxDe
 // 4 x 32/8 heads x 8192 tokens 97, 92, 84, 95, 87; 65536 tokens 77, 76, 68,
 // 84, 76; 4 x 16/16 x 4096 75, 73, 63, 70, 66; 8 x 32/8 x 512 20, 20, 20, 23,
 // 23.  Fewer lose more (1 per SM 164, 112, 107, 25).  Only small ragged
-// batches gain from more (14/2 heads, 201 tokens: 28 -> 25 with 4).
+// batches gain from more (14/2 heads, 201 tokens: 28 -> 25 with 4).  (The fp32
+// kernel, of which two fit an SM, goes by the same rule; it was not measured.)
 int gated_prefill_segment(int B, int Hkv, int T) {
   const long long units = (long long)B * Hkv, chunks = ((long long)T + kGC - 1) / kGC;
   const long long want = std::max<long long>(1, 3 * 152 / units);

@@ -21,7 +21,15 @@
 // with R = 0 for the first 32 rows and G_31 for the others, which meet before a
 // score does, and S_in^T q_i takes e^{G_i} in tensor memory; a cut gate leaves
 // the sums alone and masks the scores and S_in instead.  Other chunks form every
-// decay exp(G_i - G_j) by itself.
+// decay exp(G_i - G_j) by itself.  Prefill of 4 x 8192 tokens, 32/8 heads: 83.5 us
+// by the first way, 91.6 by the second (g = -1.5), 184 by the third (g = -3), 143
+// where every segment is taken again.
+//
+// Rounded to bf16, because the tensor cores take both factors in the inputs'
+// type: P, and the state that a chunk reads, by 2^-8 at most each.  Y is off by
+// 2.35e-3 in the mean, of which 1.66e-3 are its own rounding.  Second terms would
+// be 8 more MMAs to a step's 12 and another 8 KB a block, where three blocks
+// leave none.
 #include <algorithm>
 
 #include "gated_tc.cuh"
@@ -151,9 +159,9 @@ static_assert(3 * (sizeof(SegSmem) + 2 * 1024) <= 228 * 1024, "three blocks per 
 // Own state of each segment: K and V once.
 // A chunk's decays are a chain of shuffles as long as its products: eight
 // chunks' are formed side by side, or every chunk would wait for its own.
-// 4 x 8192 tokens of 8 KV heads, 32 query heads: 80.5 us a prefill (this
-// kernel alone 25, 2.7 TB/s), where mma.sync, 96 products a warp and chunk, took
-// 85.9.  A chunk is 2,500 cycles of a block, three of which share the SM -
+// 24.5 us for 4 x 8192 tokens of 8 KV heads (2.8 TB/s); mma.sync, 96 products a
+// warp and chunk, made the whole prefill 85.9 us where this made it 80.5.  A
+// chunk is 2,500 cycles of a block, three of which share the SM -
 // splitting 500, MMAs 800, their sums 300, waits - after 5,000 until the first
 // one is there.  A warp of its own for loads, decays and MMAs with two places
 // for the sums took 2 us more: the decays, 2,000 cycles a chunk there, were in
@@ -309,9 +317,9 @@ __device__ __noinline__ void slow_scores(const float *g, int t0, int n, int i, u
   }
 }
 
-// A block walks a segment, three blocks per SM (73 KB of shared memory, 128
-// columns of tensor memory, 121 registers).  53 us for 4 x 8192 tokens, 32/8
-// heads: 5.3 TB/s of DRAM traffic, 78% of a copy's; the rest is the chain
+// A block walks a segment, three blocks per SM (76 KB of shared memory, 128
+// columns of tensor memory, 108 registers).  57.5 us for 4 x 8192 tokens, 32/8
+// heads: 5.2 TB/s of DRAM traffic, 77% of a copy's; the rest is the chain
 // load - X - P - P V - outputs that three blocks do not quite hide.  Two teams
 // of four warps, a pair of heads each, with two blocks per SM took 86 us where
 // this took 68.

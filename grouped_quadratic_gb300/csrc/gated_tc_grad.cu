@@ -208,12 +208,11 @@ __device__ __noinline__ void fetch_heads(const CUtensorMap *tmO, const CUtensorM
   }
 }
 
-// 88 us for 4 x 4096 tokens, 32/8 heads (306 MB: 3.5 TB/s).  Bound by the chain
-// of a step - tile loads, X and Z, p and z, 20 MMAs, dQ - about 10,000 cycles a
-// pair of heads where two blocks per SM leave 5,000; tensor pipe 23% busy,
-// shared memory 30%, instruction fetches from behind the SM's cache 40% of what
-// that path can do (66% at 68 KB of code, before its rare paths went out of
-// line).
+// 97 us for 4 x 4096 tokens, 32/8 heads (307 MB: 3.2 TB/s).  Bound by the chain
+// of a step - tile loads, X and Z, p and z, 24 MMAs, dQ - about 11,000 cycles a
+// pair of heads where two blocks per SM leave half of that; tensor pipe 23% busy.
+// With S and R as two bf16 terms each, formed by the scan, it took 88, and the
+// scan 2 us more; dg was off by 3e-6 instead of 7e-7.
 __global__ void __launch_bounds__(kGradThreads, 2)
 gated_tc_grad_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                      const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
