@@ -225,8 +225,11 @@ tc_prep_kernel(const float *__restrict__ a, const float *__restrict__ b,
                const int32_t *__restrict__ group, int G, float eps, int packed,
                __nv_bfloat16 *__restrict__ coef, KPlan *__restrict__ plans, int *status,
                KtArgs kt) {
-  pdl_trigger();
+  // In this order: once this kernel signals, the intra and readout kernels may
+  // start and load Q, K and V ahead of their own waits, and what comes before
+  // the call in the stream (a kernel that signals early too) may write those.
   pdl_wait();
+  pdl_trigger();
   const int ncoef = (kKP + 255) / 256;
   if ((int)blockIdx.y > ncoef + 1) {
     // ---- K^T for the state kernel: [unit][64 dims][nC * 128 tokens], zero past T

@@ -754,3 +754,64 @@ def test_gate_gradients_as_sums_of_fp32_products(oal, span):
     oal.oal_sync_status()
     want = oracle(c, c.state0, c.dstate, backward=True)
     assert rel(got[3], want[3]) <= 2.1e-6
+
+
+# ---------------------------------------------------------------- next to other calls
+
+def test_the_quadratic_kernel_reads_what_a_gated_call_just_wrote(oal):
+    """Y of a gated prefill as Q, K and V of oal_prefill with nothing between
+    the two calls, whose kernels overlap at their ends."""
+    from grouped_quadratic_gb300 import inputs
+    B, H, T = 2, 8, 2000
+    w = inputs.make_workload("chain", B=1, Hq=H, Hkv=H, T=16, G=3, dtype="bf16", seed=78)
+    L, group = torch.from_numpy(w.L).cuda(), torch.from_numpy(w.group).cuda()
+    lay = oal.OAL_STATE_PACKED
+    a, b, C = oal.oal_expand_coeffs(L, group, w.eps, lay)
+    c = Case(torch.bfloat16, B, H, H, T, seed=95)
+    Y, state = torch.empty_like(c.Q), torch.empty_like(c.state0)
+    Z, prefix = torch.empty_like(c.Q), torch.empty(B, H, oal.oal_state_rows(64, lay), 65, device="cuda")
+    gws = torch.empty(oal.oal_gated_prefill_workspace_bytes(B, H, H, T), dtype=torch.uint8, device="cuda")
+    ows = torch.empty(oal.oal_prefill_workspace_bytes(B, H, H, T, layout=lay), dtype=torch.uint8, device="cuda")
+
+    def gated():
+        oal.oal_gated_prefill(c.Q, c.K, c.V, c.g, SCALE, state=state, Y=Y, workspace=gws)
+
+    def quadratic():
+        oal.oal_prefill(Y, Y, Y, L, group, w.eps, a, b, C, lay, state=prefix, Y=Z, workspace=ows)
+
+    gated()
+    torch.cuda.synchronize()
+    quadratic()
+    oal.oal_sync_status()
+    want = Z.clone(), prefix.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        gated()
+        quadratic()
+    for run in [lambda: (gated(), quadratic())] * 3 + [graph.replay] * 3:
+        for x in (Y, Z, prefix):
+            x.zero_()
+        torch.cuda.synchronize()
+        run()
+        oal.oal_sync_status()
+        assert torch.equal(Z, want[0]) and torch.equal(prefix, want[1])
+
+
+def test_calls_at_once_on_two_streams(oal):
+    """Prefills and backwards that share the SMs, a workspace each."""
+    c, d = Case(torch.bfloat16, 4, 8, 4, 3000, seed=96), Case(torch.bfloat16, 3, 6, 2, 2500, seed=97, lengths=[2500, 700, 1])
+    forward = lambda x, **kw: oal.oal_gated_prefill(x.Q, x.K, x.V, x.g, SCALE, lengths=x.lengths, **kw)
+    back = lambda x, **kw: oal.oal_gated_backward(x.Q, x.K, x.V, x.g, x.dY, SCALE, lengths=x.lengths, state0=x.state0, **kw)
+    want = forward(c) + back(c), forward(d) + back(d)
+    torch.cuda.synchronize()
+    one, two = torch.cuda.Stream(), torch.cuda.Stream()
+    got = [[], []]
+    for _ in range(4):
+        for out, x, stream in ((got[0], c, one), (got[1], d, two)):
+            with torch.cuda.stream(stream):
+                out.append(forward(x) + back(x))
+    torch.cuda.synchronize()
+    oal.oal_sync_status()
+    for outs, ref in zip(got, want):
+        for out in outs:
+            assert all(torch.equal(x, y) for x, y in zip(out, ref))
