@@ -11,8 +11,8 @@ Tensor layouts (row-major, contiguous, CUDA):
   state [B,Hkv,F,65] float32 (F = 4161 FULL, 2145 PACKED)
   gated recurrence: g [B,Hkv,T] float32 (log decays), state [B,Hkv,64,64] float32
 
-A gated call given a `stream` waits there for the tensors that it makes itself
-(on the current stream); tensors given to it have to be ready on `stream`.
+A call given a `stream` waits there for the tensors that it makes itself (on the
+current stream); tensors given to it have to be ready on `stream`.
 """
 import ctypes
 import os
@@ -125,10 +125,35 @@ def _check(status):
         raise OALError(status, _lib.oal_last_error().decode())
 
 
-def _stream(stream):
+def _order(stream, made):
+    """Orders the tensors a call made, from the current stream's pool, with the
+    stream it launches on.  Work queued on the current stream may still use
+    their memory, and some are being zeroed there, so `stream` waits for it;
+    and the memory must not be handed out again before `stream` is done with
+    it.  Tensors the caller gives are the caller's to order."""
+    if made:
+        current = torch.cuda.current_stream(stream.device)
+        if stream != current:
+            stream.wait_stream(current)
+            for t in made:
+                t.record_stream(stream)
+
+
+def _stream(stream, made=()):
+    """The handle to launch on; `made`: tensors the call allocated."""
     if stream is None:
         stream = torch.cuda.current_stream()
+    else:
+        _order(stream, made)
     return ctypes.c_void_p(stream.cuda_stream)
+
+
+def _make(made, t, shape, dtype, dev):
+    """t, or a new tensor, which joins `made`."""
+    if t is None:
+        t = torch.empty(shape, dtype=dtype, device=dev)
+        made.append(t)
+    return t
 
 
 def _ptr(t):
@@ -171,17 +196,13 @@ def oal_expand_coeffs(L, group, eps, layout=OAL_STATE_FULL, a=None, b=None, C=No
     lib = load_library()
     Hq, G1, _ = L.shape
     d = group.shape[1]
-    dev = L.device
-    if a is None:
-        a = torch.empty(Hq, dtype=torch.float32, device=dev)
-    if b is None:
-        b = torch.empty(Hq, d, dtype=torch.float32, device=dev)
-    if C is None:
-        C = torch.empty(Hq, lib.oal_coeff_table_elems(d, layout), dtype=torch.float32,
-                        device=dev)
+    dev, f32, made = L.device, torch.float32, []
+    a = _make(made, a, (Hq,), f32, dev)
+    b = _make(made, b, (Hq, d), f32, dev)
+    C = _make(made, C, (Hq, lib.oal_coeff_table_elems(d, layout)), f32, dev)
     _need_cuda(L, group, a, b, C)
     _check(lib.oal_expand_coeffs(_ptr(L), _ptr(group), Hq, G1 - 1, d, float(eps), layout,
-                                 _ptr(a), _ptr(b), _ptr(C), _stream(stream)))
+                                 _ptr(a), _ptr(b), _ptr(C), _stream(stream, made)))
     return a, b, C
 
 
@@ -199,21 +220,17 @@ def oal_prefill(Q, K, V, L, group, eps, a, b, C, layout=OAL_STATE_FULL, state=No
     Hkv, dv = K.shape[1], V.shape[3]
     G = L.shape[1] - 1
     dt = _dtype_code(Q)
-    dev = Q.device
-    if state is None:
-        state = torch.empty(B, Hkv, lib.oal_state_rows(d, layout), dv + 1,
-                            dtype=torch.float32, device=dev)
-    if Y is None:
-        Y = torch.empty(B, Hq, T, dv, dtype=Q.dtype, device=dev)
+    dev, made = Q.device, []
+    state = _make(made, state, (B, Hkv, lib.oal_state_rows(d, layout), dv + 1), torch.float32, dev)
+    Y = _make(made, Y, (B, Hq, T, dv), Q.dtype, dev)
     need = lib.oal_prefill_workspace_bytes(B, Hq, Hkv, T, d, dv, dt, layout, chunk)
-    if workspace is None:
-        workspace = torch.empty(max(int(need), 256), dtype=torch.uint8, device=dev)
+    workspace = _make(made, workspace, (max(int(need), 256),), torch.uint8, dev)
     _need_cuda(Q, K, V, L, group, a, b, C, state, Y, workspace)
     _check(lib.oal_prefill(_ptr(Q), _ptr(K), _ptr(V), dt, B, Hq, Hkv, T, d, dv, _ptr(L),
                            _ptr(group), G, float(eps), _ptr(a), _ptr(b), _ptr(C), layout,
                            _ptr(state), int(bool(continue_from_state)), _ptr(Y), chunk,
                            _ptr(workspace), workspace.numel() * workspace.element_size(),
-                           _stream(stream)))
+                           _stream(stream, made)))
     return Y, state
 
 
@@ -255,15 +272,13 @@ def oal_prefill_backward(Q, K, V, dY, L, group, eps, dQ=None, dK=None, dV=None, 
     B, Hq, T, d = Q.shape
     Hkv, dv = K.shape[1], V.shape[3]
     G = L.shape[1] - 1
-    dev = Q.device
-    f32 = torch.float32
-    dQ = torch.empty(B, Hq, T, d, dtype=f32, device=dev) if dQ is None else dQ
-    dK = torch.empty(B, Hkv, T, d, dtype=f32, device=dev) if dK is None else dK
-    dV = torch.empty(B, Hkv, T, dv, dtype=f32, device=dev) if dV is None else dV
-    dL = torch.empty(Hq, G + 1, G + 1, dtype=f32, device=dev) if dL is None else dL
-    if workspace is None:
-        need = lib.oal_prefill_backward_workspace_bytes(B, Hq, Hkv, T, d, dv)
-        workspace = torch.empty(max(int(need), 256), dtype=torch.uint8, device=dev)
+    dev, f32, made = Q.device, torch.float32, []
+    dQ = _make(made, dQ, (B, Hq, T, d), f32, dev)
+    dK = _make(made, dK, (B, Hkv, T, d), f32, dev)
+    dV = _make(made, dV, (B, Hkv, T, dv), f32, dev)
+    dL = _make(made, dL, (Hq, G + 1, G + 1), f32, dev)
+    need = lib.oal_prefill_backward_workspace_bytes(B, Hq, Hkv, T, d, dv)
+    workspace = _make(made, workspace, (max(int(need), 256),), torch.uint8, dev)
     if dY.dtype != Q.dtype:
         raise OALError(OAL_ERR_INVALID_ARG, "dY must have the dtype of Q")
     _need_cuda(Q, K, V, dY, L, group, dQ, dK, dV, dL, workspace)
@@ -271,7 +286,7 @@ def oal_prefill_backward(Q, K, V, dY, L, group, eps, dQ=None, dK=None, dV=None, 
                                     Hkv, T, d, dv, _ptr(L), _ptr(group), G, float(eps), _ptr(dQ),
                                     _ptr(dK), _ptr(dV), _ptr(dL), _ptr(workspace),
                                     workspace.numel() * workspace.element_size(),
-                                    _stream(stream)))
+                                    _stream(stream, made)))
     return dQ, dK, dV, dL
 
 
@@ -285,17 +300,16 @@ def oal_decode_step(q, k, v, a, b, C, state, layout=OAL_STATE_FULL, y=None,
     lib = load_library()
     B, Hq, d = q.shape
     Hkv, dv = k.shape[1], v.shape[2]
-    dt = _dtype_code(q)
-    if y is None:
-        y = torch.empty(B, Hq, dv, dtype=q.dtype, device=q.device)
+    dt, made = _dtype_code(q), []
+    y = _make(made, y, (B, Hq, dv), q.dtype, q.device)
     if workspace is None:
         need = lib.oal_decode_workspace_bytes(B, Hq, Hkv, d, dv, layout)
-        workspace = torch.empty(max(int(need), 256), dtype=torch.uint8, device=q.device)
+        workspace = _make(made, None, (max(int(need), 256),), torch.uint8, q.device)
     _need_cuda(q, k, v, a, b, C, state, y, workspace)
     _check(lib.oal_decode_step(_ptr(q), _ptr(k), _ptr(v), dt, B, Hq, Hkv, d, dv, _ptr(a),
                                _ptr(b), _ptr(C), layout, _ptr(state), _ptr(y),
                                _ptr(workspace), workspace.numel() * workspace.element_size(),
-                               _stream(stream)))
+                               _stream(stream, made)))
     return y
 
 
@@ -308,17 +322,15 @@ def oal_contribution_scores(Q, K, lengths=None, chi=None, workspace=None, stream
     [P] int32 (CUDA) or None for T tokens each.  Returns chi [P,Hq,64] float32."""
     lib = load_library()
     P, Hq, T, d = Q.shape
-    Hkv = K.shape[1]
-    if chi is None:
-        chi = torch.empty(P, Hq, d, dtype=torch.float32, device=Q.device)
-    if workspace is None:
-        need = lib.oal_contribution_workspace_bytes(P, Hq, Hkv, T, d)
-        workspace = torch.empty(max(int(need), 256), dtype=torch.uint8, device=Q.device)
+    Hkv, made = K.shape[1], []
+    chi = _make(made, chi, (P, Hq, d), torch.float32, Q.device)
+    need = lib.oal_contribution_workspace_bytes(P, Hq, Hkv, T, d)
+    workspace = _make(made, workspace, (max(int(need), 256),), torch.uint8, Q.device)
     _need_cuda(Q, K, lengths, chi, workspace)
     _check(lib.oal_contribution_scores(_ptr(Q), _ptr(K), _dtype_code(Q), P, Hq, Hkv, T, d,
                                        _ptr(lengths), _ptr(chi), _ptr(workspace),
                                        workspace.numel() * workspace.element_size(),
-                                       _stream(stream)))
+                                       _stream(stream, made)))
     return chi
 
 
@@ -365,22 +377,13 @@ def _elsewhere(dev):
 
 def _stream_on(dev, stream, made):
     """The handle to launch on: that of `stream`, or of the current stream of
-    dev.  `made`: tensors this call allocated from the current stream's pool.
-    Work queued there may still use their memory, and some are being zeroed
-    there, so `stream` waits for it; and the memory must not be handed out
-    again before `stream` is done with it.  Tensors the caller gives are the
-    caller's to order."""
+    dev.  `made`: tensors this call allocated."""
     if stream is None:
         return torch._C._cuda_getCurrentRawStream(dev.index)
     if stream.device != dev:
         raise OALError(OAL_ERR_INVALID_ARG, "the stream is on %s, the tensors on %s"
                        % (stream.device, dev))
-    if made:
-        current = torch.cuda.current_stream(dev)
-        if stream != current:
-            stream.wait_stream(current)
-            for t in made:
-                t.record_stream(stream)
+    _order(stream, made)
     return stream.cuda_stream
 
 

@@ -119,3 +119,42 @@ def test_missing_library_fails_loudly(tmp_path):
             oal.load_library(str(tmp_path / "nope.so"))
     finally:
         oal._lib = saved
+
+
+def test_calls_order_what_they_make_before_their_stream(monkeypatch):
+    """oal_prefill, its backward, the decode step, the scores and the tables on a
+    stream that is not the current one: the stream waits for the current one,
+    from whose pool they allocate, and keeps their memory."""
+    import torch
+    from grouped_quadratic_gb300 import oal
+
+    class Stream:
+        device, cuda_stream = torch.device("cuda", 0), 77
+
+        def __init__(self):
+            self.calls = []
+
+        def wait_stream(self, other):
+            self.calls.append(("wait", other))
+
+    class Lib:                                    # sizes, and calls that succeed
+        def __getattr__(self, name):
+            return lambda *a: 64 if name.endswith(("_bytes", "_elems", "_rows")) else 0
+
+    now, side = Stream(), Stream()
+    monkeypatch.setattr(oal, "load_library", lambda: Lib())
+    monkeypatch.setattr(oal, "_need_cuda", lambda *t: None)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda dev=None: now)
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: s.calls.append(("record", t)))
+    z = torch.zeros
+    Q, K, L, g = z(1, 2, 8, 64), z(1, 1, 8, 64), z(2, 3, 3), z(2, 64, dtype=torch.int32)
+    calls = [lambda: oal.oal_expand_coeffs(L, g, 0.1, stream=side),
+             lambda: oal.oal_prefill(Q, K, K, L, g, 0.1, L, L, L, stream=side),
+             lambda: oal.oal_prefill_backward(Q, K, K, Q, L, g, 0.1, stream=side),
+             lambda: oal.oal_decode_step(Q[:, :, 0], K[:, :, 0], K[:, :, 0], L, L, L, K, stream=side),
+             lambda: oal.oal_contribution_scores(Q, K, stream=side)]
+    for call, made in zip(calls, (3, 3, 5, 2, 2)):
+        side.calls.clear()
+        call()
+        assert side.calls[0] == ("wait", now) and len(side.calls) == 1 + made
+    assert now.calls == []
