@@ -8,6 +8,7 @@
 #include <algorithm>
 
 #include "gated.cuh"
+#include "paged.cuh"
 
 namespace oal {
 oal_status launch_expand_coeffs(const float *L, const int32_t *group, int Hq, int G,
@@ -56,6 +57,11 @@ oal_status launch_gated_decode(const void *q, const void *k, const void *v, int 
                                cudaStream_t stream);
 oal_status launch_state_remap(void *pool, size_t slot_bytes, int n, const int32_t *map,
                               cudaStream_t stream);
+
+oal_status launch_rope(const RopeArgs &p, int is_bf16, int form, const char *name,
+                       cudaStream_t stream);
+size_t paged_workspace_bytes(PagedArgs p, int is_bf16);
+oal_status launch_paged(PagedArgs p, int is_bf16, void *ws, cudaStream_t stream);
 
 // Device control block (one per device the library runs on): the status
 // word kernels record errors in; then, for tests of the failure path, the
@@ -613,6 +619,194 @@ oal_status oal_state_remap(void *pool, size_t slot_bytes, int n_slots, const int
   return oal::launch_state_remap(pool, slot_bytes, n_slots, map, stream);
 }
 
+// ---- rotary positions, the paged cache, attention over it
+
+oal_status oal_rope_plan(const double *freq, const int32_t *axes, int64_t *plan) {
+  t_msg[0] = 0;
+  if (!freq || !plan) return oal_fail(OAL_ERR_INVALID_ARG, "freq or plan is null");
+  for (int r = 0; r < oal::kD / 2; ++r) {
+    if (!isfinite(freq[r])) return oal_fail(OAL_ERR_INVALID_ARG, "freq[%d]=%g", r, freq[r]);
+    if (axes && axes[r] < 0) return oal_fail(OAL_ERR_INVALID_ARG, "axes[%d]=%d", r, axes[r]);
+    // freq / 2 pi as a sum of two doubles, without its whole turns, in units of 2^-64
+    const double inv = 0x1.45f306dc9c883p-3, rest = -0x1.6b01ec5417056p-57;   // 1 / (2 pi)
+    const double f = fabs(freq[r]), hi = f * inv, lo = fma(f, inv, -hi) + f * rest;
+    const uint64_t turns = (uint64_t)((hi - floor(hi)) * 0x1p64) +
+                           (uint64_t)(int64_t)llrint((lo - floor(lo + 0.5)) * 0x1p63) * 2;
+    plan[r] = (int64_t)(freq[r] < 0.0 ? 0 - turns : turns);
+    plan[oal::kD / 2 + r] = axes ? axes[r] : 0;
+  }
+  return OAL_OK;
+}
+
+// Sizes, positions and lengths of a call that turns rows; strides of its tensors.
+static oal_status rope_args(oal::RopeArgs &p, oal_dtype dtype, const void *const *x, int tensors,
+                            const int64_t *strides, int B, int Hq, int Hkv, int T, int d,
+                            const int64_t *plan, oal_rope_form form, const int32_t *positions,
+                            int n_axes, const int32_t *past, const int32_t *lengths) {
+  static const char *const names[3] = {"Q", "K", "V"};
+  if (B < 0 || T < 0 || (x[0] && Hq <= 0) || (x[1] && Hkv <= 0))
+    return oal_fail(OAL_ERR_INVALID_ARG, "bad sizes B=%d Hq=%d Hkv=%d T=%d", B, Hq, Hkv, T);
+  if (dtype != OAL_F32 && dtype != OAL_BF16)
+    return oal_fail(OAL_ERR_INVALID_ARG, "bad dtype %d", (int)dtype);
+  if (form != OAL_ROPE_HALVES && form != OAL_ROPE_PAIRS)
+    return oal_fail(OAL_ERR_INVALID_ARG, "bad form %d", (int)form);
+  if (d != oal::kD) return oal_fail(OAL_ERR_UNSUPPORTED, "only d = 64 is supported (d=%d)", d);
+  if ((long long)B * T > 1LL << 34 || (long long)Hq + 2LL * Hkv > 1 << 16)
+    return oal_fail(OAL_ERR_UNSUPPORTED, "problem too large");
+  if (positions && n_axes < 1) return oal_fail(OAL_ERR_INVALID_ARG, "n_axes=%d", n_axes);
+  const int heads[3] = {Hq, Hkv, Hkv};
+  oal::RowStrides *to[3] = {&p.q, &p.k, &p.v};
+  const int unit = dtype == OAL_BF16 ? 8 : 4;
+  for (int i = 0; i < tensors; ++i) {
+    *to[i] = {(long long)heads[i] * T * 64, (long long)T * 64, 64};
+    if (!x[i] || !strides) continue;
+    *to[i] = {strides[3 * i], strides[3 * i + 1], strides[3 * i + 2]};
+    for (int e = 0; e < 3; ++e)
+      if (strides[3 * i + e] % unit != 0 || strides[3 * i + e] < 0)
+        return oal_fail(OAL_ERR_INVALID_ARG, "stride %lld of %s is negative or no multiple of 16 bytes",
+                        (long long)strides[3 * i + e], names[i]);
+  }
+  p.Q = x[0], p.K = x[1], p.V = tensors > 2 ? x[2] : nullptr;
+  p.B = B, p.Hq = x[0] ? Hq : 0, p.Hkv = x[1] ? Hkv : 0, p.T = T;
+  p.turns = reinterpret_cast<const unsigned long long *>(plan);
+  p.axes = plan ? reinterpret_cast<const long long *>(plan) + oal::kD / 2 : nullptr;
+  p.positions = positions, p.n_axes = n_axes, p.past = past, p.lengths = lengths;
+  return OAL_OK;
+}
+
+oal_status oal_rope(const void *Q, const void *K, oal_dtype dtype, const int64_t *strides, int B,
+                    int Hq, int Hkv, int T, int d, const int64_t *plan, oal_rope_form form,
+                    const int32_t *positions, int n_axes, const int32_t *past,
+                    const int32_t *lengths, int inverse, void *Yq, void *Yk, cudaStream_t stream) {
+  t_msg[0] = 0;
+  oal::RopeArgs p = {};
+  const void *const x[2] = {Q, K};
+  OAL_TRY(rope_args(p, dtype, x, 2, strides, B, Hq, Hkv, T, d, plan, form, positions, n_axes, past, lengths));
+  t_call_launches = 0;
+  if (B == 0 || T == 0) return OAL_OK;
+  OAL_TRY(check_ptr(Q, "Q"));
+  OAL_TRY(check_ptr(Yq, "Yq"));
+  if (K) OAL_TRY(check_ptr(K, "K"));
+  if (K) OAL_TRY(check_ptr(Yk, "Yk"));
+  OAL_TRY(check_ptr(plan, "plan"));
+  if (positions) OAL_TRY(check_ptr(positions, "positions"));
+  if (past) OAL_TRY(check_ptr(past, "past"));
+  if (lengths) OAL_TRY(check_ptr(lengths, "lengths"));
+  p.Yq = Yq, p.Yk = Yk, p.inverse = inverse != 0;
+  p.status = oal_device_status_word();
+  if (!p.status) return oal_fail(OAL_ERR_CUDA, "no device status word");
+  oal_begin_call(stream);
+  return oal::launch_rope(p, dtype == OAL_BF16, form, "rope_kernel", stream);
+}
+
+static oal_status check_pages(int Hkv, int n_pages, int page_size, int64_t page_stride,
+                              int max_pages, int *shift) {
+  if (n_pages < 0 || max_pages < 0)
+    return oal_fail(OAL_ERR_INVALID_ARG, "n_pages=%d max_pages=%d", n_pages, max_pages);
+  if (page_size < 1 || (page_size & (page_size - 1)) != 0)
+    return oal_fail(OAL_ERR_INVALID_ARG, "page_size=%d is not a power of two", page_size);
+  if (page_size < 16 || page_size > 65536 || (long long)page_size * max_pages > 1LL << 30)
+    return oal_fail(OAL_ERR_UNSUPPORTED, "page_size=%d, max_pages=%d", page_size, max_pages);
+  if (page_stride < (int64_t)Hkv * page_size * oal::kD || page_stride % 8 != 0)
+    return oal_fail(OAL_ERR_INVALID_ARG, "page_stride=%lld", (long long)page_stride);
+  *shift = 0;
+  while (1 << *shift < page_size) ++*shift;
+  return OAL_OK;
+}
+
+oal_status oal_page_append(const void *Q, const void *K, const void *V, oal_dtype dtype,
+                           const int64_t *strides, int B, int Hq, int Hkv, int T, int d, int dv,
+                           const int64_t *plan, oal_rope_form form, const int32_t *positions,
+                           int n_axes, const int32_t *past, const int32_t *lengths, void *Kp,
+                           void *Vp, int n_pages, int page_size, int64_t page_stride,
+                           const int32_t *table, int max_pages, void *Yq, cudaStream_t stream) {
+  t_msg[0] = 0;
+  oal::RopeArgs p = {};
+  const void *const x[3] = {Q, K, V};
+  if (dv != oal::kDv) return oal_fail(OAL_ERR_UNSUPPORTED, "only dv = 64 is supported (dv=%d)", dv);
+  if (Hkv <= 0) return oal_fail(OAL_ERR_INVALID_ARG, "Hkv=%d", Hkv);
+  OAL_TRY(rope_args(p, dtype, x, 3, strides, B, Hq, Hkv, T, d, plan, form, positions, n_axes, past, lengths));
+  OAL_TRY(check_pages(Hkv, n_pages, page_size, page_stride, max_pages, &p.page_shift));
+  if (!plan && Q) return oal_fail(OAL_ERR_INVALID_ARG, "Q without a plan");
+  t_call_launches = 0;
+  if (B == 0 || T == 0) return OAL_OK;
+  if (Q) OAL_TRY(check_ptr(Q, "Q"));
+  if (Q) OAL_TRY(check_ptr(Yq, "Yq"));
+  OAL_TRY(check_ptr(K, "K"));
+  OAL_TRY(check_ptr(V, "V"));
+  if (plan) OAL_TRY(check_ptr(plan, "plan"));
+  if (positions) OAL_TRY(check_ptr(positions, "positions"));
+  OAL_TRY(check_ptr(past, "past"));
+  if (lengths) OAL_TRY(check_ptr(lengths, "lengths"));
+  OAL_TRY(check_ptr(Kp, "Kp"));
+  OAL_TRY(check_ptr(Vp, "Vp"));
+  OAL_TRY(check_ptr(table, "table"));
+  p.Yq = Yq, p.Kp = Kp, p.Vp = Vp;
+  p.n_pages = n_pages, p.max_pages = max_pages, p.page_stride = page_stride, p.table = table;
+  p.status = oal_device_status_word();
+  if (!p.status) return oal_fail(OAL_ERR_CUDA, "no device status word");
+  oal_begin_call(stream);
+  return oal::launch_rope(p, dtype == OAL_BF16, form, "page_append_kernel", stream);
+}
+
+static oal_status check_paged(oal::PagedArgs &p, int B, int Hq, int Hkv, int T, int d, int dv,
+                              oal_dtype dtype, int n_pages, int page_size, int64_t page_stride,
+                              int max_pages) {
+  OAL_TRY(check_common(B, Hq, Hkv, d, dv, dtype, OAL_STATE_FULL));
+  if (T < 0) return oal_fail(OAL_ERR_INVALID_ARG, "T=%d", T);
+  OAL_TRY(check_pages(Hkv, n_pages, page_size, page_stride, max_pages, &p.page_shift));
+  const int rho = Hq / Hkv;
+  if (rho > 128 || (long long)B * Hkv > 65535 || (long long)T * rho > 1LL << 28)
+    return oal_fail(OAL_ERR_UNSUPPORTED, "problem too large");
+  p.B = B, p.Hq = Hq, p.Hkv = Hkv, p.T = T, p.rho = rho;
+  p.n_pages = n_pages, p.max_pages = max_pages, p.page_stride = page_stride;
+  return OAL_OK;
+}
+
+size_t oal_paged_attention_workspace_bytes(int B, int Hq, int Hkv, int T, int d, int dv,
+                                           oal_dtype dtype, int page_size, int max_pages) {
+  oal::PagedArgs p = {};
+  const int64_t stride = (int64_t)Hkv * page_size * d;
+  if (check_paged(p, B, Hq, Hkv, T, d, dv, dtype, 0, page_size, stride, max_pages) != OAL_OK) return 0;
+  if (B == 0 || T == 0) return 256;
+  return oal::paged_workspace_bytes(p, dtype == OAL_BF16);
+}
+
+oal_status oal_paged_attention(const void *Q, oal_dtype dtype, int B, int Hq, int Hkv, int T,
+                               int d, int dv, const void *Kp, const void *Vp, int n_pages,
+                               int page_size, int64_t page_stride, const int32_t *table,
+                               int max_pages, const int32_t *past, const int32_t *lengths,
+                               float scale, float cap, int window, const float *slopes,
+                               const int32_t *prefix, const int32_t *first, void *Y,
+                               void *workspace, size_t workspace_bytes, cudaStream_t stream) {
+  t_msg[0] = 0;
+  oal::PagedArgs p = {};
+  OAL_TRY(check_paged(p, B, Hq, Hkv, T, d, dv, dtype, n_pages, page_size, page_stride, max_pages));
+  if (!(scale > 0.f) || !isfinite(scale)) return oal_fail(OAL_ERR_INVALID_ARG, "scale=%g", scale);
+  if (!(cap >= 0.f) || !isfinite(cap)) return oal_fail(OAL_ERR_INVALID_ARG, "cap=%g", cap);
+  if (window < 0) return oal_fail(OAL_ERR_INVALID_ARG, "window=%d", window);
+  t_call_launches = 0;
+  if (B == 0 || T == 0) return OAL_OK;
+  OAL_TRY(check_ptr(Q, "Q"));
+  OAL_TRY(check_ptr(Kp, "Kp"));
+  OAL_TRY(check_ptr(Vp, "Vp"));
+  OAL_TRY(check_ptr(table, "table"));
+  OAL_TRY(check_ptr(past, "past"));
+  OAL_TRY(check_ptr(Y, "Y"));
+  if (lengths) OAL_TRY(check_ptr(lengths, "lengths"));
+  if (slopes) OAL_TRY(check_ptr(slopes, "slopes"));
+  if (prefix) OAL_TRY(check_ptr(prefix, "prefix"));
+  if (first) OAL_TRY(check_ptr(first, "first"));
+  OAL_TRY(check_workspace(workspace, workspace_bytes, oal::paged_workspace_bytes(p, dtype == OAL_BF16)));
+  p.Q = Q, p.Kp = Kp, p.Vp = Vp, p.Y = Y, p.table = table, p.past = past, p.lengths = lengths;
+  p.scale = scale, p.cap = cap, p.window = window;
+  p.slopes = slopes, p.prefix = prefix, p.first = first;
+  p.status = oal_device_status_word();
+  if (!p.status) return oal_fail(OAL_ERR_CUDA, "no device status word");
+  oal_begin_call(stream);
+  return oal::launch_paged(p, dtype == OAL_BF16, workspace, stream);
+}
+
 oal_status oal_debug_wait_test(uint64_t wait_limit_cycles, int starve) {
   t_msg[0] = 0;
   if (starve < 0 || starve > 3) return oal_fail(OAL_ERR_INVALID_ARG, "starve=%d", starve);
@@ -651,8 +845,9 @@ oal_status oal_sync_status(cudaStream_t stream) {
     const int zero = 0;
     cudaMemcpy(w, &zero, sizeof zero, cudaMemcpyHostToDevice);
     const char *what = v == OAL_ERR_INVALID_ARG ? "a group id outside 1..G, a "
-                                                  "sequence length outside 0..T or a "
-                                                  "slot out of range or taken twice"
+                                                  "sequence length outside 0..T, a "
+                                                  "slot out of range or taken twice, or a "
+                                                  "page or an axis out of range"
                        : v == OAL_ERR_TIMEOUT   ? "a device-side wait timed out"
                                                 : "device error";
     return oal_fail((oal_status)v, "device status %d: %s", v, what);

@@ -1,0 +1,151 @@
+// paged.cuh -- rotary positions, the paged cache and the attention over it:
+// arguments and what the kernels share.
+#pragma once
+#include "oal_internal.cuh"
+
+namespace oal {
+
+// ---------------------------------------------------------------- rotation, append
+
+// Element (b, h, t, 0) of a tensor whose rows of 64 are contiguous.
+struct RowStrides {
+  long long b, h, t;
+};
+
+struct RopeArgs {
+  const void *Q, *K, *V;                  // K, V may be null
+  void *Yq, *Yk;                          // contiguous; Yk null where K goes to pages
+  void *Kp, *Vp;                          // pages, or null
+  RowStrides q, k, v;
+  int B, Hq, Hkv, T;
+  const unsigned long long *turns;        // [32] angle a position, in turns of 2^64; null: nothing turns
+  const long long *axes;                  // [32] axis of each pair
+  const int32_t *positions;               // [n_axes][B][T], or null: past + t
+  int n_axes;
+  const int32_t *past, *lengths;          // [B] or null
+  const int32_t *table;
+  int n_pages, page_shift, max_pages;
+  long long page_stride;
+  int inverse;
+  int *status;
+};
+
+// ---------------------------------------------------------------- attention
+
+struct PagedArgs {
+  const void *Q, *Kp, *Vp;
+  void *Y;
+  const int32_t *table, *past, *lengths, *prefix, *first;   // lengths, prefix, first may be null
+  const float *slopes;                    // [Hq] or null
+  int B, Hq, Hkv, T, rho;
+  int n_pages, page_shift, max_pages;
+  long long page_stride;                  // elements from page to page
+  float scale, cap;                       // cap: 0 = none
+  int window;                             // 0 = none
+  int *status;
+  // The split of the keys: an item's tile of `tile_rows` rows (row t * rho + h'
+  // of the KV head's queries) over keys base + [s, s + 1) * split_keys.
+  int tile_rows, splits, split_keys;
+  float *part_o;                          // [B * Hkv][splits][T * rho][64], not yet divided
+  float2 *part_ml;                        // the same rows' maximum (base 2) and sum
+};
+
+// A sequence's place in its pages.
+struct PagedSeq {
+  int n, past, total;                     // new tokens, tokens before them, keys
+};
+__device__ __forceinline__ PagedSeq paged_seq(const PagedArgs &p, int b, bool record) {
+  PagedSeq s;
+  const int n = p.lengths ? p.lengths[b] : p.T, past = p.past[b];
+  const int room = p.max_pages << p.page_shift;
+  s.n = min(max(n, 0), p.T);
+  s.past = min(max(past, 0), room);
+  s.total = min(s.past + s.n, room);
+  if (record && (n != s.n || past != s.past || s.past + s.n > room))
+    atomicCAS(p.status, kStatusOk, (int)OAL_ERR_INVALID_ARG);
+  return s;
+}
+
+// The keys that token t may see: every mask leaves an interval [lo, hi).
+__device__ __forceinline__ int2 paged_sees(const PagedArgs &p, const PagedSeq &s, int b, int t) {
+  const int i = s.past + t;
+  int lo = p.window ? max(0, i + 1 - p.window) : 0, hi = i + 1;
+  if (p.first) lo = max(lo, p.first[(size_t)b * p.T + t]);
+  if (p.prefix) hi = max(hi, p.prefix[b]);
+  hi = min(hi, s.total);
+  if (lo >= hi) lo = hi = 0;
+  return make_int2(lo, hi);
+}
+
+// First key of the splits of the tile that starts at token t: at or before
+// every key that the tile's rows see, and known without looking at the rows.
+constexpr int kSplitAlign = 128;
+__device__ __forceinline__ int paged_base(const PagedArgs &p, const PagedSeq &s, int t) {
+  return p.window ? max(0, s.past + t + 1 - p.window) & ~(kSplitAlign - 1) : 0;
+}
+
+// The page that holds key j, or -1 (a bad entry, which is recorded; its keys
+// count as zeros).
+__device__ __forceinline__ int paged_page(const PagedArgs &p, int b, int j) {
+  const int page = p.table[(size_t)b * p.max_pages + (j >> p.page_shift)];
+  if (page >= 0 && page < p.n_pages) return page;
+  atomicCAS(p.status, kStatusOk, (int)OAL_ERR_INVALID_ARG);
+  return -1;
+}
+__device__ __forceinline__ size_t paged_row(const PagedArgs &p, int page, int kv, int j) {
+  return (size_t)page * p.page_stride +
+         (((size_t)kv << p.page_shift) + (j & ((1 << p.page_shift) - 1))) * 64;
+}
+
+// The score in units of the exponent's base 2: cap, then distance.
+constexpr float kLog2e = 1.4426950408889634f;
+__device__ __forceinline__ float paged_score(const PagedArgs &p, float qk, float slope, int distance) {
+  float s = qk * p.scale;
+  if (p.cap > 0.f) s = p.cap * tanhf(s / p.cap);
+  s -= slope * (float)distance;
+  return s;
+}
+
+// One row from the start, by a warp: lane l holds elements 2 l and 2 l + 1 of
+// the result.  Keys that the row does not see are not read, so whatever they
+// hold has no part in it: for rows whose result is not finite, which a masked
+// key's infinity or NaN (times a weight of 0) may be to blame for.
+template <typename T>
+static __device__ __noinline__ float2 paged_row_again(const PagedArgs &p, int b, int h, int t, int lo, int hi) {
+  const int lane = threadIdx.x & 31, kv = h / p.rho;
+  const T *q = static_cast<const T *>(p.Q) + (((size_t)b * p.Hq + h) * p.T + t) * 64 + 2 * lane;
+  const float q0 = to_f32(q[0]), q1 = to_f32(q[1]);
+  const float slope = p.slopes ? p.slopes[h] : 0.f;
+  const int i = p.past[b] + t;
+  float m = -INFINITY, l = 0.f, o0 = 0.f, o1 = 0.f;
+  for (int j = lo; j < hi; ++j) {
+    const int page = paged_page(p, b, j);
+    float k0 = 0.f, k1 = 0.f, v0 = 0.f, v1 = 0.f;
+    if (page >= 0) {
+      const size_t at = paged_row(p, page, kv, j) + 2 * lane;
+      const T *k = static_cast<const T *>(p.Kp) + at, *v = static_cast<const T *>(p.Vp) + at;
+      k0 = to_f32(k[0]), k1 = to_f32(k[1]), v0 = to_f32(v[0]), v1 = to_f32(v[1]);
+    }
+    float s = fmaf(q0, k0, q1 * k1);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+    s = paged_score(p, s, slope, abs(i - j));
+    const float top = s > m || s != s ? s : m;        // (a NaN stays)
+    const float keep = m == top ? 1.f : expf(m - top), w = s == -INFINITY ? 0.f : expf(s - top);
+    m = top;
+    l = l * keep + w, o0 = o0 * keep + w * v0, o1 = o1 * keep + w * v1;
+  }
+  return make_float2(o0 / l, o1 / l);
+}
+
+// Rows of 64 for Y.
+template <typename T>
+__device__ __forceinline__ T *paged_y(const PagedArgs &p, int b, int h, int t) {
+  return static_cast<T *>(p.Y) + (((size_t)b * p.Hq + h) * p.T + t) * 64;
+}
+
+// A kernel's dynamic shared memory, once a device.
+oal_status paged_need_smem(const void *kernel, size_t bytes, bool (&done)[kMaxDevices]);
+oal_status launch_paged_join(const PagedArgs &p, int is_bf16, cudaStream_t stream);
+
+}  // namespace oal

@@ -1,0 +1,205 @@
+// paged_simt.cu -- attention over a paged cache on the CUDA cores, for fp32.
+//
+//     y = sum_j e^{s_j - m} v_j / sum_j e^{s_j - m},   m = max_j s_j
+// in one pass over the keys: maximum, sum and result of the keys so far are
+// multiplied by e^{m_old - m_new} when the maximum grows.
+//
+// A block takes kRows rows (queries of one KV head, row t * rho + h') and walks
+// 64 keys at a time through shared memory; a thread holds kRows / 8 rows of 4
+// keys (scores) or 4 columns (results).  fp32 products: bound by the FMA pipes
+// and shared memory together (8 16-byte loads for 64 FMAs).
+#include <algorithm>
+
+#include "paged.cuh"
+
+namespace oal {
+namespace {
+
+constexpr int kThreads = 128;
+constexpr int kKeys = 64;
+constexpr int kPitch = 68;                // floats of a row in shared memory: 4 banks on
+
+template <int kRows>
+struct SimtSmem {
+  float q[kRows][kPitch], p[kRows][kPitch];
+  float k[kKeys][kPitch], v[kKeys][kPitch];
+};
+
+__device__ __forceinline__ float4 row4(const float *row, int c) { return *reinterpret_cast<const float4 *>(row + c); }
+__device__ __forceinline__ float dot4(float4 a, float4 b, float s) {
+  return fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, fmaf(a.w, b.w, s))));
+}
+
+template <int kRows>
+__global__ void __launch_bounds__(kThreads)
+paged_simt_kernel(PagedArgs p) {
+  pdl_trigger();
+  pdl_wait();
+  constexpr int R = kRows / 8;            // rows of a thread
+  extern __shared__ uint8_t smem_raw[];
+  SimtSmem<kRows> &s = *reinterpret_cast<SimtSmem<kRows> *>(smem_raw);
+  __shared__ int s_lo, s_hi;
+  const int bh = blockIdx.y, b = bh / p.Hkv, kv = bh % p.Hkv, split = blockIdx.z;
+  const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
+  const int r0 = blockIdx.x * kRows;
+  const PagedSeq seq = paged_seq(p, b, tid == 0);
+  const int t_first = r0 / p.rho;
+  if (t_first >= seq.n) return;
+  if (tid == 0) s_lo = INT32_MAX, s_hi = 0;
+  __syncthreads();
+  int lo[R], hi[R], at[R];                // keys seen, position
+  float slope[R];
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    const int r = r0 + ty * R + i, t = r / p.rho, h = r % p.rho;
+    const bool live = t < seq.n;
+    const int2 sees = live ? paged_sees(p, seq, b, t) : make_int2(0, 0);
+    lo[i] = sees.x, hi[i] = sees.y, at[i] = seq.past + t;
+    slope[i] = live && p.slopes ? p.slopes[kv * p.rho + h] : 0.f;
+    if (tx == 0 && hi[i] > 0) atomicMin(&s_lo, lo[i]), atomicMax(&s_hi, hi[i]);
+  }
+  for (int x = tid; x < kRows * 16; x += kThreads) {
+    const int r = r0 + (x >> 4), t = r / p.rho, h = r % p.rho;
+    float4 q = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (t < seq.n)
+      q = *reinterpret_cast<const float4 *>(static_cast<const float *>(p.Q) +
+                                            (((size_t)b * p.Hq + kv * p.rho + h) * p.T + t) * 64 + 4 * (x & 15));
+    *reinterpret_cast<float4 *>(&s.q[x >> 4][4 * (x & 15)]) = q;
+  }
+  __syncthreads();
+  int k0 = s_lo, k1 = s_hi;
+  if (p.splits > 1) {
+    const int from = paged_base(p, seq, t_first) + split * p.split_keys;
+    k0 = max(k0, from), k1 = min(k1, from + p.split_keys);
+    if (k0 >= k1) return;                 // (no row's interval reaches in: nothing is joined)
+  }
+
+  float m[R], l[R];
+  float4 o[R];
+#pragma unroll
+  for (int i = 0; i < R; ++i) m[i] = -INFINITY, l[i] = 0.f, o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int j0 = k0 & ~(kKeys - 1); j0 < k1; j0 += kKeys) {
+    __syncthreads();
+    for (int x = tid; x < kKeys * 16; x += kThreads) {
+      const int j = j0 + (x >> 4), c = 4 * (x & 15);
+      float4 k = make_float4(0.f, 0.f, 0.f, 0.f), v = k;
+      if (j >= k0 && j < k1) {
+        const int page = paged_page(p, b, j);
+        if (page >= 0) {
+          const size_t from = paged_row(p, page, kv, j) + c;
+          k = *reinterpret_cast<const float4 *>(static_cast<const float *>(p.Kp) + from);
+          v = *reinterpret_cast<const float4 *>(static_cast<const float *>(p.Vp) + from);
+        }
+      }
+      *reinterpret_cast<float4 *>(&s.k[x >> 4][c]) = k;
+      *reinterpret_cast<float4 *>(&s.v[x >> 4][c]) = v;
+    }
+    __syncthreads();
+    float x[R][4];
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[i][e] = 0.f;
+#pragma unroll 4
+    for (int d = 0; d < 64; d += 4) {
+      float4 k[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) k[e] = row4(s.k[tx + 16 * e], d);
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        const float4 q = row4(s.q[ty * R + i], d);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[i][e] = dot4(q, k[e], x[i][e]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      float top = m[i];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int j = j0 + tx + 16 * e;
+        const bool seen = j >= max(lo[i], k0) && j < min(hi[i], k1);
+        x[i][e] = seen ? paged_score(p, x[i][e], slope[i], abs(at[i] - j)) : -INFINITY;
+        top = fmaxf(top, x[i][e]);
+      }
+#pragma unroll
+      for (int d = 1; d < 16; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+      const float base = top == -INFINITY ? 0.f : top;
+      const float keep = expf(m[i] - base);
+      float sum = 0.f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float w = expf(x[i][e] - base);
+        s.p[ty * R + i][tx + 16 * e] = w;
+        sum += w;
+      }
+      m[i] = top;
+      l[i] = l[i] * keep + sum;
+      o[i].x *= keep, o[i].y *= keep, o[i].z *= keep, o[i].w *= keep;
+    }
+    __syncwarp();                         // (a row's weights come from its own half warp)
+#pragma unroll 4
+    for (int j = 0; j < kKeys; j += 4) {
+      float4 v[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = row4(s.v[j + e], 4 * tx);
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        const float4 w = row4(s.p[ty * R + i], j);
+        o[i].x = fmaf(w.x, v[0].x, fmaf(w.y, v[1].x, fmaf(w.z, v[2].x, fmaf(w.w, v[3].x, o[i].x))));
+        o[i].y = fmaf(w.x, v[0].y, fmaf(w.y, v[1].y, fmaf(w.z, v[2].y, fmaf(w.w, v[3].y, o[i].y))));
+        o[i].z = fmaf(w.x, v[0].z, fmaf(w.y, v[1].z, fmaf(w.z, v[2].z, fmaf(w.w, v[3].z, o[i].z))));
+        o[i].w = fmaf(w.x, v[0].w, fmaf(w.y, v[1].w, fmaf(w.z, v[2].w, fmaf(w.w, v[3].w, o[i].w))));
+      }
+    }
+  }
+
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+#pragma unroll
+    for (int d = 1; d < 16; d <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], d);
+    const int r = r0 + ty * R + i, t = r / p.rho, h = kv * p.rho + r % p.rho;
+    const bool live = t < seq.n;
+    if (p.splits > 1) {
+      if (!live) continue;
+      const size_t row = ((size_t)bh * p.splits + split) * ((size_t)p.T * p.rho) + r;
+      *reinterpret_cast<float4 *>(p.part_o + row * 64 + 4 * tx) = o[i];
+      if (tx == 0) p.part_ml[row] = make_float2(m[i] * kLog2e, l[i]);
+      continue;
+    }
+    const float inv = hi[i] > 0 ? 1.f / l[i] : 0.f;
+    const float4 y = make_float4(o[i].x * inv, o[i].y * inv, o[i].z * inv, o[i].w * inv);
+    const bool wrong = live && !(fabsf(y.x) + fabsf(y.y) + fabsf(y.z) + fabsf(y.w) < INFINITY);
+    const uint32_t again = __ballot_sync(0xffffffffu, wrong);
+    if (live) *reinterpret_cast<float4 *>(paged_y<float>(p, b, h, t) + 4 * tx) = y;
+    for (int half = 0; half < 2; ++half)
+      if (again >> (16 * half) & 0xFFFFu) {
+        const int who = 16 * half;
+        const int h2 = __shfl_sync(0xffffffffu, h, who), t2 = __shfl_sync(0xffffffffu, t, who);
+        const int a = __shfl_sync(0xffffffffu, lo[i], who), z = __shfl_sync(0xffffffffu, hi[i], who);
+        const float2 f = paged_row_again<float>(p, b, h2, t2, a, z);
+        __syncwarp();
+        *reinterpret_cast<float2 *>(paged_y<float>(p, b, h2, t2) + 2 * (tid & 31)) = f;
+      }
+  }
+}
+
+template <int kRows>
+oal_status run(const PagedArgs &p, cudaStream_t stream) {
+  static bool done[kMaxDevices];
+  const oal_status ready =
+      paged_need_smem(reinterpret_cast<const void *>(paged_simt_kernel<kRows>), sizeof(SimtSmem<kRows>), done);
+  if (ready != OAL_OK) return ready;
+  const dim3 grid((unsigned)(((long long)p.T * p.rho + kRows - 1) / kRows), (unsigned)(p.B * p.Hkv), (unsigned)p.splits);
+  launch_pdl(paged_simt_kernel<kRows>, grid, dim3(kThreads), sizeof(SimtSmem<kRows>), stream, p);
+  const oal_status st = oal_after_launch("paged_simt_kernel", stream);
+  return st != OAL_OK || p.splits == 1 ? st : launch_paged_join(p, 0, stream);
+}
+
+}  // namespace
+
+oal_status launch_paged_simt(const PagedArgs &p, cudaStream_t stream) {
+  return p.tile_rows == 8 ? run<8>(p, stream) : run<32>(p, stream);
+}
+
+}  // namespace oal

@@ -1,0 +1,203 @@
+// rope.cu -- rotary positions, and appending to a paged cache with the rotation
+// on the way.
+//
+// Pair r of a row at position p turns by the angle p f_r.  Angles are held in
+// turns as 64-bit fractions: p times round(2^64 f_r / 2 pi), modulo 2^64, is the
+// angle modulo a turn to 2^-33 of a turn whatever the position (32 bits), in two
+// integer products where a float loses a bit for every doubling of p.  The
+// nearest quarter turn is taken out exactly and the rest (at most an eighth)
+// goes through sincospif.
+//
+// A block takes 16 tokens: their angles once, into shared memory, for all of its
+// heads; then every row is read once and written once: HBM-bound.  A thread moves
+// two 16-byte pieces whose elements pair up.  Few tokens: the heads are spread
+// over blocks instead, and the angles are formed again in each.
+#include <algorithm>
+
+#include "paged.cuh"
+
+namespace oal {
+namespace {
+
+constexpr int kRopeThreads = 256;
+constexpr int kRopeTokens = 16;
+
+struct alignas(16) Piece {
+  uint4 w;
+};
+template <typename T>
+constexpr int kPiece = 16 / (int)sizeof(T);
+
+__device__ __forceinline__ void piece_get(const Piece &x, float (&f)[8]) {
+  const uint32_t w[4] = {x.w.x, x.w.y, x.w.z, x.w.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) f[2 * e] = __uint_as_float(w[e] << 16), f[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
+}
+__device__ __forceinline__ void piece_get(const Piece &x, float (&f)[4]) {
+  f[0] = __uint_as_float(x.w.x), f[1] = __uint_as_float(x.w.y), f[2] = __uint_as_float(x.w.z), f[3] = __uint_as_float(x.w.w);
+}
+__device__ __forceinline__ Piece piece_put(const float (&f)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[e]) : "f"(f[2 * e + 1]), "f"(f[2 * e]));
+  return Piece{make_uint4(w[0], w[1], w[2], w[3])};
+}
+__device__ __forceinline__ Piece piece_put(const float (&f)[4]) {
+  return Piece{make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]))};
+}
+
+struct RopeToken {
+  long long q, k, v;                      // elements to the token's rows, without the head
+  long long yq, yk, page;                 // page: -1 = nowhere
+  int live;
+};
+
+template <typename T, bool kHalves>
+__global__ void __launch_bounds__(kRopeThreads)
+rope_kernel(RopeArgs p, int heads_a_block) {
+  pdl_trigger();
+  pdl_wait();
+  constexpr int E = kPiece<T>, kUnits = 32 / E;       // pairs of a unit, units of a row
+  __shared__ float2 s_turn[kRopeTokens][33];
+  __shared__ RopeToken s_tok[kRopeTokens];
+  const int tid = threadIdx.x;
+  const long long n0 = (long long)blockIdx.x * kRopeTokens, all = (long long)p.B * p.T;
+  if (tid < kRopeTokens) {
+    RopeToken k = {};
+    k.page = -1;
+    const long long n = n0 + tid;
+    if (n < all) {
+      const int b = (int)(n / p.T), t = (int)(n % p.T);
+      int len = p.T;
+      if (p.lengths) {
+        len = p.lengths[b];
+        if (len < 0 || len > p.T) atomicCAS(p.status, kStatusOk, (int)OAL_ERR_INVALID_ARG);
+      }
+      k.live = t < len;
+      k.q = b * p.q.b + t * p.q.t, k.k = b * p.k.b + t * p.k.t, k.v = b * p.v.b + t * p.v.t;
+      k.yq = ((long long)b * p.Hq * p.T + t) * 64, k.yk = ((long long)b * p.Hkv * p.T + t) * 64;
+      if (p.Kp && k.live) {
+        const long long at = (long long)p.past[b] + t;
+        int page = -1;
+        if (at >= 0 && (at >> p.page_shift) < p.max_pages) page = p.table[(long long)b * p.max_pages + (at >> p.page_shift)];
+        if (page >= 0 && page < p.n_pages)
+          k.page = page * p.page_stride + (at & ((1 << p.page_shift) - 1)) * 64;
+        else
+          atomicCAS(p.status, kStatusOk, (int)OAL_ERR_INVALID_ARG);
+      }
+    }
+    s_tok[tid] = k;
+  }
+  if (p.turns) {
+#pragma unroll
+    for (int x = tid; x < kRopeTokens * 32; x += kRopeThreads) {
+      const int r = x & 31;
+      const long long n = n0 + (x >> 5);
+      if (n >= all) break;
+      long long at;
+      if (p.positions) {
+        const long long axis = p.axes[r];
+        const bool bad = axis < 0 || axis >= p.n_axes;
+        if (bad) atomicCAS(p.status, kStatusOk, (int)OAL_ERR_INVALID_ARG);
+        at = p.positions[(bad ? 0 : axis) * all + n];
+      } else {
+        at = n % p.T + (p.past ? p.past[n / p.T] : 0);
+      }
+      const unsigned long long turn = (unsigned long long)at * p.turns[r];
+      const unsigned long long quarter = turn + (1ull << 61);
+      float s, c;
+      sincospif((float)(long long)(turn - (quarter & (3ull << 62))) * 0x1p-63f, &s, &c);
+      const int k = (int)(quarter >> 62);
+      if (k & 1) { const float x2 = c; c = -s, s = x2; }
+      if (k & 2) c = -c, s = -s;
+      s_turn[x >> 5][r] = make_float2(c, p.inverse ? -s : s);
+    }
+  }
+  __syncthreads();
+
+  const int heads = p.Hq + (p.K ? p.Hkv : 0) + (p.V ? p.Hkv : 0);
+  const int h0 = blockIdx.y * heads_a_block, h1 = min(heads, h0 + heads_a_block);
+  constexpr int kRows = kRopeThreads / kUnits;        // rows in flight of a pass
+  const int unit = tid % kUnits, tok = tid / kUnits % kRopeTokens;
+  const RopeToken k = s_tok[tok];
+  if (!k.live) return;
+  const int a0 = kHalves ? unit * E : 2 * unit * E, a1 = a0 + (kHalves ? 32 : E);
+  float2 turn[E];
+  if (p.turns) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) turn[e] = s_turn[tok][unit * E + e];
+  }
+#pragma unroll 4
+  for (int h = h0 + tid / (kUnits * kRopeTokens); h < h1; h += kRows / kRopeTokens) {
+    const T *src;
+    T *dst;
+    bool turns = p.turns != nullptr;
+    if (h < p.Hq) {
+      src = static_cast<const T *>(p.Q) + k.q + h * p.q.h;
+      dst = static_cast<T *>(p.Yq) + k.yq + (long long)h * p.T * 64;
+    } else if (h < p.Hq + p.Hkv) {
+      const int kv = h - p.Hq;
+      src = static_cast<const T *>(p.K) + k.k + kv * p.k.h;
+      if (p.Kp) {
+        if (k.page < 0) continue;
+        dst = static_cast<T *>(p.Kp) + k.page + ((long long)kv << p.page_shift) * 64;
+      } else {
+        dst = static_cast<T *>(p.Yk) + k.yk + (long long)kv * p.T * 64;
+      }
+    } else {
+      const int kv = h - p.Hq - p.Hkv;
+      if (k.page < 0) continue;
+      src = static_cast<const T *>(p.V) + k.v + kv * p.v.h;
+      dst = static_cast<T *>(p.Vp) + k.page + ((long long)kv << p.page_shift) * 64;
+      turns = false;
+    }
+    Piece x0 = *reinterpret_cast<const Piece *>(src + a0), x1 = *reinterpret_cast<const Piece *>(src + a1);
+    if (turns) {
+      float a[E], b[E];
+      piece_get(x0, a), piece_get(x1, b);
+      if (kHalves) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const float u = a[e], w = b[e];
+          a[e] = fmaf(u, turn[e].x, -(w * turn[e].y)), b[e] = fmaf(w, turn[e].x, u * turn[e].y);
+        }
+      } else {   // pairs inside each piece
+#pragma unroll
+        for (int e = 0; e < E / 2; ++e) {
+          const float2 t0 = turn[e], t1 = turn[E / 2 + e];
+          float u = a[2 * e], w = a[2 * e + 1];
+          a[2 * e] = fmaf(u, t0.x, -(w * t0.y)), a[2 * e + 1] = fmaf(w, t0.x, u * t0.y);
+          u = b[2 * e], w = b[2 * e + 1];
+          b[2 * e] = fmaf(u, t1.x, -(w * t1.y)), b[2 * e + 1] = fmaf(w, t1.x, u * t1.y);
+        }
+      }
+      x0 = piece_put(a), x1 = piece_put(b);
+    }
+    *reinterpret_cast<Piece *>(dst + a0) = x0;
+    *reinterpret_cast<Piece *>(dst + a1) = x1;
+  }
+}
+
+template <typename T>
+oal_status run(const RopeArgs &p, int form, const char *name, cudaStream_t stream) {
+  const int heads = p.Hq + (p.K ? p.Hkv : 0) + (p.V ? p.Hkv : 0);
+  const long long tiles = ((long long)p.B * p.T + kRopeTokens - 1) / kRopeTokens;
+  constexpr int pass = kRopeThreads / (32 / kPiece<T>) / kRopeTokens;      // heads of a pass
+  const int per = (heads + pass - 1) / pass;
+  const int groups = (int)std::min<long long>(per, std::max<long long>(1, 608 / tiles));
+  const int each = (per + groups - 1) / groups * pass;
+  const dim3 grid((unsigned)tiles, (unsigned)((heads + each - 1) / each));
+  if (form == OAL_ROPE_HALVES)
+    launch_pdl(rope_kernel<T, true>, grid, dim3(kRopeThreads), 0, stream, p, each);
+  else
+    launch_pdl(rope_kernel<T, false>, grid, dim3(kRopeThreads), 0, stream, p, each);
+  return oal_after_launch(name, stream);
+}
+
+}  // namespace
+
+oal_status launch_rope(const RopeArgs &p, int is_bf16, int form, const char *name, cudaStream_t stream) {
+  return is_bf16 ? run<__nv_bfloat16>(p, form, name, stream) : run<float>(p, form, name, stream);
+}
+
+}  // namespace oal

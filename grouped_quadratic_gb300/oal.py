@@ -10,6 +10,8 @@ Tensor layouts (row-major, contiguous, CUDA):
   L [Hq,G+1,G+1] float32 (lower triangle), group [Hq,64] int32 in 1..G
   state [B,Hkv,F,65] float32 (F = 4161 FULL, 2145 PACKED)
   gated recurrence: g [B,Hkv,T] float32 (log decays), state [B,Hkv,64,64] float32
+  paged cache: Kp/Vp [n_pages,Hkv,page_size,64] (pages may lie apart), table [B,max_pages] int32
+  rotations: Q, K, V of oal_rope and oal_page_append may be views whose rows are contiguous
 
 A call given a `stream` waits there for the tensors that it makes itself (on the
 current stream); tensors given to it have to be ready on `stream`.
@@ -25,6 +27,7 @@ LIB_PATH = os.path.join(HERE, "liboal.so")
 OAL_OK, OAL_ERR_INVALID_ARG, OAL_ERR_UNSUPPORTED, OAL_ERR_CUDA, OAL_ERR_TIMEOUT = range(5)
 OAL_F32, OAL_BF16 = 0, 1
 OAL_STATE_FULL, OAL_STATE_PACKED = 0, 1
+OAL_ROPE_HALVES, OAL_ROPE_PAIRS = 0, 1
 _STATUS_NAMES = {0: "OAL_OK", 1: "OAL_ERR_INVALID_ARG", 2: "OAL_ERR_UNSUPPORTED",
                  3: "OAL_ERR_CUDA", 4: "OAL_ERR_TIMEOUT"}
 
@@ -93,6 +96,19 @@ def load_library(path: str = LIB_PATH):
     lib.oal_gated_decode_step.restype = ci
     lib.oal_state_remap.argtypes = [vp, sz, ci, vp, vp]
     lib.oal_state_remap.restype = ci
+    lib.oal_rope_plan.argtypes = [vp, vp, vp]
+    lib.oal_rope_plan.restype = ci
+    i64 = ctypes.c_int64
+    lib.oal_rope.argtypes = [vp, vp, ci, vp, ci, ci, ci, ci, ci, vp, ci, vp, ci, vp, vp, ci, vp, vp, vp]
+    lib.oal_rope.restype = ci
+    lib.oal_page_append.argtypes = [vp, vp, vp, ci, vp, ci, ci, ci, ci, ci, ci, vp, ci, vp, ci, vp, vp,
+                                    vp, vp, ci, ci, i64, vp, ci, vp, vp]
+    lib.oal_page_append.restype = ci
+    lib.oal_paged_attention_workspace_bytes.argtypes = [ci] * 9
+    lib.oal_paged_attention_workspace_bytes.restype = sz
+    lib.oal_paged_attention.argtypes = [vp, ci, ci, ci, ci, ci, ci, ci, vp, vp, ci, ci, i64, vp, ci, vp,
+                                        vp, cf, cf, ci, vp, vp, vp, vp, vp, sz, vp]
+    lib.oal_paged_attention.restype = ci
     cd = ctypes.c_double
     lib.oal_group_dims.argtypes = [vp, ci, ci, vp, ci, cd, cd, cd, ci, cd, vp, vp]
     lib.oal_group_dims.restype = ci
@@ -561,6 +577,194 @@ def oal_state_remap(pool, map, stream=None):
     _check(lib.oal_state_remap(pool.data_ptr(), pool.numel() // n * pool.element_size() if n else 0,
                                n, map.data_ptr(), _stream_on(dev, stream, ())))
     return pool
+
+
+def oal_rope_plan(freq, axes=None, device="cuda"):
+    """What the rotations need of their angles: freq [32] radians per position of
+    each pair (host, float64), axes [32] the axis of each pair's positions (None:
+    axis 0).  Returns an int64 tensor [2,32] on `device`, to be kept."""
+    import numpy as np
+    lib = load_library()
+    freq = np.ascontiguousarray(np.asarray(freq, dtype=np.float64))
+    _need(freq.shape == (32,), "freq must have 32 entries")
+    if axes is not None:
+        axes = np.ascontiguousarray(np.asarray(axes, dtype=np.int32))
+        _need(axes.shape == (32,), "axes must have 32 entries")
+    plan = np.empty((2, 32), np.int64)
+    _check(lib.oal_rope_plan(freq.ctypes.data, None if axes is None else axes.ctypes.data,
+                             plan.ctypes.data))
+    return torch.from_numpy(plan).to(device)
+
+
+def _rows(t, name, dtype, shape, dev):
+    """The strides of a tensor whose rows of 64 are contiguous."""
+    if t.dtype != dtype or t.shape != shape or t.device != dev:
+        raise OALError(OAL_ERR_INVALID_ARG, "%s must be %s %s on %s (got %s %s on %s)"
+                       % (name, dtype, tuple(shape), dev, t.dtype, tuple(t.shape), t.device))
+    s = t.stride()
+    _need(s[3] == 1, "rows of %s must be contiguous" % name)
+    # (the stride of a dimension of one says nothing)
+    return s if min(shape) > 1 else tuple(x if n > 1 else 0 for x, n in zip(s, shape))
+
+
+def _need_positions(positions, B, T, past, lengths, plan, dev):
+    if plan is not None:
+        _need_tensor(plan, "plan", torch.int64, (2, 32), dev)
+    if past is not None:
+        _need_tensor(past, "past", torch.int32, (B,), dev)
+    _need_lengths(lengths, B, dev)
+    if positions is None:
+        return 0
+    _need(positions.dim() == 3, "positions must have 3 dimensions")
+    _need_tensor(positions, "positions", torch.int32, (positions.shape[0], B, T), dev)
+    return positions.shape[0]
+
+
+def oal_rope(Q, K, plan, positions=None, past=None, lengths=None, form=OAL_ROPE_HALVES,
+             inverse=False, Yq=None, Yk=None, stream=None):
+    """Rotary positions: Q [B,Hq,T,64] and K [B,Hkv,T,64] (or None), views whose
+    rows are contiguous; plan of oal_rope_plan; positions [n_axes,B,T] int32, or
+    past[b] + t (past [B] int32 or None) on every axis; lengths [B] int32 or None.
+    inverse: by the opposite angles, for gradients.  Returns (Yq, Yk), contiguous;
+    they may be given, also as Q and K themselves.  Rows behind a sequence's
+    length stay as given; outputs made here have zeros there."""
+    lib = load_library()
+    _need(Q.dim() == 4 and (K is None or K.dim() == 4), "Q and K must have 4 dimensions")
+    _need(plan is not None, "plan is needed")
+    B, Hq, T, d = Q.shape
+    dt, dev, Hkv = _dtype_code(Q), Q.device, 0 if K is None else K.shape[1]
+    sq = _rows(Q, "Q", Q.dtype, (B, Hq, T, d), dev)
+    sk = sq if K is None else _rows(K, "K", Q.dtype, (B, Hkv, T, d), dev)
+    n_axes = _need_positions(positions, B, T, past, lengths, plan, dev)
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return oal_rope(Q, K, plan, positions, past, lengths, form, inverse, Yq, Yk, stream)
+    made = []
+    make = torch.empty if lengths is None else torch.zeros
+    if Yq is None:
+        Yq = make(B, Hq, T, d, dtype=Q.dtype, device=dev)
+        made.append(Yq)
+    _need_tensor(Yq, "Yq", Q.dtype, (B, Hq, T, d), dev)
+    if K is None:
+        _need(Yk is None, "Yk without K")
+    elif Yk is None:
+        Yk = make(B, Hkv, T, d, dtype=Q.dtype, device=dev)
+        made.append(Yk)
+    if Yk is not None:
+        _need_tensor(Yk, "Yk", Q.dtype, (B, Hkv, T, d), dev)
+    strides = (ctypes.c_int64 * 6)(*sq[:3], *sk[:3])
+    _check(lib.oal_rope(Q.data_ptr(), _ptr_or_null(K), dt, strides, B, Hq, Hkv, T, d,
+                        plan.data_ptr(), form, _ptr_or_null(positions), n_axes, _ptr_or_null(past),
+                        _ptr_or_null(lengths), bool(inverse), Yq.data_ptr(), _ptr_or_null(Yk),
+                        _stream_on(dev, stream, made)))
+    return Yq, Yk
+
+
+def _pages(Kp, Vp, Hkv, table, B, dtype, dev):
+    """Number of pages, their size and stride, entries of the table."""
+    _need(Kp.dim() == 4 and table.dim() == 2, "Kp must have 4 dimensions, table 2")
+    n, h, P, d = Kp.shape
+    sk, sv = Kp.stride(), Vp.stride()
+    if not (Kp.dtype is dtype and Vp.dtype is dtype and h == Hkv and Vp.shape == Kp.shape
+            and Kp.device == dev and Vp.device == dev):
+        raise OALError(OAL_ERR_INVALID_ARG, "Kp and Vp must be %s [n_pages,%d,page_size,%d] on %s"
+                       % (dtype, Hkv, d, dev))
+    _need((n < 2 or sk[0] == sv[0]) and (h < 2 or sk[1] == sv[1] == P * d)
+          and sk[2] == sv[2] == d and sk[3] == sv[3] == 1,
+          "the pages of Kp and Vp must be contiguous and equally far apart")
+    _need_tensor(table, "table", torch.int32, (B, table.shape[1]), dev)
+    # (one page: how far the next would be is anyone's guess)
+    return n, P, sk[0] if n > 1 else h * P * d, table.shape[1]
+
+
+def oal_page_append(Q, K, V, plan, Kp, Vp, table, past, positions=None, lengths=None,
+                    form=OAL_ROPE_HALVES, Yq=None, stream=None):
+    """T new tokens behind the past[b] of each sequence enter the paged cache: K
+    [B,Hkv,T,64], turned as by oal_rope, and V as it is go to Kp and Vp
+    [n_pages,Hkv,page_size,64] by table [B,max_pages] int32; past [B] int32.  Q
+    [B,Hq,T,64] is turned along into Yq (both may be None); plan None: nothing
+    is turned.  Q, K, V may be views whose rows are contiguous.  Returns Yq."""
+    lib = load_library()
+    _need(K.dim() == 4 and V.dim() == 4 and (Q is None or Q.dim() == 4),
+          "Q, K and V must have 4 dimensions")
+    B, Hkv, T, d = K.shape
+    dt, dev, dv, Hq = _dtype_code(K), K.device, V.shape[3], 0 if Q is None else Q.shape[1]
+    sk = _rows(K, "K", K.dtype, (B, Hkv, T, d), dev)
+    sv = _rows(V, "V", K.dtype, (B, Hkv, T, dv), dev)
+    sq = sk if Q is None else _rows(Q, "Q", K.dtype, (B, Hq, T, d), dev)
+    _need(past is not None, "past is needed")
+    n_axes = _need_positions(positions, B, T, past, lengths, plan, dev)
+    n, P, apart, most = _pages(Kp, Vp, Hkv, table, B, K.dtype, dev)
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return oal_page_append(Q, K, V, plan, Kp, Vp, table, past, positions, lengths, form, Yq,
+                                   stream)
+    made = []
+    if Q is None:
+        _need(Yq is None, "Yq without Q")
+    elif Yq is None:
+        Yq = (torch.empty if lengths is None else torch.zeros)(B, Hq, T, d, dtype=K.dtype, device=dev)
+        made.append(Yq)
+    if Yq is not None:
+        _need_tensor(Yq, "Yq", K.dtype, (B, Hq, T, d), dev)
+    strides = (ctypes.c_int64 * 9)(*sq[:3], *sk[:3], *sv[:3])
+    _check(lib.oal_page_append(_ptr_or_null(Q), K.data_ptr(), V.data_ptr(), dt, strides, B, Hq, Hkv,
+                               T, d, dv, _ptr_or_null(plan), form, _ptr_or_null(positions), n_axes,
+                               past.data_ptr(), _ptr_or_null(lengths), Kp.data_ptr(), Vp.data_ptr(),
+                               n, P, apart, table.data_ptr(), most, _ptr_or_null(Yq),
+                               _stream_on(dev, stream, made)))
+    return Yq
+
+
+def oal_paged_attention_workspace_bytes(B, Hq, Hkv, T, page_size, max_pages, d=64, dv=64,
+                                        dtype=OAL_BF16):
+    return int(load_library().oal_paged_attention_workspace_bytes(B, Hq, Hkv, T, d, dv, dtype,
+                                                                  page_size, max_pages))
+
+
+def oal_paged_attention(Q, Kp, Vp, table, past, lengths=None, scale=0.125, cap=0.0, window=0,
+                        slopes=None, prefix=None, first=None, Y=None, workspace=None, stream=None):
+    """Softmax attention of T >= 1 new tokens, already appended, over the paged
+    cache: Q [B,Hq,T,64]; Kp, Vp, table, past, lengths as for oal_page_append.
+    Token t at i = past[b] + t sees key j if first[b,t] <= j, i - window < j
+    (window 0: no such limit), and j <= i or j < prefix[b].  Scores scale q.k are
+    capped by cap tanh(s / cap) (cap 0: not) and take -slopes[h] |i - j|.
+    slopes [Hq] float32, prefix [B] int32, first [B,T] int32, or None.  Returns
+    Y; rows behind a sequence's length stay as given (a Y made here has zeros
+    there), tokens that see nothing get zeros."""
+    lib = load_library()
+    _need(Q.dim() == 4, "Q must have 4 dimensions")
+    B, Hq, T, d = Q.shape
+    dt, dev, Hkv, dv = _dtype_code(Q), Q.device, Kp.shape[1] if Kp.dim() == 4 else 0, Vp.shape[-1]
+    _need_tensor(Q, "Q", Q.dtype, (B, Hq, T, d), dev)
+    n, P, apart, most = _pages(Kp, Vp, Hkv, table, B, Q.dtype, dev)
+    _need_tensor(past, "past", torch.int32, (B,), dev)
+    _need_lengths(lengths, B, dev)
+    if slopes is not None:
+        _need_tensor(slopes, "slopes", torch.float32, (Hq,), dev)
+    if prefix is not None:
+        _need_tensor(prefix, "prefix", torch.int32, (B,), dev)
+    if first is not None:
+        _need_tensor(first, "first", torch.int32, (B, T), dev)
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return oal_paged_attention(Q, Kp, Vp, table, past, lengths, scale, cap, window, slopes,
+                                       prefix, first, Y, workspace, stream)
+    made = []
+    if Y is None:
+        Y = (torch.empty if lengths is None else torch.zeros)(B, Hq, T, dv, dtype=Q.dtype, device=dev)
+        made.append(Y)
+    _need_tensor(Y, "Y", Q.dtype, (B, Hq, T, dv), dev)
+    workspace = _workspace(workspace, lib.oal_paged_attention_workspace_bytes, made,
+                           (B, Hq, Hkv, T, d, dv, dt, P, most), dev)
+    _check(lib.oal_paged_attention(Q.data_ptr(), dt, B, Hq, Hkv, T, d, dv, Kp.data_ptr(),
+                                   Vp.data_ptr(), n, P, apart, table.data_ptr(), most,
+                                   past.data_ptr(), _ptr_or_null(lengths), scale, cap, window,
+                                   _ptr_or_null(slopes), _ptr_or_null(prefix), _ptr_or_null(first),
+                                   Y.data_ptr(), workspace.data_ptr(),
+                                   workspace.numel() * workspace.element_size(),
+                                   _stream_on(dev, stream, made)))
+    return Y
 
 
 def oal_sync_status(stream=None):

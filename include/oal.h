@@ -336,6 +336,119 @@ oal_status oal_state_remap(void *pool, size_t slot_bytes, int n_slots, const int
                            cudaStream_t stream);
 
 /*
+ * Rotary positions, for the inputs of every attention here, and the layers that
+ * keep softmax attention: their cache in pages, and the attention over it.
+ *
+ * oal_rope_plan -- HOST function: what the rotations need of the angles, to be
+ * copied to the device once.
+ *  freq   [32] angle per position of each pair, in radians, fp64, finite.
+ *  axes   [32] axis of each pair's positions (time, height, width, ...), >= 0,
+ *         or NULL: axis 0.
+ *  plan   [64] int64 output: the angles in turns of 2^64, then the axes.
+ */
+oal_status oal_rope_plan(const double *freq, const int32_t *axes, int64_t *plan);
+
+/*
+ * oal_rope -- turns the rows of Q and K by their positions: pair r of token t by
+ * the angle positions[axis_r][b][t] * freq[r],
+ *     (x, y) -> (x cos - y sin, y cos + x sin).
+ *  Q [B][Hq][T][d], K [B][Hkv][T][d] in `dtype`; K may be NULL (Hkv is then not
+ *           used).
+ *  strides  [2][3] int64 (host): elements from batch to batch, head to head and
+ *           token to token of Q and K, e.g. of views of a projection's output;
+ *           multiples of 16 bytes.  NULL: contiguous.  A row is contiguous.
+ *  plan     of oal_rope_plan (device).
+ *  form     which elements pair up: OAL_ROPE_HALVES (r, r + 32),
+ *           OAL_ROPE_PAIRS (2r, 2r + 1).
+ *  positions  [n_axes][B][T] int32 (device), any value; or NULL: past[b] + t
+ *           on every axis.  An axis of the plan outside 0..n_axes-1 counts as 0
+ *           and is recorded in the device status word (OAL_ERR_INVALID_ARG).
+ *  past     [B] int32 (device) or NULL (zeros); used without positions.
+ *  lengths  [B] int32 (device): tokens of each sequence, 0..T; NULL = T each.
+ *           Rows behind a sequence's length are neither read nor written.  A
+ *           length outside 0..T is clamped and recorded.
+ *  inverse  != 0: by the opposite angles: the gradient of a rotation's inputs is
+ *           that of its outputs, turned back.
+ *  Yq, Yk   [B][Hq][T][d], [B][Hkv][T][d], contiguous.  Yq may be Q and Yk K
+ *           where those are contiguous; otherwise no output may overlap an input.
+ * Arithmetic: angles modulo a turn in 64-bit fixed point, cos and sin in fp32,
+ * products in fp32, rounded once.  No workspace.  Supported: d == 64.
+ */
+typedef enum { OAL_ROPE_HALVES = 0, OAL_ROPE_PAIRS = 1 } oal_rope_form;
+oal_status oal_rope(const void *Q, const void *K, oal_dtype dtype, const int64_t *strides, int B,
+                    int Hq, int Hkv, int T, int d, const int64_t *plan, oal_rope_form form,
+                    const int32_t *positions, int n_axes, const int32_t *past,
+                    const int32_t *lengths, int inverse, void *Yq, void *Yk, cudaStream_t stream);
+
+/*
+ * The cache of keys and values: pools Kp, Vp of n_pages pages, a page
+ * [Hkv][page_size][d] in `dtype`, page i at i * page_stride elements (so that a
+ * pool may hold both: [n_pages][2][Hkv][page_size][d], whose pages
+ * oal_state_remap copies and frees).  Key j of sequence b is row j % page_size
+ * of page table[b][j / page_size]; table [B][max_pages] int32 (device).
+ * page_size: a power of two, 16 .. 65536; page_size * max_pages <= 2^30;
+ * page_stride >= Hkv * page_size * d, a multiple of 16 bytes.
+ *
+ * oal_page_append -- writes T new tokens behind the past[b] that sequence b has:
+ * K, turned as by oal_rope, and V as it is; and turns Q along.
+ *  Q [B][Hq][T][d] or NULL (Hq and Yq are then not used), K [B][Hkv][T][d],
+ *  V [B][Hkv][T][dv]; strides [3][3] as for oal_rope.
+ *  plan     NULL: nothing is turned (Q has to be NULL then).
+ *  past     [B] int32 (device).  A token whose page is not in the table, or
+ *           whose entry is outside 0..n_pages-1, is not written to the cache and
+ *           recorded in the device status word (OAL_ERR_INVALID_ARG).  Two tokens
+ *           with the same place leave either there.
+ * The rest, and the arithmetic, as for oal_rope.
+ */
+oal_status oal_page_append(const void *Q, const void *K, const void *V, oal_dtype dtype,
+                           const int64_t *strides, int B, int Hq, int Hkv, int T, int d, int dv,
+                           const int64_t *plan, oal_rope_form form, const int32_t *positions,
+                           int n_axes, const int32_t *past, const int32_t *lengths, void *Kp,
+                           void *Vp, int n_pages, int page_size, int64_t page_stride,
+                           const int32_t *table, int max_pages, void *Yq, cudaStream_t stream);
+
+/*
+ * oal_paged_attention -- softmax attention of T >= 1 new tokens, already in the
+ * cache, over the cache.  Query head h reads key/value head h / (Hq / Hkv).
+ * Token t of sequence b is at i = past[b] + t and sees the keys j with
+ *     first[b][t] <= j,  i - window < j,  and j <= i or j < prefix[b],
+ * of the sequence's past[b] + lengths[b].  With
+ *     s_j = scale q.k_j;  s_j = cap tanh(s_j / cap) if cap > 0;
+ *     s_j -= slopes[h] |i - j|,
+ * y = sum_j softmax(s)_j v_j; a token that sees nothing gets zeros.
+ *  Q [B][Hq][T][d], Y [B][Hq][T][dv] in `dtype`, contiguous.
+ *  past     [B] int32 (device): tokens before the T new ones.  Negative, or
+ *           behind what the table has room for: clamped and recorded.
+ *  lengths  [B] int32 (device) or NULL: as for oal_rope.
+ *  scale    finite and > 0.  cap: 0 or a finite number > 0.  window: 0 (none)
+ *           or > 0.
+ *  slopes   [Hq] fp32 (device) or NULL; first [B][T] int32 or NULL (document
+ *           masks: the first key of the token's document); prefix [B] int32 or
+ *           NULL.
+ *  A page that holds a visible key and is outside 0..n_pages-1 counts as zeros
+ *  and is recorded.  Pages without visible keys are not looked up, and keys that
+ *  a token does not see have no part in its result whatever they hold.  Rows that
+ *  see keys or values that are not finite, or whose scores leave fp32, have
+ *  unspecified results.
+ *  workspace  >= oal_paged_attention_workspace_bytes(...) bytes, 256-byte
+ *           aligned, contents need not be initialised.  Calls that may overlap
+ *           on the GPU need one each.
+ * Arithmetic: OAL_F32 in fp32 on the CUDA cores.  OAL_BF16 on the tensor cores;
+ * scores, maxima, sums and results in fp32, softmax's weights rounded to bf16
+ * once.  Deterministic.  Supported: d == dv == 64, Hq / Hkv <= 128,
+ * B * Hkv <= 65535, T * Hq / Hkv <= 2^28.
+ */
+size_t oal_paged_attention_workspace_bytes(int B, int Hq, int Hkv, int T, int d, int dv,
+                                           oal_dtype dtype, int page_size, int max_pages);
+oal_status oal_paged_attention(const void *Q, oal_dtype dtype, int B, int Hq, int Hkv, int T,
+                               int d, int dv, const void *Kp, const void *Vp, int n_pages,
+                               int page_size, int64_t page_stride, const int32_t *table,
+                               int max_pages, const int32_t *past, const int32_t *lengths,
+                               float scale, float cap, int window, const float *slopes,
+                               const int32_t *prefix, const int32_t *first, void *Y,
+                               void *workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
  * Calibration, the step before the path ([OAL] Sec. 3.1 and App. B "Dimension
  * grouping"): the groups of each query head follow from contribution scores.
  *
