@@ -707,7 +707,7 @@ static oal_status check_pages(int Hkv, int n_pages, int page_size, int64_t page_
     return oal_fail(OAL_ERR_INVALID_ARG, "page_size=%d is not a power of two", page_size);
   if (page_size < 16 || page_size > 65536 || (long long)page_size * max_pages > 1LL << 30)
     return oal_fail(OAL_ERR_UNSUPPORTED, "page_size=%d, max_pages=%d", page_size, max_pages);
-  if (page_stride < (int64_t)Hkv * page_size * oal::kD || page_stride % 8 != 0)
+  if (page_stride < (int64_t)Hkv * page_size * oal::kD || page_stride % 8 != 0 || page_stride > 1LL << 38)
     return oal_fail(OAL_ERR_INVALID_ARG, "page_stride=%lld", (long long)page_stride);
   *shift = 0;
   while (1 << *shift < page_size) ++*shift;

@@ -8,6 +8,8 @@ namespace oal {
 
 oal_status launch_paged_simt(const PagedArgs &p, cudaStream_t stream);
 oal_status launch_paged_rows(const PagedArgs &p, cudaStream_t stream);
+int paged_tc_rows(int T, int rho);
+oal_status launch_paged_tc(const PagedArgs &p, cudaStream_t stream);
 
 namespace {
 
@@ -87,7 +89,10 @@ constexpr int kSplitLeast = 256;          // keys of a split at least
 static long long plan_tiles(PagedArgs &p, int is_bf16) {
   const long long rows = (long long)p.T * p.rho, units = (long long)p.B * p.Hkv;
   long long want;                         // blocks
-  if (is_bf16) {
+  if (is_bf16 && rows > 32) {
+    p.tile_rows = paged_tc_rows(p.T, p.rho);
+    want = 152 * 4;
+  } else if (is_bf16) {
     p.tile_rows = rows <= 16 ? 16 : 32;
     want = 152 * 2 * 4;
   } else {
@@ -120,7 +125,8 @@ oal_status launch_paged(PagedArgs p, int is_bf16, void *ws, cudaStream_t stream)
   plan_split(p, plan_tiles(p, is_bf16));
   p.part_o = static_cast<float *>(ws);
   p.part_ml = reinterpret_cast<float2 *>(p.part_o + part_rows(p, p.splits) * 64);
-  return is_bf16 ? launch_paged_rows(p, stream) : launch_paged_simt(p, stream);
+  if (!is_bf16) return launch_paged_simt(p, stream);
+  return (long long)p.T * p.rho > 32 ? launch_paged_tc(p, stream) : launch_paged_rows(p, stream);
 }
 
 }  // namespace oal

@@ -1,0 +1,475 @@
+// paged_tc.cu -- attention over a paged cache for bf16 on the tensor cores
+// (tcgen05), for chunks of new tokens.
+//
+// A block takes two tiles of 128 rows (row h' * nt + t': nt tokens of all rho
+// query heads of a KV head) over the keys that they see, 128 keys at a time:
+//     S = Q K^T                 tcgen05, operands as TMA left them
+//     P = 2^{s - m} (bf16)      four warps a tile, a row a thread: tensor memory -> registers -> tensor memory
+//     O += P V                  tcgen05, P from tensor memory
+// One warp loads (a page is a box of TMA's, or part of one), one issues.  Three
+// places for scores go round between the two tiles, so that the next scores of
+// a tile are there when its warps have finished the ones before; P lies in the
+// place of its scores.  MMAs run in the order of their issue, so scores may go
+// where a P that an earlier MMA reads lies.
+//
+// m is the row's maximum at some time, at most 2^8 below the present one: O is
+// multiplied by a power of two (through registers) only when it falls behind
+// further, which after the first keys is rare.
+//
+// What bounds it: 512 cycles of MMA and as many of the exponentials' units for
+// 128 x 128 scores.
+#include <algorithm>
+
+#include "gated_tc.cuh"
+#include "paged.cuh"
+
+namespace oal {
+namespace {
+using namespace gated;
+
+constexpr int kTcThreads = 320;           // two tiles' warps, the loading one, the issuing one
+constexpr int kLoadWarp = 8, kIssueWarp = 9;
+constexpr int kKeys = 128;
+constexpr int kTile = 128 * 128;          // bytes of 128 rows of 64
+constexpr int kRing = 4;                  // key tiles in flight, of K and of V
+constexpr uint32_t kColO = 384;           // tensor memory: three places of 128 for scores, then O of each tile
+constexpr float kBehind = 8.f;
+
+struct TcSmem {
+  uint8_t q[2][kTile], k[kRing][kTile], v[kRing][kTile];
+  uint64_t q_full, k_full[kRing], k_free[kRing], v_full[kRing], v_free[kRing], v_raw;
+  uint64_t s_full[2][3], p_full[3], o_done[2], drain;
+  int lo[8], hi[8];                       // keys that the rows of each warp see
+  uint32_t tmem;
+  WaitState wait;
+};
+constexpr size_t kTcBytes = sizeof(TcSmem) + 1024;
+
+__device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, uint64_t *bar, int x, int y, int z, int w) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t *r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t x, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// The key tiles of the block's two tiles of rows, and the order of their scores:
+// by key tile, first tile first.
+struct TcWork {
+  int from[2], to[2];                     // key tiles
+  __device__ __forceinline__ int count(int x, int j) const { return min(max(j - from[x], 0), to[x] - from[x]); }
+  __device__ __forceinline__ bool has(int x, int j) const { return j >= from[x] && j < to[x]; }
+  // the place in that order of tile x's scores with key tile j
+  __device__ __forceinline__ int unit(int x, int j) const { return count(0, x ? j + 1 : j) + count(1, j); }
+};
+
+// kExtra: scores are capped or take a distance.
+template <bool kExtra>
+__global__ void __launch_bounds__(kTcThreads, 1)
+paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                const __grid_constant__ CUtensorMap tmV, PagedArgs p, int nt) {
+  extern __shared__ uint8_t smem_raw[];
+  TcSmem &s = *reinterpret_cast<TcSmem *>(align1024(smem_raw));
+  const int bh = blockIdx.x, b = bh / p.Hkv, kv = bh % p.Hkv, split = blockIdx.z;
+  const int t0 = (gridDim.y - 1 - blockIdx.y) * 2 * nt;    // the last tokens, which see most, first
+  const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
+  if (tid == 0) {
+    s.wait.abort = 0;
+    s.wait.status = p.status;
+    mbar_init(&s.q_full, 1);
+    for (int i = 0; i < kRing; ++i) {
+      mbar_init(&s.k_full[i], 1), mbar_init(&s.k_free[i], 1);
+      mbar_init(&s.v_full[i], 1), mbar_init(&s.v_free[i], 1);
+    }
+    mbar_init(&s.v_raw, 1);
+    for (int i = 0; i < 3; ++i) mbar_init(&s.s_full[0][i], 1), mbar_init(&s.s_full[1][i], 1), mbar_init(&s.p_full[i], 4);
+    for (int i = 0; i < 2; ++i) mbar_init(&s.o_done[i], 1);
+    mbar_init(&s.drain, 1);
+    fence_mbar_init();
+  }
+  pdl_wait();
+  const PagedSeq seq = paged_seq(p, b, tid == 0);
+  if (t0 >= seq.n) return;
+  if (warp == kIssueWarp) {
+    tmem_alloc(&s.tmem, 512);
+    tmem_relinquish();
+  }
+  int from = 0, to = INT32_MAX;
+  if (p.splits > 1) {
+    from = paged_base(p, seq, t0) + split * p.split_keys;
+    to = from + p.split_keys;
+  }
+  // the thread's row, and the keys that it sees
+  const int x = warp >> 2, r = tid & 127;                    // (warps 0 .. 7)
+  const int h1 = r / nt, t = t0 + x * nt + r % nt;
+  const bool live = warp < kLoadWarp && h1 < p.rho && t < seq.n;
+  int2 sees = make_int2(0, 0);
+  if (warp < kLoadWarp) {
+    if (live) sees = paged_sees(p, seq, b, t);
+    const int a = max(sees.x, from), z = min(sees.y, to);
+    const int lo = __reduce_min_sync(0xffffffffu, a < z ? a : INT32_MAX);
+    const int hi = __reduce_max_sync(0xffffffffu, a < z ? z : 0);
+    if (lane == 0) s.lo[warp] = lo, s.hi[warp] = hi;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  pdl_trigger();   // (not before: what comes behind must not hold tensor memory that this block waits for)
+  const uint32_t tb = uniform(s.tmem);
+  TcWork work;
+  int lo = INT32_MAX, hi = 0;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int a = min(min(s.lo[4 * i], s.lo[4 * i + 1]), min(s.lo[4 * i + 2], s.lo[4 * i + 3]));
+    const int z = max(max(s.hi[4 * i], s.hi[4 * i + 1]), max(s.hi[4 * i + 2], s.hi[4 * i + 3]));
+    work.from[i] = (int)uniform(z > 0 ? a / kKeys : 0), work.to[i] = (int)uniform((z + kKeys - 1) / kKeys);
+    lo = min(lo, a), hi = max(hi, z);
+  }
+  const bool two = work.to[1] > 0;
+  if (two && work.to[0] > 0) {            // no key tile between them without a user: the rings go by key tiles
+    work.to[0] = max(work.to[0], work.from[1]);
+    work.to[1] = max(work.to[1], work.from[0]);
+  }
+  const int j_first = work.to[0] == 0 ? work.from[1] : two ? min(work.from[0], work.from[1]) : work.from[0];
+  const int j_last = max(work.to[0], work.to[1]);
+
+  if (warp == kLoadWarp) {
+    int loads = 0;
+    bool ok = true, q_loaded = false;
+    if (j_first < j_last) {
+      if (lane == 0) {
+        const int bytes = nt * p.rho * 128;
+        mbar_arrive_expect_tx(&s.q_full, (work.to[0] > 0 ? bytes : 0) + (two ? bytes : 0));
+        if (work.to[0] > 0) tma_load_4d(s.q[0], &tmQ, &s.q_full, 0, t0, 0, bh);
+        if (two) tma_load_4d(s.q[1], &tmQ, &s.q_full, 0, t0 + nt, 0, bh);
+      }
+      q_loaded = true;
+    }
+    // a lane loads a page's part of the tile
+    const int page_rows = min(1 << p.page_shift, kKeys), boxes = kKeys / page_rows;
+    auto page_of = [&](int j) {           // out of range: zeros
+      const int key = j * kKeys + lane * page_rows;
+      if (lane >= boxes || j >= j_last || key + page_rows <= lo || key >= hi) return -1;
+      return paged_page(p, b, key);
+    };
+    int raw = 0;
+    int page = page_of(j_first);
+    for (int j = j_first; j < j_last; ++j, ++loads) {
+      const int st = loads % kRing, round = loads / kRing;
+      const int at = page >= 0 ? page : max(p.n_pages, 1);
+      const int y = (j * kKeys + lane * page_rows) & ((1 << p.page_shift) - 1);
+      page = page_of(j + 1);
+      if (round > 0) ok = warp_wait(&s.k_free[st], (round - 1) & 1, &s.wait);
+      if (!ok) break;
+      if (lane == 0) mbar_arrive_expect_tx(&s.k_full[st], kTile);
+      __syncwarp();
+      if (lane < boxes) tma_load_4d(s.k[st] + lane * page_rows * 128, &tmK, &s.k_full[st], 0, y, kv, at);
+      if (round > 0) ok = warp_wait(&s.v_free[st], (round - 1) & 1, &s.wait);
+      // values outside of what the rows see meet weights of 0, which an infinity or NaN would survive: zeros
+      const bool edge = j * kKeys < lo || (j + 1) * kKeys > hi;
+      uint64_t *bar = edge ? &s.v_raw : &s.v_full[st];
+      if (ok) {
+        if (lane == 0) mbar_arrive_expect_tx(bar, kTile);
+        __syncwarp();
+        if (lane < boxes) tma_load_4d(s.v[st] + lane * page_rows * 128, &tmV, bar, 0, y, kv, at);
+        if (edge) {
+          ok = warp_wait(bar, raw++ & 1, &s.wait);
+          for (int e = lane; ok && e < kKeys * 8; e += 32) {
+            const int key = j * kKeys + (e >> 3);
+            if (key < lo || key >= hi) reinterpret_cast<uint4 *>(s.v[st])[e] = make_uint4(0u, 0u, 0u, 0u);
+          }
+          fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s.v_full[st]);
+        }
+      }
+      if (!ok) {
+        ++loads;
+        break;
+      }
+    }
+    if (lane == 0) {                      // nothing in flight at the block's end
+      if (q_loaded) mbar_wait_teardown(&s.q_full, 0, p.status);
+      if (raw > 0) mbar_wait_teardown(&s.v_raw, (raw - 1) & 1, p.status);
+      for (int i = max(0, loads - kRing); i < loads; ++i) {
+        mbar_wait_teardown(&s.k_full[i % kRing], (i / kRing) & 1, p.status);
+        if (ok) mbar_wait_teardown(&s.v_full[i % kRing], (i / kRing) & 1, p.status);
+      }
+    }
+    __syncwarp();
+  } else if (warp == kIssueWarp) {
+    const uint32_t id_s = idesc_bf16_f32(128, kKeys, 0), id_o = idesc_bf16_f32(128, 64, 1);
+    bool ok = j_first >= j_last || warp_wait(&s.q_full, 0, &s.wait);
+    // (j, x) of the next scores to issue and of the next P V
+    int sj = j_first, sx = work.has(0, j_first) ? 0 : 1, su = 0, sn[2] = {0, 0};
+    auto step = [&](int &j, int &x) {
+      do {
+        if (++x == 2) x = 0, ++j;
+      } while (j < j_last && !work.has(x, j));
+    };
+    auto scores = [&]() {
+      if (sj >= j_last) return true;
+      const int st = (sj - j_first) % kRing;
+      if (!warp_wait(&s.k_full[st], ((sj - j_first) / kRing) & 1, &s.wait)) return false;
+      const uint64_t qd = sdesc_sw128(smem_u32(s.q[sx]), 16, 1024), kd = sdesc_sw128(smem_u32(s.k[st]), 16, 1024);
+      const uint32_t to_s = tb + su % 3 * 128;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) umma_ss_warp(to_s, qd + 2 * k, kd + 2 * k, id_s, k > 0);
+      // (a barrier by the tile's own count: its warps see every phase of it)
+      umma_commit_warp(&s.s_full[sx][(sx ? sn[1]++ : sn[0]++) % 3]);
+      const int j = sj;
+      step(sj, sx), ++su;
+      if (sj != j) umma_commit_warp(&s.k_free[st]);
+      return true;
+    };
+    ok = ok && scores() && scores();
+    int j = j_first, y = work.has(0, j_first) ? 0 : 1;
+    bool fresh[2] = {true, true};
+#pragma unroll 1
+    for (int u = 0; j < j_last && ok; ++u) {
+      ok = scores();
+      const int st = (j - j_first) % kRing;
+      ok = ok && warp_wait(&s.v_full[st], ((j - j_first) / kRing) & 1, &s.wait) &&
+           warp_wait(&s.p_full[u % 3], (u / 3) & 1, &s.wait);
+      if (!ok) break;
+      tc_fence_after();
+      const uint64_t vd = sdesc_sw128(smem_u32(s.v[st]), 16, 1024);
+      const uint32_t from_p = tb + u % 3 * 128, to_o = tb + kColO + 64 * y;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) umma_ts_warp(to_o, from_p + 8 * k, vd + 128 * k, id_o, k > 0 || !fresh[y]);
+      umma_commit_warp(&s.o_done[y]);
+      fresh[y] = false;
+      const int before = j;
+      step(j, y);
+      if (j != before) umma_commit_warp(&s.v_free[st]);
+    }
+    umma_commit_warp(&s.drain);
+    if (lane == 0) mbar_wait_teardown(&s.drain, 0, p.status);
+    __syncwarp();
+  } else {
+    const uint32_t tm = tb + ((uint32_t)(32 * (warp & 3)) << 16), to_o = tm + kColO + 64 * x;
+    const int h = kv * p.rho + h1;
+    const float scale2 = p.scale * kLog2e;
+    const float cap_in = kExtra && p.cap > 0.f ? 2.f * kLog2e * p.scale / p.cap : 0.f, cap_out = p.cap * kLog2e;
+    const float slope = kExtra && live && p.slopes ? p.slopes[h] * kLog2e : 0.f;
+    const float by = kExtra ? 1.f : scale2;                // of what is held as a score
+    const int see0 = max(sees.x, from), see1 = min(sees.y, to);
+    float m = -INFINITY;
+    uint64_t sum[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
+    bool ok = true;
+    int n = 0;                                               // the tile's key tiles so far
+#pragma unroll 1
+    for (int j = work.from[x]; j < work.to[x]; ++j, ++n) {
+      const int u = work.unit(x, j), j0 = j * kKeys;
+      const uint32_t at = tm + u % 3 * 128;
+      ok = warp_wait(&s.s_full[x][n % 3], (n / 3) & 1, &s.wait);
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t w[128];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_ld32(at + 32 * c, w + 32 * c);
+      tmem_wait_ld();
+      if (kExtra) {
+#pragma unroll
+        for (int e = 0; e < 128; ++e) {
+          float f = __uint_as_float(w[e]);
+          if (p.cap > 0.f) {                // cap tanh(f) = cap - 2 cap / (e^{2 f} + 1)
+            float z;
+            asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(z) : "f"(ex2(f * cap_in) + 1.f));
+            f = fmaf(-2.f * cap_out, z, cap_out);
+          } else {
+            f *= scale2;
+          }
+          w[e] = __float_as_uint(fmaf(-slope, (float)abs(seq.past + t - j0 - e), f));
+        }
+      }
+      if (!__all_sync(0xffffffffu, see0 <= j0 && see1 >= j0 + kKeys)) {
+        const uint32_t off = (uint32_t)(see0 - j0), len = (uint32_t)max(see1 - see0, 0);
+#pragma unroll
+        for (int e = 0; e < 128; ++e) w[e] = (uint32_t)e - off < len ? w[e] : 0xFF800000u;
+      }
+      float top[4] = {m, m, m, m};
+#pragma unroll
+      for (int e = 0; e < 128; e += 8) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) top[c] = fmaxf(top[c], fmaxf(__uint_as_float(w[e + 2 * c]), __uint_as_float(w[e + 2 * c + 1])));
+      }
+      const float now = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+      const bool behind = (now - m) * by > kBehind;          // (from -inf: always)
+      if (__any_sync(0xffffffffu, behind)) {
+        const float keep = behind ? ex2((m - now) * by) : 1.f;
+        if (behind) m = now;
+        float a, z;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          unpair(sum[c], a, z);
+          sum[c] = pair(a * keep, z * keep);
+        }
+        if (n > 0) {
+          ok = warp_wait(&s.o_done[x], (n - 1) & 1, &s.wait);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t o[16];
+            tmem_ld16(to_o + 16 * c, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * keep);
+            tmem_st16(to_o + 16 * c, o);
+          }
+        }
+      }
+      const float base = m == -INFINITY ? 0.f : -m * by;
+      const uint64_t by2 = pair(by, by), base2 = pair(base, base);
+      // weights, rounded to bf16 because the tensor cores take both factors in the values' type
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t pk[16];
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) {
+          float a, z;
+          unpair(fma2(pair(__uint_as_float(w[32 * c + e]), __uint_as_float(w[32 * c + e + 1])), by2, base2), a, z);
+          a = ex2(a), z = ex2(z);
+          sum[e >> 1 & 1] = add2(sum[e >> 1 & 1], pair(a, z));
+          pk[e >> 1] = pack_bf16x2(a, z);
+        }
+        tmem_st16(at + 16 * c, pk);
+      }
+      // (every time, so that the phases stay in step)
+      if (n > 0) ok = warp_wait(&s.o_done[x], (n - 1) & 1, &s.wait);
+      if (!ok) break;
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s.p_full[u % 3]);
+    }
+    float f[4];
+    unpair(sum[0], f[0], f[1]), unpair(sum[1], f[2], f[3]);
+    const float total = (f[0] + f[1]) + (f[2] + f[3]);
+    if (n > 0 && ok) ok = warp_wait(&s.o_done[x], (n - 1) & 1, &s.wait);
+    if (ok) {
+      tc_fence_after();
+      bool wrong = false;
+      const size_t row = ((size_t)bh * p.splits + split) * ((size_t)p.T * p.rho) + (size_t)t * p.rho + h1;
+      const float inv = see0 < see1 ? 1.f / total : 0.f;
+      if (p.splits > 1 && live) p.part_ml[row] = make_float2(m == -INFINITY ? m : m * by, total);
+#pragma unroll 1
+      for (int c = 0; c < 4; ++c) {
+        uint32_t o[16];
+        if (n > 0) {
+          tmem_ld16(to_o + 16 * c, o);
+          tmem_wait_ld();
+        } else {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) o[e] = 0u;
+        }
+        if (!live) continue;
+        if (p.splits > 1) {
+          uint4 *dst = reinterpret_cast<uint4 *>(p.part_o + row * 64 + 16 * c);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) dst[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+        } else {
+          uint32_t pk[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float a = inv == 0.f ? 0.f : __uint_as_float(o[2 * e]) * inv;
+            const float z = inv == 0.f ? 0.f : __uint_as_float(o[2 * e + 1]) * inv;
+            wrong |= !(fabsf(a) + fabsf(z) < INFINITY);
+            pk[e] = pack_bf16x2(a, z);
+          }
+          uint4 *dst = reinterpret_cast<uint4 *>(paged_y<__nv_bfloat16>(p, b, h, t) + 16 * c);
+          dst[0] = make_uint4(pk[0], pk[1], pk[2], pk[3]), dst[1] = make_uint4(pk[4], pk[5], pk[6], pk[7]);
+        }
+      }
+      for (uint32_t again = __ballot_sync(0xffffffffu, wrong); again; again &= again - 1) {
+        const int who = __ffs(again) - 1;
+        const int h2 = __shfl_sync(0xffffffffu, h, who), t2 = __shfl_sync(0xffffffffu, t, who);
+        const int a = __shfl_sync(0xffffffffu, sees.x, who), z = __shfl_sync(0xffffffffu, sees.y, who);
+        const float2 y = paged_row_again<__nv_bfloat16>(p, b, h2, t2, a, z);
+        __syncwarp();
+        *reinterpret_cast<uint32_t *>(paged_y<__nv_bfloat16>(p, b, h2, t2) + 2 * lane) = pack_bf16x2(y.x, y.y);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kIssueWarp) tmem_dealloc(tb, 512);
+}
+
+oal_status tc_map(CUtensorMap *m, const void *ptr, const cuuint64_t (&dims)[4], const cuuint64_t (&strides)[3],
+                  const cuuint32_t (&box)[4]) {
+  auto fn = encode_fn();
+  if (!fn) return oal_fail(OAL_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
+  const cuuint32_t es[4] = {1, 1, 1, 1};
+  if (fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(ptr), dims, strides, box, es,
+         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return oal_fail(OAL_ERR_CUDA, "cuTensorMapEncodeTiled failed");
+  return OAL_OK;
+}
+
+template <bool kExtra>
+oal_status run(const PagedArgs &p, cudaStream_t stream) {
+  static bool done[kMaxDevices];
+  auto kernel = paged_tc_kernel<kExtra>;
+  oal_status st = paged_need_smem(reinterpret_cast<const void *>(kernel), kTcBytes, done);
+  if (st != OAL_OK) return st;
+  const int nt = p.tile_rows / (2 * p.rho);
+  CUtensorMap mq, mk, mv;
+  st = tc_map(&mq, p.Q, {64, (cuuint64_t)p.T, (cuuint64_t)p.rho, (cuuint64_t)p.B * p.Hkv},
+              {128, (cuuint64_t)p.T * 128, (cuuint64_t)p.T * p.rho * 128}, {64, (cuuint32_t)nt, (cuuint32_t)p.rho, 1});
+  const cuuint64_t page = (cuuint64_t)1 << p.page_shift;
+  const cuuint64_t dims[4] = {64, page, (cuuint64_t)p.Hkv, (cuuint64_t)std::max(p.n_pages, 1)};
+  const cuuint64_t strides[3] = {128, page * 128, (cuuint64_t)p.page_stride * 2};
+  const cuuint32_t box[4] = {64, (cuuint32_t)std::min<cuuint64_t>(page, kKeys), 1, 1};
+  if (st == OAL_OK) st = tc_map(&mk, p.Kp, dims, strides, box);
+  if (st == OAL_OK) st = tc_map(&mv, p.Vp, dims, strides, box);
+  if (st != OAL_OK) return st;
+  const dim3 grid((unsigned)(p.B * p.Hkv), (unsigned)((p.T + 2 * nt - 1) / (2 * nt)), (unsigned)p.splits);
+  launch_pdl(kernel, grid, dim3(kTcThreads), kTcBytes, stream, mq, mk, mv, p, nt);
+  st = oal_after_launch("paged_tc_kernel", stream);
+  return st != OAL_OK || p.splits == 1 ? st : launch_paged_join(p, 1, stream);
+}
+
+}  // namespace
+
+// Rows of a block: two tiles of as many tokens as fit.
+int paged_tc_rows(int T, int rho) { return 2 * rho * std::min(T, 128 / rho); }
+
+oal_status launch_paged_tc(const PagedArgs &p, cudaStream_t stream) {
+  return p.cap > 0.f || p.slopes ? run<true>(p, stream) : run<false>(p, stream);
+}
+
+}  // namespace oal

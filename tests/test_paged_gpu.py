@@ -334,6 +334,22 @@ def test_masks(oal, dtype, kind, B, Hq, Hkv, T, past, page, lengths):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("Hq,T", [(8, 1500), (2, 1100), (14, 700)])
+@pytest.mark.parametrize("turn", [0, 1])
+def test_documents_of_unequal_lengths(oal, dtype, Hq, T, turn):
+    """Neighbouring tiles of rows whose keys begin far apart, the first or the second one's earlier; tiles that see
+    nothing between others."""
+    c = Cache(1, 2, [40], [T], 32, dtype, seed=61, fill=math.nan)
+    Q = draw((1, Hq, T, 64), dtype, 62, 1.5)
+    for width in (32, 96, 128, 18):
+        t = torch.arange(T)
+        odd = t // width % 2 == turn
+        check(oal, c, Q, first=torch.where(odd, 0, (t + 40 - t % width).clamp(min=0)).to(torch.int32)[None].cuda())
+        check(oal, c, Q, first=torch.where(odd, 0, 1 << 28).to(torch.int32)[None].cuda())
+        check(oal, c, Q, first=torch.where(t % (2 * width) == (2 * width - 1 if turn else 0), t + 40, 1 << 28).to(torch.int32)[None].cuda())
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf, 3e38])
 @pytest.mark.parametrize("T,past", [(1, 5000), (6, 900), (90, 4000), (300, 200)])
 def test_masked_keys_have_no_part(oal, dtype, bad, T, past):
