@@ -6,11 +6,13 @@
 //     S = Q K^T                 tcgen05, operands as TMA left them
 //     P = 2^{s - m} (bf16)      four warps a tile, a row a thread: tensor memory -> registers -> tensor memory
 //     O += P V                  tcgen05, P from tensor memory
-// One warp loads (a page is a box of TMA's, or part of one), one issues.  Three
+// One warp loads keys and one values (a page is a box of TMA's, or part of one),
+// one issues the first product and one the second: a wait on a barrier that is
+// complete costs an issuing warp about 130 cycles beside MMAs that read shared
+// memory, and one warp for both took 1,320 cycles for the 512 of its MMAs.  Three
 // places for scores go round between the two tiles, so that the next scores of
 // a tile are there when its warps have finished the ones before; P lies in the
-// place of its scores.  MMAs run in the order of their issue, so scores may go
-// where a P that an earlier MMA reads lies.
+// place of its scores.
 //
 // m is the row's maximum at some time, at most 2^8 below the present one: O is
 // multiplied by a power of two (through registers) only when it falls behind
@@ -27,8 +29,8 @@ namespace oal {
 namespace {
 using namespace gated;
 
-constexpr int kTcThreads = 320;           // two tiles' warps, the loading one, the issuing one
-constexpr int kLoadWarp = 8, kIssueWarp = 9;
+constexpr int kTcThreads = 384;           // two tiles' warps, and four that load and issue
+constexpr int kLoadK = 8, kScoreWarp = 9, kValueWarp = 10, kLoadV = 11;
 constexpr int kKeys = 128;
 constexpr int kTile = 128 * 128;          // bytes of 128 rows of 64
 constexpr int kRing = 4;                  // key tiles in flight, of K and of V
@@ -38,7 +40,7 @@ constexpr float kBehind = 8.f;
 struct TcSmem {
   uint8_t q[2][kTile], k[kRing][kTile], v[kRing][kTile];
   uint64_t q_full, k_full[kRing], k_free[kRing], v_full[kRing], v_free[kRing], v_raw;
-  uint64_t s_full[2][3], p_full[3], o_done[2], drain;
+  uint64_t s_full[2][3], p_full[3], o_done[2], drain[2];
   int lo[8], hi[8];                       // keys that the rows of each warp see
   uint32_t tmem;
   WaitState wait;
@@ -86,12 +88,17 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 
 // The key tiles of the block's two tiles of rows, and the order of their scores:
 // by key tile, first tile first.
+// (Selected, not indexed: an index would put them into local memory, and what
+// is loaded from there is not known to be the same in all lanes.)
 struct TcWork {
-  int from[2], to[2];                     // key tiles
-  __device__ __forceinline__ int count(int x, int j) const { return min(max(j - from[x], 0), to[x] - from[x]); }
-  __device__ __forceinline__ bool has(int x, int j) const { return j >= from[x] && j < to[x]; }
+  int from0, to0, from1, to1;             // key tiles
+  __device__ __forceinline__ int from(int x) const { return x ? from1 : from0; }
+  __device__ __forceinline__ int to(int x) const { return x ? to1 : to0; }
+  __device__ __forceinline__ bool has(int x, int j) const { return j >= from(x) && j < to(x); }
   // the place in that order of tile x's scores with key tile j
-  __device__ __forceinline__ int unit(int x, int j) const { return count(0, x ? j + 1 : j) + count(1, j); }
+  __device__ __forceinline__ int unit(int x, int j) const {
+    return min(max((x ? j + 1 : j) - from0, 0), to0 - from0) + min(max(j - from1, 0), to1 - from1);
+  }
 };
 
 // kExtra: scores are capped or take a distance.
@@ -114,14 +121,13 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
     }
     mbar_init(&s.v_raw, 1);
     for (int i = 0; i < 3; ++i) mbar_init(&s.s_full[0][i], 1), mbar_init(&s.s_full[1][i], 1), mbar_init(&s.p_full[i], 4);
-    for (int i = 0; i < 2; ++i) mbar_init(&s.o_done[i], 1);
-    mbar_init(&s.drain, 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&s.o_done[i], 1), mbar_init(&s.drain[i], 1);
     fence_mbar_init();
   }
   pdl_wait();
   const PagedSeq seq = paged_seq(p, b, tid == 0);
   if (t0 >= seq.n) return;
-  if (warp == kIssueWarp) {
+  if (warp == kScoreWarp) {
     tmem_alloc(&s.tmem, 512);
     tmem_relinquish();
   }
@@ -133,9 +139,9 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
   // the thread's row, and the keys that it sees
   const int x = warp >> 2, r = tid & 127;                    // (warps 0 .. 7)
   const int h1 = r / nt, t = t0 + x * nt + r % nt;
-  const bool live = warp < kLoadWarp && h1 < p.rho && t < seq.n;
+  const bool live = warp < 8 && h1 < p.rho && t < seq.n;
   int2 sees = make_int2(0, 0);
-  if (warp < kLoadWarp) {
+  if (warp < 8) {
     if (live) sees = paged_sees(p, seq, b, t);
     const int a = max(sees.x, from), z = min(sees.y, to);
     const int lo = __reduce_min_sync(0xffffffffu, a < z ? a : INT32_MAX);
@@ -147,135 +153,147 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
   tc_fence_after();
   pdl_trigger();   // (not before: what comes behind must not hold tensor memory that this block waits for)
   const uint32_t tb = uniform(s.tmem);
+  const int lo0 = min(min(s.lo[0], s.lo[1]), min(s.lo[2], s.lo[3])), hi0 = max(max(s.hi[0], s.hi[1]), max(s.hi[2], s.hi[3]));
+  const int lo1 = min(min(s.lo[4], s.lo[5]), min(s.lo[6], s.lo[7])), hi1 = max(max(s.hi[4], s.hi[5]), max(s.hi[6], s.hi[7]));
+  const int lo = uniform(min(lo0, lo1)), hi = uniform(max(hi0, hi1));
   TcWork work;
-  int lo = INT32_MAX, hi = 0;
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int a = min(min(s.lo[4 * i], s.lo[4 * i + 1]), min(s.lo[4 * i + 2], s.lo[4 * i + 3]));
-    const int z = max(max(s.hi[4 * i], s.hi[4 * i + 1]), max(s.hi[4 * i + 2], s.hi[4 * i + 3]));
-    work.from[i] = (int)uniform(z > 0 ? a / kKeys : 0), work.to[i] = (int)uniform((z + kKeys - 1) / kKeys);
-    lo = min(lo, a), hi = max(hi, z);
+  work.from0 = uniform(hi0 > 0 ? lo0 / kKeys : 0), work.to0 = uniform((hi0 + kKeys - 1) / kKeys);
+  work.from1 = uniform(hi1 > 0 ? lo1 / kKeys : 0), work.to1 = uniform((hi1 + kKeys - 1) / kKeys);
+  const bool one = work.to0 > 0, two = work.to1 > 0;
+  if (one && two) {                       // no key tile between them without a user: the rings go by key tiles
+    work.to0 = max(work.to0, work.from1);
+    work.to1 = max(work.to1, work.from0);
   }
-  const bool two = work.to[1] > 0;
-  if (two && work.to[0] > 0) {            // no key tile between them without a user: the rings go by key tiles
-    work.to[0] = max(work.to[0], work.from[1]);
-    work.to[1] = max(work.to[1], work.from[0]);
-  }
-  const int j_first = work.to[0] == 0 ? work.from[1] : two ? min(work.from[0], work.from[1]) : work.from[0];
-  const int j_last = max(work.to[0], work.to[1]);
+  const int j_first = !one ? work.from1 : !two ? work.from0 : min(work.from0, work.from1);
+  const int j_last = max(work.to0, work.to1);
 
-  if (warp == kLoadWarp) {
-    int loads = 0;
-    bool ok = true, q_loaded = false;
-    if (j_first < j_last) {
-      if (lane == 0) {
-        const int bytes = nt * p.rho * 128;
-        mbar_arrive_expect_tx(&s.q_full, (work.to[0] > 0 ? bytes : 0) + (two ? bytes : 0));
-        if (work.to[0] > 0) tma_load_4d(s.q[0], &tmQ, &s.q_full, 0, t0, 0, bh);
-        if (two) tma_load_4d(s.q[1], &tmQ, &s.q_full, 0, t0 + nt, 0, bh);
-      }
-      q_loaded = true;
+  if (warp == kLoadK || warp == kLoadV) {
+    const bool keys = warp == kLoadK;
+    uint64_t *full = keys ? s.k_full : s.v_full, *free = keys ? s.k_free : s.v_free;
+    uint8_t *ring = keys ? s.k[0] : s.v[0];
+    const CUtensorMap *map = keys ? &tmK : &tmV;
+    if (keys && lane == 0 && j_first < j_last) {
+      const int bytes = nt * p.rho * 128;
+      mbar_arrive_expect_tx(&s.q_full, (one ? bytes : 0) + (two ? bytes : 0));
+      if (one) tma_load_4d(s.q[0], &tmQ, &s.q_full, 0, t0, 0, bh);
+      if (two) tma_load_4d(s.q[1], &tmQ, &s.q_full, 0, t0 + nt, 0, bh);
     }
     // a lane loads a page's part of the tile
     const int page_rows = min(1 << p.page_shift, kKeys), boxes = kKeys / page_rows;
-    auto page_of = [&](int j) {           // out of range: zeros
+    auto page_of = [&](int j) {           // none: zeros
       const int key = j * kKeys + lane * page_rows;
       if (lane >= boxes || j >= j_last || key + page_rows <= lo || key >= hi) return -1;
       return paged_page(p, b, key);
     };
-    int raw = 0;
+    bool ok = true;
+    int loads = 0, raw = 0, raw_at = -1;  // raw: tiles that were cleared; the last of them, if it is not handed over
     int page = page_of(j_first);
-    for (int j = j_first; j < j_last; ++j, ++loads) {
+#pragma unroll 1
+    for (int j = j_first; j < j_last; ++j) {
       const int st = loads % kRing, round = loads / kRing;
       const int at = page >= 0 ? page : max(p.n_pages, 1);
       const int y = (j * kKeys + lane * page_rows) & ((1 << p.page_shift) - 1);
       page = page_of(j + 1);
-      if (round > 0) ok = warp_wait(&s.k_free[st], (round - 1) & 1, &s.wait);
+      if (round > 0) ok = warp_wait(&free[st], (round - 1) & 1, &s.wait);
       if (!ok) break;
-      if (lane == 0) mbar_arrive_expect_tx(&s.k_full[st], kTile);
-      __syncwarp();
-      if (lane < boxes) tma_load_4d(s.k[st] + lane * page_rows * 128, &tmK, &s.k_full[st], 0, y, kv, at);
-      if (round > 0) ok = warp_wait(&s.v_free[st], (round - 1) & 1, &s.wait);
       // values outside of what the rows see meet weights of 0, which an infinity or NaN would survive: zeros
-      const bool edge = j * kKeys < lo || (j + 1) * kKeys > hi;
-      uint64_t *bar = edge ? &s.v_raw : &s.v_full[st];
-      if (ok) {
-        if (lane == 0) mbar_arrive_expect_tx(bar, kTile);
-        __syncwarp();
-        if (lane < boxes) tma_load_4d(s.v[st] + lane * page_rows * 128, &tmV, bar, 0, y, kv, at);
-        if (edge) {
-          ok = warp_wait(bar, raw++ & 1, &s.wait);
-          for (int e = lane; ok && e < kKeys * 8; e += 32) {
-            const int key = j * kKeys + (e >> 3);
-            if (key < lo || key >= hi) reinterpret_cast<uint4 *>(s.v[st])[e] = make_uint4(0u, 0u, 0u, 0u);
-          }
-          fence_proxy_async();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&s.v_full[st]);
+      const bool edge = !keys && (j * kKeys < lo || (j + 1) * kKeys > hi);
+      uint64_t *bar = edge ? &s.v_raw : &full[st];
+      if (lane == 0) mbar_arrive_expect_tx(bar, kTile);
+      __syncwarp();
+      if (lane < boxes) tma_load_4d(ring + st * kTile + lane * page_rows * 128, map, bar, 0, y, kv, at);
+      ++loads;
+      if (edge) {
+        raw_at = loads - 1;
+        ok = warp_wait(bar, raw++ & 1, &s.wait);
+        if (!ok) break;
+        for (int e = lane; e < kKeys * 8; e += 32) {
+          const int key = j * kKeys + (e >> 3);
+          if (key < lo || key >= hi) reinterpret_cast<uint4 *>(ring + st * kTile)[e] = make_uint4(0u, 0u, 0u, 0u);
         }
-      }
-      if (!ok) {
-        ++loads;
-        break;
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full[st]);
+        raw_at = -1;
       }
     }
     if (lane == 0) {                      // nothing in flight at the block's end
-      if (q_loaded) mbar_wait_teardown(&s.q_full, 0, p.status);
-      if (raw > 0) mbar_wait_teardown(&s.v_raw, (raw - 1) & 1, p.status);
-      for (int i = max(0, loads - kRing); i < loads; ++i) {
-        mbar_wait_teardown(&s.k_full[i % kRing], (i / kRing) & 1, p.status);
-        if (ok) mbar_wait_teardown(&s.v_full[i % kRing], (i / kRing) & 1, p.status);
-      }
+      if (keys && j_first < j_last) mbar_wait_teardown(&s.q_full, 0, p.status);
+      if (raw_at >= 0) mbar_wait_teardown(&s.v_raw, (raw - 1) & 1, p.status);
+      for (int i = max(0, loads - kRing); i < loads; ++i)
+        if (i != raw_at) mbar_wait_teardown(&full[i % kRing], (i / kRing) & 1, p.status);
     }
     __syncwarp();
-  } else if (warp == kIssueWarp) {
-    const uint32_t id_s = idesc_bf16_f32(128, kKeys, 0), id_o = idesc_bf16_f32(128, 64, 1);
-    bool ok = j_first >= j_last || warp_wait(&s.q_full, 0, &s.wait);
-    // (j, x) of the next scores to issue and of the next P V
-    int sj = j_first, sx = work.has(0, j_first) ? 0 : 1, su = 0, sn[2] = {0, 0};
+  } else if (warp == kScoreWarp || warp == kValueWarp) {
+    // The tiles' scores (values) in their order; j, x: the present ones
+    const uint64_t rest = sdesc_sw128(0, 16, 1024);
+    auto desc = [&](const uint8_t *at) { return rest | (uint64_t)uniform(smem_u32(at) >> 4); };   // (below 2^18)
     auto step = [&](int &j, int &x) {
       do {
         if (++x == 2) x = 0, ++j;
       } while (j < j_last && !work.has(x, j));
     };
-    auto scores = [&]() {
-      if (sj >= j_last) return true;
-      const int st = (sj - j_first) % kRing;
-      if (!warp_wait(&s.k_full[st], ((sj - j_first) / kRing) & 1, &s.wait)) return false;
-      const uint64_t qd = sdesc_sw128(smem_u32(s.q[sx]), 16, 1024), kd = sdesc_sw128(smem_u32(s.k[st]), 16, 1024);
-      const uint32_t to_s = tb + su % 3 * 128;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) umma_ss_warp(to_s, qd + 2 * k, kd + 2 * k, id_s, k > 0);
-      // (a barrier by the tile's own count: its warps see every phase of it)
-      umma_commit_warp(&s.s_full[sx][(sx ? sn[1]++ : sn[0]++) % 3]);
-      const int j = sj;
-      step(sj, sx), ++su;
-      if (sj != j) umma_commit_warp(&s.k_free[st]);
-      return true;
-    };
-    ok = ok && scores() && scores();
-    int j = j_first, y = work.has(0, j_first) ? 0 : 1;
-    bool fresh[2] = {true, true};
+    int j = j_first, x = work.has(0, j_first) ? 0 : 1, st = 0, round = 0;
+    bool ok = true, fresh = true;         // fresh: the ring's tile is not known to be there
+    if (warp == kScoreWarp) {
+      const uint32_t id = idesc_bf16_f32(128, kKeys, 0);
+      int n0 = 0, n1 = 0;                 // scores of each tile
+      int back_j = j, back_x = x, back0 = 0, back1 = 0;   // the same three scores before
+      if (j < j_last) ok = warp_wait(&s.q_full, 0, &s.wait);
 #pragma unroll 1
-    for (int u = 0; j < j_last && ok; ++u) {
-      ok = scores();
-      const int st = (j - j_first) % kRing;
-      ok = ok && warp_wait(&s.v_full[st], ((j - j_first) / kRing) & 1, &s.wait) &&
-           warp_wait(&s.p_full[u % 3], (u / 3) & 1, &s.wait);
-      if (!ok) break;
-      tc_fence_after();
-      const uint64_t vd = sdesc_sw128(smem_u32(s.v[st]), 16, 1024);
-      const uint32_t from_p = tb + u % 3 * 128, to_o = tb + kColO + 64 * y;
+      for (int u = 0, place = 0; j < j_last && ok; ++u) {
+        if (fresh) ok = warp_wait(&s.k_full[st], round & 1, &s.wait);
+        if (u >= 3) {                     // the place's P has been read
+          ok = ok && warp_wait(&s.o_done[back_x], (back_x ? back1 : back0) & 1, &s.wait);
+          back0 += 1 - back_x, back1 += back_x;
+          step(back_j, back_x);
+        }
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t qd = desc(s.q[x]), kd = desc(s.k[st]);
+        const uint32_t to_s = uniform(tb + place * 128);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) umma_ts_warp(to_o, from_p + 8 * k, vd + 128 * k, id_o, k > 0 || !fresh[y]);
-      umma_commit_warp(&s.o_done[y]);
-      fresh[y] = false;
-      const int before = j;
-      step(j, y);
-      if (j != before) umma_commit_warp(&s.v_free[st]);
+        for (int k = 0; k < 4; ++k) umma_ss_warp(to_s, qd + 2 * k, kd + 2 * k, id, k > 0);
+        // (a barrier by the tile's own count: its warps see every phase of it)
+        umma_commit_warp(&s.s_full[x][(x ? n1 : n0) % 3]);
+        n0 += 1 - x, n1 += x;
+        const int before = j;
+        step(j, x);
+        fresh = j != before;
+        if (fresh) {
+          umma_commit_warp(&s.k_free[st]);
+          if (++st == kRing) st = 0, ++round;
+        }
+        if (++place == 3) place = 0;
+      }
+    } else {
+      const uint32_t id = idesc_bf16_f32(128, 64, 1);
+      uint32_t begun = 0u;                // bit x: O of tile x holds something
+#pragma unroll 1
+      for (int u = 0, place = 0; j < j_last && ok; ++u) {
+        if (fresh) ok = warp_wait(&s.v_full[st], round & 1, &s.wait);
+        ok = ok && warp_wait(&s.p_full[place], (u / 3) & 1, &s.wait);
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t vd = desc(s.v[st]);
+        const uint32_t from_p = uniform(tb + place * 128), to_o = uniform(tb + kColO + 64 * x), more = begun >> x & 1u;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) umma_ts_warp(to_o, from_p + 8 * k, vd + 128 * k, id, k > 0 ? 1u : more);
+        umma_commit_warp(&s.o_done[x]);
+        begun |= 1u << x;
+        const int before = j;
+        step(j, x);
+        fresh = j != before;
+        if (fresh) {
+          umma_commit_warp(&s.v_free[st]);
+          if (++st == kRing) st = 0, ++round;
+        }
+        if (++place == 3) place = 0;
+      }
     }
-    umma_commit_warp(&s.drain);
-    if (lane == 0) mbar_wait_teardown(&s.drain, 0, p.status);
+    uint64_t *drain = &s.drain[warp == kValueWarp];
+    umma_commit_warp(drain);
+    if (lane == 0) mbar_wait_teardown(drain, 0, p.status);
     __syncwarp();
   } else {
     const uint32_t tm = tb + ((uint32_t)(32 * (warp & 3)) << 16), to_o = tm + kColO + 64 * x;
@@ -290,7 +308,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
     bool ok = true;
     int n = 0;                                               // the tile's key tiles so far
 #pragma unroll 1
-    for (int j = work.from[x]; j < work.to[x]; ++j, ++n) {
+    for (int j = work.from(x); j < work.to(x); ++j, ++n) {
       const int u = work.unit(x, j), j0 = j * kKeys;
       const uint32_t at = tm + u % 3 * 128;
       ok = warp_wait(&s.s_full[x][n % 3], (n / 3) & 1, &s.wait);
@@ -425,7 +443,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == kIssueWarp) tmem_dealloc(tb, 512);
+  if (warp == kScoreWarp) tmem_dealloc(tb, 512);
 }
 
 oal_status tc_map(CUtensorMap *m, const void *ptr, const cuuint64_t (&dims)[4], const cuuint64_t (&strides)[3],
