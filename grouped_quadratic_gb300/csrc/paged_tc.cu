@@ -9,10 +9,9 @@
 // One warp loads keys and one values (a page is a box of TMA's, or part of one),
 // one issues the first product and one the second: a wait on a barrier that is
 // complete costs an issuing warp about 130 cycles beside MMAs that read shared
-// memory, and one warp for both took 1,320 cycles for the 512 of its MMAs.  Three
-// places for scores go round between the two tiles, so that the next scores of
-// a tile are there when its warps have finished the ones before; P lies in the
-// place of its scores.
+// memory, and one warp for both took 1,320 cycles for the 512 of its MMAs.  P lies
+// beside S, so that the next scores of a tile come as soon as its warps have
+// taken the present ones into registers.
 //
 // m is the row's maximum at some time, at most 2^8 below the present one: O is
 // multiplied by a power of two (through registers) only when it falls behind
@@ -34,13 +33,13 @@ constexpr int kLoadK = 8, kScoreWarp = 9, kValueWarp = 10, kLoadV = 11;
 constexpr int kKeys = 128;
 constexpr int kTile = 128 * 128;          // bytes of 128 rows of 64
 constexpr int kRing = 4;                  // key tiles in flight, of K and of V
-constexpr uint32_t kColO = 384;           // tensor memory: three places of 128 for scores, then O of each tile
+constexpr uint32_t kColP = 256, kColO = 384;   // tensor memory: S of each tile (128 columns), P (64), O (64)
 constexpr float kBehind = 8.f;
 
 struct TcSmem {
   uint8_t q[2][kTile], k[kRing][kTile], v[kRing][kTile];
   uint64_t q_full, k_full[kRing], k_free[kRing], v_full[kRing], v_free[kRing], v_raw;
-  uint64_t s_full[2][3], p_full[3], o_done[2], drain[2];
+  uint64_t s_full[2], s_read[2], p_full[2], o_done[2], drain[2];
   int lo[8], hi[8];                       // keys that the rows of each warp see
   uint32_t tmem;
   WaitState wait;
@@ -86,8 +85,8 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return r;
 }
 
-// The key tiles of the block's two tiles of rows, and the order of their scores:
-// by key tile, first tile first.
+// The key tiles of the block's two tiles of rows, whose products are issued by
+// key tile, first tile first.
 // (Selected, not indexed: an index would put them into local memory, and what
 // is loaded from there is not known to be the same in all lanes.)
 struct TcWork {
@@ -95,10 +94,6 @@ struct TcWork {
   __device__ __forceinline__ int from(int x) const { return x ? from1 : from0; }
   __device__ __forceinline__ int to(int x) const { return x ? to1 : to0; }
   __device__ __forceinline__ bool has(int x, int j) const { return j >= from(x) && j < to(x); }
-  // the place in that order of tile x's scores with key tile j
-  __device__ __forceinline__ int unit(int x, int j) const {
-    return min(max((x ? j + 1 : j) - from0, 0), to0 - from0) + min(max(j - from1, 0), to1 - from1);
-  }
 };
 
 // kExtra: scores are capped or take a distance.
@@ -120,8 +115,11 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
       mbar_init(&s.v_full[i], 1), mbar_init(&s.v_free[i], 1);
     }
     mbar_init(&s.v_raw, 1);
-    for (int i = 0; i < 3; ++i) mbar_init(&s.s_full[0][i], 1), mbar_init(&s.s_full[1][i], 1), mbar_init(&s.p_full[i], 4);
-    for (int i = 0; i < 2; ++i) mbar_init(&s.o_done[i], 1), mbar_init(&s.drain[i], 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s.s_full[i], 1), mbar_init(&s.s_read[i], 4);
+      mbar_init(&s.p_full[i], 4), mbar_init(&s.o_done[i], 1);
+      mbar_init(&s.drain[i], 1);
+    }
     fence_mbar_init();
   }
   pdl_wait();
@@ -238,24 +236,19 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
     if (warp == kScoreWarp) {
       const uint32_t id = idesc_bf16_f32(128, kKeys, 0);
       int n0 = 0, n1 = 0;                 // scores of each tile
-      int back_j = j, back_x = x, back0 = 0, back1 = 0;   // the same three scores before
       if (j < j_last) ok = warp_wait(&s.q_full, 0, &s.wait);
 #pragma unroll 1
-      for (int u = 0, place = 0; j < j_last && ok; ++u) {
+      while (j < j_last && ok) {
+        const int n = x ? n1 : n0;
         if (fresh) ok = warp_wait(&s.k_full[st], round & 1, &s.wait);
-        if (u >= 3) {                     // the place's P has been read
-          ok = ok && warp_wait(&s.o_done[back_x], (back_x ? back1 : back0) & 1, &s.wait);
-          back0 += 1 - back_x, back1 += back_x;
-          step(back_j, back_x);
-        }
+        if (n > 0) ok = ok && warp_wait(&s.s_read[x], (n - 1) & 1, &s.wait);
         if (!ok) break;
         tc_fence_after();
         const uint64_t qd = desc(s.q[x]), kd = desc(s.k[st]);
-        const uint32_t to_s = uniform(tb + place * 128);
+        const uint32_t to_s = uniform(tb + 128 * x);
 #pragma unroll
         for (int k = 0; k < 4; ++k) umma_ss_warp(to_s, qd + 2 * k, kd + 2 * k, id, k > 0);
-        // (a barrier by the tile's own count: its warps see every phase of it)
-        umma_commit_warp(&s.s_full[x][(x ? n1 : n0) % 3]);
+        umma_commit_warp(&s.s_full[x]);
         n0 += 1 - x, n1 += x;
         const int before = j;
         step(j, x);
@@ -264,23 +257,23 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
           umma_commit_warp(&s.k_free[st]);
           if (++st == kRing) st = 0, ++round;
         }
-        if (++place == 3) place = 0;
       }
     } else {
       const uint32_t id = idesc_bf16_f32(128, 64, 1);
-      uint32_t begun = 0u;                // bit x: O of tile x holds something
+      int n0 = 0, n1 = 0;                 // products of each tile
 #pragma unroll 1
-      for (int u = 0, place = 0; j < j_last && ok; ++u) {
+      while (j < j_last && ok) {
+        const int n = x ? n1 : n0;
         if (fresh) ok = warp_wait(&s.v_full[st], round & 1, &s.wait);
-        ok = ok && warp_wait(&s.p_full[place], (u / 3) & 1, &s.wait);
+        ok = ok && warp_wait(&s.p_full[x], n & 1, &s.wait);
         if (!ok) break;
         tc_fence_after();
         const uint64_t vd = desc(s.v[st]);
-        const uint32_t from_p = uniform(tb + place * 128), to_o = uniform(tb + kColO + 64 * x), more = begun >> x & 1u;
+        const uint32_t from_p = uniform(tb + kColP + 64 * x), to_o = uniform(tb + kColO + 64 * x), more = n > 0;
 #pragma unroll
         for (int k = 0; k < 8; ++k) umma_ts_warp(to_o, from_p + 8 * k, vd + 128 * k, id, k > 0 ? 1u : more);
         umma_commit_warp(&s.o_done[x]);
-        begun |= 1u << x;
+        n0 += 1 - x, n1 += x;
         const int before = j;
         step(j, x);
         fresh = j != before;
@@ -288,7 +281,6 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
           umma_commit_warp(&s.v_free[st]);
           if (++st == kRing) st = 0, ++round;
         }
-        if (++place == 3) place = 0;
       }
     }
     uint64_t *drain = &s.drain[warp == kValueWarp];
@@ -309,15 +301,17 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
     int n = 0;                                               // the tile's key tiles so far
 #pragma unroll 1
     for (int j = work.from(x); j < work.to(x); ++j, ++n) {
-      const int u = work.unit(x, j), j0 = j * kKeys;
-      const uint32_t at = tm + u % 3 * 128;
-      ok = warp_wait(&s.s_full[x][n % 3], (n / 3) & 1, &s.wait);
+      const int j0 = j * kKeys;
+      ok = warp_wait(&s.s_full[x], n & 1, &s.wait);
       if (!ok) break;
       tc_fence_after();
       uint32_t w[128];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_ld32(at + 32 * c, w + 32 * c);
+      for (int c = 0; c < 4; ++c) tmem_ld32(tm + 128 * x + 32 * c, w + 32 * c);
       tmem_wait_ld();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s.s_read[x]);            // the next scores may come
       if (kExtra) {
 #pragma unroll
         for (int e = 0; e < 128; ++e) {
@@ -345,6 +339,10 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
       }
       const float now = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
       const bool behind = (now - m) * by > kBehind;          // (from -inf: always)
+      // the product before is done: O may change, and P be written over
+      if (n > 0) ok = warp_wait(&s.o_done[x], (n - 1) & 1, &s.wait);
+      if (!ok) break;
+      tc_fence_after();
       if (__any_sync(0xffffffffu, behind)) {
         const float keep = behind ? ex2((m - now) * by) : 1.f;
         if (behind) m = now;
@@ -355,9 +353,6 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
           sum[c] = pair(a * keep, z * keep);
         }
         if (n > 0) {
-          ok = warp_wait(&s.o_done[x], (n - 1) & 1, &s.wait);
-          if (!ok) break;
-          tc_fence_after();
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {
             uint32_t o[16];
@@ -383,15 +378,12 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
           sum[e >> 1 & 1] = add2(sum[e >> 1 & 1], pair(a, z));
           pk[e >> 1] = pack_bf16x2(a, z);
         }
-        tmem_st16(at + 16 * c, pk);
+        tmem_st16(tm + kColP + 64 * x + 16 * c, pk);
       }
-      // (every time, so that the phases stay in step)
-      if (n > 0) ok = warp_wait(&s.o_done[x], (n - 1) & 1, &s.wait);
-      if (!ok) break;
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&s.p_full[u % 3]);
+      if (lane == 0) mbar_arrive(&s.p_full[x]);
     }
     float f[4];
     unpair(sum[0], f[0], f[1]), unpair(sum[1], f[2], f[3]);
