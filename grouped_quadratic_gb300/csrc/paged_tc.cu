@@ -53,15 +53,28 @@ __device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, u
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
       : "memory");
 }
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t *r) {
+// 32 columns of the thread's row, and their maximum (of those that are numbers)
+__device__ __forceinline__ float tmem_ld32_max(uint32_t taddr, uint32_t *r) {
+  float top;
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
-      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      "tcgen05.ld.red.sync.aligned.32x32b.x32.max.f32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,"
+      "%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, %32, [%33];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
         "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
         "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=f"(top)
       : "r"(taddr));
+  return top;
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t *r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
 }
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -306,8 +319,9 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
       if (!ok) break;
       tc_fence_after();
       uint32_t w[128];
+      float top[4];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_ld32(tm + 128 * x + 32 * c, w + 32 * c);
+      for (int c = 0; c < 4; ++c) top[c] = tmem_ld32_max(tm + 128 * x + 32 * c, w + 32 * c);
       tmem_wait_ld();
       tc_fence_before();
       __syncwarp();
@@ -326,23 +340,23 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
           w[e] = __float_as_uint(fmaf(-slope, (float)abs(seq.past + t - j0 - e), f));
         }
       }
-      if (!__all_sync(0xffffffffu, see0 <= j0 && see1 >= j0 + kKeys)) {
+      const bool cut = !__all_sync(0xffffffffu, see0 <= j0 && see1 >= j0 + kKeys);
+      if (cut) {
         const uint32_t off = (uint32_t)(see0 - j0), len = (uint32_t)max(see1 - see0, 0);
 #pragma unroll
         for (int e = 0; e < 128; ++e) w[e] = (uint32_t)e - off < len ? w[e] : 0xFF800000u;
       }
-      float top[4] = {m, m, m, m};
+      if (kExtra || cut) {
 #pragma unroll
-      for (int e = 0; e < 128; e += 8) {
+        for (int c = 0; c < 4; ++c) {
+          top[c] = -INFINITY;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) top[c] = fmaxf(top[c], fmaxf(__uint_as_float(w[e + 2 * c]), __uint_as_float(w[e + 2 * c + 1])));
+          for (int e = 0; e < 32; e += 2)
+            top[c] = fmaxf(top[c], fmaxf(__uint_as_float(w[32 * c + e]), __uint_as_float(w[32 * c + e + 1])));
+        }
       }
-      const float now = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+      const float now = fmaxf(m, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])));
       const bool behind = (now - m) * by > kBehind;          // (from -inf: always)
-      // the product before is done: O may change, and P be written over
-      if (n > 0) ok = warp_wait(&s.o_done[x], (n - 1) & 1, &s.wait);
-      if (!ok) break;
-      tc_fence_after();
       if (__any_sync(0xffffffffu, behind)) {
         const float keep = behind ? ex2((m - now) * by) : 1.f;
         if (behind) m = now;
@@ -353,6 +367,9 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
           sum[c] = pair(a * keep, z * keep);
         }
         if (n > 0) {
+          ok = warp_wait(&s.o_done[x], (n - 1) & 1, &s.wait);
+          if (!ok) break;
+          tc_fence_after();
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {
             uint32_t o[16];
@@ -369,17 +386,23 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
       // weights, rounded to bf16 because the tensor cores take both factors in the values' type
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        uint32_t pk[16];
 #pragma unroll
         for (int e = 0; e < 32; e += 2) {
           float a, z;
           unpair(fma2(pair(__uint_as_float(w[32 * c + e]), __uint_as_float(w[32 * c + e + 1])), by2, base2), a, z);
           a = ex2(a), z = ex2(z);
           sum[e >> 1 & 1] = add2(sum[e >> 1 & 1], pair(a, z));
-          pk[e >> 1] = pack_bf16x2(a, z);
+          w[16 * c + (e >> 1)] = pack_bf16x2(a, z);
         }
-        tmem_st16(tm + kColP + 64 * x + 16 * c, pk);
+        if (c == 1) {                       // the product before is done: P may be written over
+          if (n > 0) ok = warp_wait(&s.o_done[x], (n - 1) & 1, &s.wait);
+          if (!ok) break;
+          tc_fence_after();
+          tmem_st32(tm + kColP + 64 * x, w);
+        }
       }
+      if (!ok) break;
+      tmem_st32(tm + kColP + 64 * x + 32, w + 32);
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
