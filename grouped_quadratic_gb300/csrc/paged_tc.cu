@@ -159,6 +159,10 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
     const int hi = __reduce_max_sync(0xffffffffu, a < z ? z : 0);
     if (lane == 0) s.lo[warp] = lo, s.hi[warp] = hi;
   }
+  // rows behind the last token's: scores of 0
+  for (int e = nt * p.rho * 8 + tid; e < 128 * 8; e += kTcThreads)
+    reinterpret_cast<uint4 *>(s.q[0])[e] = reinterpret_cast<uint4 *>(s.q[1])[e] = make_uint4(0u, 0u, 0u, 0u);
+  fence_proxy_async();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -307,7 +311,8 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
     const float cap_in = kExtra && p.cap > 0.f ? 2.f * kLog2e * p.scale / p.cap : 0.f, cap_out = p.cap * kLog2e;
     const float slope = kExtra && live && p.slopes ? p.slopes[h] * kLog2e : 0.f;
     const float by = kExtra ? 1.f : scale2;                // of what is held as a score
-    const int see0 = max(sees.x, from), see1 = min(sees.y, to);
+    // (a row that is none is not to make the others look at masks)
+    const int see0 = live ? max(sees.x, from) : 0, see1 = live ? min(sees.y, to) : INT32_MAX;
     float m = -INFINITY;
     uint64_t sum[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
     bool ok = true;
