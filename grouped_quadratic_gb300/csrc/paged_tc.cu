@@ -66,16 +66,6 @@ __device__ __forceinline__ float tmem_ld32_max(uint32_t taddr, uint32_t *r) {
       : "r"(taddr));
   return top;
 }
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t *r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
-      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-      : "memory");
-}
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -399,15 +389,14 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
           sum[e >> 1 & 1] = add2(sum[e >> 1 & 1], pair(a, z));
           w[16 * c + (e >> 1)] = pack_bf16x2(a, z);
         }
-        if (c == 1) {                       // the product before is done: P may be written over
+        if (c == 0) {                       // the product before is done: P may be written over
           if (n > 0) ok = warp_wait(&s.o_done[x], (n - 1) & 1, &s.wait);
           if (!ok) break;
           tc_fence_after();
-          tmem_st32(tm + kColP + 64 * x, w);
         }
+        tmem_st16(tm + kColP + 64 * x + 16 * c, *reinterpret_cast<uint32_t (*)[16]>(w + 16 * c));
       }
       if (!ok) break;
-      tmem_st32(tm + kColP + 64 * x + 32, w + 32);
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
