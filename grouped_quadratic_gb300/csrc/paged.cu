@@ -13,41 +13,68 @@ oal_status launch_paged_tc(const PagedArgs &p, cudaStream_t stream);
 
 namespace {
 
-// Joins the rows of split keys, one warp a row: y = sum_s 2^{m_s - m} o_s /
-// sum_s 2^{m_s - m} l_s over the splits that the row sees something of, in
-// their order.
-constexpr int kJoinThreads = 128;
-template <typename T>
-__global__ void __launch_bounds__(kJoinThreads)
+// Joins the rows of split keys, a block a row: y = sum_s 2^{m_s - m} o_s /
+// sum_s 2^{m_s - m} l_s over the splits that the row sees something of.  A warp
+// takes every kJoinWarps-th split, in order, and the warps' sums are added in
+// order: the same bits every time.  Eight splits a warp are one step, 2 us with
+// the launch, and each further step costs another 2: 129 splits took 10 us with
+// four warps.
+template <typename T, int kJoinWarps>
+__global__ void __launch_bounds__(32 * kJoinWarps)
 paged_join_kernel(PagedArgs p) {
   pdl_trigger();
   pdl_wait();
-  const int lane = threadIdx.x & 31;
+  __shared__ float s_m[kJoinWarps], s_l[kJoinWarps];
+  __shared__ float2 s_y[kJoinWarps][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int bh = blockIdx.y, b = bh / p.Hkv, kv = bh % p.Hkv;
-  const int r = blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5);
-  if (r >= p.T * p.rho) return;
+  const int r = blockIdx.x;
   const PagedSeq seq = paged_seq(p, b, false);
   const int t = r / p.rho, h = kv * p.rho + r % p.rho;
   if (t >= seq.n) return;
   const int2 sees = paged_sees(p, seq, b, t);
   const int base = paged_base(p, seq, r / p.tile_rows * p.tile_rows / p.rho);
   float2 y = make_float2(0.f, 0.f);
+  float m = -INFINITY, l = 0.f;
   if (sees.y > 0) {
     const int s0 = (sees.x - base) / p.split_keys, s1 = (sees.y - 1 - base) / p.split_keys;
     const size_t rows = (size_t)p.T * p.rho;
     const size_t first = (size_t)bh * p.splits * rows + r;
-    float m = -INFINITY;
-    for (int s = s0 + lane; s <= s1; s += 32) m = fmaxf(m, p.part_ml[first + s * rows].x);
+    for (int s = s0 + warp; s <= s1; s += 8 * kJoinWarps) {   // eight splits' loads in flight
+      float2 ml[8], o[8];
+      float top = m;
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-    if (m == -INFINITY) m = 0.f;
-    float l = 0.f;
-#pragma unroll 4
-    for (int s = s0; s <= s1; ++s) {
-      const float2 ml = p.part_ml[first + s * rows];
-      const float2 o = *reinterpret_cast<const float2 *>(p.part_o + (first + s * rows) * 64 + 2 * lane);
-      const float w = exp2f(ml.x - m);
-      l = fmaf(w, ml.y, l), y.x = fmaf(w, o.x, y.x), y.y = fmaf(w, o.y, y.y);
+      for (int e = 0; e < 8; ++e) {
+        const int at = min(s + e * kJoinWarps, s1);
+        ml[e] = p.part_ml[first + at * rows];
+        o[e] = *reinterpret_cast<const float2 *>(p.part_o + (first + at * rows) * 64 + 2 * lane);
+        top = fmaxf(top, ml[e].x);
+      }
+      const float zero = top == -INFINITY ? 0.f : top, keep = exp2f(m - zero);
+      l *= keep, y.x *= keep, y.y *= keep, m = top;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        if (s + e * kJoinWarps > s1) break;
+        const float w = exp2f(ml[e].x - zero);
+        l = fmaf(w, ml[e].y, l), y.x = fmaf(w, o[e].x, y.x), y.y = fmaf(w, o[e].y, y.y);
+      }
+    }
+  }
+  if (lane == 0) s_m[warp] = m, s_l[warp] = l;
+  s_y[warp][lane] = y;
+  __syncthreads();
+  if (warp != 0) return;
+  if (sees.y > 0) {
+    float top = s_m[0];
+#pragma unroll
+    for (int w = 1; w < kJoinWarps; ++w) top = fmaxf(top, s_m[w]);
+    if (top == -INFINITY) top = 0.f;
+    l = 0.f, y = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) {
+      const float f = exp2f(s_m[w] - top);
+      const float2 o = s_y[w][lane];
+      l = fmaf(f, s_l[w], l), y.x = fmaf(f, o.x, y.x), y.y = fmaf(f, o.y, y.y);
     }
     y.x /= l, y.y /= l;
     if (__any_sync(0xffffffffu, !(fabsf(y.x) + fabsf(y.y) < INFINITY)))
@@ -60,12 +87,11 @@ paged_join_kernel(PagedArgs p) {
 }  // namespace
 
 oal_status launch_paged_join(const PagedArgs &p, int is_bf16, cudaStream_t stream) {
-  const unsigned rows = kJoinThreads / 32;
-  const dim3 grid((unsigned)(((long long)p.T * p.rho + rows - 1) / rows), (unsigned)(p.B * p.Hkv));
-  if (is_bf16)
-    launch_pdl(paged_join_kernel<__nv_bfloat16>, grid, dim3(kJoinThreads), 0, stream, p);
-  else
-    launch_pdl(paged_join_kernel<float>, grid, dim3(kJoinThreads), 0, stream, p);
+  const dim3 grid((unsigned)(p.T * p.rho), (unsigned)(p.B * p.Hkv));
+  const bool many = p.splits > 32;        // more than four warps take in one step
+  auto kernel = is_bf16 ? (many ? paged_join_kernel<__nv_bfloat16, 16> : paged_join_kernel<__nv_bfloat16, 4>)
+                        : (many ? paged_join_kernel<float, 16> : paged_join_kernel<float, 4>);
+  launch_pdl(kernel, grid, dim3(many ? 512 : 128), 0, stream, p);
   return oal_after_launch("paged_join_kernel", stream);
 }
 
@@ -86,6 +112,14 @@ constexpr int kSplitLeast = 256;          // keys of a split at least
 // cut: as many as fill the GPU, where the tiles alone do not.  The grid is made
 // for the longest sequence that the table has room for; blocks behind a
 // sequence's end return at once.
+//
+// paged_rows_kernel, three blocks of which fit an SM: with few units (pairs of
+// sequence and KV head) about one wave, four blocks per SM of which a ragged
+// batch leaves some empty; with many, enough waves to even out their ends.  4,
+// 8 and 16 blocks per SM, us: 16 sequences of 8 heads with 2048 to 8192 keys
+// 35.3, 37.8, 42.2; 8 with 32768 at most 57.8, 60.7, 66.4; 32 with 5 drafted
+// tokens on 3000 43.9, 47.3, 52.5; but 64 with 8192 129, 117.8, 116.6, all of
+// one length 209, 180, 168.
 static long long plan_tiles(PagedArgs &p, int is_bf16) {
   const long long rows = (long long)p.T * p.rho, units = (long long)p.B * p.Hkv;
   long long want;                         // blocks
@@ -94,7 +128,7 @@ static long long plan_tiles(PagedArgs &p, int is_bf16) {
     want = 152 * 4;
   } else if (is_bf16) {
     p.tile_rows = rows <= 16 ? 16 : 32;
-    want = 152 * 2 * 4;
+    want = units * ((rows + p.tile_rows - 1) / p.tile_rows) <= 2 * 152 ? 152 * 4 : 152 * 16;
   } else {
     p.tile_rows = rows <= 8 ? 8 : 32;
     want = 152 * 4 * 2;

@@ -16,7 +16,7 @@ namespace {
 
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr int kGroup = 32;                // keys of a warp's step
-constexpr int kStages = 3;
+constexpr int kStages = 2;                // (three blocks per SM then; 3 and 4 leave two and one: 64 sequences 124, 143, 210 us)
 constexpr int kGroupBytes = kGroup * 128; // of K, and of V
 constexpr int kRing = kStages * 2 * kGroupBytes;
 
@@ -49,7 +49,7 @@ __device__ __forceinline__ uint32_t pack(float lo, float hi) {
 
 // kExtra: scores are capped or take a distance.
 template <int kTiles, bool kExtra>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 3)
 paged_rows_kernel(PagedArgs p) {
   pdl_trigger();
   pdl_wait();
@@ -173,25 +173,43 @@ paged_rows_kernel(PagedArgs p) {
 #pragma unroll
     for (int i = 0; i < kTiles; ++i) {
       float top[2] = {m[i][0], m[i][1]};
+      if (kExtra && p.cap > 0.f) {          // cap tanh(x) = cap - 2 cap / (e^{2 x} + 1)
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float w;
+            asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(w) : "f"(s[i][n][e] * cap_in));
+            asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(w) : "f"(w + 1.f));
+            s[i][n][e] = fmaf(-2.f * cap_out, w, cap_out);
+          }
+      } else {
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[i][n][e] *= scale2;
+      }
+      if (kExtra) {                         // (one conversion a row: those take the exponentials' units)
+        const float far[2] = {(float)(row_at[i][0] - j0 - 2 * c), (float)(row_at[i][1] - j0 - 2 * c)};
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            s[i][n][e] = fmaf(-slope[i][e >> 1], fabsf(far[e >> 1] - (float)(8 * n + (e & 1))), s[i][n][e]);
+      }
+      if (!whole) {
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int u = e >> 1, j = j0 + 8 * n + 2 * c + (e & 1);
+            if (!(j >= max(row_lo[i][u], k0) && j < min(row_hi[i][u], k1))) s[i][n][e] = -INFINITY;
+          }
+      }
 #pragma unroll
       for (int n = 0; n < 4; ++n)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int u = e >> 1, j = j0 + 8 * n + 2 * c + (e & 1);
-          float x = s[i][n][e];
-          if (kExtra && p.cap > 0.f) {      // cap tanh(x) = cap - 2 cap / (e^{2 x} + 1)
-            float w;
-            asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(w) : "f"(x * cap_in));
-            asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(w) : "f"(w + 1.f));
-            x = fmaf(-2.f * cap_out, w, cap_out);
-          } else {
-            x *= scale2;
-          }
-          if (kExtra) x = fmaf(-slope[i][u], (float)abs(row_at[i][u] - j), x);
-          if (!whole && !(j >= max(row_lo[i][u], k0) && j < min(row_hi[i][u], k1))) x = -INFINITY;
-          s[i][n][e] = x;
-          top[u] = fmaxf(top[u], x);
-        }
+        for (int e = 0; e < 4; ++e) top[e >> 1] = fmaxf(top[e >> 1], s[i][n][e]);
       float keep[2];
       bool grew = false;
 #pragma unroll
