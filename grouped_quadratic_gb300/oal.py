@@ -17,7 +17,9 @@ A call given a `stream` waits there for the tensors that it makes itself (on the
 current stream); tensors given to it have to be ready on `stream`.
 """
 import ctypes
+import functools
 import os
+import struct
 
 import torch
 
@@ -598,13 +600,16 @@ def oal_rope_plan(freq, axes=None, device="cuda"):
 
 def _rows(t, name, dtype, shape, dev):
     """The strides of a tensor whose rows of 64 are contiguous."""
-    if t.dtype != dtype or t.shape != shape or t.device != dev:
+    if not (t.dtype is dtype and t.shape == shape and t.device == dev):
         raise OALError(OAL_ERR_INVALID_ARG, "%s must be %s %s on %s (got %s %s on %s)"
                        % (name, dtype, tuple(shape), dev, t.dtype, tuple(t.shape), t.device))
     s = t.stride()
     _need(s[3] == 1, "rows of %s must be contiguous" % name)
     # (the stride of a dimension of one says nothing)
-    return s if min(shape) > 1 else tuple(x if n > 1 else 0 for x, n in zip(s, shape))
+    return s[:3] if min(shape) > 1 else tuple(x if n > 1 else 0 for x, n in zip(s[:3], shape))
+
+
+_strides6, _strides9 = struct.Struct("6q").pack, struct.Struct("9q").pack
 
 
 def _need_positions(positions, B, T, past, lengths, plan, dev):
@@ -632,9 +637,9 @@ def oal_rope(Q, K, plan, positions=None, past=None, lengths=None, form=OAL_ROPE_
     _need(Q.dim() == 4 and (K is None or K.dim() == 4), "Q and K must have 4 dimensions")
     _need(plan is not None, "plan is needed")
     B, Hq, T, d = Q.shape
-    dt, dev, Hkv = _dtype_code(Q), Q.device, 0 if K is None else K.shape[1]
-    sq = _rows(Q, "Q", Q.dtype, (B, Hq, T, d), dev)
-    sk = sq if K is None else _rows(K, "K", Q.dtype, (B, Hkv, T, d), dev)
+    dt, dev, Hkv, t = _dtype_code(Q), Q.device, 0 if K is None else K.shape[1], Q.dtype
+    sq = _rows(Q, "Q", t, (B, Hq, T, d), dev)
+    sk = sq if K is None else _rows(K, "K", t, (B, Hkv, T, d), dev)
     n_axes = _need_positions(positions, B, T, past, lengths, plan, dev)
     if _elsewhere(dev):
         with torch.cuda.device(dev):
@@ -642,18 +647,18 @@ def oal_rope(Q, K, plan, positions=None, past=None, lengths=None, form=OAL_ROPE_
     made = []
     make = torch.empty if lengths is None else torch.zeros
     if Yq is None:
-        Yq = make(B, Hq, T, d, dtype=Q.dtype, device=dev)
+        Yq = make(B, Hq, T, d, dtype=t, device=dev)
         made.append(Yq)
-    _need_tensor(Yq, "Yq", Q.dtype, (B, Hq, T, d), dev)
+    else:
+        _need_tensor(Yq, "Yq", t, (B, Hq, T, d), dev)
     if K is None:
         _need(Yk is None, "Yk without K")
     elif Yk is None:
-        Yk = make(B, Hkv, T, d, dtype=Q.dtype, device=dev)
+        Yk = make(B, Hkv, T, d, dtype=t, device=dev)
         made.append(Yk)
-    if Yk is not None:
-        _need_tensor(Yk, "Yk", Q.dtype, (B, Hkv, T, d), dev)
-    strides = (ctypes.c_int64 * 6)(*sq[:3], *sk[:3])
-    _check(lib.oal_rope(Q.data_ptr(), _ptr_or_null(K), dt, strides, B, Hq, Hkv, T, d,
+    else:
+        _need_tensor(Yk, "Yk", t, (B, Hkv, T, d), dev)
+    _check(lib.oal_rope(Q.data_ptr(), _ptr_or_null(K), dt, _strides6(*sq, *sk), B, Hq, Hkv, T, d,
                         plan.data_ptr(), form, _ptr_or_null(positions), n_axes, _ptr_or_null(past),
                         _ptr_or_null(lengths), bool(inverse), Yq.data_ptr(), _ptr_or_null(Yk),
                         _stream_on(dev, stream, made)))
@@ -664,15 +669,15 @@ def _pages(Kp, Vp, Hkv, table, B, dtype, dev):
     """Number of pages, their size and stride, entries of the table."""
     _need(Kp.dim() == 4 and table.dim() == 2, "Kp must have 4 dimensions, table 2")
     n, h, P, d = Kp.shape
-    sk, sv = Kp.stride(), Vp.stride()
     if not (Kp.dtype is dtype and Vp.dtype is dtype and h == Hkv and Vp.shape == Kp.shape
             and Kp.device == dev and Vp.device == dev):
         raise OALError(OAL_ERR_INVALID_ARG, "Kp and Vp must be %s [n_pages,%d,page_size,%d] on %s"
                        % (dtype, Hkv, d, dev))
+    _need_tensor(table, "table", torch.int32, (B, table.shape[1]), dev)
+    sk, sv = Kp.stride(), Vp.stride()
     _need((n < 2 or sk[0] == sv[0]) and (h < 2 or sk[1] == sv[1] == P * d)
           and sk[2] == sv[2] == d and sk[3] == sv[3] == 1,
           "the pages of Kp and Vp must be contiguous and equally far apart")
-    _need_tensor(table, "table", torch.int32, (B, table.shape[1]), dev)
     # (one page: how far the next would be is anyone's guess)
     return n, P, sk[0] if n > 1 else h * P * d, table.shape[1]
 
@@ -688,13 +693,14 @@ def oal_page_append(Q, K, V, plan, Kp, Vp, table, past, positions=None, lengths=
     _need(K.dim() == 4 and V.dim() == 4 and (Q is None or Q.dim() == 4),
           "Q, K and V must have 4 dimensions")
     B, Hkv, T, d = K.shape
-    dt, dev, dv, Hq = _dtype_code(K), K.device, V.shape[3], 0 if Q is None else Q.shape[1]
-    sk = _rows(K, "K", K.dtype, (B, Hkv, T, d), dev)
-    sv = _rows(V, "V", K.dtype, (B, Hkv, T, dv), dev)
-    sq = sk if Q is None else _rows(Q, "Q", K.dtype, (B, Hq, T, d), dev)
+    dt, dev, dv, t = _dtype_code(K), K.device, V.shape[3], K.dtype
+    Hq = 0 if Q is None else Q.shape[1]
+    sk = _rows(K, "K", t, (B, Hkv, T, d), dev)
+    sv = _rows(V, "V", t, (B, Hkv, T, dv), dev)
+    sq = sk if Q is None else _rows(Q, "Q", t, (B, Hq, T, d), dev)
     _need(past is not None, "past is needed")
     n_axes = _need_positions(positions, B, T, past, lengths, plan, dev)
-    n, P, apart, most = _pages(Kp, Vp, Hkv, table, B, K.dtype, dev)
+    n, P, apart, most = _pages(Kp, Vp, Hkv, table, B, t, dev)
     if _elsewhere(dev):
         with torch.cuda.device(dev):
             return oal_page_append(Q, K, V, plan, Kp, Vp, table, past, positions, lengths, form, Yq,
@@ -703,17 +709,22 @@ def oal_page_append(Q, K, V, plan, Kp, Vp, table, past, positions=None, lengths=
     if Q is None:
         _need(Yq is None, "Yq without Q")
     elif Yq is None:
-        Yq = (torch.empty if lengths is None else torch.zeros)(B, Hq, T, d, dtype=K.dtype, device=dev)
+        Yq = (torch.empty if lengths is None else torch.zeros)(B, Hq, T, d, dtype=t, device=dev)
         made.append(Yq)
-    if Yq is not None:
-        _need_tensor(Yq, "Yq", K.dtype, (B, Hq, T, d), dev)
-    strides = (ctypes.c_int64 * 9)(*sq[:3], *sk[:3], *sv[:3])
-    _check(lib.oal_page_append(_ptr_or_null(Q), K.data_ptr(), V.data_ptr(), dt, strides, B, Hq, Hkv,
-                               T, d, dv, _ptr_or_null(plan), form, _ptr_or_null(positions), n_axes,
-                               past.data_ptr(), _ptr_or_null(lengths), Kp.data_ptr(), Vp.data_ptr(),
-                               n, P, apart, table.data_ptr(), most, _ptr_or_null(Yq),
+    else:
+        _need_tensor(Yq, "Yq", t, (B, Hq, T, d), dev)
+    _check(lib.oal_page_append(_ptr_or_null(Q), K.data_ptr(), V.data_ptr(), dt,
+                               _strides9(*sq, *sk, *sv), B, Hq, Hkv, T, d, dv, _ptr_or_null(plan),
+                               form, _ptr_or_null(positions), n_axes, past.data_ptr(),
+                               _ptr_or_null(lengths), Kp.data_ptr(), Vp.data_ptr(), n, P, apart,
+                               table.data_ptr(), most, _ptr_or_null(Yq),
                                _stream_on(dev, stream, made)))
     return Yq
+
+
+@functools.lru_cache(maxsize=4096)
+def _paged_attention_bytes(*sizes):
+    return max(int(load_library().oal_paged_attention_workspace_bytes(*sizes)), 256)
 
 
 def oal_paged_attention_workspace_bytes(B, Hq, Hkv, T, page_size, max_pages, d=64, dv=64,
@@ -733,11 +744,12 @@ def oal_paged_attention(Q, Kp, Vp, table, past, lengths=None, scale=0.125, cap=0
     Y; rows behind a sequence's length stay as given (a Y made here has zeros
     there), tokens that see nothing get zeros."""
     lib = load_library()
-    _need(Q.dim() == 4, "Q must have 4 dimensions")
+    _need(Q.dim() == 4 and Kp.dim() == 4, "Q, Kp and Vp must have 4 dimensions")
     B, Hq, T, d = Q.shape
-    dt, dev, Hkv, dv = _dtype_code(Q), Q.device, Kp.shape[1] if Kp.dim() == 4 else 0, Vp.shape[-1]
-    _need_tensor(Q, "Q", Q.dtype, (B, Hq, T, d), dev)
-    n, P, apart, most = _pages(Kp, Vp, Hkv, table, B, Q.dtype, dev)
+    dt, dev, t, Hkv, dv = _dtype_code(Q), Q.device, Q.dtype, Kp.shape[1], Vp.shape[-1]
+    if not Q.is_contiguous():
+        _need_tensor(Q, "Q", t, (B, Hq, T, d), dev)
+    n, P, apart, most = _pages(Kp, Vp, Hkv, table, B, t, dev)
     _need_tensor(past, "past", torch.int32, (B,), dev)
     _need_lengths(lengths, B, dev)
     if slopes is not None:
@@ -752,17 +764,22 @@ def oal_paged_attention(Q, Kp, Vp, table, past, lengths=None, scale=0.125, cap=0
                                        prefix, first, Y, workspace, stream)
     made = []
     if Y is None:
-        Y = (torch.empty if lengths is None else torch.zeros)(B, Hq, T, dv, dtype=Q.dtype, device=dev)
+        Y = (torch.empty if lengths is None else torch.zeros)(B, Hq, T, dv, dtype=t, device=dev)
         made.append(Y)
-    _need_tensor(Y, "Y", Q.dtype, (B, Hq, T, dv), dev)
-    workspace = _workspace(workspace, lib.oal_paged_attention_workspace_bytes, made,
-                           (B, Hq, Hkv, T, d, dv, dt, P, most), dev)
+    else:
+        _need_tensor(Y, "Y", t, (B, Hq, T, dv), dev)
+    if workspace is None:
+        room = _paged_attention_bytes(B, Hq, Hkv, T, d, dv, dt, P, most)
+        workspace = torch.empty(room, dtype=torch.uint8, device=dev)
+        made.append(workspace)
+    else:
+        _need_tensor(workspace, "workspace", workspace.dtype, workspace.shape, dev)
+        room = workspace.numel() * workspace.element_size()
     _check(lib.oal_paged_attention(Q.data_ptr(), dt, B, Hq, Hkv, T, d, dv, Kp.data_ptr(),
                                    Vp.data_ptr(), n, P, apart, table.data_ptr(), most,
                                    past.data_ptr(), _ptr_or_null(lengths), scale, cap, window,
                                    _ptr_or_null(slopes), _ptr_or_null(prefix), _ptr_or_null(first),
-                                   Y.data_ptr(), workspace.data_ptr(),
-                                   workspace.numel() * workspace.element_size(),
+                                   Y.data_ptr(), workspace.data_ptr(), room,
                                    _stream_on(dev, stream, made)))
     return Y
 
