@@ -651,7 +651,7 @@ static oal_status rope_args(oal::RopeArgs &p, oal_dtype dtype, const void *const
   if (form != OAL_ROPE_HALVES && form != OAL_ROPE_PAIRS)
     return oal_fail(OAL_ERR_INVALID_ARG, "bad form %d", (int)form);
   if (d != oal::kD) return oal_fail(OAL_ERR_UNSUPPORTED, "only d = 64 is supported (d=%d)", d);
-  if ((long long)B * T > 1LL << 34 || (long long)Hq + 2LL * Hkv > 1 << 16)
+  if ((long long)B * T > 1LL << 31 || (long long)Hq + 2LL * Hkv > 1 << 16)
     return oal_fail(OAL_ERR_UNSUPPORTED, "problem too large");
   if (positions && n_axes < 1) return oal_fail(OAL_ERR_INVALID_ARG, "n_axes=%d", n_axes);
   const int heads[3] = {Hq, Hkv, Hkv};

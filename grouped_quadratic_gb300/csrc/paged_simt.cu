@@ -78,23 +78,42 @@ paged_simt_kernel(PagedArgs p) {
   float4 o[R];
 #pragma unroll
   for (int i = 0; i < R; ++i) m[i] = -INFINITY, l[i] = 0.f, o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  // A thread moves piece tid % 16 of rows tid / 16 + 8 i of a tile, the next one's
+  // while the present one is worked on; 16 keys lie on one page.
+  int page[kKeys / 16];
+  auto look = [&](int j0) {
+#pragma unroll
+    for (int i = 0; i < kKeys / 16; ++i) {
+      const int j = j0 + 16 * i;
+      page[i] = j < k1 && j + 16 > k0 ? paged_page(p, b, j) : -1;
+    }
+  };
+  float4 kn[kKeys / 8], vn[kKeys / 8];
+  auto fetch = [&](int j0) {
+#pragma unroll
+    for (int i = 0; i < kKeys / 8; ++i) {
+      const int j = j0 + (tid >> 4) + 8 * i;
+      kn[i] = vn[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (page[i >> 1] >= 0 && j >= k0 && j < k1) {
+        const size_t from = paged_row(p, page[i >> 1], kv, j) + 4 * (tid & 15);
+        kn[i] = *reinterpret_cast<const float4 *>(static_cast<const float *>(p.Kp) + from);
+        vn[i] = *reinterpret_cast<const float4 *>(static_cast<const float *>(p.Vp) + from);
+      }
+    }
+  };
+  look(k0 & ~(kKeys - 1));
+  fetch(k0 & ~(kKeys - 1));
+  look((k0 & ~(kKeys - 1)) + kKeys);
   for (int j0 = k0 & ~(kKeys - 1); j0 < k1; j0 += kKeys) {
     __syncthreads();
-    for (int x = tid; x < kKeys * 16; x += kThreads) {
-      const int j = j0 + (x >> 4), c = 4 * (x & 15);
-      float4 k = make_float4(0.f, 0.f, 0.f, 0.f), v = k;
-      if (j >= k0 && j < k1) {
-        const int page = paged_page(p, b, j);
-        if (page >= 0) {
-          const size_t from = paged_row(p, page, kv, j) + c;
-          k = *reinterpret_cast<const float4 *>(static_cast<const float *>(p.Kp) + from);
-          v = *reinterpret_cast<const float4 *>(static_cast<const float *>(p.Vp) + from);
-        }
-      }
-      *reinterpret_cast<float4 *>(&s.k[x >> 4][c]) = k;
-      *reinterpret_cast<float4 *>(&s.v[x >> 4][c]) = v;
+#pragma unroll
+    for (int i = 0; i < kKeys / 8; ++i) {
+      *reinterpret_cast<float4 *>(&s.k[(tid >> 4) + 8 * i][4 * (tid & 15)]) = kn[i];
+      *reinterpret_cast<float4 *>(&s.v[(tid >> 4) + 8 * i][4 * (tid & 15)]) = vn[i];
     }
     __syncthreads();
+    fetch(j0 + kKeys);
+    look(j0 + 2 * kKeys);
     float x[R][4];
 #pragma unroll
     for (int i = 0; i < R; ++i)
@@ -199,7 +218,7 @@ oal_status run(const PagedArgs &p, cudaStream_t stream) {
 }  // namespace
 
 oal_status launch_paged_simt(const PagedArgs &p, cudaStream_t stream) {
-  return p.tile_rows == 8 ? run<8>(p, stream) : run<32>(p, stream);
+  return p.tile_rows == 8 ? run<8>(p, stream) : p.tile_rows == 16 ? run<16>(p, stream) : run<32>(p, stream);
 }
 
 }  // namespace oal

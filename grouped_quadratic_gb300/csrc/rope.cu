@@ -8,10 +8,13 @@
 // nearest quarter turn is taken out exactly and the rest (at most an eighth)
 // goes through sincospif.
 //
-// A block takes 16 tokens: their angles once, into shared memory, for all of its
-// heads; then every row is read once and written once: HBM-bound.  A thread moves
-// two 16-byte pieces whose elements pair up.  Few tokens: the heads are spread
-// over blocks instead, and the angles are formed again in each.
+// A block takes 4 tokens: their angles once, into shared memory, for all of its
+// heads, while the first rows are on their way; then every row is read once and
+// written once: HBM-bound.  A thread moves two 16-byte pieces whose elements pair
+// up.  4 x 8192 tokens, 32/8 heads, bf16, as views of a projection: 53.8 us (6.24
+// TB/s), appending them 63.7 (6.32); blocks of 4, 8 and 16 tokens 53.8, 54.7 and
+// 60.0.  Few tokens: the heads are spread over blocks instead, and the angles are
+// formed again in each.
 #include <algorithm>
 
 #include "paged.cuh"
@@ -19,8 +22,8 @@
 namespace oal {
 namespace {
 
-constexpr int kRopeThreads = 256;
-constexpr int kRopeTokens = 16;
+constexpr int kRopeThreads = 64;
+constexpr int kRopeTokens = 4;
 
 struct alignas(16) Piece {
   uint4 w;
@@ -46,62 +49,73 @@ __device__ __forceinline__ Piece piece_put(const float (&f)[4]) {
   return Piece{make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]))};
 }
 
-struct RopeToken {
-  long long q, k, v;                      // elements to the token's rows, without the head
-  long long yq, yk, page;                 // page: -1 = nowhere
-  int live;
-};
-
 template <typename T, bool kHalves>
 __global__ void __launch_bounds__(kRopeThreads)
 rope_kernel(RopeArgs p, int heads_a_block) {
   pdl_trigger();
   pdl_wait();
   constexpr int E = kPiece<T>, kUnits = 32 / E;       // pairs of a unit, units of a row
+  constexpr int kStep = kRopeThreads / kUnits / kRopeTokens;   // heads of a pass
   __shared__ float2 s_turn[kRopeTokens][33];
-  __shared__ RopeToken s_tok[kRopeTokens];
-  const int tid = threadIdx.x;
-  const long long n0 = (long long)blockIdx.x * kRopeTokens, all = (long long)p.B * p.T;
-  if (tid < kRopeTokens) {
-    RopeToken k = {};
-    k.page = -1;
-    const long long n = n0 + tid;
-    if (n < all) {
-      const int b = (int)(n / p.T), t = (int)(n % p.T);
-      int len = p.T;
-      if (p.lengths) {
-        len = p.lengths[b];
-        if (len < 0 || len > p.T) atomicCAS(p.status, kStatusOk, (int)OAL_ERR_INVALID_ARG);
-      }
-      k.live = t < len;
-      k.q = b * p.q.b + t * p.q.t, k.k = b * p.k.b + t * p.k.t, k.v = b * p.v.b + t * p.v.t;
-      k.yq = ((long long)b * p.Hq * p.T + t) * 64, k.yk = ((long long)b * p.Hkv * p.T + t) * 64;
-      if (p.Kp && k.live) {
-        const long long at = (long long)p.past[b] + t;
-        int page = -1;
-        if (at >= 0 && (at >> p.page_shift) < p.max_pages) page = p.table[(long long)b * p.max_pages + (at >> p.page_shift)];
-        if (page >= 0 && page < p.n_pages)
-          k.page = page * p.page_stride + (at & ((1 << p.page_shift) - 1)) * 64;
-        else
-          atomicCAS(p.status, kStatusOk, (int)OAL_ERR_INVALID_ARG);
-      }
-    }
-    s_tok[tid] = k;
+  const int tid = threadIdx.x, unit = tid % kUnits, tok = tid / kUnits % kRopeTokens;
+  const uint32_t T_ = (uint32_t)p.T, n0 = blockIdx.x * kRopeTokens, all = (uint32_t)p.B * T_;
+  const int a0 = kHalves ? unit * E : 2 * unit * E, a1 = a0 + (kHalves ? 32 : E);
+
+  // the thread's token: in its sequence, and (page) its place in the cache
+  const uint32_t n = min(n0 + tok, all - 1), b = n / T_, t = n - b * T_;
+  bool live = n0 + tok < all;
+  if (live && p.lengths) {
+    const int len = p.lengths[b];
+    if (len < 0 || len > p.T) atomicCAS(p.status, kStatusOk, (int)OAL_ERR_INVALID_ARG);
+    live = (int)t < len;
+  }
+  long long page = -1;
+  if (p.Kp && live) {
+    const long long at = (long long)p.past[b] + t;
+    int i = -1;
+    if (at >= 0 && (at >> p.page_shift) < p.max_pages) i = p.table[(size_t)b * p.max_pages + (at >> p.page_shift)];
+    if (i >= 0 && i < p.n_pages)
+      page = i * p.page_stride + (at & ((1 << p.page_shift) - 1)) * 64;
+    else
+      atomicCAS(p.status, kStatusOk, (int)OAL_ERR_INVALID_ARG);
+  }
+  const int heads = p.Hq + (p.K ? p.Hkv : 0) + (p.V ? p.Hkv : 0);
+  const int h0 = blockIdx.y * heads_a_block, h1 = live ? min(heads, h0 + heads_a_block) : 0;
+  auto source = [&](int h) {
+    if (h < p.Hq) return static_cast<const T *>(p.Q) + b * p.q.b + t * p.q.t + h * p.q.h;
+    h -= p.Hq;
+    if (h < p.Hkv) return static_cast<const T *>(p.K) + b * p.k.b + t * p.k.t + h * p.k.h;
+    return static_cast<const T *>(p.V) + b * p.v.b + t * p.v.t + (h - p.Hkv) * p.v.h;
+  };
+  auto target = [&](int h) -> T * {       // null: nowhere
+    if (h < p.Hq) return static_cast<T *>(p.Yq) + (((size_t)b * p.Hq + h) * p.T + t) * 64;
+    h -= p.Hq;
+    const bool key = h < p.Hkv;
+    if (!p.Kp) return static_cast<T *>(p.Yk) + (((size_t)b * p.Hkv + h) * p.T + t) * 64;
+    if (page < 0) return nullptr;
+    if (!key) h -= p.Hkv;
+    return static_cast<T *>(key ? p.Kp : p.Vp) + page + ((long long)h << p.page_shift) * 64;
+  };
+  // the first rows are on their way while the angles are formed
+  int h = h0 + tid / (kUnits * kRopeTokens);
+  Piece x0 = {}, x1 = {};
+  if (h < h1) {
+    const T *src = source(h);
+    x0 = *reinterpret_cast<const Piece *>(src + a0), x1 = *reinterpret_cast<const Piece *>(src + a1);
   }
   if (p.turns) {
-#pragma unroll
     for (int x = tid; x < kRopeTokens * 32; x += kRopeThreads) {
       const int r = x & 31;
-      const long long n = n0 + (x >> 5);
-      if (n >= all) break;
+      const uint32_t m = n0 + (x >> 5);
+      if (m >= all) break;
       long long at;
       if (p.positions) {
         const long long axis = p.axes[r];
         const bool bad = axis < 0 || axis >= p.n_axes;
         if (bad) atomicCAS(p.status, kStatusOk, (int)OAL_ERR_INVALID_ARG);
-        at = p.positions[(bad ? 0 : axis) * all + n];
+        at = p.positions[(bad ? 0 : axis) * all + m];
       } else {
-        at = n % p.T + (p.past ? p.past[n / p.T] : 0);
+        at = (long long)(m % T_) + (p.past ? p.past[m / T_] : 0);
       }
       const unsigned long long turn = (unsigned long long)at * p.turns[r];
       const unsigned long long quarter = turn + (1ull << 61);
@@ -114,52 +128,27 @@ rope_kernel(RopeArgs p, int heads_a_block) {
     }
   }
   __syncthreads();
-
-  const int heads = p.Hq + (p.K ? p.Hkv : 0) + (p.V ? p.Hkv : 0);
-  const int h0 = blockIdx.y * heads_a_block, h1 = min(heads, h0 + heads_a_block);
-  constexpr int kRows = kRopeThreads / kUnits;        // rows in flight of a pass
-  const int unit = tid % kUnits, tok = tid / kUnits % kRopeTokens;
-  const RopeToken k = s_tok[tok];
-  if (!k.live) return;
-  const int a0 = kHalves ? unit * E : 2 * unit * E, a1 = a0 + (kHalves ? 32 : E);
   float2 turn[E];
   if (p.turns) {
 #pragma unroll
     for (int e = 0; e < E; ++e) turn[e] = s_turn[tok][unit * E + e];
   }
+  const int turned = p.turns ? p.Hq + p.Hkv : 0;      // heads that turn
 #pragma unroll 4
-  for (int h = h0 + tid / (kUnits * kRopeTokens); h < h1; h += kRows / kRopeTokens) {
-    const T *src;
-    T *dst;
-    bool turns = p.turns != nullptr;
-    if (h < p.Hq) {
-      src = static_cast<const T *>(p.Q) + k.q + h * p.q.h;
-      dst = static_cast<T *>(p.Yq) + k.yq + (long long)h * p.T * 64;
-    } else if (h < p.Hq + p.Hkv) {
-      const int kv = h - p.Hq;
-      src = static_cast<const T *>(p.K) + k.k + kv * p.k.h;
-      if (p.Kp) {
-        if (k.page < 0) continue;
-        dst = static_cast<T *>(p.Kp) + k.page + ((long long)kv << p.page_shift) * 64;
-      } else {
-        dst = static_cast<T *>(p.Yk) + k.yk + (long long)kv * p.T * 64;
-      }
-    } else {
-      const int kv = h - p.Hq - p.Hkv;
-      if (k.page < 0) continue;
-      src = static_cast<const T *>(p.V) + k.v + kv * p.v.h;
-      dst = static_cast<T *>(p.Vp) + k.page + ((long long)kv << p.page_shift) * 64;
-      turns = false;
+  for (; h < h1; h += kStep) {
+    Piece y0 = x0, y1 = x1;
+    if (h + kStep < h1) {
+      const T *src = source(h + kStep);
+      x0 = *reinterpret_cast<const Piece *>(src + a0), x1 = *reinterpret_cast<const Piece *>(src + a1);
     }
-    Piece x0 = *reinterpret_cast<const Piece *>(src + a0), x1 = *reinterpret_cast<const Piece *>(src + a1);
-    if (turns) {
-      float a[E], b[E];
-      piece_get(x0, a), piece_get(x1, b);
+    if (h < turned) {
+      float a[E], c[E];
+      piece_get(y0, a), piece_get(y1, c);
       if (kHalves) {
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-          const float u = a[e], w = b[e];
-          a[e] = fmaf(u, turn[e].x, -(w * turn[e].y)), b[e] = fmaf(w, turn[e].x, u * turn[e].y);
+          const float u = a[e], w = c[e];
+          a[e] = fmaf(u, turn[e].x, -(w * turn[e].y)), c[e] = fmaf(w, turn[e].x, u * turn[e].y);
         }
       } else {   // pairs inside each piece
 #pragma unroll
@@ -167,14 +156,14 @@ rope_kernel(RopeArgs p, int heads_a_block) {
           const float2 t0 = turn[e], t1 = turn[E / 2 + e];
           float u = a[2 * e], w = a[2 * e + 1];
           a[2 * e] = fmaf(u, t0.x, -(w * t0.y)), a[2 * e + 1] = fmaf(w, t0.x, u * t0.y);
-          u = b[2 * e], w = b[2 * e + 1];
-          b[2 * e] = fmaf(u, t1.x, -(w * t1.y)), b[2 * e + 1] = fmaf(w, t1.x, u * t1.y);
+          u = c[2 * e], w = c[2 * e + 1];
+          c[2 * e] = fmaf(u, t1.x, -(w * t1.y)), c[2 * e + 1] = fmaf(w, t1.x, u * t1.y);
         }
       }
-      x0 = piece_put(a), x1 = piece_put(b);
+      y0 = piece_put(a), y1 = piece_put(c);
     }
-    *reinterpret_cast<Piece *>(dst + a0) = x0;
-    *reinterpret_cast<Piece *>(dst + a1) = x1;
+    T *dst = target(h);
+    if (dst) *reinterpret_cast<Piece *>(dst + a0) = y0, *reinterpret_cast<Piece *>(dst + a1) = y1;
   }
 }
 
