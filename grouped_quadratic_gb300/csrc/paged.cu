@@ -13,22 +13,25 @@ oal_status launch_paged_tc(const PagedArgs &p, cudaStream_t stream);
 
 namespace {
 
-// Joins the rows of split keys, a block a row: y = sum_s 2^{m_s - m} o_s /
-// sum_s 2^{m_s - m} l_s over the splits that the row sees something of.  A warp
-// takes every kJoinWarps-th split, in order, and the warps' sums are added in
+// Joins the rows of split keys: y = sum_s 2^{m_s - m} o_s / sum_s 2^{m_s - m} l_s
+// over the splits that the row sees something of.  A row has kJoinWarps warps,
+// each with every kJoinWarps-th split, in order, and their sums are added in
 // order: the same bits every time.  Eight splits a warp are one step, 2 us with
 // the launch, and each further step costs another 2: 129 splits took 10 us with
-// four warps.
+// four warps; but 6,216 rows of 4 splits take 6 us with four warps, 3 with one.
+constexpr int kJoinThreads = 128;
 template <typename T, int kJoinWarps>
-__global__ void __launch_bounds__(32 * kJoinWarps)
+__global__ void __launch_bounds__(kJoinWarps > 4 ? 32 * kJoinWarps : kJoinThreads)
 paged_join_kernel(PagedArgs p) {
   pdl_trigger();
   pdl_wait();
+  constexpr int kRows = kJoinWarps > 4 ? 1 : kJoinThreads / 32 / kJoinWarps;   // of a block
   __shared__ float s_m[kJoinWarps], s_l[kJoinWarps];
   __shared__ float2 s_y[kJoinWarps][32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) % kJoinWarps;
   const int bh = blockIdx.y, b = bh / p.Hkv, kv = bh % p.Hkv;
-  const int r = blockIdx.x;
+  const int r = blockIdx.x * kRows + (threadIdx.x >> 5) / kJoinWarps;
+  if (r >= p.T * p.rho) return;
   const PagedSeq seq = paged_seq(p, b, false);
   const int t = r / p.rho, h = kv * p.rho + r % p.rho;
   if (t >= seq.n) return;
@@ -60,11 +63,11 @@ paged_join_kernel(PagedArgs p) {
       }
     }
   }
-  if (lane == 0) s_m[warp] = m, s_l[warp] = l;
-  s_y[warp][lane] = y;
-  __syncthreads();
-  if (warp != 0) return;
-  if (sees.y > 0) {
+  if (kJoinWarps > 1) {                   // (one row a block)
+    if (lane == 0) s_m[warp] = m, s_l[warp] = l;
+    s_y[warp][lane] = y;
+    __syncthreads();
+    if (warp != 0) return;
     float top = s_m[0];
 #pragma unroll
     for (int w = 1; w < kJoinWarps; ++w) top = fmaxf(top, s_m[w]);
@@ -76,9 +79,13 @@ paged_join_kernel(PagedArgs p) {
       const float2 o = s_y[w][lane];
       l = fmaf(f, s_l[w], l), y.x = fmaf(f, o.x, y.x), y.y = fmaf(f, o.y, y.y);
     }
+  }
+  if (sees.y > 0) {
     y.x /= l, y.y /= l;
     if (__any_sync(0xffffffffu, !(fabsf(y.x) + fabsf(y.y) < INFINITY)))
       y = paged_row_again<T>(p, b, h, t, sees.x, sees.y);
+  } else {
+    y = make_float2(0.f, 0.f);
   }
   T *to = paged_y<T>(p, b, h, t) + 2 * lane;
   to[0] = from_f32<T>(y.x), to[1] = from_f32<T>(y.y);
@@ -87,11 +94,16 @@ paged_join_kernel(PagedArgs p) {
 }  // namespace
 
 oal_status launch_paged_join(const PagedArgs &p, int is_bf16, cudaStream_t stream) {
-  const dim3 grid((unsigned)(p.T * p.rho), (unsigned)(p.B * p.Hkv));
-  const bool many = p.splits > 32;        // more than four warps take in one step
-  auto kernel = is_bf16 ? (many ? paged_join_kernel<__nv_bfloat16, 16> : paged_join_kernel<__nv_bfloat16, 4>)
-                        : (many ? paged_join_kernel<float, 16> : paged_join_kernel<float, 4>);
-  launch_pdl(kernel, grid, dim3(many ? 512 : 128), 0, stream, p);
+  // warps a row: so that eight splits each are enough, up to 16
+  const int warps = p.splits <= 8 ? 1 : p.splits <= 32 ? 4 : 16, each = warps == 1 ? kJoinThreads / 32 : 1;
+  const dim3 grid((unsigned)((p.T * p.rho + each - 1) / each), (unsigned)(p.B * p.Hkv));
+  auto kernel = is_bf16 ? (warps == 1   ? paged_join_kernel<__nv_bfloat16, 1>
+                           : warps == 4 ? paged_join_kernel<__nv_bfloat16, 4>
+                                        : paged_join_kernel<__nv_bfloat16, 16>)
+                        : (warps == 1   ? paged_join_kernel<float, 1>
+                           : warps == 4 ? paged_join_kernel<float, 4>
+                                        : paged_join_kernel<float, 16>);
+  launch_pdl(kernel, grid, dim3(warps == 16 ? 512 : kJoinThreads), 0, stream, p);
   return oal_after_launch("paged_join_kernel", stream);
 }
 

@@ -26,8 +26,11 @@ struct SimtSmem {
 };
 
 __device__ __forceinline__ float4 row4(const float *row, int c) { return *reinterpret_cast<const float4 *>(row + c); }
-__device__ __forceinline__ float dot4(float4 a, float4 b, float s) {
-  return fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, fmaf(a.w, b.w, s))));
+__device__ __forceinline__ ulonglong2 row2(const float *row, int c) { return *reinterpret_cast<const ulonglong2 *>(row + c); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
 }
 
 template <int kRows>
@@ -114,23 +117,28 @@ paged_simt_kernel(PagedArgs p) {
     __syncthreads();
     fetch(j0 + kKeys);
     look(j0 + 2 * kKeys);
+    uint64_t x2[R][4];                    // sums over even and odd elements, side by side: half the instructions
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x2[i][e] = 0u;
+#pragma unroll 4
+    for (int d = 0; d < 64; d += 4) {
+      ulonglong2 k[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) k[e] = row2(s.k[tx + 16 * e], d);
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        const ulonglong2 q = row2(s.q[ty * R + i], d);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x2[i][e] = fma2(q.y, k[e].y, fma2(q.x, k[e].x, x2[i][e]));
+      }
+    }
     float x[R][4];
 #pragma unroll
     for (int i = 0; i < R; ++i)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) x[i][e] = 0.f;
-#pragma unroll 4
-    for (int d = 0; d < 64; d += 4) {
-      float4 k[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) k[e] = row4(s.k[tx + 16 * e], d);
-#pragma unroll
-      for (int i = 0; i < R; ++i) {
-        const float4 q = row4(s.q[ty * R + i], d);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[i][e] = dot4(q, k[e], x[i][e]);
-      }
-    }
+      for (int e = 0; e < 4; ++e) x[i][e] = __uint_as_float((uint32_t)x2[i][e]) + __uint_as_float((uint32_t)(x2[i][e] >> 32));
 #pragma unroll
     for (int i = 0; i < R; ++i) {
       float top = m[i];
