@@ -756,7 +756,8 @@ static oal_status check_paged(oal::PagedArgs &p, int B, int Hq, int Hkv, int T, 
   if (T < 0) return oal_fail(OAL_ERR_INVALID_ARG, "T=%d", T);
   OAL_TRY(check_pages(Hkv, n_pages, page_size, page_stride, max_pages, &p.page_shift));
   const int rho = Hq / Hkv;
-  if (rho > 128 || (long long)B * Hkv > 65535 || (long long)T * rho > 1LL << 28)
+  if (rho > 128 || (long long)B * Hkv > 65535 || (long long)T * rho > 1LL << 28 ||
+      (long long)B * Hkv * T > 1LL << 31)
     return oal_fail(OAL_ERR_UNSUPPORTED, "problem too large");
   p.B = B, p.Hq = Hq, p.Hkv = Hkv, p.T = T, p.rho = rho;
   p.n_pages = n_pages, p.max_pages = max_pages, p.page_stride = page_stride;
@@ -783,7 +784,8 @@ oal_status oal_paged_attention(const void *Q, oal_dtype dtype, int B, int Hq, in
   oal::PagedArgs p = {};
   OAL_TRY(check_paged(p, B, Hq, Hkv, T, d, dv, dtype, n_pages, page_size, page_stride, max_pages));
   if (!(scale > 0.f) || !isfinite(scale)) return oal_fail(OAL_ERR_INVALID_ARG, "scale=%g", scale);
-  if (!(cap >= 0.f) || !isfinite(cap)) return oal_fail(OAL_ERR_INVALID_ARG, "cap=%g", cap);
+  if (!(cap >= 0.f) || !isfinite(cap) || (cap > 0.f && !isfinite(4.f * scale / cap)))
+    return oal_fail(OAL_ERR_INVALID_ARG, "cap=%g", cap);
   if (window < 0) return oal_fail(OAL_ERR_INVALID_ARG, "window=%d", window);
   t_call_launches = 0;
   if (B == 0 || T == 0) return OAL_OK;

@@ -83,7 +83,7 @@ paged_join_kernel(PagedArgs p) {
   if (sees.y > 0) {
     y.x /= l, y.y /= l;
     if (__any_sync(0xffffffffu, !(fabsf(y.x) + fabsf(y.y) < INFINITY)))
-      y = paged_row_again<T>(p, b, h, t, sees.x, sees.y);
+      y = paged_row_again<T>(p, seq, b, h, t, sees.x, sees.y);
   } else {
     y = make_float2(0.f, 0.f);
   }

@@ -111,12 +111,12 @@ __device__ __forceinline__ float paged_score(const PagedArgs &p, float qk, float
 // hold has no part in it: for rows whose result is not finite, which a masked
 // key's infinity or NaN (times a weight of 0) may be to blame for.
 template <typename T>
-static __device__ __noinline__ float2 paged_row_again(const PagedArgs &p, int b, int h, int t, int lo, int hi) {
+static __device__ __noinline__ float2 paged_row_again(const PagedArgs &p, const PagedSeq &seq, int b, int h, int t, int lo, int hi) {
   const int lane = threadIdx.x & 31, kv = h / p.rho;
   const T *q = static_cast<const T *>(p.Q) + (((size_t)b * p.Hq + h) * p.T + t) * 64 + 2 * lane;
   const float q0 = to_f32(q[0]), q1 = to_f32(q[1]);
   const float slope = p.slopes ? p.slopes[h] : 0.f;
-  const int i = p.past[b] + t;
+  const int i = seq.past + t;
   float m = -INFINITY, l = 0.f, o0 = 0.f, o1 = 0.f;
   for (int j = lo; j < hi; ++j) {
     const int page = paged_page(p, b, j);

@@ -299,7 +299,7 @@ paged_rows_kernel(PagedArgs p) {
     if (row_k1 > 0) {
       y.x /= sum, y.y /= sum;
       if (__any_sync(0xffffffffu, !(fabsf(y.x) + fabsf(y.y) < INFINITY)))
-        y = paged_row_again<__nv_bfloat16>(p, b, h, t, row_k0, row_k1);
+        y = paged_row_again<__nv_bfloat16>(p, seq, b, h, t, row_k0, row_k1);
     } else {
       y = make_float2(0.f, 0.f);
     }

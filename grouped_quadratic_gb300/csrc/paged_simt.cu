@@ -204,7 +204,7 @@ paged_simt_kernel(PagedArgs p) {
         const int who = 16 * half;
         const int h2 = __shfl_sync(0xffffffffu, h, who), t2 = __shfl_sync(0xffffffffu, t, who);
         const int a = __shfl_sync(0xffffffffu, lo[i], who), z = __shfl_sync(0xffffffffu, hi[i], who);
-        const float2 f = paged_row_again<float>(p, b, h2, t2, a, z);
+        const float2 f = paged_row_again<float>(p, seq, b, h2, t2, a, z);
         __syncwarp();
         *reinterpret_cast<float2 *>(paged_y<float>(p, b, h2, t2) + 2 * (tid & 31)) = f;
       }

@@ -124,8 +124,9 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                 const __grid_constant__ CUtensorMap tmV, PagedArgs p, int nt) {
   extern __shared__ uint8_t smem_raw[];
   TcSmem &s = *reinterpret_cast<TcSmem *>(align1024(smem_raw));
-  const int bh = blockIdx.x, b = bh / p.Hkv, kv = bh % p.Hkv, split = blockIdx.z;
-  const int t0 = (gridDim.y - 1 - blockIdx.y) * 2 * nt;    // the last tokens, which see most, first
+  const uint32_t units = (uint32_t)(p.B * p.Hkv);
+  const int bh = blockIdx.x % units, b = bh / p.Hkv, kv = bh % p.Hkv, split = blockIdx.y;
+  const int t0 = (gridDim.x / units - 1 - blockIdx.x / units) * 2 * nt;   // the last tokens, which see most, first
   const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
   if (tid == 0) {
     s.wait.abort = 0;
@@ -481,7 +482,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         const int who = __ffs(again) - 1;
         const int h2 = __shfl_sync(0xffffffffu, h, who), t2 = __shfl_sync(0xffffffffu, t, who);
         const int a = __shfl_sync(0xffffffffu, sees.x, who), z = __shfl_sync(0xffffffffu, sees.y, who);
-        const float2 y = paged_row_again<__nv_bfloat16>(p, b, h2, t2, a, z);
+        const float2 y = paged_row_again<__nv_bfloat16>(p, seq, b, h2, t2, a, z);
         __syncwarp();
         *reinterpret_cast<uint32_t *>(paged_y<__nv_bfloat16>(p, b, h2, t2) + 2 * lane) = pack_bf16x2(y.x, y.y);
       }
@@ -521,7 +522,7 @@ oal_status run(const PagedArgs &p, cudaStream_t stream) {
   if (st == OAL_OK) st = tc_map(&mk, p.Kp, dims, strides, box);
   if (st == OAL_OK) st = tc_map(&mv, p.Vp, dims, strides, box);
   if (st != OAL_OK) return st;
-  const dim3 grid((unsigned)(p.B * p.Hkv), (unsigned)((p.T + 2 * nt - 1) / (2 * nt)), (unsigned)p.splits);
+  const dim3 grid((unsigned)((long long)p.B * p.Hkv * ((p.T + 2 * nt - 1) / (2 * nt))), (unsigned)p.splits);
   launch_pdl(kernel, grid, dim3(kTcThreads), kTcBytes, stream, mq, mk, mv, p, nt);
   st = oal_after_launch("paged_tc_kernel", stream);
   return st != OAL_OK || p.splits == 1 ? st : launch_paged_join(p, 1, stream);

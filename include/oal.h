@@ -420,8 +420,8 @@ oal_status oal_page_append(const void *Q, const void *K, const void *V, oal_dtyp
  *  past     [B] int32 (device): tokens before the T new ones.  Negative, or
  *           behind what the table has room for: clamped and recorded.
  *  lengths  [B] int32 (device) or NULL: as for oal_rope.
- *  scale    finite and > 0.  cap: 0 or a finite number > 0.  window: 0 (none)
- *           or > 0.
+ *  scale    finite and > 0.  cap: 0 or a finite number > 0, of which 4 scale / cap
+ *           is finite too.  window: 0 (none) or > 0.
  *  slopes   [Hq] fp32 (device) or NULL; first [B][T] int32 or NULL (document
  *           masks: the first key of the token's document); prefix [B] int32 or
  *           NULL.
@@ -436,7 +436,7 @@ oal_status oal_page_append(const void *Q, const void *K, const void *V, oal_dtyp
  * Arithmetic: OAL_F32 in fp32 on the CUDA cores.  OAL_BF16 on the tensor cores;
  * scores, maxima, sums and results in fp32, softmax's weights rounded to bf16
  * once.  Deterministic.  Supported: d == dv == 64, Hq / Hkv <= 128,
- * B * Hkv <= 65535, T * Hq / Hkv <= 2^28.
+ * B * Hkv <= 65535, T * Hq / Hkv <= 2^28, B * Hkv * T <= 2^31.
  */
 size_t oal_paged_attention_workspace_bytes(int B, int Hq, int Hkv, int T, int d, int dv,
                                            oal_dtype dtype, int page_size, int max_pages);

@@ -298,14 +298,14 @@ def test_attention(oal, dtype, B, Hq, Hkv, T, past, page, lengths):
     check(oal, c, draw((B, Hq, T, 64), dtype, 22, 1.5), lengths)
 
 
-MASKS = ["cap", "window", "bias", "docs", "prefix", "window+prefix", "cap+bias", "all", "nothing"]
+MASKS = ["cap", "small cap", "window", "bias", "docs", "prefix", "window+prefix", "cap+bias", "all", "nothing"]
 
 
 def masks(kind, B, Hq, T, past, lengths):
     new = lengths or [T] * B
     kw = {}
     if "cap" in kind or kind == "all":
-        kw["cap"] = 3.0
+        kw["cap"] = 30.0 if "small" in kind else 3.0      # (of small scores: their share of the cap is)
     if "window" in kind or kind == "all":
         kw["window"] = 50
     if "bias" in kind or kind == "all":
@@ -451,6 +451,22 @@ def test_offsets_behind_two_to_the_31(oal):
     assert torch.equal(c.rows(c.Vp, 0, 1500, 2100), K[0])
     c.past, c.total = ints([2099]), [2100]
     check(oal, c, draw((1, 2, 1, 64), BF16, 36))
+
+
+@pytest.mark.parametrize("Hq", [1, 2])
+def test_sixteen_million_tokens(oal, Hq):
+    """More tiles than a grid's second and third dimension hold; everyone sees itself, the last ones one key more."""
+    T, page = (1 << 24) + 300, 65536
+    n = -(-T // page)
+    gen = torch.Generator(device="cuda").manual_seed(63)
+    V = torch.randn(n, 1, page, 64, device="cuda", dtype=BF16, generator=gen)
+    K = torch.randn(n, 1, page, 64, device="cuda", dtype=BF16, generator=gen)
+    Q = torch.randn(1, Hq, T, 64, device="cuda", dtype=BF16, generator=gen)
+    table = torch.arange(n, device="cuda", dtype=torch.int32)[None]
+    Y = oal.oal_paged_attention(Q, K, V, table, ints([0]), window=1)
+    oal.oal_sync_status()
+    for h in range(Hq):                            # a weight of 1: the values themselves
+        assert torch.equal(Y[0, h], V.view(-1, 64)[:T])
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
