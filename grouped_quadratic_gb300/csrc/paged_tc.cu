@@ -117,11 +117,12 @@ struct TcWork {
   __device__ __forceinline__ bool has(int x, int j) const { return j >= from(x) && j < to(x); }
 };
 
-// kExtra: scores are capped or take a distance.
-template <bool kExtra>
+// kCap: scores are capped; kBias: they take a distance.
+template <bool kCap, bool kBias>
 __global__ void __launch_bounds__(kTcThreads, 1)
 paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                 const __grid_constant__ CUtensorMap tmV, PagedArgs p, int nt) {
+  constexpr bool kExtra = kCap || kBias;
   extern __shared__ uint8_t smem_raw[];
   TcSmem &s = *reinterpret_cast<TcSmem *>(align1024(smem_raw));
   const uint32_t units = (uint32_t)(p.B * p.Hkv);
@@ -317,12 +318,12 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
     const uint32_t tm = tb + ((uint32_t)(32 * (warp & 3)) << 16), to_o = tm + kColO + 64 * x;
     const int h = kv * p.rho + h1;
     const float scale2 = p.scale * kLog2e;
-    const float cap_in = kExtra && p.cap > 0.f ? 2.f * kLog2e * p.scale / p.cap : 0.f, cap_out = p.cap * kLog2e;
-    const float in_cap = kExtra && p.cap > 0.f ? p.scale / p.cap : 0.f;
+    const float cap_in = kCap ? 2.f * kLog2e * p.scale / p.cap : 0.f, cap_out = p.cap * kLog2e;
+    const float in_cap = kCap ? p.scale / p.cap : 0.f;
     auto times = [&](float c) { return pair(c * cap_out, c * cap_out); };
     const uint64_t tanh0 = times(0.9999998807907104f), tanh1 = times(-0.3333197236061096f), tanh2 = times(0.13304771482944489f),
                    tanh3 = times(-0.05183185636997223f), tanh4 = times(0.015063672326505184f);
-    const float slope = kExtra && live && p.slopes ? p.slopes[h] * kLog2e : 0.f;
+    const float slope = kBias && live ? p.slopes[h] * kLog2e : 0.f;
     const float by = kExtra ? 1.f : scale2;                // of what is held as a score
     // (a row that is none is not to make the others look at masks)
     const int see0 = live ? max(sees.x, from) : 0, see1 = live ? min(sees.y, to) : INT32_MAX;
@@ -339,14 +340,14 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
       uint32_t w[128];
       float top[4];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) top[c] = tmem_ld32_max<kExtra>(tm + 128 * x + 32 * c, w + 32 * c);
+      for (int c = 0; c < 4; ++c) top[c] = tmem_ld32_max<kCap>(tm + 128 * x + 32 * c, w + 32 * c);
       tmem_wait_ld();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&s.s_read[x]);            // the next scores may come
-      if (kExtra) {
+      if (kCap) {
         const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * in_cap;
-        if (p.cap > 0.f && __all_sync(0xffffffffu, most <= kTanhSpan)) {
+        if (__all_sync(0xffffffffu, most <= kTanhSpan)) {
 #pragma unroll
           for (int e = 0; e < 128; e += 2) {
             const uint64_t f = mul2(pair(__uint_as_float(w[e]), __uint_as_float(w[e + 1])), pair(in_cap, in_cap)), f2 = mul2(f, f);
@@ -356,21 +357,30 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             unpair(mul2(f, q), a, z);
             w[e] = __float_as_uint(a), w[e + 1] = __float_as_uint(z);
           }
-        } else if (p.cap > 0.f) {           // cap tanh(f) = cap - 2 cap / (e^{2 f} + 1)
+        } else {                            // cap tanh(f) = cap - 2 cap / (e^{2 f} + 1)
 #pragma unroll
           for (int e = 0; e < 128; ++e) {
             float z;
             asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(z) : "f"(ex2(__uint_as_float(w[e]) * cap_in) + 1.f));
             w[e] = __float_as_uint(fmaf(-2.f * cap_out, z, cap_out));
           }
+        }
+      }
+      if (kBias) {                          // with the scale where no cap has taken it in; packed where no key lies behind its row
+        const float far = (float)(seq.past + t - j0), times = kCap ? 1.f : scale2;
+        if (__all_sync(0xffffffffu, far >= 127.f)) {
+          const uint64_t times2 = pair(times, times), slope2 = pair(slope, slope), start2 = pair(-slope * far, -slope * far);
+#pragma unroll
+          for (int e = 0; e < 128; e += 2) {
+            float a, z;
+            unpair(fma2(pair(__uint_as_float(w[e]), __uint_as_float(w[e + 1])), times2,
+                        fma2(pair((float)e, (float)(e + 1)), slope2, start2)), a, z);
+            w[e] = __float_as_uint(a), w[e + 1] = __float_as_uint(z);
+          }
         } else {
 #pragma unroll
-          for (int e = 0; e < 128; ++e) w[e] = __float_as_uint(__uint_as_float(w[e]) * scale2);
-        }
-        if (p.slopes) {                     // (one conversion a row: those take the exponentials' units)
-          const float far = (float)(seq.past + t - j0);
-#pragma unroll
-          for (int e = 0; e < 128; ++e) w[e] = __float_as_uint(fmaf(-slope, fabsf(far - (float)e), __uint_as_float(w[e])));
+          for (int e = 0; e < 128; ++e)
+            w[e] = __float_as_uint(fmaf(-slope, fabsf(far - (float)e), __uint_as_float(w[e]) * times));
         }
       }
       const bool cut = !__all_sync(0xffffffffu, see0 <= j0 && see1 >= j0 + kKeys);
@@ -505,10 +515,10 @@ oal_status tc_map(CUtensorMap *m, const void *ptr, const cuuint64_t (&dims)[4], 
   return OAL_OK;
 }
 
-template <bool kExtra>
+template <bool kCap, bool kBias>
 oal_status run(const PagedArgs &p, cudaStream_t stream) {
   static bool done[kMaxDevices];
-  auto kernel = paged_tc_kernel<kExtra>;
+  auto kernel = paged_tc_kernel<kCap, kBias>;
   oal_status st = paged_need_smem(reinterpret_cast<const void *>(kernel), kTcBytes, done);
   if (st != OAL_OK) return st;
   const int nt = p.tile_rows / (2 * p.rho);
@@ -534,7 +544,8 @@ oal_status run(const PagedArgs &p, cudaStream_t stream) {
 int paged_tc_rows(int T, int rho) { return 2 * rho * std::min(T, 128 / rho); }
 
 oal_status launch_paged_tc(const PagedArgs &p, cudaStream_t stream) {
-  return p.cap > 0.f || p.slopes ? run<true>(p, stream) : run<false>(p, stream);
+  if (p.cap > 0.f) return p.slopes ? run<true, true>(p, stream) : run<true, false>(p, stream);
+  return p.slopes ? run<false, true>(p, stream) : run<false, false>(p, stream);
 }
 
 }  // namespace oal
