@@ -598,31 +598,47 @@ def oal_rope_plan(freq, axes=None, device="cuda"):
     return torch.from_numpy(plan).to(device)
 
 
-def _rows(t, name, dtype, shape, dev):
+def _rows(t, name, dtype, shape, at):
     """The strides of a tensor whose rows of 64 are contiguous."""
-    if not (t.dtype is dtype and t.shape == shape and t.device == dev):
-        raise OALError(OAL_ERR_INVALID_ARG, "%s must be %s %s on %s (got %s %s on %s)"
-                       % (name, dtype, tuple(shape), dev, t.dtype, tuple(t.shape), t.device))
     s = t.stride()
-    _need(s[3] == 1, "rows of %s must be contiguous" % name)
+    if not (t.dtype is dtype and t.shape == shape and t.get_device() == at and s[3] == 1):
+        raise OALError(OAL_ERR_INVALID_ARG, "%s must be %s %s on CUDA device %d, its rows contiguous (got %s %s on %s)"
+                       % (name, dtype, tuple(shape), at, t.dtype, tuple(t.shape), t.device))
     # (the stride of a dimension of one says nothing)
-    return s[:3] if min(shape) > 1 else tuple(x if n > 1 else 0 for x, n in zip(s[:3], shape))
+    return s[:3] if min(shape) > 1 else tuple([x if n > 1 else 0 for x, n in zip(s, shape[:3])])
 
 
 _strides6, _strides9 = struct.Struct("6q").pack, struct.Struct("9q").pack
 
 
-def _need_positions(positions, B, T, past, lengths, plan, dev):
-    if plan is not None:
-        _need_tensor(plan, "plan", torch.int64, (2, 32), dev)
-    if past is not None:
-        _need_tensor(past, "past", torch.int32, (B,), dev)
-    _need_lengths(lengths, B, dev)
+# The calls below check their arguments in one expression each, of the cheapest
+# questions that settle them (a token's call is worth a few microseconds); where
+# that fails, the slow checks say why.
+_I32, _I64, _F32, _BF16 = torch.int32, torch.int64, torch.float32, torch.bfloat16
+
+
+def _vector(t, n, at, dtype=_I32):
+    """Whether t is None or n contiguous numbers on device `at`."""
+    return t is None or (t.dtype is dtype and t.dim() == 1 and t.numel() == n
+                         and t.is_contiguous() and t.get_device() == at)
+
+
+def _positions(positions, B, T, past, lengths, plan, at, dev):
+    """Number of axes of the positions; checks them, past, lengths and plan."""
+    if not ((plan is None or (plan.dtype is _I64 and plan.shape == (2, 32) and plan.is_contiguous()
+                              and plan.get_device() == at))
+            and _vector(past, B, at) and _vector(lengths, B, at)):
+        if plan is not None:
+            _need_tensor(plan, "plan", _I64, (2, 32), dev)
+        if past is not None:
+            _need_tensor(past, "past", _I32, (B,), dev)
+        _need_lengths(lengths, B, dev)
     if positions is None:
         return 0
     _need(positions.dim() == 3, "positions must have 3 dimensions")
-    _need_tensor(positions, "positions", torch.int32, (positions.shape[0], B, T), dev)
-    return positions.shape[0]
+    n = positions.shape[0]
+    _need_tensor(positions, "positions", _I32, (n, B, T), dev)
+    return n
 
 
 def oal_rope(Q, K, plan, positions=None, past=None, lengths=None, form=OAL_ROPE_HALVES,
@@ -636,28 +652,36 @@ def oal_rope(Q, K, plan, positions=None, past=None, lengths=None, form=OAL_ROPE_
     lib = load_library()
     _need(Q.dim() == 4 and (K is None or K.dim() == 4), "Q and K must have 4 dimensions")
     _need(plan is not None, "plan is needed")
-    B, Hq, T, d = Q.shape
-    dt, dev, Hkv, t = _dtype_code(Q), Q.device, 0 if K is None else K.shape[1], Q.dtype
-    sq = _rows(Q, "Q", t, (B, Hq, T, d), dev)
-    sk = sq if K is None else _rows(K, "K", t, (B, Hkv, T, d), dev)
-    n_axes = _need_positions(positions, B, T, past, lengths, plan, dev)
-    if _elsewhere(dev):
+    q = Q.shape
+    B, Hq, T, d = q
+    at, t, dev = Q.get_device(), Q.dtype, Q.device
+    dt = _dtype_code(Q)
+    _need(at >= 0, "tensors must be CUDA tensors")
+    sq = _rows(Q, "Q", t, q, at)
+    if K is None:
+        Hkv, k, sk = 0, None, sq
+    else:
+        Hkv = K.size(1)
+        k = (B, Hkv, T, d)
+        sk = _rows(K, "K", t, k, at)
+    n_axes = _positions(positions, B, T, past, lengths, plan, at, dev)
+    if at != torch._C._cuda_getDevice():
         with torch.cuda.device(dev):
             return oal_rope(Q, K, plan, positions, past, lengths, form, inverse, Yq, Yk, stream)
     made = []
     make = torch.empty if lengths is None else torch.zeros
     if Yq is None:
-        Yq = make(B, Hq, T, d, dtype=t, device=dev)
+        Yq = make(q, dtype=t, device=dev)
         made.append(Yq)
     else:
-        _need_tensor(Yq, "Yq", t, (B, Hq, T, d), dev)
+        _need_tensor(Yq, "Yq", t, q, dev)
     if K is None:
         _need(Yk is None, "Yk without K")
     elif Yk is None:
-        Yk = make(B, Hkv, T, d, dtype=t, device=dev)
+        Yk = make(k, dtype=t, device=dev)
         made.append(Yk)
     else:
-        _need_tensor(Yk, "Yk", t, (B, Hkv, T, d), dev)
+        _need_tensor(Yk, "Yk", t, k, dev)
     _check(lib.oal_rope(Q.data_ptr(), _ptr_or_null(K), dt, _strides6(*sq, *sk), B, Hq, Hkv, T, d,
                         plan.data_ptr(), form, _ptr_or_null(positions), n_axes, _ptr_or_null(past),
                         _ptr_or_null(lengths), bool(inverse), Yq.data_ptr(), _ptr_or_null(Yk),
@@ -665,21 +689,24 @@ def oal_rope(Q, K, plan, positions=None, past=None, lengths=None, form=OAL_ROPE_
     return Yq, Yk
 
 
-def _pages(Kp, Vp, Hkv, table, B, dtype, dev):
-    """Number of pages, their size and stride, entries of the table."""
-    _need(Kp.dim() == 4 and table.dim() == 2, "Kp must have 4 dimensions, table 2")
-    n, h, P, d = Kp.shape
-    if not (Kp.dtype is dtype and Vp.dtype is dtype and h == Hkv and Vp.shape == Kp.shape
-            and Kp.device == dev and Vp.device == dev):
-        raise OALError(OAL_ERR_INVALID_ARG, "Kp and Vp must be %s [n_pages,%d,page_size,%d] on %s"
-                       % (dtype, Hkv, d, dev))
-    _need_tensor(table, "table", torch.int32, (B, table.shape[1]), dev)
+def _pages(Kp, Vp, pages, Hkv, d, table, B, dtype, at):
+    """Elements from page to page, entries of the table; checks the cache."""
+    n, h, P, dk = pages
+    if not (Kp.dtype is dtype and Vp.dtype is dtype and h == Hkv and dk == d and Vp.shape == pages
+            and Kp.get_device() == at and Vp.get_device() == at):
+        raise OALError(OAL_ERR_INVALID_ARG, "Kp and Vp must be %s [n_pages,%d,page_size,%d] on CUDA device %d"
+                       % (dtype, Hkv, d, at))
+    if not (table.dtype is _I32 and table.dim() == 2 and table.size(0) == B and table.is_contiguous()
+            and table.get_device() == at):
+        raise OALError(OAL_ERR_INVALID_ARG, "table must be contiguous int32 [%d,max_pages] on CUDA device %d" % (B, at))
+    if Kp.is_contiguous() and Vp.is_contiguous():
+        return h * P * d, table.size(1)
     sk, sv = Kp.stride(), Vp.stride()
     _need((n < 2 or sk[0] == sv[0]) and (h < 2 or sk[1] == sv[1] == P * d)
           and sk[2] == sv[2] == d and sk[3] == sv[3] == 1,
           "the pages of Kp and Vp must be contiguous and equally far apart")
     # (one page: how far the next would be is anyone's guess)
-    return n, P, sk[0] if n > 1 else h * P * d, table.shape[1]
+    return sk[0] if n > 1 else h * P * d, table.size(1)
 
 
 def oal_page_append(Q, K, V, plan, Kp, Vp, table, past, positions=None, lengths=None,
@@ -690,18 +717,25 @@ def oal_page_append(Q, K, V, plan, Kp, Vp, table, past, positions=None, lengths=
     [B,Hq,T,64] is turned along into Yq (both may be None); plan None: nothing
     is turned.  Q, K, V may be views whose rows are contiguous.  Returns Yq."""
     lib = load_library()
-    _need(K.dim() == 4 and V.dim() == 4 and (Q is None or Q.dim() == 4),
-          "Q, K and V must have 4 dimensions")
-    B, Hkv, T, d = K.shape
-    dt, dev, dv, t = _dtype_code(K), K.device, V.shape[3], K.dtype
-    Hq = 0 if Q is None else Q.shape[1]
-    sk = _rows(K, "K", t, (B, Hkv, T, d), dev)
-    sv = _rows(V, "V", t, (B, Hkv, T, dv), dev)
-    sq = sk if Q is None else _rows(Q, "Q", t, (B, Hq, T, d), dev)
+    _need(K.dim() == 4 and V.dim() == 4 and Kp.dim() == 4 and (Q is None or Q.dim() == 4),
+          "Q, K, V, Kp and Vp must have 4 dimensions")
     _need(past is not None, "past is needed")
-    n_axes = _need_positions(positions, B, T, past, lengths, plan, dev)
-    n, P, apart, most = _pages(Kp, Vp, Hkv, table, B, t, dev)
-    if _elsewhere(dev):
+    k, pages = K.shape, Kp.shape
+    B, Hkv, T, d = k
+    at, t, dev = K.get_device(), K.dtype, K.device
+    dt = _dtype_code(K)
+    _need(at >= 0, "tensors must be CUDA tensors")
+    sk = _rows(K, "K", t, k, at)
+    sv = _rows(V, "V", t, k, at)
+    if Q is None:
+        Hq, q, sq = 0, None, sk
+    else:
+        Hq = Q.size(1)
+        q = (B, Hq, T, d)
+        sq = _rows(Q, "Q", t, q, at)
+    n_axes = _positions(positions, B, T, past, lengths, plan, at, dev)
+    apart, most = _pages(Kp, Vp, pages, Hkv, d, table, B, t, at)
+    if at != torch._C._cuda_getDevice():
         with torch.cuda.device(dev):
             return oal_page_append(Q, K, V, plan, Kp, Vp, table, past, positions, lengths, form, Yq,
                                    stream)
@@ -709,15 +743,15 @@ def oal_page_append(Q, K, V, plan, Kp, Vp, table, past, positions=None, lengths=
     if Q is None:
         _need(Yq is None, "Yq without Q")
     elif Yq is None:
-        Yq = (torch.empty if lengths is None else torch.zeros)(B, Hq, T, d, dtype=t, device=dev)
+        Yq = (torch.empty if lengths is None else torch.zeros)(q, dtype=t, device=dev)
         made.append(Yq)
     else:
-        _need_tensor(Yq, "Yq", t, (B, Hq, T, d), dev)
+        _need_tensor(Yq, "Yq", t, q, dev)
     _check(lib.oal_page_append(_ptr_or_null(Q), K.data_ptr(), V.data_ptr(), dt,
-                               _strides9(*sq, *sk, *sv), B, Hq, Hkv, T, d, dv, _ptr_or_null(plan),
+                               _strides9(*sq, *sk, *sv), B, Hq, Hkv, T, d, d, _ptr_or_null(plan),
                                form, _ptr_or_null(positions), n_axes, past.data_ptr(),
-                               _ptr_or_null(lengths), Kp.data_ptr(), Vp.data_ptr(), n, P, apart,
-                               table.data_ptr(), most, _ptr_or_null(Yq),
+                               _ptr_or_null(lengths), Kp.data_ptr(), Vp.data_ptr(), pages[0],
+                               pages[2], apart, table.data_ptr(), most, _ptr_or_null(Yq),
                                _stream_on(dev, stream, made)))
     return Yq
 
@@ -745,42 +779,52 @@ def oal_paged_attention(Q, Kp, Vp, table, past, lengths=None, scale=0.125, cap=0
     there), tokens that see nothing get zeros."""
     lib = load_library()
     _need(Q.dim() == 4 and Kp.dim() == 4, "Q, Kp and Vp must have 4 dimensions")
-    B, Hq, T, d = Q.shape
-    dt, dev, t, Hkv, dv = _dtype_code(Q), Q.device, Q.dtype, Kp.shape[1], Vp.shape[-1]
-    if not Q.is_contiguous():
-        _need_tensor(Q, "Q", t, (B, Hq, T, d), dev)
-    n, P, apart, most = _pages(Kp, Vp, Hkv, table, B, t, dev)
-    _need_tensor(past, "past", torch.int32, (B,), dev)
-    _need_lengths(lengths, B, dev)
-    if slopes is not None:
-        _need_tensor(slopes, "slopes", torch.float32, (Hq,), dev)
-    if prefix is not None:
-        _need_tensor(prefix, "prefix", torch.int32, (B,), dev)
+    q, pages = Q.shape, Kp.shape
+    B, Hq, T, d = q
+    n, Hkv, P, _ = pages
+    at, t = Q.get_device(), Q.dtype
+    dt = _dtype_code(Q)
+    _need(at >= 0 and Q.is_contiguous(), "Q must be a contiguous CUDA tensor")
+    apart, most = _pages(Kp, Vp, pages, Hkv, d, table, B, t, at)
+    if not (past is not None and _vector(past, B, at) and _vector(lengths, B, at)
+            and _vector(slopes, Hq, at, _F32) and _vector(prefix, B, at)):
+        dev = Q.device
+        _need(past is not None, "past is needed")
+        _need_tensor(past, "past", _I32, (B,), dev)
+        _need_lengths(lengths, B, dev)
+        if slopes is not None:
+            _need_tensor(slopes, "slopes", _F32, (Hq,), dev)
+        if prefix is not None:
+            _need_tensor(prefix, "prefix", _I32, (B,), dev)
     if first is not None:
-        _need_tensor(first, "first", torch.int32, (B, T), dev)
-    if _elsewhere(dev):
-        with torch.cuda.device(dev):
+        _need_tensor(first, "first", _I32, (B, T), Q.device)
+    if at != torch._C._cuda_getDevice():
+        with torch.cuda.device(at):
             return oal_paged_attention(Q, Kp, Vp, table, past, lengths, scale, cap, window, slopes,
                                        prefix, first, Y, workspace, stream)
     made = []
     if Y is None:
-        Y = (torch.empty if lengths is None else torch.zeros)(B, Hq, T, dv, dtype=t, device=dev)
+        Y = (torch.empty if lengths is None else torch.zeros)(q, dtype=t, device=Q.device)
         made.append(Y)
-    else:
-        _need_tensor(Y, "Y", t, (B, Hq, T, dv), dev)
+    elif not (Y.dtype is t and Y.shape == q and Y.is_contiguous() and Y.get_device() == at):
+        _need_tensor(Y, "Y", t, q, Q.device)
     if workspace is None:
-        room = _paged_attention_bytes(B, Hq, Hkv, T, d, dv, dt, P, most)
-        workspace = torch.empty(room, dtype=torch.uint8, device=dev)
+        room = _paged_attention_bytes(B, Hq, Hkv, T, d, d, dt, P, most)
+        workspace = torch.empty(room, dtype=torch.uint8, device=Q.device)
         made.append(workspace)
     else:
-        _need_tensor(workspace, "workspace", workspace.dtype, workspace.shape, dev)
+        _need_tensor(workspace, "workspace", workspace.dtype, workspace.shape, Q.device)
         room = workspace.numel() * workspace.element_size()
-    _check(lib.oal_paged_attention(Q.data_ptr(), dt, B, Hq, Hkv, T, d, dv, Kp.data_ptr(),
-                                   Vp.data_ptr(), n, P, apart, table.data_ptr(), most,
-                                   past.data_ptr(), _ptr_or_null(lengths), scale, cap, window,
-                                   _ptr_or_null(slopes), _ptr_or_null(prefix), _ptr_or_null(first),
-                                   Y.data_ptr(), workspace.data_ptr(), room,
-                                   _stream_on(dev, stream, made)))
+    if stream is None:
+        handle = torch._C._cuda_getCurrentRawStream(at)
+    else:
+        handle = _stream_on(Q.device, stream, made)
+    _check(lib.oal_paged_attention(
+        Q.data_ptr(), dt, B, Hq, Hkv, T, d, d, Kp.data_ptr(), Vp.data_ptr(), n, P, apart,
+        table.data_ptr(), most, past.data_ptr(), None if lengths is None else lengths.data_ptr(),
+        scale, cap, window, None if slopes is None else slopes.data_ptr(),
+        None if prefix is None else prefix.data_ptr(), None if first is None else first.data_ptr(),
+        Y.data_ptr(), workspace.data_ptr(), room, handle))
     return Y
 
 
