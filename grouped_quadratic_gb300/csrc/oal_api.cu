@@ -799,7 +799,8 @@ oal_status oal_paged_attention(const void *Q, oal_dtype dtype, int B, int Hq, in
   if (slopes) OAL_TRY(check_ptr(slopes, "slopes"));
   if (prefix) OAL_TRY(check_ptr(prefix, "prefix"));
   if (first) OAL_TRY(check_ptr(first, "first"));
-  OAL_TRY(check_workspace(workspace, workspace_bytes, oal::paged_workspace_bytes(p, dtype == OAL_BF16)));
+  const size_t need = oal::paged_workspace_bytes(p, dtype == OAL_BF16);
+  if (workspace || need > 256) OAL_TRY(check_workspace(workspace, workspace_bytes, need));
   p.Q = Q, p.Kp = Kp, p.Vp = Vp, p.Y = Y, p.table = table, p.past = past, p.lengths = lengths;
   p.scale = scale, p.cap = cap, p.window = window;
   p.slopes = slopes, p.prefix = prefix, p.first = first;

@@ -808,23 +808,31 @@ def oal_paged_attention(Q, Kp, Vp, table, past, lengths=None, scale=0.125, cap=0
         made.append(Y)
     elif not (Y.dtype is t and Y.shape == q and Y.is_contiguous() and Y.get_device() == at):
         _need_tensor(Y, "Y", t, q, Q.device)
-    if workspace is None:
-        room = _paged_attention_bytes(B, Hq, Hkv, T, d, d, dt, P, most)
-        workspace = torch.empty(room, dtype=torch.uint8, device=Q.device)
-        made.append(workspace)
-    else:
-        _need_tensor(workspace, "workspace", workspace.dtype, workspace.shape, Q.device)
-        room = workspace.numel() * workspace.element_size()
     if stream is None:
         handle = torch._C._cuda_getCurrentRawStream(at)
     else:
         handle = _stream_on(Q.device, stream, made)
-    _check(lib.oal_paged_attention(
-        Q.data_ptr(), dt, B, Hq, Hkv, T, d, d, Kp.data_ptr(), Vp.data_ptr(), n, P, apart,
-        table.data_ptr(), most, past.data_ptr(), None if lengths is None else lengths.data_ptr(),
-        scale, cap, window, None if slopes is None else slopes.data_ptr(),
-        None if prefix is None else prefix.data_ptr(), None if first is None else first.data_ptr(),
-        Y.data_ptr(), workspace.data_ptr(), room, handle))
+    # A workspace of the call's own comes from the allocator as memory of the stream
+    # that it launches on, and goes back in that stream's order.
+    room, own = _paged_attention_bytes(B, Hq, Hkv, T, d, d, dt, P, most), None
+    if workspace is not None:
+        _need_tensor(workspace, "workspace", workspace.dtype, workspace.shape, Q.device)
+        room, where = workspace.numel() * workspace.element_size(), workspace.data_ptr()
+    elif room > 256:
+        where = own = torch._C._cuda_cudaCachingAllocator_raw_alloc(room, handle)
+    else:
+        where = None
+    try:
+        status = lib.oal_paged_attention(
+            Q.data_ptr(), dt, B, Hq, Hkv, T, d, d, Kp.data_ptr(), Vp.data_ptr(), n, P, apart,
+            table.data_ptr(), most, past.data_ptr(), None if lengths is None else lengths.data_ptr(),
+            scale, cap, window, None if slopes is None else slopes.data_ptr(),
+            None if prefix is None else prefix.data_ptr(), None if first is None else first.data_ptr(),
+            Y.data_ptr(), where, room, handle)
+    finally:
+        if own is not None:
+            torch._C._cuda_cudaCachingAllocator_raw_delete(own)
+    _check(status)
     return Y
 
 

@@ -431,8 +431,8 @@ oal_status oal_page_append(const void *Q, const void *K, const void *V, oal_dtyp
  *  see keys or values that are not finite, or whose scores leave fp32, have
  *  unspecified results.
  *  workspace  >= oal_paged_attention_workspace_bytes(...) bytes, 256-byte
- *           aligned, contents need not be initialised.  Calls that may overlap
- *           on the GPU need one each.
+ *           aligned, contents need not be initialised; 256 bytes: none is needed,
+ *           it may be NULL.  Calls that may overlap on the GPU need one each.
  * Arithmetic: OAL_F32 in fp32 on the CUDA cores.  OAL_BF16 on the tensor cores;
  * scores, maxima, sums and results in fp32, softmax's weights rounded to bf16
  * once.  Deterministic.  Supported: d == dv == 64, Hq / Hkv <= 128,

@@ -77,7 +77,7 @@ def test_append_refuses(lib, kw, status):
     (dict(dtype=3), 1), (dict(Hq=258), 2), (dict(B=40000), 2), (dict(T=1 << 28), 2), (dict(scale=0.0), 1),
     (dict(scale=-1.0), 1), (dict(scale=math.inf), 1), (dict(scale=math.nan), 1), (dict(cap=-1.0), 1),
     (dict(cap=math.nan), 1), (dict(cap=1e-40), 1), (dict(B=1 << 13, T=1 << 19), 2), (dict(cap=math.inf), 1), (dict(window=-1), 1), (dict(Q=NULL), 1), (dict(Y=ODD), 1),
-    (dict(lengths=ODD), 1), (dict(slopes=ODD), 1), (dict(prefix=ODD), 1), (dict(first=ODD), 1), (dict(ws=NULL), 1),
+    (dict(lengths=ODD), 1), (dict(slopes=ODD), 1), (dict(prefix=ODD), 1), (dict(first=ODD), 1), (dict(ws=NULL, T=1, max_pages=1 << 16), 1),
     (dict(ws=ctypes.c_void_p(4096 + 16)), 1), (dict(ws_bytes=100), 1),
     (dict(T=1, max_pages=1 << 16, ws_bytes=1024), 1)])
 def test_attention_refuses(lib, kw, status):
