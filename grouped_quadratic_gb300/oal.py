@@ -623,22 +623,32 @@ def _vector(t, n, at, dtype=_I32):
                          and t.is_contiguous() and t.get_device() == at)
 
 
-def _positions(positions, B, T, past, lengths, plan, at, dev):
-    """Number of axes of the positions; checks them, past, lengths and plan."""
+def _positions(positions, B, T, past, lengths, plan, at, x):
+    """Number of axes of the positions; checks them, past, lengths and plan.  x: a tensor on device `at`."""
     if not ((plan is None or (plan.dtype is _I64 and plan.shape == (2, 32) and plan.is_contiguous()
                               and plan.get_device() == at))
             and _vector(past, B, at) and _vector(lengths, B, at)):
         if plan is not None:
-            _need_tensor(plan, "plan", _I64, (2, 32), dev)
+            _need_tensor(plan, "plan", _I64, (2, 32), x.device)
         if past is not None:
-            _need_tensor(past, "past", _I32, (B,), dev)
-        _need_lengths(lengths, B, dev)
+            _need_tensor(past, "past", _I32, (B,), x.device)
+        _need_lengths(lengths, B, x.device)
     if positions is None:
         return 0
     _need(positions.dim() == 3, "positions must have 3 dimensions")
     n = positions.shape[0]
-    _need_tensor(positions, "positions", _I32, (n, B, T), dev)
+    _need_tensor(positions, "positions", _I32, (n, B, T), x.device)
     return n
+
+
+def _given(t, name, dtype, shape, at, x):
+    """An output that the caller gives."""
+    if not (t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == at):
+        _need_tensor(t, name, dtype, shape, x.device)
+
+
+def _handle(at, x, stream, made):
+    return torch._C._cuda_getCurrentRawStream(at) if stream is None else _stream_on(x.device, stream, made)
 
 
 def oal_rope(Q, K, plan, positions=None, past=None, lengths=None, form=OAL_ROPE_HALVES,
@@ -654,7 +664,7 @@ def oal_rope(Q, K, plan, positions=None, past=None, lengths=None, form=OAL_ROPE_
     _need(plan is not None, "plan is needed")
     q = Q.shape
     B, Hq, T, d = q
-    at, t, dev = Q.get_device(), Q.dtype, Q.device
+    at, t = Q.get_device(), Q.dtype
     dt = _dtype_code(Q)
     _need(at >= 0, "tensors must be CUDA tensors")
     sq = _rows(Q, "Q", t, q, at)
@@ -664,28 +674,28 @@ def oal_rope(Q, K, plan, positions=None, past=None, lengths=None, form=OAL_ROPE_
         Hkv = K.size(1)
         k = (B, Hkv, T, d)
         sk = _rows(K, "K", t, k, at)
-    n_axes = _positions(positions, B, T, past, lengths, plan, at, dev)
+    n_axes = _positions(positions, B, T, past, lengths, plan, at, Q)
     if at != torch._C._cuda_getDevice():
-        with torch.cuda.device(dev):
+        with torch.cuda.device(at):
             return oal_rope(Q, K, plan, positions, past, lengths, form, inverse, Yq, Yk, stream)
     made = []
     make = torch.empty if lengths is None else torch.zeros
     if Yq is None:
-        Yq = make(q, dtype=t, device=dev)
+        Yq = make(q, dtype=t, device=Q.device)
         made.append(Yq)
     else:
-        _need_tensor(Yq, "Yq", t, q, dev)
+        _given(Yq, "Yq", t, q, at, Q)
     if K is None:
         _need(Yk is None, "Yk without K")
     elif Yk is None:
-        Yk = make(k, dtype=t, device=dev)
+        Yk = make(k, dtype=t, device=Q.device)
         made.append(Yk)
     else:
-        _need_tensor(Yk, "Yk", t, k, dev)
+        _given(Yk, "Yk", t, k, at, Q)
     _check(lib.oal_rope(Q.data_ptr(), _ptr_or_null(K), dt, _strides6(*sq, *sk), B, Hq, Hkv, T, d,
                         plan.data_ptr(), form, _ptr_or_null(positions), n_axes, _ptr_or_null(past),
                         _ptr_or_null(lengths), bool(inverse), Yq.data_ptr(), _ptr_or_null(Yk),
-                        _stream_on(dev, stream, made)))
+                        _handle(at, Q, stream, made)))
     return Yq, Yk
 
 
@@ -722,7 +732,7 @@ def oal_page_append(Q, K, V, plan, Kp, Vp, table, past, positions=None, lengths=
     _need(past is not None, "past is needed")
     k, pages = K.shape, Kp.shape
     B, Hkv, T, d = k
-    at, t, dev = K.get_device(), K.dtype, K.device
+    at, t = K.get_device(), K.dtype
     dt = _dtype_code(K)
     _need(at >= 0, "tensors must be CUDA tensors")
     sk = _rows(K, "K", t, k, at)
@@ -733,26 +743,26 @@ def oal_page_append(Q, K, V, plan, Kp, Vp, table, past, positions=None, lengths=
         Hq = Q.size(1)
         q = (B, Hq, T, d)
         sq = _rows(Q, "Q", t, q, at)
-    n_axes = _positions(positions, B, T, past, lengths, plan, at, dev)
+    n_axes = _positions(positions, B, T, past, lengths, plan, at, K)
     apart, most = _pages(Kp, Vp, pages, Hkv, d, table, B, t, at)
     if at != torch._C._cuda_getDevice():
-        with torch.cuda.device(dev):
+        with torch.cuda.device(at):
             return oal_page_append(Q, K, V, plan, Kp, Vp, table, past, positions, lengths, form, Yq,
                                    stream)
     made = []
     if Q is None:
         _need(Yq is None, "Yq without Q")
     elif Yq is None:
-        Yq = (torch.empty if lengths is None else torch.zeros)(q, dtype=t, device=dev)
+        Yq = (torch.empty if lengths is None else torch.zeros)(q, dtype=t, device=K.device)
         made.append(Yq)
     else:
-        _need_tensor(Yq, "Yq", t, q, dev)
+        _given(Yq, "Yq", t, q, at, K)
     _check(lib.oal_page_append(_ptr_or_null(Q), K.data_ptr(), V.data_ptr(), dt,
                                _strides9(*sq, *sk, *sv), B, Hq, Hkv, T, d, d, _ptr_or_null(plan),
                                form, _ptr_or_null(positions), n_axes, past.data_ptr(),
                                _ptr_or_null(lengths), Kp.data_ptr(), Vp.data_ptr(), pages[0],
                                pages[2], apart, table.data_ptr(), most, _ptr_or_null(Yq),
-                               _stream_on(dev, stream, made)))
+                               _handle(at, K, stream, made)))
     return Yq
 
 
@@ -806,12 +816,9 @@ def oal_paged_attention(Q, Kp, Vp, table, past, lengths=None, scale=0.125, cap=0
     if Y is None:
         Y = (torch.empty if lengths is None else torch.zeros)(q, dtype=t, device=Q.device)
         made.append(Y)
-    elif not (Y.dtype is t and Y.shape == q and Y.is_contiguous() and Y.get_device() == at):
-        _need_tensor(Y, "Y", t, q, Q.device)
-    if stream is None:
-        handle = torch._C._cuda_getCurrentRawStream(at)
     else:
-        handle = _stream_on(Q.device, stream, made)
+        _given(Y, "Y", t, q, at, Q)
+    handle = _handle(at, Q, stream, made)
     # A workspace of the call's own comes from the allocator as memory of the stream
     # that it launches on, and goes back in that stream's order.
     room, own = _paged_attention_bytes(B, Hq, Hkv, T, d, d, dt, P, most), None

@@ -572,3 +572,38 @@ def test_serving_run(oal, dtype):
             d = 4e-5 if dtype is F32 else 2.0 ** -8 + 2.0 ** -8 * 3.2
             assert ((Y[b, :, :new[b]].double() - want).abs() <= size * d + want.abs() * HALF[dtype]).all()
             past[b] += new[b]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_rotations_feed_the_other_layers(oal, dtype):
+    """The quadratic and the gated layer on what a rotation has just written, and paged attention on what an append
+    has: the same bits as with a pause between the calls."""
+    B, Hq, Hkv, T = 2, 4, 2, 300
+    L = torch.tril(0.2 * torch.randn(Hq, 3, 3, generator=torch.Generator().manual_seed(1))).cuda() + 0.6 * torch.eye(3, device="cuda")
+    group = torch.ones(Hq, 64, dtype=torch.int32, device="cuda")
+    group[:, :5] = 2
+    tables = oal.oal_expand_coeffs(L, group, 1e-6, oal.OAL_STATE_PACKED)
+    plan, gate = oal.oal_rope_plan(FREQ), torch.full((B, Hkv, T), -0.05, device="cuda")
+    c = Cache(B, Hkv, [10, 70], [T, T], 16, dtype, seed=90)
+    Yq, Yk = torch.empty(B, Hq, T, 64, dtype=dtype, device="cuda"), torch.empty(B, Hkv, T, 64, dtype=dtype, device="cuda")
+    layers = [lambda V: oal.oal_prefill(Yq, Yk, V, L, group, 1e-6, *tables, oal.OAL_STATE_PACKED),
+              lambda V: oal.oal_gated_prefill(Yq, Yk, V, gate),
+              lambda V: [oal.oal_paged_attention(Yq, c.Kp, c.Vp, c.table, c.past)]]
+    for step in range(4):
+        Q, K, V = (draw((B, h, T, 64), dtype, 7 * step + i, 0.7) for i, h in enumerate((Hq, Hkv, Hkv)))
+        for i, layer in enumerate(layers):
+            got = []
+            for pause in (False, True):
+                Yq.fill_(9.0), Yk.fill_(9.0)
+                torch.cuda.synchronize()
+                if i < 2:
+                    oal.oal_rope(Q, K, plan, past=c.past, Yq=Yq, Yk=Yk)
+                else:
+                    c.Kp.fill_(9.0), c.Vp.fill_(9.0)
+                    oal.oal_page_append(Q, K, V, plan, c.Kp, c.Vp, c.table, c.past, Yq=Yq)
+                if pause:
+                    torch.cuda.synchronize()
+                got.append(layer(V))
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(*got))
+    oal.oal_sync_status()
