@@ -119,6 +119,7 @@ oal_status paged_need_smem(const void *kernel, size_t bytes, bool (&done)[kMaxDe
 }
 
 constexpr int kSplitLeast = 256;          // keys of a split at least
+constexpr int kRowsMost = 32;             // rows a KV head up to which bf16 goes by paged_rows_kernel
 
 // The kernel's tile of rows, and into how many pieces the keys of a tile may be
 // cut: as many as fill the GPU, where the tiles alone do not.  The grid is made
@@ -135,7 +136,7 @@ constexpr int kSplitLeast = 256;          // keys of a split at least
 static long long plan_tiles(PagedArgs &p, int is_bf16) {
   const long long rows = (long long)p.T * p.rho, units = (long long)p.B * p.Hkv;
   long long want;                         // blocks
-  if (is_bf16 && rows > 32) {
+  if (is_bf16 && rows > kRowsMost) {
     p.tile_rows = paged_tc_rows(p.T, p.rho);
     want = 152 * 4;
   } else if (is_bf16) {
@@ -149,12 +150,28 @@ static long long plan_tiles(PagedArgs &p, int is_bf16) {
   const long long most = (((long long)p.max_pages << p.page_shift) + kSplitLeast - 1) / kSplitLeast;
   return std::max<long long>(1, std::min(most, want / tiles));
 }
-static void plan_split(PagedArgs &p, long long pieces) {
+static void plan_split(PagedArgs &p, int is_bf16, long long pieces) {
   const long long room = (long long)p.max_pages << p.page_shift;
   long long span = room;                  // keys from a tile's first to its last
   if (p.window && !p.prefix) span = std::min(room, (long long)p.window + p.tile_rows / p.rho + 1 + kSplitAlign);
-  const long long keys = std::max<long long>(kSplitLeast, (span + pieces - 1) / pieces);
-  p.split_keys = (int)((keys + kSplitAlign - 1) / kSplitAlign * kSplitAlign);
+  auto keys_of = [&](long long n) {
+    const long long keys = std::max<long long>(kSplitLeast, (span + n - 1) / n);
+    return (keys + kSplitAlign - 1) / kSplitAlign * kSplitAlign;
+  };
+  const long long rows = (long long)p.T * p.rho, units = (long long)p.B * p.Hkv;
+  if (is_bf16 && rows > kRowsMost && pieces > 1) {
+    // paged_tc_kernel: the fewest waves of one block per SM, a wave's time in keys: its blocks' and 700 that a block
+    // costs beside; 300 and the partial results of 130 rows a key for the join.  114 tiles on 65536 keys: 4 pieces,
+    // three full waves, 371 us; 5 pieces 399, 3 pieces 465.  16 tiles on 4300 keys: 3 pieces 23.0, 2 and 4 26.5, 28.2.
+    const long long tiles = units * ((rows + p.tile_rows - 1) / p.tile_rows), most = pieces;
+    long long best = INT64_MAX;
+    for (long long n = 1; n <= most; ++n) {
+      const long long keys = keys_of(n), cuts = (span + keys - 1) / keys;
+      const long long cost = (tiles * cuts + 151) / 152 * (keys + 700) + (cuts > 1 ? 300 + units * rows * cuts / 130 : 0);
+      if (cost < best) best = cost, pieces = n;
+    }
+  }
+  p.split_keys = (int)keys_of(pieces);
   p.splits = (int)std::max<long long>(1, (span + p.split_keys - 1) / p.split_keys);
 }
 
@@ -168,11 +185,11 @@ size_t paged_workspace_bytes(PagedArgs p, int is_bf16) {
 }
 
 oal_status launch_paged(PagedArgs p, int is_bf16, void *ws, cudaStream_t stream) {
-  plan_split(p, plan_tiles(p, is_bf16));
+  plan_split(p, is_bf16, plan_tiles(p, is_bf16));
   p.part_o = static_cast<float *>(ws);
   p.part_ml = reinterpret_cast<float2 *>(p.part_o + part_rows(p, p.splits) * 64);
   if (!is_bf16) return launch_paged_simt(p, stream);
-  return (long long)p.T * p.rho > 32 ? launch_paged_tc(p, stream) : launch_paged_rows(p, stream);
+  return (long long)p.T * p.rho > kRowsMost ? launch_paged_tc(p, stream) : launch_paged_rows(p, stream);
 }
 
 }  // namespace oal
