@@ -55,6 +55,7 @@ paged_rows_kernel(PagedArgs p) {
   pdl_wait();
   extern __shared__ __align__(128) uint8_t smem_raw[];
   constexpr int kRows = 16 * kTiles;
+  static_assert(kRing >= kRows * 66 * 4, "the warps' results meet where the rings were");
   const int bh = blockIdx.y, b = bh / p.Hkv, kv = bh % p.Hkv, split = blockIdx.z;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   const int r0 = blockIdx.x * kRows, all = p.T * p.rho;
@@ -104,10 +105,10 @@ paged_rows_kernel(PagedArgs p) {
   const int first = (k0 & ~(kGroup - 1)) + warp * kGroup;
   const int steps = first < k1 ? (k1 - first + kWarps * kGroup - 1) / (kWarps * kGroup) : 0;
   // pages of a group's two halves (a page has 16 keys at least); -1: no key of it is wanted
-  int page[2];
+  int page[kGroup / 16];
   auto look = [&](int it) {
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
+    for (int u = 0; u < kGroup / 16; ++u) {
       const int j = first + it * kWarps * kGroup + 16 * u;
       page[u] = it < steps && j < k1 && j + 16 > k0 ? paged_page(p, b, j) : -1;
     }
@@ -154,9 +155,9 @@ paged_rows_kernel(PagedArgs p) {
     look(it + kStages);
     const int j0 = first + it * kWarps * kGroup;
     const uint32_t kt = ring + it % kStages * (2 * kGroupBytes), vt = kt + kGroupBytes;
-    float s[kTiles][4][4];
+    float s[kTiles][kGroup / 8][4];
 #pragma unroll
-    for (int n = 0; n < 4; ++n) {
+    for (int n = 0; n < kGroup / 8; ++n) {
 #pragma unroll
       for (int i = 0; i < kTiles; ++i)
 #pragma unroll
@@ -175,7 +176,7 @@ paged_rows_kernel(PagedArgs p) {
       float top[2] = {m[i][0], m[i][1]};
       if (kExtra && p.cap > 0.f) {          // cap tanh(x) = cap - 2 cap / (e^{2 x} + 1)
 #pragma unroll
-        for (int n = 0; n < 4; ++n)
+        for (int n = 0; n < kGroup / 8; ++n)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             float w;
@@ -185,21 +186,21 @@ paged_rows_kernel(PagedArgs p) {
           }
       } else {
 #pragma unroll
-        for (int n = 0; n < 4; ++n)
+        for (int n = 0; n < kGroup / 8; ++n)
 #pragma unroll
           for (int e = 0; e < 4; ++e) s[i][n][e] *= scale2;
       }
       if (kExtra) {                         // (one conversion a row: those take the exponentials' units)
         const float far[2] = {(float)(row_at[i][0] - j0 - 2 * c), (float)(row_at[i][1] - j0 - 2 * c)};
 #pragma unroll
-        for (int n = 0; n < 4; ++n)
+        for (int n = 0; n < kGroup / 8; ++n)
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             s[i][n][e] = fmaf(-slope[i][e >> 1], fabsf(far[e >> 1] - (float)(8 * n + (e & 1))), s[i][n][e]);
       }
       if (!whole) {
 #pragma unroll
-        for (int n = 0; n < 4; ++n)
+        for (int n = 0; n < kGroup / 8; ++n)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int u = e >> 1, j = j0 + 8 * n + 2 * c + (e & 1);
@@ -207,7 +208,7 @@ paged_rows_kernel(PagedArgs p) {
           }
       }
 #pragma unroll
-      for (int n = 0; n < 4; ++n)
+      for (int n = 0; n < kGroup / 8; ++n)
 #pragma unroll
         for (int e = 0; e < 4; ++e) top[e >> 1] = fmaxf(top[e >> 1], s[i][n][e]);
       float keep[2];
@@ -230,7 +231,7 @@ paged_rows_kernel(PagedArgs p) {
           for (int e = 0; e < 4; ++e) o[i][n][e] *= keep[e >> 1];
       }
 #pragma unroll
-      for (int n = 0; n < 4; ++n)
+      for (int n = 0; n < kGroup / 8; ++n)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(s[i][n][e]) : "f"(s[i][n][e] - top[e >> 1]));
@@ -239,7 +240,7 @@ paged_rows_kernel(PagedArgs p) {
     }
     // the weights, rounded to bf16 (2^-9 of each at most), are left factors as they lie
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
+    for (int k = 0; k < kGroup / 16; ++k) {
       uint32_t w[kTiles][4];
 #pragma unroll
       for (int i = 0; i < kTiles; ++i)

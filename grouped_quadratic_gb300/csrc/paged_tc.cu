@@ -578,7 +578,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             w[16 * c + (e >> 1)] = pack_bf16x2(a, z);
           }
           if (c == 0) {                       // the product before is done: P may be written over
-            if (j > j_from) ok = warp_wait(&s.o_done[x], (count - 1) & 1, &s.wait);
+            ok = warp_wait(&s.o_done[x], (count & 1) ^ 1, &s.wait);   // (none before: at once)
             if (!ok) break;
             tc_fence_after();
           }
