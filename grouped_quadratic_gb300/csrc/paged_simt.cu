@@ -7,7 +7,9 @@
 // A block takes kRows rows (queries of one KV head, row t * rho + h') and walks
 // 64 keys at a time through shared memory; a thread holds kRows / 8 rows of 4
 // keys (scores) or 4 columns (results).  fp32 products: bound by the FMA pipes
-// and shared memory together (8 16-byte loads for 64 FMAs).
+// and shared memory together (8 16-byte loads for 64 FMAs), four blocks per SM
+// hiding each other's loads and barriers.  1 x 3000 tokens, 4 heads: 179 us (27
+// TFLOP/s); with the next tile in registers, two blocks per SM, 199.
 #include <algorithm>
 
 #include "paged.cuh"
@@ -34,7 +36,7 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
 }
 
 template <int kRows>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, kRows == 32 ? 4 : 1)
 paged_simt_kernel(PagedArgs p) {
   pdl_trigger();
   pdl_wait();
@@ -81,8 +83,7 @@ paged_simt_kernel(PagedArgs p) {
   float4 o[R];
 #pragma unroll
   for (int i = 0; i < R; ++i) m[i] = -INFINITY, l[i] = 0.f, o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-  // A thread moves piece tid % 16 of rows tid / 16 + 8 i of a tile, the next one's
-  // while the present one is worked on; 16 keys lie on one page.
+  // A thread moves piece tid % 16 of rows tid / 16 + 8 i of a tile; 16 keys lie on one page.
   int page[kKeys / 16];
   auto look = [&](int j0) {
 #pragma unroll
@@ -105,9 +106,9 @@ paged_simt_kernel(PagedArgs p) {
     }
   };
   look(k0 & ~(kKeys - 1));
-  fetch(k0 & ~(kKeys - 1));
-  look((k0 & ~(kKeys - 1)) + kKeys);
   for (int j0 = k0 & ~(kKeys - 1); j0 < k1; j0 += kKeys) {
+    fetch(j0);
+    look(j0 + kKeys);
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < kKeys / 8; ++i) {
@@ -115,8 +116,6 @@ paged_simt_kernel(PagedArgs p) {
       *reinterpret_cast<float4 *>(&s.v[(tid >> 4) + 8 * i][4 * (tid & 15)]) = vn[i];
     }
     __syncthreads();
-    fetch(j0 + kKeys);
-    look(j0 + 2 * kKeys);
     uint64_t x2[R][4];                    // sums over even and odd elements, side by side: half the instructions
 #pragma unroll
     for (int i = 0; i < R; ++i)
