@@ -48,17 +48,19 @@ paged_join_kernel(PagedArgs p) {
       float top = m;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const int at = min(s + e * kJoinWarps, s1);
-        ml[e] = p.part_ml[first + at * rows];
-        o[e] = *reinterpret_cast<const float2 *>(p.part_o + (first + at * rows) * 64 + 2 * lane);
+        const int at = s + e * kJoinWarps;
+        ml[e] = make_float2(-INFINITY, 0.f), o[e] = make_float2(0.f, 0.f);
+        if (at <= s1) {
+          ml[e] = p.part_ml[first + at * rows];
+          o[e] = *reinterpret_cast<const float2 *>(p.part_o + (first + at * rows) * 64 + 2 * lane);
+        }
         top = fmaxf(top, ml[e].x);
       }
       const float zero = top == -INFINITY ? 0.f : top, keep = exp2f(m - zero);
       l *= keep, y.x *= keep, y.y *= keep, m = top;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        if (s + e * kJoinWarps > s1) break;
-        const float w = exp2f(ml[e].x - zero);
+        const float w = s + e * kJoinWarps <= s1 ? exp2f(ml[e].x - zero) : 0.f;
         l = fmaf(w, ml[e].y, l), y.x = fmaf(w, o[e].x, y.x), y.y = fmaf(w, o[e].y, y.y);
       }
     }

@@ -419,7 +419,8 @@ oal_status oal_page_append(const void *Q, const void *K, const void *V, oal_dtyp
  *  Q [B][Hq][T][d], Y [B][Hq][T][dv] in `dtype`, contiguous.
  *  past     [B] int32 (device): tokens before the T new ones.  Negative, or
  *           behind what the table has room for: clamped and recorded.
- *  lengths  [B] int32 (device) or NULL: as for oal_rope.
+ *  lengths  [B] int32 (device) or NULL: as for oal_rope, but rows of Q behind a
+ *           sequence's length may be read; they have no part in anything.
  *  scale    finite and > 0.  cap: 0 or a finite number > 0, of which 4 scale / cap
  *           is finite too.  window: 0 (none) or > 0.
  *  slopes   [Hq] fp32 (device) or NULL; first [B][T] int32 or NULL (document
