@@ -18,7 +18,8 @@ namespace {
 // each with every kJoinWarps-th split, in order, and their sums are added in
 // order: the same bits every time.  Eight splits a warp are one step, 2 us with
 // the launch, and each further step costs another 2: 129 splits took 10 us with
-// four warps; but 6,216 rows of 4 splits take 6 us with four warps, 3 with one.
+// four warps; but 6,216 rows of 4 splits take 16 us (cold) with four warps, 6.6
+// with one.
 constexpr int kJoinThreads = 128;
 template <typename T, int kJoinWarps>
 __global__ void __launch_bounds__(kJoinWarps > 4 ? 32 * kJoinWarps : kJoinThreads)

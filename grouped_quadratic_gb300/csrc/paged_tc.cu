@@ -15,8 +15,8 @@
 //
 // The launch has a block for every pair of tiles; one that has loaded its keys asks
 // for the work of one that has not started (cluster launch control), whose scores
-// are there when the results of the first leave: 4 x 8192 tokens, 32/8 heads, 840
-// us (1.31 PFLOP/s), with blocks that end 905.  Asked for at a block's start, work
+// are there when the results of the first leave: 4 x 8192 tokens, 32/8 heads, 831
+// us (1.32 PFLOP/s), with blocks that end 905.  Asked for at a block's start, work
 // went to blocks that were longer at theirs (documents 18.4 -> 24 us).
 //
 // m is the row's maximum at some time, at most 2^8 below the present one: O is

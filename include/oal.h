@@ -416,7 +416,8 @@ oal_status oal_page_append(const void *Q, const void *K, const void *V, oal_dtyp
  *     s_j = scale q.k_j;  s_j = cap tanh(s_j / cap) if cap > 0;
  *     s_j -= slopes[h] |i - j|,
  * y = sum_j softmax(s)_j v_j; a token that sees nothing gets zeros.
- *  Q [B][Hq][T][d], Y [B][Hq][T][dv] in `dtype`, contiguous.
+ *  Q [B][Hq][T][d], Y [B][Hq][T][dv] in `dtype`, contiguous.  Y may not overlap an
+ *           input.
  *  past     [B] int32 (device): tokens before the T new ones.  Negative, or
  *           behind what the table has room for: clamped and recorded.
  *  lengths  [B] int32 (device) or NULL: as for oal_rope, but rows of Q behind a

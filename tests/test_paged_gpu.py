@@ -607,3 +607,46 @@ def test_rotations_feed_the_other_layers(oal, dtype):
             torch.cuda.synchronize()
             assert all(torch.equal(a, b) for a, b in zip(*got))
     oal.oal_sync_status()
+
+
+@pytest.mark.parametrize("T", [1, 12, 300])
+def test_graphs_with_workspaces_of_their_own(oal, T):
+    """Two captured calls that split their keys and were given no workspace, replayed at once on two streams, eager
+    calls in between."""
+    cs = [Cache(1, 2, [past], [T], 32, BF16, seed=91 + past) for past in (9000, 7001)]
+    qs = [draw((1, 8, T, 64), BF16, 95 + i) for i in range(2)]
+    want = [check(oal, c, q) for c, q in zip(cs, qs)]
+    ys, graphs = [torch.zeros_like(q) for q in qs], []
+    side = torch.cuda.Stream()
+    for c, q, y in zip(cs, qs, ys):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            for _ in range(3):
+                oal.oal_paged_attention(q, c.Kp, c.Vp, c.table, c.past, Y=y)
+        graphs.append(graph)
+    assert oal.oal_paged_attention_workspace_bytes(1, 8, 2, T, 32, cs[0].table.shape[1]) > 256
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(20):
+        for y in ys:
+            y.zero_()
+        torch.cuda.synchronize()
+        for graph, stream in zip(graphs, streams):
+            with torch.cuda.stream(stream):
+                graph.replay()
+        eager = oal.oal_paged_attention(qs[0], cs[0].Kp, cs[0].Vp, cs[0].table, cs[0].past)
+        torch.cuda.synchronize()
+        assert torch.equal(eager, want[0])
+        assert all(torch.equal(a, b) for a, b in zip(ys, want))
+    oal.oal_sync_status()
+
+
+def test_append_in_place(oal):
+    """The turned queries may take the place of the queries."""
+    c = Cache(2, 2, [3, 40], [50, 50], 16, BF16, seed=99)
+    Q, K, V = (draw((2, h, 50, 64), BF16, 99 + i) for i, h in enumerate((6, 2, 2)))
+    plan = oal.oal_rope_plan(FREQ)
+    want = oal.oal_page_append(Q, K, V, plan, c.Kp, c.Vp, c.table, c.past)
+    pools = c.Kp.clone(), c.Vp.clone()
+    oal.oal_page_append(Q, K, V, plan, c.Kp, c.Vp, c.table, c.past, Yq=Q)
+    assert torch.equal(Q, want) and torch.equal(c.Kp, pools[0]) and torch.equal(c.Vp, pools[1])
+    oal.oal_sync_status()
