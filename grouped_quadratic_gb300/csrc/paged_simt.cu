@@ -193,8 +193,9 @@ paged_simt_kernel(PagedArgs p) {
       if (tx == 0) p.part_ml[row] = make_float2(m[i] * kLog2e, l[i]);
       continue;
     }
-    const float inv = hi[i] > 0 ? 1.f / l[i] : 0.f;
-    const float4 y = make_float4(o[i].x * inv, o[i].y * inv, o[i].z * inv, o[i].w * inv);
+    // (a row that sees nothing: zeros whatever its o is, which a bad value times a weight of 0 may have reached)
+    const float inv = 1.f / l[i];
+    const float4 y = hi[i] > 0 ? make_float4(o[i].x * inv, o[i].y * inv, o[i].z * inv, o[i].w * inv) : make_float4(0.f, 0.f, 0.f, 0.f);
     const bool wrong = live && !(fabsf(y.x) + fabsf(y.y) + fabsf(y.z) + fabsf(y.w) < INFINITY);
     const uint32_t again = __ballot_sync(0xffffffffu, wrong);
     if (live) *reinterpret_cast<float4 *>(paged_y<float>(p, b, h, t) + 4 * tx) = y;
