@@ -83,13 +83,10 @@ paged_join_kernel(PagedArgs p) {
       l = fmaf(f, s_l[w], l), y.x = fmaf(f, o.x, y.x), y.y = fmaf(f, o.y, y.y);
     }
   }
-  if (sees.y > 0) {
+  if (sees.y > 0)
     y.x /= l, y.y /= l;
-    if (__any_sync(0xffffffffu, !(fabsf(y.x) + fabsf(y.y) < INFINITY)))
-      y = paged_row_again<T>(p, seq, b, h, t, sees.x, sees.y);
-  } else {
+  else
     y = make_float2(0.f, 0.f);
-  }
   T *to = paged_y<T>(p, b, h, t) + 2 * lane;
   to[0] = from_f32<T>(y.x), to[1] = from_f32<T>(y.y);
 }

@@ -92,6 +92,11 @@ __device__ __forceinline__ int paged_page(const PagedArgs &p, int b, int j) {
   atomicCAS(p.status, kStatusOk, (int)OAL_ERR_INVALID_ARG);
   return -1;
 }
+// The same for keys that were looked up before (loads may pass it).
+__device__ __forceinline__ int paged_page_again(const PagedArgs &p, int b, int j) {
+  const int page = p.table[(size_t)b * p.max_pages + (j >> p.page_shift)];
+  return page >= 0 && page < p.n_pages ? page : -1;
+}
 __device__ __forceinline__ size_t paged_row(const PagedArgs &p, int page, int kv, int j) {
   return (size_t)page * p.page_stride +
          (((size_t)kv << p.page_shift) + (j & ((1 << p.page_shift) - 1))) * 64;
@@ -104,38 +109,6 @@ __device__ __forceinline__ float paged_score(const PagedArgs &p, float qk, float
   if (p.cap > 0.f) s = p.cap * tanhf(s / p.cap);
   s -= slope * (float)distance;
   return s;
-}
-
-// One row from the start, by a warp: lane l holds elements 2 l and 2 l + 1 of
-// the result.  Keys that the row does not see are not read, so whatever they
-// hold has no part in it: for rows whose result is not finite, which a masked
-// key's infinity or NaN (times a weight of 0) may be to blame for.
-template <typename T>
-static __device__ __noinline__ float2 paged_row_again(const PagedArgs &p, const PagedSeq &seq, int b, int h, int t, int lo, int hi) {
-  const int lane = threadIdx.x & 31, kv = h / p.rho;
-  const T *q = static_cast<const T *>(p.Q) + (((size_t)b * p.Hq + h) * p.T + t) * 64 + 2 * lane;
-  const float q0 = to_f32(q[0]), q1 = to_f32(q[1]);
-  const float slope = p.slopes ? p.slopes[h] : 0.f;
-  const int i = seq.past + t;
-  float m = -INFINITY, l = 0.f, o0 = 0.f, o1 = 0.f;
-  for (int j = lo; j < hi; ++j) {
-    const int page = paged_page(p, b, j);
-    float k0 = 0.f, k1 = 0.f, v0 = 0.f, v1 = 0.f;
-    if (page >= 0) {
-      const size_t at = paged_row(p, page, kv, j) + 2 * lane;
-      const T *k = static_cast<const T *>(p.Kp) + at, *v = static_cast<const T *>(p.Vp) + at;
-      k0 = to_f32(k[0]), k1 = to_f32(k[1]), v0 = to_f32(v[0]), v1 = to_f32(v[1]);
-    }
-    float s = fmaf(q0, k0, q1 * k1);
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-    s = paged_score(p, s, slope, abs(i - j));
-    const float top = s > m || s != s ? s : m;        // (a NaN stays)
-    const float keep = m == top ? 1.f : expf(m - top), w = s == -INFINITY ? 0.f : expf(s - top);
-    m = top;
-    l = l * keep + w, o0 = o0 * keep + w * v0, o1 = o1 * keep + w * v1;
-  }
-  return make_float2(o0 / l, o1 / l);
 }
 
 // Rows of 64 for Y.

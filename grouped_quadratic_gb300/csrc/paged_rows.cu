@@ -9,7 +9,7 @@
 // row; the work is HBM's, each key and value read once.
 #include <algorithm>
 
-#include "paged.cuh"
+#include "paged_again.cuh"
 
 namespace oal {
 namespace {
@@ -275,6 +275,7 @@ paged_rows_kernel(PagedArgs p) {
     }
   }
   __syncthreads();
+  uint32_t again = 0u;                    // the warp's rows whose result is not finite
   for (int at = warp; at < kRows; at += kWarps) {
     const int r = r0 + at, t = r / p.rho, h = kv * p.rho + r % p.rho;
     if (r >= all || t >= seq.n) break;
@@ -290,21 +291,24 @@ paged_rows_kernel(PagedArgs p) {
       const float f = exp2f(x[64] - base);
       sum = fmaf(f, x[65], sum), y.x = fmaf(f, x[2 * lane], y.x), y.y = fmaf(f, x[2 * lane + 1], y.y);
     }
+    if (__any_sync(0xffffffffu, !(fabsf(y.x) + fabsf(y.y) + sum < INFINITY))) again |= 1u << at;
     if (p.splits > 1) {
       const size_t to_row = ((size_t)bh * p.splits + split) * all + r;
       *reinterpret_cast<float2 *>(p.part_o + to_row * 64 + 2 * lane) = y;
       if (lane == 0) p.part_ml[to_row] = make_float2(top, sum);
       continue;
     }
-    const int row_k0 = __shfl_sync(0xffffffffu, lo, at), row_k1 = __shfl_sync(0xffffffffu, hi, at);
-    if (row_k1 > 0) {
+    if (__shfl_sync(0xffffffffu, hi, at) > 0)
       y.x /= sum, y.y /= sum;
-      if (__any_sync(0xffffffffu, !(fabsf(y.x) + fabsf(y.y) < INFINITY)))
-        y = paged_row_again<__nv_bfloat16>(p, seq, b, h, t, row_k0, row_k1);
-    } else {
+    else
       y = make_float2(0.f, 0.f);
-    }
     *reinterpret_cast<uint32_t *>(paged_y<__nv_bfloat16>(p, b, h, t) + 2 * lane) = pack(y.x, y.y);
+  }
+  if (again != 0u) {
+    const int r = r0 + lane;
+    const bool mine = again >> lane & 1u;
+    __syncwarp();                         // (other lanes write these rows now)
+    paged_rows_again(p, bh, split, seq.past, kv * p.rho + r % p.rho, r / p.rho, mine ? max(lo, k0) : 0, mine ? min(hi, k1) : 0);
   }
 }
 

@@ -35,6 +35,77 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   return r;
 }
 
+// One row once more, by a warp, over the keys [lo, hi) that it sees of a split:
+// for rows whose result is not finite, which the value of a key that they do not
+// see may be to blame for (0 times infinity or NaN).  A row that does see a bad key
+// stays as it is, which a look at its keys tells first; then lanes take 32 keys for
+// the scores, and the columns 2 l and 2 l + 1 of the values.
+static __device__ __noinline__ void paged_row_again(const PagedArgs &p, int bh, int split, int past, int h, int t, int lo, int hi) {
+  const int lane = threadIdx.x & 31, b = bh / p.Hkv, kv = bh % p.Hkv;
+  const float *Kp = static_cast<const float *>(p.Kp), *Vp = static_cast<const float *>(p.Vp);
+  const float4 *q = reinterpret_cast<const float4 *>(static_cast<const float *>(p.Q) + (((size_t)b * p.Hq + h) * p.T + t) * 64);
+  const float slope = p.slopes ? p.slopes[h] : 0.f;
+  float m = -INFINITY, l = 0.f, o0 = 0.f, o1 = 0.f;
+#pragma unroll 1
+  for (int j0 = lo & ~15; j0 < hi; j0 += 16) {      // (16 keys lie on one page)
+    const int page = paged_page_again(p, b, j0);
+    float worst = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {           // a lane takes 16 bytes of every other key
+      const int j = j0 + 2 * i + (lane >> 4);
+      if (page < 0 || j < lo || j >= hi) continue;
+      const size_t at = paged_row(p, page, kv, j) + 4 * (lane & 15);
+      const float4 k = *reinterpret_cast<const float4 *>(Kp + at), v = *reinterpret_cast<const float4 *>(Vp + at);
+      worst += (k.x * 0.f + k.y * 0.f) + (k.z * 0.f + k.w * 0.f);         // (0 unless one is not finite)
+      worst += (v.x * 0.f + v.y * 0.f) + (v.z * 0.f + v.w * 0.f);
+    }
+    if (__any_sync(0xffffffffu, worst != worst)) return;
+  }
+#pragma unroll 1
+  for (int j0 = lo & ~31; j0 < hi; j0 += 32) {
+    const int j = j0 + lane;
+    const bool seen = j >= lo && j < hi;
+    const int page = seen ? paged_page_again(p, b, j) : -1;
+    float x = -INFINITY;
+    if (seen) {
+      float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (page >= 0) {
+        const float4 *k = reinterpret_cast<const float4 *>(Kp + paged_row(p, page, kv, j));
+#pragma unroll 8
+        for (int d = 0; d < 16; ++d) {
+          const float4 a = q[d], c = k[d];
+          s.x = fmaf(a.x, c.x, s.x), s.y = fmaf(a.y, c.y, s.y), s.z = fmaf(a.z, c.z, s.z), s.w = fmaf(a.w, c.w, s.w);
+        }
+      }
+      x = paged_score(p, (s.x + s.y) + (s.z + s.w), slope, abs(past + t - j));
+    }
+    float top = fmaxf(m, x);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+    const float base = top == -INFINITY ? 0.f : top, keep = expf(m - base), w = expf(x - base);
+    m = top;
+    l = l * keep + w, o0 *= keep, o1 *= keep;
+#pragma unroll 8
+    for (int i = 0; i < 32; ++i) {
+      const int pg = __shfl_sync(0xffffffffu, page, i);       // (-1: not seen, or zeros)
+      const float f = __shfl_sync(0xffffffffu, w, i);
+      if (pg >= 0) {
+        const float2 v = *reinterpret_cast<const float2 *>(Vp + paged_row(p, pg, kv, j0 + i) + 2 * lane);
+        o0 = fmaf(f, v.x, o0), o1 = fmaf(f, v.y, o1);
+      }
+    }
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+  if (p.splits > 1) {
+    const size_t row = ((size_t)bh * p.splits + split) * ((size_t)p.T * p.rho) + (size_t)t * p.rho + h % p.rho;
+    *reinterpret_cast<float2 *>(p.part_o + row * 64 + 2 * lane) = make_float2(o0, o1);
+    if (lane == 0) p.part_ml[row] = make_float2(m * kLog2e, l);
+  } else {
+    *reinterpret_cast<float2 *>(paged_y<float>(p, b, h, t) + 2 * lane) = make_float2(o0 / l, o1 / l);
+  }
+}
+
 template <int kRows>
 __global__ void __launch_bounds__(kThreads, kRows == 32 ? 4 : 1)
 paged_simt_kernel(PagedArgs p) {
@@ -186,27 +257,26 @@ paged_simt_kernel(PagedArgs p) {
     for (int d = 1; d < 16; d <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], d);
     const int r = r0 + ty * R + i, t = r / p.rho, h = kv * p.rho + r % p.rho;
     const bool live = t < seq.n;
-    if (p.splits > 1) {
-      if (!live) continue;
+    const int a = max(lo[i], k0), z = min(hi[i], k1);          // of this split
+    const float all = fabsf(o[i].x) + fabsf(o[i].y) + fabsf(o[i].z) + fabsf(o[i].w) + l[i];
+    const bool wrong = live && a < z && !(all < INFINITY);
+    if (live && p.splits > 1) {
       const size_t row = ((size_t)bh * p.splits + split) * ((size_t)p.T * p.rho) + r;
       *reinterpret_cast<float4 *>(p.part_o + row * 64 + 4 * tx) = o[i];
       if (tx == 0) p.part_ml[row] = make_float2(m[i] * kLog2e, l[i]);
-      continue;
+    } else if (live) {
+      // (a row that sees nothing: zeros whatever its o is, which a bad value times a weight of 0 may have reached)
+      const float inv = 1.f / l[i];
+      *reinterpret_cast<float4 *>(paged_y<float>(p, b, h, t) + 4 * tx) =
+          a < z ? make_float4(o[i].x * inv, o[i].y * inv, o[i].z * inv, o[i].w * inv) : make_float4(0.f, 0.f, 0.f, 0.f);
     }
-    // (a row that sees nothing: zeros whatever its o is, which a bad value times a weight of 0 may have reached)
-    const float inv = 1.f / l[i];
-    const float4 y = hi[i] > 0 ? make_float4(o[i].x * inv, o[i].y * inv, o[i].z * inv, o[i].w * inv) : make_float4(0.f, 0.f, 0.f, 0.f);
-    const bool wrong = live && !(fabsf(y.x) + fabsf(y.y) + fabsf(y.z) + fabsf(y.w) < INFINITY);
     const uint32_t again = __ballot_sync(0xffffffffu, wrong);
-    if (live) *reinterpret_cast<float4 *>(paged_y<float>(p, b, h, t) + 4 * tx) = y;
+    __syncwarp();                         // (other lanes write these rows then)
     for (int half = 0; half < 2; ++half)
       if (again >> (16 * half) & 0xFFFFu) {
         const int who = 16 * half;
-        const int h2 = __shfl_sync(0xffffffffu, h, who), t2 = __shfl_sync(0xffffffffu, t, who);
-        const int a = __shfl_sync(0xffffffffu, lo[i], who), z = __shfl_sync(0xffffffffu, hi[i], who);
-        const float2 f = paged_row_again<float>(p, seq, b, h2, t2, a, z);
-        __syncwarp();
-        *reinterpret_cast<float2 *>(paged_y<float>(p, b, h2, t2) + 2 * (tid & 31)) = f;
+        paged_row_again(p, bh, split, seq.past, __shfl_sync(0xffffffffu, h, who), __shfl_sync(0xffffffffu, t, who),
+                        __shfl_sync(0xffffffffu, a, who), __shfl_sync(0xffffffffu, z, who));
       }
   }
 }

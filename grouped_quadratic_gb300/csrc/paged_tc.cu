@@ -31,7 +31,7 @@
 #include <algorithm>
 
 #include "gated_tc.cuh"
-#include "paged.cuh"
+#include "paged_again.cuh"
 
 namespace oal {
 namespace {
@@ -62,7 +62,9 @@ struct TcSmem {
   uint64_t s_full[2], s_read[2], p_full[2], o_done[2], drain[2];
   uint64_t item_full[2], item_free[2], next_full;
   ulonglong2 next;                        // the answer to a request for another block's work
-  TcItem item[2];
+  TcItem item[4];                         // the present one, the next, and two whose rows may be formed again
+  uint32_t again[4][8];                   // their rows whose result is not finite, by warp
+  int stop;                               // there are such: no more items
   uint32_t tmem;
   WaitState wait;
 };
@@ -178,7 +180,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
   TcSmem &s = *reinterpret_cast<TcSmem *>(align1024(smem_raw));
   const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
   if (tid == 0) {
-    s.wait.abort = 0;
+    s.wait.abort = 0, s.stop = 0;
     s.wait.status = p.status;
     mbar_init(&s.q_full, 1), mbar_init(&s.q_free, 1);
     for (int i = 0; i < kRing; ++i) {
@@ -213,7 +215,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
   // an item, as every warp but the first loading one takes it: copied, its place free at once
   auto take = [&](int it, TcItem &item) {
     if (!warp_wait(&s.item_full[it & 1], (it >> 1) & 1, &s.wait)) return false;
-    item = s.item[it & 1];
+    item = s.item[it & 3];
     __syncwarp();
     if (lane == 0) mbar_arrive(&s.item_free[it & 1]);
     return uniform(item.bh) != 0xFFFFFFFFu;
@@ -306,7 +308,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
           if (it >= 2) ok = warp_wait(&s.item_free[it & 1], ((it >> 1) - 1) & 1, &s.wait);
           if (!ok) break;
           if (lane == 0) {
-            s.item[it & 1] = item;
+            s.item[it & 3] = item;
             mbar_arrive(&s.item_full[it & 1]);
           }
           __syncwarp();
@@ -327,22 +329,25 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
           }
         }
         // (asked for when this one's keys are on their way: earlier would take it from a block that is done sooner)
-        if (lane == 0) {
-          mbar_arrive_expect_tx(&s.next_full, 16);
-          next_ask(&s.next, &s.next_full);
+        bool more = !uniform(*(volatile int *)&s.stop);
+        if (more) {
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&s.next_full, 16);
+            next_ask(&s.next, &s.next_full);
+          }
+          __syncwarp();
+          ++asked;
+          ok = warp_wait(&s.next_full, (asked - 1) & 1, &s.wait);
+          if (!ok) break;
+          more = next_read(s.next, bx, by);
+          bx = uniform(bx), by = uniform(by);
+          fence_proxy_async();              // (read before the next answer is written)
+          __syncwarp();
         }
-        __syncwarp();
-        ++asked;
-        ok = warp_wait(&s.next_full, (asked - 1) & 1, &s.wait);
-        if (!ok) break;
-        const bool more = next_read(s.next, bx, by);
-        bx = uniform(bx), by = uniform(by);
-        fence_proxy_async();                // (read before the next answer is written)
-        __syncwarp();
         if (!more) {                        // the end, for the others
           if (it >= 2) ok = warp_wait(&s.item_free[it & 1], ((it >> 1) - 1) & 1, &s.wait);
           if (ok && lane == 0) {
-            s.item[it & 1].bh = -1;
+            s.item[it & 3].bh = -1;
             mbar_arrive(&s.item_full[it & 1]);
           }
           break;
@@ -435,7 +440,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
   } else {
     const uint32_t tm = tb + ((uint32_t)(32 * (warp & 3)) << 16), to_o = tm + kColO + 64 * x;
     bool ok = true;
-    int count = 0;                                           // key tiles so far, of all items
+    int count = 0, it = 0;                                   // key tiles so far, of all items; items
     // The thread's row of an item: its query head in the KV head's, its token.  (Formed anew where it is wanted.)
     auto row_of = [&](const TcItem &item, int &h, int &t) {
       int r = tid & 127;
@@ -444,8 +449,8 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
       return h < p.rho && t < item.n;
     };
 #pragma unroll 1
-    for (int it = 0; ok; ++it) {
-      const TcItem &item = s.item[it & 1];                     // (read again at the end: registers are short in between)
+    for (; ok; ++it) {
+      const TcItem &item = s.item[it & 3];                     // (read again at the end: registers are short in between)
       ok = warp_wait(&s.item_full[it & 1], (it >> 1) & 1, &s.wait);
       if (!ok || uniform(item.bh) == 0xFFFFFFFFu) break;
       int see0, see1, at;                                      // the keys that the row sees, its position
@@ -600,8 +605,6 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         int h1, t;
         const bool live = row_of(item, h1, t);
         const int h = bh % p.Hkv * p.rho + h1;
-        PagedSeq seq;
-        seq.n = item.n, seq.past = item.past, seq.total = item.total;
         bool wrong = false;
         const size_t row = ((size_t)bh * p.splits + split) * ((size_t)p.T * p.rho) + (size_t)t * p.rho + h1;
         const float inv = see0 < see1 ? 1.f / total : 0.f;
@@ -620,7 +623,11 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
           if (p.splits > 1) {
             uint4 *dst = reinterpret_cast<uint4 *>(p.part_o + row * 64 + 16 * c);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) dst[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+            for (int e = 0; e < 4; ++e) {
+              dst[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+              wrong |= !(fabsf(__uint_as_float(o[4 * e])) + fabsf(__uint_as_float(o[4 * e + 1])) +
+                         fabsf(__uint_as_float(o[4 * e + 2])) + fabsf(__uint_as_float(o[4 * e + 3])) < INFINITY);
+            }
           } else {
             uint32_t pk[8];
 #pragma unroll
@@ -634,17 +641,28 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             dst[0] = make_uint4(pk[0], pk[1], pk[2], pk[3]), dst[1] = make_uint4(pk[4], pk[5], pk[6], pk[7]);
           }
         }
-        for (uint32_t again = __ballot_sync(0xffffffffu, wrong); again; again &= again - 1) {
-          const int who = __ffs(again) - 1;
-          const int h2 = __shfl_sync(0xffffffffu, h, who), t2 = __shfl_sync(0xffffffffu, t, who);
-          const int a = __shfl_sync(0xffffffffu, see0, who), z = __shfl_sync(0xffffffffu, see1, who);   // (not split)
-          const float2 y = paged_row_again<__nv_bfloat16>(p, seq, b, h2, t2, a, z);
-          __syncwarp();
-          *reinterpret_cast<uint32_t *>(paged_y<__nv_bfloat16>(p, b, h2, t2) + 2 * lane) = pack_bf16x2(y.x, y.y);
-        }
+        const uint32_t again = __ballot_sync(0xffffffffu, wrong && see0 < see1);
+        if (lane == 0) s.again[it & 3][warp] = again;
+        if (lane == 0 && again) s.stop = 1;   // (the loading warp reads it before it goes three items further)
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&s.item_free[it & 1]);
+    }
+    // Rows whose result is not finite, now that nothing waits for this warp, of the last three items: the first item
+    // with such rows lets go of its place before the loading warp hands out the second item behind it.
+#pragma unroll 1
+    for (int i = max(0, it - 3); ok && i < it; ++i) {
+      const uint32_t again = s.again[i & 3][warp];
+      if (again == 0u) continue;
+      const TcItem &item = s.item[i & 3];
+      int h, t;
+      row_of(item, h, t);
+      PagedSeq seq;
+      seq.n = item.n, seq.past = item.past, seq.total = item.total;
+      const int bh = item.bh;
+      int2 sees = make_int2(0, 0);
+      if (again >> lane & 1u) sees = paged_sees(p, seq, bh / p.Hkv, t);
+      paged_rows_again(p, bh, item.split, seq.past, bh % p.Hkv * p.rho + h, t, max(sees.x, item.from), min(sees.y, item.to));
     }
   }
   tc_fence_before();

@@ -431,7 +431,8 @@ oal_status oal_page_append(const void *Q, const void *K, const void *V, oal_dtyp
  *  and is recorded.  Pages without visible keys are not looked up, and keys that
  *  a token does not see have no part in its result whatever they hold.  Rows that
  *  see keys or values that are not finite, or whose scores leave fp32, have
- *  unspecified results.
+ *  unspecified results.  A call that reads such keys or values takes up to 10 times
+ *  as long.
  *  workspace  >= oal_paged_attention_workspace_bytes(...) bytes, 256-byte
  *           aligned, contents need not be initialised; 256 bytes: none is needed,
  *           it may be NULL.  Calls that may overlap on the GPU need one each.

@@ -41,3 +41,82 @@ def test_tokens_that_see_nothing_beside_bad_numbers(oal, dtype, bad, T, past):
     want, size = oracle(c, Q, [T], first=first.cuda())
     off = (Y.double() - want).abs() - tolerance(dtype, want, size)
     assert (off[:, :, 1::3] <= 0).all()
+
+
+def positive(n, Hkv, page, dtype, seed):
+    """Pools whose values lie in 0.5 .. 1.5: a result is then as large as what its errors are counted in."""
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    K = torch.randn(n, Hkv, page, 64, device="cuda", generator=gen).to(dtype)
+    return K, (0.5 + torch.rand(n, Hkv, page, 64, device="cuda", generator=gen)).to(dtype)
+
+
+def same_within(dtype, a, b):
+    """Two results of the same definition, each within its own tolerance."""
+    b = b.double()
+    return ((a.double() - b).abs() <= 2 * tolerance(dtype, b, b)).all()
+
+
+def fastest(f):
+    times = []
+    for _ in range(4):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        f()
+        b.record()
+        b.synchronize()
+        times.append(a.elapsed_time(b))
+    return min(times)
+
+
+@pytest.mark.parametrize("where", ["value", "both"])
+@pytest.mark.parametrize("dtype,B,Hq,Hkv,T,past", [
+    (BF16, 2, 16, 4, 8192, 0), (BF16, 2, 7, 1, 200, 60000), (BF16, 64, 32, 8, 4, 8000), (BF16, 2, 8, 2, 2, 131000),
+    (F32, 2, 4, 2, 2500, 0), (F32, 32, 8, 2, 2, 6000)])
+def test_one_bad_number_in_a_long_sequence(oal, dtype, B, Hq, Hkv, T, past, where):
+    """A NaN in the first sequence, not seen by the tokens before it and by every third one behind it, whose documents
+    start later: they and the other sequences do not change, and the call does not take many times as long."""
+    page, most = 64, -(-(past + T) // 64)
+    K, V = positive(B * most, Hkv, page, dtype, 131)
+    Q = draw((B, Hq, T, 64), dtype, 132, 1.5)
+    table = torch.arange(B * most, dtype=torch.int32, device="cuda").view(B, most)
+    at, j = torch.full((B,), past, dtype=torch.int32, device="cuda"), past + T // 2
+    first = torch.zeros(B, T, dtype=torch.int32, device="cuda")
+    first[0, T // 2 + 1::3] = j + 1
+    sees_not = (torch.arange(T, device="cuda") < T // 2) | (first[0] > j)
+    call = lambda: oal.oal_paged_attention(Q, K, V, table, at, first=first)
+    want, clean = call(), fastest(call)
+    V[j // page, :, j % page, 5] = math.nan
+    if where == "both":
+        K[j // page, :, j % page, 7] = math.nan
+    got, bad = call(), fastest(call)
+    oal.oal_sync_status()
+    assert torch.equal(got[1:], want[1:])
+    assert same_within(dtype, got[0][:, sees_not], want[0][:, sees_not])
+    assert bad <= 12 * clean + 0.1, (bad, clean)
+
+
+def test_rows_formed_again_outlast_no_wait(oal):
+    """Rows of 2^18 keys in one piece that do not see a NaN which others of their tile see, under waits of half a
+    millisecond: nothing waits for them, and the other sequences are as without it."""
+    B, T, past, page = 8, 9984, 1 << 18, 128
+    K, V = positive(9, 1, page, BF16, 141)
+    Q = draw((B, 1, T, 64), BF16, 142, 1.5)
+    table = 1 + torch.arange((past + T) // page, dtype=torch.int32, device="cuda") % 8
+    table[0] = 0                                     # the first page is one of its own
+    table = table.expand(B, -1).contiguous()
+    first = torch.full((B, T), 8, dtype=torch.int32, device="cuda")
+    first[0, 64:192:2] = 0
+    at = torch.full((B,), past, dtype=torch.int32, device="cuda")
+    call = lambda: oal.oal_paged_attention(Q, K, V, table, at, first=first)
+    assert oal.oal_paged_attention_workspace_bytes(B, 1, 1, T, page, table.shape[1]) == 256
+    want = call()
+    V[0, :, 5] = math.nan
+    oal.oal_debug_wait_test(1 << 20, 0)
+    try:
+        got = call()
+        oal.oal_sync_status()
+    finally:
+        oal.oal_debug_wait_test(0, 0)
+    assert torch.equal(got[1:], want[1:])
+    rows = first[0] > 0
+    assert same_within(BF16, got[0][:, rows], want[0][:, rows])
