@@ -111,6 +111,26 @@ __device__ __forceinline__ float paged_score(const PagedArgs &p, float qk, float
   return s;
 }
 
+// Caps of bf16's scores, in units of the exponent's base 2: cap tanh(f), f = qk
+// in_cap, in two forms.  cap - 2 cap / (e^{2 f} + 1) is off by up to 2^-22 of the cap,
+// which is nothing up to kCapNear (1.5e-5 of a score) and more than small scores
+// are under large caps.  Up to kTanhSpan, tanh(f) = f (c0 + c1 f^2 + .. + c4 f^8) to
+// 6e-8 of itself, by least squares at Chebyshev's points.
+constexpr float kCapNear = 64.f, kTanhSpan = 0.625f;
+constexpr float kTanh0 = 0.9999998807907104f, kTanh1 = -0.3333197236061096f, kTanh2 = 0.13304771482944489f,
+                kTanh3 = -0.05183185636997223f, kTanh4 = 0.015063672326505184f;
+__device__ __forceinline__ float paged_cap_near(float qk, float cap_in, float cap_out) {   // cap_in = 2 log2(e) in_cap
+  float w;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(w) : "f"(qk * cap_in));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(w) : "f"(w + 1.f));
+  return fmaf(-2.f * cap_out, w, cap_out);
+}
+__device__ __forceinline__ float paged_cap_far(float qk, float in_cap, float cap_in, float cap_out) {
+  const float f = qk * in_cap, f2 = f * f;
+  const float q = fmaf(fmaf(fmaf(fmaf(f2, kTanh4, kTanh3), f2, kTanh2), f2, kTanh1), f2, kTanh0);
+  return fabsf(f) <= kTanhSpan ? cap_out * (f * q) : paged_cap_near(qk, cap_in, cap_out);
+}
+
 // Rows of 64 for Y.
 template <typename T>
 __device__ __forceinline__ T *paged_y(const PagedArgs &p, int b, int h, int t) {

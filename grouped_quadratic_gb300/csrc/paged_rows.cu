@@ -174,16 +174,16 @@ paged_rows_kernel(PagedArgs p) {
 #pragma unroll
     for (int i = 0; i < kTiles; ++i) {
       float top[2] = {m[i][0], m[i][1]};
-      if (kExtra && p.cap > 0.f) {          // cap tanh(x) = cap - 2 cap / (e^{2 x} + 1)
+      if (kExtra && p.cap > kCapNear) {
 #pragma unroll
         for (int n = 0; n < kGroup / 8; ++n)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float w;
-            asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(w) : "f"(s[i][n][e] * cap_in));
-            asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(w) : "f"(w + 1.f));
-            s[i][n][e] = fmaf(-2.f * cap_out, w, cap_out);
-          }
+          for (int e = 0; e < 4; ++e) s[i][n][e] = paged_cap_far(s[i][n][e], p.scale / p.cap, cap_in, cap_out);
+      } else if (kExtra && p.cap > 0.f) {
+#pragma unroll
+        for (int n = 0; n < kGroup / 8; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[i][n][e] = paged_cap_near(s[i][n][e], cap_in, cap_out);
       } else {
 #pragma unroll
         for (int n = 0; n < kGroup / 8; ++n)

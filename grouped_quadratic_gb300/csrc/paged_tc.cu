@@ -44,10 +44,6 @@ constexpr int kTile = 128 * 128;          // bytes of 128 rows of 64
 constexpr int kRing = 4;                  // key tiles in flight, of K and of V
 constexpr uint32_t kColP = 256, kColO = 384;   // tensor memory: S of each tile (128 columns), P (64), O (64)
 constexpr float kBehind = 8.f;
-// Up to here tanh(f) = f (c0 + c1 f^2 + .. + c4 f^8) to 6e-8, by least squares at
-// Chebyshev's points: no exponential and no division, whose units the softmax
-// needs.  64 chats of up to 201 tokens, cap 30, window 1024: 140 us without it.
-constexpr float kTanhSpan = 0.625f;
 
 // Two tiles of rows and the keys that they see: what a block works on next.
 struct TcItem {
@@ -471,8 +467,8 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
       const float cap_in = kCap ? 2.f * kLog2e * p.scale / p.cap : 0.f, cap_out = p.cap * kLog2e;
       const float in_cap = kCap ? p.scale / p.cap : 0.f;
       auto times = [&](float c) { return pair(c * cap_out, c * cap_out); };
-      const uint64_t tanh0 = times(0.9999998807907104f), tanh1 = times(-0.3333197236061096f), tanh2 = times(0.13304771482944489f),
-                     tanh3 = times(-0.05183185636997223f), tanh4 = times(0.015063672326505184f);
+      const uint64_t tanh0 = times(kTanh0), tanh1 = times(kTanh1), tanh2 = times(kTanh2), tanh3 = times(kTanh3),
+                     tanh4 = times(kTanh4);
       const float by = kExtra ? 1.f : scale2;                // of what is held as a score
       float m = -INFINITY;
       uint64_t sum[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
@@ -492,7 +488,9 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         if (lane == 0) mbar_arrive(&s.s_read[x]);            // the next scores may come
         if (kCap) {
           const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * in_cap;
-          if (__all_sync(0xffffffffu, most <= kTanhSpan)) {
+          // (The polynomial takes no exponential and no division, whose units the softmax needs: 64 chats of up to 201
+          // tokens, cap 30, window 1024, 140 us without it.  What a row that is none holds is not to change the others.)
+          if (__all_sync(0xffffffffu, most <= kTanhSpan || see1 == INT32_MAX)) {
 #pragma unroll
             for (int e = 0; e < 128; e += 2) {
               const uint64_t f = mul2(pair(__uint_as_float(w[e]), __uint_as_float(w[e + 1])), pair(in_cap, in_cap)), f2 = mul2(f, f);
@@ -502,13 +500,12 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
               unpair(mul2(f, q), a, z);
               w[e] = __float_as_uint(a), w[e + 1] = __float_as_uint(z);
             }
-          } else {                            // cap tanh(f) = cap - 2 cap / (e^{2 f} + 1)
+          } else if (p.cap <= kCapNear) {
 #pragma unroll
-            for (int e = 0; e < 128; ++e) {
-              float z;
-              asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(z) : "f"(ex2(__uint_as_float(w[e]) * cap_in) + 1.f));
-              w[e] = __float_as_uint(fmaf(-2.f * cap_out, z, cap_out));
-            }
+            for (int e = 0; e < 128; ++e) w[e] = __float_as_uint(paged_cap_near(__uint_as_float(w[e]), cap_in, cap_out));
+          } else {
+#pragma unroll
+            for (int e = 0; e < 128; ++e) w[e] = __float_as_uint(paged_cap_far(__uint_as_float(w[e]), in_cap, cap_in, cap_out));
           }
         }
         if (kBias) {                          // with the scale where no cap has taken it in; packed where no key lies behind its row

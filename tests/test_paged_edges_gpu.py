@@ -120,3 +120,54 @@ def test_rows_formed_again_outlast_no_wait(oal):
     assert torch.equal(got[1:], want[1:])
     rows = first[0] > 0
     assert same_within(BF16, got[0][:, rows], want[0][:, rows])
+
+
+# ------------------------------------------------------------------ caps
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("cap", [100.0, 1e4, 1e6, 1e9])
+@pytest.mark.parametrize("T", [1, 5, 40, 200])
+def test_caps_far_above_the_scores(oal, dtype, cap, T):
+    """Scores that a cap leaves nearly as they are.  (The tolerance knows no cap: such scores are as exact as without
+    one: tanh(f) / f to 6e-8 and a few roundings, of scores up to 30 less than the 2e-5 of all scores.)"""
+    c = Cache(2, 2, [300, 61], [T, T], 16, dtype, seed=111)
+    Q = draw((2, 8, T, 64), dtype, 112, 1.5)
+    Y = oal.oal_paged_attention(Q, c.Kp, c.Vp, c.table, c.past, cap=cap)
+    oal.oal_sync_status()
+    want, size = oracle(c, Q, [T, T], cap=cap)
+    assert ((Y.double() - want).abs() <= tolerance(dtype, want, size)).all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("slopes", [False, True])
+@pytest.mark.parametrize("T", [4, 40, 200])
+def test_caps_near_some_scores_and_far_above_others(oal, dtype, slopes, T):
+    """Every fifth token's scores reach the cap, its neighbours' do not."""
+    c = Cache(1, 2, [333], [T], 16, dtype, seed=113)
+    Q = draw((1, 8, T, 64), dtype, 114, 1.5)
+    Q[:, :, ::5] *= 1e6
+    kw = dict(cap=1e6, slopes=torch.linspace(0.0, 0.4, 8, device="cuda") if slopes else None)
+    Y = oal.oal_paged_attention(Q, c.Kp, c.Vp, c.table, c.past, **kw)
+    oal.oal_sync_status()
+    want, size = oracle(c, Q, [T], **kw)
+    # (scores of up to 1e6 are off by 2^-24 of it and more: their tokens are not looked at)
+    off = (Y.double() - want).abs() - tolerance(dtype, want, size)
+    off[:, :, ::5] = 0
+    assert (off <= 0).all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("cap", [0.0, 30.0, 1e6])
+@pytest.mark.parametrize("T", [5, 300])
+def test_queries_behind_a_length_have_no_part(oal, dtype, cap, T):
+    n = [T - T // 3, T // 2]
+    c = Cache(2, 2, [200, 7], n, 16, dtype, seed=115, room=T // 16 + 1)
+    Q = draw((2, 8, T, 64), dtype, 116, 1.5)
+    got = []
+    for rest in (0.0, 1e4, 1e30, math.nan, math.inf):
+        for b in range(2):
+            Q[b, :, n[b]:] = rest
+        got.append(oal.oal_paged_attention(Q, c.Kp, c.Vp, c.table, c.past, cap=cap,
+                                           lengths=torch.tensor(n, dtype=torch.int32, device="cuda")))
+        oal.oal_sync_status()
+    assert all(torch.equal(got[0], y) for y in got[1:])
