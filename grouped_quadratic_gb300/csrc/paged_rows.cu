@@ -81,6 +81,8 @@ paged_rows_kernel(PagedArgs p) {
     const int from = paged_base(p, seq, t_first) + split * p.split_keys;
     k0 = max(k0, from), k1 = min(k1, from + p.split_keys);
     if (k0 >= k1) return;                 // (no row's interval reaches in: nothing is joined)
+  } else if (k1 == 0) {
+    k0 = 0;                               // (no row sees anything)
   }
 
   uint32_t q[kTiles][4][4];

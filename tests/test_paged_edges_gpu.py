@@ -171,3 +171,22 @@ def test_queries_behind_a_length_have_no_part(oal, dtype, cap, T):
                                            lengths=torch.tensor(n, dtype=torch.int32, device="cuda")))
         oal.oal_sync_status()
     assert all(torch.equal(got[0], y) for y in got[1:])
+
+
+# ------------------------------------------------------------------ nothing to see
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("Hq,T,past,page", [(2, 1, 0, 16), (8, 1, 100, 16), (8, 4, 100, 128), (16, 4, 250, 256),
+                                                 (4, 40, 60, 128), (14, 300, 0, 16)])
+def test_tiles_of_which_no_token_sees_anything(oal, dtype, Hq, T, past, page):
+    """Keys in one piece where they are few: zeros, beside a sequence that is as it was."""
+    c = Cache(2, 2, [past, past], [T, T], page, dtype, seed=151, fill=math.nan)
+    Q = draw((2, Hq, T, 64), dtype, 152, 1.5)
+    first = torch.zeros(2, T, dtype=torch.int32, device="cuda")
+    want = oal.oal_paged_attention(Q, c.Kp, c.Vp, c.table, c.past, first=first)
+    for nothing in (1 << 28, 2 ** 31 - 1):
+        first[0] = nothing
+        Y = torch.full_like(Q, 7.0)
+        oal.oal_paged_attention(Q, c.Kp, c.Vp, c.table, c.past, first=first, Y=Y)
+        oal.oal_sync_status()
+        assert (Y[0] == 0).all() and torch.equal(Y[1], want[1])
