@@ -123,6 +123,9 @@ oal_status paged_need_smem(const void *kernel, size_t bytes, bool (&done)[kMaxDe
 // keys 14.3 us instead of 11.2.)
 static int split_least(int is_bf16) { return is_bf16 ? 256 : 128; }
 constexpr int kRowsMost = 32;             // rows a KV head up to which bf16 goes by paged_rows_kernel
+// Keys of a split of paged_rows_kernel at most.  Its four warps add to accumulators that the tensor cores cut: values
+// of one sign come out 1.7e-3 low after 2^20 keys, 4e-4 after these, a tenth of a bf16's step.
+constexpr int kRowsKeys = 1 << 18;
 
 // The kernel's tile of rows, and into how many pieces the keys of a tile may be
 // cut: as many as fill the GPU, where the tiles alone do not.  The grid is made
@@ -153,6 +156,10 @@ static long long plan_tiles(PagedArgs &p, int is_bf16) {
   const long long least = split_least(is_bf16), most = (((long long)p.max_pages << p.page_shift) + least - 1) / least;
   return std::max<long long>(1, std::min(most, want / tiles));
 }
+// ... and must be, of so many keys.
+static long long plan_fewest(const PagedArgs &p, int is_bf16, long long span) {
+  return is_bf16 && (long long)p.T * p.rho <= kRowsMost ? (span + kRowsKeys - 1) / kRowsKeys : 1;
+}
 static void plan_split(PagedArgs &p, int is_bf16, long long pieces) {
   const long long room = (long long)p.max_pages << p.page_shift;
   long long span = room;                  // keys from a tile's first to its last
@@ -162,6 +169,7 @@ static void plan_split(PagedArgs &p, int is_bf16, long long pieces) {
     return (keys + kSplitAlign - 1) / kSplitAlign * kSplitAlign;
   };
   const long long rows = (long long)p.T * p.rho, units = (long long)p.B * p.Hkv;
+  pieces = std::max(pieces, plan_fewest(p, is_bf16, span));
   if (is_bf16 && rows > kRowsMost && pieces > 1) {
     // paged_tc_kernel: the fewest waves of one block per SM, a wave's time in keys: its blocks' and 700 that a block
     // costs beside; 300 and the partial results of 130 rows a key for the join.  114 tiles on 65536 keys: 4 pieces,
@@ -183,7 +191,8 @@ static size_t part_rows(const PagedArgs &p, long long splits) {
 }
 constexpr size_t kPartBytes = 64 * sizeof(float) + sizeof(float2);
 size_t paged_workspace_bytes(PagedArgs p, int is_bf16) {
-  const size_t bytes = part_rows(p, plan_tiles(p, is_bf16)) * kPartBytes;   // whatever the window
+  const long long room = (long long)p.max_pages << p.page_shift;            // (whatever the window)
+  const size_t bytes = part_rows(p, std::max(plan_tiles(p, is_bf16), plan_fewest(p, is_bf16, room))) * kPartBytes;
   return std::max<size_t>(256, (bytes + 255) & ~(size_t)255);
 }
 

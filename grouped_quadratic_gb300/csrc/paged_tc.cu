@@ -28,6 +28,8 @@
 // for; they take 1,600.  The loop of a row's scores needs nearly all registers: a
 // few more values that live across it (the row's head, its place) cost 15% in
 // spilled ones, so they are formed again behind it.
+#include <stddef.h>
+
 #include <algorithm>
 
 #include "gated_tc.cuh"
@@ -63,8 +65,16 @@ struct TcSmem {
   int stop;                               // there are such: no more items
   uint32_t tmem;
   WaitState wait;
+  // (only where a split has more than kFold key tiles)
+  float fold_l[256], fold_o[2][64][128];  // sums and results of the key tiles so far, by row
 };
-constexpr size_t kTcBytes = sizeof(TcSmem) + 1024;
+// The tensor cores cut what they add to an accumulator instead of rounding it, a
+// loss in proportion to the keys: values of one sign came out 6e-4 low after 65536
+// keys, 6.6e-3 after 2^20.  So O starts anew every kFold key tiles (1.3e-4), and
+// what it held is added in fp32 to a sum in shared memory, a row a thread.
+constexpr int kFold = 128;
+constexpr size_t kTcBytes = offsetof(TcSmem, fold_l) + 1024, kTcFoldBytes = sizeof(TcSmem) + 1024;
+static_assert(kTcFoldBytes <= 227 * 1024, "shared memory of a block");
 
 __device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, uint64_t *bar, int x, int y, int z, int w) {
   asm volatile(
@@ -166,8 +176,10 @@ __device__ __forceinline__ bool next_read(const ulonglong2 &answer, int &x, int 
   return got != 0;
 }
 
-// kCap: scores are capped; kBias: they take a distance.
-template <bool kCap, bool kBias>
+// kCap: scores are capped; kBias: they take a distance; kFolds: a split has more
+// than kFold key tiles (kernels of their own: the code that others do not run cost
+// them 1 to 6%).
+template <bool kCap, bool kBias, bool kFolds>
 __global__ void __launch_bounds__(kTcThreads, 1)
 paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                 const __grid_constant__ CUtensorMap tmV, PagedArgs p, int nt) {
@@ -404,7 +416,6 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         umma_commit_warp(&s.q_free);
       } else {
         const uint32_t id = idesc_bf16_f32(128, 64, 1);
-        uint32_t begun = 0u;              // bit y: O of tile y holds something of this item
 #pragma unroll 1
         while (j < work.last && ok) {
           const int c = y ? c1 : c0;
@@ -413,11 +424,11 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
           if (!ok) break;
           tc_fence_after();
           const uint64_t vd = desc(s.v[st]);
-          const uint32_t from_p = uniform(tb + kColP + 64 * y), to_o = uniform(tb + kColO + 64 * y), more = begun >> y & 1u;
+          const uint32_t from_p = uniform(tb + kColP + 64 * y), to_o = uniform(tb + kColO + 64 * y), since = (uint32_t)(j - work.from(y));
+          const uint32_t more = kFolds ? since & (kFold - 1) : since;   // O holds something to add to
 #pragma unroll
-          for (int k = 0; k < 8; ++k) umma_ts_warp(to_o, from_p + 8 * k, vd + 128 * k, id, k > 0 ? 1u : more);
+          for (int k = 0; k < 8; ++k) umma_ts_warp(to_o, from_p + 8 * k, vd + 128 * k, id, k > 0 ? 1u : more != 0u);
           umma_commit_warp(&s.o_done[y]);
-          begun |= 1u << y;
           c0 += 1 - y, c1 += y;
           const int before = j;
           work.step(j, y);
@@ -540,6 +551,30 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
               top[c] = fmaxf(top[c], fmaxf(__uint_as_float(w[32 * c + e]), __uint_as_float(w[32 * c + e + 1])));
           }
         }
+        if (kFolds && j > j_from && ((j - j_from) & (kFold - 1)) == 0) {
+          ok = warp_wait(&s.o_done[x], (count - 1) & 1, &s.wait);
+          if (!ok) break;
+          tc_fence_after();
+          const bool more = j - j_from > kFold;
+          float a, z, l = more ? s.fold_l[tid] : 0.f;
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            unpair(sum[c], a, z);
+            l += a + z, sum[c] = pair(0.f, 0.f);
+          }
+          s.fold_l[tid] = l;
+#pragma unroll 1
+          for (int c = 0; c < 64; c += 16) {
+            uint32_t o[16];
+            tmem_ld16(to_o + c, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              float &at = s.fold_o[x][c + e][tid & 127];
+              at = __uint_as_float(o[e]) + (more ? at : 0.f);
+            }
+          }
+        }
         const float now = fmaxf(m, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])));
         const bool behind = (now - m) * by > kBehind;          // (from -inf: always)
         if (__any_sync(0xffffffffu, behind)) {
@@ -564,6 +599,11 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
               for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * keep);
               tmem_st16(to_o + 16 * c, o);
             }
+          }
+          if (kFolds && j - j_from >= kFold) {
+            s.fold_l[tid] *= keep;
+#pragma unroll 4
+            for (int c = 0; c < 64; ++c) s.fold_o[x][c][tid & 127] *= keep;
           }
         }
         const float base = m == -INFINITY ? 0.f : -m * by;
@@ -594,7 +634,8 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
       }
       float f[4];
       unpair(sum[0], f[0], f[1]), unpair(sum[1], f[2], f[3]);
-      const float total = (f[0] + f[1]) + (f[2] + f[3]);
+      const bool folded = kFolds && j_to - j_from > kFold;
+      const float total = (f[0] + f[1]) + (f[2] + f[3]) + (folded ? s.fold_l[tid] : 0.f);
       if (j_from < j_to && ok) ok = warp_wait(&s.o_done[x], (count - 1) & 1, &s.wait);
       if (ok) {
         tc_fence_after();
@@ -615,6 +656,10 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
           } else {
 #pragma unroll
             for (int e = 0; e < 16; ++e) o[e] = 0u;
+          }
+          if (folded) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) + s.fold_o[x][16 * c + e][tid & 127]);
           }
           if (!live) continue;
           if (p.splits > 1) {
@@ -679,11 +724,12 @@ oal_status tc_map(CUtensorMap *m, const void *ptr, const cuuint64_t (&dims)[4], 
   return OAL_OK;
 }
 
-template <bool kCap, bool kBias>
+template <bool kCap, bool kBias, bool kFolds>
 oal_status run(const PagedArgs &p, cudaStream_t stream) {
   static bool done[kMaxDevices];
-  auto kernel = paged_tc_kernel<kCap, kBias>;
-  oal_status st = paged_need_smem(reinterpret_cast<const void *>(kernel), kTcBytes, done);
+  auto kernel = paged_tc_kernel<kCap, kBias, kFolds>;
+  constexpr size_t bytes = kFolds ? kTcFoldBytes : kTcBytes;
+  oal_status st = paged_need_smem(reinterpret_cast<const void *>(kernel), bytes, done);
   if (st != OAL_OK) return st;
   const int nt = p.tile_rows / (2 * p.rho);
   CUtensorMap mq, mk, mv;
@@ -697,7 +743,7 @@ oal_status run(const PagedArgs &p, cudaStream_t stream) {
   if (st == OAL_OK) st = tc_map(&mv, p.Vp, dims, strides, box);
   if (st != OAL_OK) return st;
   const dim3 grid((unsigned)((long long)p.B * p.Hkv * ((p.T + 2 * nt - 1) / (2 * nt))), (unsigned)p.splits);
-  launch_pdl(kernel, grid, dim3(kTcThreads), kTcBytes, stream, mq, mk, mv, p, nt);
+  launch_pdl(kernel, grid, dim3(kTcThreads), bytes, stream, mq, mk, mv, p, nt);
   st = oal_after_launch("paged_tc_kernel", stream);
   return st != OAL_OK || p.splits == 1 ? st : launch_paged_join(p, 1, stream);
 }
@@ -707,9 +753,13 @@ oal_status run(const PagedArgs &p, cudaStream_t stream) {
 // Rows of a block: two tiles of as many tokens as fit.
 int paged_tc_rows(int T, int rho) { return 2 * rho * std::min(T, 128 / rho); }
 
+template <bool kFolds>
+static oal_status run_tc(const PagedArgs &p, cudaStream_t stream) {
+  if (p.cap > 0.f) return p.slopes ? run<true, true, kFolds>(p, stream) : run<true, false, kFolds>(p, stream);
+  return p.slopes ? run<false, true, kFolds>(p, stream) : run<false, false, kFolds>(p, stream);
+}
 oal_status launch_paged_tc(const PagedArgs &p, cudaStream_t stream) {
-  if (p.cap > 0.f) return p.slopes ? run<true, true>(p, stream) : run<true, false>(p, stream);
-  return p.slopes ? run<false, true>(p, stream) : run<false, false>(p, stream);
+  return p.split_keys > kFold * kKeys ? run_tc<true>(p, stream) : run_tc<false>(p, stream);
 }
 
 }  // namespace oal

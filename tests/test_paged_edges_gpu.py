@@ -190,3 +190,40 @@ def test_tiles_of_which_no_token_sees_anything(oal, dtype, Hq, T, past, page):
         oal.oal_paged_attention(Q, c.Kp, c.Vp, c.table, c.past, first=first, Y=Y)
         oal.oal_sync_status()
         assert (Y[0] == 0).all() and torch.equal(Y[1], want[1])
+
+
+# ------------------------------------------------------------------ long sums
+
+def repeated(oal, B, Hkv, rho, T, past, seed, page=128, distinct=8):
+    """Mean relative error of attention over keys whose pages repeat (the definition then is a weighted softmax over
+    one period), values of one sign."""
+    per = page * distinct
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    K = torch.randn(distinct, Hkv, page, 64, device="cuda", generator=gen).to(BF16)
+    V = (0.5 + torch.rand(distinct, Hkv, page, 64, device="cuda", generator=gen)).to(BF16)
+    Q = (1.5 * torch.randn(B, Hkv * rho, T, 64, device="cuda", generator=gen)).to(BF16)
+    n = -(-(past + T) // page)
+    table = (torch.arange(n, device="cuda", dtype=torch.int32) % distinct).expand(B, n).contiguous()
+    Y = oal.oal_paged_attention(Q, K, V, table, torch.full((B,), past, dtype=torch.int32, device="cuda"))
+    oal.oal_sync_status()
+    k, v = (x.transpose(0, 1).flatten(1, 2).double() for x in (K, V))
+    off, j = [], torch.arange(per, device="cuda")
+    for t in range(0, T, max(1, T // 64)):
+        keys = past + t + 1
+        q = Q[:, :, t].double().view(B, Hkv, rho, 64)
+        s = 0.125 * torch.einsum("bhrd,hjd->bhrj", q, k)
+        w = torch.exp(s - s.amax(-1, keepdim=True)) * (keys // per + (j < keys % per))
+        y = torch.einsum("bhrj,hjd->bhrd", w, v) / w.sum(-1, keepdim=True)
+        off.append(((Y[:, :, t].double().view(B, Hkv, rho, 64) - y) / y).flatten())
+    return float(torch.cat(off).mean())
+
+
+@pytest.mark.parametrize("B,Hkv,rho,T,past,most", [
+    # The tensor cores cut what they add to an accumulator instead of rounding it: up to 2 2^-23 of it for every 16
+    # keys (the accumulator's last bit and the products' lined up with it), which adds up over 16384 keys of a sum (a
+    # chunk's) or 65536 (a token's) to 2.5e-4 and 9.8e-4.  The outputs' and weights' own roundings, independent in some
+    # 32,768 of them, 2^-8 each: 6e-5 and less on the mean.
+    (8, 1, 1, 9984, 1 << 20, 3.1e-4), (8, 1, 1, 9984, (1 << 18) + 77, 3.1e-4), (4, 2, 4, 4999, 1 << 19, 3.1e-4),
+    (1217, 1, 4, 1, (1 << 20) - 1, 1.04e-3), (1217, 1, 4, 1, 1 << 18, 1.04e-3)])
+def test_long_sums_of_one_sign(oal, B, Hkv, rho, T, past, most):
+    assert abs(repeated(oal, B, Hkv, rho, T, past, 121)) <= most
