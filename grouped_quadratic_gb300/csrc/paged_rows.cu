@@ -81,8 +81,6 @@ paged_rows_kernel(PagedArgs p) {
     const int from = paged_base(p, seq, t_first) + split * p.split_keys;
     k0 = max(k0, from), k1 = min(k1, from + p.split_keys);
     if (k0 >= k1) return;                 // (no row's interval reaches in: nothing is joined)
-  } else if (k1 == 0) {
-    k0 = 0;                               // (no row sees anything)
   }
 
   uint32_t q[kTiles][4][4];
@@ -104,7 +102,7 @@ paged_rows_kernel(PagedArgs p) {
     }
 
   const uint32_t ring = smem_at(smem_raw) + warp * kRing;
-  const int first = (k0 & ~(kGroup - 1)) + warp * kGroup;
+  const int first = k1 > 0 ? (k0 & ~(kGroup - 1)) + warp * kGroup : 0;   // (no row sees anything: no step)
   const int steps = first < k1 ? (k1 - first + kWarps * kGroup - 1) / (kWarps * kGroup) : 0;
   // pages of a group's two halves (a page has 16 keys at least); -1: no key of it is wanted
   int page[kGroup / 16];
