@@ -788,6 +788,7 @@ def oal_paged_attention(Q, Kp, Vp, table, past, lengths=None, scale=0.125, cap=0
     Y; rows behind a sequence's length stay as given (a Y made here has zeros
     there), tokens that see nothing get zeros."""
     lib = load_library()
+    _need(0 <= window < 1 << 31, "window must be 0 .. 2^31 - 1")   # (a C int would take it modulo 2^32)
     _need(Q.dim() == 4 and Kp.dim() == 4, "Q, Kp and Vp must have 4 dimensions")
     q, pages = Q.shape, Kp.shape
     B, Hq, T, d = q
