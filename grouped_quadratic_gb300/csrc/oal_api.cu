@@ -699,15 +699,16 @@ oal_status oal_rope(const void *Q, const void *K, oal_dtype dtype, const int64_t
   return oal::launch_rope(p, dtype == OAL_BF16, form, "rope_kernel", stream);
 }
 
-static oal_status check_pages(int Hkv, int n_pages, int page_size, int64_t page_stride,
-                              int max_pages, int *shift) {
+static oal_status check_pages(oal_dtype dtype, int Hkv, int n_pages, int page_size,
+                              int64_t page_stride, int max_pages, int *shift) {
   if (n_pages < 0 || max_pages < 0)
     return oal_fail(OAL_ERR_INVALID_ARG, "n_pages=%d max_pages=%d", n_pages, max_pages);
   if (page_size < 1 || (page_size & (page_size - 1)) != 0)
     return oal_fail(OAL_ERR_INVALID_ARG, "page_size=%d is not a power of two", page_size);
   if (page_size < 16 || page_size > 65536 || (long long)page_size * max_pages > 1LL << 30)
     return oal_fail(OAL_ERR_UNSUPPORTED, "page_size=%d, max_pages=%d", page_size, max_pages);
-  if (page_stride < (int64_t)Hkv * page_size * oal::kD || page_stride % 8 != 0 || page_stride > 1LL << 38)
+  if (page_stride < (int64_t)Hkv * page_size * oal::kD || page_stride % (dtype == OAL_BF16 ? 8 : 4) != 0 ||
+      page_stride > 1LL << 38)
     return oal_fail(OAL_ERR_INVALID_ARG, "page_stride=%lld", (long long)page_stride);
   *shift = 0;
   while (1 << *shift < page_size) ++*shift;
@@ -726,7 +727,7 @@ oal_status oal_page_append(const void *Q, const void *K, const void *V, oal_dtyp
   if (dv != oal::kDv) return oal_fail(OAL_ERR_UNSUPPORTED, "only dv = 64 is supported (dv=%d)", dv);
   if (Hkv <= 0) return oal_fail(OAL_ERR_INVALID_ARG, "Hkv=%d", Hkv);
   OAL_TRY(rope_args(p, dtype, x, 3, strides, B, Hq, Hkv, T, d, plan, form, positions, n_axes, past, lengths));
-  OAL_TRY(check_pages(Hkv, n_pages, page_size, page_stride, max_pages, &p.page_shift));
+  OAL_TRY(check_pages(dtype, Hkv, n_pages, page_size, page_stride, max_pages, &p.page_shift));
   if (!plan && Q) return oal_fail(OAL_ERR_INVALID_ARG, "Q without a plan");
   t_call_launches = 0;
   if (B == 0 || T == 0) return OAL_OK;
@@ -754,7 +755,7 @@ static oal_status check_paged(oal::PagedArgs &p, int B, int Hq, int Hkv, int T, 
                               int max_pages) {
   OAL_TRY(check_common(B, Hq, Hkv, d, dv, dtype, OAL_STATE_FULL));
   if (T < 0) return oal_fail(OAL_ERR_INVALID_ARG, "T=%d", T);
-  OAL_TRY(check_pages(Hkv, n_pages, page_size, page_stride, max_pages, &p.page_shift));
+  OAL_TRY(check_pages(dtype, Hkv, n_pages, page_size, page_stride, max_pages, &p.page_shift));
   const int rho = Hq / Hkv;
   if (rho > 128 || (long long)B * Hkv > 65535 || (long long)T * rho > 1LL << 28 ||
       (long long)B * Hkv * T > 1LL << 31)

@@ -227,3 +227,22 @@ def repeated(oal, B, Hkv, rho, T, past, seed, page=128, distinct=8):
     (1217, 1, 4, 1, (1 << 20) - 1, 1.04e-3), (1217, 1, 4, 1, 1 << 18, 1.04e-3)])
 def test_long_sums_of_one_sign(oal, B, Hkv, rho, T, past, most):
     assert abs(repeated(oal, B, Hkv, rho, T, past, 121)) <= most
+
+
+# ------------------------------------------------------------------ layouts
+
+@pytest.mark.parametrize("dtype,gap", [(F32, 4), (F32, 12), (BF16, 8)])
+@pytest.mark.parametrize("T", [1, 100])
+def test_pages_apart_by_any_multiple_of_16_bytes(oal, dtype, gap, T):
+    c = Cache(1, 2, [70], [T], 16, dtype, seed=161)
+    Q, K, V = (draw((1, h, T, 64), dtype, 162 + i, 1.5) for i, h in enumerate((4, 2, 2)))
+    oal.oal_page_append(None, K, V, None, c.Kp, c.Vp, c.table, c.past)
+    want = oal.oal_paged_attention(Q, c.Kp, c.Vp, c.table, c.past)
+    shape, size = c.Kp.shape, c.Kp[0].numel()
+    Kp, Vp = (torch.full((shape[0] * (size + gap),), math.nan, dtype=dtype, device="cuda")
+              .as_strided(shape, (size + gap, *x.stride()[1:])) for x in (c.Kp, c.Vp))
+    Kp.copy_(c.Kp), Vp.copy_(c.Vp)
+    oal.oal_page_append(None, K, V, None, Kp, Vp, c.table, c.past)
+    assert torch.equal(Kp, c.Kp) and torch.equal(Vp, c.Vp)
+    assert torch.equal(oal.oal_paged_attention(Q, Kp, Vp, c.table, c.past), want)
+    oal.oal_sync_status()
