@@ -397,7 +397,8 @@ oal_status oal_rope(const void *Q, const void *K, oal_dtype dtype, const int64_t
  *  past     [B] int32 (device).  A token whose page is not in the table, or
  *           whose entry is outside 0..n_pages-1, is not written to the cache and
  *           recorded in the device status word (OAL_ERR_INVALID_ARG).  Two tokens
- *           with the same place leave either there.
+ *           with the same place (a page twice in a table, or in two) leave parts
+ *           of either there.
  * The rest, and the arithmetic, as for oal_rope.
  */
 oal_status oal_page_append(const void *Q, const void *K, const void *V, oal_dtype dtype,
@@ -428,8 +429,10 @@ oal_status oal_page_append(const void *Q, const void *K, const void *V, oal_dtyp
  *           masks: the first key of the token's document); prefix [B] int32 or
  *           NULL.
  *  A page that holds a visible key and is outside 0..n_pages-1 counts as zeros
- *  and is recorded.  Pages without visible keys are not looked up, and keys that
- *  a token does not see have no part in its result whatever they hold.  Rows that
+ *  and is recorded.  Pages before the first and behind the last key that tokens
+ *  of a sequence see are not looked up (one between whose keys no token sees may be,
+ *  and be recorded), and keys that a token does not see have no part in its result
+ *  whatever they hold.  Rows that
  *  see keys or values that are not finite, or whose scores leave fp32, have
  *  unspecified results.  A call that reads such keys or values takes up to 10 times
  *  as long.
