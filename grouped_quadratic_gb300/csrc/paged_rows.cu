@@ -238,7 +238,7 @@ paged_rows_kernel(PagedArgs p) {
           l[i][e >> 1] += s[i][n][e];
         }
     }
-    // the weights, rounded to bf16 (2^-9 of each at most), are left factors as they lie
+    // the weights, rounded to bf16 (by 2^-8 of each at most), are left factors as they lie
 #pragma unroll
     for (int k = 0; k < kGroup / 16; ++k) {
       uint32_t w[kTiles][4];

@@ -296,7 +296,7 @@ oal_status run(const PagedArgs &p, cudaStream_t stream) {
 }  // namespace
 
 oal_status launch_paged_simt(const PagedArgs &p, cudaStream_t stream) {
-  return p.tile_rows == 8 ? run<8>(p, stream) : p.tile_rows == 16 ? run<16>(p, stream) : run<32>(p, stream);
+  return p.tile_rows == 8 ? run<8>(p, stream) : run<32>(p, stream);
 }
 
 }  // namespace oal

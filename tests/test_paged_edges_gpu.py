@@ -246,3 +246,44 @@ def test_pages_apart_by_any_multiple_of_16_bytes(oal, dtype, gap, T):
     assert torch.equal(Kp, c.Kp) and torch.equal(Vp, c.Vp)
     assert torch.equal(oal.oal_paged_attention(Q, Kp, Vp, c.table, c.past), want)
     oal.oal_sync_status()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_two_tokens_of_one_place(oal, dtype):
+    """Whatever is left there is of one or the other, and the rest of the cache as it was."""
+    c = Cache(2, 2, [0, 0], [40, 40], 16, dtype, seed=171)
+    c.table[1, 1] = c.table[0, 1]
+    K = draw((2, 2, 40, 64), dtype, 172)
+    before = c.Kp.clone()
+    oal.oal_page_append(None, K, K, None, c.Kp, c.Vp, c.table, c.past)
+    oal.oal_sync_status()
+    at = c.table[0, 1].item()
+    for pool in (c.Kp, c.Vp):
+        assert ((pool[at] == K[0, :, 16:32]) | (pool[at] == K[1, :, 16:32])).all()
+    for b in range(2):
+        for i in (0, 2):
+            rows = K[b, :, 16 * i:16 * i + 16]
+            assert torch.equal(c.Kp[c.table[b, i].item(), :, :rows.shape[1]], rows)
+    others = [i for i in range(c.n) if i not in c.table.flatten().tolist()]
+    assert torch.equal(c.Kp[others], before[others])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("B,Hq,Hkv,T,past,page,most", [
+    (1, 14, 2, 1, 5000, 64, 128), (3, 8, 2, 4, 900, 16, 5000), (1, 4, 1, 300, 3000, 32, 2000), (2, 8, 8, 65, 100, 128, 40),
+    (1, 2, 1, 1, 70000, 65536, 2), (1, 6, 2, 2000, 0, 64, 40), (9, 2, 2, 1, 250, 16, 17), (1300, 2, 1, 1, 50, 16, 20000)])
+def test_workspace_is_not_overrun(oal, dtype, B, Hq, Hkv, T, past, page, most):
+    """Exactly the size that is asked for, and numbers behind it that stay, whatever the masks."""
+    c = Cache(B, Hkv, [past] * B, [T] * B, page, dtype, seed=181)
+    c.table = torch.cat([c.table, torch.full((B, most - c.table.shape[1]), -1, dtype=torch.int32, device="cuda")], 1)
+    Q = draw((B, Hq, T, 64), dtype, 182)
+    need = oal.oal_paged_attention_workspace_bytes(B, Hq, Hkv, T, page, most, dtype=int(dtype is BF16))
+    prefix = torch.full((B,), past + T, dtype=torch.int32, device="cuda")
+    first = torch.full((B, T), past, dtype=torch.int32, device="cuda")
+    for kw in (dict(), dict(window=1), dict(window=100), dict(window=1000), dict(window=2 ** 31 - 1), dict(prefix=prefix),
+               dict(prefix=prefix, window=300), dict(first=first), dict(first=first, window=300)):
+        want = oal.oal_paged_attention(Q, c.Kp, c.Vp, c.table, c.past, **kw)
+        room = torch.full((need + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+        Y = oal.oal_paged_attention(Q, c.Kp, c.Vp, c.table, c.past, workspace=room[:need], **kw)
+        oal.oal_sync_status()
+        assert torch.equal(Y, want) and (room[need:] == 0xA5).all()
