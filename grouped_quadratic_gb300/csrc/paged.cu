@@ -120,17 +120,19 @@ oal_status paged_need_smem(const void *kernel, size_t bytes, bool (&done)[kMaxDe
 
 // Keys of a split at least: a bf16 block's start and end cost more than 256 keys, an fp32 block's less.
 // (256 for both: 2 x 300 tokens of 4 fp32 heads 32 us instead of 24.5; 128 for both: one bf16 token on 32768
-// keys 14.3 us instead of 11.2.)
+// keys 3 us more.)
 static int split_least(int is_bf16) { return is_bf16 ? 256 : 128; }
 constexpr int kRowsMost = 32;             // rows a KV head up to which bf16 goes by paged_rows_kernel
 // Keys of a split of paged_rows_kernel at most.  Its four warps add to accumulators that the tensor cores cut: values
-// of one sign come out 1.7e-3 low after 2^20 keys, 4e-4 after these, a tenth of a bf16's step.
+// of one sign come out 1.7e-3 low after 2^20 keys, 4e-4 after these, a tenth of a bf16's rounding.
 constexpr int kRowsKeys = 1 << 18;
 
 // The kernel's tile of rows, and into how many pieces the keys of a tile may be
 // cut: as many as fill the GPU, where the tiles alone do not.  The grid is made
 // for the longest sequence that the table has room for; blocks behind a
-// sequence's end return at once.
+// sequence's end return at once.  So a table far wider than its sequences leaves
+// the GPU part empty: 8 tokens on 4096 keys each, 32/8 heads, 15.0 us with a table
+// of 4096 keys and 32.9 with one of 131072; 128 tokens on 2000, 13.0 and 28.0.
 //
 // paged_rows_kernel, three blocks of which fit an SM: with few units (pairs of
 // sequence and KV head) about one wave, four blocks per SM of which a ragged

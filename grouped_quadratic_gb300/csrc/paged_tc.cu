@@ -15,9 +15,10 @@
 //
 // The launch has a block for every pair of tiles; one that has loaded its keys asks
 // for the work of one that has not started (cluster launch control), whose scores
-// are there when the results of the first leave: 4 x 8192 tokens, 32/8 heads, 831
-// us (1.32 PFLOP/s), with blocks that end 905.  Asked for at a block's start, work
-// went to blocks that were longer at theirs (documents 18.4 -> 24 us).
+// are there when the results of the first leave: 4 x 8192 tokens, 32/8 heads, 845
+// to 865 us from box to box (1.3 PFLOP/s), with blocks that end 8% more.  Asked for
+// at a block's start, work went to blocks that were longer at theirs (documents 18.4
+// -> 24 us).
 //
 // m is the row's maximum at some time, at most 2^8 below the present one: O is
 // multiplied by a power of two (through registers) only when it falls behind
@@ -25,9 +26,12 @@
 //
 // What bounds it: for 128 x 128 scores of both tiles 1,024 cycles of MMAs, 1,024 of
 // the exponentials' units, 1,400 of the softmax's instructions with nothing to wait
-// for; they take 1,600.  The loop of a row's scores needs nearly all registers: a
-// few more values that live across it (the row's head, its place) cost 15% in
-// spilled ones, so they are formed again behind it.
+// for; a whole launch takes 1,780 for each (2048 tokens on 63488 keys, three items a
+// block) or 1,830 (4 x 8192, 27 items), items' starts and ends among them; what else
+// the other 300 go to is not known.  The loop of a row's scores needs nearly all
+// registers: a few more values that live across it (the row's head, its place) cost
+// 15% in spilled ones, so they are formed again behind it.  (With caps or distances 16
+// to 32 bytes are stored apart, 24 to 68 loaded.)
 #include <stddef.h>
 
 #include <algorithm>
