@@ -287,3 +287,36 @@ def test_workspace_is_not_overrun(oal, dtype, B, Hq, Hkv, T, past, page, most):
         Y = oal.oal_paged_attention(Q, c.Kp, c.Vp, c.table, c.past, workspace=room[:need], **kw)
         oal.oal_sync_status()
         assert torch.equal(Y, want) and (room[need:] == 0xA5).all()
+
+
+@pytest.mark.parametrize("kind", ["none", "cap", "bias", "cap+bias", "window", "docs", "prefix", "all"])
+def test_long_splits_as_short_ones(oal, kind):
+    """6700 tokens on 36000 keys take splits of more than 16384 keys; 64 of them at a time, splits of fewer (compared
+    with the definition above), to the tolerances of both.  Distances make the maximum grow all along the keys."""
+    T, past, page = 6700, 36000, 64
+    most = -(-(past + T) // page)
+    K, V = positive(most, 2, page, BF16, 191)
+    Q = draw((1, 8, T, 64), BF16, 192, 1.5)
+    table = torch.randperm(most, generator=torch.Generator().manual_seed(1)).to(torch.int32)[None].cuda()
+    kw, first = {}, None
+    if "cap" in kind or kind == "all":
+        kw["cap"] = 5.0
+    if "bias" in kind or kind == "all":
+        kw["slopes"] = torch.linspace(0.0, 2e-3, 8, device="cuda")
+    if kind in ("window", "all"):
+        kw["window"] = 30000
+    if kind in ("prefix", "all"):
+        kw["prefix"] = torch.tensor([past + T // 2], dtype=torch.int32, device="cuda")
+    if kind in ("docs", "all"):
+        t = torch.arange(T, dtype=torch.int32, device="cuda")[None]
+        first = torch.where(t % 300 < 150, 7 * t, 11000)
+    at = lambda x: torch.tensor([x], dtype=torch.int32, device="cuda")
+    Y = oal.oal_paged_attention(Q, K, V, table, at(past), first=first, **kw)
+    for t0 in (0, 1777, 3333, T - 64):
+        part = slice(t0, t0 + 64)
+        want = oal.oal_paged_attention(Q[:, :, part].contiguous(), K, V, table, at(past + t0), **kw,
+                                       first=None if first is None else first[:, part].clone())
+        oal.oal_sync_status()
+        if "prefix" in kw and t0 + 64 < T // 2:      # (a prefix reaches as far as the sequence's keys)
+            continue
+        assert same_within(BF16, Y[:, :, part], want)
